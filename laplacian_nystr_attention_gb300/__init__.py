@@ -8,7 +8,8 @@ Linear Attention with Laplacian Kernel", explainer pages.)
 The compute lives in liblapl_attn.so (hand-written CUDA kernels, C ABI in
 include/lapl_attn.h).  ``_lib`` binds that ABI with the same names; ``LaplacianNystromAttention``
 below is a convenience layer that uses PyTorch only to allocate device memory and to pick the
-current CUDA stream.
+current CUDA stream.  ``GatedScan``, ``ResidualNorm`` and ``GradClip`` (operators.py) are the same
+for the operators beside the attention (C ABI in include/lapl_ops.h).
 """
 from __future__ import annotations
 
@@ -26,6 +27,14 @@ from ._lib import (LAPL_BF16, LAPL_F32, LAPL_KERNEL_GAUSSIAN, LAPL_KERNEL_LAPLAC
                    lapl_attn_plan_info_get, lapl_attn_version, lapl_attn_workspace_size,
                    lapl_attn_backward, lapl_attn_backward_kernels, lapl_attn_forward_train,
                    lapl_attn_backward_workspace_size)
+from ._lib import (LAPL_F8E4M3, LAPL_GATE_DECAY, LAPL_GATE_SIGMOID, LAPL_SCAN_CHUNK,
+                   lapl_clip_apply, lapl_clip_config, lapl_clip_create, lapl_clip_destroy,
+                   lapl_clip_last_error, lapl_clip_norm, lapl_clip_workspace_size,
+                   lapl_norm_backward, lapl_norm_config, lapl_norm_create, lapl_norm_destroy,
+                   lapl_norm_forward, lapl_norm_last_error, lapl_norm_workspace_size,
+                   lapl_scan_backward, lapl_scan_config, lapl_scan_create, lapl_scan_destroy,
+                   lapl_scan_forward, lapl_scan_last_error, lapl_scan_plan_info_get)
+from .operators import (GatedScan, GradClip, ResidualNorm, make_norm_config, make_scan_config)
 
 __all__ = [
     "LaplacianNystromAttention", "LaplAttnError", "lapl_attn_config", "lapl_attn_debug",
@@ -38,6 +47,14 @@ __all__ = [
     "make_config", "lapl_attn_backward", "lapl_attn_backward_kernels", "lapl_attn_forward_train",
     "lapl_attn_backward_workspace_size", "LAPL_KERNEL_LAPLACIAN", "LAPL_KERNEL_GAUSSIAN", "LAPL_SOLVER_NEWTON_SCHULZ",
     "LAPL_SOLVER_CG",
+    "GatedScan", "ResidualNorm", "GradClip", "make_scan_config", "make_norm_config",
+    "LAPL_F8E4M3", "LAPL_GATE_DECAY", "LAPL_GATE_SIGMOID", "LAPL_SCAN_CHUNK",
+    "lapl_scan_config", "lapl_scan_create", "lapl_scan_forward", "lapl_scan_backward",
+    "lapl_scan_plan_info_get", "lapl_scan_last_error", "lapl_scan_destroy",
+    "lapl_norm_config", "lapl_norm_create", "lapl_norm_forward", "lapl_norm_workspace_size",
+    "lapl_norm_backward", "lapl_norm_last_error", "lapl_norm_destroy",
+    "lapl_clip_config", "lapl_clip_create", "lapl_clip_workspace_size", "lapl_clip_norm",
+    "lapl_clip_apply", "lapl_clip_last_error", "lapl_clip_destroy",
 ]
 
 _DTYPES = {"f32": LAPL_F32, "bf16": LAPL_BF16}
@@ -130,12 +147,15 @@ class LaplacianNystromAttention:
 
     __call__ = forward
 
-    def backward(self, q, k, v, dout, bias=None, grads=None, stream=None):
+    def backward(self, q, k, v, dout, bias=None, grads=None, stream=None, max_norm=None):
         """(dq, dk, dv, dbias) for a loss with dLoss/dO = dout, after
         forward(q, k, v, bias, keep_for_backward=True) on this object (whose workspace holds
         what that forward kept; run nothing else on it in between).  dout: fp32 [B,H,N,d].  grads: optional dict with preallocated fp32 "dq",
         "dk", "dv" ([B,H,N,d]) and "dbias" ([H,m]) tensors.  The backward workspace is
-        allocated on first use."""
+        allocated on first use.
+
+        max_norm: clip the four gradients together to this global norm (GradClip, in place, on
+        the same stream); their norm before that is kept in ``grad_norm`` (a device scalar)."""
         import torch
         c = self.cfg
         if not getattr(self, "_kept", False):
@@ -165,9 +185,17 @@ class LaplacianNystromAttention:
                            g["dbias"].data_ptr(), self.workspace.data_ptr(),
                            self.workspace_bytes, self.bwd_workspace.data_ptr(),
                            self.bwd_workspace_bytes, st.cuda_stream)
+        if max_norm is not None:
+            all_four = [g["dq"], g["dk"], g["dv"], g["dbias"]]
+            if getattr(self, "_clip", None) is None:
+                self._clip = GradClip([t.numel() for t in all_four], ["f32"] * 4)
+            self.grad_norm = self._clip.clip(all_four, max_norm, stream=stream)
         return g["dq"], g["dk"], g["dv"], g["dbias"]
 
     def close(self):
+        if getattr(self, "_clip", None) is not None:
+            self._clip.close()
+            self._clip = None
         if getattr(self, "handle", None) is not None:
             lapl_attn_destroy(self.handle)
             self.handle = None

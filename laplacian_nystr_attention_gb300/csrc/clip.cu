@@ -1,0 +1,443 @@
+// clip.cu -- global norm of many gradient tensors and clipping: lapl_clip_* of
+// include/lapl_ops.h.
+//
+// The tensors are cut into pieces of kPiece values; the piece table travels as a kernel parameter
+// (no table in device memory, nothing to upload), for up to kTable tensors a launch.  First pass:
+// CTA b sums the squares of pieces b, b + grid, ... and writes one partial.  Second pass: every CTA
+// sums all partials in the same order, so each has the same norm to the last bit, and scales its
+// pieces.  HBM-bound: the first pass reads every value, the second reads and writes it.
+//
+// Squares.  fp32 holds values over 2^-149 .. 2^128, whose squares need twice that range.  Two sums
+// are kept: of (x 2^35)^2, exact enough for every value between 2^-98 and 2^28, and of (x 2^-72)^2
+// for what is larger.  The first is used unless it overflows; then some |x| is 2^24 or more, against
+// which what the second loses is nothing.  Partial sums are fp32 over at most some thousand values
+// of one thread, then double.
+#include <algorithm>
+#include <new>
+#include <vector>
+
+#include "ops_common.cuh"
+
+namespace lapl {
+namespace clip {
+
+constexpr int kThreads = 512;
+constexpr int kPiece = 16384;        // values
+constexpr int kTable = 1000;         // tensors of a launch: 20 KB of its 32 KB of parameters
+constexpr int kSmallTable = 64;
+constexpr float kLow = 34359738368.f;                // 2^35
+constexpr float kHigh = 2.117582368135751e-22f;      // 2^-72
+
+template <int N>
+struct Table {
+  const void* in[N];
+  void* out[N];
+  int first[N + 1];     // first piece of each tensor, and the number of pieces
+  int last[N];          // values of its last piece
+  unsigned char kind[N];   // lapl_dtype
+  int tensors;
+};
+
+// One piece: where it is and how many values it has.
+struct Piece {
+  const char* in;
+  char* out;
+  int count;
+  bool half;   // bf16
+};
+template <int N>
+__device__ __forceinline__ Piece piece_of(const Table<N>& t, int i) {
+  int lo = 0, hi = t.tensors;   // first[lo] <= i < first[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (t.first[mid] <= i) lo = mid; else hi = mid;
+  }
+  Piece p;
+  p.half = t.kind[lo] == LAPL_BF16;
+  const long long off = (long long)(i - t.first[lo]) * kPiece * (p.half ? 2 : 4);
+  p.in = reinterpret_cast<const char*>(t.in[lo]) + off;
+  p.out = t.out[lo] ? reinterpret_cast<char*>(t.out[lo]) + off : nullptr;
+  p.count = i + 1 == t.first[lo + 1] ? t.last[lo] : kPiece;
+  return p;
+}
+
+struct Sums {
+  float low, high;
+  __device__ __forceinline__ void add(float x) {
+    const float l = x * kLow, h = x * kHigh;
+    low = fmaf(l, l, low);
+    high = fmaf(h, h, high);
+  }
+};
+
+__device__ __forceinline__ float value_of(const char* p, bool half, int i) {
+  return half ? ops::bf16_bits(reinterpret_cast<const uint16_t*>(p)[i])
+              : reinterpret_cast<const float*>(p)[i];
+}
+
+// Sum over the CTA, the same double in every thread (fixed order).
+__device__ __forceinline__ double2 block_sum(double low, double high, double2* sm) {
+  for (int o = 16; o > 0; o >>= 1) {
+    low += __shfl_xor_sync(0xffffffffu, low, o);
+    high += __shfl_xor_sync(0xffffffffu, high, o);
+  }
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = make_double2(low, high);
+  __syncthreads();
+  double2 s = sm[0];
+  for (int k = 1; k < kThreads / 32; ++k) {
+    s.x += sm[k].x;
+    s.y += sm[k].y;
+  }
+  return s;
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads)
+clip_norm_kernel(const __grid_constant__ Table<N> t, double2* part) {
+  __shared__ double2 sm[kThreads / 32];
+  double low = 0., high = 0.;
+  const int pieces = t.first[t.tensors];
+  for (int i = blockIdx.x; i < pieces; i += gridDim.x) {
+    const Piece p = piece_of(t, i);
+    const int eb = p.half ? 2 : 4;
+    // Values before the first 16-byte boundary, 16 bytes at a time, and the rest.
+    const int head = min(p.count, (int)((16 - ((uintptr_t)p.in & 15)) & 15) / eb);
+    const int vectors = (p.count - head) * eb / 16;
+    Sums s = {0.f, 0.f};
+    const uint4* v = reinterpret_cast<const uint4*>(p.in + head * eb);
+    for (int k = threadIdx.x; k < vectors; k += kThreads) {
+      const uint4 r = v[k];
+      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (p.half) {
+          s.add(bf16_lo(w[u]));
+          s.add(bf16_hi(w[u]));
+        } else {
+          s.add(__uint_as_float(w[u]));
+        }
+      }
+    }
+    const int body = vectors * 16 / eb;
+    for (int k = threadIdx.x; k < p.count - body; k += kThreads)
+      s.add(value_of(p.in, p.half, k < head ? k : k + body));
+    low += s.low;
+    high += s.high;
+  }
+  const double2 sum = block_sum(low, high, sm);
+  if (threadIdx.x == 0) part[blockIdx.x] = sum;
+}
+
+// The norm from all partials.
+__device__ __forceinline__ float norm_of(const double2* part, int parts, double2* sm, double* exact) {
+  double low = 0., high = 0.;
+  for (int k = threadIdx.x; k < parts; k += kThreads) {
+    low += part[k].x;
+    high += part[k].y;
+  }
+  const double2 s = block_sum(low, high, sm);
+  *exact = isinf(s.x) ? sqrt(s.y) / kHigh : sqrt(s.x) / kLow;
+  return (float)*exact;
+}
+
+__global__ void __launch_bounds__(kThreads)
+clip_finish_kernel(const double2* part, int parts, float* norm) {
+  __shared__ double2 sm[kThreads / 32];
+  double exact;
+  const float v = norm_of(part, parts, sm, &exact);
+  if (threadIdx.x == 0) *norm = v;
+}
+
+template <int N>
+__global__ void __launch_bounds__(kThreads)
+clip_scale_kernel(const __grid_constant__ Table<N> t, const double2* part, int parts, float max_norm,
+                  float* norm) {
+  __shared__ double2 sm[kThreads / 32];
+  double exact;
+  const float v = norm_of(part, parts, sm, &exact);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && norm) *norm = v;
+  const bool clip = isfinite(v) && exact > (double)max_norm;
+  const float scale = clip ? (float)((double)max_norm / exact) : 1.f;
+  const int pieces = t.first[t.tensors];
+  // Last pieces first: those the first pass has left in L2.
+  for (int i = pieces - 1 - (int)blockIdx.x; i >= 0; i -= gridDim.x) {
+    const Piece p = piece_of(t, i);
+    if (!clip && p.in == p.out) continue;
+    const int eb = p.half ? 2 : 4;
+    const bool together = (((uintptr_t)p.in ^ (uintptr_t)p.out) & 15) == 0;
+    const int head = together ? min(p.count, (int)((16 - ((uintptr_t)p.in & 15)) & 15) / eb) : 0;
+    const int vectors = together ? (p.count - head) * eb / 16 : 0;
+    const uint4* in = reinterpret_cast<const uint4*>(p.in + head * eb);
+    uint4* out = reinterpret_cast<uint4*>(p.out + head * eb);
+    for (int k = threadIdx.x; k < vectors; k += kThreads) {
+      const uint4 r = in[k];
+      uint32_t w[4] = {r.x, r.y, r.z, r.w};
+      if (clip) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          w[u] = p.half ? ops::pack_bf16(bf16_lo(w[u]) * scale, bf16_hi(w[u]) * scale)
+                        : __float_as_uint(__uint_as_float(w[u]) * scale);
+      }
+      out[k] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    const int body = vectors * 16 / eb;
+    for (int k = threadIdx.x; k < p.count - body; k += kThreads) {
+      const int e = k < head ? k : k + body;
+      if (p.half) {
+        const uint16_t raw = reinterpret_cast<const uint16_t*>(p.in)[e];
+        reinterpret_cast<uint16_t*>(p.out)[e] =
+            clip ? (uint16_t)ops::pack_bf16(ops::bf16_bits(raw) * scale, 0.f) : raw;
+      } else {
+        const uint32_t raw = reinterpret_cast<const uint32_t*>(p.in)[e];
+        reinterpret_cast<uint32_t*>(p.out)[e] =
+            clip ? __float_as_uint(__uint_as_float(raw) * scale) : raw;
+      }
+    }
+  }
+}
+
+}  // namespace clip
+}  // namespace lapl
+
+struct lapl_clip_plan {
+  std::vector<long long> counts;
+  std::vector<int> dtypes;
+  struct Batch {       // the tensors of one launch
+    std::vector<int> index;   // those with values
+    int pieces, grid, first_part;
+  };
+  std::vector<Batch> batches;
+  std::vector<std::pair<uintptr_t, uintptr_t>> spans;   // scratch of the overlap check
+  int parts;           // partials of all launches
+  int device;
+  char last_error[lapl::ops::kErrorText];
+};
+
+using namespace lapl;
+
+namespace {
+
+lapl_status validate(const lapl_clip_config* c) {
+  if (!c || c->tensors < 0) return LAPL_ERR_INVALID_ARG;
+  if (c->tensors > 0 && (!c->counts || !c->dtypes)) return LAPL_ERR_INVALID_ARG;
+  for (int i = 0; i < c->tensors; ++i) {
+    if (c->counts[i] < 0 || !ops::is_float_dtype(c->dtypes[i])) return LAPL_ERR_INVALID_ARG;
+    if (c->counts[i] > (1LL << 40)) return LAPL_ERR_UNSUPPORTED;
+  }
+  return LAPL_OK;
+}
+
+// Fills the table of one batch.
+template <int N>
+void fill(const lapl_clip_plan& p, const lapl_clip_plan::Batch& b, const void* const* in,
+          void* const* out, clip::Table<N>* t) {
+  int first = 0, k = 0;
+  for (const int i : b.index) {
+    t->in[k] = in[i];
+    t->out[k] = out ? out[i] : nullptr;
+    t->first[k] = first;
+    const long long pieces = (p.counts[i] + clip::kPiece - 1) / clip::kPiece;
+    first += (int)pieces;
+    t->last[k] = (int)(p.counts[i] - (pieces - 1) * clip::kPiece);
+    t->kind[k] = (unsigned char)p.dtypes[i];
+    ++k;
+  }
+  t->first[k] = first;
+  t->tensors = k;
+}
+
+template <int N>
+cudaError_t launch_norm(const lapl_clip_plan& p, const lapl_clip_plan::Batch& b,
+                        const void* const* in, double2* part, cudaStream_t st) {
+  clip::Table<N> t;
+  fill(p, b, in, nullptr, &t);
+  clip::clip_norm_kernel<N><<<b.grid, clip::kThreads, 0, st>>>(t, part + b.first_part);
+  return cudaGetLastError();
+}
+template <int N>
+cudaError_t launch_scale(const lapl_clip_plan& p, const lapl_clip_plan::Batch& b,
+                         const void* const* in, void* const* out, const double2* part,
+                         float max_norm, float* norm, cudaStream_t st) {
+  clip::Table<N> t;
+  fill(p, b, in, out, &t);
+  clip::clip_scale_kernel<N><<<b.grid, clip::kThreads, 0, st>>>(t, part, p.parts, max_norm, norm);
+  return cudaGetLastError();
+}
+
+lapl_status check_pointers(const lapl_clip_plan& p, const void* const* a) {
+  for (size_t i = 0; i < p.counts.size(); ++i) {
+    if (p.counts[i] == 0) continue;
+    if (!a[i]) return LAPL_ERR_INVALID_ARG;
+    if (!ops::aligned(a[i], ops::dtype_bytes(p.dtypes[i]))) return LAPL_ERR_ALIGNMENT;
+  }
+  return LAPL_OK;
+}
+
+// Whether outputs overlap each other, or an input that is not their own.
+bool overlapping(lapl_clip_plan* p, const void* const* in, void* const* out) {
+  auto& s = p->spans;
+  s.clear();
+  for (size_t i = 0; i < p->counts.size(); ++i) {
+    if (p->counts[i] == 0) continue;
+    const uintptr_t bytes = (uintptr_t)p->counts[i] * ops::dtype_bytes(p->dtypes[i]);
+    // An output's end is odd-tagged: spans are doubled to make room for the tag.
+    const uintptr_t o = (uintptr_t)out[i], a = (uintptr_t)in[i];
+    s.emplace_back(o, (o + bytes) * 2 + 1);
+    if (a != o) s.emplace_back(a, (a + bytes) * 2);
+  }
+  std::sort(s.begin(), s.end());
+  uintptr_t end = 0, out_end = 0;   // furthest end so far, of all spans and of outputs
+  for (const auto& v : s) {
+    const bool is_out = v.second & 1;
+    if (v.first < (is_out ? end : out_end)) return true;
+    end = std::max(end, v.second / 2);
+    if (is_out) out_end = std::max(out_end, v.second / 2);
+  }
+  return false;
+}
+
+// The norm's partials of every launch.
+cudaError_t partials(const lapl_clip_plan& p, const void* const* in, double2* part, cudaStream_t st) {
+  cudaError_t e = cudaSuccess;
+  for (const auto& b : p.batches) {
+    e = (int)b.index.size() <= clip::kSmallTable
+            ? launch_norm<clip::kSmallTable>(p, b, in, part, st)
+            : launch_norm<clip::kTable>(p, b, in, part, st);
+    if (e != cudaSuccess) break;
+  }
+  return e;
+}
+
+lapl_status check(lapl_clip_plan* p, const void* const* grads, float* norm, void* workspace,
+                  size_t workspace_bytes, const char* where) {
+  if (!grads && !p->counts.empty()) return LAPL_ERR_INVALID_ARG;
+  if (!norm || !workspace) return LAPL_ERR_INVALID_ARG;
+  if (!ops::aligned(norm, 4) || !ops::aligned(workspace, 16)) return LAPL_ERR_ALIGNMENT;
+  size_t need = 0;
+  lapl_clip_workspace_size(p, &need);
+  if (workspace_bytes < need) return LAPL_ERR_WORKSPACE;
+  const lapl_status st = check_pointers(*p, grads);
+  if (st != LAPL_OK) return st;
+  return ops::check_device(p->device, p->last_error, where);
+}
+
+lapl_status create(const lapl_clip_config* cfg, int sms, int device, lapl_clip_plan** out) {
+  lapl_clip_plan* p = new lapl_clip_plan();
+  *out = p;
+  p->device = device;
+  p->counts.assign(cfg->counts, cfg->counts + cfg->tensors);
+  p->dtypes.assign(cfg->dtypes, cfg->dtypes + cfg->tensors);
+  p->spans.reserve(2 * p->counts.size());
+  p->parts = 0;
+  long long pieces = 0;
+  auto close = [&] {
+    auto& b = p->batches.back();
+    b.pieces = (int)pieces;
+    b.grid = (int)std::min<long long>(pieces, 4LL * sms);
+    b.first_part = p->parts;
+    p->parts += b.grid;
+    pieces = 0;
+  };
+  for (int i = 0; i < cfg->tensors; ++i) {
+    if (p->counts[i] == 0) continue;
+    const long long more = (p->counts[i] + clip::kPiece - 1) / clip::kPiece;
+    if (!p->batches.empty() && ((int)p->batches.back().index.size() == clip::kTable ||
+                                pieces + more > (1LL << 30))) {
+      close();
+      p->batches.emplace_back();
+    }
+    if (p->batches.empty()) p->batches.emplace_back();
+    p->batches.back().index.push_back(i);
+    pieces += more;
+  }
+  if (!p->batches.empty()) close();
+  return LAPL_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+lapl_status lapl_clip_create(const lapl_clip_config* cfg, lapl_clip_handle* out) {
+  if (!out) return LAPL_ERR_INVALID_ARG;
+  *out = nullptr;
+  const lapl_status st = validate(cfg);
+  if (st != LAPL_OK) return st;
+  int sms = 0, device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
+  if (e != cudaSuccess) return LAPL_ERR_CUDA;
+  lapl_clip_plan* p = nullptr;
+  try {
+    create(cfg, sms, device, &p);
+  } catch (const std::exception&) {   // out of host memory
+    delete p;
+    return LAPL_ERR_INVALID_ARG;
+  }
+  *out = p;
+  return LAPL_OK;
+}
+
+lapl_status lapl_clip_workspace_size(lapl_clip_handle p, size_t* bytes) {
+  if (!p || !bytes) return LAPL_ERR_INVALID_ARG;
+  *bytes = align_up((size_t)std::max(p->parts, 1) * sizeof(double2), kAlign);
+  return LAPL_OK;
+}
+
+lapl_status lapl_clip_norm(lapl_clip_handle p, const void* const* grads, float* norm,
+                           void* workspace, size_t workspace_bytes, void* stream) {
+  if (!p) return LAPL_ERR_INVALID_ARG;
+  const lapl_status st = check(p, grads, norm, workspace, workspace_bytes, "clip_norm/device");
+  if (st != LAPL_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  double2* part = static_cast<double2*>(workspace);
+  cudaError_t e = partials(*p, grads, part, s);
+  if (e == cudaSuccess) {
+    clip::clip_finish_kernel<<<1, clip::kThreads, 0, s>>>(part, p->parts, norm);
+    e = cudaGetLastError();
+  }
+  if (e != cudaSuccess) {
+    ops::set_error(p->last_error, e, "clip_norm");
+    return LAPL_ERR_CUDA;
+  }
+  return LAPL_OK;
+}
+
+lapl_status lapl_clip_apply(lapl_clip_handle p, const void* const* grads, void* const* outs,
+                            float max_norm, float* norm, void* workspace, size_t workspace_bytes,
+                            void* stream) {
+  if (!p) return LAPL_ERR_INVALID_ARG;
+  if (!(max_norm >= 0.f) || !isfinite(max_norm)) return LAPL_ERR_INVALID_ARG;
+  lapl_status st = check(p, grads, norm, workspace, workspace_bytes, "clip_apply/device");
+  if (st != LAPL_OK) return st;
+  void* const* to = outs ? outs : const_cast<void* const*>(grads);
+  st = check_pointers(*p, to);
+  if (st != LAPL_OK) return st;
+  if (overlapping(p, grads, to)) return LAPL_ERR_INVALID_ARG;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  double2* part = static_cast<double2*>(workspace);
+  cudaError_t e = partials(*p, grads, part, s);
+  for (size_t k = 0; k < p->batches.size() && e == cudaSuccess; ++k) {
+    const auto& b = p->batches[k];
+    float* out_norm = k == 0 ? norm : nullptr;
+    e = (int)b.index.size() <= clip::kSmallTable
+            ? launch_scale<clip::kSmallTable>(*p, b, grads, to, part, max_norm, out_norm, s)
+            : launch_scale<clip::kTable>(*p, b, grads, to, part, max_norm, out_norm, s);
+  }
+  if (e == cudaSuccess && p->batches.empty()) e = cudaMemsetAsync(norm, 0, sizeof(float), s);
+  if (e != cudaSuccess) {
+    ops::set_error(p->last_error, e, "clip_apply");
+    return LAPL_ERR_CUDA;
+  }
+  return LAPL_OK;
+}
+
+const char* lapl_clip_last_error(lapl_clip_handle p) { return p ? p->last_error : ""; }
+
+lapl_status lapl_clip_destroy(lapl_clip_handle p) {
+  delete p;
+  return LAPL_OK;
+}
+
+}  // extern "C"
