@@ -14,7 +14,7 @@
 // memory, every thread walks the maps of the runs before its own (at most 256 / lanes), and then
 // repeats its 16 steps from the true state: x and g are read from memory once and nothing but
 // maps is exchanged.  The CTA goes along the sequence tile by tile with the state in registers.
-// Where sequences and channels are too few to fill the GPU, a cluster of up to 8 CTAs takes
+// Where sequences and channels are too few to fill the GPU, a cluster of up to 16 CTAs takes
 // consecutive tiles at once and exchanges the tiles' maps through distributed shared memory.
 // The order of every composition is fixed, so results are the same bit for bit from call to call.
 //
@@ -35,7 +35,7 @@ namespace scan {
 
 constexpr int kT = LAPL_SCAN_CHUNK;   // tokens of a thread's run
 constexpr int kThreads = 256;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 constexpr int kMaxChannels = 64;      // channels of a tile: 32 lanes x 2
 
 struct Geo {
@@ -91,10 +91,22 @@ __device__ __forceinline__ void store_vec(void* base, long long e, const float (
   }
 }
 
-// z = 1 - a of a step that has a gate: sigmoid: 1 / (1 + exp(g)).
+// z = 1 - a = 1 / (1 + exp(g)) of the sigmoid gate.  exp(g) = 2^n 2^f with n = round(g log2 e) and
+// f = g log2 e - n by one fused step, so that the hardware's exponential sees |f| <= 1/2 and its
+// relative error (2 ulp) is not multiplied by |g|; 2^n is an exponent field.  g is held within
+// [-87, 88], where neither overflows (z is 1 and 6e-39 there); NaN passes through.
 __device__ __forceinline__ float sigmoid_z(float g) {
-  // expf overflows to infinity for g > 88.7: z = 0.
-  return __fdividef(1.f, 1.f + expf(g));
+  constexpr float kLog2e = 1.44269504f;
+  constexpr float kRound = 12582912.f;   // 1.5 2^23: adding it leaves the rounded value in the low bits
+  asm("min.NaN.f32 %0, %0, 0f42b00000;" : "+f"(g));   // 88
+  asm("max.NaN.f32 %0, %0, 0fc2ae0000;" : "+f"(g));   // -87
+  const float m = fmaf(g, kLog2e, kRound);
+  const float f = fmaf(g, kLog2e, -(m - kRound));
+  float e, z;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(f));
+  const float scale = __uint_as_float((__float_as_uint(m) << 23) + 0x3f800000u);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(z) : "f"(fmaf(e, scale, 1.f)));
+  return z;
 }
 
 // A step's decay as one register: a (decay gate) or z = 1 - a (sigmoid gate).
@@ -135,45 +147,59 @@ __device__ __forceinline__ void exchange(Shared& sm, int parity, int lane, int g
   for (int v = 0; v < V; ++v)
     sm.run[parity][group * cpb + lane * V + v] = make_float2(A[v], B[v]);
   __syncthreads();
-  float past[V];
+  const float2* runs = &sm.run[parity][(kDown ? (groups - 1) * cpb : 0) + lane * V];
+  const int step = kDown ? -cpb : cpb;
+  const int mine = kDown ? groups - 1 - group : group;   // runs before this one
+  if constexpr (!kCluster) {
+#pragma unroll 4
+    for (int k = 0; k < groups; ++k, runs += step) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) past[v] = carry[v];
-  if constexpr (kCluster) {
-    cg::cluster_group cl = cg::this_cluster();
-    // One thread a channel composes the CTA's runs and hands the map to every CTA of the cluster.
-    for (int ch = threadIdx.x; ch < cpb; ch += blockDim.x) {
-      float ta = 1.f, tb = 0.f;
-      for (int k = 0; k < groups; ++k) {
-        const float2 m = sm.run[parity][(kDown ? groups - 1 - k : k) * cpb + ch];
-        tb = fmaf(m.x, tb, m.y);
-        ta *= m.x;
+      for (int v = 0; v < V; ++v) {
+        if (k == mine) enter[v] = carry[v];
+        carry[v] = fmaf(runs[v].x, carry[v], runs[v].y);
       }
-      for (int r = 0; r < cluster; ++r)
-        *cl.map_shared_rank(&sm.tile[parity][rank][ch], r) = make_float2(ta, tb);
     }
-    cl.sync();
+  } else {
+    // One thread a channel composes the CTA's runs and hands the map to every CTA of the cluster.
+    if ((int)threadIdx.x < cpb) {
+      const float2* p = &sm.run[parity][(kDown ? (groups - 1) * cpb : 0) + threadIdx.x];
+      float ta = 1.f, tb = 0.f;
+#pragma unroll 4
+      for (int k = 0; k < groups; ++k, p += step) {
+        tb = fmaf(p->x, tb, p->y);
+        ta *= p->x;
+      }
+      float2* to = &sm.tile[parity][rank][threadIdx.x];
+      for (int r = 0; r < cluster; ++r)
+        *cg::this_cluster().map_shared_rank(to, r) = make_float2(ta, tb);
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    // Meanwhile, the map of the CTA's runs before this thread's.
+    float pa[V], pb[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      pa[v] = 1.f;
+      pb[v] = 0.f;
+    }
+#pragma unroll 4
+    for (int k = 0; k < mine; ++k, runs += step) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        pb[v] = fmaf(runs[v].x, pb[v], runs[v].y);
+        pa[v] *= runs[v].x;
+      }
+    }
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+#pragma unroll 4
     for (int k = 0; k < cluster; ++k) {
       const int r = kDown ? cluster - 1 - k : k;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        if (r == rank) past[v] = carry[v];
+        if (r == rank) enter[v] = fmaf(pa[v], carry[v], pb[v]);
         const float2 m = sm.tile[parity][r][lane * V + v];
         carry[v] = fmaf(m.x, carry[v], m.y);
       }
     }
-  }
-  for (int k = 0; k < groups; ++k) {
-    const int q = kDown ? groups - 1 - k : k;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      if (q == group) enter[v] = past[v];
-      const float2 m = sm.run[parity][q * cpb + lane * V + v];
-      past[v] = fmaf(m.x, past[v], m.y);
-    }
-  }
-  if constexpr (!kCluster) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) carry[v] = past[v];
   }
 }
 
@@ -199,12 +225,48 @@ __device__ __forceinline__ Place place_of(const Args& a) {
   return p;
 }
 
+// Where a thread's run of round t lies: its first place in processing order, and the address step
+// from one place to the next.
+struct Run {
+  int i0;            // clipped to N
+  long long row;     // of place i0
+};
+__device__ __forceinline__ Run run_of(const Args& a, const Place& p, int t, int tile) {
+  const long long start = ((long long)t * a.geo.cluster + p.rank) * tile + p.group * kT;
+  Run r;
+  r.i0 = (int)min(start, (long long)a.n);
+  r.row = p.s * a.n + (a.reverse ? p.len - 1 - r.i0 : r.i0);
+  return r;
+}
+
+// kT tokens of one tensor, zeros where `live` ends.
+template <bool k16, int V>
+__device__ __forceinline__ void load_run(uint32_t (&w)[kT], const void* base, const Run& r,
+                                         long long stride, int c, bool reverse, int live) {
+  constexpr int kBytes = k16 ? 2 : 4;
+  const char* q = reinterpret_cast<const char*>(base) + (r.row * stride + c) * kBytes;
+  const long long step = (reverse ? -stride : stride) * kBytes;
+  if (r.i0 + kT <= live) {
+#pragma unroll
+    for (int u = 0; u < kT; ++u) {
+      w[u] = load_raw<k16, V>(q, 0);
+      q += step;
+    }
+  } else {
+#pragma unroll
+    for (int u = 0; u < kT; ++u) {
+      w[u] = 0u;
+      if (r.i0 + u < live) w[u] = load_raw<k16, V>(q, 0);
+      q += step;
+    }
+  }
+}
+
 template <bool kIn16, bool kOut16, int V, bool kSig, bool kCluster>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 scan_forward_kernel(const Args a) {
   __shared__ Shared sm;
   const Place p = place_of<V>(a);
-  const long long row0 = p.s * a.n;
   float carry[V];
 #pragma unroll
   for (int v = 0; v < V; ++v)
@@ -213,24 +275,32 @@ scan_forward_kernel(const Args a) {
   const int live = p.on ? p.len : 0;
   // No CTA writes into another's shared memory before that one runs.
   if constexpr (kCluster) cg::this_cluster().sync();
+  uint32_t rx[kT], rg[kT];
+  Run run = run_of(a, p, 0, tile);
+  load_run<kIn16, V>(rx, a.x, run, a.x_stride, p.c, a.reverse, live);
+  load_run<kIn16, V>(rg, a.g, run, a.g_stride, p.c, a.reverse, live);
   for (int t = 0; t < a.geo.tiles; ++t) {
-    const long long start = ((long long)t * a.geo.cluster + p.rank) * tile + p.group * kT;
-    const int i0 = (int)min(start, (long long)a.n);
     float gate[kT][V], x[kT][V];
 #pragma unroll
     for (int u = 0; u < kT; ++u) {
-      const int i = i0 + u;
-      uint32_t rx = 0u, rg = 0u;
-      if (i < live) {
-        const long long row = row0 + (a.reverse ? p.len - 1 - i : i);
-        rx = load_raw<kIn16, V>(a.x, row * a.x_stride + p.c);
-        rg = load_raw<kIn16, V>(a.g, row * a.g_stride + p.c);
-      }
-      widen<kIn16, V>(rx, x[u]);
-      widen<kIn16, V>(rg, gate[u]);
+      widen<kIn16, V>(rx[u], x[u]);
+      widen<kIn16, V>(rg[u], gate[u]);
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-        gate[u][v] = i < live ? gate_of<kSig>(gate[u][v]) : identity_gate<kSig>();
+      for (int v = 0; v < V; ++v) gate[u][v] = gate_of<kSig>(gate[u][v]);
+    }
+    const Run now = run;
+    if (now.i0 + kT > live) {
+#pragma unroll
+      for (int u = 0; u < kT; ++u)
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          if (now.i0 + u >= live) gate[u][v] = identity_gate<kSig>();
+    }
+    // The next round's tokens are on their way while this one is exchanged and written.
+    if (t + 1 < a.geo.tiles) {
+      run = run_of(a, p, t + 1, tile);
+      load_run<kIn16, V>(rx, a.x, run, a.x_stride, p.c, a.reverse, live);
+      load_run<kIn16, V>(rg, a.g, run, a.g_stride, p.c, a.reverse, live);
     }
     float A[V], B[V], h[V];
 #pragma unroll
@@ -244,24 +314,36 @@ scan_forward_kernel(const Args a) {
       }
     exchange<V, kCluster, false>(sm, t & 1, p.lane, p.group, p.groups, a.geo.lanes, p.rank,
                                  a.geo.cluster, A, B, carry, h);
-    if (p.on && i0 < a.n) {
+    if (p.on && now.i0 < a.n) {
       if (a.states) {
-        float* st = a.states + (p.s * a.chunks + i0 / kT) * a.c + p.c;
+        float* st = a.states + (p.s * a.chunks + now.i0 / kT) * a.c + p.c;
 #pragma unroll
         for (int v = 0; v < V; ++v) st[v] = h[v];
       }
+      constexpr int kBytes = kOut16 ? 2 : 4;
+      char* q = reinterpret_cast<char*>(a.out) + (now.row * a.c + p.c) * kBytes;
+      const long long by = (a.reverse ? -(long long)a.c : (long long)a.c) * kBytes;
+      if (now.i0 + kT <= live) {
 #pragma unroll
-      for (int u = 0; u < kT; ++u) {
-        const int i = i0 + u;
-        float y[V];
+        for (int u = 0; u < kT; ++u) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          h[v] = step<kSig>(gate[u][v], x[u][v], h[v]);
-          y[v] = i < live ? h[v] : 0.f;
+          for (int v = 0; v < V; ++v) h[v] = step<kSig>(gate[u][v], x[u][v], h[v]);
+          store_vec<kOut16, V>(q, 0, h);
+          q += by;
         }
-        if (i < a.n) {
-          const long long row = row0 + (a.reverse && i < live ? p.len - 1 - i : i);
-          store_vec<kOut16, V>(a.out, row * a.c + p.c, y);
+      } else {
+#pragma unroll
+        for (int u = 0; u < kT; ++u) {
+          const int i = now.i0 + u;
+#pragma unroll
+          for (int v = 0; v < V; ++v) h[v] = step<kSig>(gate[u][v], x[u][v], h[v]);
+          if (i < live) {
+            store_vec<kOut16, V>(q, 0, h);
+          } else if (i < a.n) {
+            const float none[V] = {};
+            store_vec<kOut16, V>(a.out, (p.s * a.n + i) * a.c + p.c, none);
+          }
+          q += by;
         }
       }
     }
@@ -273,11 +355,10 @@ scan_forward_kernel(const Args a) {
 }
 
 template <bool kIn16, bool kGrad16, int V, bool kSig, bool kCluster>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 scan_backward_kernel(const Args a) {
   __shared__ Shared sm;
   const Place p = place_of<V>(a);
-  const long long row0 = p.s * a.n;
   float carry[V];
 #pragma unroll
   for (int v = 0; v < V; ++v)
@@ -286,38 +367,45 @@ scan_backward_kernel(const Args a) {
   const int live = p.on ? p.len : 0;
   if constexpr (kCluster) cg::this_cluster().sync();
   for (int t = a.geo.tiles - 1; t >= 0; --t) {
-    const long long start = ((long long)t * a.geo.cluster + p.rank) * tile + p.group * kT;
-    const int i0 = (int)min(start, (long long)a.n);
+    const Run run = run_of(a, p, t, tile);
     float gate[kT][V], x[kT][V], dh[kT][V], h[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      h[v] = p.on && i0 < a.n ? a.states[(p.s * a.chunks + i0 / kT) * a.c + p.c + v] : 0.f;
-#pragma unroll
-    for (int u = 0; u < kT; ++u) {
-      const int i = i0 + u;
-      uint32_t rx = 0u, rg = 0u, rd = 0u;
-      if (i < live) {
-        const long long row = row0 + (a.reverse ? p.len - 1 - i : i);
-        rx = load_raw<kIn16, V>(a.x, row * a.x_stride + p.c);
-        rg = load_raw<kIn16, V>(a.g, row * a.g_stride + p.c);
-        if constexpr (!kGrad16 && V == 2) {
-          const float2 d = *reinterpret_cast<const float2*>(
-              reinterpret_cast<const float*>(a.dout) + row * a.c + p.c);
-          dh[u][0] = d.x;
-          dh[u][V - 1] = d.y;
-        } else {
-          rd = load_raw<kGrad16, V>(a.dout, row * a.c + p.c);
-        }
-      } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v) dh[u][v] = 0.f;
-      }
-      if constexpr (kGrad16 || V == 1) widen<kGrad16, V>(rd, dh[u]);
-      widen<kIn16, V>(rx, x[u]);
-      widen<kIn16, V>(rg, gate[u]);
+    {
+      uint32_t rx[kT], rg[kT];
+      load_run<kIn16, V>(rg, a.g, run, a.g_stride, p.c, a.reverse, live);
+      load_run<kIn16, V>(rx, a.x, run, a.x_stride, p.c, a.reverse, live);
 #pragma unroll
       for (int v = 0; v < V; ++v)
-        gate[u][v] = i < live ? gate_of<kSig>(gate[u][v]) : identity_gate<kSig>();
+        h[v] = p.on && run.i0 < a.n ? a.states[(p.s * a.chunks + run.i0 / kT) * a.c + p.c + v] : 0.f;
+      if constexpr (kGrad16 || V == 1) {
+        uint32_t rd[kT];
+        load_run<kGrad16, V>(rd, a.dout, run, a.c, p.c, a.reverse, live);
+#pragma unroll
+        for (int u = 0; u < kT; ++u) widen<kGrad16, V>(rd[u], dh[u]);
+      } else {
+        const float* q = reinterpret_cast<const float*>(a.dout) + run.row * a.c + p.c;
+#pragma unroll
+        for (int u = 0; u < kT; ++u) {
+          float2 d = make_float2(0.f, 0.f);
+          if (run.i0 + u < live) d = *reinterpret_cast<const float2*>(q);
+          dh[u][0] = d.x;
+          dh[u][V - 1] = d.y;
+          q += a.reverse ? -a.c : a.c;
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kT; ++u) {
+        widen<kIn16, V>(rx[u], x[u]);
+        widen<kIn16, V>(rg[u], gate[u]);
+#pragma unroll
+        for (int v = 0; v < V; ++v) gate[u][v] = gate_of<kSig>(gate[u][v]);
+      }
+    }
+    if (run.i0 + kT > live) {
+#pragma unroll
+      for (int u = 0; u < kT; ++u)
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+          if (run.i0 + u >= live) gate[u][v] = identity_gate<kSig>();
     }
     // The slope of a step in its decay, h_{i-1} - x_i or h_{i-1}, in x's place.
 #pragma unroll
@@ -340,10 +428,16 @@ scan_backward_kernel(const Args a) {
       }
     exchange<V, kCluster, true>(sm, t & 1, p.lane, p.group, p.groups, a.geo.lanes, p.rank,
                                 a.geo.cluster, A, B, carry, E);
-    if (p.on && i0 < a.n) {
+    if (p.on && run.i0 < a.n) {
+      constexpr int kBytes = kGrad16 ? 2 : 4;
+      const int last = run.i0 + kT - 1;
+      const long long row = run.row + (a.reverse ? 1 - kT : kT - 1);
+      char* qx = reinterpret_cast<char*>(a.dx) + (row * a.x_stride + p.c) * kBytes;
+      char* qg = reinterpret_cast<char*>(a.dg) + (row * a.g_stride + p.c) * kBytes;
+      const long long bx = (a.reverse ? a.x_stride : -a.x_stride) * kBytes;
+      const long long bg = (a.reverse ? a.g_stride : -a.g_stride) * kBytes;
 #pragma unroll
       for (int u = kT - 1; u >= 0; --u) {
-        const int i = i0 + u;
         float dx[V], dg[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -351,13 +445,18 @@ scan_backward_kernel(const Args a) {
           E[v] = decayed<kSig>(gate[u][v], D);
           dx[v] = kSig ? gate[u][v] * D : D;
           dg[v] = kSig ? gate[u][v] * x[u][v] * E[v] : x[u][v] * D;
-          if (i >= live) dx[v] = dg[v] = 0.f;
         }
-        if (i < a.n) {
-          const long long row = row0 + (a.reverse && i < live ? p.len - 1 - i : i);
-          store_vec<kGrad16, V>(a.dx, row * a.x_stride + p.c, dx);
-          store_vec<kGrad16, V>(a.dg, row * a.g_stride + p.c, dg);
+        if (last < live || run.i0 + u < live) {
+          store_vec<kGrad16, V>(qx, 0, dx);
+          store_vec<kGrad16, V>(qg, 0, dg);
+        } else if (run.i0 + u < a.n) {
+          const float none[V] = {};
+          const long long at = p.s * a.n + run.i0 + u;
+          store_vec<kGrad16, V>(a.dx, at * a.x_stride + p.c, none);
+          store_vec<kGrad16, V>(a.dg, at * a.g_stride + p.c, none);
         }
+        qx += bx;
+        qg += bg;
       }
     }
   }
@@ -406,26 +505,30 @@ Kernel pick(bool in16, bool other16, bool sig, int v, bool cluster) {
 Geo geometry(const lapl_scan_config& c, int num_sms, int v) {
   Geo g;
   const int need = (c.channels + v - 1) / v;   // lanes' worth of channels
+  const int runs = (c.tokens + kT - 1) / kT;
   // The most lanes of which at most a quarter are idle: full 128-byte rows where there are
   // channels for them.
   g.lanes = 32;
   while (g.lanes > 4 && 3LL * ((need + g.lanes - 1) / g.lanes) * g.lanes > 4LL * need)
     g.lanes >>= 1;
+  // Two CTAs for every SM: by splitting the tokens over a cluster, and where that is not enough
+  // the channels further, down to 32-byte pieces of a row.
+  for (;; g.lanes >>= 1) {
+    g.blocks = (need + g.lanes - 1) / g.lanes;
+    int groups = kThreads / g.lanes;
+    while (groups > 1 && groups / 2 >= runs && groups / 2 * g.lanes >= 32) groups >>= 1;
+    g.threads = groups * g.lanes;
+    const long long units = (long long)c.sequences * g.blocks;
+    g.cluster = 1;
+    while (g.cluster < kMaxCluster && units * g.cluster * 5 < 8LL * num_sms &&
+           g.cluster * groups < runs)
+      g.cluster *= 2;
+    const int per_round = g.cluster * groups;
+    g.tiles = (runs + per_round - 1) / per_round;
+    if (g.lanes <= 8 || g.tiles == 1 || units * g.cluster * 5 >= 8LL * num_sms) break;
+  }
   g.lanes_log2 = 0;
   while ((1 << g.lanes_log2) < g.lanes) ++g.lanes_log2;
-  g.blocks = (need + g.lanes - 1) / g.lanes;
-  const int runs = (c.tokens + kT - 1) / kT;
-  int groups = kThreads / g.lanes;
-  while (groups > 1 && groups / 2 >= runs && groups / 2 * g.lanes >= 32) groups >>= 1;
-  g.threads = groups * g.lanes;
-  // Two CTAs for every SM, by splitting the tokens where the channels do not give them.
-  const long long units = (long long)c.sequences * g.blocks;
-  g.cluster = 1;
-  while (g.cluster < kMaxCluster && units * g.cluster < 2LL * num_sms &&
-         g.cluster * groups < runs)
-    g.cluster *= 2;
-  const int per_round = g.cluster * groups;
-  g.tiles = (runs + per_round - 1) / per_round;
   return g;
 }
 
@@ -441,8 +544,8 @@ lapl_status validate(const lapl_scan_config* c) {
       (c->g_stride != 0 && c->g_stride < c->channels))
     return LAPL_ERR_INVALID_ARG;
   if (c->tokens > (1 << 30) || c->channels > (1 << 24)) return LAPL_ERR_UNSUPPORTED;
-  // The grid has up to 8 CTAs for each sequence and each 4 channels.
-  if ((long long)c->sequences * ((c->channels + 3) / 4) > (1LL << 27)) return LAPL_ERR_UNSUPPORTED;
+  // The grid has up to 16 CTAs for each sequence and each 4 channels.
+  if ((long long)c->sequences * ((c->channels + 3) / 4) > (1LL << 26)) return LAPL_ERR_UNSUPPORTED;
   return LAPL_OK;
 }
 
@@ -485,7 +588,11 @@ lapl_status launch(lapl_scan_plan* p, scan::Kernel k, scan::Args& a, int v, void
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = a.geo.cluster > 1 ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, a);
+  cudaError_t e = cudaSuccess;
+  if (a.geo.cluster > 8)
+    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k),
+                             cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, k, a);
   if (e != cudaSuccess) {
     ops::set_error(p->last_error, e, where);
     return LAPL_ERR_CUDA;
