@@ -1,8 +1,9 @@
 // clip.cu -- global norm of many gradient tensors and clipping: lapl_clip_* of
 // include/lapl_ops.h.
 //
-// The tensors are cut into pieces of kPiece values; the piece table travels as a kernel parameter
-// (no table in device memory, nothing to upload), for up to kTable tensors a launch.  First pass:
+// The tensors are cut into pieces of 2048 to 16384 values (a power of two: four or more for each CTA
+// where the values give them); the table of tensors travels as a kernel parameter (no table in
+// device memory, nothing to upload), for up to kTable tensors a launch.  First pass:
 // CTA b sums the squares of pieces b, b + grid, ... and writes one partial.  Second pass: every CTA
 // sums all partials in the same order, so each has the same norm to the last bit, and scales its
 // pieces.  HBM-bound: the first pass reads every value, the second reads and writes it.
@@ -22,7 +23,8 @@ namespace lapl {
 namespace clip {
 
 constexpr int kThreads = 512;
-constexpr int kPiece = 16384;        // values
+constexpr int kMinPiece = 11, kMaxPiece = 14;   // log2 of a piece's values
+constexpr int kUnroll = 4;           // 16-byte loads of a thread in flight
 constexpr int kTable = 1000;         // tensors of a launch: 20 KB of its 32 KB of parameters
 constexpr int kSmallTable = 64;
 constexpr float kLow = 34359738368.f;                // 2^35
@@ -36,6 +38,7 @@ struct Table {
   int last[N];          // values of its last piece
   unsigned char kind[N];   // lapl_dtype
   int tensors;
+  int piece;            // log2 of a piece's values
 };
 
 // One piece: where it is and how many values it has.
@@ -54,10 +57,10 @@ __device__ __forceinline__ Piece piece_of(const Table<N>& t, int i) {
   }
   Piece p;
   p.half = t.kind[lo] == LAPL_BF16;
-  const long long off = (long long)(i - t.first[lo]) * kPiece * (p.half ? 2 : 4);
+  const long long off = ((long long)(i - t.first[lo]) << t.piece) * (p.half ? 2 : 4);
   p.in = reinterpret_cast<const char*>(t.in[lo]) + off;
   p.out = t.out[lo] ? reinterpret_cast<char*>(t.out[lo]) + off : nullptr;
-  p.count = i + 1 == t.first[lo + 1] ? t.last[lo] : kPiece;
+  p.count = i + 1 == t.first[lo + 1] ? t.last[lo] : 1 << t.piece;
   return p;
 }
 
@@ -68,11 +71,30 @@ struct Sums {
     low = fmaf(l, l, low);
     high = fmaf(h, h, high);
   }
+  template <bool kHalf>
+  __device__ __forceinline__ void add(uint32_t w) {
+    if constexpr (kHalf) {
+      add(bf16_lo(w));
+      add(bf16_hi(w));
+    } else {
+      add(__uint_as_float(w));
+    }
+  }
 };
 
-__device__ __forceinline__ float value_of(const char* p, bool half, int i) {
-  return half ? ops::bf16_bits(reinterpret_cast<const uint16_t*>(p)[i])
-              : reinterpret_cast<const float*>(p)[i];
+// Calls use(k, v) for each of n 16-byte vectors at p (k: its index), kUnroll of a thread's loads
+// at a time.
+template <class Use>
+__device__ __forceinline__ void each_vector(const uint4* p, int n, Use use) {
+  int k = threadIdx.x;
+  for (; k + (kUnroll - 1) * kThreads < n; k += kUnroll * kThreads) {
+    uint4 v[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) v[u] = p[k + u * kThreads];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) use(k + u * kThreads, v[u]);
+  }
+  for (; k < n; k += kThreads) use(k, p[k]);
 }
 
 // Sum over the CTA, the same double in every thread (fixed order).
@@ -92,36 +114,40 @@ __device__ __forceinline__ double2 block_sum(double low, double high, double2* s
   return s;
 }
 
+// The squares of one piece.
+template <bool kHalf>
+__device__ __forceinline__ Sums squares(const Piece& p) {
+  constexpr int kBytes = kHalf ? 2 : 4;
+  // Values before the first 16-byte boundary, 16 bytes at a time, and the rest.
+  const int head = min(p.count, (int)((16 - ((uintptr_t)p.in & 15)) & 15) / kBytes);
+  const int vectors = (p.count - head) * kBytes / 16;
+  Sums s = {0.f, 0.f};
+  each_vector(reinterpret_cast<const uint4*>(p.in + head * kBytes), vectors,
+              [&](int, const uint4& v) {
+                s.add<kHalf>(v.x);
+                s.add<kHalf>(v.y);
+                s.add<kHalf>(v.z);
+                s.add<kHalf>(v.w);
+              });
+  const int body = vectors * 16 / kBytes;
+  for (int k = threadIdx.x; k < p.count - body; k += kThreads) {
+    const int e = k < head ? k : k + body;
+    if constexpr (kHalf) s.add(ops::bf16_bits(reinterpret_cast<const uint16_t*>(p.in)[e]));
+    else s.add(reinterpret_cast<const float*>(p.in)[e]);
+  }
+  return s;
+}
+
 template <int N>
 __global__ void __launch_bounds__(kThreads)
 clip_norm_kernel(const __grid_constant__ Table<N> t, double2* part) {
   __shared__ double2 sm[kThreads / 32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   double low = 0., high = 0.;
   const int pieces = t.first[t.tensors];
   for (int i = blockIdx.x; i < pieces; i += gridDim.x) {
     const Piece p = piece_of(t, i);
-    const int eb = p.half ? 2 : 4;
-    // Values before the first 16-byte boundary, 16 bytes at a time, and the rest.
-    const int head = min(p.count, (int)((16 - ((uintptr_t)p.in & 15)) & 15) / eb);
-    const int vectors = (p.count - head) * eb / 16;
-    Sums s = {0.f, 0.f};
-    const uint4* v = reinterpret_cast<const uint4*>(p.in + head * eb);
-    for (int k = threadIdx.x; k < vectors; k += kThreads) {
-      const uint4 r = v[k];
-      const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        if (p.half) {
-          s.add(bf16_lo(w[u]));
-          s.add(bf16_hi(w[u]));
-        } else {
-          s.add(__uint_as_float(w[u]));
-        }
-      }
-    }
-    const int body = vectors * 16 / eb;
-    for (int k = threadIdx.x; k < p.count - body; k += kThreads)
-      s.add(value_of(p.in, p.half, k < head ? k : k + body));
+    const Sums s = p.half ? squares<true>(p) : squares<false>(p);
     low += s.low;
     high += s.high;
   }
@@ -144,9 +170,40 @@ __device__ __forceinline__ float norm_of(const double2* part, int parts, double2
 __global__ void __launch_bounds__(kThreads)
 clip_finish_kernel(const double2* part, int parts, float* norm) {
   __shared__ double2 sm[kThreads / 32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the partials are written
   double exact;
   const float v = norm_of(part, parts, sm, &exact);
   if (threadIdx.x == 0) *norm = v;
+}
+
+// One piece to its output, times scale where kScale.  Values are read and written for the last
+// time: L2 keeps what the pieces still to come need.
+template <bool kHalf, bool kScale>
+__device__ __forceinline__ void copy_piece(const Piece& p, float scale) {
+  constexpr int kBytes = kHalf ? 2 : 4;
+  auto scaled = [&](uint32_t w) {
+    if constexpr (!kScale) return w;
+    else if constexpr (kHalf) return ops::pack_bf16(bf16_lo(w) * scale, bf16_hi(w) * scale);
+    else return __float_as_uint(__uint_as_float(w) * scale);
+  };
+  const bool together = (((uintptr_t)p.in ^ (uintptr_t)p.out) & 15) == 0;
+  const int head =
+      together ? min(p.count, (int)((16 - ((uintptr_t)p.in & 15)) & 15) / kBytes) : 0;
+  const int vectors = together ? (p.count - head) * kBytes / 16 : 0;
+  uint4* out = reinterpret_cast<uint4*>(p.out + head * kBytes);
+  each_vector(reinterpret_cast<const uint4*>(p.in + head * kBytes), vectors,
+              [&](int k, const uint4& v) {
+                __stcs(out + k, make_uint4(scaled(v.x), scaled(v.y), scaled(v.z), scaled(v.w)));
+              });
+  const int body = vectors * 16 / kBytes;
+  for (int k = threadIdx.x; k < p.count - body; k += kThreads) {
+    const int e = k < head ? k : k + body;
+    if constexpr (kHalf)
+      reinterpret_cast<uint16_t*>(p.out)[e] =
+          (uint16_t)scaled(reinterpret_cast<const uint16_t*>(p.in)[e]);
+    else
+      reinterpret_cast<uint32_t*>(p.out)[e] = scaled(reinterpret_cast<const uint32_t*>(p.in)[e]);
+  }
 }
 
 template <int N>
@@ -154,6 +211,7 @@ __global__ void __launch_bounds__(kThreads)
 clip_scale_kernel(const __grid_constant__ Table<N> t, const double2* part, int parts, float max_norm,
                   float* norm) {
   __shared__ double2 sm[kThreads / 32];
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the partials are written
   double exact;
   const float v = norm_of(part, parts, sm, &exact);
   if (blockIdx.x == 0 && threadIdx.x == 0 && norm) *norm = v;
@@ -163,36 +221,12 @@ clip_scale_kernel(const __grid_constant__ Table<N> t, const double2* part, int p
   // Last pieces first: those the first pass has left in L2.
   for (int i = pieces - 1 - (int)blockIdx.x; i >= 0; i -= gridDim.x) {
     const Piece p = piece_of(t, i);
-    if (!clip && p.in == p.out) continue;
-    const int eb = p.half ? 2 : 4;
-    const bool together = (((uintptr_t)p.in ^ (uintptr_t)p.out) & 15) == 0;
-    const int head = together ? min(p.count, (int)((16 - ((uintptr_t)p.in & 15)) & 15) / eb) : 0;
-    const int vectors = together ? (p.count - head) * eb / 16 : 0;
-    const uint4* in = reinterpret_cast<const uint4*>(p.in + head * eb);
-    uint4* out = reinterpret_cast<uint4*>(p.out + head * eb);
-    for (int k = threadIdx.x; k < vectors; k += kThreads) {
-      const uint4 r = in[k];
-      uint32_t w[4] = {r.x, r.y, r.z, r.w};
-      if (clip) {
-#pragma unroll
-        for (int u = 0; u < 4; ++u)
-          w[u] = p.half ? ops::pack_bf16(bf16_lo(w[u]) * scale, bf16_hi(w[u]) * scale)
-                        : __float_as_uint(__uint_as_float(w[u]) * scale);
-      }
-      out[k] = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-    const int body = vectors * 16 / eb;
-    for (int k = threadIdx.x; k < p.count - body; k += kThreads) {
-      const int e = k < head ? k : k + body;
-      if (p.half) {
-        const uint16_t raw = reinterpret_cast<const uint16_t*>(p.in)[e];
-        reinterpret_cast<uint16_t*>(p.out)[e] =
-            clip ? (uint16_t)ops::pack_bf16(ops::bf16_bits(raw) * scale, 0.f) : raw;
-      } else {
-        const uint32_t raw = reinterpret_cast<const uint32_t*>(p.in)[e];
-        reinterpret_cast<uint32_t*>(p.out)[e] =
-            clip ? __float_as_uint(__uint_as_float(raw) * scale) : raw;
-      }
+    if (clip) {
+      if (p.half) copy_piece<true, true>(p, scale);
+      else copy_piece<false, true>(p, scale);
+    } else if (p.in != p.out) {
+      if (p.half) copy_piece<true, false>(p, scale);
+      else copy_piece<false, false>(p, scale);
     }
   }
 }
@@ -205,6 +239,7 @@ struct lapl_clip_plan {
   std::vector<int> dtypes;
   struct Batch {       // the tensors of one launch
     std::vector<int> index;   // those with values
+    int piece;                // log2 of a piece's values
     int pieces, grid, first_part;
   };
   std::vector<Batch> batches;
@@ -237,14 +272,30 @@ void fill(const lapl_clip_plan& p, const lapl_clip_plan::Batch& b, const void* c
     t->in[k] = in[i];
     t->out[k] = out ? out[i] : nullptr;
     t->first[k] = first;
-    const long long pieces = (p.counts[i] + clip::kPiece - 1) / clip::kPiece;
+    const long long pieces = ((p.counts[i] - 1) >> b.piece) + 1;
     first += (int)pieces;
-    t->last[k] = (int)(p.counts[i] - (pieces - 1) * clip::kPiece);
+    t->last[k] = (int)(p.counts[i] - ((pieces - 1) << b.piece));
     t->kind[k] = (unsigned char)p.dtypes[i];
     ++k;
   }
   t->first[k] = first;
   t->tensors = k;
+  t->piece = b.piece;
+}
+
+// dependent: placed before the kernel before it has ended, for whose end it waits itself.
+template <class... P, class... A>
+cudaError_t launch(void (*kernel)(P...), int grid, bool dependent, cudaStream_t st, const A&... a) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(clip::kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = dependent ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, a...);
 }
 
 template <int N>
@@ -252,17 +303,15 @@ cudaError_t launch_norm(const lapl_clip_plan& p, const lapl_clip_plan::Batch& b,
                         const void* const* in, double2* part, cudaStream_t st) {
   clip::Table<N> t;
   fill(p, b, in, nullptr, &t);
-  clip::clip_norm_kernel<N><<<b.grid, clip::kThreads, 0, st>>>(t, part + b.first_part);
-  return cudaGetLastError();
+  return launch(clip::clip_norm_kernel<N>, b.grid, false, st, t, part + b.first_part);
 }
 template <int N>
 cudaError_t launch_scale(const lapl_clip_plan& p, const lapl_clip_plan::Batch& b,
                          const void* const* in, void* const* out, const double2* part,
-                         float max_norm, float* norm, cudaStream_t st) {
+                         float max_norm, float* norm, bool dependent, cudaStream_t st) {
   clip::Table<N> t;
   fill(p, b, in, out, &t);
-  clip::clip_scale_kernel<N><<<b.grid, clip::kThreads, 0, st>>>(t, part, p.parts, max_norm, norm);
-  return cudaGetLastError();
+  return launch(clip::clip_scale_kernel<N>, b.grid, dependent, st, t, part, p.parts, max_norm, norm);
 }
 
 lapl_status check_pointers(const lapl_clip_plan& p, const void* const* a) {
@@ -330,28 +379,33 @@ lapl_status create(const lapl_clip_config* cfg, int sms, int device, lapl_clip_p
   p->dtypes.assign(cfg->dtypes, cfg->dtypes + cfg->tensors);
   p->spans.reserve(2 * p->counts.size());
   p->parts = 0;
+  // Tensors with values, kTable to a launch and at most 2^30 of the largest pieces.
   long long pieces = 0;
-  auto close = [&] {
-    auto& b = p->batches.back();
-    b.pieces = (int)pieces;
-    b.grid = (int)std::min<long long>(pieces, 4LL * sms);
-    b.first_part = p->parts;
-    p->parts += b.grid;
-    pieces = 0;
-  };
   for (int i = 0; i < cfg->tensors; ++i) {
     if (p->counts[i] == 0) continue;
-    const long long more = (p->counts[i] + clip::kPiece - 1) / clip::kPiece;
-    if (!p->batches.empty() && ((int)p->batches.back().index.size() == clip::kTable ||
-                                pieces + more > (1LL << 30))) {
-      close();
+    const long long more = ((p->counts[i] - 1) >> clip::kMaxPiece) + 1;
+    if (p->batches.empty() || (int)p->batches.back().index.size() == clip::kTable ||
+        pieces + more > (1LL << 30)) {
       p->batches.emplace_back();
+      pieces = 0;
     }
-    if (p->batches.empty()) p->batches.emplace_back();
     p->batches.back().index.push_back(i);
     pieces += more;
   }
-  if (!p->batches.empty()) close();
+  const long long ctas = 4LL * sms;   // of 512 threads: all resident at once
+  for (auto& b : p->batches) {
+    auto count = [&](int log2) {
+      long long n = 0;
+      for (const int i : b.index) n += ((p->counts[i] - 1) >> log2) + 1;
+      return n;
+    };
+    b.piece = clip::kMaxPiece;
+    while (b.piece > clip::kMinPiece && count(b.piece) < 4 * ctas) --b.piece;
+    b.pieces = (int)count(b.piece);
+    b.grid = (int)std::min<long long>(b.pieces, ctas);
+    b.first_part = p->parts;
+    p->parts += b.grid;
+  }
   return LAPL_OK;
 }
 
@@ -394,8 +448,8 @@ lapl_status lapl_clip_norm(lapl_clip_handle p, const void* const* grads, float* 
   double2* part = static_cast<double2*>(workspace);
   cudaError_t e = partials(*p, grads, part, s);
   if (e == cudaSuccess) {
-    clip::clip_finish_kernel<<<1, clip::kThreads, 0, s>>>(part, p->parts, norm);
-    e = cudaGetLastError();
+    e = launch(clip::clip_finish_kernel, 1, p->batches.size() == 1, s,
+               static_cast<const double2*>(part), p->parts, norm);
   }
   if (e != cudaSuccess) {
     ops::set_error(p->last_error, e, "clip_norm");
@@ -418,12 +472,15 @@ lapl_status lapl_clip_apply(lapl_clip_handle p, const void* const* grads, void* 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   double2* part = static_cast<double2*>(workspace);
   cudaError_t e = partials(*p, grads, part, s);
+  // One launch after one: the second may be placed early.  (Of several, a later one would only wait
+  // for the one just before it.)
+  const bool alone = p->batches.size() == 1;
   for (size_t k = 0; k < p->batches.size() && e == cudaSuccess; ++k) {
     const auto& b = p->batches[k];
     float* out_norm = k == 0 ? norm : nullptr;
     e = (int)b.index.size() <= clip::kSmallTable
-            ? launch_scale<clip::kSmallTable>(*p, b, grads, to, part, max_norm, out_norm, s)
-            : launch_scale<clip::kTable>(*p, b, grads, to, part, max_norm, out_norm, s);
+            ? launch_scale<clip::kSmallTable>(*p, b, grads, to, part, max_norm, out_norm, alone, s)
+            : launch_scale<clip::kTable>(*p, b, grads, to, part, max_norm, out_norm, alone, s);
   }
   if (e == cudaSuccess && p->batches.empty()) e = cudaMemsetAsync(norm, 0, sizeof(float), s);
   if (e != cudaSuccess) {
