@@ -1,7 +1,7 @@
 // clip.cu -- global norm of many gradient tensors and clipping: lapl_clip_* of
 // include/lapl_ops.h.
 //
-// The tensors are cut into pieces of 2048 to 16384 values (a power of two: four or more for each CTA
+// The tensors are cut into pieces of 2048 to 65536 values (a power of two: four or more for each CTA
 // where the values give them); the table of tensors travels as a kernel parameter (no table in
 // device memory, nothing to upload), for up to kTable tensors a launch.  First pass:
 // CTA b sums the squares of pieces b, b + grid, ... and writes one partial.  Second pass: every CTA
@@ -12,7 +12,7 @@
 // are kept: of (x 2^35)^2, exact enough for every value between 2^-98 and 2^28, and of (x 2^-72)^2
 // for what is larger.  The first is used unless it overflows; then some |x| is 2^24 or more, against
 // which what the second loses is nothing.  Partial sums are fp32 over at most some thousand values
-// of one thread, then double.
+// of one thread, then pairs of floats.
 #include <algorithm>
 #include <new>
 #include <vector>
@@ -23,7 +23,7 @@ namespace lapl {
 namespace clip {
 
 constexpr int kThreads = 512;
-constexpr int kMinPiece = 11, kMaxPiece = 14;   // log2 of a piece's values
+constexpr int kMinPiece = 11, kMaxPiece = 16;   // log2 of a piece's values
 constexpr int kUnroll = 4;           // 16-byte loads of a thread in flight
 constexpr int kTable = 1000;         // tensors of a launch: 20 KB of its 32 KB of parameters
 constexpr int kSmallTable = 64;
@@ -97,20 +97,43 @@ __device__ __forceinline__ void each_vector(const uint4* p, int n, Use use) {
   for (; k < n; k += kThreads) use(k, p[k]);
 }
 
-// Sum over the CTA, the same double in every thread (fixed order).
-__device__ __forceinline__ double2 block_sum(double low, double high, double2* sm) {
-  for (int o = 16; o > 0; o >>= 1) {
-    low += __shfl_xor_sync(0xffffffffu, low, o);
-    high += __shfl_xor_sync(0xffffffffu, high, o);
+// A sum held as two floats, its value and what that lost (Knuth's two-sum): 48 bits without the
+// double-precision units, of which this GPU has few (sums in double took 36 us of a pass of 57).
+// Where the sum is not finite, hi says so and lo nothing.
+struct Pair {
+  float hi, lo;
+  __device__ __forceinline__ void add(float v, float v_lo = 0.f) {
+    const float s = hi + v, b = s - hi;
+    lo += (hi - (s - b)) + (v - b) + v_lo;
+    hi = s;
   }
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = make_double2(low, high);
-  __syncthreads();
-  double2 s = sm[0];
-  for (int k = 1; k < kThreads / 32; ++k) {
-    s.x += sm[k].x;
-    s.y += sm[k].y;
+  __device__ __forceinline__ float value() const { return isfinite(hi) ? hi + lo : hi; }
+};
+struct Pairs {
+  Pair low, high;
+  __device__ __forceinline__ void add(const Pairs& o) {
+    low.add(o.low.hi, o.low.lo);
+    high.add(o.high.hi, o.high.lo);
   }
+};
+
+// Sum over the CTA in thread 0 (fixed order).
+__device__ __forceinline__ Pairs block_sum(Pairs s, Pairs* sm) {
+  auto across = [](Pairs s, int n) {
+    for (int o = n / 2; o > 0; o >>= 1) {
+      Pairs other;
+      other.low.hi = __shfl_down_sync(0xffffffffu, s.low.hi, o);
+      other.low.lo = __shfl_down_sync(0xffffffffu, s.low.lo, o);
+      other.high.hi = __shfl_down_sync(0xffffffffu, s.high.hi, o);
+      other.high.lo = __shfl_down_sync(0xffffffffu, s.high.lo, o);
+      s.add(other);
+    }
+    return s;
+  };
+  s = across(s, 32);
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = s;
+  __syncthreads();
+  if (threadIdx.x < 32) s = across(sm[threadIdx.x & (kThreads / 32 - 1)], kThreads / 32);
   return s;
 }
 
@@ -140,39 +163,40 @@ __device__ __forceinline__ Sums squares(const Piece& p) {
 
 template <int N>
 __global__ void __launch_bounds__(kThreads)
-clip_norm_kernel(const __grid_constant__ Table<N> t, double2* part) {
-  __shared__ double2 sm[kThreads / 32];
+clip_norm_kernel(const __grid_constant__ Table<N> t, Pairs* part) {
+  __shared__ Pairs sm[kThreads / 32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  double low = 0., high = 0.;
+  Pairs sum = {};
   const int pieces = t.first[t.tensors];
   for (int i = blockIdx.x; i < pieces; i += gridDim.x) {
     const Piece p = piece_of(t, i);
     const Sums s = p.half ? squares<true>(p) : squares<false>(p);
-    low += s.low;
-    high += s.high;
+    sum.low.add(s.low);
+    sum.high.add(s.high);
   }
-  const double2 sum = block_sum(low, high, sm);
+  sum = block_sum(sum, sm);
   if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
 
-// The norm from all partials.
-__device__ __forceinline__ float norm_of(const double2* part, int parts, double2* sm, double* exact) {
-  double low = 0., high = 0.;
-  for (int k = threadIdx.x; k < parts; k += kThreads) {
-    low += part[k].x;
-    high += part[k].y;
+// The norm from all partials, the same in every thread.
+__device__ __forceinline__ float norm_of(const Pairs* part, int parts) {
+  __shared__ Pairs sm[kThreads / 32];
+  __shared__ float norm;
+  Pairs s = {};
+  for (int k = threadIdx.x; k < parts; k += kThreads) s.add(part[k]);
+  s = block_sum(s, sm);
+  if (threadIdx.x == 0) {
+    const float low = s.low.value();
+    norm = isinf(low) ? sqrtf(s.high.value()) * (1.f / kHigh) : sqrtf(low) * (1.f / kLow);
   }
-  const double2 s = block_sum(low, high, sm);
-  *exact = isinf(s.x) ? sqrt(s.y) / kHigh : sqrt(s.x) / kLow;
-  return (float)*exact;
+  __syncthreads();
+  return norm;
 }
 
 __global__ void __launch_bounds__(kThreads)
-clip_finish_kernel(const double2* part, int parts, float* norm) {
-  __shared__ double2 sm[kThreads / 32];
+clip_finish_kernel(const Pairs* part, int parts, float* norm) {
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the partials are written
-  double exact;
-  const float v = norm_of(part, parts, sm, &exact);
+  const float v = norm_of(part, parts);
   if (threadIdx.x == 0) *norm = v;
 }
 
@@ -208,15 +232,13 @@ __device__ __forceinline__ void copy_piece(const Piece& p, float scale) {
 
 template <int N>
 __global__ void __launch_bounds__(kThreads)
-clip_scale_kernel(const __grid_constant__ Table<N> t, const double2* part, int parts, float max_norm,
+clip_scale_kernel(const __grid_constant__ Table<N> t, const Pairs* part, int parts, float max_norm,
                   float* norm) {
-  __shared__ double2 sm[kThreads / 32];
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the partials are written
-  double exact;
-  const float v = norm_of(part, parts, sm, &exact);
+  const float v = norm_of(part, parts);
   if (blockIdx.x == 0 && threadIdx.x == 0 && norm) *norm = v;
-  const bool clip = isfinite(v) && exact > (double)max_norm;
-  const float scale = clip ? (float)((double)max_norm / exact) : 1.f;
+  const bool clip = isfinite(v) && v > max_norm;
+  const float scale = clip ? max_norm / v : 1.f;
   const int pieces = t.first[t.tensors];
   // Last pieces first: those the first pass has left in L2.
   for (int i = pieces - 1 - (int)blockIdx.x; i >= 0; i -= gridDim.x) {
@@ -300,14 +322,14 @@ cudaError_t launch(void (*kernel)(P...), int grid, bool dependent, cudaStream_t 
 
 template <int N>
 cudaError_t launch_norm(const lapl_clip_plan& p, const lapl_clip_plan::Batch& b,
-                        const void* const* in, double2* part, cudaStream_t st) {
+                        const void* const* in, clip::Pairs* part, cudaStream_t st) {
   clip::Table<N> t;
   fill(p, b, in, nullptr, &t);
   return launch(clip::clip_norm_kernel<N>, b.grid, false, st, t, part + b.first_part);
 }
 template <int N>
 cudaError_t launch_scale(const lapl_clip_plan& p, const lapl_clip_plan::Batch& b,
-                         const void* const* in, void* const* out, const double2* part,
+                         const void* const* in, void* const* out, const clip::Pairs* part,
                          float max_norm, float* norm, bool dependent, cudaStream_t st) {
   clip::Table<N> t;
   fill(p, b, in, out, &t);
@@ -347,7 +369,7 @@ bool overlapping(lapl_clip_plan* p, const void* const* in, void* const* out) {
 }
 
 // The norm's partials of every launch.
-cudaError_t partials(const lapl_clip_plan& p, const void* const* in, double2* part, cudaStream_t st) {
+cudaError_t partials(const lapl_clip_plan& p, const void* const* in, clip::Pairs* part, cudaStream_t st) {
   cudaError_t e = cudaSuccess;
   for (const auto& b : p.batches) {
     e = (int)b.index.size() <= clip::kSmallTable
@@ -435,7 +457,7 @@ lapl_status lapl_clip_create(const lapl_clip_config* cfg, lapl_clip_handle* out)
 
 lapl_status lapl_clip_workspace_size(lapl_clip_handle p, size_t* bytes) {
   if (!p || !bytes) return LAPL_ERR_INVALID_ARG;
-  *bytes = align_up((size_t)std::max(p->parts, 1) * sizeof(double2), kAlign);
+  *bytes = align_up((size_t)std::max(p->parts, 1) * sizeof(clip::Pairs), kAlign);
   return LAPL_OK;
 }
 
@@ -445,11 +467,11 @@ lapl_status lapl_clip_norm(lapl_clip_handle p, const void* const* grads, float* 
   const lapl_status st = check(p, grads, norm, workspace, workspace_bytes, "clip_norm/device");
   if (st != LAPL_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  double2* part = static_cast<double2*>(workspace);
+  clip::Pairs* part = static_cast<clip::Pairs*>(workspace);
   cudaError_t e = partials(*p, grads, part, s);
   if (e == cudaSuccess) {
     e = launch(clip::clip_finish_kernel, 1, p->batches.size() == 1, s,
-               static_cast<const double2*>(part), p->parts, norm);
+               static_cast<const clip::Pairs*>(part), p->parts, norm);
   }
   if (e != cudaSuccess) {
     ops::set_error(p->last_error, e, "clip_norm");
@@ -470,7 +492,7 @@ lapl_status lapl_clip_apply(lapl_clip_handle p, const void* const* grads, void* 
   if (st != LAPL_OK) return st;
   if (overlapping(p, grads, to)) return LAPL_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  double2* part = static_cast<double2*>(workspace);
+  clip::Pairs* part = static_cast<clip::Pairs*>(workspace);
   cudaError_t e = partials(*p, grads, part, s);
   // One launch after one: the second may be placed early.  (Of several, a later one would only wait
   // for the one just before it.)

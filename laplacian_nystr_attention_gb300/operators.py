@@ -335,12 +335,13 @@ class GradClip(_Plan):
         """The tensors' addresses, if they are the plan's."""
         if len(tensors) != len(self.counts):
             raise ValueError(f"{name}: expected {len(self.counts)} tensors, got {len(tensors)}")
-        for i, (t, n, dtype) in enumerate(zip(tensors, self.counts, self._torch_dtypes)):
-            if (t.dtype is not dtype or t.numel() != n or t.get_device() != self._index
+        device = self._index
+        for t, n, dtype in zip(tensors, self.counts, self._torch_dtypes):
+            if (t.dtype is not dtype or t.numel() != n or t.get_device() != device
                     or not t.is_contiguous()):
-                raise ValueError(f"{name}[{i}]: expected a contiguous {dtype} tensor of {n} "
-                                 f"values on {self.device}, got {t.dtype} {tuple(t.shape)} with "
-                                 f"strides {t.stride()} on {t.device}")
+                raise ValueError(f"{name}: expected a contiguous {dtype} tensor of {n} values on "
+                                 f"{self.device}, got {t.dtype} {tuple(t.shape)} with strides "
+                                 f"{t.stride()} on {t.device}")
         return [t.data_ptr() for t in tensors]
 
     def _room(self):
