@@ -60,6 +60,8 @@ norm_backward_kernel(const Args a) {
       cs[j] = rs[j];
       cy[j] = ry[j];
       cd[j] = rd[j];
+      cols.template trim<kRes16>(cs[j], j);
+      cols.template trim<kGrad16>(cy[j], j);
     }
     if constexpr (kAhead) fetch(row + rows.stride);
     float dot = 0.f;
@@ -147,11 +149,10 @@ Shape shape_of(int width, Cut cut, bool backward) {
   int vectors = width;
   s.nv = 1;
   if (cut != kValues) {
-    // One warp where up to 4 (forward) or 2 (backward) vectors a thread do: no exchange between
-    // warps.  Longer rows: 2 vectors (forward) or 1 for as long as 512 threads do.
+    // One warp where up to 2 vectors a thread do: no exchange between warps.  Longer rows: 2
+    // vectors (forward) or 1 for as long as 512 threads do.
     vectors = (width + (cut == kShifted ? 14 : 7)) / 8;
-    const int most = backward ? 2 : 4;
-    if (vectors <= 32 * most) {
+    if (vectors <= 64) {
       while (32 * s.nv < vectors) s.nv *= 2;
     } else {
       s.nv = backward ? 1 : 2;

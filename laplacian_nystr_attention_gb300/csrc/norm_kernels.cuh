@@ -215,21 +215,25 @@ struct Columns {
     if constexpr (kWeights) return w[j][i];
     else return load_weight(a, j, i);
   }
-  // Vector j at element e of a tensor that ends at `end`; zeros where it is not the row's.
+  // Vector j at element e of a tensor that ends at `end`, with its neighbours' values where it is
+  // not the row's (trim() clears them when the values are used: the load is not waited for here).
   template <bool k16>
   __device__ __forceinline__ void fetch(Raw<k16, VEC>& r, const void* base, int j, long long e,
                                         long long end) const {
     if (!kShift || e + VEC <= end) {
       load(r, base, e);
-      if (!whole(j)) {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i)
-          if (!valid(j, i)) clear(r, i);
-      }
     } else {
 #pragma unroll
       for (int i = 0; i < VEC; ++i)
         if (valid(j, i)) load_one(r, base, e, i);
+    }
+  }
+  template <bool k16>
+  __device__ __forceinline__ void trim(Raw<k16, VEC>& r, int j) const {
+    if (!whole(j)) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i)
+        if (!valid(j, i)) clear(r, i);
     }
   }
   template <bool k16>
@@ -277,7 +281,7 @@ norm_forward_kernel(const Args a) {
   __shared__ float scratch[2][2][kMaxThreads / 32];
   __shared__ float seg[VEC == 1 && kOut == kF8 ? 2 : 1][VEC == 1 && kOut == kF8 ? kMaxWidth / 32 : 1];
   // Registers for a row ahead: where a thread's part of a row is small.
-  constexpr bool kAhead = NV * VEC <= 16;
+  constexpr bool kAhead = NV * ((kX16 ? 4 : 8) + (kRes16 ? 4 : 8)) * VEC / 8 <= 32;
   const int t = place_in_row(a);
   Rows<kShift> rows(a);
   Columns<VEC, NV, kShift> cols;
@@ -308,12 +312,15 @@ norm_forward_kernel(const Args a) {
     float s[NV][VEC];
     float sq = 0.f;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
+      cols.template trim<kX16>(rx[j], j);
+      cols.template trim<kRes16>(rr[j], j);
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
         s[j][i] = get(rx[j], i) + get(rr[j], i);
         sq = fmaf(s[j][i], s[j][i], sq);
       }
+    }
     if constexpr (kAhead) fetch(row + rows.stride);
     if (a.sum) {
 #pragma unroll
