@@ -26,182 +26,21 @@
 #include <algorithm>
 #include <new>
 
-#include "ops_common.cuh"
+#include "scan_pipe.cuh"
 
 namespace cg = cooperative_groups;
 
 namespace lapl {
 namespace scan {
 
-constexpr int kT = LAPL_SCAN_CHUNK;   // tokens of a thread's run
 constexpr int kThreads = 256;
 constexpr int kMaxCluster = 16;
 constexpr int kMaxChannels = 64;      // channels of a tile: 32 lanes x 2
-
-struct Geo {
-  int lanes, lanes_log2;   // threads across the channels
-  int blocks;              // channel blocks of a sequence
-  int threads;             // threads of a CTA
-  int cluster;             // CTAs along the tokens
-  int tiles;               // rounds of cluster tiles along the tokens
-};
-
-struct Args {
-  const void* x;
-  const void* g;
-  const float* h0;
-  const int* lengths;
-  void* out;
-  float* states;
-  float* final_state;
-  const void* dout;
-  const float* dfinal;
-  void* dx;
-  void* dg;
-  float* dh0;
-  long long x_stride, g_stride;
-  int n, c, chunks, reverse;
-  Geo geo;
-};
-
-// One lane's V channels of a token, as they lie in memory.
-template <bool k16, int V>
-__device__ __forceinline__ uint32_t load_raw(const void* base, long long e) {
-  if constexpr (!k16) return __ldg(reinterpret_cast<const uint32_t*>(base) + e);
-  else if constexpr (V == 2) return __ldg(reinterpret_cast<const uint32_t*>(
-      reinterpret_cast<const uint16_t*>(base) + e));
-  else return (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(base) + e);
-}
-template <bool k16, int V>
-__device__ __forceinline__ void widen(uint32_t w, float (&f)[V]) {
-  if constexpr (!k16) f[0] = __uint_as_float(w);
-  else if constexpr (V == 2) { f[0] = bf16_lo(w); f[1] = bf16_hi(w); }
-  else f[0] = bf16_lo(w);
-}
-template <bool k16, int V>
-__device__ __forceinline__ void store_vec(void* base, long long e, const float (&f)[V]) {
-  if constexpr (k16) {
-    uint16_t* p = reinterpret_cast<uint16_t*>(base) + e;
-    if constexpr (V == 2) *reinterpret_cast<uint32_t*>(p) = ops::pack_bf16(f[0], f[1]);
-    else *p = (uint16_t)ops::pack_bf16(f[0], 0.f);
-  } else {
-    float* p = reinterpret_cast<float*>(base) + e;
-    if constexpr (V == 2) *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
-    else *p = f[0];
-  }
-}
-
-// z = 1 - a = 1 / (1 + exp(g)) of the sigmoid gate.  exp(g) = 2^n 2^f with n = round(g log2 e) and
-// f = g log2 e - n by one fused step, so that the hardware's exponential sees |f| <= 1/2 and its
-// relative error (2 ulp) is not multiplied by |g|; 2^n is an exponent field.  g is held within
-// [-87, 88], where neither overflows (z is 1 and 6e-39 there); NaN passes through.
-__device__ __forceinline__ float sigmoid_z(float g) {
-  constexpr float kLog2e = 1.44269504f;
-  constexpr float kRound = 12582912.f;   // 1.5 2^23: adding it leaves the rounded value in the low bits
-  asm("min.NaN.f32 %0, %0, 0f42b00000;" : "+f"(g));   // 88
-  asm("max.NaN.f32 %0, %0, 0fc2ae0000;" : "+f"(g));   // -87
-  const float m = fmaf(g, kLog2e, kRound);
-  const float f = fmaf(g, kLog2e, -(m - kRound));
-  float e, z;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(f));
-  const float scale = __uint_as_float((__float_as_uint(m) << 23) + 0x3f800000u);
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(z) : "f"(fmaf(e, scale, 1.f)));
-  return z;
-}
-
-// A step's decay as one register: a (decay gate) or z = 1 - a (sigmoid gate).
-template <bool kSig>
-__device__ __forceinline__ float gate_of(float g) {
-  if constexpr (kSig) return sigmoid_z(g);
-  else return g;
-}
-template <bool kSig>
-__device__ __forceinline__ float identity_gate() { return kSig ? 0.f : 1.f; }
-// h after a step.
-template <bool kSig>
-__device__ __forceinline__ float step(float gate, float x, float h) {
-  if constexpr (kSig) return fmaf(gate, x - h, h);
-  else return fmaf(gate, h, x);
-}
-// a times v.
-template <bool kSig>
-__device__ __forceinline__ float decayed(float gate, float v) {
-  if constexpr (kSig) return fmaf(-gate, v, v);
-  else return gate * v;
-}
 
 struct Shared {
   float2 run[2][kThreads * 2];                          // maps of the runs, by round parity
   float2 tile[2][kMaxCluster][kMaxChannels];            // maps of the cluster's tiles
 };
-
-// From the run map (A, B) of every thread: the value that enters this thread's run, and `carry`
-// moved past the whole round.  kDown: runs and CTAs in descending order.
-template <int V, bool kCluster, bool kDown>
-__device__ __forceinline__ void exchange(Shared& sm, int parity, int lane, int group, int groups,
-                                         int lanes, int rank, int cluster, const float (&A)[V],
-                                         const float (&B)[V], float (&carry)[V],
-                                         float (&enter)[V]) {
-  const int cpb = lanes * V;
-#pragma unroll
-  for (int v = 0; v < V; ++v)
-    sm.run[parity][group * cpb + lane * V + v] = make_float2(A[v], B[v]);
-  __syncthreads();
-  const float2* runs = &sm.run[parity][(kDown ? (groups - 1) * cpb : 0) + lane * V];
-  const int step = kDown ? -cpb : cpb;
-  const int mine = kDown ? groups - 1 - group : group;   // runs before this one
-  if constexpr (!kCluster) {
-#pragma unroll 4
-    for (int k = 0; k < groups; ++k, runs += step) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        if (k == mine) enter[v] = carry[v];
-        carry[v] = fmaf(runs[v].x, carry[v], runs[v].y);
-      }
-    }
-  } else {
-    // One thread a channel composes the CTA's runs and hands the map to every CTA of the cluster.
-    if ((int)threadIdx.x < cpb) {
-      const float2* p = &sm.run[parity][(kDown ? (groups - 1) * cpb : 0) + threadIdx.x];
-      float ta = 1.f, tb = 0.f;
-#pragma unroll 4
-      for (int k = 0; k < groups; ++k, p += step) {
-        tb = fmaf(p->x, tb, p->y);
-        ta *= p->x;
-      }
-      float2* to = &sm.tile[parity][rank][threadIdx.x];
-      for (int r = 0; r < cluster; ++r)
-        *cg::this_cluster().map_shared_rank(to, r) = make_float2(ta, tb);
-    }
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    // Meanwhile, the map of the CTA's runs before this thread's.
-    float pa[V], pb[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      pa[v] = 1.f;
-      pb[v] = 0.f;
-    }
-#pragma unroll 4
-    for (int k = 0; k < mine; ++k, runs += step) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        pb[v] = fmaf(runs[v].x, pb[v], runs[v].y);
-        pa[v] *= runs[v].x;
-      }
-    }
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-#pragma unroll 4
-    for (int k = 0; k < cluster; ++k) {
-      const int r = kDown ? cluster - 1 - k : k;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        if (r == rank) enter[v] = fmaf(pa[v], carry[v], pb[v]);
-        const float2 m = sm.tile[parity][r][lane * V + v];
-        carry[v] = fmaf(m.x, carry[v], m.y);
-      }
-    }
-  }
-}
 
 // What a thread is: sequence, channels, place along the tokens.
 struct Place {
@@ -225,11 +64,72 @@ __device__ __forceinline__ Place place_of(const Args& a) {
   return p;
 }
 
-// Where a thread's run of round t lies: its first place in processing order, and the address step
-// from one place to the next.
+// From the run map (A, B) of every thread: the value that enters this thread's run, and `carry`
+// moved past the whole round.  kDown: runs and CTAs in descending order.
+template <int V, bool kCluster, bool kDown>
+__device__ __forceinline__ void exchange(Shared& sm, int parity, const Place& p, int lanes,
+                                         int cluster, const Vec<V>& A, const Vec<V>& B,
+                                         Vec<V>& carry, Vec<V>& enter) {
+  const int cpb = lanes * V, groups = p.groups;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    sm.run[parity][p.group * cpb + p.lane * V + v] = make_float2(A.f[v], B.f[v]);
+  __syncthreads();
+  const float2* runs = &sm.run[parity][(kDown ? (groups - 1) * cpb : 0) + p.lane * V];
+  const int by = kDown ? -cpb : cpb;
+  const int mine = kDown ? groups - 1 - p.group : p.group;   // runs before this one
+  if constexpr (!kCluster) {
+#pragma unroll 4
+    for (int k = 0; k < groups; ++k, runs += by) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (k == mine) enter.f[v] = carry.f[v];
+        carry.f[v] = fmaf(runs[v].x, carry.f[v], runs[v].y);
+      }
+    }
+  } else {
+    // One thread a channel composes the CTA's runs and hands the map to every CTA of the cluster.
+    if ((int)threadIdx.x < cpb) {
+      const float2* q = &sm.run[parity][(kDown ? (groups - 1) * cpb : 0) + threadIdx.x];
+      float ta = 1.f, tb = 0.f;
+#pragma unroll 4
+      for (int k = 0; k < groups; ++k, q += by) {
+        tb = fmaf(q->x, tb, q->y);
+        ta *= q->x;
+      }
+      float2* to = &sm.tile[parity][p.rank][threadIdx.x];
+      for (int r = 0; r < cluster; ++r)
+        *cg::this_cluster().map_shared_rank(to, r) = make_float2(ta, tb);
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    // Meanwhile, the map of the CTA's runs before this thread's.
+    Vec<V> pa = fill<V>(1.f), pb = fill<V>(0.f);
+#pragma unroll 4
+    for (int k = 0; k < mine; ++k, runs += by) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        pb.f[v] = fmaf(runs[v].x, pb.f[v], runs[v].y);
+        pa.f[v] *= runs[v].x;
+      }
+    }
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+#pragma unroll 4
+    for (int k = 0; k < cluster; ++k) {
+      const int r = kDown ? cluster - 1 - k : k;
+      if (r == p.rank) enter = fma(pa, carry, pb);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float2 m = sm.tile[parity][r][p.lane * V + v];
+        carry.f[v] = fmaf(m.x, carry.f[v], m.y);
+      }
+    }
+  }
+}
+
+// Where a thread's run of round t lies: its first place in processing order, and that place's row.
 struct Run {
   int i0;            // clipped to N
-  long long row;     // of place i0
+  long long row;
 };
 __device__ __forceinline__ Run run_of(const Args& a, const Place& p, int t, int tile) {
   const long long start = ((long long)t * a.geo.cluster + p.rank) * tile + p.group * kT;
@@ -241,24 +141,18 @@ __device__ __forceinline__ Run run_of(const Args& a, const Place& p, int t, int 
 
 // kT tokens of one tensor, zeros where `live` ends.
 template <bool k16, int V>
-__device__ __forceinline__ void load_run(uint32_t (&w)[kT], const void* base, const Run& r,
+__device__ __forceinline__ void load_run(Raw<k16, V> (&w)[kT], const void* base, const Run& r,
                                          long long stride, int c, bool reverse, int live) {
   constexpr int kBytes = k16 ? 2 : 4;
   const char* q = reinterpret_cast<const char*>(base) + (r.row * stride + c) * kBytes;
-  const long long step = (reverse ? -stride : stride) * kBytes;
+  const long long by = (reverse ? -stride : stride) * kBytes;
   if (r.i0 + kT <= live) {
 #pragma unroll
-    for (int u = 0; u < kT; ++u) {
-      w[u] = load_raw<k16, V>(q, 0);
-      q += step;
-    }
+    for (int u = 0; u < kT; ++u, q += by) w[u] = load_raw<k16, V>(q);
   } else {
 #pragma unroll
-    for (int u = 0; u < kT; ++u) {
-      w[u] = 0u;
-      if (r.i0 + u < live) w[u] = load_raw<k16, V>(q, 0);
-      q += step;
-    }
+    for (int u = 0; u < kT; ++u, q += by)
+      w[u] = r.i0 + u < live ? load_raw<k16, V>(q) : zero_raw<k16, V>();
   }
 }
 
@@ -267,91 +161,70 @@ __global__ void __launch_bounds__(kThreads, 2)
 scan_forward_kernel(const Args a) {
   __shared__ Shared sm;
   const Place p = place_of<V>(a);
-  float carry[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v)
-    carry[v] = a.h0 && p.on ? a.h0[p.s * a.c + p.c + v] : 0.f;
+  Vec<V> carry = fill<V>(0.f);
+  if (a.h0 && p.on) carry = widen(load_raw<false, V>(a.h0 + p.s * a.c + p.c));
   const int tile = p.groups * kT;
   const int live = p.on ? p.len : 0;
   // No CTA writes into another's shared memory before that one runs.
   if constexpr (kCluster) cg::this_cluster().sync();
-  uint32_t rx[kT], rg[kT];
+  Raw<kIn16, V> rx[kT], rg[kT];
   Run run = run_of(a, p, 0, tile);
-  load_run<kIn16, V>(rx, a.x, run, a.x_stride, p.c, a.reverse, live);
-  load_run<kIn16, V>(rg, a.g, run, a.g_stride, p.c, a.reverse, live);
+  load_run(rx, a.x, run, a.x_stride, p.c, a.reverse, live);
+  load_run(rg, a.g, run, a.g_stride, p.c, a.reverse, live);
   for (int t = 0; t < a.geo.tiles; ++t) {
-    float gate[kT][V], x[kT][V];
+    Vec<V> gate[kT], x[kT];
 #pragma unroll
     for (int u = 0; u < kT; ++u) {
-      widen<kIn16, V>(rx[u], x[u]);
-      widen<kIn16, V>(rg[u], gate[u]);
-#pragma unroll
-      for (int v = 0; v < V; ++v) gate[u][v] = gate_of<kSig>(gate[u][v]);
+      x[u] = widen(rx[u]);
+      gate[u] = gate_of<kSig>(widen(rg[u]));
     }
     const Run now = run;
     if (now.i0 + kT > live) {
 #pragma unroll
       for (int u = 0; u < kT; ++u)
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-          if (now.i0 + u >= live) gate[u][v] = identity_gate<kSig>();
+        if (now.i0 + u >= live) gate[u] = identity_gate<kSig, V>();
     }
     // The next round's tokens are on their way while this one is exchanged and written.
     if (t + 1 < a.geo.tiles) {
       run = run_of(a, p, t + 1, tile);
-      load_run<kIn16, V>(rx, a.x, run, a.x_stride, p.c, a.reverse, live);
-      load_run<kIn16, V>(rg, a.g, run, a.g_stride, p.c, a.reverse, live);
+      load_run(rx, a.x, run, a.x_stride, p.c, a.reverse, live);
+      load_run(rg, a.g, run, a.g_stride, p.c, a.reverse, live);
     }
-    float A[V], B[V], h[V];
+    Vec<V> A = fill<V>(1.f), B = fill<V>(0.f), h;
 #pragma unroll
-    for (int v = 0; v < V; ++v) { A[v] = 1.f; B[v] = 0.f; }
-#pragma unroll
-    for (int u = 0; u < kT; ++u)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        A[v] = decayed<kSig>(gate[u][v], A[v]);
-        B[v] = step<kSig>(gate[u][v], x[u][v], B[v]);
-      }
-    exchange<V, kCluster, false>(sm, t & 1, p.lane, p.group, p.groups, a.geo.lanes, p.rank,
-                                 a.geo.cluster, A, B, carry, h);
+    for (int u = 0; u < kT; ++u) {
+      A = decayed<kSig>(gate[u], A);
+      B = step<kSig>(gate[u], x[u], B);
+    }
+    exchange<V, kCluster, false>(sm, t & 1, p, a.geo.lanes, a.geo.cluster, A, B, carry, h);
     if (p.on && now.i0 < a.n) {
-      if (a.states) {
-        float* st = a.states + (p.s * a.chunks + now.i0 / kT) * a.c + p.c;
-#pragma unroll
-        for (int v = 0; v < V; ++v) st[v] = h[v];
-      }
+      if (a.states)
+        store_vec<false>(a.states + (p.s * a.chunks + now.i0 / kT) * a.c + p.c, h);
       constexpr int kBytes = kOut16 ? 2 : 4;
       char* q = reinterpret_cast<char*>(a.out) + (now.row * a.c + p.c) * kBytes;
       const long long by = (a.reverse ? -(long long)a.c : (long long)a.c) * kBytes;
       if (now.i0 + kT <= live) {
 #pragma unroll
-        for (int u = 0; u < kT; ++u) {
-#pragma unroll
-          for (int v = 0; v < V; ++v) h[v] = step<kSig>(gate[u][v], x[u][v], h[v]);
-          store_vec<kOut16, V>(q, 0, h);
-          q += by;
+        for (int u = 0; u < kT; ++u, q += by) {
+          h = step<kSig>(gate[u], x[u], h);
+          store_vec<kOut16>(q, h);
         }
       } else {
 #pragma unroll
-        for (int u = 0; u < kT; ++u) {
+        for (int u = 0; u < kT; ++u, q += by) {
           const int i = now.i0 + u;
-#pragma unroll
-          for (int v = 0; v < V; ++v) h[v] = step<kSig>(gate[u][v], x[u][v], h[v]);
-          if (i < live) {
-            store_vec<kOut16, V>(q, 0, h);
-          } else if (i < a.n) {
-            const float none[V] = {};
-            store_vec<kOut16, V>(a.out, (p.s * a.n + i) * a.c + p.c, none);
-          }
-          q += by;
+          h = step<kSig>(gate[u], x[u], h);
+          if (i < live)
+            store_vec<kOut16>(q, h);
+          else if (i < a.n)
+            store_vec<kOut16>(reinterpret_cast<char*>(a.out) + ((p.s * a.n + i) * a.c + p.c) * kBytes,
+                              fill<V>(0.f));
         }
       }
     }
   }
-  if (a.final_state && p.on && p.rank == 0 && p.group == 0) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) a.final_state[p.s * a.c + p.c + v] = carry[v];
-  }
+  if (a.final_state && p.on && p.rank == 0 && p.group == 0)
+    store_vec<false>(a.final_state + p.s * a.c + p.c, carry);
 }
 
 template <bool kIn16, bool kGrad16, int V, bool kSig, bool kCluster>
@@ -359,111 +232,76 @@ __global__ void __launch_bounds__(kThreads, 2)
 scan_backward_kernel(const Args a) {
   __shared__ Shared sm;
   const Place p = place_of<V>(a);
-  float carry[V];
-#pragma unroll
-  for (int v = 0; v < V; ++v)
-    carry[v] = a.dfinal && p.on ? a.dfinal[p.s * a.c + p.c + v] : 0.f;
+  Vec<V> carry = fill<V>(0.f);
+  if (a.dfinal && p.on) carry = widen(load_raw<false, V>(a.dfinal + p.s * a.c + p.c));
   const int tile = p.groups * kT;
   const int live = p.on ? p.len : 0;
   if constexpr (kCluster) cg::this_cluster().sync();
   for (int t = a.geo.tiles - 1; t >= 0; --t) {
     const Run run = run_of(a, p, t, tile);
-    float gate[kT][V], x[kT][V], dh[kT][V], h[V];
+    Vec<V> gate[kT], x[kT], dh[kT], h = fill<V>(0.f);
     {
-      uint32_t rx[kT], rg[kT];
-      load_run<kIn16, V>(rg, a.g, run, a.g_stride, p.c, a.reverse, live);
-      load_run<kIn16, V>(rx, a.x, run, a.x_stride, p.c, a.reverse, live);
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        h[v] = p.on && run.i0 < a.n ? a.states[(p.s * a.chunks + run.i0 / kT) * a.c + p.c + v] : 0.f;
-      if constexpr (kGrad16 || V == 1) {
-        uint32_t rd[kT];
-        load_run<kGrad16, V>(rd, a.dout, run, a.c, p.c, a.reverse, live);
-#pragma unroll
-        for (int u = 0; u < kT; ++u) widen<kGrad16, V>(rd[u], dh[u]);
-      } else {
-        const float* q = reinterpret_cast<const float*>(a.dout) + run.row * a.c + p.c;
-#pragma unroll
-        for (int u = 0; u < kT; ++u) {
-          float2 d = make_float2(0.f, 0.f);
-          if (run.i0 + u < live) d = *reinterpret_cast<const float2*>(q);
-          dh[u][0] = d.x;
-          dh[u][V - 1] = d.y;
-          q += a.reverse ? -a.c : a.c;
-        }
-      }
+      Raw<kIn16, V> rx[kT], rg[kT];
+      Raw<kGrad16, V> rd[kT];
+      load_run(rg, a.g, run, a.g_stride, p.c, a.reverse, live);
+      load_run(rx, a.x, run, a.x_stride, p.c, a.reverse, live);
+      load_run(rd, a.dout, run, a.c, p.c, a.reverse, live);
+      if (p.on && run.i0 < a.n)
+        h = widen(load_raw<false, V>(a.states + (p.s * a.chunks + run.i0 / kT) * a.c + p.c));
 #pragma unroll
       for (int u = 0; u < kT; ++u) {
-        widen<kIn16, V>(rx[u], x[u]);
-        widen<kIn16, V>(rg[u], gate[u]);
-#pragma unroll
-        for (int v = 0; v < V; ++v) gate[u][v] = gate_of<kSig>(gate[u][v]);
+        x[u] = widen(rx[u]);
+        gate[u] = gate_of<kSig>(widen(rg[u]));
+        dh[u] = widen(rd[u]);
       }
     }
     if (run.i0 + kT > live) {
 #pragma unroll
       for (int u = 0; u < kT; ++u)
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-          if (run.i0 + u >= live) gate[u][v] = identity_gate<kSig>();
+        if (run.i0 + u >= live) gate[u] = identity_gate<kSig, V>();
     }
     // The slope of a step in its decay, h_{i-1} - x_i or h_{i-1}, in x's place.
 #pragma unroll
-    for (int u = 0; u < kT; ++u)
+    for (int u = 0; u < kT; ++u) {
+      const Vec<V> before = h;
+      h = step<kSig>(gate[u], x[u], h);
+      x[u] = kSig ? sub(before, x[u]) : before;
+    }
+    Vec<V> A = fill<V>(1.f), B = fill<V>(0.f), E;
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float before = h[v];
-        h[v] = step<kSig>(gate[u][v], x[u][v], h[v]);
-        x[u][v] = kSig ? before - x[u][v] : before;
-      }
-    float A[V], B[V], E[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) { A[v] = 1.f; B[v] = 0.f; }
-#pragma unroll
-    for (int u = kT - 1; u >= 0; --u)
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        A[v] = decayed<kSig>(gate[u][v], A[v]);
-        B[v] = decayed<kSig>(gate[u][v], dh[u][v] + B[v]);
-      }
-    exchange<V, kCluster, true>(sm, t & 1, p.lane, p.group, p.groups, a.geo.lanes, p.rank,
-                                a.geo.cluster, A, B, carry, E);
+    for (int u = kT - 1; u >= 0; --u) {
+      A = decayed<kSig>(gate[u], A);
+      B = decayed<kSig>(gate[u], add(dh[u], B));
+    }
+    exchange<V, kCluster, true>(sm, t & 1, p, a.geo.lanes, a.geo.cluster, A, B, carry, E);
     if (p.on && run.i0 < a.n) {
       constexpr int kBytes = kGrad16 ? 2 : 4;
-      const int last = run.i0 + kT - 1;
+      const bool whole = run.i0 + kT <= live;
       const long long row = run.row + (a.reverse ? 1 - kT : kT - 1);
       char* qx = reinterpret_cast<char*>(a.dx) + (row * a.x_stride + p.c) * kBytes;
       char* qg = reinterpret_cast<char*>(a.dg) + (row * a.g_stride + p.c) * kBytes;
       const long long bx = (a.reverse ? a.x_stride : -a.x_stride) * kBytes;
       const long long bg = (a.reverse ? a.g_stride : -a.g_stride) * kBytes;
 #pragma unroll
-      for (int u = kT - 1; u >= 0; --u) {
-        float dx[V], dg[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float D = dh[u][v] + E[v];
-          E[v] = decayed<kSig>(gate[u][v], D);
-          dx[v] = kSig ? gate[u][v] * D : D;
-          dg[v] = kSig ? gate[u][v] * x[u][v] * E[v] : x[u][v] * D;
+      for (int u = kT - 1; u >= 0; --u, qx += bx, qg += bg) {
+        const Vec<V> D = add(dh[u], E);
+        E = decayed<kSig>(gate[u], D);
+        Vec<V> dx, dg;
+        step_gradients<kSig>(gate[u], x[u], D, E, dx, dg);
+        const int i = run.i0 + u;
+        if (whole || i < live) {
+          store_vec<kGrad16>(qx, dx);
+          store_vec<kGrad16>(qg, dg);
+        } else if (i < a.n) {
+          const long long at = p.s * a.n + i;
+          store_vec<kGrad16>(reinterpret_cast<char*>(a.dx) + (at * a.x_stride + p.c) * kBytes, fill<V>(0.f));
+          store_vec<kGrad16>(reinterpret_cast<char*>(a.dg) + (at * a.g_stride + p.c) * kBytes, fill<V>(0.f));
         }
-        if (last < live || run.i0 + u < live) {
-          store_vec<kGrad16, V>(qx, 0, dx);
-          store_vec<kGrad16, V>(qg, 0, dg);
-        } else if (run.i0 + u < a.n) {
-          const float none[V] = {};
-          const long long at = p.s * a.n + run.i0 + u;
-          store_vec<kGrad16, V>(a.dx, at * a.x_stride + p.c, none);
-          store_vec<kGrad16, V>(a.dg, at * a.g_stride + p.c, none);
-        }
-        qx += bx;
-        qg += bg;
       }
     }
   }
-  if (a.dh0 && p.on && p.rank == 0 && p.group == 0) {
-#pragma unroll
-    for (int v = 0; v < V; ++v) a.dh0[p.s * a.c + p.c + v] = carry[v];
-  }
+  if (a.dh0 && p.on && p.rank == 0 && p.group == 0)
+    store_vec<false>(a.dh0 + p.s * a.c + p.c, carry);
 }
 
 // ---- host --------------------------------------------------------------------------------
@@ -532,6 +370,60 @@ Geo geometry(const lapl_scan_config& c, int num_sms, int v) {
   return g;
 }
 
+// A kernel of scan_pipe.cuh with its launch shape; kernel null where it is not taken.
+struct Pipe {
+  pipe::Pick pick;
+  Geo geo;
+};
+
+// The shape with the least work on the longest path: waves of clusters, as many as the GPU holds at
+// once, times rounds, and three rounds' time to start and end each wave.
+cudaError_t choose_pipe(const lapl_scan_config& c, bool backward, Pipe* out) {
+  const bool in16 = c.in_dtype == LAPL_BF16, sig = c.gate == LAPL_GATE_SIGMOID;
+  const bool other16 = (backward ? c.grad_dtype : c.out_dtype) == LAPL_BF16;
+  const int v = in16 ? 2 : 1;
+  out->pick.kernel = nullptr;
+  double best = 0;
+  for (int lanes = 32; lanes >= 8; lanes /= 2) {
+    const pipe::Pick k =
+        backward ? (in16 ? pipe::backward_bf16(other16, sig, lanes) : pipe::backward_f32(other16, sig, lanes))
+                 : (in16 ? pipe::forward_bf16(other16, sig, lanes) : pipe::forward_f32(other16, sig, lanes));
+    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k.kernel),
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.smem);
+    if (e != cudaSuccess) return e;
+    Geo g = {};
+    g.lanes = lanes;
+    g.blocks = (c.channels + lanes * v - 1) / (lanes * v);
+    g.threads = (pipe::kTeams * k.warps + 1) * 32;
+    const long long units = (long long)c.sequences * g.blocks;
+    const int tile = k.warps * (32 / lanes) * kT;
+    for (g.cluster = 1; g.cluster <= pipe::kMaxCluster; g.cluster *= 2) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3((unsigned)g.cluster);
+      cfg.blockDim = dim3((unsigned)g.threads);
+      cfg.dynamicSmemBytes = k.smem;
+      cudaLaunchAttribute at[1];
+      at[0].id = cudaLaunchAttributeClusterDimension;
+      at[0].val.clusterDim.x = (unsigned)g.cluster;
+      at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+      cfg.attrs = at;
+      cfg.numAttrs = 1;
+      int held = 0;
+      e = cudaOccupancyMaxActiveClusters(&held, k.kernel, &cfg);
+      if (e != cudaSuccess) return e;
+      if (held < 1) continue;
+      g.tiles = (int)(((long long)c.tokens + (long long)g.cluster * tile - 1) / ((long long)g.cluster * tile));
+      const double cost = (double)((units + held - 1) / held) * (g.tiles + 3);
+      if (!out->pick.kernel || cost < 0.95 * best) {
+        best = cost;
+        out->pick = k;
+        out->geo = g;
+      }
+    }
+  }
+  return cudaSuccess;
+}
+
 lapl_status validate(const lapl_scan_config* c) {
   if (!c) return LAPL_ERR_INVALID_ARG;
   if (c->sequences < 0 || c->tokens < 1 || c->channels < 1) return LAPL_ERR_INVALID_ARG;
@@ -555,7 +447,9 @@ lapl_status validate(const lapl_scan_config* c) {
 struct lapl_scan_plan {
   lapl_scan_config cfg;
   int device;
+  unsigned* dev_err;
   lapl::scan::Geo geo[2];   // by channels a lane: 1, 2
+  lapl::scan::Pipe fwd, bwd;
   char last_error[lapl::ops::kErrorText];
 };
 
@@ -563,15 +457,22 @@ using namespace lapl;
 
 namespace {
 
-// Channels a lane takes: two bf16 values where rows and pointers let it load them as one word.
+// Tokens from which the pipelined kernels are taken.
+constexpr int kPipeTokens = 512;
+
+// Channels a lane takes: two bf16 values where rows and pointers let it load them as one word, and
+// two of the other tensors' values (other_bytes each) and of the fp32 states at once.
 int lane_channels(const lapl_scan_plan& p, std::initializer_list<const void*> in,
-                  std::initializer_list<const void*> other, int other_dtype, long long xs,
-                  long long gs) {
-  if (p.cfg.in_dtype != LAPL_BF16 || p.cfg.channels % 2 || xs % 2 || gs % 2) return 1;
+                  std::initializer_list<const void*> other, int other_bytes,
+                  std::initializer_list<const void*> states, const scan::Args& a) {
+  if (p.cfg.in_dtype != LAPL_BF16 || p.cfg.channels % 2 || a.x_stride % 2 || a.g_stride % 2)
+    return 1;
   for (const void* q : in)
     if (!ops::aligned(q, 4)) return 1;
   for (const void* q : other)
-    if (!ops::aligned(q, 2 * ops::dtype_bytes(other_dtype))) return 1;
+    if (!ops::aligned(q, 2 * other_bytes)) return 1;
+  for (const void* q : states)
+    if (!ops::aligned(q, 8)) return 1;
   return 2;
 }
 
@@ -593,6 +494,28 @@ lapl_status launch(lapl_scan_plan* p, scan::Kernel k, scan::Args& a, int v, void
     e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k),
                              cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, k, a);
+  if (e != cudaSuccess) {
+    ops::set_error(p->last_error, e, where);
+    return LAPL_ERR_CUDA;
+  }
+  return LAPL_OK;
+}
+
+lapl_status launch_pipe(lapl_scan_plan* p, const scan::Pipe& k, scan::Args& a, void* stream,
+                        const char* where) {
+  a.geo = k.geo;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((long long)p->cfg.sequences * a.geo.blocks * a.geo.cluster));
+  cfg.blockDim = dim3((unsigned)a.geo.threads);
+  cfg.dynamicSmemBytes = k.pick.smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)a.geo.cluster;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k.pick.kernel, a, p->dev_err);
   if (e != cudaSuccess) {
     ops::set_error(p->last_error, e, where);
     return LAPL_ERR_CUDA;
@@ -633,6 +556,20 @@ lapl_status lapl_scan_create(const lapl_scan_config* cfg, lapl_scan_handle* out)
     return LAPL_ERR_CUDA;
   }
   for (int v = 1; v <= 2; ++v) p->geo[v - 1] = scan::geometry(*cfg, sms, v);
+  // Long sequences in pieces of 16 bytes: the pipelined kernels.
+  const long long ib = ops::dtype_bytes(cfg->in_dtype);
+  const bool pieces = cfg->channels * ib % 16 == 0 && cfg->x_stride * ib % 16 == 0 &&
+                      cfg->g_stride * ib % 16 == 0;
+  e = device_error_word(&p->dev_err);
+  if (e == cudaSuccess && pieces && cfg->tokens >= kPipeTokens && cfg->sequences > 0) {
+    e = scan::choose_pipe(*cfg, false, &p->fwd);
+    if (e == cudaSuccess && cfg->channels * ops::dtype_bytes(cfg->grad_dtype) % 16 == 0)
+      e = scan::choose_pipe(*cfg, true, &p->bwd);
+  }
+  if (e != cudaSuccess) {
+    delete p;
+    return LAPL_ERR_CUDA;
+  }
   *out = p;
   return LAPL_OK;
 }
@@ -659,7 +596,11 @@ lapl_status lapl_scan_forward(lapl_scan_handle p, const void* x, const void* g, 
   a.out = out;
   a.states = states;
   a.final_state = final_state;
-  const int v = lane_channels(*p, {x, g}, {out}, c.out_dtype, a.x_stride, a.g_stride);
+  if (p->fwd.pick.kernel && ops::aligned(x, 16) && ops::aligned(g, 16) && ops::aligned(out, 8) &&
+      ops::aligned(h0, 8) && ops::aligned(states, 8) && ops::aligned(final_state, 8))
+    return launch_pipe(p, p->fwd, a, stream, "scan_forward");
+  const int v = lane_channels(*p, {x, g}, {out}, ops::dtype_bytes(c.out_dtype),
+                              {h0, states, final_state}, a);
   const scan::Kernel k = scan::pick<false>(c.in_dtype == LAPL_BF16, c.out_dtype == LAPL_BF16,
                                            c.gate == LAPL_GATE_SIGMOID, v,
                                            p->geo[v - 1].cluster > 1);
@@ -691,8 +632,11 @@ lapl_status lapl_scan_backward(lapl_scan_handle p, const void* x, const void* g,
   a.dx = dx;
   a.dg = dg;
   a.dh0 = dh0;
-  const int v =
-      lane_channels(*p, {x, g}, {dout, dx, dg}, c.grad_dtype, a.x_stride, a.g_stride);
+  if (p->bwd.pick.kernel && ops::aligned(x, 16) && ops::aligned(g, 16) && ops::aligned(dout, 16) &&
+      ops::aligned(dx, 8) && ops::aligned(dg, 8) && ops::aligned(states, 8) &&
+      ops::aligned(dfinal, 8) && ops::aligned(dh0, 8))
+    return launch_pipe(p, p->bwd, a, stream, "scan_backward");
+  const int v = lane_channels(*p, {x, g}, {dout, dx, dg}, gb, {states, dfinal, dh0}, a);
   const scan::Kernel k = scan::pick<true>(c.in_dtype == LAPL_BF16, c.grad_dtype == LAPL_BF16,
                                           c.gate == LAPL_GATE_SIGMOID, v,
                                           p->geo[v - 1].cluster > 1);

@@ -1,0 +1,187 @@
+// scan.cuh -- what the kernels of the gated linear recurrence share (lapl_scan_* of
+// include/lapl_ops.h; scan.cu has the formulas): launch arguments, typed accesses, and the step.
+#pragma once
+
+#include "ops_common.cuh"
+
+namespace lapl {
+namespace scan {
+
+constexpr int kT = LAPL_SCAN_CHUNK;   // tokens of a thread's run
+
+struct Geo {
+  int lanes, lanes_log2;   // threads across the channels
+  int blocks;              // channel blocks of a sequence
+  int threads;             // threads of a CTA
+  int cluster;             // CTAs along the tokens
+  int tiles;               // rounds of cluster tiles along the tokens
+};
+
+struct Args {
+  const void* x;
+  const void* g;
+  const float* h0;
+  const int* lengths;
+  void* out;
+  float* states;
+  float* final_state;
+  const void* dout;
+  const float* dfinal;
+  void* dx;
+  void* dg;
+  float* dh0;
+  long long x_stride, g_stride;
+  int n, c, chunks, reverse;
+  Geo geo;
+};
+
+// The V channels of a thread, one or two.  Two go through the packed fp32 instructions.
+template <int V>
+struct Vec {
+  float f[V];
+};
+template <int V>
+__device__ __forceinline__ Vec<V> fill(float v) {
+  Vec<V> r;
+#pragma unroll
+  for (int i = 0; i < V; ++i) r.f[i] = v;
+  return r;
+}
+__device__ __forceinline__ Vec<1> fma(const Vec<1>& a, const Vec<1>& b, const Vec<1>& c) {
+  return {{fmaf(a.f[0], b.f[0], c.f[0])}};
+}
+__device__ __forceinline__ Vec<1> mul(const Vec<1>& a, const Vec<1>& b) { return {{a.f[0] * b.f[0]}}; }
+__device__ __forceinline__ Vec<1> add(const Vec<1>& a, const Vec<1>& b) { return {{a.f[0] + b.f[0]}}; }
+__device__ __forceinline__ Vec<1> sub(const Vec<1>& a, const Vec<1>& b) { return {{a.f[0] - b.f[0]}}; }
+#define LAPL_SCAN_PACKED(name, op)                                                              \
+  __device__ __forceinline__ Vec<2> name(const Vec<2>& a, const Vec<2>& b) {                    \
+    Vec<2> d;                                                                                   \
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t" op          \
+        ".f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"                                          \
+        : "=f"(d.f[0]), "=f"(d.f[1])                                                            \
+        : "f"(a.f[0]), "f"(a.f[1]), "f"(b.f[0]), "f"(b.f[1]));                                  \
+    return d;                                                                                   \
+  }
+LAPL_SCAN_PACKED(mul, "mul.rn")
+LAPL_SCAN_PACKED(add, "add.rn")
+LAPL_SCAN_PACKED(sub, "sub.rn")
+#undef LAPL_SCAN_PACKED
+__device__ __forceinline__ Vec<2> fma(const Vec<2>& a, const Vec<2>& b, const Vec<2>& c) {
+  Vec<2> d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.f[0]), "=f"(d.f[1])
+      : "f"(a.f[0]), "f"(a.f[1]), "f"(b.f[0]), "f"(b.f[1]), "f"(c.f[0]), "f"(c.f[1]));
+  return d;
+}
+
+// A thread's channels of a token, as they lie in memory: one word, or two for two fp32 values.
+template <bool k16, int V>
+struct Raw {
+  uint32_t w[!k16 && V == 2 ? 2 : 1];
+};
+template <bool k16, int V>
+__device__ __forceinline__ Raw<k16, V> load_raw(const void* p) {
+  Raw<k16, V> r;
+  if constexpr (k16 && V == 1) {
+    r.w[0] = *reinterpret_cast<const uint16_t*>(p);
+  } else if constexpr (!k16 && V == 2) {
+    const uint2 t = *reinterpret_cast<const uint2*>(p);
+    r.w[0] = t.x;
+    r.w[1] = t.y;
+  } else {
+    r.w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+  return r;
+}
+template <bool k16, int V>
+__device__ __forceinline__ Raw<k16, V> zero_raw() {
+  Raw<k16, V> r;
+  r.w[0] = 0u;
+  if constexpr (!k16 && V == 2) r.w[1] = 0u;
+  return r;
+}
+template <bool k16, int V>
+__device__ __forceinline__ Vec<V> widen(const Raw<k16, V>& r) {
+  Vec<V> v;
+  if constexpr (!k16) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) v.f[i] = __uint_as_float(r.w[i]);
+  } else {
+    v.f[0] = bf16_lo(r.w[0]);
+    if constexpr (V == 2) v.f[V - 1] = bf16_hi(r.w[0]);
+  }
+  return v;
+}
+template <bool k16, int V>
+__device__ __forceinline__ void store_vec(void* p, const Vec<V>& v) {
+  if constexpr (k16) {
+    if constexpr (V == 2) *reinterpret_cast<uint32_t*>(p) = ops::pack_bf16(v.f[0], v.f[V - 1]);
+    else *reinterpret_cast<uint16_t*>(p) = (uint16_t)ops::pack_bf16(v.f[0], 0.f);
+  } else {
+    if constexpr (V == 2) *reinterpret_cast<float2*>(p) = make_float2(v.f[0], v.f[V - 1]);
+    else *reinterpret_cast<float*>(p) = v.f[0];
+  }
+}
+
+// A step's decay as it is kept: a (decay gate), or -z (sigmoid gate) with z = 1 - a = 1 / (1 + exp(g)).  exp(g) = 2^n 2^f with n = round(g log2 e)
+// and f = g log2 e - n by one fused step, so that the hardware's exponential sees |f| <= 1/2 and
+// its relative error (2 ulp) is not multiplied by |g|; 2^n is an exponent field.  g is held within
+// [-87, 88], where neither overflows (z is 1 and 6e-39 there); NaN passes through.
+template <bool kSig, int V>
+__device__ __forceinline__ Vec<V> gate_of(Vec<V> g) {
+  if constexpr (!kSig) {
+    return g;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      asm("min.NaN.f32 %0, %0, 0f42b00000;" : "+f"(g.f[i]));   // 88
+      asm("max.NaN.f32 %0, %0, 0fc2ae0000;" : "+f"(g.f[i]));   // -87
+    }
+    const Vec<V> log2e = fill<V>(1.44269504f);
+    const Vec<V> round = fill<V>(12582912.f);   // 1.5 2^23: a sum with it has n in its low bits
+    const Vec<V> m = fma(g, log2e, round);
+    const Vec<V> f = fma(g, log2e, sub(round, m));
+    Vec<V> e, scale;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.f[i]) : "f"(f.f[i]));
+      scale.f[i] = __uint_as_float((__float_as_uint(m.f[i]) << 23) + 0xbf800000u);   // -2^n
+    }
+    Vec<V> z = fma(e, scale, fill<V>(-1.f));
+#pragma unroll
+    for (int i = 0; i < V; ++i) asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(z.f[i]));
+    return z;
+  }
+}
+// The decay of a step that leaves the state as it is.
+template <bool kSig, int V>
+__device__ __forceinline__ Vec<V> identity_gate() {
+  return fill<V>(kSig ? 0.f : 1.f);
+}
+// h after a step: h - z (h - x), or a h + x.
+template <bool kSig, int V>
+__device__ __forceinline__ Vec<V> step(const Vec<V>& gate, const Vec<V>& x, const Vec<V>& h) {
+  if constexpr (kSig) return fma(gate, sub(h, x), h);
+  else return fma(gate, h, x);
+}
+// a times v.
+template <bool kSig, int V>
+__device__ __forceinline__ Vec<V> decayed(const Vec<V>& gate, const Vec<V>& v) {
+  if constexpr (kSig) return fma(gate, v, v);
+  else return mul(gate, v);
+}
+// The gradients of a step from D, with E = a D and slope = h_{i-1} - x_i or h_{i-1}.
+template <bool kSig, int V>
+__device__ __forceinline__ void step_gradients(const Vec<V>& gate, const Vec<V>& slope,
+                                               const Vec<V>& D, const Vec<V>& E, Vec<V>& dx,
+                                               Vec<V>& dg) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    dx.f[i] = kSig ? -gate.f[i] * D.f[i] : D.f[i];
+    dg.f[i] = kSig ? -gate.f[i] * slope.f[i] * E.f[i] : slope.f[i] * D.f[i];
+  }
+}
+
+}  // namespace scan
+}  // namespace lapl

@@ -1,0 +1,540 @@
+// scan_pipe.cuh -- the gated linear recurrence over long sequences: the kernels of scan.cu's
+// formulas with the tokens copied ahead, and the exchange of maps taken out of the threads' way.
+//
+// As in scan.cu a thread reduces a run of 16 tokens to an affine map and repeats it from the true
+// state once it knows that; what comes between is a chain over the whole sequence, and waiting for
+// it is what bounds scan.cu's kernels on long sequences with few channels.  Here:
+//   * A CTA has two groups of worker warps that take the rounds of tiles in turn: while one waits
+//     for its states, the other reduces its runs.
+//   * One more warp, the chain warp, does nothing but the chain: per round it composes the CTA's
+//     runs, sends the tile's map to every CTA of the cluster (st.async into distributed shared
+//     memory, counted by an mbarrier there), composes the tiles of the cluster in order, and hands
+//     every run its state.  A thread's part in the exchange is one store and one load.
+//   * Each warp copies its own tokens ahead into its own ring of stages (cp.async, 16 bytes at a
+//     time): no barrier between warps, and the bytes in flight are those of the ring.
+// Two values go through the packed fp32 instructions (bf16 inputs); 17 instructions a value then,
+// against 35 in scan.cu's kernel.
+//
+// Wants rows, pointers and channel counts in multiples of 16 bytes; scan.cu's kernels take the rest.
+//
+// The chain warp's wait for the cluster's maps is bounded (one second): when it gives up it sets
+// kErrBitScan in the device error word and goes on without waiting, so that the kernel ends; its
+// outputs are then undefined.  No CTA of a cluster leaves before all have come to their end.
+#pragma once
+
+#include "scan.cuh"
+
+namespace lapl {
+namespace scan {
+namespace pipe {
+
+constexpr int kTeams = 2;          // groups of worker warps
+constexpr int kMaxCluster = 8;     // CTAs
+// Worker warps of a team: with the chain warp 17 warps of 96 registers, or 15 of 128.
+constexpr int kForwardWarps = 8, kBackwardWarps = 7;
+constexpr unsigned long long kWaitNs = 1000000000ull;
+
+// Bytes of a row of one tensor in shared memory, and from one run of kT rows to the next: a warp
+// reads rows of 32 / kLanes runs at once, which lie side by side in the banks thanks to one row of
+// space after each run.
+template <int kLanes, int kBytes>
+struct Tile {
+  static constexpr int kRow = kLanes * kBytes;
+  static constexpr int kRun = kT * kRow + (kLanes < 32 ? kRow : 0);
+  static constexpr int kWarp = 32 / kLanes * kRun;       // of a warp's stage
+  static constexpr int kPieces = kRow / 16;              // 16-byte pieces of a row
+  static constexpr int kRows = 32 / kPieces;             // rows that a warp copies at once
+  static constexpr int kCopies = 32 / kLanes * kT / kRows;   // of a thread for a stage
+};
+
+struct Layout {
+  unsigned runs, enters, slots, total;   // after the stages; in bytes
+};
+template <int V>
+__host__ __device__ constexpr Layout layout_of(int warps, unsigned stage_bytes, int stages) {
+  Layout l = {};
+  l.runs = (unsigned)(kTeams * warps * stages) * stage_bytes;
+  l.enters = l.runs + kTeams * warps * 32 * 2 * V * 4;
+  l.slots = l.enters + kTeams * warps * 32 * V * 4;
+  l.total = l.slots + 2 * kMaxCluster * 32 * 2 * V * 4 + 16;
+  return l;
+}
+
+__device__ __forceinline__ unsigned smem_u32(const void* p) {
+  return static_cast<unsigned>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ unsigned at_rank(unsigned addr, int rank) {
+  unsigned r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+// `bytes` of the 16 at src (0 or 16), zeros for the rest.
+__device__ __forceinline__ void copy16(unsigned dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+template <int kPending>
+__device__ __forceinline__ void copies_left() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(int id, int threads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+// A map as it lies in shared memory: V factors, then V terms.
+template <int V>
+struct Map {
+  Vec<V> a, b;
+};
+__device__ __forceinline__ void put_map(unsigned at, const Map<2>& m) {
+  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(m.a.f[0]), "f"(m.a.f[1]),
+               "f"(m.b.f[0]), "f"(m.b.f[1]) : "memory");
+}
+__device__ __forceinline__ void put_map(unsigned at, const Map<1>& m) {
+  asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(m.a.f[0]), "f"(m.b.f[0]) : "memory");
+}
+__device__ __forceinline__ void get_map(unsigned at, Map<2>& m) {
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(m.a.f[0]), "=f"(m.a.f[1]), "=f"(m.b.f[0]), "=f"(m.b.f[1]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void get_map(unsigned at, Map<1>& m) {
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(m.a.f[0]), "=f"(m.b.f[0]) : "r"(at) : "memory");
+}
+// The same into a CTA of the cluster, counted by an mbarrier there.
+__device__ __forceinline__ void send_map(unsigned at, unsigned bar, const Map<2>& m) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%2, %3, %4, %5}, [%1];"
+               ::"r"(at), "r"(bar), "f"(m.a.f[0]), "f"(m.a.f[1]), "f"(m.b.f[0]), "f"(m.b.f[1])
+               : "memory");
+}
+__device__ __forceinline__ void send_map(unsigned at, unsigned bar, const Map<1>& m) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%2, %3}, [%1];"
+               ::"r"(at), "r"(bar), "f"(m.a.f[0]), "f"(m.b.f[0]) : "memory");
+}
+__device__ __forceinline__ void put_state(unsigned at, const Vec<2>& v) {
+  asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(v.f[0]), "f"(v.f[1]) : "memory");
+}
+__device__ __forceinline__ void put_state(unsigned at, const Vec<1>& v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v.f[0]) : "memory");
+}
+__device__ __forceinline__ void get_state(unsigned at, Vec<2>& v) {
+  asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v.f[0]), "=f"(v.f[1]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void get_state(unsigned at, Vec<1>& v) {
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v.f[0]) : "r"(at) : "memory");
+}
+
+// Until the phase of the given parity is complete, or false after kWaitNs.
+__device__ __forceinline__ bool wait_phase(unsigned bar, unsigned parity) {
+  auto done = [&] {
+    unsigned d;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(d) : "r"(bar), "r"(parity) : "memory");
+    return d != 0;
+  };
+  auto now = [] {
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+  };
+  if (done()) return true;
+  const unsigned long long t0 = now();
+  while (!done())
+    if (now() - t0 > kWaitNs) return false;
+  return true;
+}
+
+// What a CTA works on.
+template <int kLanes, int V>
+struct Unit {
+  long long s;
+  int c0;             // first channel
+  int rank, cluster, len;
+  __device__ __forceinline__ explicit Unit(const Args& a) {
+    cluster = a.geo.cluster;
+    const int unit = blockIdx.x / cluster;
+    rank = blockIdx.x - unit * cluster;
+    s = unit / a.geo.blocks;
+    c0 = (unit - (int)s * a.geo.blocks) * kLanes * V;
+    len = a.n;
+    if (a.lengths) len = max(0, min(a.n, a.lengths[s]));
+  }
+};
+
+// Copies a warp's tokens of a round into a stage: rows of `first`.. in processing order, those from
+// `len` on as zeros, and channels from C on too.
+template <int kLanes, int kBytes, int kElem>
+__device__ __forceinline__ void copy_stage(unsigned stage, const void* base, long long stride,
+                                           const Args& a, long long s, int c0, int len,
+                                           long long first) {
+  using T = Tile<kLanes, kBytes>;
+  const int lane = threadIdx.x & 31;
+  const int row = lane / T::kPieces, piece = lane % T::kPieces;
+  const bool on = c0 + piece * (16 / kElem) < a.c;
+  const long long i0 = first + row;
+  const long long token = s * a.n + (a.reverse ? len - 1 - i0 : i0);
+  const char* src = reinterpret_cast<const char*>(base) + (token * stride + c0) * kElem + piece * 16;
+  const long long by = (a.reverse ? -stride : stride) * (T::kRows * kElem);
+  const unsigned dst = stage + row * T::kRow + row / kT * (T::kRun - kT * T::kRow) + piece * 16;
+  const int live = on ? (int)max(0ll, min((long long)len - i0, 64ll)) : 0;   // rows from i0 on
+#pragma unroll
+  for (int k = 0; k < T::kCopies; ++k, src += by) {
+    const bool in = k * T::kRows < live;
+    copy16(dst + k * T::kRows * T::kRow + k * T::kRows / kT * (T::kRun - kT * T::kRow),
+           in ? src : base, in ? 16 : 0);
+  }
+}
+
+template <int V>
+__device__ __forceinline__ Vec<V> shuffle(const Vec<V>& v, int from) {
+  Vec<V> r;
+#pragma unroll
+  for (int i = 0; i < V; ++i) r.f[i] = __shfl_sync(0xffffffffu, v.f[i], from);
+  return r;
+}
+
+// The chain warp: see the head of the file.  kDown: rounds, CTAs and runs in descending order.
+// Lanes 0 .. kLanes-1 have the first kWarps runs in that order, the next kLanes lanes the next.
+template <int kLanes, int V, int kWarps, bool kDown>
+__device__ __forceinline__ void chain(const Args& a, const Unit<kLanes, V>& u, unsigned smem,
+                                      const Layout& l, unsigned bars, const float* start,
+                                      float* finish, unsigned* err) {
+  constexpr int kMap = 2 * V * 4, kState = V * 4, kThreads = kWarps * 32 + 32;
+  constexpr int kSets = 32 / kLanes, kRuns = kWarps * kSets;
+  const int lane = threadIdx.x & 31, pos = lane & (kLanes - 1), set = lane / kLanes;
+  const int c = u.c0 + pos * V;
+  const bool on = c < a.c;
+  // The lane's first run, and the step to its next.
+  const int run = kDown ? kRuns - 1 - set * kWarps : set * kWarps;
+  constexpr int kBy = kDown ? -kLanes : kLanes;
+  Vec<V> carry = fill<V>(0.f);
+  if (start && on) carry = widen(load_raw<false, V>(start + u.s * a.c + c));
+  bool lost = false;
+  for (int r = 0; r < a.geo.tiles; ++r) {
+    const int team = r & 1, parity = r & 1;
+    bar_sync(1 + team, kThreads);      // the team's runs are written
+    const unsigned place = team * kWarps * 32 + run * kLanes + pos;
+    Map<V> m[kWarps];
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) get_map(smem + l.runs + (place + k * kBy) * kMap, m[k]);
+    Map<V> all = m[0];
+#pragma unroll
+    for (int k = 1; k < kWarps; ++k) {
+      all.b = fma(m[k].a, all.b, m[k].b);
+      all.a = mul(m[k].a, all.a);
+    }
+    // Over the sets: `all` up to and with this one, `before` without it.
+#pragma unroll
+    for (int o = 1; o < kSets; o *= 2) {
+      const Map<V> low = {shuffle(all.a, lane - o * kLanes), shuffle(all.b, lane - o * kLanes)};
+      if (set >= o) {
+        all.b = fma(all.a, low.b, all.b);
+        all.a = mul(all.a, low.a);
+      }
+    }
+    Map<V> before = {fill<V>(1.f), fill<V>(0.f)};
+    if constexpr (kSets > 1) {
+      const Map<V> low = {shuffle(all.a, lane - kLanes), shuffle(all.b, lane - kLanes)};
+      if (set > 0) before = low;
+      all = {shuffle(all.a, 32 - kLanes + pos), shuffle(all.b, 32 - kLanes + pos)};
+    }
+    const unsigned slots = smem + l.slots + parity * kMaxCluster * 32 * kMap;
+    const unsigned bar = bars + parity * 8;
+    if (lane == 0)
+      asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
+                   ::"r"(bar), "r"(u.cluster * kLanes * kMap) : "memory");
+    __syncwarp();
+    for (int k = set; k < u.cluster; k += kSets)
+      send_map(at_rank(slots + (u.rank * 32 + pos) * kMap, k), at_rank(bar, k), all);
+    if (!lost && !wait_phase(bar, (r >> 1) & 1)) lost = true;
+    Vec<V> enter = carry;
+#pragma unroll
+    for (int k = 0; k < kMaxCluster; ++k) {
+      if (k < u.cluster) {
+        const int rank = kDown ? u.cluster - 1 - k : k;
+        if (rank == u.rank) enter = carry;
+        Map<V> t;
+        get_map(slots + (rank * 32 + pos) * kMap, t);
+        carry = fma(t.a, carry, t.b);
+      }
+    }
+    enter = fma(before.a, enter, before.b);
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) {
+      put_state(smem + l.enters + (place + k * kBy) * kState, enter);
+      enter = fma(m[k].a, enter, m[k].b);
+    }
+    bar_arrive(3 + team, kThreads);
+  }
+  if (lost && lane == 0) atomicOr(err, kErrBitScan);
+  if (finish && on && set == 0 && u.rank == 0) store_vec<false>(finish + u.s * a.c + c, carry);
+}
+
+__device__ __forceinline__ void start_barriers(unsigned bars) {
+  if (threadIdx.x == 0) {
+    for (int k = 0; k < 2; ++k)
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + k * 8) : "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+template <bool kIn16, bool kOut16, bool kSig, int kLanes, int kStages, int kWarps>
+__global__ void __launch_bounds__((kTeams * kWarps + 1) * 32, 1)
+scan_forward_pipe_kernel(const Args a, unsigned* err) {
+  constexpr int V = kIn16 ? 2 : 1, kElem = kIn16 ? 2 : 4, kOut = kOut16 ? 2 : 4;
+  using T = Tile<kLanes, V * kElem>;
+  constexpr unsigned kStage = 2 * T::kWarp;
+  extern __shared__ __align__(128) unsigned char dynamic[];
+  const unsigned smem = smem_u32(dynamic);
+  constexpr Layout l = layout_of<V>(kWarps, kStage, kStages);
+  const unsigned bars = smem + l.total - 16;
+  const Unit<kLanes, V> unit(a);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  start_barriers(bars);
+  cluster_sync();
+  if (warp == kTeams * kWarps) {
+    chain<kLanes, V, kWarps, false>(a, unit, smem, l, bars, a.h0, a.final_state, err);
+  } else {
+    const int team = warp / kWarps, wt = warp - team * kWarps;   // place in the team
+    const int run = wt * (32 / kLanes) + lane / kLanes, threads = kWarps * 32 + 32;
+    const int pos = lane & (kLanes - 1), c = unit.c0 + pos * V;
+    const bool on = c < a.c;
+    const int live = on ? unit.len : 0;
+    const unsigned ring = smem + warp * kStages * kStage;
+    const unsigned my = pos * (V * kElem) + (lane / kLanes) * T::kRun;   // within a stage
+    const int tile = kWarps * (32 / kLanes) * kT;
+    auto place = [&](int r, int k) {   // first token of run k of the team's tile in round r
+      return ((long long)r * unit.cluster + unit.rank) * tile + k * kT;
+    };
+    auto ahead = [&](int r, int stage) {
+      if (r < a.geo.tiles) {
+        const long long first = place(r, wt * (32 / kLanes));
+        copy_stage<kLanes, V * kElem, kElem>(ring + stage * kStage, a.g, a.g_stride, a, unit.s,
+                                             unit.c0, unit.len, first);
+        copy_stage<kLanes, V * kElem, kElem>(ring + stage * kStage + T::kWarp, a.x, a.x_stride, a,
+                                             unit.s, unit.c0, unit.len, first);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int k = 0; k < kStages; ++k) ahead(team + k * kTeams, k);
+    int stage = 0;
+    for (int r = team; r < a.geo.tiles; r += kTeams) {
+      const long long start = place(r, run);
+      const int i0 = (int)min(start, (long long)a.n);
+      copies_left<kStages - 1>();
+      __syncwarp();
+      const unsigned from = ring + stage * kStage + my;
+      Vec<V> gate[kT];
+      Raw<kIn16, V> rx[kT];
+#pragma unroll
+      for (int k = 0; k < kT; ++k) {
+        Raw<kIn16, V> w;
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w.w[0]) : "r"(from + k * T::kRow) : "memory");
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(rx[k].w[0]) : "r"(from + T::kWarp + k * T::kRow) : "memory");
+        gate[k] = gate_of<kSig>(widen(w));
+      }
+      __syncwarp();
+      ahead(r + kStages * kTeams, stage);
+      if (++stage == kStages) stage = 0;
+      if (i0 + kT > live) {
+#pragma unroll
+        for (int k = 0; k < kT; ++k)
+          if (i0 + k >= live) gate[k] = identity_gate<kSig, V>();
+      }
+      Map<V> m = {fill<V>(1.f), fill<V>(0.f)};
+#pragma unroll
+      for (int k = 0; k < kT; ++k) {
+        m.a = decayed<kSig>(gate[k], m.a);
+        m.b = step<kSig>(gate[k], widen(rx[k]), m.b);
+      }
+      put_map(smem + l.runs + (team * kWarps * 32 + wt * 32 + lane) * (2 * V * 4), m);
+      bar_arrive(1 + team, threads);
+      bar_sync(3 + team, threads);
+      Vec<V> h;
+      get_state(smem + l.enters + (team * kWarps * 32 + wt * 32 + lane) * (V * 4), h);
+      if (on && i0 < a.n) {
+        if (a.states) store_vec<false>(a.states + (unit.s * a.chunks + i0 / kT) * a.c + c, h);
+        const long long row = unit.s * a.n + (a.reverse ? unit.len - 1 - i0 : i0);
+        char* q = reinterpret_cast<char*>(a.out) + (row * a.c + c) * kOut;
+        const long long by = (a.reverse ? -(long long)a.c : (long long)a.c) * kOut;
+        if (i0 + kT <= live) {
+#pragma unroll
+          for (int k = 0; k < kT; ++k, q += by) {
+            h = step<kSig>(gate[k], widen(rx[k]), h);
+            store_vec<kOut16>(q, h);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < kT; ++k, q += by) {
+            const int i = i0 + k;
+            h = step<kSig>(gate[k], widen(rx[k]), h);
+            if (i < live)
+              store_vec<kOut16>(q, h);
+            else if (i < a.n)
+              store_vec<kOut16>(reinterpret_cast<char*>(a.out) + ((unit.s * a.n + i) * a.c + c) * kOut,
+                                fill<V>(0.f));
+          }
+        }
+      }
+    }
+    copies_left<0>();
+  }
+  cluster_sync();
+}
+
+template <bool kIn16, bool kGrad16, bool kSig, int kLanes, int kStages, int kWarps>
+__global__ void __launch_bounds__((kTeams * kWarps + 1) * 32, 1)
+scan_backward_pipe_kernel(const Args a, unsigned* err) {
+  constexpr int V = kIn16 ? 2 : 1, kElem = kIn16 ? 2 : 4, kGrad = kGrad16 ? 2 : 4;
+  using T = Tile<kLanes, V * kElem>;
+  using TG = Tile<kLanes, V * kGrad>;
+  constexpr unsigned kStage = 2 * T::kWarp + TG::kWarp;
+  extern __shared__ __align__(128) unsigned char dynamic[];
+  const unsigned smem = smem_u32(dynamic);
+  constexpr Layout l = layout_of<V>(kWarps, kStage, kStages);
+  const unsigned bars = smem + l.total - 16;
+  const Unit<kLanes, V> unit(a);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  start_barriers(bars);
+  cluster_sync();
+  if (warp == kTeams * kWarps) {
+    chain<kLanes, V, kWarps, true>(a, unit, smem, l, bars, a.dfinal, a.dh0, err);
+  } else {
+    const int team = warp / kWarps, wt = warp - team * kWarps;
+    const int run = wt * (32 / kLanes) + lane / kLanes, threads = kWarps * 32 + 32;
+    const int pos = lane & (kLanes - 1), c = unit.c0 + pos * V;
+    const bool on = c < a.c;
+    const int live = on ? unit.len : 0;
+    const unsigned ring = smem + warp * kStages * kStage;
+    const unsigned my = pos * (V * kElem) + (lane / kLanes) * T::kRun;
+    const unsigned my_grad = 2 * T::kWarp + pos * (V * kGrad) + (lane / kLanes) * TG::kRun;
+    const int tile = kWarps * (32 / kLanes) * kT;
+    auto place = [&](int r, int k) {   // rounds go down the sequence
+      return ((long long)(a.geo.tiles - 1 - r) * unit.cluster + unit.rank) * tile + k * kT;
+    };
+    auto ahead = [&](int r, int stage) {
+      if (r < a.geo.tiles) {
+        const long long first = place(r, wt * (32 / kLanes));
+        const unsigned to = ring + stage * kStage;
+        copy_stage<kLanes, V * kElem, kElem>(to, a.g, a.g_stride, a, unit.s, unit.c0, unit.len, first);
+        copy_stage<kLanes, V * kElem, kElem>(to + T::kWarp, a.x, a.x_stride, a, unit.s, unit.c0,
+                                             unit.len, first);
+        copy_stage<kLanes, V * kGrad, kGrad>(to + 2 * T::kWarp, a.dout, a.c, a, unit.s, unit.c0,
+                                             unit.len, first);
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto state = [&](int r) {
+      const long long i = place(r, run);
+      if (r < a.geo.tiles && on && i < a.n)
+        return widen(load_raw<false, V>(a.states + (unit.s * a.chunks + i / kT) * a.c + c));
+      return fill<V>(0.f);
+    };
+#pragma unroll
+    for (int k = 0; k < kStages; ++k) ahead(team + k * kTeams, k);
+    Vec<V> next = state(team);
+    int stage = 0;
+    for (int r = team; r < a.geo.tiles; r += kTeams) {
+      const int i0 = (int)min(place(r, run), (long long)a.n);
+      copies_left<kStages - 1>();
+      __syncwarp();
+      const unsigned from = ring + stage * kStage;
+      Vec<V> gate[kT], slope[kT], h = next;
+      Raw<kGrad16, V> rd[kT];
+#pragma unroll
+      for (int k = 0; k < kT; ++k) {
+        Raw<kIn16, V> w, x;
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w.w[0]) : "r"(from + my + k * T::kRow) : "memory");
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x.w[0]) : "r"(from + my + T::kWarp + k * T::kRow) : "memory");
+        if constexpr (V * kGrad == 8)
+          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(rd[k].w[0]), "=r"(rd[k].w[V * kGrad == 8 ? 1 : 0])
+                       : "r"(from + my_grad + k * TG::kRow) : "memory");
+        else if constexpr (V * kGrad == 4)
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(rd[k].w[0]) : "r"(from + my_grad + k * TG::kRow) : "memory");
+        else
+          asm volatile("{\n\t.reg .u16 t;\n\tld.shared.u16 t, [%1];\n\tcvt.u32.u16 %0, t;\n\t}"
+                       : "=r"(rd[k].w[0]) : "r"(from + my_grad + k * TG::kRow) : "memory");
+        gate[k] = gate_of<kSig>(widen(w));
+        slope[k] = widen(x);
+      }
+      __syncwarp();
+      ahead(r + kStages * kTeams, stage);
+      next = state(r + kTeams);
+      if (++stage == kStages) stage = 0;
+      if (i0 + kT > live) {
+#pragma unroll
+        for (int k = 0; k < kT; ++k)
+          if (i0 + k >= live) gate[k] = identity_gate<kSig, V>();
+      }
+      Map<V> m = {fill<V>(1.f), fill<V>(0.f)};
+#pragma unroll
+      for (int k = kT - 1; k >= 0; --k) {
+        m.a = decayed<kSig>(gate[k], m.a);
+        m.b = decayed<kSig>(gate[k], add(widen(rd[k]), m.b));
+      }
+      put_map(smem + l.runs + (team * kWarps * 32 + wt * 32 + lane) * (2 * V * 4), m);
+      bar_arrive(1 + team, threads);
+      // The slope of a step in its decay, h_{i-1} - x_i or h_{i-1}, while the chain goes on.
+#pragma unroll
+      for (int k = 0; k < kT; ++k) {
+        const Vec<V> before = h;
+        h = step<kSig>(gate[k], slope[k], h);
+        slope[k] = kSig ? sub(before, slope[k]) : before;
+      }
+      bar_sync(3 + team, threads);
+      Vec<V> E;
+      get_state(smem + l.enters + (team * kWarps * 32 + wt * 32 + lane) * (V * 4), E);
+      if (on && i0 < a.n) {
+        const bool whole = i0 + kT <= live;
+        const long long row = unit.s * a.n + (a.reverse ? unit.len - kT - i0 : i0 + kT - 1);
+        char* qx = reinterpret_cast<char*>(a.dx) + (row * a.x_stride + c) * kGrad;
+        char* qg = reinterpret_cast<char*>(a.dg) + (row * a.g_stride + c) * kGrad;
+        const long long bx = (a.reverse ? a.x_stride : -a.x_stride) * kGrad;
+        const long long bg = (a.reverse ? a.g_stride : -a.g_stride) * kGrad;
+#pragma unroll
+        for (int k = kT - 1; k >= 0; --k, qx += bx, qg += bg) {
+          const Vec<V> D = add(widen(rd[k]), E);
+          E = decayed<kSig>(gate[k], D);
+          Vec<V> dx, dg;
+          step_gradients<kSig>(gate[k], slope[k], D, E, dx, dg);
+          const int i = i0 + k;
+          if (whole || i < live) {
+            store_vec<kGrad16>(qx, dx);
+            store_vec<kGrad16>(qg, dg);
+          } else if (i < a.n) {
+            const long long at = unit.s * a.n + i;
+            store_vec<kGrad16>(reinterpret_cast<char*>(a.dx) + (at * a.x_stride + c) * kGrad, fill<V>(0.f));
+            store_vec<kGrad16>(reinterpret_cast<char*>(a.dg) + (at * a.g_stride + c) * kGrad, fill<V>(0.f));
+          }
+        }
+      }
+    }
+    copies_left<0>();
+  }
+  cluster_sync();
+}
+
+using PipeKernel = void (*)(Args, unsigned*);
+
+// A kernel, its worker warps a team and its shared memory.
+struct Pick {
+  PipeKernel kernel;
+  int warps;
+  size_t smem;
+};
+// For lanes of 32, 16 or 8.
+Pick forward_f32(bool out16, bool sig, int lanes);
+Pick forward_bf16(bool out16, bool sig, int lanes);
+Pick backward_f32(bool grad16, bool sig, int lanes);
+Pick backward_bf16(bool grad16, bool sig, int lanes);
+
+}  // namespace pipe
+}  // namespace scan
+}  // namespace lapl
