@@ -394,7 +394,7 @@ cudaError_t choose_pipe(const lapl_scan_config& c, bool backward, Pipe* out) {
     Geo g = {};
     g.lanes = lanes;
     g.blocks = (c.channels + lanes * v - 1) / (lanes * v);
-    g.threads = (pipe::kTeams * k.warps + 1) * 32;
+    g.threads = (pipe::kTeams * k.warps + 2) * 32;
     const long long units = (long long)c.sequences * g.blocks;
     const int tile = k.warps * (32 / lanes) * kT;
     for (g.cluster = 1; g.cluster <= pipe::kMaxCluster; g.cluster *= 2) {
@@ -552,6 +552,7 @@ lapl_status lapl_scan_create(const lapl_scan_config* cfg, lapl_scan_handle* out)
   if (e == cudaSuccess)
     e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, p->device);
   if (e != cudaSuccess) {
+    cudaGetLastError();
     delete p;
     return LAPL_ERR_CUDA;
   }
@@ -567,6 +568,7 @@ lapl_status lapl_scan_create(const lapl_scan_config* cfg, lapl_scan_handle* out)
       e = scan::choose_pipe(*cfg, true, &p->bwd);
   }
   if (e != cudaSuccess) {
+    cudaGetLastError();
     delete p;
     return LAPL_ERR_CUDA;
   }

@@ -6,10 +6,11 @@
 // it is what bounds scan.cu's kernels on long sequences with few channels.  Here:
 //   * A CTA has two groups of worker warps that take the rounds of tiles in turn: while one waits
 //     for its states, the other reduces its runs.
-//   * One more warp, the chain warp, does nothing but the chain: per round it composes the CTA's
-//     runs, sends the tile's map to every CTA of the cluster (st.async into distributed shared
-//     memory, counted by an mbarrier there), composes the tiles of the cluster in order, and hands
-//     every run its state.  A thread's part in the exchange is one store and one load.
+//   * Two more warps do nothing but the chain.  The sending warp composes a tile's runs and sends
+//     the tile's map to every CTA of the cluster (st.async into distributed shared memory, counted
+//     by an mbarrier there); the receiving warp composes the tiles of the cluster in order and
+//     hands every run its state.  A thread's part in the exchange is one store and one load, and
+//     a round's maps are under way while the round before is still being received.
 //   * Each warp copies its own tokens ahead into its own ring of stages (cp.async, 16 bytes at a
 //     time): no barrier between warps, and the bytes in flight are those of the ring.
 // Two values go through the packed fp32 instructions (bf16 inputs); 17 instructions a value then,
@@ -17,7 +18,10 @@
 //
 // Wants rows, pointers and channel counts in multiples of 16 bytes; scan.cu's kernels take the rest.
 //
-// The chain warp's wait for the cluster's maps is bounded (one second): when it gives up it sets
+// A CTA may be ahead of another's receiving warp by three rounds: it sends round r + 4 only after that
+// CTA's map of round r + 2, whose tokens were reduced after it received round r.  Hence four slots.
+//
+// The receiving warp's wait for the cluster's maps is bounded (one second): when it gives up it sets
 // kErrBitScan in the device error word and goes on without waiting, so that the kernel ends; its
 // outputs are then undefined.  No CTA of a cluster leaves before all have come to their end.
 #pragma once
@@ -30,7 +34,8 @@ namespace pipe {
 
 constexpr int kTeams = 2;          // groups of worker warps
 constexpr int kMaxCluster = 8;     // CTAs
-// Worker warps of a team: with the chain warp 17 warps of 96 registers, or 15 of 128.
+constexpr int kSlots = 4;          // rounds of maps that may have arrived
+// Worker warps of a team: with the chain's two 18 warps of 96 registers, or 16 of 128.
 constexpr int kForwardWarps = 8, kBackwardWarps = 7;
 constexpr unsigned long long kWaitNs = 1000000000ull;
 
@@ -50,13 +55,13 @@ struct Tile {
 struct Layout {
   unsigned runs, enters, slots, total;   // after the stages; in bytes
 };
-template <int V>
+template <int V, int kLanes>
 __host__ __device__ constexpr Layout layout_of(int warps, unsigned stage_bytes, int stages) {
   Layout l = {};
   l.runs = (unsigned)(kTeams * warps * stages) * stage_bytes;
   l.enters = l.runs + kTeams * warps * 32 * 2 * V * 4;
   l.slots = l.enters + kTeams * warps * 32 * V * 4;
-  l.total = l.slots + 2 * kMaxCluster * 32 * 2 * V * 4 + 16;
+  l.total = l.slots + kSlots * kMaxCluster * kLanes * 2 * V * 4 + kSlots * 8;
   return l;
 }
 
@@ -196,37 +201,31 @@ __device__ __forceinline__ Vec<V> shuffle(const Vec<V>& v, int from) {
   return r;
 }
 
-// The chain warp: see the head of the file.  kDown: rounds, CTAs and runs in descending order.
-// Lanes 0 .. kLanes-1 have the first kWarps runs in that order, the next kLanes lanes the next.
+// The runs of a team's tile, as the two chain warps see them: lanes 0 .. kLanes-1 have the first
+// kWarps runs in processing order, the next kLanes lanes the next.
 template <int kLanes, int V, int kWarps, bool kDown>
-__device__ __forceinline__ void chain(const Args& a, const Unit<kLanes, V>& u, unsigned smem,
-                                      const Layout& l, unsigned bars, const float* start,
-                                      float* finish, unsigned* err) {
-  constexpr int kMap = 2 * V * 4, kState = V * 4, kThreads = kWarps * 32 + 32;
-  constexpr int kSets = 32 / kLanes, kRuns = kWarps * kSets;
-  const int lane = threadIdx.x & 31, pos = lane & (kLanes - 1), set = lane / kLanes;
-  const int c = u.c0 + pos * V;
-  const bool on = c < a.c;
-  // The lane's first run, and the step to its next.
-  const int run = kDown ? kRuns - 1 - set * kWarps : set * kWarps;
-  constexpr int kBy = kDown ? -kLanes : kLanes;
-  Vec<V> carry = fill<V>(0.f);
-  if (start && on) carry = widen(load_raw<false, V>(start + u.s * a.c + c));
-  bool lost = false;
-  for (int r = 0; r < a.geo.tiles; ++r) {
-    const int team = r & 1, parity = r & 1;
-    bar_sync(1 + team, kThreads);      // the team's runs are written
-    const unsigned place = team * kWarps * 32 + run * kLanes + pos;
-    Map<V> m[kWarps];
+struct Chain {
+  static constexpr int kMap = 2 * V * 4, kState = V * 4, kSets = 32 / kLanes, kRuns = kWarps * kSets;
+  static constexpr int kBy = kDown ? -kLanes : kLanes;   // from a lane's run to its next
+  int lane, pos, set;
+  unsigned first;        // the lane's first run
+  Map<V> m[kWarps];      // its runs
+  Map<V> all, before;    // of the whole tile, of the runs before the lane's
+  __device__ __forceinline__ Chain() {
+    lane = threadIdx.x & 31;
+    pos = lane & (kLanes - 1);
+    set = lane / kLanes;
+    first = (kDown ? kRuns - 1 - set * kWarps : set * kWarps) * kLanes + pos;
+  }
+  __device__ __forceinline__ void reduce(unsigned runs) {
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k) get_map(smem + l.runs + (place + k * kBy) * kMap, m[k]);
-    Map<V> all = m[0];
+    for (int k = 0; k < kWarps; ++k) get_map(runs + (first + k * kBy) * kMap, m[k]);
+    all = m[0];
 #pragma unroll
     for (int k = 1; k < kWarps; ++k) {
       all.b = fma(m[k].a, all.b, m[k].b);
       all.a = mul(m[k].a, all.a);
     }
-    // Over the sets: `all` up to and with this one, `before` without it.
 #pragma unroll
     for (int o = 1; o < kSets; o *= 2) {
       const Map<V> low = {shuffle(all.a, lane - o * kLanes), shuffle(all.b, lane - o * kLanes)};
@@ -235,47 +234,78 @@ __device__ __forceinline__ void chain(const Args& a, const Unit<kLanes, V>& u, u
         all.a = mul(all.a, low.a);
       }
     }
-    Map<V> before = {fill<V>(1.f), fill<V>(0.f)};
+    before = {fill<V>(1.f), fill<V>(0.f)};
     if constexpr (kSets > 1) {
       const Map<V> low = {shuffle(all.a, lane - kLanes), shuffle(all.b, lane - kLanes)};
       if (set > 0) before = low;
       all = {shuffle(all.a, 32 - kLanes + pos), shuffle(all.b, 32 - kLanes + pos)};
     }
-    const unsigned slots = smem + l.slots + parity * kMaxCluster * 32 * kMap;
-    const unsigned bar = bars + parity * 8;
-    if (lane == 0)
+  }
+};
+
+// The sending warp: the map of every round's tile to all CTAs of the cluster.
+template <int kLanes, int V, int kWarps, bool kDown>
+__device__ __forceinline__ void send_chain(const Args& a, const Unit<kLanes, V>& u, unsigned smem,
+                                           const Layout& l, unsigned bars) {
+  Chain<kLanes, V, kWarps, kDown> t;
+  for (int r = 0; r < a.geo.tiles; ++r) {
+    const int team = r & 1, slot = r & (kSlots - 1);
+    bar_sync(1 + team, kWarps * 32 + 64);      // the team's runs are written
+    t.reduce(smem + l.runs + team * kWarps * 32 * t.kMap);
+    const unsigned to = smem + l.slots + ((slot * kMaxCluster + u.rank) * kLanes + t.pos) * t.kMap;
+    for (int k = t.set; k < u.cluster; k += t.kSets)
+      send_map(at_rank(to, k), at_rank(bars + slot * 8, k), t.all);
+  }
+}
+
+// The receiving warp: the state that enters every run.
+template <int kLanes, int V, int kWarps, bool kDown>
+__device__ __forceinline__ void receive_chain(const Args& a, const Unit<kLanes, V>& u, unsigned smem,
+                                              const Layout& l, unsigned bars, const float* start,
+                                              float* finish, unsigned* err) {
+  Chain<kLanes, V, kWarps, kDown> t;
+  const int c = u.c0 + t.pos * V;
+  const bool on = c < a.c;
+  Vec<V> carry = fill<V>(0.f);
+  if (start && on) carry = widen(load_raw<false, V>(start + u.s * a.c + c));
+  bool lost = false;
+  for (int r = 0; r < a.geo.tiles; ++r) {
+    const int team = r & 1, slot = r & (kSlots - 1);
+    const unsigned bar = bars + slot * 8;
+    if (t.lane == 0)
       asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
-                   ::"r"(bar), "r"(u.cluster * kLanes * kMap) : "memory");
-    __syncwarp();
-    for (int k = set; k < u.cluster; k += kSets)
-      send_map(at_rank(slots + (u.rank * 32 + pos) * kMap, k), at_rank(bar, k), all);
-    if (!lost && !wait_phase(bar, (r >> 1) & 1)) lost = true;
+                   ::"r"(bar), "r"(u.cluster * kLanes * t.kMap) : "memory");
+    bar_sync(1 + team, kWarps * 32 + 64);
+    t.reduce(smem + l.runs + team * kWarps * 32 * t.kMap);
+    if (!lost && !wait_phase(bar, (r / kSlots) & 1)) lost = true;
+    const unsigned slots = smem + l.slots + (slot * kMaxCluster * kLanes + t.pos) * t.kMap;
     Vec<V> enter = carry;
 #pragma unroll
     for (int k = 0; k < kMaxCluster; ++k) {
       if (k < u.cluster) {
         const int rank = kDown ? u.cluster - 1 - k : k;
         if (rank == u.rank) enter = carry;
-        Map<V> t;
-        get_map(slots + (rank * 32 + pos) * kMap, t);
-        carry = fma(t.a, carry, t.b);
+        Map<V> m;
+        get_map(slots + rank * kLanes * t.kMap, m);
+        carry = fma(m.a, carry, m.b);
       }
     }
-    enter = fma(before.a, enter, before.b);
+    enter = fma(t.before.a, enter, t.before.b);
+    const unsigned enters = smem + l.enters + (team * kWarps * 32 + t.first) * t.kState;
 #pragma unroll
     for (int k = 0; k < kWarps; ++k) {
-      put_state(smem + l.enters + (place + k * kBy) * kState, enter);
-      enter = fma(m[k].a, enter, m[k].b);
+      put_state(enters + k * t.kBy * t.kState, enter);
+      enter = fma(t.m[k].a, enter, t.m[k].b);
     }
-    bar_arrive(3 + team, kThreads);
+    bar_arrive(3 + team, kWarps * 32 + 32);
   }
-  if (lost && lane == 0) atomicOr(err, kErrBitScan);
-  if (finish && on && set == 0 && u.rank == 0) store_vec<false>(finish + u.s * a.c + c, carry);
+  if (lost && t.lane == 0) atomicOr(err, kErrBitScan);
+  if (finish && on && t.set == 0 && u.rank == 0) store_vec<false>(finish + u.s * a.c + c, carry);
 }
 
 __device__ __forceinline__ void start_barriers(unsigned bars) {
   if (threadIdx.x == 0) {
-    for (int k = 0; k < 2; ++k)
+    for (int k = 0; k < kSlots; ++k)
       asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + k * 8) : "memory");
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -285,24 +315,26 @@ __device__ __forceinline__ void cluster_sync() {
 }
 
 template <bool kIn16, bool kOut16, bool kSig, int kLanes, int kStages, int kWarps>
-__global__ void __launch_bounds__((kTeams * kWarps + 1) * 32, 1)
+__global__ void __launch_bounds__((kTeams * kWarps + 2) * 32, 1)
 scan_forward_pipe_kernel(const Args a, unsigned* err) {
   constexpr int V = kIn16 ? 2 : 1, kElem = kIn16 ? 2 : 4, kOut = kOut16 ? 2 : 4;
   using T = Tile<kLanes, V * kElem>;
   constexpr unsigned kStage = 2 * T::kWarp;
   extern __shared__ __align__(128) unsigned char dynamic[];
   const unsigned smem = smem_u32(dynamic);
-  constexpr Layout l = layout_of<V>(kWarps, kStage, kStages);
-  const unsigned bars = smem + l.total - 16;
+  constexpr Layout l = layout_of<V, kLanes>(kWarps, kStage, kStages);
+  const unsigned bars = smem + l.total - kSlots * 8;
   const Unit<kLanes, V> unit(a);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   start_barriers(bars);
   cluster_sync();
   if (warp == kTeams * kWarps) {
-    chain<kLanes, V, kWarps, false>(a, unit, smem, l, bars, a.h0, a.final_state, err);
+    send_chain<kLanes, V, kWarps, false>(a, unit, smem, l, bars);
+  } else if (warp == kTeams * kWarps + 1) {
+    receive_chain<kLanes, V, kWarps, false>(a, unit, smem, l, bars, a.h0, a.final_state, err);
   } else {
     const int team = warp / kWarps, wt = warp - team * kWarps;   // place in the team
-    const int run = wt * (32 / kLanes) + lane / kLanes, threads = kWarps * 32 + 32;
+    const int run = wt * (32 / kLanes) + lane / kLanes;
     const int pos = lane & (kLanes - 1), c = unit.c0 + pos * V;
     const bool on = c < a.c;
     const int live = on ? unit.len : 0;
@@ -355,8 +387,8 @@ scan_forward_pipe_kernel(const Args a, unsigned* err) {
         m.b = step<kSig>(gate[k], widen(rx[k]), m.b);
       }
       put_map(smem + l.runs + (team * kWarps * 32 + wt * 32 + lane) * (2 * V * 4), m);
-      bar_arrive(1 + team, threads);
-      bar_sync(3 + team, threads);
+      bar_arrive(1 + team, kWarps * 32 + 64);
+      bar_sync(3 + team, kWarps * 32 + 32);
       Vec<V> h;
       get_state(smem + l.enters + (team * kWarps * 32 + wt * 32 + lane) * (V * 4), h);
       if (on && i0 < a.n) {
@@ -390,7 +422,7 @@ scan_forward_pipe_kernel(const Args a, unsigned* err) {
 }
 
 template <bool kIn16, bool kGrad16, bool kSig, int kLanes, int kStages, int kWarps>
-__global__ void __launch_bounds__((kTeams * kWarps + 1) * 32, 1)
+__global__ void __launch_bounds__((kTeams * kWarps + 2) * 32, 1)
 scan_backward_pipe_kernel(const Args a, unsigned* err) {
   constexpr int V = kIn16 ? 2 : 1, kElem = kIn16 ? 2 : 4, kGrad = kGrad16 ? 2 : 4;
   using T = Tile<kLanes, V * kElem>;
@@ -398,17 +430,19 @@ scan_backward_pipe_kernel(const Args a, unsigned* err) {
   constexpr unsigned kStage = 2 * T::kWarp + TG::kWarp;
   extern __shared__ __align__(128) unsigned char dynamic[];
   const unsigned smem = smem_u32(dynamic);
-  constexpr Layout l = layout_of<V>(kWarps, kStage, kStages);
-  const unsigned bars = smem + l.total - 16;
+  constexpr Layout l = layout_of<V, kLanes>(kWarps, kStage, kStages);
+  const unsigned bars = smem + l.total - kSlots * 8;
   const Unit<kLanes, V> unit(a);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   start_barriers(bars);
   cluster_sync();
   if (warp == kTeams * kWarps) {
-    chain<kLanes, V, kWarps, true>(a, unit, smem, l, bars, a.dfinal, a.dh0, err);
+    send_chain<kLanes, V, kWarps, true>(a, unit, smem, l, bars);
+  } else if (warp == kTeams * kWarps + 1) {
+    receive_chain<kLanes, V, kWarps, true>(a, unit, smem, l, bars, a.dfinal, a.dh0, err);
   } else {
     const int team = warp / kWarps, wt = warp - team * kWarps;
-    const int run = wt * (32 / kLanes) + lane / kLanes, threads = kWarps * 32 + 32;
+    const int run = wt * (32 / kLanes) + lane / kLanes;
     const int pos = lane & (kLanes - 1), c = unit.c0 + pos * V;
     const bool on = c < a.c;
     const int live = on ? unit.len : 0;
@@ -480,7 +514,7 @@ scan_backward_pipe_kernel(const Args a, unsigned* err) {
         m.b = decayed<kSig>(gate[k], add(widen(rd[k]), m.b));
       }
       put_map(smem + l.runs + (team * kWarps * 32 + wt * 32 + lane) * (2 * V * 4), m);
-      bar_arrive(1 + team, threads);
+      bar_arrive(1 + team, kWarps * 32 + 64);
       // The slope of a step in its decay, h_{i-1} - x_i or h_{i-1}, while the chain goes on.
 #pragma unroll
       for (int k = 0; k < kT; ++k) {
@@ -488,7 +522,7 @@ scan_backward_pipe_kernel(const Args a, unsigned* err) {
         h = step<kSig>(gate[k], slope[k], h);
         slope[k] = kSig ? sub(before, slope[k]) : before;
       }
-      bar_sync(3 + team, threads);
+      bar_sync(3 + team, kWarps * 32 + 32);
       Vec<V> E;
       get_state(smem + l.enters + (team * kWarps * 32 + wt * 32 + lane) * (V * 4), E);
       if (on && i0 < a.n) {

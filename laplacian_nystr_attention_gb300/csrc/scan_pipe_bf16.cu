@@ -13,7 +13,7 @@ template <bool kOut16, bool kSig, int kLanes>
 Pick forward() {
   constexpr int kStages = 3;
   return {scan_forward_pipe_kernel<kIn16, kOut16, kSig, kLanes, kStages, kForwardWarps>, kForwardWarps,
-          layout_of<V>(kForwardWarps, 2 * Tile<kLanes, V * kElem>::kWarp, kStages).total};
+          layout_of<V, kLanes>(kForwardWarps, 2 * Tile<kLanes, V * kElem>::kWarp, kStages).total};
 }
 template <bool kGrad16, bool kSig, int kLanes>
 Pick backward() {
@@ -21,7 +21,7 @@ Pick backward() {
   // fp32 gradients of bf16 inputs take twice the space: six warps a team.
   constexpr int kWarps = kIn16 && !kGrad16 ? 6 : kBackwardWarps;
   return {scan_backward_pipe_kernel<kIn16, kGrad16, kSig, kLanes, kStages, kWarps>, kWarps,
-          layout_of<V>(kWarps, 2 * Tile<kLanes, V * kElem>::kWarp +
+          layout_of<V, kLanes>(kWarps, 2 * Tile<kLanes, V * kElem>::kWarp +
                                   Tile<kLanes, V * (kGrad16 ? 2 : 4)>::kWarp, kStages).total};
 }
 template <bool kOther16, bool kSig, bool kBackward>
