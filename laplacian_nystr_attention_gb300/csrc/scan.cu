@@ -394,7 +394,7 @@ cudaError_t choose_pipe(const lapl_scan_config& c, bool backward, Pipe* out) {
     Geo g = {};
     g.lanes = lanes;
     g.blocks = (c.channels + lanes * v - 1) / (lanes * v);
-    g.threads = (pipe::kTeams * k.warps + 2) * 32;
+    g.threads = (k.teams * k.warps + 2) * 32;
     const long long units = (long long)c.sequences * g.blocks;
     const int tile = k.warps * (32 / lanes) * kT;
     for (g.cluster = 1; g.cluster <= pipe::kMaxCluster; g.cluster *= 2) {

@@ -8,9 +8,10 @@
 //     for its states, the other reduces its runs.
 //   * Two more warps do nothing but the chain.  The sending warp composes a tile's runs and sends
 //     the tile's map to every CTA of the cluster (st.async into distributed shared memory, counted
-//     by an mbarrier there); the receiving warp composes the tiles of the cluster in order and
-//     hands every run its state.  A thread's part in the exchange is one store and one load, and
-//     a round's maps are under way while the round before is still being received.
+//     by an mbarrier there), and leaves each run the map of those before it; the receiving warp
+//     composes the tiles of the cluster in order and hands the team the state that enters its tile.
+//     A thread's part in the exchange is one store and two loads, and a round's maps are under way
+//     while the round before is still being received.
 //   * Each warp copies its own tokens ahead into its own ring of stages (cp.async, 16 bytes at a
 //     time): no barrier between warps, and the bytes in flight are those of the ring.
 // Two values go through the packed fp32 instructions (bf16 inputs); 17 instructions a value then,
@@ -32,11 +33,10 @@ namespace lapl {
 namespace scan {
 namespace pipe {
 
-constexpr int kTeams = 2;          // groups of worker warps
 constexpr int kMaxCluster = 8;     // CTAs
-constexpr int kSlots = 4;          // rounds of maps that may have arrived
+constexpr int kSlots = 8;          // rounds of maps that may have arrived
 // Worker warps of a team: with the chain's two 18 warps of 96 registers, or 16 of 128.
-constexpr int kForwardWarps = 8, kBackwardWarps = 7;
+constexpr int kForwardTeams = 4, kForwardWarps = 4, kBackwardTeams = 3, kBackwardWarps = 4;
 constexpr unsigned long long kWaitNs = 1000000000ull;
 
 // Bytes of a row of one tensor in shared memory, and from one run of kT rows to the next: a warp
@@ -56,11 +56,11 @@ struct Layout {
   unsigned runs, enters, slots, total;   // after the stages; in bytes
 };
 template <int V, int kLanes>
-__host__ __device__ constexpr Layout layout_of(int warps, unsigned stage_bytes, int stages) {
+__host__ __device__ constexpr Layout layout_of(int kTeams, int warps, unsigned stage_bytes, int stages) {
   Layout l = {};
   l.runs = (unsigned)(kTeams * warps * stages) * stage_bytes;
   l.enters = l.runs + kTeams * warps * 32 * 2 * V * 4;
-  l.slots = l.enters + kTeams * warps * 32 * V * 4;
+  l.slots = l.enters + kTeams * kLanes * V * 4;
   l.total = l.slots + kSlots * kMaxCluster * kLanes * 2 * V * 4 + kSlots * 8;
   return l;
 }
@@ -201,31 +201,30 @@ __device__ __forceinline__ Vec<V> shuffle(const Vec<V>& v, int from) {
   return r;
 }
 
-// The runs of a team's tile, as the two chain warps see them: lanes 0 .. kLanes-1 have the first
-// kWarps runs in processing order, the next kLanes lanes the next.
-template <int kLanes, int V, int kWarps, bool kDown>
-struct Chain {
-  static constexpr int kMap = 2 * V * 4, kState = V * 4, kSets = 32 / kLanes, kRuns = kWarps * kSets;
-  static constexpr int kBy = kDown ? -kLanes : kLanes;   // from a lane's run to its next
-  int lane, pos, set;
-  unsigned first;        // the lane's first run
-  Map<V> m[kWarps];      // its runs
-  Map<V> all, before;    // of the whole tile, of the runs before the lane's
-  __device__ __forceinline__ Chain() {
-    lane = threadIdx.x & 31;
-    pos = lane & (kLanes - 1);
-    set = lane / kLanes;
-    first = (kDown ? kRuns - 1 - set * kWarps : set * kWarps) * kLanes + pos;
-  }
-  __device__ __forceinline__ void reduce(unsigned runs) {
+// The sending warp: composes the runs of every round's tile, sends the tile's map to all CTAs of
+// the cluster, and leaves in each run's place the map of the runs before it.  Lanes 0 .. kLanes-1
+// have the first kWarps runs in processing order, the next kLanes lanes the next.
+template <int kLanes, int V, int kTeams, int kWarps, bool kDown>
+__device__ __forceinline__ void send_chain(const Args& a, const Unit<kLanes, V>& u, unsigned smem,
+                                           const Layout& l, unsigned bars) {
+  constexpr int kMap = 2 * V * 4, kSets = 32 / kLanes, kRuns = kWarps * kSets;
+  constexpr int kBy = (kDown ? -kLanes : kLanes) * kMap;   // from a lane's run to its next
+  const int lane = threadIdx.x & 31, pos = lane & (kLanes - 1), set = lane / kLanes;
+  const int first = (kDown ? kRuns - 1 - set * kWarps : set * kWarps) * kLanes + pos;
+  for (int r = 0; r < a.geo.tiles; ++r) {
+    const int team = r % kTeams, slot = r & (kSlots - 1);
+    const unsigned runs = smem + l.runs + (team * kWarps * 32 + first) * kMap;
+    bar_sync(1 + team, kWarps * 32 + 32);      // the team's runs are written
+    Map<V> m[kWarps];
 #pragma unroll
-    for (int k = 0; k < kWarps; ++k) get_map(runs + (first + k * kBy) * kMap, m[k]);
-    all = m[0];
+    for (int k = 0; k < kWarps; ++k) get_map(runs + k * kBy, m[k]);
+    Map<V> all = m[0], before = {fill<V>(1.f), fill<V>(0.f)};
 #pragma unroll
     for (int k = 1; k < kWarps; ++k) {
       all.b = fma(m[k].a, all.b, m[k].b);
       all.a = mul(m[k].a, all.a);
     }
+    // Over the sets of lanes: `all` up to and with this one, `before` without it.
 #pragma unroll
     for (int o = 1; o < kSets; o *= 2) {
       const Map<V> low = {shuffle(all.a, lane - o * kLanes), shuffle(all.b, lane - o * kLanes)};
@@ -234,73 +233,57 @@ struct Chain {
         all.a = mul(all.a, low.a);
       }
     }
-    before = {fill<V>(1.f), fill<V>(0.f)};
     if constexpr (kSets > 1) {
       const Map<V> low = {shuffle(all.a, lane - kLanes), shuffle(all.b, lane - kLanes)};
       if (set > 0) before = low;
       all = {shuffle(all.a, 32 - kLanes + pos), shuffle(all.b, 32 - kLanes + pos)};
     }
-  }
-};
-
-// The sending warp: the map of every round's tile to all CTAs of the cluster.
-template <int kLanes, int V, int kWarps, bool kDown>
-__device__ __forceinline__ void send_chain(const Args& a, const Unit<kLanes, V>& u, unsigned smem,
-                                           const Layout& l, unsigned bars) {
-  Chain<kLanes, V, kWarps, kDown> t;
-  for (int r = 0; r < a.geo.tiles; ++r) {
-    const int team = r & 1, slot = r & (kSlots - 1);
-    bar_sync(1 + team, kWarps * 32 + 64);      // the team's runs are written
-    t.reduce(smem + l.runs + team * kWarps * 32 * t.kMap);
-    const unsigned to = smem + l.slots + ((slot * kMaxCluster + u.rank) * kLanes + t.pos) * t.kMap;
-    for (int k = t.set; k < u.cluster; k += t.kSets)
-      send_map(at_rank(to, k), at_rank(bars + slot * 8, k), t.all);
+    const unsigned to = smem + l.slots + ((slot * kMaxCluster + u.rank) * kLanes + pos) * kMap;
+    for (int k = set; k < u.cluster; k += kSets)
+      send_map(at_rank(to, k), at_rank(bars + slot * 8, k), all);
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) {
+      put_map(runs + k * kBy, before);
+      before.b = fma(m[k].a, before.b, m[k].b);
+      before.a = mul(m[k].a, before.a);
+    }
+    bar_arrive(1 + kTeams + team, kWarps * 32 + 64);
   }
 }
 
-// The receiving warp: the state that enters every run.
-template <int kLanes, int V, int kWarps, bool kDown>
+// The receiving warp: the state that enters every round's tile, from the tiles of the cluster.
+template <int kLanes, int V, int kTeams, int kWarps, bool kDown>
 __device__ __forceinline__ void receive_chain(const Args& a, const Unit<kLanes, V>& u, unsigned smem,
                                               const Layout& l, unsigned bars, const float* start,
                                               float* finish, unsigned* err) {
-  Chain<kLanes, V, kWarps, kDown> t;
-  const int c = u.c0 + t.pos * V;
-  const bool on = c < a.c;
+  constexpr int kMap = 2 * V * 4;
+  const int lane = threadIdx.x & 31, pos = lane & (kLanes - 1);
+  const int c = u.c0 + pos * V;
+  const bool on = lane < kLanes && c < a.c;
   Vec<V> carry = fill<V>(0.f);
-  if (start && on) carry = widen(load_raw<false, V>(start + u.s * a.c + c));
+  if (start && c < a.c) carry = widen(load_raw<false, V>(start + u.s * a.c + c));
   bool lost = false;
   for (int r = 0; r < a.geo.tiles; ++r) {
-    const int team = r & 1, slot = r & (kSlots - 1);
+    const int team = r % kTeams, slot = r & (kSlots - 1);
     const unsigned bar = bars + slot * 8;
-    if (t.lane == 0)
+    if (lane == 0)
       asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
-                   ::"r"(bar), "r"(u.cluster * kLanes * t.kMap) : "memory");
-    bar_sync(1 + team, kWarps * 32 + 64);
-    t.reduce(smem + l.runs + team * kWarps * 32 * t.kMap);
+                   ::"r"(bar), "r"(u.cluster * kLanes * kMap) : "memory");
     if (!lost && !wait_phase(bar, (r / kSlots) & 1)) lost = true;
-    const unsigned slots = smem + l.slots + (slot * kMaxCluster * kLanes + t.pos) * t.kMap;
+    const unsigned slots = smem + l.slots + (slot * kMaxCluster * kLanes + pos) * kMap;
     Vec<V> enter = carry;
-#pragma unroll
-    for (int k = 0; k < kMaxCluster; ++k) {
-      if (k < u.cluster) {
-        const int rank = kDown ? u.cluster - 1 - k : k;
-        if (rank == u.rank) enter = carry;
-        Map<V> m;
-        get_map(slots + rank * kLanes * t.kMap, m);
-        carry = fma(m.a, carry, m.b);
-      }
+    for (int k = 0; k < u.cluster; ++k) {
+      const int rank = kDown ? u.cluster - 1 - k : k;
+      if (rank == u.rank) enter = carry;
+      Map<V> m;
+      get_map(slots + rank * kLanes * kMap, m);
+      carry = fma(m.a, carry, m.b);
     }
-    enter = fma(t.before.a, enter, t.before.b);
-    const unsigned enters = smem + l.enters + (team * kWarps * 32 + t.first) * t.kState;
-#pragma unroll
-    for (int k = 0; k < kWarps; ++k) {
-      put_state(enters + k * t.kBy * t.kState, enter);
-      enter = fma(t.m[k].a, enter, t.m[k].b);
-    }
-    bar_arrive(3 + team, kWarps * 32 + 32);
+    if (lane < kLanes) put_state(smem + l.enters + (team * kLanes + pos) * (V * 4), enter);
+    bar_arrive(1 + kTeams + team, kWarps * 32 + 64);
   }
-  if (lost && t.lane == 0) atomicOr(err, kErrBitScan);
-  if (finish && on && t.set == 0 && u.rank == 0) store_vec<false>(finish + u.s * a.c + c, carry);
+  if (lost && lane == 0) atomicOr(err, kErrBitScan);
+  if (finish && on && u.rank == 0) store_vec<false>(finish + u.s * a.c + c, carry);
 }
 
 __device__ __forceinline__ void start_barriers(unsigned bars) {
@@ -314,7 +297,7 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
-template <bool kIn16, bool kOut16, bool kSig, int kLanes, int kStages, int kWarps>
+template <bool kIn16, bool kOut16, bool kSig, int kLanes, int kStages, int kTeams, int kWarps>
 __global__ void __launch_bounds__((kTeams * kWarps + 2) * 32, 1)
 scan_forward_pipe_kernel(const Args a, unsigned* err) {
   constexpr int V = kIn16 ? 2 : 1, kElem = kIn16 ? 2 : 4, kOut = kOut16 ? 2 : 4;
@@ -322,16 +305,16 @@ scan_forward_pipe_kernel(const Args a, unsigned* err) {
   constexpr unsigned kStage = 2 * T::kWarp;
   extern __shared__ __align__(128) unsigned char dynamic[];
   const unsigned smem = smem_u32(dynamic);
-  constexpr Layout l = layout_of<V, kLanes>(kWarps, kStage, kStages);
+  constexpr Layout l = layout_of<V, kLanes>(kTeams, kWarps, kStage, kStages);
   const unsigned bars = smem + l.total - kSlots * 8;
   const Unit<kLanes, V> unit(a);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   start_barriers(bars);
   cluster_sync();
   if (warp == kTeams * kWarps) {
-    send_chain<kLanes, V, kWarps, false>(a, unit, smem, l, bars);
+    send_chain<kLanes, V, kTeams, kWarps, false>(a, unit, smem, l, bars);
   } else if (warp == kTeams * kWarps + 1) {
-    receive_chain<kLanes, V, kWarps, false>(a, unit, smem, l, bars, a.h0, a.final_state, err);
+    receive_chain<kLanes, V, kTeams, kWarps, false>(a, unit, smem, l, bars, a.h0, a.final_state, err);
   } else {
     const int team = warp / kWarps, wt = warp - team * kWarps;   // place in the team
     const int run = wt * (32 / kLanes) + lane / kLanes;
@@ -387,10 +370,12 @@ scan_forward_pipe_kernel(const Args a, unsigned* err) {
         m.b = step<kSig>(gate[k], widen(rx[k]), m.b);
       }
       put_map(smem + l.runs + (team * kWarps * 32 + wt * 32 + lane) * (2 * V * 4), m);
-      bar_arrive(1 + team, kWarps * 32 + 64);
-      bar_sync(3 + team, kWarps * 32 + 32);
+      bar_arrive(1 + team, kWarps * 32 + 32);
+      bar_sync(1 + kTeams + team, kWarps * 32 + 64);
       Vec<V> h;
-      get_state(smem + l.enters + (team * kWarps * 32 + wt * 32 + lane) * (V * 4), h);
+      get_state(smem + l.enters + (team * kLanes + pos) * (V * 4), h);
+      get_map(smem + l.runs + (team * kWarps * 32 + wt * 32 + lane) * (2 * V * 4), m);
+      h = fma(m.a, h, m.b);
       if (on && i0 < a.n) {
         if (a.states) store_vec<false>(a.states + (unit.s * a.chunks + i0 / kT) * a.c + c, h);
         const long long row = unit.s * a.n + (a.reverse ? unit.len - 1 - i0 : i0);
@@ -421,7 +406,7 @@ scan_forward_pipe_kernel(const Args a, unsigned* err) {
   cluster_sync();
 }
 
-template <bool kIn16, bool kGrad16, bool kSig, int kLanes, int kStages, int kWarps>
+template <bool kIn16, bool kGrad16, bool kSig, int kLanes, int kStages, int kTeams, int kWarps>
 __global__ void __launch_bounds__((kTeams * kWarps + 2) * 32, 1)
 scan_backward_pipe_kernel(const Args a, unsigned* err) {
   constexpr int V = kIn16 ? 2 : 1, kElem = kIn16 ? 2 : 4, kGrad = kGrad16 ? 2 : 4;
@@ -430,16 +415,16 @@ scan_backward_pipe_kernel(const Args a, unsigned* err) {
   constexpr unsigned kStage = 2 * T::kWarp + TG::kWarp;
   extern __shared__ __align__(128) unsigned char dynamic[];
   const unsigned smem = smem_u32(dynamic);
-  constexpr Layout l = layout_of<V, kLanes>(kWarps, kStage, kStages);
+  constexpr Layout l = layout_of<V, kLanes>(kTeams, kWarps, kStage, kStages);
   const unsigned bars = smem + l.total - kSlots * 8;
   const Unit<kLanes, V> unit(a);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   start_barriers(bars);
   cluster_sync();
   if (warp == kTeams * kWarps) {
-    send_chain<kLanes, V, kWarps, true>(a, unit, smem, l, bars);
+    send_chain<kLanes, V, kTeams, kWarps, true>(a, unit, smem, l, bars);
   } else if (warp == kTeams * kWarps + 1) {
-    receive_chain<kLanes, V, kWarps, true>(a, unit, smem, l, bars, a.dfinal, a.dh0, err);
+    receive_chain<kLanes, V, kTeams, kWarps, true>(a, unit, smem, l, bars, a.dfinal, a.dh0, err);
   } else {
     const int team = warp / kWarps, wt = warp - team * kWarps;
     const int run = wt * (32 / kLanes) + lane / kLanes;
@@ -514,7 +499,7 @@ scan_backward_pipe_kernel(const Args a, unsigned* err) {
         m.b = decayed<kSig>(gate[k], add(widen(rd[k]), m.b));
       }
       put_map(smem + l.runs + (team * kWarps * 32 + wt * 32 + lane) * (2 * V * 4), m);
-      bar_arrive(1 + team, kWarps * 32 + 64);
+      bar_arrive(1 + team, kWarps * 32 + 32);
       // The slope of a step in its decay, h_{i-1} - x_i or h_{i-1}, while the chain goes on.
 #pragma unroll
       for (int k = 0; k < kT; ++k) {
@@ -522,9 +507,11 @@ scan_backward_pipe_kernel(const Args a, unsigned* err) {
         h = step<kSig>(gate[k], slope[k], h);
         slope[k] = kSig ? sub(before, slope[k]) : before;
       }
-      bar_sync(3 + team, kWarps * 32 + 32);
+      bar_sync(1 + kTeams + team, kWarps * 32 + 64);
       Vec<V> E;
-      get_state(smem + l.enters + (team * kWarps * 32 + wt * 32 + lane) * (V * 4), E);
+      get_state(smem + l.enters + (team * kLanes + pos) * (V * 4), E);
+      get_map(smem + l.runs + (team * kWarps * 32 + wt * 32 + lane) * (2 * V * 4), m);
+      E = fma(m.a, E, m.b);
       if (on && i0 < a.n) {
         const bool whole = i0 + kT <= live;
         const long long row = unit.s * a.n + (a.reverse ? unit.len - kT - i0 : i0 + kT - 1);
@@ -560,7 +547,7 @@ using PipeKernel = void (*)(Args, unsigned*);
 // A kernel, its worker warps a team and its shared memory.
 struct Pick {
   PipeKernel kernel;
-  int warps;
+  int teams, warps;
   size_t smem;
 };
 // For lanes of 32, 16 or 8.

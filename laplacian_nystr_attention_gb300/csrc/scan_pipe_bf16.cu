@@ -11,17 +11,17 @@ constexpr int V = kIn16 ? 2 : 1, kElem = kIn16 ? 2 : 4;
 
 template <bool kOut16, bool kSig, int kLanes>
 Pick forward() {
-  constexpr int kStages = 3;
-  return {scan_forward_pipe_kernel<kIn16, kOut16, kSig, kLanes, kStages, kForwardWarps>, kForwardWarps,
-          layout_of<V, kLanes>(kForwardWarps, 2 * Tile<kLanes, V * kElem>::kWarp, kStages).total};
+  constexpr int kStages = 2;
+  return {scan_forward_pipe_kernel<kIn16, kOut16, kSig, kLanes, kStages, kForwardTeams, kForwardWarps>,
+          kForwardTeams, kForwardWarps,
+          layout_of<V, kLanes>(kForwardTeams, kForwardWarps, 2 * Tile<kLanes, V * kElem>::kWarp, kStages).total};
 }
 template <bool kGrad16, bool kSig, int kLanes>
 Pick backward() {
   constexpr int kStages = 2;
-  // fp32 gradients of bf16 inputs take twice the space: six warps a team.
-  constexpr int kWarps = kIn16 && !kGrad16 ? 6 : kBackwardWarps;
-  return {scan_backward_pipe_kernel<kIn16, kGrad16, kSig, kLanes, kStages, kWarps>, kWarps,
-          layout_of<V, kLanes>(kWarps, 2 * Tile<kLanes, V * kElem>::kWarp +
+  return {scan_backward_pipe_kernel<kIn16, kGrad16, kSig, kLanes, kStages, kBackwardTeams, kBackwardWarps>,
+          kBackwardTeams, kBackwardWarps,
+          layout_of<V, kLanes>(kBackwardTeams, kBackwardWarps, 2 * Tile<kLanes, V * kElem>::kWarp +
                                   Tile<kLanes, V * (kGrad16 ? 2 : 4)>::kWarp, kStages).total};
 }
 template <bool kOther16, bool kSig, bool kBackward>
