@@ -176,7 +176,7 @@ scan_forward_kernel(const Args a) {
 #pragma unroll
     for (int u = 0; u < kT; ++u) {
       x[u] = widen(rx[u]);
-      gate[u] = gate_of<kSig>(widen(rg[u]));
+      gate[u] = gate_of<kSig>(rg[u]);
     }
     const Run now = run;
     if (now.i0 + kT > live) {
@@ -251,7 +251,7 @@ scan_backward_kernel(const Args a) {
 #pragma unroll
       for (int u = 0; u < kT; ++u) {
         x[u] = widen(rx[u]);
-        gate[u] = gate_of<kSig>(widen(rg[u]));
+        gate[u] = gate_of<kSig>(rg[u]);
         dh[u] = widen(rd[u]);
       }
     }

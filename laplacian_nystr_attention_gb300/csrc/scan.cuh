@@ -124,31 +124,36 @@ __device__ __forceinline__ void store_vec(void* p, const Vec<V>& v) {
   }
 }
 
-// A step's decay as it is kept: a (decay gate), or -z (sigmoid gate) with z = 1 - a = 1 / (1 + exp(g)).  exp(g) = 2^n 2^f with n = round(g log2 e)
-// and f = g log2 e - n by one fused step, so that the hardware's exponential sees |f| <= 1/2 and
-// its relative error (2 ulp) is not multiplied by |g|; 2^n is an exponent field.  g is held within
+// A step's decay as it is kept: a (decay gate), or -z (sigmoid gate) with z = 1 - a = 1 / (1 + exp(g)).
+//
+// The hardware's base-2 exponential is good to 2 ulp, but its argument t = g log2 e is rounded, which
+// is a relative error of |t| ulp in exp(g).  The part that the rounding lost, r = g log2 e - t, comes
+// exactly out of one more fused step, and 2^(t + r) = 2^t (1 + r ln 2) puts it back.  g is held within
 // [-87, 88], where neither overflows (z is 1 and 6e-39 there); NaN passes through.
-template <bool kSig, int V>
-__device__ __forceinline__ Vec<V> gate_of(Vec<V> g) {
+template <bool kSig, bool k16, int V>
+__device__ __forceinline__ Vec<V> gate_of(Raw<k16, V> w) {
   if constexpr (!kSig) {
-    return g;
+    return widen(w);
   } else {
+    Vec<V> g;
+    if constexpr (k16) {   // both values at once (with one, the other half is 0)
+      asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(w.w[0]) : "r"(0x42b042b0u));
+      asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w.w[0]) : "r"(0xc2aec2aeu));
+      g = widen(w);
+    } else {
+      g = widen(w);
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      asm("min.NaN.f32 %0, %0, 0f42b00000;" : "+f"(g.f[i]));   // 88
-      asm("max.NaN.f32 %0, %0, 0fc2ae0000;" : "+f"(g.f[i]));   // -87
+      for (int i = 0; i < V; ++i) {
+        asm("min.NaN.f32 %0, %0, 0f42b00000;" : "+f"(g.f[i]));   // 88
+        asm("max.NaN.f32 %0, %0, 0fc2ae0000;" : "+f"(g.f[i]));   // -87
+      }
     }
-    const Vec<V> log2e = fill<V>(1.44269504f);
-    const Vec<V> round = fill<V>(12582912.f);   // 1.5 2^23: a sum with it has n in its low bits
-    const Vec<V> m = fma(g, log2e, round);
-    const Vec<V> f = fma(g, log2e, sub(round, m));
-    Vec<V> e, scale;
+    const Vec<V> t = mul(g, fill<V>(-1.44269504f));            // -g log2 e, rounded
+    const Vec<V> r = fma(g, fill<V>(1.44269504f), t);
+    Vec<V> e;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.f[i]) : "f"(f.f[i]));
-      scale.f[i] = __uint_as_float((__float_as_uint(m.f[i]) << 23) + 0xbf800000u);   // -2^n
-    }
-    Vec<V> z = fma(e, scale, fill<V>(-1.f));
+    for (int i = 0; i < V; ++i) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.f[i]) : "f"(-t.f[i]));
+    Vec<V> z = fma(mul(e, fill<V>(-0.693147181f)), r, sub(fill<V>(-1.f), e));   // -1 - exp(g)
 #pragma unroll
     for (int i = 0; i < V; ++i) asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(z.f[i]));
     return z;

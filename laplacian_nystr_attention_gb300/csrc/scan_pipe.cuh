@@ -353,7 +353,7 @@ scan_forward_pipe_kernel(const Args a, unsigned* err) {
         Raw<kIn16, V> w;
         asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w.w[0]) : "r"(from + k * T::kRow) : "memory");
         asm volatile("ld.shared.u32 %0, [%1];" : "=r"(rx[k].w[0]) : "r"(from + T::kWarp + k * T::kRow) : "memory");
-        gate[k] = gate_of<kSig>(widen(w));
+        gate[k] = gate_of<kSig>(w);
       }
       __syncwarp();
       ahead(r + kStages * kTeams, stage);
@@ -480,7 +480,7 @@ scan_backward_pipe_kernel(const Args a, unsigned* err) {
         else
           asm volatile("{\n\t.reg .u16 t;\n\tld.shared.u16 t, [%1];\n\tcvt.u32.u16 %0, t;\n\t}"
                        : "=r"(rd[k].w[0]) : "r"(from + my_grad + k * TG::kRow) : "memory");
-        gate[k] = gate_of<kSig>(widen(w));
+        gate[k] = gate_of<kSig>(w);
         slope[k] = widen(x);
       }
       __syncwarp();
