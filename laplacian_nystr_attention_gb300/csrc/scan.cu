@@ -457,23 +457,28 @@ using namespace lapl;
 
 namespace {
 
-// Tokens from which the pipelined kernels are taken.
-constexpr int kPipeTokens = 512;
+// Tokens from which the pipelined kernels are taken (784 tokens of 128 x 64 channels, bf16: 14.8
+// against 19.4 us; 512 tokens of 64 x 64: equal; shorter ones leave their teams without work).
+constexpr int kPipeTokens = 768;
+
+bool whole(std::initializer_list<const void*> pointers, int bytes) {
+  for (const void* q : pointers)
+    if (!ops::aligned(q, bytes)) return false;
+  return true;
+}
+// Whether a tensor's rows, `stride` elements apart, all start at multiples of 16 bytes.
+bool coarse(const void* base, long long stride, int bytes) {
+  return ops::aligned(base, 16) && stride * bytes % 16 == 0;
+}
 
 // Channels a lane takes: two bf16 values where rows and pointers let it load them as one word, and
 // two of the other tensors' values (other_bytes each) and of the fp32 states at once.
 int lane_channels(const lapl_scan_plan& p, std::initializer_list<const void*> in,
                   std::initializer_list<const void*> other, int other_bytes,
                   std::initializer_list<const void*> states, const scan::Args& a) {
-  if (p.cfg.in_dtype != LAPL_BF16 || p.cfg.channels % 2 || a.x_stride % 2 || a.g_stride % 2)
-    return 1;
-  for (const void* q : in)
-    if (!ops::aligned(q, 4)) return 1;
-  for (const void* q : other)
-    if (!ops::aligned(q, 2 * other_bytes)) return 1;
-  for (const void* q : states)
-    if (!ops::aligned(q, 8)) return 1;
-  return 2;
+  const bool pairs = p.cfg.in_dtype == LAPL_BF16 && p.cfg.channels % 2 == 0 &&
+                     a.x_stride % 2 == 0 && a.g_stride % 2 == 0;
+  return pairs && whole(in, 4) && whole(other, 2 * other_bytes) && whole(states, 8) ? 2 : 1;
 }
 
 lapl_status launch(lapl_scan_plan* p, scan::Kernel k, scan::Args& a, int v, void* stream,
@@ -557,15 +562,13 @@ lapl_status lapl_scan_create(const lapl_scan_config* cfg, lapl_scan_handle* out)
     return LAPL_ERR_CUDA;
   }
   for (int v = 1; v <= 2; ++v) p->geo[v - 1] = scan::geometry(*cfg, sms, v);
-  // Long sequences in pieces of 16 bytes: the pipelined kernels.
-  const long long ib = ops::dtype_bytes(cfg->in_dtype);
-  const bool pieces = cfg->channels * ib % 16 == 0 && cfg->x_stride * ib % 16 == 0 &&
-                      cfg->g_stride * ib % 16 == 0;
+  // Long sequences: the pipelined kernels, for bf16 inputs in pairs of channels.
   e = device_error_word(&p->dev_err);
-  if (e == cudaSuccess && pieces && cfg->tokens >= kPipeTokens && cfg->sequences > 0) {
+  const bool pairs = cfg->in_dtype == LAPL_F32 ||
+                     (cfg->channels % 2 == 0 && cfg->x_stride % 2 == 0 && cfg->g_stride % 2 == 0);
+  if (e == cudaSuccess && pairs && cfg->tokens >= kPipeTokens && cfg->sequences > 0) {
     e = scan::choose_pipe(*cfg, false, &p->fwd);
-    if (e == cudaSuccess && cfg->channels * ops::dtype_bytes(cfg->grad_dtype) % 16 == 0)
-      e = scan::choose_pipe(*cfg, true, &p->bwd);
+    if (e == cudaSuccess) e = scan::choose_pipe(*cfg, true, &p->bwd);
   }
   if (e != cudaSuccess) {
     cudaGetLastError();
@@ -598,11 +601,14 @@ lapl_status lapl_scan_forward(lapl_scan_handle p, const void* x, const void* g, 
   a.out = out;
   a.states = states;
   a.final_state = final_state;
-  if (p->fwd.pick.kernel && ops::aligned(x, 16) && ops::aligned(g, 16) && ops::aligned(out, 8) &&
-      ops::aligned(h0, 8) && ops::aligned(states, 8) && ops::aligned(final_state, 8))
-    return launch_pipe(p, p->fwd, a, stream, "scan_forward");
-  const int v = lane_channels(*p, {x, g}, {out}, ops::dtype_bytes(c.out_dtype),
-                              {h0, states, final_state}, a);
+  const int ib = ops::dtype_bytes(c.in_dtype), ob = ops::dtype_bytes(c.out_dtype);
+  if (p->fwd.pick.kernel) {
+    const int pair = c.in_dtype == LAPL_BF16 ? 2 : 1;
+    a.fine = !coarse(x, a.x_stride, ib) || !coarse(g, a.g_stride, ib);
+    if (whole({x, g}, 4) && whole({out}, pair * ob) && whole({h0, states, final_state}, pair * 4))
+      return launch_pipe(p, p->fwd, a, stream, "scan_forward");
+  }
+  const int v = lane_channels(*p, {x, g}, {out}, ob, {h0, states, final_state}, a);
   const scan::Kernel k = scan::pick<false>(c.in_dtype == LAPL_BF16, c.out_dtype == LAPL_BF16,
                                            c.gate == LAPL_GATE_SIGMOID, v,
                                            p->geo[v - 1].cluster > 1);
@@ -634,10 +640,14 @@ lapl_status lapl_scan_backward(lapl_scan_handle p, const void* x, const void* g,
   a.dx = dx;
   a.dg = dg;
   a.dh0 = dh0;
-  if (p->bwd.pick.kernel && ops::aligned(x, 16) && ops::aligned(g, 16) && ops::aligned(dout, 16) &&
-      ops::aligned(dx, 8) && ops::aligned(dg, 8) && ops::aligned(states, 8) &&
-      ops::aligned(dfinal, 8) && ops::aligned(dh0, 8))
-    return launch_pipe(p, p->bwd, a, stream, "scan_backward");
+  if (p->bwd.pick.kernel) {
+    const int pair = c.in_dtype == LAPL_BF16 ? 2 : 1;
+    a.fine = !coarse(x, a.x_stride, ib) || !coarse(g, a.g_stride, ib);
+    a.fine_dout = !coarse(dout, a.c, gb);
+    if (whole({x, g}, 4) && whole({dout, dx, dg}, pair * gb) &&
+        whole({states, dfinal, dh0}, pair * 4) && !(a.fine_dout && pair * gb < 4))
+      return launch_pipe(p, p->bwd, a, stream, "scan_backward");
+  }
   const int v = lane_channels(*p, {x, g}, {dout, dx, dg}, gb, {states, dfinal, dh0}, a);
   const scan::Kernel k = scan::pick<true>(c.in_dtype == LAPL_BF16, c.grad_dtype == LAPL_BF16,
                                           c.gate == LAPL_GATE_SIGMOID, v,

@@ -32,6 +32,7 @@ struct Args {
   float* dh0;
   long long x_stride, g_stride;
   int n, c, chunks, reverse;
+  bool fine, fine_dout;   // scan_pipe.cuh: x and g, and dout, copied in less than 16 bytes
   Geo geo;
 };
 

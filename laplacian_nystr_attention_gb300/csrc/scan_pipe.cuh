@@ -4,8 +4,8 @@
 // As in scan.cu a thread reduces a run of 16 tokens to an affine map and repeats it from the true
 // state once it knows that; what comes between is a chain over the whole sequence, and waiting for
 // it is what bounds scan.cu's kernels on long sequences with few channels.  Here:
-//   * A CTA has two groups of worker warps that take the rounds of tiles in turn: while one waits
-//     for its states, the other reduces its runs.
+//   * A CTA has teams of four worker warps that take the rounds of tiles in turn: while one waits
+//     for its states, the others reduce their runs.
 //   * Two more warps do nothing but the chain.  The sending warp composes a tile's runs and sends
 //     the tile's map to every CTA of the cluster (st.async into distributed shared memory, counted
 //     by an mbarrier there), and leaves each run the map of those before it; the receiving warp
@@ -17,10 +17,11 @@
 // Two values go through the packed fp32 instructions (bf16 inputs); 17 instructions a value then,
 // against 35 in scan.cu's kernel.
 //
-// Wants rows, pointers and channel counts in multiples of 16 bytes; scan.cu's kernels take the rest.
+// Copies are of 16 bytes where rows and pointers allow it, else of each thread's own 4 or 8 (which
+// takes more instructions).  scan.cu's kernels take short sequences and what is odd beyond that.
 //
-// A CTA may be ahead of another's receiving warp by three rounds: it sends round r + 4 only after that
-// CTA's map of round r + 2, whose tokens were reduced after it received round r.  Hence four slots.
+// With T teams, a CTA whose receiving warp is at round r has sent maps up to round r + T - 1, so
+// another may be at r + T and send up to r + 2T - 1: maps of 2T rounds may be there at once.
 //
 // The receiving warp's wait for the cluster's maps is bounded (one second): when it gives up it sets
 // kErrBitScan in the device error word and goes on without waiting, so that the kernel ends; its
@@ -34,7 +35,8 @@ namespace scan {
 namespace pipe {
 
 constexpr int kMaxCluster = 8;     // CTAs
-constexpr int kSlots = 8;          // rounds of maps that may have arrived
+// Rounds of maps that may have arrived: see above.
+__host__ __device__ constexpr int slots_of(int teams) { return 2 * teams; }
 // Worker warps of a team: with the chain's two 18 warps of 96 registers, or 16 of 128.
 constexpr int kForwardTeams = 4, kForwardWarps = 4, kBackwardTeams = 3, kBackwardWarps = 4;
 constexpr unsigned long long kWaitNs = 1000000000ull;
@@ -61,7 +63,7 @@ __host__ __device__ constexpr Layout layout_of(int kTeams, int warps, unsigned s
   l.runs = (unsigned)(kTeams * warps * stages) * stage_bytes;
   l.enters = l.runs + kTeams * warps * 32 * 2 * V * 4;
   l.slots = l.enters + kTeams * kLanes * V * 4;
-  l.total = l.slots + kSlots * kMaxCluster * kLanes * 2 * V * 4 + kSlots * 8;
+  l.total = l.slots + slots_of(kTeams) * kMaxCluster * kLanes * 2 * V * 4 + slots_of(kTeams) * 8;
   return l;
 }
 
@@ -77,6 +79,11 @@ __device__ __forceinline__ unsigned at_rank(unsigned addr, int rank) {
 __device__ __forceinline__ void copy16(unsigned dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
+}
+template <int kBytes>
+__device__ __forceinline__ void copy_own(unsigned dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(bytes),
+               "n"(kBytes) : "memory");
 }
 template <int kPending>
 __device__ __forceinline__ void copies_left() {
@@ -170,26 +177,37 @@ struct Unit {
 };
 
 // Copies a warp's tokens of a round into a stage: rows of `first`.. in processing order, those from
-// `len` on as zeros, and channels from C on too.
+// `len` on as zeros, and channels from C on too.  In 16-byte pieces, or with `fine` in the threads'
+// own kBytes (4 or 8) where a row or the tensor does not start at a multiple of 16 bytes.
 template <int kLanes, int kBytes, int kElem>
 __device__ __forceinline__ void copy_stage(unsigned stage, const void* base, long long stride,
                                            const Args& a, long long s, int c0, int len,
-                                           long long first) {
+                                           long long first, bool fine) {
   using T = Tile<kLanes, kBytes>;
   const int lane = threadIdx.x & 31;
-  const int row = lane / T::kPieces, piece = lane % T::kPieces;
-  const bool on = c0 + piece * (16 / kElem) < a.c;
+  const int pieces = fine ? kLanes : T::kPieces;    // of a row
+  const int row = fine ? lane / kLanes * kT : lane / T::kPieces, piece = lane & (pieces - 1);
+  const int size = fine ? kBytes : 16;
+  const int bytes = max(0, min(size, (a.c - c0) * kElem - piece * size));   // within C
   const long long i0 = first + row;
   const long long token = s * a.n + (a.reverse ? len - 1 - i0 : i0);
-  const char* src = reinterpret_cast<const char*>(base) + (token * stride + c0) * kElem + piece * 16;
-  const long long by = (a.reverse ? -stride : stride) * (T::kRows * kElem);
-  const unsigned dst = stage + row * T::kRow + row / kT * (T::kRun - kT * T::kRow) + piece * 16;
-  const int live = on ? (int)max(0ll, min((long long)len - i0, 64ll)) : 0;   // rows from i0 on
+  const char* src = reinterpret_cast<const char*>(base) + (token * stride + c0) * kElem + piece * size;
+  const int live = bytes ? (int)max(0ll, min((long long)len - i0, 64ll)) : 0;   // rows from i0 on
+  const unsigned dst = stage + row * T::kRow + row / kT * (T::kRun - kT * T::kRow) + piece * size;
+  if (!fine) {
+    const long long by = (a.reverse ? -stride : stride) * (T::kRows * kElem);
 #pragma unroll
-  for (int k = 0; k < T::kCopies; ++k, src += by) {
-    const bool in = k * T::kRows < live;
-    copy16(dst + k * T::kRows * T::kRow + k * T::kRows / kT * (T::kRun - kT * T::kRow),
-           in ? src : base, in ? 16 : 0);
+    for (int k = 0; k < T::kCopies; ++k, src += by) {
+      const bool in = k * T::kRows < live;
+      copy16(dst + k * T::kRows * T::kRow + k * T::kRows / kT * (T::kRun - kT * T::kRow),
+             in ? src : base, in ? bytes : 0);
+    }
+  } else if constexpr (kBytes >= 4) {
+    // A thread copies what it will read itself: its run.
+    const long long by = (a.reverse ? -stride : stride) * kElem;
+#pragma unroll
+    for (int k = 0; k < kT; ++k, src += by)
+      copy_own<kBytes>(dst + k * T::kRow, k < live ? src : base, k < live ? bytes : 0);
   }
 }
 
@@ -212,7 +230,7 @@ __device__ __forceinline__ void send_chain(const Args& a, const Unit<kLanes, V>&
   const int lane = threadIdx.x & 31, pos = lane & (kLanes - 1), set = lane / kLanes;
   const int first = (kDown ? kRuns - 1 - set * kWarps : set * kWarps) * kLanes + pos;
   for (int r = 0; r < a.geo.tiles; ++r) {
-    const int team = r % kTeams, slot = r & (kSlots - 1);
+    const int team = r % kTeams, slot = r % slots_of(kTeams);
     const unsigned runs = smem + l.runs + (team * kWarps * 32 + first) * kMap;
     bar_sync(1 + team, kWarps * 32 + 32);      // the team's runs are written
     Map<V> m[kWarps];
@@ -264,12 +282,12 @@ __device__ __forceinline__ void receive_chain(const Args& a, const Unit<kLanes, 
   if (start && c < a.c) carry = widen(load_raw<false, V>(start + u.s * a.c + c));
   bool lost = false;
   for (int r = 0; r < a.geo.tiles; ++r) {
-    const int team = r % kTeams, slot = r & (kSlots - 1);
+    const int team = r % kTeams, slot = r % slots_of(kTeams);
     const unsigned bar = bars + slot * 8;
     if (lane == 0)
       asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
                    ::"r"(bar), "r"(u.cluster * kLanes * kMap) : "memory");
-    if (!lost && !wait_phase(bar, (r / kSlots) & 1)) lost = true;
+    if (!lost && !wait_phase(bar, (r / slots_of(kTeams)) & 1)) lost = true;
     const unsigned slots = smem + l.slots + (slot * kMaxCluster * kLanes + pos) * kMap;
     Vec<V> enter = carry;
     for (int k = 0; k < u.cluster; ++k) {
@@ -286,9 +304,9 @@ __device__ __forceinline__ void receive_chain(const Args& a, const Unit<kLanes, 
   if (finish && on && u.rank == 0) store_vec<false>(finish + u.s * a.c + c, carry);
 }
 
-__device__ __forceinline__ void start_barriers(unsigned bars) {
+__device__ __forceinline__ void start_barriers(unsigned bars, int slots) {
   if (threadIdx.x == 0) {
-    for (int k = 0; k < kSlots; ++k)
+    for (int k = 0; k < slots; ++k)
       asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + k * 8) : "memory");
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -306,10 +324,10 @@ scan_forward_pipe_kernel(const Args a, unsigned* err) {
   extern __shared__ __align__(128) unsigned char dynamic[];
   const unsigned smem = smem_u32(dynamic);
   constexpr Layout l = layout_of<V, kLanes>(kTeams, kWarps, kStage, kStages);
-  const unsigned bars = smem + l.total - kSlots * 8;
+  const unsigned bars = smem + l.total - slots_of(kTeams) * 8;
   const Unit<kLanes, V> unit(a);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  start_barriers(bars);
+  start_barriers(bars, slots_of(kTeams));
   cluster_sync();
   if (warp == kTeams * kWarps) {
     send_chain<kLanes, V, kTeams, kWarps, false>(a, unit, smem, l, bars);
@@ -331,9 +349,9 @@ scan_forward_pipe_kernel(const Args a, unsigned* err) {
       if (r < a.geo.tiles) {
         const long long first = place(r, wt * (32 / kLanes));
         copy_stage<kLanes, V * kElem, kElem>(ring + stage * kStage, a.g, a.g_stride, a, unit.s,
-                                             unit.c0, unit.len, first);
+                                             unit.c0, unit.len, first, a.fine);
         copy_stage<kLanes, V * kElem, kElem>(ring + stage * kStage + T::kWarp, a.x, a.x_stride, a,
-                                             unit.s, unit.c0, unit.len, first);
+                                             unit.s, unit.c0, unit.len, first, a.fine);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -416,10 +434,10 @@ scan_backward_pipe_kernel(const Args a, unsigned* err) {
   extern __shared__ __align__(128) unsigned char dynamic[];
   const unsigned smem = smem_u32(dynamic);
   constexpr Layout l = layout_of<V, kLanes>(kTeams, kWarps, kStage, kStages);
-  const unsigned bars = smem + l.total - kSlots * 8;
+  const unsigned bars = smem + l.total - slots_of(kTeams) * 8;
   const Unit<kLanes, V> unit(a);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  start_barriers(bars);
+  start_barriers(bars, slots_of(kTeams));
   cluster_sync();
   if (warp == kTeams * kWarps) {
     send_chain<kLanes, V, kTeams, kWarps, true>(a, unit, smem, l, bars);
@@ -442,11 +460,12 @@ scan_backward_pipe_kernel(const Args a, unsigned* err) {
       if (r < a.geo.tiles) {
         const long long first = place(r, wt * (32 / kLanes));
         const unsigned to = ring + stage * kStage;
-        copy_stage<kLanes, V * kElem, kElem>(to, a.g, a.g_stride, a, unit.s, unit.c0, unit.len, first);
+        copy_stage<kLanes, V * kElem, kElem>(to, a.g, a.g_stride, a, unit.s, unit.c0, unit.len, first,
+                                             a.fine);
         copy_stage<kLanes, V * kElem, kElem>(to + T::kWarp, a.x, a.x_stride, a, unit.s, unit.c0,
-                                             unit.len, first);
+                                             unit.len, first, a.fine);
         copy_stage<kLanes, V * kGrad, kGrad>(to + 2 * T::kWarp, a.dout, a.c, a, unit.s, unit.c0,
-                                             unit.len, first);
+                                             unit.len, first, a.fine_dout);
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };

@@ -283,3 +283,102 @@ def test_refusals():
             plan.forward(good, good, out=bad)
     with pytest.raises(lna.LaplAttnError):
         lna.GatedScan(lna.make_scan_config(S, 0, C))
+
+
+# ---- long sequences: the pipelined kernels ------------------------------------------------
+
+@pytest.mark.parametrize("gate", ["decay", "sigmoid"])
+@pytest.mark.parametrize("reverse", [False, True])
+@pytest.mark.parametrize("dtype,out,grad", [("f32", "f32", "f32"), ("bf16", "bf16", "bf16"),
+                                            ("bf16", "f32", "f32"), ("f32", "bf16", "bf16")])
+def test_long_types(gate, reverse, dtype, out, grad):
+    run(3, 1111, 72, gate, dtype, out, grad, reverse=reverse, lens=[1111, 600, 1000])
+
+
+@pytest.mark.parametrize("C", [1, 2, 8, 10, 15, 16, 31, 32, 33, 63, 64, 65, 100, 129, 334])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_long_channels(C, dtype):
+    """Rows of 16 bytes, of 4, and of odd bf16 channels (the other kernels)."""
+    run(2, 1025, C, "sigmoid", dtype, dtype, dtype)
+
+
+@pytest.mark.parametrize("S,N,C", [(1, 768, 8), (1, 20000, 64), (3, 3000, 16), (40, 1500, 64),
+                                   (160, 800, 32), (2, 9001, 256)])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_long_splits(S, N, C, dtype):
+    """One CTA a sequence up to a cluster of eight; lanes over 8, 16 or 32 pieces of a row."""
+    run(S, N, C, "sigmoid", dtype, dtype, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("C,packed", [(24, 48), (24, 64), (22, 46), (64, 128), (333, 672), (334, 670)])
+def test_long_rows_apart(dtype, C, packed):
+    run(2, 900, C, "sigmoid", dtype, dtype, dtype, packed=packed, lens=[900, 333])
+
+
+def test_long_and_short_lengths():
+    run(6, 2000, 48, "sigmoid", "bf16", "bf16", "bf16", lens=[0, 1, 17, 1999, 2000, 1024])
+    run(6, 2000, 48, "decay", lens=[0, 1, 17, 1999, 2000, 1024], reverse=True, h0=False)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_long_misaligned(dtype):
+    """Tensors off 16 bytes, and off the pairs that bf16 channels are read in."""
+    import laplacian_nystr_attention_gb300 as lna
+    S, N, C = 2, 1000, 32
+    x, g, h0, dout, dfinal = make(S, N, C, "sigmoid", dtype)
+    want = None
+    for off in (0, 1, 2, 4, 8):
+        def place(a, t, off=off):
+            room = torch.zeros(a.size + 16, dtype=TYPES[t], device="cuda")
+            got = room[off:off + a.size].view(a.shape)
+            got.copy_(dev(a, t))
+            return got
+        plan = lna.GatedScan(lna.make_scan_config(S, N, C, in_dtype=dtype, out_dtype=dtype,
+                                                  grad_dtype=dtype))
+        xs, gs, ds = place(x, dtype), place(g, dtype), place(ref.rounded(dout, dtype), dtype)
+        hs, dfs = place(h0, "f32"), place(dfinal, "f32")
+        states = place(np.zeros(plan.states_shape), "f32")
+        y = plan.forward(xs, gs, h0=hs, states=states, out=place(np.zeros((S, N, C)), dtype))
+        grads = {"dx": place(np.zeros((S, N, C)), dtype), "dg": place(np.zeros((S, N, C)), dtype)}
+        dx, dg, dh0 = plan.backward(xs, gs, states, ds, dfinal=dfs, grads=grads)
+        if want is None:
+            want = ref.scan(x, g, "sigmoid", h0, dout=ref.rounded(dout, dtype), dfinal=dfinal)
+        ref.check("h", y, want["h"], dtype)
+        ref.check("states", states, want["states"])
+        ref.check("dx", dx, want["dx"], dtype)
+        ref.check("dg", dg, want["dg"], dtype)
+        ref.check("dh0", dh0, want["dh0"])
+
+
+def test_long_bit_for_bit_on_two_streams():
+    """Two plans at work at once, a few calls each, on streams of their own."""
+    import laplacian_nystr_attention_gb300 as lna
+    S, N, C = 4, 5000, 128
+    plans = [lna.GatedScan(lna.make_scan_config(S, N, C)) for _ in range(2)]
+    ins = [[dev(a) for a in make(S, N, C, "sigmoid", "f32", seed=s)] for s in (0, 1)]
+
+    def both(plan, x, g, h0, dout, dfinal):
+        states, final = torch.empty(plan.states_shape, device="cuda"), torch.empty_like(h0)
+        y = plan.forward(x, g, h0=h0, states=states, final=final)
+        return [y, final, states, *plan.backward(x, g, states, dout, dfinal)]
+
+    want = [both(p, *i) for p, i in zip(plans, ins)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in plans]
+    for _ in range(3):
+        got = []
+        for p, i, s in zip(plans, ins, streams):
+            with torch.cuda.stream(s):
+                got.append(both(p, *i))
+        torch.cuda.synchronize()
+        for a, b in zip(want, got):
+            assert all(torch.equal(t, u) for t, u in zip(a, b))
+
+
+def test_no_wait_gave_up():
+    """After all of the above the device error word is clear."""
+    import laplacian_nystr_attention_gb300 as lna
+    att = lna.LaplacianNystromAttention(lna.make_config(1, 1, 4, 4, 8, 4))
+    assert lna.lapl_attn_device_errors(att.handle, torch.cuda.current_stream().cuda_stream) == 0
+    att.close()
