@@ -215,7 +215,7 @@ int lapl_attn_kernels_per_forward(lapl_attn_handle h);
  * kernel's TMA pipeline, the tensor-core Newton-Schulz solve) bound every such wait (one second
  * by default); a wait that gives up sets a bit of a device error word (one per device, shared
  * by all handles) -- bit 1 the distance kernel, bit 2 the tensor-core solve, bit 4 a tensor-core
- * kernel of the output chain -- and the waiting
+ * kernel of the output chain, bit 8 the recurrence of lapl_ops.h -- and the waiting
  * warps leave the kernel after the copies and tensor-core operations they issued have
  * completed, so a failed forward ends instead of hanging, the context stays usable, and its
  * outputs are undefined.  This call copies the word to *flags, clears it, and synchronises

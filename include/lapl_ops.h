@@ -57,11 +57,13 @@ typedef struct {
 
 typedef struct lapl_scan_plan* lapl_scan_handle;
 
-/* Launch choices of a plan (fixed at create). */
+/* Launch choices of a plan's forward (fixed at create), where pointers allow its fastest kernel. */
 typedef struct {
   int cluster;  /* CTAs (one thread-block cluster) that share a sequence's tokens               */
   int lanes;    /* threads across the channels of one token                                     */
   int threads;  /* threads of a CTA                                                             */
+  int teams;    /* teams of warps that take the tokens in turn, copied ahead (the kernels for long
+                   sequences: 768 tokens or more, fp32 or an even number of bf16 channels), or 0  */
 } lapl_scan_plan_info;
 
 lapl_status lapl_scan_create(const lapl_scan_config* cfg, lapl_scan_handle* out);
@@ -91,6 +93,23 @@ lapl_status lapl_scan_backward(lapl_scan_handle h, const void* x, const void* g,
                                void* stream);
 
 lapl_status lapl_scan_plan_info_get(lapl_scan_handle h, lapl_scan_plan_info* info);
+
+/*
+ * Device-side failure report, as lapl_attn_device_errors (the same word, one per device, read and
+ * cleared; synchronises `stream`): the kernels for long sequences exchange maps between CTAs and
+ * bound every wait for them (one second); one that gives up sets bit 8, the kernel ends, and its
+ * outputs are undefined.  LAPL_ERR_DEVICE_TIMEOUT when a flag was set.
+ */
+lapl_status lapl_scan_device_errors(lapl_scan_handle h, void* stream, unsigned* flags);
+
+/*
+ * Fault injection, for testing that report: wait_ns: the bound of the waits of this plan's calls
+ * from now on (0: one second); skip_last = 1: the last round's maps are never sent, so that the
+ * waits for them run out (kernels for long sequences only: plan_info teams > 0); 0: normal.
+ */
+lapl_status lapl_scan_set_fault_injection(lapl_scan_handle h, unsigned long long wait_ns,
+                                          int skip_last);
+
 const char* lapl_scan_last_error(lapl_scan_handle h);
 lapl_status lapl_scan_destroy(lapl_scan_handle h);
 

@@ -33,7 +33,8 @@ from ._lib import (LAPL_F8E4M3, LAPL_GATE_DECAY, LAPL_GATE_SIGMOID, LAPL_SCAN_CH
                    lapl_norm_backward, lapl_norm_config, lapl_norm_create, lapl_norm_destroy,
                    lapl_norm_forward, lapl_norm_last_error, lapl_norm_workspace_size,
                    lapl_scan_backward, lapl_scan_config, lapl_scan_create, lapl_scan_destroy,
-                   lapl_scan_forward, lapl_scan_last_error, lapl_scan_plan_info_get)
+                   lapl_scan_device_errors, lapl_scan_forward, lapl_scan_last_error,
+                   lapl_scan_plan_info_get, lapl_scan_set_fault_injection)
 from .operators import (GatedScan, GradClip, ResidualNorm, make_norm_config, make_scan_config)
 
 __all__ = [
@@ -50,7 +51,8 @@ __all__ = [
     "GatedScan", "ResidualNorm", "GradClip", "make_scan_config", "make_norm_config",
     "LAPL_F8E4M3", "LAPL_GATE_DECAY", "LAPL_GATE_SIGMOID", "LAPL_SCAN_CHUNK",
     "lapl_scan_config", "lapl_scan_create", "lapl_scan_forward", "lapl_scan_backward",
-    "lapl_scan_plan_info_get", "lapl_scan_last_error", "lapl_scan_destroy",
+    "lapl_scan_plan_info_get", "lapl_scan_device_errors", "lapl_scan_set_fault_injection",
+    "lapl_scan_last_error", "lapl_scan_destroy",
     "lapl_norm_config", "lapl_norm_create", "lapl_norm_forward", "lapl_norm_workspace_size",
     "lapl_norm_backward", "lapl_norm_last_error", "lapl_norm_destroy",
     "lapl_clip_config", "lapl_clip_create", "lapl_clip_workspace_size", "lapl_clip_norm",

@@ -67,7 +67,7 @@ class lapl_scan_config(ctypes.Structure):
 
 
 class lapl_scan_plan_info(ctypes.Structure):
-    _fields_ = [(name, ctypes.c_int) for name in ("cluster", "lanes", "threads")]
+    _fields_ = [(name, ctypes.c_int) for name in ("cluster", "lanes", "threads", "teams")]
 
 
 class lapl_norm_config(ctypes.Structure):
@@ -124,6 +124,8 @@ def _load():
         "lapl_scan_forward": ([H, vp, vp, vp, vp, vp, vp, vp, vp], st),
         "lapl_scan_backward": ([H, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp], st),
         "lapl_scan_plan_info_get": ([H, ctypes.POINTER(lapl_scan_plan_info)], st),
+        "lapl_scan_device_errors": ([H, vp, ctypes.POINTER(ctypes.c_uint)], st),
+        "lapl_scan_set_fault_injection": ([H, ctypes.c_ulonglong, ctypes.c_int], st),
         "lapl_scan_last_error": ([H], ctypes.c_char_p),
         "lapl_scan_destroy": ([H], st),
         "lapl_norm_create": ([ctypes.POINTER(lapl_norm_config), ctypes.POINTER(H)], st),
@@ -159,7 +161,8 @@ EXPORTED = ["lapl_attn_version", "lapl_attn_status_string", "lapl_attn_last_erro
             "lapl_attn_backward_workspace_size", "lapl_attn_backward",
             "lapl_attn_backward_kernels", "lapl_attn_destroy",
             "lapl_scan_create", "lapl_scan_forward", "lapl_scan_backward",
-            "lapl_scan_plan_info_get", "lapl_scan_last_error", "lapl_scan_destroy",
+            "lapl_scan_plan_info_get", "lapl_scan_device_errors",
+            "lapl_scan_set_fault_injection", "lapl_scan_last_error", "lapl_scan_destroy",
             "lapl_norm_create", "lapl_norm_forward", "lapl_norm_workspace_size",
             "lapl_norm_backward", "lapl_norm_last_error", "lapl_norm_destroy",
             "lapl_clip_create", "lapl_clip_workspace_size", "lapl_clip_norm", "lapl_clip_apply",
@@ -330,6 +333,19 @@ def lapl_scan_plan_info_get(handle) -> dict:
     _check(LIB.lapl_scan_plan_info_get(handle, ctypes.byref(info)), "lapl_scan_plan_info_get",
            handle, "lapl_scan_last_error")
     return {name: int(getattr(info, name)) for name, _ in lapl_scan_plan_info._fields_}
+
+
+def lapl_scan_device_errors(handle, stream) -> int:
+    """Read and clear the device error word (synchronises `stream`); raises on a set flag."""
+    flags = ctypes.c_uint(0)
+    _check(LIB.lapl_scan_device_errors(handle, stream, ctypes.byref(flags)),
+           "lapl_scan_device_errors", handle, "lapl_scan_last_error")
+    return flags.value
+
+
+def lapl_scan_set_fault_injection(handle, wait_ns: int, skip_last: int) -> None:
+    _check(LIB.lapl_scan_set_fault_injection(handle, int(wait_ns), int(skip_last)),
+           "lapl_scan_set_fault_injection", handle, "lapl_scan_last_error")
 
 
 def lapl_scan_last_error(handle) -> str:

@@ -26,7 +26,7 @@
 #include <algorithm>
 #include <new>
 
-#include "common.cuh"
+#include "ops_common.cuh"
 
 namespace lapl {
 
@@ -906,10 +906,11 @@ lapl_status lapl_attn_device_errors(lapl_attn_handle h, void* stream, unsigned* 
   *flags = word;
   if (word) {
     snprintf(h->last_error, sizeof(h->last_error),
-             "device error flags 0x%x: a bounded barrier wait gave up in:%s%s%s", word,
+             "device error flags 0x%x: a bounded barrier wait gave up in:%s%s%s%s", word,
              (word & kErrBitCdist) ? " the distance kernel;" : "",
              (word & kErrBitSolve) ? " the tensor-core Newton-Schulz solve;" : "",
-             (word & kErrBitChain) ? " a tensor-core kernel of the output chain;" : "");
+             (word & kErrBitChain) ? " a tensor-core kernel of the output chain;" : "",
+             (word & kErrBitScan) ? " the gated linear recurrence (lapl_ops.h);" : "");
     return LAPL_ERR_DEVICE_TIMEOUT;
   }
   return LAPL_OK;

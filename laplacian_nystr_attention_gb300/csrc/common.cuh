@@ -18,7 +18,6 @@ namespace lapl {
 constexpr unsigned kErrBitCdist = 1u;   // distance kernel (TMA pipeline)
 constexpr unsigned kErrBitSolve = 2u;   // Newton-Schulz solve on the tensor cores
 constexpr unsigned kErrBitChain = 4u;   // tensor-core B V or output product
-constexpr unsigned kErrBitScan = 8u;    // cluster exchange of the gated linear recurrence
 
 constexpr int kMaxS = 8;            // landmark grid side: m = s*s <= 64
 constexpr int kMaxM = kMaxS * kMaxS;

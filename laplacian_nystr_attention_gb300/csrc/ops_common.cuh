@@ -9,6 +9,11 @@
 #include "lapl_ops.h"
 
 namespace lapl {
+
+// A bit of the device error word beside those of common.cuh: the exchange between CTAs of the gated
+// linear recurrence.
+constexpr unsigned kErrBitScan = 8u;
+
 namespace ops {
 
 constexpr int kErrorText = 256;

@@ -376,44 +376,58 @@ struct Pipe {
   Geo geo;
 };
 
-// The shape with the least work on the longest path: waves of clusters, as many as the GPU holds at
-// once, times rounds, and three rounds' time to start and end each wave.
-cudaError_t choose_pipe(const lapl_scan_config& c, bool backward, Pipe* out) {
+// Clusters of 1 .. kMaxCluster pipelined CTAs that the device holds at once: by cluster size, the
+// same for all these kernels (each takes an SM to itself).
+struct Held {
+  int clusters[pipe::kMaxCluster + 1];
+};
+cudaError_t clusters_held(const pipe::Pick& k, Held* out) {
+  for (int n = 1; n <= pipe::kMaxCluster; ++n) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)n);
+    cfg.blockDim = dim3((unsigned)(k.teams * k.warps + 2) * 32);
+    cfg.dynamicSmemBytes = k.smem;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)n;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(&out->clusters[n], k.kernel, &cfg);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+pipe::Pick pick_pipe(const lapl_scan_config& c, bool backward, int lanes) {
   const bool in16 = c.in_dtype == LAPL_BF16, sig = c.gate == LAPL_GATE_SIGMOID;
   const bool other16 = (backward ? c.grad_dtype : c.out_dtype) == LAPL_BF16;
-  const int v = in16 ? 2 : 1;
+  if (backward)
+    return in16 ? pipe::backward_bf16(other16, sig, lanes) : pipe::backward_f32(other16, sig, lanes);
+  return in16 ? pipe::forward_bf16(other16, sig, lanes) : pipe::forward_f32(other16, sig, lanes);
+}
+
+// The shape with the least work on the longest path: waves of clusters, as many as the GPU holds at
+// once, times rounds, and three rounds' time to start and end each wave.  Of nearly equal ones
+// (within 5%) the one with the longest pieces of a row.
+cudaError_t choose_pipe(const lapl_scan_config& c, bool backward, const Held& held, Pipe* out) {
+  const int v = c.in_dtype == LAPL_BF16 ? 2 : 1;
   out->pick.kernel = nullptr;
   double best = 0;
   for (int lanes = 32; lanes >= 8; lanes /= 2) {
-    const pipe::Pick k =
-        backward ? (in16 ? pipe::backward_bf16(other16, sig, lanes) : pipe::backward_f32(other16, sig, lanes))
-                 : (in16 ? pipe::forward_bf16(other16, sig, lanes) : pipe::forward_f32(other16, sig, lanes));
-    cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k.kernel),
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.smem);
-    if (e != cudaSuccess) return e;
+    const pipe::Pick k = pick_pipe(c, backward, lanes);
     Geo g = {};
     g.lanes = lanes;
     g.blocks = (c.channels + lanes * v - 1) / (lanes * v);
     g.threads = (k.teams * k.warps + 2) * 32;
     const long long units = (long long)c.sequences * g.blocks;
     const int tile = k.warps * (32 / lanes) * kT;
-    for (g.cluster = 1; g.cluster <= pipe::kMaxCluster; g.cluster *= 2) {
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3((unsigned)g.cluster);
-      cfg.blockDim = dim3((unsigned)g.threads);
-      cfg.dynamicSmemBytes = k.smem;
-      cudaLaunchAttribute at[1];
-      at[0].id = cudaLaunchAttributeClusterDimension;
-      at[0].val.clusterDim.x = (unsigned)g.cluster;
-      at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-      cfg.attrs = at;
-      cfg.numAttrs = 1;
-      int held = 0;
-      e = cudaOccupancyMaxActiveClusters(&held, k.kernel, &cfg);
-      if (e != cudaSuccess) return e;
-      if (held < 1) continue;
-      g.tiles = (int)(((long long)c.tokens + (long long)g.cluster * tile - 1) / ((long long)g.cluster * tile));
-      const double cost = (double)((units + held - 1) / held) * (g.tiles + 3);
+    for (g.cluster = 1; g.cluster <= pipe::kMaxCluster; ++g.cluster) {
+      const int at_once = held.clusters[g.cluster];
+      if (at_once < 1) continue;
+      const long long round = (long long)g.cluster * tile;
+      g.tiles = (int)((c.tokens + round - 1) / round);
+      const double cost = (double)((units + at_once - 1) / at_once) * (g.tiles + 3);
       if (!out->pick.kernel || cost < 0.95 * best) {
         best = cost;
         out->pick = k;
@@ -421,7 +435,8 @@ cudaError_t choose_pipe(const lapl_scan_config& c, bool backward, Pipe* out) {
       }
     }
   }
-  return cudaSuccess;
+  return cudaFuncSetAttribute(reinterpret_cast<const void*>(out->pick.kernel),
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)out->pick.smem);
 }
 
 lapl_status validate(const lapl_scan_config* c) {
@@ -450,12 +465,16 @@ struct lapl_scan_plan {
   unsigned* dev_err;
   lapl::scan::Geo geo[2];   // by channels a lane: 1, 2
   lapl::scan::Pipe fwd, bwd;
+  unsigned long long wait_ns;
+  int skip_last;
   char last_error[lapl::ops::kErrorText];
 };
 
 using namespace lapl;
 
 namespace {
+
+constexpr unsigned long long kWaitNs = 1000000000ull;   // one second
 
 // Tokens from which the pipelined kernels are taken (784 tokens of 128 x 64 channels, bf16: 14.8
 // against 19.4 us; 512 tokens of 64 x 64: equal; shorter ones leave their teams without work).
@@ -535,6 +554,8 @@ scan::Args base_args(const lapl_scan_plan& p) {
   a.c = c.channels;
   a.chunks = (c.tokens + scan::kT - 1) / scan::kT;
   a.reverse = c.reverse;
+  a.wait_ns = p.wait_ns;
+  a.skip_last = p.skip_last != 0;
   a.x_stride = c.x_stride ? c.x_stride : c.channels;
   a.g_stride = c.g_stride ? c.g_stride : c.channels;
   return a;
@@ -552,6 +573,7 @@ lapl_status lapl_scan_create(const lapl_scan_config* cfg, lapl_scan_handle* out)
   lapl_scan_plan* p = new (std::nothrow) lapl_scan_plan();
   if (!p) return LAPL_ERR_INVALID_ARG;
   p->cfg = *cfg;
+  p->wait_ns = kWaitNs;
   int sms = 0;
   cudaError_t e = cudaGetDevice(&p->device);
   if (e == cudaSuccess)
@@ -567,8 +589,13 @@ lapl_status lapl_scan_create(const lapl_scan_config* cfg, lapl_scan_handle* out)
   const bool pairs = cfg->in_dtype == LAPL_F32 ||
                      (cfg->channels % 2 == 0 && cfg->x_stride % 2 == 0 && cfg->g_stride % 2 == 0);
   if (e == cudaSuccess && pairs && cfg->tokens >= kPipeTokens && cfg->sequences > 0) {
-    e = scan::choose_pipe(*cfg, false, &p->fwd);
-    if (e == cudaSuccess) e = scan::choose_pipe(*cfg, true, &p->bwd);
+    scan::Held held = {};
+    const scan::pipe::Pick one = scan::pick_pipe(*cfg, false, 32);
+    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(one.kernel),
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)one.smem);
+    if (e == cudaSuccess) e = scan::clusters_held(one, &held);
+    if (e == cudaSuccess) e = scan::choose_pipe(*cfg, false, held, &p->fwd);
+    if (e == cudaSuccess) e = scan::choose_pipe(*cfg, true, held, &p->bwd);
   }
   if (e != cudaSuccess) {
     cudaGetLastError();
@@ -658,9 +685,42 @@ lapl_status lapl_scan_backward(lapl_scan_handle p, const void* x, const void* g,
 lapl_status lapl_scan_plan_info_get(lapl_scan_handle p, lapl_scan_plan_info* info) {
   if (!p || !info) return LAPL_ERR_INVALID_ARG;
   const int v = p->cfg.in_dtype == LAPL_BF16 && p->cfg.channels % 2 == 0 ? 2 : 1;
-  info->cluster = p->geo[v - 1].cluster;
-  info->lanes = p->geo[v - 1].lanes;
-  info->threads = p->geo[v - 1].threads;
+  const bool pipe = p->fwd.pick.kernel != nullptr;
+  const scan::Geo& g = pipe ? p->fwd.geo : p->geo[v - 1];
+  info->cluster = g.cluster;
+  info->lanes = g.lanes;
+  info->threads = g.threads;
+  info->teams = pipe ? p->fwd.pick.teams : 0;
+  return LAPL_OK;
+}
+
+lapl_status lapl_scan_device_errors(lapl_scan_handle p, void* stream, unsigned* flags) {
+  if (!p || !flags) return LAPL_ERR_INVALID_ARG;
+  const lapl_status ok = ops::check_device(p->device, p->last_error, "device_errors/device");
+  if (ok != LAPL_OK) return ok;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  unsigned word = 0;
+  cudaError_t e = cudaMemcpyAsync(&word, p->dev_err, sizeof(word), cudaMemcpyDeviceToHost, st);
+  if (e == cudaSuccess) e = cudaMemsetAsync(p->dev_err, 0, sizeof(word), st);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(st);
+  if (e != cudaSuccess) {
+    ops::set_error(p->last_error, e, "device_errors");
+    return LAPL_ERR_CUDA;
+  }
+  *flags = word;
+  if (!word) return LAPL_OK;
+  snprintf(p->last_error, sizeof(p->last_error),
+           "device error flags 0x%x: a bounded wait gave up in:%s%s", word,
+           (word & kErrBitScan) ? " the recurrence's exchange between CTAs;" : "",
+           (word & ~kErrBitScan) ? " a kernel of the attention;" : "");
+  return LAPL_ERR_DEVICE_TIMEOUT;
+}
+
+lapl_status lapl_scan_set_fault_injection(lapl_scan_handle p, unsigned long long wait_ns,
+                                          int skip_last) {
+  if (!p || skip_last < 0 || skip_last > 1) return LAPL_ERR_INVALID_ARG;
+  p->wait_ns = wait_ns ? wait_ns : kWaitNs;
+  p->skip_last = skip_last;
   return LAPL_OK;
 }
 

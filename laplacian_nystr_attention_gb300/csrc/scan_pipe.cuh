@@ -39,7 +39,6 @@ constexpr int kMaxCluster = 8;     // CTAs
 __host__ __device__ constexpr int slots_of(int teams) { return 2 * teams; }
 // Worker warps of a team: with the chain's two 18 warps of 96 registers, or 16 of 128.
 constexpr int kForwardTeams = 4, kForwardWarps = 4, kBackwardTeams = 3, kBackwardWarps = 4;
-constexpr unsigned long long kWaitNs = 1000000000ull;
 
 // Bytes of a row of one tensor in shared memory, and from one run of kT rows to the next: a warp
 // reads rows of 32 / kLanes runs at once, which lie side by side in the banks thanks to one row of
@@ -138,8 +137,8 @@ __device__ __forceinline__ void get_state(unsigned at, Vec<1>& v) {
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v.f[0]) : "r"(at) : "memory");
 }
 
-// Until the phase of the given parity is complete, or false after kWaitNs.
-__device__ __forceinline__ bool wait_phase(unsigned bar, unsigned parity) {
+// Until the phase of the given parity is complete, or false after `bound` ns.
+__device__ __forceinline__ bool wait_phase(unsigned bar, unsigned parity, unsigned long long bound) {
   auto done = [&] {
     unsigned d;
     asm volatile("{\n\t.reg .pred p;\n\t"
@@ -155,7 +154,7 @@ __device__ __forceinline__ bool wait_phase(unsigned bar, unsigned parity) {
   if (done()) return true;
   const unsigned long long t0 = now();
   while (!done())
-    if (now() - t0 > kWaitNs) return false;
+    if (now() - t0 > bound) return false;
   return true;
 }
 
@@ -257,8 +256,9 @@ __device__ __forceinline__ void send_chain(const Args& a, const Unit<kLanes, V>&
       all = {shuffle(all.a, 32 - kLanes + pos), shuffle(all.b, 32 - kLanes + pos)};
     }
     const unsigned to = smem + l.slots + ((slot * kMaxCluster + u.rank) * kLanes + pos) * kMap;
-    for (int k = set; k < u.cluster; k += kSets)
-      send_map(at_rank(to, k), at_rank(bars + slot * 8, k), all);
+    if (!(a.skip_last && r == a.geo.tiles - 1))
+      for (int k = set; k < u.cluster; k += kSets)
+        send_map(at_rank(to, k), at_rank(bars + slot * 8, k), all);
 #pragma unroll
     for (int k = 0; k < kWarps; ++k) {
       put_map(runs + k * kBy, before);
@@ -287,7 +287,7 @@ __device__ __forceinline__ void receive_chain(const Args& a, const Unit<kLanes, 
     if (lane == 0)
       asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
                    ::"r"(bar), "r"(u.cluster * kLanes * kMap) : "memory");
-    if (!lost && !wait_phase(bar, (r / slots_of(kTeams)) & 1)) lost = true;
+    if (!lost && !wait_phase(bar, (r / slots_of(kTeams)) & 1, a.wait_ns)) lost = true;
     const unsigned slots = smem + l.slots + (slot * kMaxCluster * kLanes + pos) * kMap;
     Vec<V> enter = carry;
     for (int k = 0; k < u.cluster; ++k) {

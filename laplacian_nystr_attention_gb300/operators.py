@@ -320,6 +320,7 @@ class GradClip(_Plan):
         self.workspace_bytes = _lib.lapl_clip_workspace_size(self.handle)
         self._workspace_floats = self.workspace_bytes // 4
         self._float = _torch_dtype(LAPL_F32)
+        self._devices = [self._index] * n
 
     @classmethod
     def like(cls, tensors):
@@ -335,13 +336,16 @@ class GradClip(_Plan):
         """The tensors' addresses, if they are the plan's."""
         if len(tensors) != len(self.counts):
             raise ValueError(f"{name}: expected {len(self.counts)} tensors, got {len(tensors)}")
-        device = self._index
-        for t, n, dtype in zip(tensors, self.counts, self._torch_dtypes):
-            if (t.dtype is not dtype or t.numel() != n or t.get_device() != device
-                    or not t.is_contiguous()):
-                raise ValueError(f"{name}: expected a contiguous {dtype} tensor of {n} values on "
-                                 f"{self.device}, got {t.dtype} {tuple(t.shape)} with strides "
-                                 f"{t.stride()} on {t.device}")
+        if ([t.dtype for t in tensors] != self._torch_dtypes
+                or [t.numel() for t in tensors] != self.counts
+                or [t.get_device() for t in tensors] != self._devices
+                or not all([t.is_contiguous() for t in tensors])):
+            for t, n, dtype in zip(tensors, self.counts, self._torch_dtypes):
+                if (t.dtype is not dtype or t.numel() != n or t.get_device() != self._index
+                        or not t.is_contiguous()):
+                    raise ValueError(f"{name}: expected a contiguous {dtype} tensor of {n} values "
+                                     f"on {self.device}, got {t.dtype} {tuple(t.shape)} with "
+                                     f"strides {t.stride()} on {t.device}")
         return [t.data_ptr() for t in tensors]
 
     def _room(self):

@@ -376,6 +376,30 @@ def test_long_bit_for_bit_on_two_streams():
             assert all(torch.equal(t, u) for t, u in zip(a, b))
 
 
+@pytest.mark.parametrize("S,N,C", [(1, 20000, 64), (40, 1500, 64)])
+def test_wait_that_gives_up_is_reported(S, N, C):
+    """The last round's maps are never sent: the waits for them run out after 2 ms, the kernel ends,
+    and the report says so; the next call is right again."""
+    import laplacian_nystr_attention_gb300 as lna
+    plan = lna.GatedScan(lna.make_scan_config(S, N, C))
+    assert _info(plan)["teams"] > 0
+    x, g, h0, dout, dfinal = (dev(a) for a in make(S, N, C, "sigmoid", "f32"))
+    states, final = torch.empty(plan.states_shape, device="cuda"), torch.empty_like(h0)
+    want = plan.forward(x, g, h0=h0, states=states)
+    grads = plan.backward(x, g, states, dout, dfinal)
+    st = torch.cuda.current_stream().cuda_stream
+    lna.lapl_scan_set_fault_injection(plan.handle, 2_000_000, 1)
+    for call in (lambda: plan.forward(x, g, h0=h0), lambda: plan.backward(x, g, states, dout)):
+        call()
+        with pytest.raises(lna.LaplAttnError) as e:
+            lna.lapl_scan_device_errors(plan.handle, st)
+        assert e.value.status == 6 and "recurrence" in str(e.value)
+    lna.lapl_scan_set_fault_injection(plan.handle, 0, 0)
+    assert torch.equal(plan.forward(x, g, h0=h0), want)
+    assert all(torch.equal(a, b) for a, b in zip(grads, plan.backward(x, g, states, dout, dfinal)))
+    assert lna.lapl_scan_device_errors(plan.handle, st) == 0
+
+
 def test_no_wait_gave_up():
     """After all of the above the device error word is clear."""
     import laplacian_nystr_attention_gb300 as lna

@@ -26,7 +26,7 @@ def lib():
 
 
 def test_every_entry_point_is_exported_and_wrapped(lib):
-    assert len(ENTRY_POINTS) == 18
+    assert len(ENTRY_POINTS) == 20
     raw = ctypes.CDLL(lib.LIB_PATH)
     for name in ENTRY_POINTS:
         assert hasattr(raw, name) and name in lib.EXPORTED and callable(getattr(lib, name)), name
@@ -108,6 +108,8 @@ def test_null_arguments(lib):
     assert lib.LIB.lapl_scan_forward(*[None] * 9) == 1
     assert lib.LIB.lapl_scan_backward(*[None] * 11) == 1
     assert lib.LIB.lapl_scan_plan_info_get(None, None) == 1
+    assert lib.LIB.lapl_scan_device_errors(None, None, None) == 1
+    assert lib.LIB.lapl_scan_set_fault_injection(None, 0, 0) == 1
     assert lib.LIB.lapl_norm_forward(*[None] * 9) == 1
     assert lib.LIB.lapl_norm_backward(*[None] * 10, 0, None) == 1
     assert lib.LIB.lapl_norm_workspace_size(None, None) == 1
@@ -148,6 +150,7 @@ def test_tensor_checks_refuse(lib):
         n._by_head(torch.zeros(2, 5, 1, 8), n._x, n._x_row)
     c = lna.GradClip.__new__(lna.GradClip)
     c.counts, c._torch_dtypes = [4, 0], [torch.float32, torch.bfloat16]
+    c._devices = [-1, -1]
     c.device = torch.device("cpu")
     assert len(c._list([torch.zeros(2, 2), torch.zeros(0, dtype=torch.bfloat16)], "g")) == 2
     for bad in ([torch.zeros(4)], [torch.zeros(5), torch.zeros(0, dtype=torch.bfloat16)],
