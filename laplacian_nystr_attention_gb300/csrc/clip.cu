@@ -65,19 +65,22 @@ __device__ __forceinline__ Piece piece_of(const Table<N>& t, int i) {
 }
 
 struct Sums {
-  float low, high;
-  __device__ __forceinline__ void add(float x) {
-    const float l = x * kLow, h = x * kHigh;
-    low = fmaf(l, l, low);
-    high = fmaf(h, h, high);
+  ops::Vec<2> low, high;   // of even and odd values
+  __device__ __forceinline__ void add(const ops::Vec<2>& x) {
+    const ops::Vec<2> l = ops::mul(x, ops::fill<2>(kLow)), h = ops::mul(x, ops::fill<2>(kHigh));
+    low = ops::fma(l, l, low);
+    high = ops::fma(h, h, high);
   }
   template <bool kHalf>
-  __device__ __forceinline__ void add(uint32_t w) {
+  __device__ __forceinline__ void add(const uint4& v) {
     if constexpr (kHalf) {
-      add(bf16_lo(w));
-      add(bf16_hi(w));
+      add({bf16_lo(v.x), bf16_hi(v.x)});
+      add({bf16_lo(v.y), bf16_hi(v.y)});
+      add({bf16_lo(v.z), bf16_hi(v.z)});
+      add({bf16_lo(v.w), bf16_hi(v.w)});
     } else {
-      add(__uint_as_float(w));
+      add({__uint_as_float(v.x), __uint_as_float(v.y)});
+      add({__uint_as_float(v.z), __uint_as_float(v.w)});
     }
   }
 };
@@ -144,19 +147,14 @@ __device__ __forceinline__ Sums squares(const Piece& p) {
   // Values before the first 16-byte boundary, 16 bytes at a time, and the rest.
   const int head = min(p.count, (int)((16 - ((uintptr_t)p.in & 15)) & 15) / kBytes);
   const int vectors = (p.count - head) * kBytes / 16;
-  Sums s = {0.f, 0.f};
+  Sums s = {};
   each_vector(reinterpret_cast<const uint4*>(p.in + head * kBytes), vectors,
-              [&](int, const uint4& v) {
-                s.add<kHalf>(v.x);
-                s.add<kHalf>(v.y);
-                s.add<kHalf>(v.z);
-                s.add<kHalf>(v.w);
-              });
+              [&](int, const uint4& v) { s.add<kHalf>(v); });
   const int body = vectors * 16 / kBytes;
   for (int k = threadIdx.x; k < p.count - body; k += kThreads) {
     const int e = k < head ? k : k + body;
-    if constexpr (kHalf) s.add(ops::bf16_bits(reinterpret_cast<const uint16_t*>(p.in)[e]));
-    else s.add(reinterpret_cast<const float*>(p.in)[e]);
+    if constexpr (kHalf) s.add({ops::bf16_bits(reinterpret_cast<const uint16_t*>(p.in)[e]), 0.f});
+    else s.add({reinterpret_cast<const float*>(p.in)[e], 0.f});
   }
   return s;
 }
@@ -171,8 +169,8 @@ clip_norm_kernel(const __grid_constant__ Table<N> t, Pairs* part) {
   for (int i = blockIdx.x; i < pieces; i += gridDim.x) {
     const Piece p = piece_of(t, i);
     const Sums s = p.half ? squares<true>(p) : squares<false>(p);
-    sum.low.add(s.low);
-    sum.high.add(s.high);
+    sum.low.add(s.low.f[0] + s.low.f[1]);
+    sum.high.add(s.high.f[0] + s.high.f[1]);
   }
   sum = block_sum(sum, sm);
   if (threadIdx.x == 0) part[blockIdx.x] = sum;

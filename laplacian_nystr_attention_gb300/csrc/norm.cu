@@ -13,7 +13,7 @@ __global__ void __launch_bounds__(kMaxThreads)
 norm_backward_kernel(const Args a) {
   __shared__ float scratch[2][kMaxThreads / 32];
   extern __shared__ float sums[];   // [rows side by side, W]
-  constexpr bool kAhead = NV * VEC <= 8;
+  constexpr bool kAhead = NV * ((kRes16 ? 4 : 8) + 2 * (kGrad16 ? 4 : 8)) * VEC / 8 <= 24;
   // The kernel that sums the partials may be placed now; it waits for this grid's end.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int t = place_in_row(a);
@@ -111,24 +111,27 @@ norm_backward_kernel(const Args a) {
   }
 }
 
-// dweight[c] = sum over the CTAs' partials in a fixed order: 32 columns by 32 slices a CTA.
+// dweight[c] = sum over the CTAs' partials in a fixed order: 8 columns by 128 slices a CTA.
 __global__ void __launch_bounds__(1024)
 norm_dweight_kernel(const float* part, float* dweight, int ctas, int width) {
-  __shared__ float sm[32][33];
+  __shared__ float sm[32][9];
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the partials are written
-  const int c = blockIdx.x * 32 + threadIdx.x;
+  const int c = blockIdx.x * 8 + (threadIdx.x & 7);
   float v = 0.f;
   if (c < width) {
-#pragma unroll 8
-    for (int k = threadIdx.y; k < ctas; k += 32) v += part[(size_t)k * width + c];
+#pragma unroll 4
+    for (int k = threadIdx.x >> 3; k < ctas; k += 128) v += part[(size_t)k * width + c];
   }
-  sm[threadIdx.y][threadIdx.x] = v;
+  v += __shfl_xor_sync(0xffffffffu, v, 8);
+  v += __shfl_xor_sync(0xffffffffu, v, 16);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane < 8) sm[warp][lane] = v;
   __syncthreads();
-  // Column threadIdx.y's 32 slices, one a lane.
-  v = sm[threadIdx.x][threadIdx.y];
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  const int mine = blockIdx.x * 32 + threadIdx.y;
-  if (threadIdx.x == 0 && mine < width) dweight[mine] = v;
+  if (warp < 8) {   // column `warp`, one of its sums a lane
+    v = sm[lane][warp];
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane == 0 && blockIdx.x * 8 + warp < width) dweight[blockIdx.x * 8 + warp] = v;
+  }
 }
 
 // ---- host --------------------------------------------------------------------------------
@@ -144,18 +147,19 @@ Divisor divisor(unsigned long long n) {
 struct Shape {
   int g, nv, threads, per, per_log2;
 };
-Shape shape_of(int width, Cut cut, bool backward) {
+// `two`: longer rows take two vectors a thread (the forward, and the backward where all is bf16: its
+// part of dweight and of the next row fits the registers), else one, for as long as 512 threads do.
+Shape shape_of(int width, Cut cut, bool two) {
   Shape s;
   int vectors = width;
   s.nv = 1;
   if (cut != kValues) {
-    // One warp where up to 2 vectors a thread do: no exchange between warps.  Longer rows: 2
-    // vectors (forward) or 1 for as long as 512 threads do.
+    // One warp where up to 2 vectors a thread do: no exchange between warps.
     vectors = (width + (cut == kShifted ? 14 : 7)) / 8;
     if (vectors <= 64) {
       while (32 * s.nv < vectors) s.nv *= 2;
     } else {
-      s.nv = backward ? 1 : 2;
+      s.nv = two ? 2 : 1;
       while (kMaxThreads * s.nv < vectors && s.nv < 4) s.nv *= 2;
     }
   } else {
@@ -318,8 +322,8 @@ lapl_status lapl_norm_create(const lapl_norm_config* cfg, lapl_norm_handle* out)
   while (p->period > 1 && (long long)p->period / 2 * p->width % 8 == 0) p->period /= 2;
   for (int k = 0; k < norm::kCuts && e == cudaSuccess; ++k) {
     const norm::Cut cut = (norm::Cut)k;
-    const norm::Shape f = norm::shape_of(p->width, cut, false);
-    const norm::Shape b = norm::shape_of(p->width, cut, true);
+    const norm::Shape f = norm::shape_of(p->width, cut, true);
+    const norm::Shape b = norm::shape_of(p->width, cut, r16 && g16);
     e = choose(*p, sms, norm::forward_kernel(cfg->out_dtype, x16, r16, cut, f.nv), f, cut, 0,
                &p->fwd[k]);
     if (e == cudaSuccess)
@@ -421,8 +425,8 @@ lapl_status lapl_norm_backward(lapl_norm_handle p, const void* sum, const float*
     e = cudaGetLastError();
     if (e == cudaSuccess && dweight) {
       cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3((unsigned)((p->width + 31) / 32));
-      cfg.blockDim = dim3(32, 32);
+      cfg.gridDim = dim3((unsigned)((p->width + 7) / 8));
+      cfg.blockDim = dim3(1024);
       cfg.stream = st;
       cudaLaunchAttribute at[1];
       at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

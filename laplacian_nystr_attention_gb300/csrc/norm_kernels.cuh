@@ -151,10 +151,15 @@ __device__ __forceinline__ float row_reduce(float v, int g, float* scratch) {
     v = kMax ? fmaxf(v, other) : v + other;
   }
   if (g > 32) {
-    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) scratch[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = scratch[0];
-    for (int k = 1; k < (g >> 5); ++k) v = kMax ? fmaxf(v, scratch[k]) : v + scratch[k];
+    v = lane < (g >> 5) ? scratch[lane] : 0.f;     // sums and largest magnitudes: 0 changes neither
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const float other = __shfl_xor_sync(0xffffffffu, v, o);
+      v = kMax ? fmaxf(v, other) : v + other;
+    }
   }
   return v;
 }

@@ -46,5 +46,45 @@ __device__ __forceinline__ float bf16_bits(uint16_t b) {
   return __uint_as_float((uint32_t)b << 16);
 }
 
+// One or two floats; two go through the packed fp32 instructions.
+template <int V>
+struct Vec {
+  float f[V];
+};
+template <int V>
+__device__ __forceinline__ Vec<V> fill(float v) {
+  Vec<V> r;
+#pragma unroll
+  for (int i = 0; i < V; ++i) r.f[i] = v;
+  return r;
+}
+__device__ __forceinline__ Vec<1> fma(const Vec<1>& a, const Vec<1>& b, const Vec<1>& c) {
+  return {{fmaf(a.f[0], b.f[0], c.f[0])}};
+}
+__device__ __forceinline__ Vec<1> mul(const Vec<1>& a, const Vec<1>& b) { return {{a.f[0] * b.f[0]}}; }
+__device__ __forceinline__ Vec<1> add(const Vec<1>& a, const Vec<1>& b) { return {{a.f[0] + b.f[0]}}; }
+__device__ __forceinline__ Vec<1> sub(const Vec<1>& a, const Vec<1>& b) { return {{a.f[0] - b.f[0]}}; }
+#define LAPL_PACKED(name, op)                                                              \
+  __device__ __forceinline__ Vec<2> name(const Vec<2>& a, const Vec<2>& b) {                    \
+    Vec<2> d;                                                                                   \
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t" op          \
+        ".f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"                                          \
+        : "=f"(d.f[0]), "=f"(d.f[1])                                                            \
+        : "f"(a.f[0]), "f"(a.f[1]), "f"(b.f[0]), "f"(b.f[1]));                                  \
+    return d;                                                                                   \
+  }
+LAPL_PACKED(mul, "mul.rn")
+LAPL_PACKED(add, "add.rn")
+LAPL_PACKED(sub, "sub.rn")
+#undef LAPL_PACKED
+__device__ __forceinline__ Vec<2> fma(const Vec<2>& a, const Vec<2>& b, const Vec<2>& c) {
+  Vec<2> d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.f[0]), "=f"(d.f[1])
+      : "f"(a.f[0]), "f"(a.f[1]), "f"(b.f[0]), "f"(b.f[1]), "f"(c.f[0]), "f"(c.f[1]));
+  return d;
+}
+
 }  // namespace ops
 }  // namespace lapl
