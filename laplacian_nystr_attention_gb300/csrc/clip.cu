@@ -198,8 +198,7 @@ clip_finish_kernel(const Pairs* part, int parts, float* norm) {
   if (threadIdx.x == 0) *norm = v;
 }
 
-// One piece to its output, times scale where kScale.  Values are read and written for the last
-// time: L2 keeps what the pieces still to come need.
+// One piece to its output, times scale where kScale.
 template <bool kHalf, bool kScale>
 __device__ __forceinline__ void copy_piece(const Piece& p, float scale) {
   constexpr int kBytes = kHalf ? 2 : 4;
@@ -215,7 +214,7 @@ __device__ __forceinline__ void copy_piece(const Piece& p, float scale) {
   uint4* out = reinterpret_cast<uint4*>(p.out + head * kBytes);
   each_vector(reinterpret_cast<const uint4*>(p.in + head * kBytes), vectors,
               [&](int k, const uint4& v) {
-                __stcs(out + k, make_uint4(scaled(v.x), scaled(v.y), scaled(v.z), scaled(v.w)));
+                out[k] = make_uint4(scaled(v.x), scaled(v.y), scaled(v.z), scaled(v.w));
               });
   const int body = vectors * 16 / kBytes;
   for (int k = threadIdx.x; k < p.count - body; k += kThreads) {
