@@ -260,12 +260,13 @@ scan_backward_kernel(const Args a) {
       for (int u = 0; u < kT; ++u)
         if (run.i0 + u >= live) gate[u] = identity_gate<kSig, V>();
     }
-    // The slope of a step in its decay, h_{i-1} - x_i or h_{i-1}, in x's place.
+    // The slope of a step in its decay, x_i - h_{i-1} (with -z: the signs cancel) or h_{i-1}, in x's
+    // place.
 #pragma unroll
     for (int u = 0; u < kT; ++u) {
       const Vec<V> before = h;
       h = step<kSig>(gate[u], x[u], h);
-      x[u] = kSig ? sub(before, x[u]) : before;
+      x[u] = kSig ? sub(x[u], before) : before;
     }
     Vec<V> A = fill<V>(1.f), B = fill<V>(0.f), E;
 #pragma unroll

@@ -143,16 +143,14 @@ __device__ __forceinline__ Vec<V> decayed(const Vec<V>& gate, const Vec<V>& v) {
   if constexpr (kSig) return fma(gate, v, v);
   else return mul(gate, v);
 }
-// The gradients of a step from D, with E = a D and slope = h_{i-1} - x_i or h_{i-1}.
+// The gradients of a step from D, with E = a D and slope = x_i - h_{i-1} (gate is -z) or h_{i-1}.
 template <bool kSig, int V>
 __device__ __forceinline__ void step_gradients(const Vec<V>& gate, const Vec<V>& slope,
                                                const Vec<V>& D, const Vec<V>& E, Vec<V>& dx,
                                                Vec<V>& dg) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    dx.f[i] = kSig ? -gate.f[i] * D.f[i] : D.f[i];
-    dg.f[i] = kSig ? -gate.f[i] * slope.f[i] * E.f[i] : slope.f[i] * D.f[i];
-  }
+  for (int i = 0; i < V; ++i) dx.f[i] = kSig ? -gate.f[i] * D.f[i] : D.f[i];
+  dg = kSig ? mul(mul(gate, slope), E) : mul(slope, D);
 }
 
 }  // namespace scan

@@ -519,12 +519,13 @@ scan_backward_pipe_kernel(const Args a, unsigned* err) {
       }
       put_map(smem + l.runs + (team * kWarps * 32 + wt * 32 + lane) * (2 * V * 4), m);
       bar_arrive(1 + team, kWarps * 32 + 32);
-      // The slope of a step in its decay, h_{i-1} - x_i or h_{i-1}, while the chain goes on.
+      // The slope of a step in its decay, x_i - h_{i-1} (with -z: the signs cancel) or h_{i-1}, while
+      // the chain goes on.
 #pragma unroll
       for (int k = 0; k < kT; ++k) {
         const Vec<V> before = h;
         h = step<kSig>(gate[k], slope[k], h);
-        slope[k] = kSig ? sub(before, slope[k]) : before;
+        slope[k] = kSig ? sub(slope[k], before) : before;
       }
       bar_sync(1 + kTeams + team, kWarps * 32 + 64);
       Vec<V> E;
@@ -532,7 +533,7 @@ scan_backward_pipe_kernel(const Args a, unsigned* err) {
       get_map(smem + l.runs + (team * kWarps * 32 + wt * 32 + lane) * (2 * V * 4), m);
       E = fma(m.a, E, m.b);
       if (on && i0 < a.n) {
-        const bool whole = i0 + kT <= live;
+        const int left = live - i0;
         const long long row = unit.s * a.n + (a.reverse ? unit.len - kT - i0 : i0 + kT - 1);
         char* qx = reinterpret_cast<char*>(a.dx) + (row * a.x_stride + c) * kGrad;
         char* qg = reinterpret_cast<char*>(a.dg) + (row * a.g_stride + c) * kGrad;
@@ -544,15 +545,15 @@ scan_backward_pipe_kernel(const Args a, unsigned* err) {
           E = decayed<kSig>(gate[k], D);
           Vec<V> dx, dg;
           step_gradients<kSig>(gate[k], slope[k], D, E, dx, dg);
-          const int i = i0 + k;
-          if (whole || i < live) {
+          if (k < left) {
             store_vec<kGrad16>(qx, dx);
             store_vec<kGrad16>(qg, dg);
-          } else if (i < a.n) {
-            const long long at = unit.s * a.n + i;
-            store_vec<kGrad16>(reinterpret_cast<char*>(a.dx) + (at * a.x_stride + c) * kGrad, fill<V>(0.f));
-            store_vec<kGrad16>(reinterpret_cast<char*>(a.dg) + (at * a.g_stride + c) * kGrad, fill<V>(0.f));
           }
+        }
+        for (int i = max(i0, live); i < min(i0 + kT, a.n); ++i) {
+          const long long at = unit.s * a.n + i;
+          store_vec<kGrad16>(reinterpret_cast<char*>(a.dx) + (at * a.x_stride + c) * kGrad, fill<V>(0.f));
+          store_vec<kGrad16>(reinterpret_cast<char*>(a.dg) + (at * a.g_stride + c) * kGrad, fill<V>(0.f));
         }
       }
     }
