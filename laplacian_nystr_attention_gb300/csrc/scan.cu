@@ -391,7 +391,7 @@ cudaError_t clusters_held(const pipe::Pick& k, Held* out) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)n);
     cfg.blockDim = dim3((unsigned)(k.teams * k.warps + 2) * 32);
-    cfg.dynamicSmemBytes = k.smem;
+    cfg.dynamicSmemBytes = k.layout.total(n);
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
     at[0].val.clusterDim.x = (unsigned)n;
@@ -415,7 +415,8 @@ pipe::Pick pick_pipe(const lapl_scan_config& c, bool backward, int lanes) {
 // The shape with the least work on the longest path: waves of clusters, as many as the GPU holds at
 // once, times rounds, and three rounds' time to start and end each wave.  Of nearly equal ones
 // (within 5%) the one with the longest pieces of a row.
-cudaError_t choose_pipe(const lapl_scan_config& c, bool backward, const Held& held, Pipe* out) {
+cudaError_t choose_pipe(const lapl_scan_config& c, bool backward, const Held& held,
+                        unsigned smem_most, Pipe* out) {
   const int v = c.in_dtype == LAPL_BF16 ? 2 : 1;
   out->pick.kernel = nullptr;
   double best = 0;
@@ -429,7 +430,7 @@ cudaError_t choose_pipe(const lapl_scan_config& c, bool backward, const Held& he
     const int tile = k.warps * (32 / lanes) * kT;
     for (g.cluster = 1; g.cluster <= pipe::kMaxCluster; ++g.cluster) {
       const int at_once = held.clusters[g.cluster];
-      if (at_once < 1) continue;
+      if (at_once < 1 || k.layout.total(g.cluster) > smem_most) continue;
       const long long round = (long long)g.cluster * tile;
       g.tiles = (int)((c.tokens + round - 1) / round);
       const double cost = (double)((units + at_once - 1) / at_once) * (g.tiles + 3);
@@ -440,8 +441,10 @@ cudaError_t choose_pipe(const lapl_scan_config& c, bool backward, const Held& he
       }
     }
   }
+  if (!out->pick.kernel) return cudaSuccess;
   return cudaFuncSetAttribute(reinterpret_cast<const void*>(out->pick.kernel),
-                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)out->pick.smem);
+                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)out->pick.layout.total(out->geo.cluster));
 }
 
 lapl_status validate(const lapl_scan_config* c) {
@@ -536,7 +539,7 @@ lapl_status launch_pipe(lapl_scan_plan* p, const scan::Pipe& k, scan::Args& a, v
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((long long)p->cfg.sequences * a.geo.blocks * a.geo.cluster));
   cfg.blockDim = dim3((unsigned)a.geo.threads);
-  cfg.dynamicSmemBytes = k.pick.smem;
+  cfg.dynamicSmemBytes = k.pick.layout.total(a.geo.cluster);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -596,11 +599,14 @@ lapl_status lapl_scan_create(const lapl_scan_config* cfg, lapl_scan_handle* out)
   if (e == cudaSuccess && pairs && cfg->tokens >= kPipeTokens && cfg->sequences > 0) {
     scan::Held held = {};
     const scan::pipe::Pick one = scan::pick_pipe(*cfg, false, 32);
-    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(one.kernel),
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)one.smem);
+    int most = 0;
+    e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, p->device);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(reinterpret_cast<const void*>(one.kernel),
+                               cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e == cudaSuccess) e = scan::clusters_held(one, &held);
-    if (e == cudaSuccess) e = scan::choose_pipe(*cfg, false, held, &p->fwd);
-    if (e == cudaSuccess) e = scan::choose_pipe(*cfg, true, held, &p->bwd);
+    if (e == cudaSuccess) e = scan::choose_pipe(*cfg, false, held, (unsigned)most, &p->fwd);
+    if (e == cudaSuccess) e = scan::choose_pipe(*cfg, true, held, (unsigned)most, &p->bwd);
   }
   if (e != cudaSuccess) {
     cudaGetLastError();

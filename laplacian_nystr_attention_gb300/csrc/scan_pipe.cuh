@@ -61,16 +61,20 @@ struct Tile {
   static constexpr int kCopies = 32 / kLanes * kT / kRows;   // of a thread for a stage
 };
 
+// Shared memory after the stages, in bytes: runs' maps, states that enter the teams' tiles, mbarriers,
+// and for each CTA of the cluster the maps that have arrived.
 struct Layout {
-  unsigned runs, enters, slots, total;   // after the stages; in bytes
+  unsigned runs, enters, bars, slots, a_cta;
+  __host__ __device__ constexpr unsigned total(int cluster) const { return slots + a_cta * cluster; }
 };
 template <int V, int kLanes>
-__host__ __device__ constexpr Layout layout_of(int kTeams, int warps, unsigned stage_bytes, int stages) {
+__host__ __device__ constexpr Layout layout_of(int teams, int warps, unsigned stage_bytes, int stages) {
   Layout l = {};
-  l.runs = (unsigned)(kTeams * warps * stages) * stage_bytes;
-  l.enters = l.runs + kTeams * warps * 32 * 2 * V * 4;
-  l.slots = l.enters + kTeams * kLanes * V * 4;
-  l.total = l.slots + slots_of(kTeams) * kMaxCluster * kLanes * 2 * V * 4 + slots_of(kTeams) * 8;
+  l.runs = (unsigned)(teams * warps * stages) * stage_bytes;
+  l.enters = l.runs + teams * warps * 32 * 2 * V * 4;
+  l.bars = l.enters + teams * kLanes * V * 4;
+  l.slots = l.bars + (slots_of(teams) * 8 + 15) / 16 * 16;
+  l.a_cta = slots_of(teams) * kLanes * 2 * V * 4;
   return l;
 }
 
@@ -143,6 +147,22 @@ __device__ __forceinline__ void get_state(unsigned at, Vec<2>& v) {
 }
 __device__ __forceinline__ void get_state(unsigned at, Vec<1>& v) {
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v.f[0]) : "r"(at) : "memory");
+}
+
+// A thread's channels of a token in a stage.
+template <bool k16, int V>
+__device__ __forceinline__ Raw<k16, V> read_raw(unsigned at) {
+  Raw<k16, V> r;
+  if constexpr (k16 && V == 1) {
+    unsigned short t;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(t) : "r"(at) : "memory");
+    r.w[0] = t;
+  } else if constexpr (!k16 && V == 2) {
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.w[0]), "=r"(r.w[V - 1]) : "r"(at) : "memory");
+  } else {
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r.w[0]) : "r"(at) : "memory");
+  }
+  return r;
 }
 
 // Until the phase of the given parity is complete, or false after `bound` ns.
@@ -263,7 +283,7 @@ __device__ __forceinline__ void send_chain(const Args& a, const Unit<kLanes, V>&
       if (set > 0) before = low;
       all = {shuffle(all.a, 32 - kLanes + pos), shuffle(all.b, 32 - kLanes + pos)};
     }
-    const unsigned to = smem + l.slots + ((slot * kMaxCluster + u.rank) * kLanes + pos) * kMap;
+    const unsigned to = smem + l.slots + ((slot * u.cluster + u.rank) * kLanes + pos) * kMap;
     if (!(a.skip_last && r == a.geo.tiles - 1))
       for (int k = set; k < u.cluster; k += kSets)
         send_map(at_rank(to, k), at_rank(bars + slot * 8, k), all);
@@ -296,7 +316,7 @@ __device__ __forceinline__ void receive_chain(const Args& a, const Unit<kLanes, 
       asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
                    ::"r"(bar), "r"(u.cluster * kLanes * kMap) : "memory");
     if (!lost && !wait_phase(bar, (r / slots_of(kTeams)) & 1, a.wait_ns)) lost = true;
-    const unsigned slots = smem + l.slots + (slot * kMaxCluster * kLanes + pos) * kMap;
+    const unsigned slots = smem + l.slots + (slot * u.cluster * kLanes + pos) * kMap;
     Vec<V> enter = carry;
     for (int k = 0; k < u.cluster; ++k) {
       const int rank = kDown ? u.cluster - 1 - k : k;
@@ -332,7 +352,7 @@ scan_forward_pipe_kernel(const Args a, unsigned* err) {
   extern __shared__ __align__(128) unsigned char dynamic[];
   const unsigned smem = smem_u32(dynamic);
   constexpr Layout l = layout_of<V, kLanes>(kTeams, kWarps, kStage, kStages);
-  const unsigned bars = smem + l.total - slots_of(kTeams) * 8;
+  const unsigned bars = smem + l.bars;
   const Unit<kLanes, V> unit(a);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   start_barriers(bars, slots_of(kTeams));
@@ -373,17 +393,8 @@ scan_forward_pipe_kernel(const Args a, unsigned* err) {
       __syncwarp();
       const unsigned from = ring + stage * kStage + my;
       Vec<V> gate[kT];
-      Raw<kIn16, V> rx[kT];
 #pragma unroll
-      for (int k = 0; k < kT; ++k) {
-        Raw<kIn16, V> w;
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w.w[0]) : "r"(from + k * T::kRow) : "memory");
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(rx[k].w[0]) : "r"(from + T::kWarp + k * T::kRow) : "memory");
-        gate[k] = gate_of<kSig>(w);
-      }
-      __syncwarp();
-      ahead(r + kStages * kTeams, stage);
-      if (++stage == kStages) stage = 0;
+      for (int k = 0; k < kT; ++k) gate[k] = gate_of<kSig>(read_raw<kIn16, V>(from + k * T::kRow));
       if (i0 + kT > live) {
 #pragma unroll
         for (int k = 0; k < kT; ++k)
@@ -393,7 +404,7 @@ scan_forward_pipe_kernel(const Args a, unsigned* err) {
 #pragma unroll
       for (int k = 0; k < kT; ++k) {
         m.a = decayed<kSig>(gate[k], m.a);
-        m.b = step<kSig>(gate[k], widen(rx[k]), m.b);
+        m.b = step<kSig>(gate[k], widen(read_raw<kIn16, V>(from + T::kWarp + k * T::kRow)), m.b);
       }
       put_map(smem + l.runs + (team * kWarps * 32 + wt * 32 + lane) * (2 * V * 4), m);
       bar_arrive(1 + team, kWarps * 32 + 32);
@@ -410,14 +421,14 @@ scan_forward_pipe_kernel(const Args a, unsigned* err) {
         if (i0 + kT <= live) {
 #pragma unroll
           for (int k = 0; k < kT; ++k, q += by) {
-            h = step<kSig>(gate[k], widen(rx[k]), h);
+            h = step<kSig>(gate[k], widen(read_raw<kIn16, V>(from + T::kWarp + k * T::kRow)), h);
             store_vec<kOut16>(q, h);
           }
         } else {
 #pragma unroll
           for (int k = 0; k < kT; ++k, q += by) {
             const int i = i0 + k;
-            h = step<kSig>(gate[k], widen(rx[k]), h);
+            h = step<kSig>(gate[k], widen(read_raw<kIn16, V>(from + T::kWarp + k * T::kRow)), h);
             if (i < live)
               store_vec<kOut16>(q, h);
             else if (i < a.n)
@@ -426,6 +437,10 @@ scan_forward_pipe_kernel(const Args a, unsigned* err) {
           }
         }
       }
+      // The stage is read: the team's round after the next one goes into it.
+      __syncwarp();
+      ahead(r + kStages * kTeams, stage);
+      if (++stage == kStages) stage = 0;
     }
     copies_left<0>();
   }
@@ -442,7 +457,7 @@ scan_backward_pipe_kernel(const Args a, unsigned* err) {
   extern __shared__ __align__(128) unsigned char dynamic[];
   const unsigned smem = smem_u32(dynamic);
   constexpr Layout l = layout_of<V, kLanes>(kTeams, kWarps, kStage, kStages);
-  const unsigned bars = smem + l.total - slots_of(kTeams) * 8;
+  const unsigned bars = smem + l.bars;
   const Unit<kLanes, V> unit(a);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   start_barriers(bars, slots_of(kTeams));
@@ -493,27 +508,9 @@ scan_backward_pipe_kernel(const Args a, unsigned* err) {
       __syncwarp();
       const unsigned from = ring + stage * kStage;
       Vec<V> gate[kT], slope[kT], h = next;
-      Raw<kGrad16, V> rd[kT];
 #pragma unroll
-      for (int k = 0; k < kT; ++k) {
-        Raw<kIn16, V> w, x;
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w.w[0]) : "r"(from + my + k * T::kRow) : "memory");
-        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(x.w[0]) : "r"(from + my + T::kWarp + k * T::kRow) : "memory");
-        if constexpr (V * kGrad == 8)
-          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(rd[k].w[0]), "=r"(rd[k].w[V * kGrad == 8 ? 1 : 0])
-                       : "r"(from + my_grad + k * TG::kRow) : "memory");
-        else if constexpr (V * kGrad == 4)
-          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(rd[k].w[0]) : "r"(from + my_grad + k * TG::kRow) : "memory");
-        else
-          asm volatile("{\n\t.reg .u16 t;\n\tld.shared.u16 t, [%1];\n\tcvt.u32.u16 %0, t;\n\t}"
-                       : "=r"(rd[k].w[0]) : "r"(from + my_grad + k * TG::kRow) : "memory");
-        gate[k] = gate_of<kSig>(w);
-        slope[k] = widen(x);
-      }
-      __syncwarp();
-      ahead(r + kStages * kTeams, stage);
+      for (int k = 0; k < kT; ++k) gate[k] = gate_of<kSig>(read_raw<kIn16, V>(from + my + k * T::kRow));
       next = state(r + kTeams);
-      if (++stage == kStages) stage = 0;
       if (i0 + kT > live) {
 #pragma unroll
         for (int k = 0; k < kT; ++k)
@@ -523,7 +520,7 @@ scan_backward_pipe_kernel(const Args a, unsigned* err) {
 #pragma unroll
       for (int k = kT - 1; k >= 0; --k) {
         m.a = decayed<kSig>(gate[k], m.a);
-        m.b = decayed<kSig>(gate[k], add(widen(rd[k]), m.b));
+        m.b = decayed<kSig>(gate[k], add(widen(read_raw<kGrad16, V>(from + my_grad + k * TG::kRow)), m.b));
       }
       put_map(smem + l.runs + (team * kWarps * 32 + wt * 32 + lane) * (2 * V * 4), m);
       bar_arrive(1 + team, kWarps * 32 + 32);
@@ -531,9 +528,9 @@ scan_backward_pipe_kernel(const Args a, unsigned* err) {
       // the chain goes on.
 #pragma unroll
       for (int k = 0; k < kT; ++k) {
-        const Vec<V> before = h;
-        h = step<kSig>(gate[k], slope[k], h);
-        slope[k] = kSig ? sub(slope[k], before) : before;
+        const Vec<V> x = widen(read_raw<kIn16, V>(from + my + T::kWarp + k * T::kRow));
+        slope[k] = kSig ? sub(x, h) : h;
+        h = step<kSig>(gate[k], x, h);
       }
       bar_sync(1 + kTeams + team, kWarps * 32 + 64);
       Vec<V> E;
@@ -549,7 +546,7 @@ scan_backward_pipe_kernel(const Args a, unsigned* err) {
         const long long bg = (a.reverse ? a.g_stride : -a.g_stride) * kGrad;
 #pragma unroll
         for (int k = kT - 1; k >= 0; --k, qx += bx, qg += bg) {
-          const Vec<V> D = add(widen(rd[k]), E);
+          const Vec<V> D = add(widen(read_raw<kGrad16, V>(from + my_grad + k * TG::kRow)), E);
           E = decayed<kSig>(gate[k], D);
           Vec<V> dx, dg;
           step_gradients<kSig>(gate[k], slope[k], D, E, dx, dg);
@@ -564,6 +561,9 @@ scan_backward_pipe_kernel(const Args a, unsigned* err) {
           store_vec<kGrad16>(reinterpret_cast<char*>(a.dg) + (at * a.g_stride + c) * kGrad, fill<V>(0.f));
         }
       }
+      __syncwarp();
+      ahead(r + kStages * kTeams, stage);
+      if (++stage == kStages) stage = 0;
     }
     copies_left<0>();
   }
@@ -576,7 +576,7 @@ using PipeKernel = void (*)(Args, unsigned*);
 struct Pick {
   PipeKernel kernel;
   int teams, warps;
-  size_t smem;
+  Layout layout;
 };
 // For lanes of 32, 16 or 8.
 Pick forward_f32(bool out16, bool sig, int lanes);

@@ -14,7 +14,7 @@ Pick forward() {
   constexpr int kStages = 2;
   return {scan_forward_pipe_kernel<kIn16, kOut16, kSig, kLanes, kStages, kForwardTeams, kForwardWarps>,
           kForwardTeams, kForwardWarps,
-          layout_of<V, kLanes>(kForwardTeams, kForwardWarps, 2 * Tile<kLanes, V * kElem>::kWarp, kStages).total};
+          layout_of<V, kLanes>(kForwardTeams, kForwardWarps, 2 * Tile<kLanes, V * kElem>::kWarp, kStages)};
 }
 template <bool kGrad16, bool kSig, int kLanes>
 Pick backward() {
@@ -22,7 +22,7 @@ Pick backward() {
   return {scan_backward_pipe_kernel<kIn16, kGrad16, kSig, kLanes, kStages, kBackwardTeams, kBackwardWarps>,
           kBackwardTeams, kBackwardWarps,
           layout_of<V, kLanes>(kBackwardTeams, kBackwardWarps, 2 * Tile<kLanes, V * kElem>::kWarp +
-                                  Tile<kLanes, V * (kGrad16 ? 2 : 4)>::kWarp, kStages).total};
+                                  Tile<kLanes, V * (kGrad16 ? 2 : 4)>::kWarp, kStages)};
 }
 template <bool kOther16, bool kSig, bool kBackward>
 Pick pick(int lanes) {
