@@ -26,11 +26,12 @@ norm_backward_kernel(const Args a) {
   Columns<VEC, NV, kShift> cols;
   cols.init(a, t, rows.shift);
   const long long end = (long long)a.rows * a.width;
-  float dw[NV][VEC];
+  using X = Values<VEC>;
+  X dw[NV];
 #pragma unroll
   for (int j = 0; j < NV; ++j)
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) dw[j][i] = 0.f;
+    for (int i = 0; i < X::kN; ++i) dw[j].v[i] = ops::fill<X::kW>(0.f);
   Raw<kRes16, VEC> rs[NV];
   Raw<kGrad16, VEC> ry[NV], rd[NV];
   float next_rstd = 0.f;
@@ -55,7 +56,7 @@ norm_backward_kernel(const Args a) {
     const unsigned row = rows.row;
     if constexpr (!kAhead) fetch(row);
     const bool live = row < a.rows;
-    const long long at = (long long)row * a.width;
+    const long long row0 = (long long)row * a.width;
     const float rstd = next_rstd;
     Raw<kRes16, VEC> cs[NV];
     Raw<kGrad16, VEC> cy[NV], cd[NV];
@@ -68,26 +69,29 @@ norm_backward_kernel(const Args a) {
       cols.template trim<kGrad16>(cy[j], j);
     }
     if constexpr (kAhead) fetch(row + rows.stride);
-    float dot = 0.f;
+    ops::Vec<X::kW> dots = ops::fill<X::kW>(0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const float dyn = get(cy[j], i) * (get(cs[j], i) * rstd);
-        dw[j][i] += dyn;
-        dot = fmaf(dyn, cols.weight(a, j, i), dot);
+      for (int i = 0; i < X::kN; ++i) {
+        const auto dyn = ops::mul(get(cy[j], i), ops::mul(get(cs[j], i), ops::fill<X::kW>(rstd)));
+        dw[j].v[i] = ops::add(dw[j].v[i], dyn);
+        dots = ops::fma(dyn, cols.weight(a, j, i), dots);
       }
+    float dot = dots.f[0];
+    if constexpr (X::kW == 2) dot += dots.f[X::kW - 1];
     dot = row_reduce<false>(dot, a.g, scratch[parity]);
     const float back = -rstd * rstd * dot * a.inv_width;   // of s
     const long long hr = a.dx ? head_row(a, row) : 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if (!(live && cols.in(j))) continue;
-      float d[VEC];
+      X d;
 #pragma unroll
-      for (int i = 0; i < VEC; ++i)
-        d[i] = fmaf(rstd, get(cy[j], i) * cols.weight(a, j, i), fmaf(back, get(cs[j], i), get(cd[j], i)));
-      if (a.dres) cols.template put<kGrad16>(a.dres, j, at + cols.col(j), d);
+      for (int i = 0; i < X::kN; ++i)
+        d.v[i] = ops::fma(ops::fill<X::kW>(rstd), ops::mul(get(cy[j], i), cols.weight(a, j, i)),
+                          ops::fma(ops::fill<X::kW>(back), get(cs[j], i), get(cd[j], i)));
+      if (a.dres) cols.template put<kGrad16>(a.dres, j, row0 + cols.col(j), d);
       if (a.dx) cols.template put<kGrad16>(a.dx, j, hr + cols.head(a, j), d);
     }
   }
@@ -99,7 +103,7 @@ norm_backward_kernel(const Args a) {
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int i = 0; i < VEC; ++i)
-        if (cols.valid(j, i)) sums[(size_t)mine * a.width + cols.col(j) + i] = dw[j][i];
+        if (cols.valid(j, i)) sums[(size_t)mine * a.width + cols.col(j) + i] = at(dw[j], i);
     __syncthreads();
     for (int c = threadIdx.x; c < a.width; c += blockDim.x) {
       float v = 0.f;
@@ -111,7 +115,7 @@ norm_backward_kernel(const Args a) {
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int i = 0; i < VEC; ++i)
-        if (cols.valid(j, i)) part[cols.col(j) + i] = dw[j][i];
+        if (cols.valid(j, i)) part[cols.col(j) + i] = at(dw[j], i);
   }
 }
 

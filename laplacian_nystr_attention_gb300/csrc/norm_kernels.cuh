@@ -123,26 +123,45 @@ __device__ __forceinline__ void load_one(Raw<k16, VEC>& r, const void* base, lon
   if constexpr (!k16) r.w[i] = reinterpret_cast<const uint32_t*>(base)[e + i];
   else r.w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(base)[e + i] << (16 * (i & 1));
 }
+// Values are worked on two at a time (packed fp32 instructions), or one where vectors have one.
+template <int VEC>
+struct Values {
+  static constexpr int kW = VEC == 8 ? 2 : 1, kN = VEC / kW;
+  ops::Vec<kW> v[kN];
+};
 template <bool k16, int VEC>
-__device__ __forceinline__ float get(const Raw<k16, VEC>& r, int i) {
-  if constexpr (!k16) return __uint_as_float(r.w[i]);
-  else return (i & 1) ? bf16_hi(r.w[i / 2]) : bf16_lo(r.w[i / 2]);
+__device__ __forceinline__ ops::Vec<Values<VEC>::kW> get(const Raw<k16, VEC>& r, int i) {
+  ops::Vec<Values<VEC>::kW> v;
+  if constexpr (VEC == 1) {
+    v.f[0] = k16 ? bf16_lo(r.w[0]) : __uint_as_float(r.w[0]);
+  } else if constexpr (k16) {
+    v.f[0] = bf16_lo(r.w[i]);
+    v.f[Values<VEC>::kW - 1] = bf16_hi(r.w[i]);
+  } else {
+    v.f[0] = __uint_as_float(r.w[2 * i]);
+    v.f[Values<VEC>::kW - 1] = __uint_as_float(r.w[2 * i + 1]);
+  }
+  return v;
+}
+template <int VEC>
+__device__ __forceinline__ float at(const Values<VEC>& x, int i) {
+  return x.v[i / Values<VEC>::kW].f[i % Values<VEC>::kW];
 }
 template <bool k16, int VEC>
-__device__ __forceinline__ void store(void* base, long long e, const float (&f)[VEC]) {
+__device__ __forceinline__ void store(void* base, long long e, const Values<VEC>& x) {
   if constexpr (VEC == 8) {
     uint4* p = reinterpret_cast<uint4*>(reinterpret_cast<char*>(base) + e * (k16 ? 2 : 4));
     if constexpr (k16) {
-      *p = make_uint4(ops::pack_bf16(f[0], f[1]), ops::pack_bf16(f[2], f[3]),
-                      ops::pack_bf16(f[4], f[5]), ops::pack_bf16(f[6], f[7]));
+      *p = make_uint4(ops::pack_bf16(at(x, 0), at(x, 1)), ops::pack_bf16(at(x, 2), at(x, 3)),
+                      ops::pack_bf16(at(x, 4), at(x, 5)), ops::pack_bf16(at(x, 6), at(x, 7)));
     } else {
-      reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-      reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+      reinterpret_cast<float4*>(p)[0] = make_float4(at(x, 0), at(x, 1), at(x, 2), at(x, 3));
+      reinterpret_cast<float4*>(p)[1] = make_float4(at(x, 4), at(x, 5), at(x, 6), at(x, 7));
     }
   } else if constexpr (k16) {
-    reinterpret_cast<uint16_t*>(base)[e] = (uint16_t)ops::pack_bf16(f[0], 0.f);
+    reinterpret_cast<uint16_t*>(base)[e] = (uint16_t)ops::pack_bf16(at(x, 0), 0.f);
   } else {
-    reinterpret_cast<float*>(base)[e] = f[0];
+    reinterpret_cast<float*>(base)[e] = at(x, 0);
   }
 }
 
@@ -191,18 +210,18 @@ template <int VEC, int NV, bool kShift>
 struct Columns {
   static constexpr bool kHeads = VEC == 8 && !kShift, kWeights = NV * VEC <= 16;
   int first, step, width;
-  long long at[kHeads ? NV : 1];                 // in [B,H,N,d]
-  float w[kWeights ? NV : 1][kWeights ? VEC : 1];
+  long long place[kHeads ? NV : 1];              // in [B,H,N,d]
+  Values<VEC> w[kWeights ? NV : 1];
   __device__ __forceinline__ void init(const Args& a, int t, int shift) {
     first = t * VEC - (kShift ? shift : 0);
     step = a.g * VEC;
     width = a.width;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if constexpr (kHeads) at[j] = in(j) ? head_col(a, col(j)) : 0;
+      if constexpr (kHeads) place[j] = in(j) ? head_col(a, col(j)) : 0;
       if constexpr (kWeights)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) w[j][i] = load_weight(a, j, i);
+        for (int i = 0; i < Values<VEC>::kN; ++i) w[j].v[i] = load_weight(a, j, i);
     }
   }
   __device__ __forceinline__ int col(int j) const { return first + j * step; }
@@ -213,15 +232,20 @@ struct Columns {
   __device__ __forceinline__ bool whole(int j) const {
     return !kShift || (col(j) >= 0 && col(j) + VEC <= width);
   }
-  __device__ __forceinline__ float load_weight(const Args& a, int j, int i) const {
-    return a.weight && valid(j, i) ? __ldg(a.weight + col(j) + i) : 1.f;
+  __device__ __forceinline__ ops::Vec<Values<VEC>::kW> load_weight(const Args& a, int j, int i) const {
+    constexpr int kW = Values<VEC>::kW;
+    ops::Vec<kW> r;
+#pragma unroll
+    for (int k = 0; k < kW; ++k)
+      r.f[k] = a.weight && valid(j, i * kW + k) ? __ldg(a.weight + col(j) + i * kW + k) : 1.f;
+    return r;
   }
   __device__ __forceinline__ long long head(const Args& a, int j) const {
-    if constexpr (kHeads) return at[j];
+    if constexpr (kHeads) return place[j];
     else return head_col(a, col(j));
   }
-  __device__ __forceinline__ float weight(const Args& a, int j, int i) const {
-    if constexpr (kWeights) return w[j][i];
+  __device__ __forceinline__ ops::Vec<Values<VEC>::kW> weight(const Args& a, int j, int i) const {
+    if constexpr (kWeights) return w[j].v[i];
     else return load_weight(a, j, i);
   }
   // Vector j at element e of a tensor that ends at `end`, with its neighbours' values where it is
@@ -246,16 +270,13 @@ struct Columns {
     }
   }
   template <bool k16>
-  __device__ __forceinline__ void put(void* base, int j, long long e, const float (&f)[VEC]) const {
+  __device__ __forceinline__ void put(void* base, int j, long long e, const Values<VEC>& x) const {
     if (whole(j)) {
-      store<k16, VEC>(base, e, f);
+      store<k16, VEC>(base, e, x);
     } else {
 #pragma unroll
       for (int i = 0; i < VEC; ++i)
-        if (valid(j, i)) {
-          const float one[1] = {f[i]};
-          store<k16, 1>(base, e + i, one);
-        }
+        if (valid(j, i)) store<k16, 1>(base, e + i, Values<1>{{{at(x, i)}}});
     }
   }
 };
@@ -317,24 +338,27 @@ norm_forward_kernel(const Args a) {
     const unsigned row = rows.row;
     if constexpr (!kAhead) fetch(row);
     const bool live = row < a.rows;
-    const long long at = (long long)row * a.width;
-    float s[NV][VEC];
-    float sq = 0.f;
+    const long long row0 = (long long)row * a.width;
+    using X = Values<VEC>;
+    X s[NV];
+    ops::Vec<X::kW> sums = ops::fill<X::kW>(0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       cols.template trim<kX16>(rx[j], j);
       cols.template trim<kRes16>(rr[j], j);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        s[j][i] = get(rx[j], i) + get(rr[j], i);
-        sq = fmaf(s[j][i], s[j][i], sq);
+      for (int i = 0; i < X::kN; ++i) {
+        s[j].v[i] = ops::add(get(rx[j], i), get(rr[j], i));
+        sums = ops::fma(s[j].v[i], s[j].v[i], sums);
       }
     }
+    float sq = sums.f[0];
+    if constexpr (X::kW == 2) sq += sums.f[X::kW - 1];
     if constexpr (kAhead) fetch(row + rows.stride);
     if (a.sum) {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
-        if (live && cols.in(j)) cols.template put<kRes16>(a.sum, j, at + cols.col(j), s[j]);
+        if (live && cols.in(j)) cols.template put<kRes16>(a.sum, j, row0 + cols.col(j), s[j]);
     }
     sq = row_reduce<false>(sq, a.g, scratch[parity][0]);
     const float rstd = rsqrtf(fmaf(sq, a.inv_width, a.eps));
@@ -342,12 +366,13 @@ norm_forward_kernel(const Args a) {
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) s[j][i] *= rstd * cols.weight(a, j, i);
+      for (int i = 0; i < X::kN; ++i)
+        s[j].v[i] = ops::mul(s[j].v[i], ops::mul(cols.weight(a, j, i), ops::fill<X::kW>(rstd)));
     if constexpr (kOut != kF8) {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
         if (live && cols.in(j))
-          cols.template put<kOut == kBf16>(a.y, j, at + cols.col(j), s[j]);
+          cols.template put<kOut == kBf16>(a.y, j, row0 + cols.col(j), s[j]);
     } else {
       float top[NV];
 #pragma unroll
@@ -355,7 +380,7 @@ norm_forward_kernel(const Args a) {
         top[j] = 0.f;
         if (cols.in(j))
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) top[j] = fmaxf(top[j], fabsf(s[j][i]));
+          for (int i = 0; i < VEC; ++i) top[j] = fmaxf(top[j], fabsf(at(s[j], i)));
       }
       if (a.group_log2 < 0) {
         float m = 0.f;
@@ -398,13 +423,14 @@ norm_forward_kernel(const Args a) {
         if (a.group_log2 < 0) {
           if (t == 0 && j == 0) a.scales[row] = m * (1.f / kE4m3Max);
         } else if ((col & ((1 << a.group_log2) - 1)) == 0) {
-          a.scales[(at + col) >> a.group_log2] = m * (1.f / kE4m3Max);
+          a.scales[(row0 + col) >> a.group_log2] = m * (1.f / kE4m3Max);
         }
-        unsigned char* p = reinterpret_cast<unsigned char*>(a.y) + at + col;
+        unsigned char* p = reinterpret_cast<unsigned char*>(a.y) + row0 + col;
         if constexpr (VEC == 8) {
-          const uint2 q =
-              make_uint2(pack_e4m3(s[j][0] * inv, s[j][1] * inv, s[j][2] * inv, s[j][3] * inv),
-                         pack_e4m3(s[j][4] * inv, s[j][5] * inv, s[j][6] * inv, s[j][7] * inv));
+#pragma unroll
+          for (int i = 0; i < X::kN; ++i) s[j].v[i] = ops::mul(s[j].v[i], ops::fill<X::kW>(inv));
+          const uint2 q = make_uint2(pack_e4m3(at(s[j], 0), at(s[j], 1), at(s[j], 2), at(s[j], 3)),
+                                     pack_e4m3(at(s[j], 4), at(s[j], 5), at(s[j], 6), at(s[j], 7)));
           if (cols.whole(j)) {
             *reinterpret_cast<uint2*>(p) = q;
           } else {
@@ -413,7 +439,7 @@ norm_forward_kernel(const Args a) {
               if (cols.valid(j, i)) p[i] = (unsigned char)((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
           }
         } else {
-          *p = (unsigned char)pack_e4m3(s[j][0] * inv, 0.f, 0.f, 0.f);
+          *p = (unsigned char)pack_e4m3(at(s[j], 0) * inv, 0.f, 0.f, 0.f);
         }
       }
     }
