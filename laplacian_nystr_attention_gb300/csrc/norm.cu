@@ -12,12 +12,24 @@
 namespace lapl {
 namespace norm {
 
+// Rows of bf16 that start at any value (kShifted) reach a thread through shared memory, up to
+// kStages rows ahead: 35 us instead of 40 with the next row in registers, at 8193 rows of 2049
+// values, 60 instead of 67 at 32768 of 1001.  Rows of whole vectors gain nothing by it (57 and 55 us
+// at 32768 of 1000), and of fp32 they lose, a vector's two copies taking half of a sector each (28
+// us and 23 at 8192 of 512).
+constexpr int kStages = 4;
+constexpr bool in_stages(bool res16, bool grad16, bool shift, int nv) {
+  return shift && res16 && grad16 && nv <= 2;
+}
+
 template <bool kRes16, bool kGrad16, int VEC, int NV, bool kShift>
 __global__ void __launch_bounds__(kMaxThreads)
 norm_backward_kernel(const Args a) {
   __shared__ float scratch[2][kMaxThreads / 32];
-  extern __shared__ float sums[];   // [rows side by side, W]
-  constexpr bool kAhead = NV * ((kRes16 ? 4 : 8) + 2 * (kGrad16 ? 4 : 8)) * VEC / 8 <= 24;
+  extern __shared__ __align__(16) float dynamic[];
+  constexpr bool kInStages = VEC == 8 && in_stages(kRes16, kGrad16, kShift, NV);
+  constexpr bool kAhead =
+      !kInStages && NV * ((kRes16 ? 4 : 8) + 2 * (kGrad16 ? 4 : 8)) * VEC / 8 <= 24;
   // The kernel that sums the partials may be placed now; it waits for this grid's end.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int t = place_in_row(a);
@@ -34,10 +46,8 @@ norm_backward_kernel(const Args a) {
     for (int i = 0; i < X::kN; ++i) dw[j].v[i] = ops::fill<X::kW>(0.f);
   Raw<kRes16, VEC> rs[NV];
   Raw<kGrad16, VEC> ry[NV], rd[NV];
-  float next_rstd = 0.f;
   auto fetch = [&](unsigned r) {
     const long long at = (long long)r * a.width;
-    next_rstd = r < a.rows ? a.rstd[r] : 0.f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       zero(rs[j]);
@@ -50,14 +60,53 @@ norm_backward_kernel(const Args a) {
       }
     }
   };
-  if constexpr (kAhead) fetch(rows.row);
+  // A stage: 3 vectors of 16 bytes for each of a thread's, beside its neighbours'.  A thread reads
+  // what it copied itself, so that nothing else waits.
+  const unsigned apart = blockDim.x * 16, stage_bytes = NV * 3 * apart;
+  const unsigned stages = ops::smem_u32(dynamic) + threadIdx.x * 16;
+  auto copy = [&](unsigned r, unsigned stage) {
+    const long long at = (long long)r * a.width;
+    unsigned to = stages + stage * stage_bytes;
+#pragma unroll
+    for (int j = 0; j < NV; ++j, to += 3 * apart) {
+      const bool on = r < a.rows && cols.in(j);
+      cols.copy(to, a.res, on, at + cols.col(j), end);
+      cols.copy(to + apart, a.dy, on, at + cols.col(j), end);
+      if (a.dsum) cols.copy(to + 2 * apart, a.dsum, on, at + cols.col(j), end);
+    }
+    ops::close_copies();
+  };
+  auto rstd_of = [&](unsigned r) { return r < a.rows ? a.rstd[r] : 0.f; };
+  float next_rstd = rstd_of(rows.row);
+  unsigned stage = 0;
+  if constexpr (kInStages) {
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) copy(rows.row + k * rows.stride, k);
+  } else if constexpr (kAhead) {
+    fetch(rows.row);
+  }
   int parity = 0;
   for (; rows.first < a.rows; rows.first += rows.stride, rows.row += rows.stride, parity ^= 1) {
     const unsigned row = rows.row;
-    if constexpr (!kAhead) fetch(row);
     const bool live = row < a.rows;
     const long long row0 = (long long)row * a.width;
     const float rstd = next_rstd;
+    next_rstd = rstd_of(row + rows.stride);
+    if constexpr (kInStages) {
+      copy(row + (kStages - 1) * rows.stride, (stage + kStages - 1) % kStages);
+      ops::copies_left<kStages - 1>();
+      unsigned from = stages + stage * stage_bytes;
+      stage = (stage + 1) % kStages;
+#pragma unroll
+      for (int j = 0; j < NV; ++j, from += 3 * apart) {
+        read_copy(rs[j], from);
+        read_copy(ry[j], from + apart);
+        if (a.dsum) read_copy(rd[j], from + 2 * apart);
+        else zero(rd[j]);
+      }
+    } else if constexpr (!kAhead) {
+      fetch(row);
+    }
     Raw<kRes16, VEC> cs[NV];
     Raw<kGrad16, VEC> cy[NV], cd[NV];
 #pragma unroll
@@ -95,10 +144,13 @@ norm_backward_kernel(const Args a) {
       if (a.dx) cols.template put<kGrad16>(a.dx, j, hr + cols.head(a, j), d);
     }
   }
+  if constexpr (kInStages) ops::copies_left<0>();
   if (!a.part) return;
   // The CTA's part: its rows side by side, one after the other.
   float* part = a.part + (size_t)blockIdx.x * a.width;
   if (per > 1) {
+    float* sums = dynamic;   // [rows side by side, W], where the stages were
+    __syncthreads();
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
@@ -211,6 +263,14 @@ Kernel backward_kernel(bool r16, bool g16, Cut cut, int nv) {
              : (g16 ? backward_kernel<false, true>(cut, nv) : backward_kernel<false, false>(cut, nv));
 }
 
+// Dynamic shared memory of the backward: the stages of rows to come, then the side-by-side sums.
+size_t backward_smem(const lapl_norm_config& c, const Shape& s, Cut cut) {
+  const bool stages = in_stages(c.res_dtype == LAPL_BF16, c.grad_dtype == LAPL_BF16,
+                                cut == kShifted, s.nv);
+  const size_t sums = s.per > 1 ? (size_t)s.per * c.heads * c.head_dim * sizeof(float) : 0;
+  return std::max(stages ? (size_t)kStages * s.nv * 3 * 16 * s.threads : 0, sums);
+}
+
 // A kernel of a plan, with its launch shape.
 struct Choice {
   Kernel kernel;
@@ -260,8 +320,15 @@ namespace {
 cudaError_t choose(const lapl_norm_plan& p, int sms, norm::Kernel kernel, const norm::Shape& s,
                    norm::Cut cut, size_t smem, norm::Choice* out) {
   int per_sm = 0;
-  const cudaError_t e =
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, s.threads, smem);
+  cudaError_t e = cudaSuccess;
+  // The same for every plan: it is the kernel's, not the launch's.
+  constexpr size_t kMost = norm::kStages * 2 * 3 * 16 * norm::kMaxThreads;
+  if (smem > kMost) return cudaErrorInvalidValue;
+  if (smem > 0)
+    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMost);
+  if (e != cudaSuccess) return e;
+  e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, s.threads, smem);
   if (e != cudaSuccess) return e;
   out->kernel = kernel;
   out->shape = s;
@@ -336,7 +403,7 @@ lapl_status lapl_norm_create(const lapl_norm_config* cfg, lapl_norm_handle* out)
                &p->fwd[k]);
     if (e == cudaSuccess)
       e = choose(*p, sms, norm::backward_kernel(r16, g16, cut, b.nv), b, cut,
-                 b.per > 1 ? (size_t)b.per * p->width * sizeof(float) : 0, &p->bwd[k]);
+                 norm::backward_smem(*cfg, b, cut), &p->bwd[k]);
   }
   if (e != cudaSuccess) {
     delete p;

@@ -123,6 +123,12 @@ __device__ __forceinline__ void load_one(Raw<k16, VEC>& r, const void* base, lon
   if constexpr (!k16) r.w[i] = reinterpret_cast<const uint32_t*>(base)[e + i];
   else r.w[i / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(base)[e + i] << (16 * (i & 1));
 }
+// A vector of bf16 from shared memory.
+__device__ __forceinline__ void read_copy(Raw<true, 8>& r, unsigned at) {
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r.w[0]), "=r"(r.w[1]), "=r"(r.w[2]), "=r"(r.w[3]) : "r"(at) : "memory");
+}
+
 // Values are worked on two at a time (packed fp32 instructions), or one where vectors have one.
 template <int VEC>
 struct Values {
@@ -260,6 +266,12 @@ struct Columns {
       for (int i = 0; i < VEC; ++i)
         if (valid(j, i)) load_one(r, base, e, i);
     }
+  }
+  // The same of bf16 into shared memory; zeros where `on` is not set, and behind `end`.
+  __device__ __forceinline__ void copy(unsigned to, const void* base, bool on, long long e,
+                                       long long end) const {
+    ops::copy16(to, reinterpret_cast<const char*>(base) + e * 2,
+                on ? (int)max(0LL, min(8LL, end - e)) * 2 : 0);
   }
   template <bool k16>
   __device__ __forceinline__ void trim(Raw<k16, VEC>& r, int j) const {

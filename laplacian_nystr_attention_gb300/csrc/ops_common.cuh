@@ -86,5 +86,20 @@ __device__ __forceinline__ Vec<2> fma(const Vec<2>& a, const Vec<2>& b, const Ve
   return d;
 }
 
+__device__ __forceinline__ unsigned smem_u32(const void* p) {
+  return static_cast<unsigned>(__cvta_generic_to_shared(p));
+}
+// `bytes` of the 16 at src (both multiples of 16 bytes; none are read of 0), zeros for the rest.
+__device__ __forceinline__ void copy16(unsigned dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void close_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until all but the last kPending groups of this thread's copies are there.
+template <int kPending>
+__device__ __forceinline__ void copies_left() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
+}
+
 }  // namespace ops
 }  // namespace lapl

@@ -78,27 +78,18 @@ __host__ __device__ constexpr Layout layout_of(int teams, int warps, unsigned st
   return l;
 }
 
-__device__ __forceinline__ unsigned smem_u32(const void* p) {
-  return static_cast<unsigned>(__cvta_generic_to_shared(p));
-}
+using ops::smem_u32, ops::copy16, ops::copies_left;
+
 __device__ __forceinline__ unsigned at_rank(unsigned addr, int rank) {
   unsigned r;
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-// `bytes` of the 16 at src (0 or 16), zeros for the rest.
-__device__ __forceinline__ void copy16(unsigned dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
-}
+// The same for a thread's own 4 or 8.
 template <int kBytes>
 __device__ __forceinline__ void copy_own(unsigned dst, const void* src, int bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(bytes),
                "n"(kBytes) : "memory");
-}
-template <int kPending>
-__device__ __forceinline__ void copies_left() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(kPending) : "memory");
 }
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -381,7 +372,7 @@ scan_forward_pipe_kernel(const Args a, unsigned* err) {
         copy_stage<kLanes, V * kElem, kElem>(ring + stage * kStage + T::kWarp, a.x, a.x_stride, a,
                                              unit.s, unit.c0, unit.len, first, a.fine);
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
+      ops::close_copies();
     };
 #pragma unroll
     for (int k = 0; k < kStages; ++k) ahead(team + k * kTeams, k);
@@ -490,7 +481,7 @@ scan_backward_pipe_kernel(const Args a, unsigned* err) {
         copy_stage<kLanes, V * kGrad, kGrad>(to + 2 * T::kWarp, a.dout, a.c, a, unit.s, unit.c0,
                                              unit.len, first, a.fine_dout);
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
+      ops::close_copies();
     };
     auto state = [&](int r) {
       const long long i = place(r, run);
