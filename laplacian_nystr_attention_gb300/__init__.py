@@ -180,6 +180,8 @@ class LaplacianNystromAttention:
             self.bwd_workspace_bytes = lapl_attn_backward_workspace_size(self.handle)
             self.bwd_workspace = torch.empty(max(self.bwd_workspace_bytes, 256),
                                              dtype=torch.uint8, device=q.device)
+        if max_norm is not None and not 0 <= max_norm < float("inf"):
+            raise ValueError(f"max_norm must be finite and not negative, got {max_norm}")
         st = stream if stream is not None else torch.cuda.current_stream()
         lapl_attn_backward(self.handle, q.data_ptr(), k.data_ptr(), v.data_ptr(),
                            bias.data_ptr() if bias is not None else None, dout.data_ptr(),
@@ -189,8 +191,12 @@ class LaplacianNystromAttention:
                            self.bwd_workspace_bytes, st.cuda_stream)
         if max_norm is not None:
             all_four = [g["dq"], g["dk"], g["dv"], g["dbias"]]
+            if c.batch == 0:   # an empty batch writes no gradient, and the bias's is zero
+                with torch.cuda.stream(st):
+                    g["dbias"].zero_()
             if getattr(self, "_clip", None) is None:
-                self._clip = GradClip([t.numel() for t in all_four], ["f32"] * 4)
+                with torch.cuda.device(q.device):
+                    self._clip = GradClip([t.numel() for t in all_four], ["f32"] * 4)
             self.grad_norm = self._clip.clip(all_four, max_norm, stream=stream)
         return g["dq"], g["dk"], g["dv"], g["dbias"]
 

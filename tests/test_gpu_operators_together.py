@@ -106,6 +106,21 @@ def test_attention_backward_clips():
     att.close()
 
 
+def test_attention_backward_clips_an_empty_batch():
+    """No gradient reaches the bias, whatever its tensor held."""
+    import laplacian_nystr_attention_gb300 as lna
+    w = WORKLOADS["tiny_f32"].replace(heads=2, batch=0)
+    att = lna.LaplacianNystromAttention(lna.make_config(**w.config()))
+    empty = torch.empty(0, 2, w.grid_h * w.grid_w, w.head_dim, device="cuda")
+    dbias = torch.full((2, att.cfg.num_landmarks), 7.0, device="cuda")
+    att.forward(empty, empty, empty, keep_for_backward=True)
+    got = att.backward(empty, empty, empty, empty, grads={"dbias": dbias}, max_norm=0.5)
+    assert att.grad_norm.item() == 0 and torch.equal(got[3], torch.zeros_like(dbias))
+    with pytest.raises(ValueError):
+        att.backward(empty, empty, empty, empty, grads={"dbias": dbias}, max_norm=-1.0)
+    att.close()
+
+
 def test_training_step_captured():
     """norm -> recurrence -> back -> clip in one graph, replayed."""
     import laplacian_nystr_attention_gb300 as lna
