@@ -435,9 +435,9 @@ cudaError_t choose_pipe(const lapl_scan_config& c, bool backward, const Held& he
     }
   }
   if (!out->pick.kernel) return cudaSuccess;
+  // The most there is, whatever this plan's clusters take: it is the kernel's, and other plans' too.
   return cudaFuncSetAttribute(reinterpret_cast<const void*>(out->pick.kernel),
-                              cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)out->pick.layout.total(out->geo.cluster));
+                              cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_most);
 }
 
 lapl_status validate(const lapl_scan_config* c) {

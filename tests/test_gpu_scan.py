@@ -376,6 +376,23 @@ def test_long_bit_for_bit_on_two_streams():
             assert all(torch.equal(t, u) for t, u in zip(a, b))
 
 
+def test_long_plans_side_by_side():
+    """A plan whose clusters need less shared memory, made after one that needs more."""
+    import laplacian_nystr_attention_gb300 as lna
+    made = []
+    for S, N in ((1, 20000), (600, 800)):
+        x, g, *_ = make(S, N, 64, "sigmoid", "bf16", seed=3)
+        plan = lna.GatedScan(lna.make_scan_config(S, N, 64, in_dtype="bf16", grad_dtype="bf16"))
+        made.append((plan, dev(x, "bf16"), dev(g, "bf16"), ref.scan(x, g, "sigmoid")))
+    infos = [_info(m[0]) for m in made]
+    assert infos[0]["cluster"] > infos[1]["cluster"] and infos[1]["teams"]
+    for plan, x, g, want in made:
+        states = torch.empty(plan.states_shape, device="cuda")
+        ref.check("h", plan.forward(x, g, states=states), want["h"])
+        plan.backward(x, g, states, x)
+    torch.cuda.synchronize()
+
+
 @pytest.mark.parametrize("S,N,C", [(1, 20000, 64), (40, 1500, 64)])
 def test_wait_that_gives_up_is_reported(S, N, C):
     """The last round's maps are never sent: the waits for them run out after 2 ms, the kernel ends,
