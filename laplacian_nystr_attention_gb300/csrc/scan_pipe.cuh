@@ -288,17 +288,25 @@ __device__ __forceinline__ void send_chain(const Args& a, const Unit<kLanes, V>&
   }
 }
 
+// The receiving warp's state before the first round.  Read before the cluster meets for the first
+// time: its first CTA may write the last state over it, once all have sent their maps.
+template <int kLanes, int V>
+__device__ __forceinline__ Vec<V> first_state(const Args& a, const Unit<kLanes, V>& u, bool receives,
+                                              const float* start) {
+  const int c = u.c0 + ((int)threadIdx.x & (kLanes - 1)) * V;
+  return receives && start && c < a.c ? widen(load_raw<false, V>(start + u.s * a.c + c))
+                                      : fill<V>(0.f);
+}
+
 // The receiving warp: the state that enters every round's tile, from the tiles of the cluster.
 template <int kLanes, int V, int kTeams, int kWarps, bool kDown>
 __device__ __forceinline__ void receive_chain(const Args& a, const Unit<kLanes, V>& u, unsigned smem,
-                                              const Layout& l, unsigned bars, const float* start,
+                                              const Layout& l, unsigned bars, Vec<V> carry,
                                               float* finish, unsigned* err) {
   constexpr int kMap = 2 * V * 4;
   const int lane = threadIdx.x & 31, pos = lane & (kLanes - 1);
   const int c = u.c0 + pos * V;
   const bool on = lane < kLanes && c < a.c;
-  Vec<V> carry = fill<V>(0.f);
-  if (start && c < a.c) carry = widen(load_raw<false, V>(start + u.s * a.c + c));
   bool lost = false;
   for (int r = 0; r < a.geo.tiles; ++r) {
     const int team = r % kTeams, slot = r % slots_of(kTeams);
@@ -346,12 +354,13 @@ scan_forward_pipe_kernel(const Args a, unsigned* err) {
   const unsigned bars = smem + l.bars;
   const Unit<kLanes, V> unit(a);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Vec<V> start = first_state(a, unit, warp == kTeams * kWarps + 1, a.h0);
   start_barriers(bars, slots_of(kTeams));
   cluster_sync();
   if (warp == kTeams * kWarps) {
     send_chain<kLanes, V, kTeams, kWarps, false>(a, unit, smem, l, bars);
   } else if (warp == kTeams * kWarps + 1) {
-    receive_chain<kLanes, V, kTeams, kWarps, false>(a, unit, smem, l, bars, a.h0, a.final_state, err);
+    receive_chain<kLanes, V, kTeams, kWarps, false>(a, unit, smem, l, bars, start, a.final_state, err);
   } else {
     const int team = warp / kWarps, wt = warp - team * kWarps;   // place in the team
     const int run = wt * (32 / kLanes) + lane / kLanes;
@@ -451,12 +460,13 @@ scan_backward_pipe_kernel(const Args a, unsigned* err) {
   const unsigned bars = smem + l.bars;
   const Unit<kLanes, V> unit(a);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Vec<V> start = first_state(a, unit, warp == kTeams * kWarps + 1, a.dfinal);
   start_barriers(bars, slots_of(kTeams));
   cluster_sync();
   if (warp == kTeams * kWarps) {
     send_chain<kLanes, V, kTeams, kWarps, true>(a, unit, smem, l, bars);
   } else if (warp == kTeams * kWarps + 1) {
-    receive_chain<kLanes, V, kTeams, kWarps, true>(a, unit, smem, l, bars, a.dfinal, a.dh0, err);
+    receive_chain<kLanes, V, kTeams, kWarps, true>(a, unit, smem, l, bars, start, a.dh0, err);
   } else {
     const int team = warp / kWarps, wt = warp - team * kWarps;
     const int run = wt * (32 / kLanes) + lane / kLanes;
