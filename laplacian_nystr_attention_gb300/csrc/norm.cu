@@ -33,7 +33,7 @@ norm_backward_kernel(const Args a) {
   // The kernel that sums the partials may be placed now; it waits for this grid's end.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int t = place_in_row(a);
-  const unsigned per = 1u << a.per_log2, mine = row_in_cta(a);
+  const unsigned per = 1u << a.per_log2;
   Rows<kShift> rows(a);
   Columns<VEC, NV, kShift> cols;
   cols.init(a, t, rows.shift);
@@ -146,20 +146,30 @@ norm_backward_kernel(const Args a) {
   }
   if constexpr (kInStages) ops::copies_left<0>();
   if (!a.part) return;
-  // The CTA's part: its rows side by side, one after the other.
+  // The CTA's part: its rows side by side, those of a warp first, then one warp after the other.
   float* part = a.part + (size_t)blockIdx.x * a.width;
   if (per > 1) {
-    float* sums = dynamic;   // [rows side by side, W], where the stages were
+    for (int o = a.g; o < 32; o *= 2)
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < X::kN; ++i)
+#pragma unroll
+          for (int k = 0; k < X::kW; ++k)
+            dw[j].v[i].f[k] += __shfl_xor_sync(0xffffffffu, dw[j].v[i].f[k], o);
+    float* sums = dynamic;   // [warps, W], where the stages were
+    float* mine = sums + (size_t)(threadIdx.x >> 5) * a.width;
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
       for (int i = 0; i < VEC; ++i)
-        if (cols.valid(j, i)) sums[(size_t)mine * a.width + cols.col(j) + i] = at(dw[j], i);
+        if ((int)(threadIdx.x & 31) < a.g && cols.valid(j, i)) mine[cols.col(j) + i] = at(dw[j], i);
     __syncthreads();
     for (int c = threadIdx.x; c < a.width; c += blockDim.x) {
       float v = 0.f;
-      for (unsigned k = 0; k < per; ++k) v += sums[(size_t)k * a.width + c];
+#pragma unroll
+      for (int k = 0; k < kThreads / 32; ++k) v += sums[(size_t)k * a.width + c];
       part[c] = v;
     }
   } else {
@@ -267,7 +277,7 @@ Kernel backward_kernel(bool r16, bool g16, Cut cut, int nv) {
 size_t backward_smem(const lapl_norm_config& c, const Shape& s, Cut cut) {
   const bool stages = in_stages(c.res_dtype == LAPL_BF16, c.grad_dtype == LAPL_BF16,
                                 cut == kShifted, s.nv);
-  const size_t sums = s.per > 1 ? (size_t)s.per * c.heads * c.head_dim * sizeof(float) : 0;
+  const size_t sums = s.per > 1 ? (size_t)(kThreads / 32) * c.heads * c.head_dim * sizeof(float) : 0;
   return std::max(stages ? (size_t)kStages * s.nv * 3 * 16 * s.threads : 0, sums);
 }
 
