@@ -30,6 +30,7 @@ norm_backward_kernel(const Args a) {
   constexpr bool kInStages = VEC == 8 && in_stages(kRes16, kGrad16, kShift, NV);
   constexpr bool kAhead =
       !kInStages && NV * ((kRes16 ? 4 : 8) + 2 * (kGrad16 ? 4 : 8)) * VEC / 8 <= 24;
+  constexpr bool kLate = NV * VEC >= 32;   // dsum is read after the row's sum: registers
   // The kernel that sums the partials may be placed now; it waits for this grid's end.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int t = place_in_row(a);
@@ -56,7 +57,7 @@ norm_backward_kernel(const Args a) {
       if (r < a.rows && cols.in(j)) {
         cols.template fetch<kRes16>(rs[j], a.res, j, at + cols.col(j), end);
         cols.template fetch<kGrad16>(ry[j], a.dy, j, at + cols.col(j), end);
-        if (a.dsum) cols.template fetch<kGrad16>(rd[j], a.dsum, j, at + cols.col(j), end);
+        if (a.dsum && !kLate) cols.template fetch<kGrad16>(rd[j], a.dsum, j, at + cols.col(j), end);
       }
     }
   };
@@ -135,13 +136,14 @@ norm_backward_kernel(const Args a) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       if (!(live && cols.in(j))) continue;
+      if (kLate && a.dsum) cols.template fetch<kGrad16>(cd[j], a.dsum, j, row0 + cols.col(j), end);
       X d;
 #pragma unroll
       for (int i = 0; i < X::kN; ++i)
         d.v[i] = ops::fma(ops::fill<X::kW>(rstd), ops::mul(get(cy[j], i), cols.weight(a, j, i)),
                           ops::fma(ops::fill<X::kW>(back), get(cs[j], i), get(cd[j], i)));
       if (a.dres) cols.template put<kGrad16>(a.dres, j, row0 + cols.col(j), d);
-      if (a.dx) cols.template put<kGrad16>(a.dx, j, hr + cols.head(a, j), d);
+      if (a.dx) cols.template scatter<kGrad16>(a.dx, a, j, hr, d);
     }
   }
   if constexpr (kInStages) ops::copies_left<0>();
@@ -181,26 +183,35 @@ norm_backward_kernel(const Args a) {
   }
 }
 
-// dweight[c] = sum over the CTAs' partials in a fixed order: 8 columns by 128 slices a CTA.
-__global__ void __launch_bounds__(1024)
+// dweight[c] = sum over the CTAs' partials in a fixed order: kCols columns a CTA, kSlices threads of
+// each.  Wide rows and few partials take 32 by 8, others 8 by 128.
+template <int kCols, int kSlices>
+__global__ void __launch_bounds__(kCols * kSlices)
 norm_dweight_kernel(const float* part, float* dweight, int ctas, int width) {
-  __shared__ float sm[32][9];
+  constexpr int kWarps = kCols * kSlices / 32;
+  __shared__ float sm[kWarps][kCols + 1];
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the partials are written
-  const int c = blockIdx.x * 8 + (threadIdx.x & 7);
+  const int c = blockIdx.x * kCols + threadIdx.x % kCols;
   float v = 0.f;
   if (c < width) {
 #pragma unroll 4
-    for (int k = threadIdx.x >> 3; k < ctas; k += 128) v += part[(size_t)k * width + c];
+    for (int k = threadIdx.x / kCols; k < ctas; k += kSlices) v += part[(size_t)k * width + c];
   }
-  v += __shfl_xor_sync(0xffffffffu, v, 8);
-  v += __shfl_xor_sync(0xffffffffu, v, 16);
+#pragma unroll
+  for (int o = kCols; o < 32; o *= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (lane < 8) sm[warp][lane] = v;
+  if (lane < kCols) sm[warp][lane] = v;
   __syncthreads();
-  if (warp < 8) {   // column `warp`, one of its sums a lane
+  if constexpr (kWarps == 32) {   // column `warp`, one of its sums a lane
+    if (warp >= kCols) return;
     v = sm[lane][warp];
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (lane == 0 && blockIdx.x * 8 + warp < width) dweight[blockIdx.x * 8 + warp] = v;
+    if (lane == 0 && blockIdx.x * kCols + warp < width) dweight[blockIdx.x * kCols + warp] = v;
+  } else if (warp == 0 && c < width) {
+    v = 0.f;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) v += sm[k][lane];
+    dweight[c] = v;
   }
 }
 
@@ -352,13 +363,17 @@ cudaError_t choose(const lapl_norm_plan& p, int sms, norm::Kernel kernel, const 
   return cudaSuccess;
 }
 
-// aligned: every tensor starts at a multiple of 16 bytes.
-norm::Cut cut_of(const lapl_norm_plan& p, bool aligned) {
+// aligned: every tensor starts at a multiple of 16 bytes; by_head: written head by head, too.
+norm::Cut cut_of(const lapl_norm_plan& p, bool aligned, bool by_head) {
   if (!aligned) return norm::kValues;
   if (p.cfg.head_dim % 8 == 0) return norm::kVectors;
+  // Values written one by one of a thread's 8 in a row cost more than the vectors read give, where a
+  // value a thread keeps a CTA's threads busy and 4 do for a row (backward, 8000 x 8 x 150 fp32: 39
+  // against 61 us; 60000 x 4 x 3: 21 against 9; 186 x 2 x 1718: 40 against 12).
+  if (by_head && p.cfg.heads > 1 && p.width >= 64 && p.width <= 4 * norm::kMaxThreads)
+    return norm::kValues;
   // A row of W values touches up to (W + 14) / 8 vectors; 512 threads have 4 each.
-  return p.cfg.heads == 1 && p.width + 14 < 8 * (4 * norm::kMaxThreads + 1) ? norm::kShifted
-                                                                           : norm::kValues;
+  return p.width + 14 < 8 * (4 * norm::kMaxThreads + 1) ? norm::kShifted : norm::kValues;
 }
 
 norm::Args base_args(const lapl_norm_plan& p, const norm::Shape& s) {
@@ -440,7 +455,7 @@ lapl_status lapl_norm_forward(lapl_norm_handle p, const void* x, const void* res
   if (st != LAPL_OK) return st;
   const norm::Choice& k = p->fwd[cut_of(
       *p, ops::aligned(x, 16) && ops::aligned(residual, 16) && ops::aligned(sum, 16) &&
-              ops::aligned(y, 16))];
+              ops::aligned(y, 16), false)];
   norm::Args a = base_args(*p, k.shape);
   a.x = x;
   a.res = residual;
@@ -496,7 +511,7 @@ lapl_status lapl_norm_backward(lapl_norm_handle p, const void* sum, const float*
   } else {
     const norm::Choice& k = p->bwd[cut_of(
         *p, ops::aligned(sum, 16) && ops::aligned(dy, 16) && ops::aligned(dsum, 16) &&
-                ops::aligned(dx, 16) && ops::aligned(dres, 16))];
+                ops::aligned(dx, 16) && ops::aligned(dres, 16), dx != nullptr)];
     norm::Args a = base_args(*p, k.shape);
     a.res = sum;
     a.rstd = const_cast<float*>(rstd);
@@ -509,17 +524,19 @@ lapl_status lapl_norm_backward(lapl_norm_handle p, const void* sum, const float*
     k.kernel<<<k.ctas, k.shape.threads, k.smem, st>>>(a);
     e = cudaGetLastError();
     if (e == cudaSuccess && dweight) {
+      const bool few = k.ctas <= 64 || p->width >= 8192;
       cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3((unsigned)((p->width + 7) / 8));
-      cfg.blockDim = dim3(1024);
+      cfg.gridDim = dim3((unsigned)((p->width + (few ? 31 : 7)) / (few ? 32 : 8)));
+      cfg.blockDim = dim3(few ? 256 : 1024);
       cfg.stream = st;
       cudaLaunchAttribute at[1];
       at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
       at[0].val.programmaticStreamSerializationAllowed = 1;
       cfg.attrs = at;
       cfg.numAttrs = 1;
-      e = cudaLaunchKernelEx(&cfg, norm::norm_dweight_kernel, static_cast<const float*>(a.part),
-                             dweight, k.ctas, p->width);
+      e = cudaLaunchKernelEx(&cfg, few ? norm::norm_dweight_kernel<32, 8>
+                                       : norm::norm_dweight_kernel<8, 128>,
+                             static_cast<const float*>(a.part), dweight, k.ctas, p->width);
     }
   }
   if (e != cudaSuccess) {

@@ -18,10 +18,10 @@
 // x comes head by head ([B,H,N,d]); a vector never straddles a head (d a multiple of 8), so
 // merging the heads costs only where the pieces are read from.
 // Rows of a length that is no multiple of 8 start anywhere among the vectors of the whole tensor.
-// There (one head) a CTA takes only rows that start at the same place, every 8th, 4th or 2nd one, so
-// its threads' columns still stay their own; a row's first and last vector are shared with its
-// neighbours and written value by value.  What is left (heads of such a length, a pointer off 16
-// bytes) runs with vectors of one value, a row to a CTA.
+// There a CTA takes only rows that start at the same place, every 8th, 4th or 2nd one, so its threads'
+// columns still stay their own; a row's first and last vector are shared with its neighbours and
+// written value by value, and heads of such a length are read and written so.  What is left (a
+// pointer off 16 bytes) runs with vectors of one value, a row to a CTA.
 //
 // HBM-bound.  Measured (of 6.78 TB/s): the attention's fp32 output at 4 x 8 x 16384 x 64 with a bf16
 // residual 52 us (6.5 TB/s, 95%); rows of 4096 bf16 values to e4m3 by groups of 128 38.5 us (90%; a
@@ -210,6 +210,26 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d
   return (uint32_t)lo | ((uint32_t)hi << 16);
 }
 
+// A row's values one after the other where the heads' lengths are no multiple of 8.
+struct Walk {
+  long long at;
+  int left;   // of the head
+  __device__ __forceinline__ Walk(const Args& a, long long row, int col) {
+    const unsigned c = (unsigned)max(col, 0), h = a.by_d(c);
+    at = row + (long long)h * a.n * a.d + (c - h * a.d);
+    left = a.d - (int)(c - h * a.d);
+  }
+  __device__ __forceinline__ long long next(const Args& a) {
+    const long long now = at;
+    ++at;
+    if (--left == 0) {
+      left = a.d;
+      at += (long long)(a.n - 1) * a.d;
+    }
+    return now;
+  }
+};
+
 // A thread's columns: vector j is columns col(j) .. col(j) + VEC - 1, of which those from 0 to W - 1
 // are the row's (kShift: col(0) of thread 0 is -shift).
 template <int VEC, int NV, bool kShift>
@@ -267,6 +287,19 @@ struct Columns {
         if (valid(j, i)) load_one(r, base, e, i);
     }
   }
+  // The same of a tensor by heads, whose row starts at element `row`.
+  template <bool k16>
+  __device__ __forceinline__ void gather(Raw<k16, VEC>& r, const void* base, const Args& a, int j,
+                                         long long row, long long end) const {
+    if (!kShift || a.heads == 1) {
+      fetch(r, base, j, row + head(a, j), end);
+    } else {
+      Walk w(a, row, col(j));
+#pragma unroll
+      for (int i = 0; i < VEC; ++i)
+        if (valid(j, i)) load_one(r, base, w.next(a) - i, i);
+    }
+  }
   // The same of bf16 into shared memory; zeros where `on` is not set, and behind `end`.
   __device__ __forceinline__ void copy(unsigned to, const void* base, bool on, long long e,
                                        long long end) const {
@@ -289,6 +322,18 @@ struct Columns {
 #pragma unroll
       for (int i = 0; i < VEC; ++i)
         if (valid(j, i)) store<k16, 1>(base, e + i, Values<1>{{{at(x, i)}}});
+    }
+  }
+  template <bool k16>
+  __device__ __forceinline__ void scatter(void* base, const Args& a, int j, long long row,
+                                          const Values<VEC>& x) const {
+    if (!kShift || a.heads == 1) {
+      put<k16>(base, j, row + head(a, j), x);
+    } else {
+      Walk w(a, row, col(j));
+#pragma unroll
+      for (int i = 0; i < VEC; ++i)
+        if (valid(j, i)) store<k16, 1>(base, w.next(a), Values<1>{{{at(x, i)}}});
     }
   }
 };
@@ -338,7 +383,7 @@ norm_forward_kernel(const Args a) {
       zero(rx[j]);
       zero(rr[j]);
       if (r < a.rows && cols.in(j)) {
-        cols.template fetch<kX16>(rx[j], a.x, j, xr + cols.head(a, j), end);
+        cols.template gather<kX16>(rx[j], a.x, a, j, xr, end);
         if (a.res) cols.template fetch<kRes16>(rr[j], a.res, j, rr0 + cols.col(j), end);
       }
     }

@@ -132,6 +132,24 @@ def test_rows(rows):
     backward(1, 1, rows, 37)
 
 
+@pytest.mark.parametrize("H,d", [(3, 1), (4, 3), (8, 5), (5, 13), (2, 333), (8, 257), (3, 1001),
+                                 (7, 2333), (9, 1819)])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_heads_of_odd_lengths(H, d, kind):
+    """Rows of several heads that start anywhere among the vectors, enough for every thread."""
+    rows = 1 + 40000 // (H * d)
+    forward(1, H, rows, d, kind, kind, kind)
+    forward(3, H, 7, d, kind, "f32", "bf16")
+    backward(1, H, rows, d, kind, kind)
+    backward(3, H, 7, d, "f32", kind, dsum=False)
+
+
+@pytest.mark.parametrize("rows", [150, 20000])
+def test_many_partials_of_dweight(rows):
+    backward(1, 1, rows, 64)
+    backward(1, 2, min(rows, 2000), 4500)
+
+
 @pytest.mark.parametrize("group", [0, 32, 64, 128])
 @pytest.mark.parametrize("H,d", [(1, 128), (4, 32), (2, 640), (8, 16), (32, 20), (1, 4096),
                                  (1, 16384), (128, 51)])
