@@ -63,7 +63,8 @@ typedef struct {
   int lanes;    /* threads across the channels of one token                                     */
   int threads;  /* threads of a CTA                                                             */
   int teams;    /* teams of warps that take the tokens in turn, copied ahead (the kernels for long
-                   sequences: 768 tokens or more, fp32 or an even number of bf16 channels), or 0  */
+                   sequences: 768 tokens or more, backward of bf16 512, and an even number of bf16
+                   channels), or 0                                                                */
 } lapl_scan_plan_info;
 
 lapl_status lapl_scan_create(const lapl_scan_config* cfg, lapl_scan_handle* out);

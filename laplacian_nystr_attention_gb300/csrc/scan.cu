@@ -477,9 +477,11 @@ namespace {
 
 constexpr unsigned long long kWaitNs = 1000000000ull;   // one second
 
-// Tokens from which the pipelined kernels are taken (784 tokens of 128 x 64 channels, bf16: 14.8
-// against 19.4 us; 512 tokens of 64 x 64: equal; shorter ones leave their teams without work).
-constexpr int kPipeTokens = 768;
+// Tokens from which the pipelined kernels are taken; shorter sequences leave their teams without work.
+// 32 x 16384 x 64 ones of bf16 fall to half the time; at 800 tokens forward, 40 to 700 sequences of 32
+// to 128 channels, bf16 93 to 114% of the other kernel's time, fp32 97 to 118; backward 63 to 95%, at
+// 512 tokens of bf16 80 to 97%, fp32 94 to 115, at 256 of bf16 100 to 133.
+constexpr int kPipeTokens = 768, kPipeTokensBackward16 = 512;
 
 bool whole(std::initializer_list<const void*> pointers, int bytes) {
   for (const void* q : pointers)
@@ -589,7 +591,10 @@ lapl_status lapl_scan_create(const lapl_scan_config* cfg, lapl_scan_handle* out)
   e = device_error_word(&p->dev_err);
   const bool pairs = cfg->in_dtype == LAPL_F32 ||
                      (cfg->channels % 2 == 0 && cfg->x_stride % 2 == 0 && cfg->g_stride % 2 == 0);
-  if (e == cudaSuccess && pairs && cfg->tokens >= kPipeTokens && cfg->sequences > 0) {
+  const bool forward = cfg->tokens >= kPipeTokens;
+  const bool backward =
+      cfg->tokens >= (cfg->in_dtype == LAPL_BF16 ? kPipeTokensBackward16 : kPipeTokens);
+  if (e == cudaSuccess && pairs && backward && cfg->sequences > 0) {
     scan::Held held = {};
     const scan::pipe::Pick one = scan::pick_pipe(*cfg, false, 32);
     int most = 0;
@@ -598,7 +603,8 @@ lapl_status lapl_scan_create(const lapl_scan_config* cfg, lapl_scan_handle* out)
       e = cudaFuncSetAttribute(reinterpret_cast<const void*>(one.kernel),
                                cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e == cudaSuccess) e = scan::clusters_held(one, &held);
-    if (e == cudaSuccess) e = scan::choose_pipe(*cfg, false, held, (unsigned)most, &p->fwd);
+    if (e == cudaSuccess && forward)
+      e = scan::choose_pipe(*cfg, false, held, (unsigned)most, &p->fwd);
     if (e == cudaSuccess) e = scan::choose_pipe(*cfg, true, held, (unsigned)most, &p->bwd);
   }
   if (e != cudaSuccess) {
@@ -636,9 +642,10 @@ lapl_status lapl_scan_forward(lapl_scan_handle p, const void* x, const void* g, 
   if (p->fwd.pick.kernel) {
     const int pair = c.in_dtype == LAPL_BF16 ? 2 : 1;
     a.fine = !coarse(x, a.x_stride, ib) || !coarse(g, a.g_stride, ib);
-    // Without 16-byte pieces, and with sequences and channels for the whole GPU, the other kernel is
-    // the faster one forward (16 x 4096 x 333 fp32: 66 against 83 us; backward 128 against 124).
-    const bool other = a.fine && p->geo[pair - 1].cluster == 1;
+    // Without 16-byte pieces, and with sequences and channels for nearly the whole GPU, the other
+    // kernel is the faster one (16 x 4096 x 333 fp32, clusters of 2: 64 against 83 us; 5 x 8484 x 23,
+    // of 16: 17 against 9).
+    const bool other = a.fine && p->geo[pair - 1].cluster <= 2;
     if (!other && whole({x, g}, 4) && whole({out}, pair * ob) &&
         whole({h0, states, final_state}, pair * 4))
       return launch_pipe(p, p->fwd, a, stream, "scan_forward");
@@ -679,7 +686,10 @@ lapl_status lapl_scan_backward(lapl_scan_handle p, const void* x, const void* g,
     const int pair = c.in_dtype == LAPL_BF16 ? 2 : 1;
     a.fine = !coarse(x, a.x_stride, ib) || !coarse(g, a.g_stride, ib);
     a.fine_dout = !coarse(dout, a.c, gb);
-    if (whole({x, g}, 4) && whole({dout, dx, dg}, pair * gb) &&
+    // As forward, for the whole GPU (24 x 4096 x 333 fp32: 140 against 162 us; 16 x 4096 x 333, clusters
+    // of 2: 141 against 126).
+    const bool other = a.fine && p->geo[pair - 1].cluster == 1;
+    if (!other && whole({x, g}, 4) && whole({dout, dx, dg}, pair * gb) &&
         whole({states, dfinal, dh0}, pair * 4) && !(a.fine_dout && pair * gb < 4))
       return launch_pipe(p, p->bwd, a, stream, "scan_backward");
   }

@@ -302,8 +302,8 @@ def test_long_channels(C, dtype):
     run(2, 1025, C, "sigmoid", dtype, dtype, dtype)
 
 
-@pytest.mark.parametrize("S,N,C", [(1, 768, 8), (1, 20000, 64), (3, 3000, 16), (40, 1500, 64),
-                                   (160, 800, 32), (2, 9001, 256)])
+@pytest.mark.parametrize("S,N,C", [(1, 512, 8), (50, 600, 64), (1, 768, 8), (1, 20000, 64),
+                                   (3, 3000, 16), (40, 1500, 64), (160, 800, 32), (2, 9001, 256)])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_long_splits(S, N, C, dtype):
     """One CTA a sequence up to a cluster of eight; lanes over 8, 16 or 32 pieces of a row."""
