@@ -18,9 +18,10 @@
 // consecutive tiles at once and exchanges the tiles' maps through distributed shared memory.
 // The order of every composition is fixed, so results are the same bit for bit from call to call.
 // What bounds it is the exchange: a round of tiles costs a load, a barrier and a walk one after the
-// other, whatever the bytes.  These kernels take sequences of less than 768 tokens, single tokens
-// (64 x 512 channels: 2.9 us, the launch) and odd bf16 channel counts; 512 x 256 x 64 bf16 takes 16 us
-// (7.4 us of bytes), where the kernels of scan_pipe.cuh, made for longer sequences, take 24.
+// other, whatever the bytes.  These kernels take single tokens (64 x 512 channels: 3.0 us, the launch),
+// sequences shorter than scan_pipe.cuh's kernels are made for (512 x 256 x 64 bf16: 14 us forward, 23
+// backward, of which 7.4 and 12.7 are bytes), odd bf16 channel counts, and rows of odd lengths where
+// they are many (16 x 4096 x 333 fp32: 64 us of 39).
 //
 // The sigmoid gate's steps are written h + z (x - h) with z = 1 - a = 1 / (1 + exp(g)) computed as
 // such: near a = 1 the rounding of a would be a relative error of z of 2^-24 / z, and that error

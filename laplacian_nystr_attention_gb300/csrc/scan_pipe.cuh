@@ -13,20 +13,21 @@
 //     A thread's part in the exchange is one store and two loads, and a round's maps are under way
 //     while the round before is still being received.
 //   * Each warp copies its own tokens ahead into its own ring of stages (cp.async, 16 bytes at a
-//     time): no barrier between warps, and the bytes in flight are those of the ring.
-// Two values go through the packed fp32 instructions (bf16 inputs): 24 instructions a value on 65536
-// tokens of 8 x 64 channels, against 35 in scan.cu's kernel.
+//     time): no barrier between warps, and the bytes in flight are those of the ring.  A stage is kept
+//     until its tokens are read a second time, so that registers hold the gates alone (and in the
+//     backward the slopes): holding the tokens as well took 73 us instead of 58 below.
+// Two values go through the packed fp32 instructions (bf16 inputs).
 //
-// Measured (of 6.78 TB/s): 32 x 16384 x 64 bf16, sigmoid gate: 41.6 us forward (5.0 TB/s, 74%) and
-// 73 us backward (69%); 4 x 8192 x 512 fp32: 36 and 60 us (82%).  bf16 is bound by issue and by the
-// latency of 16 warps an SM (12 in the backward, whose registers hold a run's decays, slopes and
-// gradients), fp32 by memory.  Teams of four warps put one on each scheduler, so that all four end
-// together: with three teams of six the slowest scheduler held up the chain (50.8 against 44.0 us).
-// Sequences and channels too few for the GPU's clusters cost the rest: 8 x 65536 x 64 bf16 runs in
-// 32-byte pieces of a row on 128 SMs, 48 us.
+// Measured (of 6.78 TB/s): 32 x 16384 x 64 bf16, sigmoid gate: 38.7 us forward (77%) and 57.5 us backward
+// (88%), decay gate 33.3 (89%) and 56.1 (90%); 4 x 8192 x 512 fp32: 33.0 and 54.6 us (90 and 92%).  bf16
+// with the sigmoid gate is bound by issue and by the chain, the others by memory.  Teams of four warps
+// put one on each scheduler, so that all four end together: with three teams of six the slowest
+// scheduler held up the chain (50.8 against 44.0 us).  Sequences and channels too few for the GPU's
+// clusters cost the rest: 8 x 65536 x 64 bf16 runs in 32-byte pieces of a row on 128 SMs, 44.7 us (69%).
 //
 // Copies are of 16 bytes where rows and pointers allow it, else of each thread's own 4 or 8 (which
-// takes more instructions).  scan.cu's kernels take short sequences and what is odd beyond that.
+// takes more instructions).  scan.cu's kernels take short sequences and what is odd beyond that; where
+// they meet is in lapl_scan_create, lapl_scan_forward and lapl_scan_backward.
 //
 // With T teams, a CTA whose receiving warp is at round r has sent maps up to round r + T - 1, so
 // another may be at r + T and send up to r + 2T - 1: maps of 2T rounds may be there at once.
@@ -45,7 +46,8 @@ namespace pipe {
 constexpr int kMaxCluster = 8;     // CTAs
 // Rounds of maps that may have arrived: see above.
 __host__ __device__ constexpr int slots_of(int teams) { return 2 * teams; }
-// Worker warps of a team: with the chain's two 18 warps of 96 registers, or 16 of 128.
+// Teams, and worker warps of a team: with the chain's two warps 18 of up to 112 registers forward, 14
+// of up to 128 backward.
 constexpr int kForwardTeams = 4, kForwardWarps = 4, kBackwardTeams = 3, kBackwardWarps = 4;
 
 // Bytes of a row of one tensor in shared memory, and from one run of kT rows to the next: a warp
