@@ -213,3 +213,14 @@ def test_refusals():
     assert f(plan.handle, good, p + 2, p, need, st) == _lib.LAPL_ERR_ALIGNMENT
     assert f(plan.handle, good, p, p + 8, need, st) == _lib.LAPL_ERR_ALIGNMENT
     assert f(plan.handle, good, p, p, need - 1, st) == _lib.LAPL_ERR_WORKSPACE
+
+
+def test_offsets_past_32_bits():
+    import laplacian_nystr_attention_gb300 as lna
+    t = torch.zeros((1 << 31) + 4099, dtype=torch.bfloat16, device="cuda")
+    t[-1], t[5] = 3.0, 4.0
+    out = torch.empty_like(t)
+    assert lna.GradClip.like([t]).clip([t], 1.0, outs=[out]).item() == 5.0
+    # 3 and 4 by 1/5 in fp32, rounded to bf16.
+    assert out[-1].item() == torch.tensor(0.6).bfloat16() and out[5].item() == torch.tensor(0.8).bfloat16()
+    assert out.count_nonzero() == 2

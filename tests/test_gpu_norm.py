@@ -301,3 +301,32 @@ def test_refusals():
         plan.forward(t[:64].view(1, 2, 4, 8), scales=t[:4])
     with pytest.raises(ValueError):
         plan.forward(t[:64].view(1, 2, 4, 8).cpu())
+
+
+@pytest.mark.parametrize("H,d", [(2, 1024), (1, 2049), (3, 683)])
+def test_offsets_past_32_bits(H, d):
+    """More than 2^31 values: the last rows."""
+    import laplacian_nystr_attention_gb300 as lna
+    N, last, W = (1 << 20) + 8, 4, H * d
+    assert N * W > 1 << 31
+    m = make(1, H, last, d, "bf16", "bf16", "bf16")
+    x = torch.zeros(1, H, N, d, dtype=torch.bfloat16, device="cuda")
+    res, dy = (torch.zeros(1, N, W, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    x[:, :, N - last:], res[:, N - last:] = dev(m["x"], "bf16"), dev(m["res"], "bf16")
+    dy[:, N - last:] = dev(m["dy"], "bf16")
+    w = dev(m["weight"])
+    plan = lna.ResidualNorm(lna.make_norm_config(1, H, N, d, x_dtype="bf16", res_dtype="bf16",
+                                                 out_dtype="bf16", grad_dtype="bf16"))
+    total, rstd = torch.empty_like(res), torch.empty(1, N, device="cuda")
+    y = plan.forward(x, w, residual=res, sum=total, rstd=rstd)
+    want = ref.norm(m["x"], m["res"], m["weight"], float(np.float32(1e-6)), 0, False)
+    ref.check("y", y[:, N - last:], want["y"], "bf16")
+    ref.check("sum", total[:, N - last:], want["sum"], "bf16")
+    assert (y[:, :N - last] == 0).all()
+    dx, dres, dw = plan.backward(total, rstd, w, dy)
+    kept = [t[:, N - last:].double().cpu().numpy() for t in (total, rstd)]
+    want = ref.norm_backward(kept[0], kept[1], m["weight"], m["dy"], None, H)
+    ref.check("dx", dx[:, :, N - last:], want["dx"], "bf16")
+    ref.check("dres", dres[:, N - last:], want["dres"], "bf16")
+    ref.check("dweight", dw, want["dweight"])
+    assert (dres[:, :N - last] == 0).all()

@@ -423,3 +423,26 @@ def test_no_wait_gave_up():
     att = lna.LaplacianNystromAttention(lna.make_config(1, 1, 4, 4, 8, 4))
     assert lna.lapl_attn_device_errors(att.handle, torch.cuda.current_stream().cuda_stream) == 0
     att.close()
+
+
+@pytest.mark.parametrize("S,N,C", [(36000, 512, 128), (2800, 3000, 258)])
+def test_offsets_past_32_bits(S, N, C):
+    """More than 2^31 values: the last sequence, by the kernels for short and for long ones."""
+    import laplacian_nystr_attention_gb300 as lna
+    assert S * N * C > 1 << 31
+    x, g, _, dout, _ = make(1, N, C, "sigmoid", "bf16", seed=9)
+    dout = ref.rounded(dout, "bf16")
+    want = ref.scan(x, g, "sigmoid", dout=dout)
+    # (S, N, C) tensors are 4.6 GB each: the others' values are those of zeros.
+    big = [torch.zeros(S, N, C, dtype=torch.bfloat16, device="cuda") for _ in range(3)]
+    for t, a in zip(big, (x, g, dout)):
+        t[-1:] = dev(a, "bf16")
+    plan = lna.GatedScan(lna.make_scan_config(S, N, C, in_dtype="bf16", out_dtype="bf16",
+                                              grad_dtype="bf16"))
+    states = torch.empty(plan.states_shape, device="cuda")
+    y = plan.forward(big[0], big[1], states=states)
+    dx, dg, _ = plan.backward(big[0], big[1], states, big[2])
+    ref.check("h", y[-1:], want["h"], "bf16")
+    ref.check("dx", dx[-1:], want["dx"], "bf16")
+    ref.check("dg", dg[-1:], want["dg"], "bf16")
+    assert (y[:-1] == 0).all() and (dx[:-1] == 0).all()
