@@ -12,14 +12,15 @@
 namespace lapl {
 namespace norm {
 
-// Rows of bf16 that start at any value (kShifted) reach a thread through shared memory, up to
-// kStages rows ahead: 35 us instead of 40 with the next row in registers, at 8193 rows of 2049
-// values, 60 instead of 67 at 32768 of 1001.  Rows of whole vectors gain nothing by it (57 and 55 us
-// at 32768 of 1000), and of fp32 they lose, a vector's two copies taking half of a sector each (28
-// us and 23 at 8192 of 512).
-constexpr int kStages = 4;
+// Rows of bf16 that start at any value (kShifted), and the longest ones, reach a thread through shared
+// memory, kStages - 1 rows ahead: 36 us instead of 40 with the next row in registers, at 8193 rows of
+// 2049 values, 62 instead of 67 at 32768 of 1001; 63 instead of 81 with none ahead at 2046 of 8200.
+// Shorter rows of whole vectors gain nothing by it (57 and 55 us at 32768 of 1000), and of fp32 they
+// lose, a vector's two copies taking half of a sector each (28 us and 23 at 8192 of 512).
+constexpr int stages_of(int nv) { return nv == 4 ? 2 : 4; }
+constexpr int staged(int nv) { return nv == 4 ? 2 : 3; }   // tensors: all, or all but dsum
 constexpr bool in_stages(bool res16, bool grad16, bool shift, int nv) {
-  return shift && res16 && grad16 && nv <= 2;
+  return res16 && grad16 && (shift || nv == 4);
 }
 
 template <bool kRes16, bool kGrad16, int VEC, int NV, bool kShift>
@@ -28,16 +29,17 @@ norm_backward_kernel(const Args a) {
   __shared__ float scratch[2][kMaxThreads / 32];
   extern __shared__ __align__(16) float dynamic[];
   constexpr bool kInStages = VEC == 8 && in_stages(kRes16, kGrad16, kShift, NV);
+  constexpr int kStages = stages_of(NV), kStaged = staged(NV);
   constexpr bool kAhead =
       !kInStages && NV * ((kRes16 ? 4 : 8) + 2 * (kGrad16 ? 4 : 8)) * VEC / 8 <= 24;
-  constexpr bool kLate = NV * VEC >= 32;   // dsum is read after the row's sum: registers
+  constexpr bool kLate = NV * VEC >= 32 && !kInStages;   // dsum is read after the row's sum: registers
   // The kernel that sums the partials may be placed now; it waits for this grid's end.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int t = place_in_row(a);
   const unsigned per = 1u << a.per_log2;
   Rows<kShift> rows(a);
   Columns<VEC, NV, kShift> cols;
-  cols.init(a, t, rows.shift);
+  cols.init(a, t, rows.shift, dynamic);
   const long long end = (long long)a.rows * a.width;
   using X = Values<VEC>;
   X dw[NV];
@@ -61,19 +63,20 @@ norm_backward_kernel(const Args a) {
       }
     }
   };
-  // A stage: 3 vectors of 16 bytes for each of a thread's, beside its neighbours'.  A thread reads
-  // what it copied itself, so that nothing else waits.
-  const unsigned apart = blockDim.x * 16, stage_bytes = NV * 3 * apart;
-  const unsigned stages = ops::smem_u32(dynamic) + threadIdx.x * 16;
+  // A stage: kStaged vectors of 16 bytes for each of a thread's, beside its neighbours'.  A thread
+  // reads what it copied itself, so that nothing else waits.
+  const unsigned apart = blockDim.x * 16, stage_bytes = NV * kStaged * apart;
+  const unsigned stages =
+      ops::smem_u32(dynamic) + threadIdx.x * 16 + blockDim.x * weight_bytes(VEC, NV);
   auto copy = [&](unsigned r, unsigned stage) {
     const long long at = (long long)r * a.width;
     unsigned to = stages + stage * stage_bytes;
 #pragma unroll
-    for (int j = 0; j < NV; ++j, to += 3 * apart) {
+    for (int j = 0; j < NV; ++j, to += kStaged * apart) {
       const bool on = r < a.rows && cols.in(j);
       cols.copy(to, a.res, on, at + cols.col(j), end);
       cols.copy(to + apart, a.dy, on, at + cols.col(j), end);
-      if (a.dsum) cols.copy(to + 2 * apart, a.dsum, on, at + cols.col(j), end);
+      if (kStaged == 3 && a.dsum) cols.copy(to + 2 * apart, a.dsum, on, at + cols.col(j), end);
     }
     ops::close_copies();
   };
@@ -99,11 +102,14 @@ norm_backward_kernel(const Args a) {
       unsigned from = stages + stage * stage_bytes;
       stage = (stage + 1) % kStages;
 #pragma unroll
-      for (int j = 0; j < NV; ++j, from += 3 * apart) {
+      for (int j = 0; j < NV; ++j, from += kStaged * apart) {
         read_copy(rs[j], from);
         read_copy(ry[j], from + apart);
-        if (a.dsum) read_copy(rd[j], from + 2 * apart);
-        else zero(rd[j]);
+        zero(rd[j]);
+        if (!a.dsum) continue;
+        if constexpr (kStaged == 3) read_copy(rd[j], from + 2 * apart);
+        else if (live && cols.in(j))
+          cols.template fetch<kGrad16>(rd[j], a.dsum, j, row0 + cols.col(j), end);
       }
     } else if constexpr (!kAhead) {
       fetch(row);
@@ -121,13 +127,15 @@ norm_backward_kernel(const Args a) {
     if constexpr (kAhead) fetch(row + rows.stride);
     ops::Vec<X::kW> dots = ops::fill<X::kW>(0.f);
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
+      const X w = cols.weights(a, j);
 #pragma unroll
       for (int i = 0; i < X::kN; ++i) {
         const auto dyn = ops::mul(get(cy[j], i), ops::mul(get(cs[j], i), ops::fill<X::kW>(rstd)));
         dw[j].v[i] = ops::add(dw[j].v[i], dyn);
-        dots = ops::fma(dyn, cols.weight(a, j, i), dots);
+        dots = ops::fma(dyn, w.v[i], dots);
       }
+    }
     float dot = dots.f[0];
     if constexpr (X::kW == 2) dot += dots.f[X::kW - 1];
     dot = row_reduce<false>(dot, a.g, scratch[parity]);
@@ -137,10 +145,11 @@ norm_backward_kernel(const Args a) {
     for (int j = 0; j < NV; ++j) {
       if (!(live && cols.in(j))) continue;
       if (kLate && a.dsum) cols.template fetch<kGrad16>(cd[j], a.dsum, j, row0 + cols.col(j), end);
+      const X w = cols.weights(a, j);
       X d;
 #pragma unroll
       for (int i = 0; i < X::kN; ++i)
-        d.v[i] = ops::fma(ops::fill<X::kW>(rstd), ops::mul(get(cy[j], i), cols.weight(a, j, i)),
+        d.v[i] = ops::fma(ops::fill<X::kW>(rstd), ops::mul(get(cy[j], i), w.v[i]),
                           ops::fma(ops::fill<X::kW>(back), get(cs[j], i), get(cd[j], i)));
       if (a.dres) cols.template put<kGrad16>(a.dres, j, row0 + cols.col(j), d);
       if (a.dx) cols.template scatter<kGrad16>(a.dx, a, j, hr, d);
@@ -293,7 +302,9 @@ size_t backward_smem(const lapl_norm_config& c, const Shape& s, Cut cut) {
   const bool stages = in_stages(c.res_dtype == LAPL_BF16, c.grad_dtype == LAPL_BF16,
                                 cut == kShifted, s.nv);
   const size_t sums = s.per > 1 ? (size_t)(kThreads / 32) * c.heads * c.head_dim * sizeof(float) : 0;
-  return std::max(stages ? (size_t)kStages * s.nv * 3 * 16 * s.threads : 0, sums);
+  const size_t a_thread = (cut == kValues ? 0 : weight_bytes(8, s.nv)) +
+                          (stages ? stages_of(s.nv) * s.nv * staged(s.nv) * 16 : 0);
+  return std::max(a_thread * s.threads, sums);
 }
 
 // A kernel of a plan, with its launch shape.
@@ -348,7 +359,7 @@ cudaError_t choose(const lapl_norm_plan& p, int sms, norm::Kernel kernel, const 
   int per_sm = 0;
   cudaError_t e = cudaSuccess;
   // The same for every plan: it is the kernel's, not the launch's.
-  constexpr size_t kMost = norm::kStages * 2 * 3 * 16 * norm::kMaxThreads;
+  constexpr size_t kMost = 24 * 16 * norm::kMaxThreads;   // pieces of a thread
   if (smem > kMost) return cudaErrorInvalidValue;
   if (smem > 0)
     e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
@@ -430,8 +441,8 @@ lapl_status lapl_norm_create(const lapl_norm_config* cfg, lapl_norm_handle* out)
     const norm::Cut cut = (norm::Cut)k;
     const norm::Shape f = norm::shape_of(p->width, cut, true, !x16 && r16);
     const norm::Shape b = norm::shape_of(p->width, cut, r16 && g16, true);
-    e = choose(*p, sms, norm::forward_kernel(cfg->out_dtype, x16, r16, cut, f.nv), f, cut, 0,
-               &p->fwd[k]);
+    e = choose(*p, sms, norm::forward_kernel(cfg->out_dtype, x16, r16, cut, f.nv), f, cut,
+               cut == norm::kValues ? 0 : (size_t)norm::weight_bytes(8, f.nv) * f.threads, &p->fwd[k]);
     if (e == cudaSuccess)
       e = choose(*p, sms, norm::backward_kernel(r16, g16, cut, b.nv), b, cut,
                  norm::backward_smem(*cfg, b, cut), &p->bwd[k]);
@@ -470,7 +481,7 @@ lapl_status lapl_norm_forward(lapl_norm_handle p, const void* x, const void* res
   a.rstd = rstd;
   a.y = y;
   a.scales = scales;
-  k.kernel<<<k.ctas, k.shape.threads, 0, static_cast<cudaStream_t>(stream)>>>(a);
+  k.kernel<<<k.ctas, k.shape.threads, k.smem, static_cast<cudaStream_t>(stream)>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {
     ops::set_error(p->last_error, e, "norm_forward");

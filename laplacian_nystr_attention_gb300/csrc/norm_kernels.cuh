@@ -230,15 +230,25 @@ struct Walk {
   }
 };
 
+// Shared memory of a thread for its weights.
+constexpr int weight_bytes(int vec, int nv) { return vec == 8 && nv > 2 ? nv * 32 : 0; }
+
 // A thread's columns: vector j is columns col(j) .. col(j) + VEC - 1, of which those from 0 to W - 1
 // are the row's (kShift: col(0) of thread 0 is -shift).
 template <int VEC, int NV, bool kShift>
 struct Columns {
-  static constexpr bool kHeads = VEC == 8 && !kShift, kWeights = NV * VEC <= 16;
+  static constexpr bool kHeads = VEC == 8 && !kShift;
+  // Weights in registers, or (longer rows) in shared memory, a thread's 16-byte pieces beside its
+  // neighbours' (read from global memory for each row: 2^24 bf16 values in rows of 8191 forward 63
+  // instead of 33 us).
+  static constexpr bool kWeights = NV * VEC <= 16, kShared = !kWeights && VEC == 8;
   int first, step, width;
   long long place[kHeads ? NV : 1];              // in [B,H,N,d]
   Values<VEC> w[kWeights ? NV : 1];
-  __device__ __forceinline__ void init(const Args& a, int t, int shift) {
+  unsigned shared;
+  // room: of shared memory, weight_bytes(NV) for each of the CTA's threads.
+  __device__ __forceinline__ void init(const Args& a, int t, int shift, void* room) {
+    shared = kShared ? ops::smem_u32(room) + threadIdx.x * 16 : 0u;
     first = t * VEC - (kShift ? shift : 0);
     step = a.g * VEC;
     width = a.width;
@@ -248,6 +258,13 @@ struct Columns {
       if constexpr (kWeights)
 #pragma unroll
         for (int i = 0; i < Values<VEC>::kN; ++i) w[j].v[i] = load_weight(a, j, i);
+      if constexpr (kShared)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const auto lo = load_weight(a, j, 2 * k), hi = load_weight(a, j, 2 * k + 1);
+          asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(piece(j, k)), "f"(lo.f[0]),
+                       "f"(lo.f[1]), "f"(hi.f[0]), "f"(hi.f[1]) : "memory");
+        }
     }
   }
   __device__ __forceinline__ int col(int j) const { return first + j * step; }
@@ -270,9 +287,23 @@ struct Columns {
     if constexpr (kHeads) return place[j];
     else return head_col(a, col(j));
   }
-  __device__ __forceinline__ ops::Vec<Values<VEC>::kW> weight(const Args& a, int j, int i) const {
-    if constexpr (kWeights) return w[j].v[i];
-    else return load_weight(a, j, i);
+  __device__ __forceinline__ unsigned piece(int j, int k) const {
+    return shared + (2 * j + k) * blockDim.x * 16;
+  }
+  __device__ __forceinline__ Values<VEC> weights(const Args& a, int j) const {
+    Values<VEC> r;
+    if constexpr (kWeights) {
+      r = w[j];
+    } else if constexpr (kShared) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(r.v[2 * k].f[0]), "=f"(r.v[2 * k].f[1]), "=f"(r.v[2 * k + 1].f[0]),
+                       "=f"(r.v[2 * k + 1].f[1]) : "r"(piece(j, k)) : "memory");
+    } else {
+      r.v[0] = load_weight(a, j, 0);
+    }
+    return r;
   }
   // Vector j at element e of a tensor that ends at `end`, with its neighbours' values where it is
   // not the row's (trim() clears them when the values are used: the load is not waited for here).
@@ -366,13 +397,14 @@ template <bool kX16, bool kRes16, int kOut, int VEC, int NV, bool kShift>
 __global__ void __launch_bounds__(kMaxThreads)
 norm_forward_kernel(const Args a) {
   __shared__ float scratch[2][2][kMaxThreads / 32];
+  extern __shared__ __align__(16) float room[];
   __shared__ float seg[VEC == 1 && kOut == kF8 ? 2 : 1][VEC == 1 && kOut == kF8 ? kMaxWidth / 32 : 1];
   // Registers for a row ahead: where a thread's part of a row is small.
   constexpr bool kAhead = NV * ((kX16 ? 4 : 8) + (kRes16 ? 4 : 8)) * VEC / 8 <= 32;
   const int t = place_in_row(a);
   Rows<kShift> rows(a);
   Columns<VEC, NV, kShift> cols;
-  cols.init(a, t, rows.shift);
+  cols.init(a, t, rows.shift, room);
   const long long end = (long long)a.rows * a.width;
   Raw<kX16, VEC> rx[NV];
   Raw<kRes16, VEC> rr[NV];
@@ -421,10 +453,12 @@ norm_forward_kernel(const Args a) {
     const float rstd = rsqrtf(fmaf(sq, a.inv_width, a.eps));
     if (a.rstd && live && t == 0) a.rstd[row] = rstd;
 #pragma unroll
-    for (int j = 0; j < NV; ++j)
+    for (int j = 0; j < NV; ++j) {
+      const X w = cols.weights(a, j);
 #pragma unroll
       for (int i = 0; i < X::kN; ++i)
-        s[j].v[i] = ops::mul(s[j].v[i], ops::mul(cols.weight(a, j, i), ops::fill<X::kW>(rstd)));
+        s[j].v[i] = ops::mul(s[j].v[i], ops::mul(w.v[i], ops::fill<X::kW>(rstd)));
+    }
     if constexpr (kOut != kF8) {
 #pragma unroll
       for (int j = 0; j < NV; ++j)
