@@ -110,9 +110,6 @@ class _Plan:
         if t.numel() and any(n != 1 and a != b for n, a, b in zip(shape, t.stride(), strides)):
             raise ValueError(f"{want.name}: expected strides {strides}, got {t.stride()}")
 
-    def _optional(self, t, want):
-        return None if t is None else self._check(t, want)
-
     def _on(self, stream, tensors):
         """A context in which the call's stream is current; tensors that the call uses on a stream
         that is not theirs are kept for it."""
@@ -172,13 +169,19 @@ class GatedScan(_Plan):
         if stream is not None:
             with self._on(stream, (x, g, h0, lengths, out, states, final)):
                 return self.forward(x, g, h0, lengths, out, states, final)
+        at_x = self._check(x, self._x)
         if out is None:
             out = self._empty(x.shape, dtype=self._out.dtype, device=self.device)
+            at_out = out.data_ptr()
+        else:
+            at_out = self._check(out, self._out)
         _lib.lapl_scan_forward(
-            self.handle, self._check(x, self._x), self._check(g, self._g),
-            self._optional(h0, self._state["h0"]), self._optional(lengths, self._lengths),
-            self._check(out, self._out), self._optional(states, self._states),
-            self._optional(final, self._state["final"]), self._raw_stream(self._index))
+            self.handle, at_x, self._check(g, self._g),
+            None if h0 is None else self._check(h0, self._state["h0"]),
+            None if lengths is None else self._check(lengths, self._lengths), at_out,
+            None if states is None else self._check(states, self._states),
+            None if final is None else self._check(final, self._state["final"]),
+            self._raw_stream(self._index))
         return out
 
     __call__ = forward
@@ -188,24 +191,37 @@ class GatedScan(_Plan):
         forward() wrote for the same x, g, h0 and lengths.  grads: optional dict with preallocated
         "dx", "dg" (grad_dtype, rows apart as x's and g's) and "dh0" (fp32 [S, C]; may be
         dfinal)."""
-        d = dict(grads) if grads else {}
         if stream is not None:
-            with self._on(stream, (x, g, states, dout, dfinal, lengths, *d.values())):
+            with self._on(stream, (x, g, states, dout, dfinal, lengths, *(grads or {}).values())):
                 return self.backward(x, g, states, dout, dfinal, lengths, grads)
-        for want, like in ((self._dx, x), (self._dg, g)):
-            if want.name not in d:
-                t = self._empty((*like.shape[:-1], want.rows), dtype=want.dtype,
-                                device=self.device)
-                d[want.name] = t if want.rows == want.shape[-1] else t[..., :want.shape[-1]]
-        if "dh0" not in d:
-            d["dh0"] = self._empty(self.state_shape, dtype=self._states.dtype, device=self.device)
+        get = (grads or {}).get
+        dx, dg, dh0 = get("dx"), get("dg"), get("dh0")
+        at_x, at_g = self._check(x, self._x), self._check(g, self._g)
+        dx, at_dx = self._like(dx, self._dx, x)
+        dg, at_dg = self._like(dg, self._dg, g)
+        if dh0 is None:
+            dh0 = self._empty(self.state_shape, dtype=self._states.dtype, device=self.device)
+            at_dh0 = dh0.data_ptr()
+        else:
+            at_dh0 = self._check(dh0, self._state["dh0"])
         _lib.lapl_scan_backward(
-            self.handle, self._check(x, self._x), self._check(g, self._g),
-            self._check(states, self._states), self._optional(lengths, self._lengths),
-            self._check(dout, self._dout), self._optional(dfinal, self._state["dfinal"]),
-            self._check(d["dx"], self._dx), self._check(d["dg"], self._dg),
-            self._check(d["dh0"], self._state["dh0"]), self._raw_stream(self._index))
-        return d["dx"], d["dg"], d["dh0"]
+            self.handle, at_x, at_g, self._check(states, self._states),
+            None if lengths is None else self._check(lengths, self._lengths),
+            self._check(dout, self._dout),
+            None if dfinal is None else self._check(dfinal, self._state["dfinal"]),
+            at_dx, at_dg, at_dh0, self._raw_stream(self._index))
+        return dx, dg, dh0
+
+    def _like(self, grad, want, like):
+        """A gradient and its address: the one given, checked, or a new one in rows as like's."""
+        if grad is not None:
+            return grad, self._check(grad, want)
+        if want.rows == want.shape[-1]:
+            grad = self._empty(like.shape, dtype=want.dtype, device=self.device)
+        else:
+            grad = self._empty((*like.shape[:-1], want.rows), dtype=want.dtype,
+                               device=self.device)[..., :want.shape[-1]]
+        return grad, grad.data_ptr()
 
 
 class ResidualNorm(_Plan):
@@ -259,13 +275,18 @@ class ResidualNorm(_Plan):
             raise ValueError("scales: only for 8-bit outputs")
         if out is None:
             out = self._empty(self.rows_shape, dtype=self._out.dtype, device=self.device)
+            at_out = out.data_ptr()
+        else:
+            at_out = self._check(out, self._out)
         if scales is None and self.f8:
             scales = self._empty(self.scales_shape, dtype=self._scales.dtype, device=self.device)
         _lib.lapl_norm_forward(
             self.handle, self._by_head(x, self._x, self._x_row),
-            self._optional(residual, self._residual), self._optional(weight, self._weight),
-            self._optional(sum, self._sum), self._optional(rstd, self._rstd),
-            self._check(out, self._out), self._optional(scales, self._scales),
+            None if residual is None else self._check(residual, self._residual),
+            None if weight is None else self._check(weight, self._weight),
+            None if sum is None else self._check(sum, self._sum),
+            None if rstd is None else self._check(rstd, self._rstd), at_out,
+            None if scales is None else self._check(scales, self._scales),
             self._raw_stream(self._index))
         return (out, scales) if self.f8 else out
 
@@ -277,27 +298,35 @@ class ResidualNorm(_Plan):
         itself).  grads: optional dict with preallocated "dx" ([B, H, N, d], the dout that the
         attention's backward takes), "dres" ([B, N, W]; may be dsum) and "dweight" (fp32 [W]), or
         None for one that is not wanted."""
-        d = dict(grads) if grads else {}
         if stream is not None:
-            with self._on(stream, (sum, rstd, weight, dy, dsum, *d.values())):
+            with self._on(stream, (sum, rstd, weight, dy, dsum, *(grads or {}).values())):
                 return self.backward(sum, rstd, weight, dy, dsum, grads)
-        for want in (self._dx, self._dres, self._dweight):
-            if want.name not in d:
-                d[want.name] = self._empty(want.shape, dtype=want.dtype, device=self.device)
-        dx, dres, dweight = d["dx"], d["dres"], d["dweight"]
+        grads = grads or {}
+        dx, at_dx = self._wanted(grads, self._dx)
+        dres, at_dres = self._wanted(grads, self._dres)
+        dweight, at_dweight = self._wanted(grads, self._dweight)
         workspace = None
         if dweight is not None:
             workspace = self._empty(self._workspace_floats, dtype=self._rstd.dtype,
                                     device=self.device)
         _lib.lapl_norm_backward(
             self.handle, self._check(sum, self._sum), self._check(rstd, self._rstd),
-            self._optional(weight, self._weight), self._check(dy, self._dy),
-            self._optional(dsum, self._dsum),
-            None if dx is None else self._by_head(dx, self._dx, self._dx_row),
-            self._optional(dres, self._dres), self._optional(dweight, self._dweight),
+            None if weight is None else self._check(weight, self._weight),
+            self._check(dy, self._dy), None if dsum is None else self._check(dsum, self._dsum),
+            at_dx, at_dres, at_dweight,
             None if workspace is None else workspace.data_ptr(), self.workspace_bytes,
             self._raw_stream(self._index))
         return dx, dres, dweight
+
+    def _wanted(self, grads, want):
+        """A gradient and its address: the one given, checked, or a new one; None for None."""
+        if want.name not in grads:
+            t = self._empty(want.shape, dtype=want.dtype, device=self.device)
+            return t, t.data_ptr()
+        t = grads[want.name]
+        if t is None:
+            return None, None
+        return t, self._by_head(t, want, self._dx_row) if want is self._dx else self._check(t, want)
 
 
 class GradClip(_Plan):
