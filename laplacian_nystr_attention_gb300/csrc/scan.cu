@@ -18,8 +18,8 @@
 // consecutive tiles at once and exchanges the tiles' maps through distributed shared memory.
 // The order of every composition is fixed, so results are the same bit for bit from call to call.
 // What bounds it is the exchange: a round of tiles costs a load, a barrier and a walk one after the
-// other, whatever the bytes.  These kernels take single tokens (64 x 512 channels: 3.0 us, the launch),
-// sequences shorter than scan_pipe.cuh's kernels are made for (512 x 256 x 64 bf16: 14 us forward, 23
+// other, whatever the bytes.  These kernels take sequences of more than scan_few.cu's four tokens
+// that are shorter than scan_pipe.cuh's are made for (512 x 256 x 64 bf16: 14 us forward, 23
 // backward, of which 7.4 and 12.7 are bytes), odd bf16 channel counts, and rows of odd lengths where
 // they are many (16 x 4096 x 333 fp32: 64 us of 39).
 //
@@ -31,6 +31,7 @@
 #include <algorithm>
 #include <new>
 
+#include "scan_few.cuh"
 #include "scan_pipe.cuh"
 
 namespace cg = cooperative_groups;
@@ -551,9 +552,39 @@ lapl_status launch_pipe(lapl_scan_plan* p, const scan::Pipe& k, scan::Args& a, v
   return LAPL_OK;
 }
 
+// Few tokens (forward): four channels a thread where every tensor's rows start at multiples of them.
+lapl_status launch_few(lapl_scan_plan* p, scan::Args& a, void* stream, const char* where) {
+  const lapl_scan_config& c = p->cfg;
+  const int ib = ops::dtype_bytes(c.in_dtype), ob = ops::dtype_bytes(c.out_dtype);
+  const bool fours = c.channels % 4 == 0 && a.x_stride % 4 == 0 && a.g_stride % 4 == 0 &&
+                     whole({a.x, a.g}, 4 * ib) && whole({a.out}, 4 * ob) &&
+                     whole({a.h0, a.states, a.final_state}, 16);
+  const int v = fours ? 4 : 1, need = (c.channels + v - 1) / v;
+  scan::Geo& g = a.geo;
+  g.lanes = 1;
+  g.lanes_log2 = 0;
+  while (g.lanes < need && g.lanes < scan::few::kThreads) {
+    g.lanes *= 2;
+    ++g.lanes_log2;
+  }
+  g.blocks = (need + g.lanes - 1) / g.lanes;
+  const int per = scan::few::kThreads >> g.lanes_log2;
+  const long long ctas = (long long)((c.sequences - 1) / per + 1) * g.blocks;
+  scan::few::forward(c.in_dtype == LAPL_BF16, c.out_dtype == LAPL_BF16, c.gate == LAPL_GATE_SIGMOID,
+                     v, c.tokens)<<<(unsigned)ctas, scan::few::kThreads, 0,
+                                    static_cast<cudaStream_t>(stream)>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) {
+    ops::set_error(p->last_error, e, where);
+    return LAPL_ERR_CUDA;
+  }
+  return LAPL_OK;
+}
+
 scan::Args base_args(const lapl_scan_plan& p) {
   scan::Args a = {};
   const lapl_scan_config& c = p.cfg;
+  a.sequences = c.sequences;
   a.n = c.tokens;
   a.c = c.channels;
   a.chunks = (c.tokens + scan::kT - 1) / scan::kT;
@@ -640,6 +671,7 @@ lapl_status lapl_scan_forward(lapl_scan_handle p, const void* x, const void* g, 
   a.states = states;
   a.final_state = final_state;
   const int ib = ops::dtype_bytes(c.in_dtype), ob = ops::dtype_bytes(c.out_dtype);
+  if (c.tokens <= scan::few::kTokens) return launch_few(p, a, stream, "scan_forward");
   if (p->fwd.pick.kernel) {
     const int pair = c.in_dtype == LAPL_BF16 ? 2 : 1;
     a.fine = !coarse(x, a.x_stride, ib) || !coarse(g, a.g_stride, ib);

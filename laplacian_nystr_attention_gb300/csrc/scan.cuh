@@ -31,7 +31,7 @@ struct Args {
   void* dg;
   float* dh0;
   long long x_stride, g_stride;
-  int n, c, chunks, reverse;
+  int sequences, n, c, chunks, reverse;
   // scan_pipe.cuh: x and g, and dout, copied in less than 16 bytes; the bound of a wait, and whether
   // the last round's maps are not sent (fault injection for tests).
   bool fine, fine_dout, skip_last;

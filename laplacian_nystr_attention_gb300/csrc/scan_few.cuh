@@ -1,0 +1,19 @@
+// scan_few.cuh -- what scan.cu launches of scan_few.cu.
+#pragma once
+
+#include "scan.cuh"
+
+namespace lapl {
+namespace scan {
+namespace few {
+
+constexpr int kTokens = 4;      // the most these kernels take
+constexpr int kThreads = 256;   // of a CTA: lanes across the channels, the rest sequences
+
+using Kernel = void (*)(Args);
+// v: channels of a thread, 4 or 1.
+Kernel forward(bool in16, bool out16, bool sig, int v, int tokens);
+
+}  // namespace few
+}  // namespace scan
+}  // namespace lapl

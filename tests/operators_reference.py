@@ -36,7 +36,12 @@ def scan(x, g, gate, h0=None, lens=None, reverse=False, dout=None, dfinal=None):
     most 4 (expf 2, the sum 1/2, the division 1, rounded up); the same step is taken a second time
     as a map, whose two parts round alike, and each composition of maps adds 2.  That is at most 16
     roundings for each step, relative to |h_{i-1}| + |b_i| with absolute values carried through the
-    recurrence (H); errors decay as the state does."""
+    recurrence (H); errors decay as the state does.
+
+    Backward the sigmoid gate's decay is 1 - z, too: with z (1 + t), |t| <= 4 U, in its place
+    E = (1 - z) D is off by t z D, which is 4 U of z D and not of E: where a = 1 - z is small, more
+    than any number of roundings of a D.  8 U z |D| is added to E's bound for that, and, as
+    dg = z slope E, z |slope| times it to dg's."""
     S, N, C = x.shape
     lens = [N] * S if lens is None else [int(min(max(n, 0), N)) for n in lens]
     x, g = _turned(x, lens, reverse), _turned(g, lens, reverse)
@@ -76,8 +81,10 @@ def scan(x, g, gate, h0=None, lens=None, reverse=False, dout=None, dfinal=None):
             slope, es, ms = before[:, i], eb[:, i], Hb[:, i]
         dg[:, i] = k * slope * here
         eg[:, i] = k * ((es + 16 * U * ms) * mag + np.abs(slope) * eh + 16 * U * ms * mag)
+        ez = 8 * U * z[:, i] * mag if gate == "sigmoid" else 0.0
+        eg[:, i] += z[:, i] * np.abs(slope) * ez
         keep = live[:, i]
-        ED = np.where(keep, np.abs(a[:, i]) * eh, ED)
+        ED = np.where(keep, np.abs(a[:, i]) * eh + ez, ED)
         M = np.where(keep, np.abs(a[:, i]) * mag, M)
         D = np.where(keep, a[:, i] * here, D)
     for name, v, e in (("dx", dx, ex), ("dg", dg, eg)):

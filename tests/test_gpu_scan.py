@@ -136,6 +136,39 @@ def test_padding_is_not_read():
     assert torch.equal(got[0][2][0], h0[0])                # a length of zero hands h0 on
 
 
+@pytest.mark.parametrize("gate", ["decay", "sigmoid"])
+@pytest.mark.parametrize("reverse", [False, True])
+@pytest.mark.parametrize("dtype,out", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32"),
+                                       ("f32", "bf16")])
+def test_few_tokens(gate, reverse, dtype, out):
+    """One to four tokens and just more; channels by four and not; several sequences a CTA and
+    several CTAs a sequence; lengths of zero."""
+    for N in (1, 2, 3, 4, 5):
+        lens = [N, 0, 1, N - 1, N + 3, -2, N]
+        for S, C, packed in ((7, 8, 0), (7, 65, 0), (7, 1100, 2200), (7, 12, 30)):
+            run(S, N, C, gate, dtype, out, reverse=reverse, lens=lens, packed=packed)
+    run(300, 1, 20, gate, dtype, out, h0=False)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_few_tokens_misaligned(dtype):
+    """Every pointer one element off 16 bytes, the state in place."""
+    import laplacian_nystr_attention_gb300 as lna
+    S, N, C = 3, 2, 64
+    x, g, h0, _, _ = make(S, N, C, "sigmoid", dtype, seed=4)
+    want = ref.scan(x, g, "sigmoid", h0)
+
+    def off(a, kind):
+        t = torch.empty(a.size + 1, dtype=TYPES[kind], device="cuda")[1:].view(a.shape)
+        return t.copy_(dev(a, kind))
+
+    state, out = off(h0, "f32"), off(x, dtype)
+    plan = lna.GatedScan(lna.make_scan_config(S, N, C, in_dtype=dtype, out_dtype=dtype))
+    plan.forward(off(x, dtype), off(g, dtype), h0=state, final=state, out=out)
+    ref.check("h", out, want["h"], dtype)
+    ref.check("final", state, want["final"])
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("C,packed", [(24, 48), (24, 64), (23, 47), (22, 46), (333, 700)])
 def test_rows_apart(dtype, C, packed):
