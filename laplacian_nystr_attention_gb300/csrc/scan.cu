@@ -18,8 +18,8 @@
 // consecutive tiles at once and exchanges the tiles' maps through distributed shared memory.
 // The order of every composition is fixed, so results are the same bit for bit from call to call.
 // What bounds it is the exchange: a round of tiles costs a load, a barrier and a walk one after the
-// other, whatever the bytes.  These kernels take sequences of more than scan_few.cu's four tokens
-// that are shorter than scan_pipe.cuh's are made for (512 x 256 x 64 bf16: 14 us forward, 23
+// other, whatever the bytes.  These kernels take sequences longer than scan_few.cu's few tokens and
+// shorter than scan_pipe.cuh's are made for (512 x 256 x 64 bf16: 14 us forward, 23
 // backward, of which 7.4 and 12.7 are bytes), odd bf16 channel counts, and rows of odd lengths where
 // they are many (16 x 4096 x 333 fp32: 64 us of 39).
 //
@@ -468,6 +468,7 @@ struct lapl_scan_plan {
   unsigned* dev_err;
   lapl::scan::Geo geo[2];   // by channels a lane: 1, 2
   lapl::scan::Pipe fwd, bwd;
+  bool few;                 // forward by scan_few.cu
   unsigned long long wait_ns;
   int skip_last;
   char last_error[lapl::ops::kErrorText];
@@ -552,6 +553,20 @@ lapl_status launch_pipe(lapl_scan_plan* p, const scan::Pipe& k, scan::Args& a, v
   return LAPL_OK;
 }
 
+scan::Geo few_geometry(const lapl_scan_config& c, int v) {
+  const int need = (c.channels + v - 1) / v;
+  scan::Geo g = {};
+  g.lanes = 1;
+  while (g.lanes < need && g.lanes < scan::few::kThreads) {
+    g.lanes *= 2;
+    ++g.lanes_log2;
+  }
+  g.blocks = (need + g.lanes - 1) / g.lanes;
+  g.threads = scan::few::kThreads;
+  g.cluster = g.tiles = 1;
+  return g;
+}
+
 // Few tokens (forward): four channels a thread where every tensor's rows start at multiples of them.
 lapl_status launch_few(lapl_scan_plan* p, scan::Args& a, void* stream, const char* where) {
   const lapl_scan_config& c = p->cfg;
@@ -559,15 +574,8 @@ lapl_status launch_few(lapl_scan_plan* p, scan::Args& a, void* stream, const cha
   const bool fours = c.channels % 4 == 0 && a.x_stride % 4 == 0 && a.g_stride % 4 == 0 &&
                      whole({a.x, a.g}, 4 * ib) && whole({a.out}, 4 * ob) &&
                      whole({a.h0, a.states, a.final_state}, 16);
-  const int v = fours ? 4 : 1, need = (c.channels + v - 1) / v;
-  scan::Geo& g = a.geo;
-  g.lanes = 1;
-  g.lanes_log2 = 0;
-  while (g.lanes < need && g.lanes < scan::few::kThreads) {
-    g.lanes *= 2;
-    ++g.lanes_log2;
-  }
-  g.blocks = (need + g.lanes - 1) / g.lanes;
+  const int v = fours ? 4 : 1;
+  const scan::Geo& g = a.geo = few_geometry(c, v);
   const int per = scan::few::kThreads >> g.lanes_log2;
   const long long ctas = (long long)((c.sequences - 1) / per + 1) * g.blocks;
   scan::few::forward(c.in_dtype == LAPL_BF16, c.out_dtype == LAPL_BF16, c.gate == LAPL_GATE_SIGMOID,
@@ -619,6 +627,11 @@ lapl_status lapl_scan_create(const lapl_scan_config* cfg, lapl_scan_handle* out)
     return LAPL_ERR_CUDA;
   }
   for (int v = 1; v <= 2; ++v) p->geo[v - 1] = scan::geometry(*cfg, sms, v);
+  // Tokens one after the other in a thread: where there are few, and with threads for the GPU some more
+  // (bf16 and fp32, 8 tokens of 64 x 4096 channels: 42 and 38% of the other kernel's time, of 1 x 4096,
+  // 110 and 117; 32 tokens of 64 x 4096: 94 and 80, of 256 x 512: 107 and 98).
+  p->few = cfg->tokens <= 8 ||
+           (cfg->tokens <= 32 && (long long)cfg->sequences * cfg->channels >= 1600LL * sms);
   // Long sequences: the pipelined kernels, for bf16 inputs in pairs of channels.
   e = device_error_word(&p->dev_err);
   const bool pairs = cfg->in_dtype == LAPL_F32 ||
@@ -671,7 +684,7 @@ lapl_status lapl_scan_forward(lapl_scan_handle p, const void* x, const void* g, 
   a.states = states;
   a.final_state = final_state;
   const int ib = ops::dtype_bytes(c.in_dtype), ob = ops::dtype_bytes(c.out_dtype);
-  if (c.tokens <= scan::few::kTokens) return launch_few(p, a, stream, "scan_forward");
+  if (p->few) return launch_few(p, a, stream, "scan_forward");
   if (p->fwd.pick.kernel) {
     const int pair = c.in_dtype == LAPL_BF16 ? 2 : 1;
     a.fine = !coarse(x, a.x_stride, ib) || !coarse(g, a.g_stride, ib);
@@ -737,7 +750,8 @@ lapl_status lapl_scan_plan_info_get(lapl_scan_handle p, lapl_scan_plan_info* inf
   if (!p || !info) return LAPL_ERR_INVALID_ARG;
   const int v = p->cfg.in_dtype == LAPL_BF16 && p->cfg.channels % 2 == 0 ? 2 : 1;
   const bool pipe = p->fwd.pick.kernel != nullptr;
-  const scan::Geo& g = pipe ? p->fwd.geo : p->geo[v - 1];
+  const scan::Geo g = p->few ? few_geometry(p->cfg, p->cfg.channels % 4 == 0 ? 4 : 1)
+                      : pipe ? p->fwd.geo : p->geo[v - 1];
   info->cluster = g.cluster;
   info->lanes = g.lanes;
   info->threads = g.threads;

@@ -1,10 +1,12 @@
-// scan_few.cu -- the gated linear recurrence for one to four tokens, as a model that answers token by
-// token calls it: scan.cu's formulas without its exchange.
+// scan_few.cu -- the gated linear recurrence over few tokens, as a model that answers token by token
+// calls it: scan.cu's formulas without its exchange.
 //
-// A thread has the tokens of four channels (one where rows or pointers are not multiples of four
-// elements), reads them all at once, goes through the steps with the state in registers, and is done:
-// 128 x 1 x 4096 bf16 takes 2.4 us where the kernel for longer sequences, 32 threads a CTA and 16 tokens
-// a thread, takes 15.8; 64 x 1 x 512 1.7 and 2.9; 20000 x 2 x 512 34 (89% of the copy's rate) and 317.  What bounds it is the launch, then the bytes.
+// A thread has all tokens of four channels (one where rows or pointers are not multiples of four
+// elements) and goes through the steps with the state in registers: of up to four tokens it reads all
+// at once, of more some at a time with the next ones on their way.  128 x 1 x 4096 bf16 takes 2.4 us where
+// the kernel for longer sequences, 32 threads a CTA and 16 tokens a thread, takes 15.8; 64 x 1 x 512 1.7
+// and 2.9; 20000 x 2 x 512 34 (89% of the copy's rate) and 317; 64 x 8 x 4096 4.1 and 9.8.  What bounds
+// it is the launch, then the bytes.
 #include "scan_few.cuh"
 
 namespace lapl {
@@ -56,8 +58,8 @@ __device__ __forceinline__ void store_state(void* base, long long e, const State
   }
 }
 
-// T: tokens, at most.
-template <bool kIn16, bool kOut16, int V, bool kSig, int T>
+// T: tokens at a time; kMore: and the next T on their way while those are worked on.
+template <bool kIn16, bool kOut16, int V, bool kSig, int T, bool kMore>
 __global__ void __launch_bounds__(kThreads) scan_few_kernel(const Args a) {
   constexpr int kW = Parts<V>::kW, kN = Parts<V>::kN;
   const int unit = blockIdx.x / a.geo.blocks, block = blockIdx.x - unit * a.geo.blocks;
@@ -69,32 +71,46 @@ __global__ void __launch_bounds__(kThreads) scan_few_kernel(const Args a) {
   State<V> h;
 #pragma unroll
   for (int k = 0; k < kN; ++k) h.p[k] = fill<kW>(0.f);
+  auto row = [&](int i) { return s * a.n + (a.reverse ? len - 1 - i : i); };
   Token<kIn16, V> x[T], g[T];
+  auto fetch = [&](int i0) {
 #pragma unroll
-  for (int i = 0; i < T; ++i)
-    if (i < len) {
-      const long long row = s * a.n + (a.reverse ? len - 1 - i : i);
-      g[i] = load_token<kIn16, V>(a.g, row * a.g_stride + c);
-      x[i] = load_token<kIn16, V>(a.x, row * a.x_stride + c);
-    }
+    for (int u = 0; u < T; ++u)
+      if (i0 + u < len) {
+        g[u] = load_token<kIn16, V>(a.g, row(i0 + u) * a.g_stride + c);
+        x[u] = load_token<kIn16, V>(a.x, row(i0 + u) * a.x_stride + c);
+      }
+  };
+  fetch(0);
   if (a.h0) {
     const Token<false, V> t = load_token<false, V>(a.h0, s * a.c + c);
 #pragma unroll
     for (int k = 0; k < kN; ++k) h.p[k] = widen(t.p[k]);
   }
-  if (a.states) store_state<false>(a.states, s * a.c + c, h);
+  for (int i0 = 0; i0 < (kMore ? a.n : 1); i0 += T) {
+    Token<kIn16, V> nx[T], ng[T];
 #pragma unroll
-  for (int i = 0; i < T; ++i) {
-    if (i < len) {
+    for (int u = 0; u < T; ++u) {
+      nx[u] = x[u];
+      ng[u] = g[u];
+    }
+    if (kMore) fetch(i0 + T);
+    if (a.states && i0 % kT == 0)
+      store_state<false>(a.states, (s * a.chunks + i0 / kT) * a.c + c, h);
 #pragma unroll
-      for (int k = 0; k < kN; ++k)
-        h.p[k] = step<kSig>(gate_of<kSig>(g[i].p[k]), widen(x[i].p[k]), h.p[k]);
-      store_state<kOut16>(a.out, (s * a.n + (a.reverse ? len - 1 - i : i)) * a.c + c, h);
-    } else if (i < a.n) {
-      State<V> zero;
+    for (int u = 0; u < T; ++u) {
+      const int i = i0 + u;
+      if (i < len) {
 #pragma unroll
-      for (int k = 0; k < kN; ++k) zero.p[k] = fill<kW>(0.f);
-      store_state<kOut16>(a.out, (s * a.n + i) * a.c + c, zero);
+        for (int k = 0; k < kN; ++k)
+          h.p[k] = step<kSig>(gate_of<kSig>(ng[u].p[k]), widen(nx[u].p[k]), h.p[k]);
+        store_state<kOut16>(a.out, row(i) * a.c + c, h);
+      } else if (i < a.n) {
+        State<V> zero;
+#pragma unroll
+        for (int k = 0; k < kN; ++k) zero.p[k] = fill<kW>(0.f);
+        store_state<kOut16>(a.out, (s * a.n + i) * a.c + c, zero);
+      }
     }
   }
   if (a.final_state) store_state<false>(a.final_state, s * a.c + c, h);
@@ -102,11 +118,15 @@ __global__ void __launch_bounds__(kThreads) scan_few_kernel(const Args a) {
 
 template <bool kIn16, bool kOut16, bool kSig>
 Kernel pick(int v, int tokens) {
-  if (v == 4)
-    return tokens == 1 ? scan_few_kernel<kIn16, kOut16, 4, kSig, 1>
-                       : scan_few_kernel<kIn16, kOut16, 4, kSig, kTokens>;
-  return tokens == 1 ? scan_few_kernel<kIn16, kOut16, 1, kSig, 1>
-                     : scan_few_kernel<kIn16, kOut16, 1, kSig, kTokens>;
+  constexpr int kAtOnce = kIn16 ? 8 : 4;
+  if (tokens == 1)
+    return v == 4 ? scan_few_kernel<kIn16, kOut16, 4, kSig, 1, false>
+                  : scan_few_kernel<kIn16, kOut16, 1, kSig, 1, false>;
+  if (tokens <= kTokens)
+    return v == 4 ? scan_few_kernel<kIn16, kOut16, 4, kSig, kTokens, false>
+                  : scan_few_kernel<kIn16, kOut16, 1, kSig, kTokens, false>;
+  return v == 4 ? scan_few_kernel<kIn16, kOut16, 4, kSig, kAtOnce, true>
+                : scan_few_kernel<kIn16, kOut16, 1, kSig, 8, true>;
 }
 template <bool kIn16, bool kOut16>
 Kernel pick(bool sig, int v, int tokens) {

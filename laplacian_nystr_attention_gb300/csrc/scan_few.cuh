@@ -7,7 +7,7 @@ namespace lapl {
 namespace scan {
 namespace few {
 
-constexpr int kTokens = 4;      // the most these kernels take
+constexpr int kTokens = 4;      // read at once
 constexpr int kThreads = 256;   // of a CTA: lanes across the channels, the rest sequences
 
 using Kernel = void (*)(Args);

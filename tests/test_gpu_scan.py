@@ -141,13 +141,15 @@ def test_padding_is_not_read():
 @pytest.mark.parametrize("dtype,out", [("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32"),
                                        ("f32", "bf16")])
 def test_few_tokens(gate, reverse, dtype, out):
-    """One to four tokens and just more; channels by four and not; several sequences a CTA and
+    """One to eight tokens and just more; channels by four and not; several sequences a CTA and
     several CTAs a sequence; lengths of zero."""
-    for N in (1, 2, 3, 4, 5):
+    for N in (1, 2, 3, 4, 5, 8, 9):
         lens = [N, 0, 1, N - 1, N + 3, -2, N]
         for S, C, packed in ((7, 8, 0), (7, 65, 0), (7, 1100, 2200), (7, 12, 30)):
             run(S, N, C, gate, dtype, out, reverse=reverse, lens=lens, packed=packed)
-    run(300, 1, 20, gate, dtype, out, h0=False)
+    info = run(300, 1, 20, gate, dtype, out, h0=False)[1]
+    assert info == {"cluster": 1, "lanes": 8, "threads": 256, "teams": 0}
+    run(700, 32, 360, gate, dtype, out, reverse=reverse, lens=[32, 17, 16, 0, 31] * 140)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
