@@ -567,20 +567,25 @@ scan::Geo few_geometry(const lapl_scan_config& c, int v) {
   return g;
 }
 
-// Few tokens (forward): four channels a thread where every tensor's rows start at multiples of them.
-lapl_status launch_few(lapl_scan_plan* p, scan::Args& a, void* stream, const char* where) {
+// Few tokens: v channels a thread where every tensor's rows start at multiples of them, else one.
+// in, other, states: the tensors in in_dtype, in other_dtype, and of states.
+lapl_status launch_few(lapl_scan_plan* p, bool backward, scan::Args& a, int v,
+                       std::initializer_list<const void*> in,
+                       std::initializer_list<const void*> other, int other_dtype,
+                       std::initializer_list<const void*> states, void* stream, const char* where) {
   const lapl_scan_config& c = p->cfg;
-  const int ib = ops::dtype_bytes(c.in_dtype), ob = ops::dtype_bytes(c.out_dtype);
-  const bool fours = c.channels % 4 == 0 && a.x_stride % 4 == 0 && a.g_stride % 4 == 0 &&
-                     whole({a.x, a.g}, 4 * ib) && whole({a.out}, 4 * ob) &&
-                     whole({a.h0, a.states, a.final_state}, 16);
-  const int v = fours ? 4 : 1;
+  if (c.channels % v || a.x_stride % v || a.g_stride % v ||
+      !whole(in, v * ops::dtype_bytes(c.in_dtype)) ||
+      !whole(other, v * ops::dtype_bytes(other_dtype)) || !whole(states, v * 4))
+    v = 1;
   const scan::Geo& g = a.geo = few_geometry(c, v);
   const int per = scan::few::kThreads >> g.lanes_log2;
   const long long ctas = (long long)((c.sequences - 1) / per + 1) * g.blocks;
-  scan::few::forward(c.in_dtype == LAPL_BF16, c.out_dtype == LAPL_BF16, c.gate == LAPL_GATE_SIGMOID,
-                     v, c.tokens)<<<(unsigned)ctas, scan::few::kThreads, 0,
-                                    static_cast<cudaStream_t>(stream)>>>(a);
+  const bool in16 = c.in_dtype == LAPL_BF16, other16 = other_dtype == LAPL_BF16;
+  const bool sig = c.gate == LAPL_GATE_SIGMOID;
+  const scan::few::Kernel k = backward ? scan::few::backward(in16, other16, sig, v, c.tokens)
+                                       : scan::few::forward(in16, other16, sig, v, c.tokens);
+  k<<<(unsigned)ctas, scan::few::kThreads, 0, static_cast<cudaStream_t>(stream)>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) {
     ops::set_error(p->last_error, e, where);
@@ -684,7 +689,9 @@ lapl_status lapl_scan_forward(lapl_scan_handle p, const void* x, const void* g, 
   a.states = states;
   a.final_state = final_state;
   const int ib = ops::dtype_bytes(c.in_dtype), ob = ops::dtype_bytes(c.out_dtype);
-  if (p->few) return launch_few(p, a, stream, "scan_forward");
+  if (p->few)
+    return launch_few(p, false, a, 4, {x, g}, {out}, c.out_dtype, {h0, states, final_state}, stream,
+                      "scan_forward");
   if (p->fwd.pick.kernel) {
     const int pair = c.in_dtype == LAPL_BF16 ? 2 : 1;
     a.fine = !coarse(x, a.x_stride, ib) || !coarse(g, a.g_stride, ib);
@@ -728,6 +735,9 @@ lapl_status lapl_scan_backward(lapl_scan_handle p, const void* x, const void* g,
   a.dx = dx;
   a.dg = dg;
   a.dh0 = dh0;
+  if (c.tokens <= scan::few::kBackwardTokens)
+    return launch_few(p, true, a, c.tokens <= scan::few::kTokens ? 4 : 2, {x, g}, {dout, dx, dg},
+                      c.grad_dtype, {states, dfinal, dh0}, stream, "scan_backward");
   if (p->bwd.pick.kernel) {
     const int pair = c.in_dtype == LAPL_BF16 ? 2 : 1;
     a.fine = !coarse(x, a.x_stride, ib) || !coarse(g, a.g_stride, ib);

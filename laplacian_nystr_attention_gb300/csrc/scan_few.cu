@@ -5,8 +5,9 @@
 // elements) and goes through the steps with the state in registers: of up to four tokens it reads all
 // at once, of more some at a time with the next ones on their way.  128 x 1 x 4096 bf16 takes 2.4 us where
 // the kernel for longer sequences, 32 threads a CTA and 16 tokens a thread, takes 15.8; 64 x 1 x 512 1.7
-// and 2.9; 20000 x 2 x 512 34 (89% of the copy's rate) and 317; 64 x 8 x 4096 4.1 and 9.8.  What bounds
-// it is the launch, then the bytes.
+// and 2.9; 20000 x 2 x 512 34 (89% of the copy's rate) and 317; 64 x 8 x 4096 4.1 and 9.8.  The backward
+// of up to eight tokens holds them all: 64 x 1 x 4096 2.0 and 10.7 us, 64 x 8 x 4096 6.9 and 13.2.  What
+// bounds them is the launch, then the bytes.
 #include "scan_few.cuh"
 
 namespace lapl {
@@ -14,10 +15,10 @@ namespace scan {
 namespace few {
 namespace {
 
-// V channels of a token: pairs of them, or one.
+// V channels of a token, 4, 2 or 1: pairs of them, or one.
 template <int V>
 struct Parts {
-  static constexpr int kW = V == 4 ? 2 : 1, kN = V / kW;
+  static constexpr int kW = V >= 2 ? 2 : 1, kN = V / kW;
 };
 template <int V>
 struct State {
@@ -31,8 +32,8 @@ template <bool k16, int V>
 __device__ __forceinline__ Token<k16, V> load_token(const void* base, long long e) {
   Token<k16, V> t;
   const char* q = reinterpret_cast<const char*>(base) + e * (k16 ? 2 : 4);
-  if constexpr (V == 1) {
-    t.p[0] = load_raw<k16, 1>(q);
+  if constexpr (V <= 2) {
+    t.p[0] = load_raw<k16, V>(q);
   } else if constexpr (k16) {
     const uint2 w = *reinterpret_cast<const uint2*>(q);
     t.p[0].w[0] = w.x;
@@ -47,7 +48,7 @@ __device__ __forceinline__ Token<k16, V> load_token(const void* base, long long 
 template <bool k16, int V>
 __device__ __forceinline__ void store_state(void* base, long long e, const State<V>& h) {
   char* q = reinterpret_cast<char*>(base) + e * (k16 ? 2 : 4);
-  if constexpr (V == 1) {
+  if constexpr (V <= 2) {
     store_vec<k16>(q, h.p[0]);
   } else if constexpr (k16) {
     *reinterpret_cast<uint2*>(q) = make_uint2(ops::pack_bf16(h.p[0].f[0], h.p[0].f[1]),
@@ -58,35 +59,60 @@ __device__ __forceinline__ void store_state(void* base, long long e, const State
   }
 }
 
+// What a thread is: sequence, first channel, tokens of the sequence.
+template <int V>
+struct Spot {
+  long long s;
+  int c, len;
+  bool on;
+  __device__ __forceinline__ explicit Spot(const Args& a) {
+    const int unit = blockIdx.x / a.geo.blocks, block = blockIdx.x - unit * a.geo.blocks;
+    s = (long long)unit * (kThreads >> a.geo.lanes_log2) + (threadIdx.x >> a.geo.lanes_log2);
+    c = (block * a.geo.lanes + ((int)threadIdx.x & (a.geo.lanes - 1))) * V;
+    on = s < a.sequences && c < a.c;
+    len = on && a.lengths ? max(0, min(a.n, a.lengths[s])) : a.n;
+  }
+  // Row of the i-th token in processing order.
+  __device__ __forceinline__ long long row(const Args& a, int i) const {
+    return s * a.n + (a.reverse ? len - 1 - i : i);
+  }
+};
+template <int V>
+__device__ __forceinline__ State<V> zeros() {
+  State<V> h;
+#pragma unroll
+  for (int k = 0; k < Parts<V>::kN; ++k) h.p[k] = fill<Parts<V>::kW>(0.f);
+  return h;
+}
+template <int V>
+__device__ __forceinline__ State<V> load_state(const float* base, long long e) {
+  const Token<false, V> t = load_token<false, V>(base, e);
+  State<V> h;
+#pragma unroll
+  for (int k = 0; k < Parts<V>::kN; ++k) h.p[k] = widen(t.p[k]);
+  return h;
+}
+
 // T: tokens at a time; kMore: and the next T on their way while those are worked on.
 template <bool kIn16, bool kOut16, int V, bool kSig, int T, bool kMore>
 __global__ void __launch_bounds__(kThreads) scan_few_kernel(const Args a) {
-  constexpr int kW = Parts<V>::kW, kN = Parts<V>::kN;
-  const int unit = blockIdx.x / a.geo.blocks, block = blockIdx.x - unit * a.geo.blocks;
-  const long long s =
-      (long long)unit * (kThreads >> a.geo.lanes_log2) + (threadIdx.x >> a.geo.lanes_log2);
-  const int c = (block * a.geo.lanes + ((int)threadIdx.x & (a.geo.lanes - 1))) * V;
-  if (s >= a.sequences || c >= a.c) return;
-  const int len = a.lengths ? max(0, min(a.n, a.lengths[s])) : a.n;
-  State<V> h;
-#pragma unroll
-  for (int k = 0; k < kN; ++k) h.p[k] = fill<kW>(0.f);
-  auto row = [&](int i) { return s * a.n + (a.reverse ? len - 1 - i : i); };
+  constexpr int kN = Parts<V>::kN;
+  const Spot<V> spot(a);
+  if (!spot.on) return;
+  const long long s = spot.s;
+  const int c = spot.c, len = spot.len;
+  State<V> h = zeros<V>();
   Token<kIn16, V> x[T], g[T];
   auto fetch = [&](int i0) {
 #pragma unroll
     for (int u = 0; u < T; ++u)
       if (i0 + u < len) {
-        g[u] = load_token<kIn16, V>(a.g, row(i0 + u) * a.g_stride + c);
-        x[u] = load_token<kIn16, V>(a.x, row(i0 + u) * a.x_stride + c);
+        g[u] = load_token<kIn16, V>(a.g, spot.row(a, i0 + u) * a.g_stride + c);
+        x[u] = load_token<kIn16, V>(a.x, spot.row(a, i0 + u) * a.x_stride + c);
       }
   };
   fetch(0);
-  if (a.h0) {
-    const Token<false, V> t = load_token<false, V>(a.h0, s * a.c + c);
-#pragma unroll
-    for (int k = 0; k < kN; ++k) h.p[k] = widen(t.p[k]);
-  }
+  if (a.h0) h = load_state<V>(a.h0, s * a.c + c);
   for (int i0 = 0; i0 < (kMore ? a.n : 1); i0 += T) {
     Token<kIn16, V> nx[T], ng[T];
 #pragma unroll
@@ -104,16 +130,79 @@ __global__ void __launch_bounds__(kThreads) scan_few_kernel(const Args a) {
 #pragma unroll
         for (int k = 0; k < kN; ++k)
           h.p[k] = step<kSig>(gate_of<kSig>(ng[u].p[k]), widen(nx[u].p[k]), h.p[k]);
-        store_state<kOut16>(a.out, row(i) * a.c + c, h);
+        store_state<kOut16>(a.out, spot.row(a, i) * a.c + c, h);
       } else if (i < a.n) {
-        State<V> zero;
-#pragma unroll
-        for (int k = 0; k < kN; ++k) zero.p[k] = fill<kW>(0.f);
-        store_state<kOut16>(a.out, (s * a.n + i) * a.c + c, zero);
+        store_state<kOut16>(a.out, (s * a.n + i) * a.c + c, zeros<V>());
       }
     }
   }
   if (a.final_state) store_state<false>(a.final_state, s * a.c + c, h);
+}
+
+// Backward of up to T tokens, all in registers.
+template <bool kIn16, bool kGrad16, int V, bool kSig, int T>
+__global__ void __launch_bounds__(kThreads) scan_few_backward_kernel(const Args a) {
+  constexpr int kN = Parts<V>::kN;
+  const Spot<V> spot(a);
+  if (!spot.on) return;
+  const long long s = spot.s;
+  const int c = spot.c, len = spot.len;
+  Token<kIn16, V> x[T], g[T];
+  Token<kGrad16, V> dh[T];
+#pragma unroll
+  for (int i = 0; i < T; ++i)
+    if (i < len) {
+      const long long row = spot.row(a, i);
+      g[i] = load_token<kIn16, V>(a.g, row * a.g_stride + c);
+      x[i] = load_token<kIn16, V>(a.x, row * a.x_stride + c);
+      dh[i] = load_token<kGrad16, V>(a.dout, row * a.c + c);
+    }
+  State<V> h = load_state<V>(a.states, s * a.c + c), E = zeros<V>();   // one kept state a sequence
+  if (a.dfinal) E = load_state<V>(a.dfinal, s * a.c + c);
+  State<V> gate[T], slope[T];
+#pragma unroll
+  for (int i = 0; i < T; ++i)
+    if (i < len)
+#pragma unroll
+      for (int k = 0; k < kN; ++k) {
+        const auto in = widen(x[i].p[k]);
+        gate[i].p[k] = gate_of<kSig>(g[i].p[k]);
+        slope[i].p[k] = kSig ? sub(in, h.p[k]) : h.p[k];
+        h.p[k] = step<kSig>(gate[i].p[k], in, h.p[k]);
+      }
+#pragma unroll
+  for (int i = T - 1; i >= 0; --i) {
+    if (i >= a.n) continue;
+    State<V> dx = zeros<V>(), dg = zeros<V>();
+    if (i < len)
+#pragma unroll
+      for (int k = 0; k < kN; ++k) {
+        const auto D = add(widen(dh[i].p[k]), E.p[k]);
+        E.p[k] = decayed<kSig>(gate[i].p[k], D);
+        step_gradients<kSig>(gate[i].p[k], slope[i].p[k], D, E.p[k], dx.p[k], dg.p[k]);
+      }
+    const long long row = i < len ? spot.row(a, i) : s * a.n + i;
+    store_state<kGrad16>(a.dx, row * a.x_stride + c, dx);
+    store_state<kGrad16>(a.dg, row * a.g_stride + c, dg);
+  }
+  if (a.dh0) store_state<false>(a.dh0, s * a.c + c, E);
+}
+
+template <bool kIn16, bool kGrad16, bool kSig>
+Kernel pick_backward(int v, int tokens) {
+  if (tokens == 1)
+    return v == 4 ? scan_few_backward_kernel<kIn16, kGrad16, 4, kSig, 1>
+                  : scan_few_backward_kernel<kIn16, kGrad16, 1, kSig, 1>;
+  if (tokens <= kTokens)
+    return v == 4 ? scan_few_backward_kernel<kIn16, kGrad16, 4, kSig, kTokens>
+                  : scan_few_backward_kernel<kIn16, kGrad16, 1, kSig, kTokens>;
+  return v == 2 ? scan_few_backward_kernel<kIn16, kGrad16, 2, kSig, kBackwardTokens>
+                : scan_few_backward_kernel<kIn16, kGrad16, 1, kSig, kBackwardTokens>;
+}
+template <bool kIn16, bool kGrad16>
+Kernel pick_backward(bool sig, int v, int tokens) {
+  return sig ? pick_backward<kIn16, kGrad16, true>(v, tokens)
+             : pick_backward<kIn16, kGrad16, false>(v, tokens);
 }
 
 template <bool kIn16, bool kOut16, bool kSig>
@@ -138,6 +227,12 @@ Kernel pick(bool sig, int v, int tokens) {
 Kernel forward(bool in16, bool out16, bool sig, int v, int tokens) {
   return in16 ? (out16 ? pick<true, true>(sig, v, tokens) : pick<true, false>(sig, v, tokens))
               : (out16 ? pick<false, true>(sig, v, tokens) : pick<false, false>(sig, v, tokens));
+}
+Kernel backward(bool in16, bool grad16, bool sig, int v, int tokens) {
+  return in16 ? (grad16 ? pick_backward<true, true>(sig, v, tokens)
+                        : pick_backward<true, false>(sig, v, tokens))
+              : (grad16 ? pick_backward<false, true>(sig, v, tokens)
+                        : pick_backward<false, false>(sig, v, tokens));
 }
 
 }  // namespace few

@@ -146,7 +146,7 @@ def test_few_tokens(gate, reverse, dtype, out):
     for N in (1, 2, 3, 4, 5, 8, 9):
         lens = [N, 0, 1, N - 1, N + 3, -2, N]
         for S, C, packed in ((7, 8, 0), (7, 65, 0), (7, 1100, 2200), (7, 12, 30)):
-            run(S, N, C, gate, dtype, out, reverse=reverse, lens=lens, packed=packed)
+            run(S, N, C, gate, dtype, out, out, reverse=reverse, lens=lens, packed=packed)
     info = run(300, 1, 20, gate, dtype, out, h0=False)[1]
     assert info == {"cluster": 1, "lanes": 8, "threads": 256, "teams": 0}
     run(700, 32, 360, gate, dtype, out, reverse=reverse, lens=[32, 17, 16, 0, 31] * 140)
@@ -154,21 +154,30 @@ def test_few_tokens(gate, reverse, dtype, out):
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_few_tokens_misaligned(dtype):
-    """Every pointer one element off 16 bytes, the state in place."""
+    """Every pointer one element off 16 bytes, the states in place."""
     import laplacian_nystr_attention_gb300 as lna
     S, N, C = 3, 2, 64
-    x, g, h0, _, _ = make(S, N, C, "sigmoid", dtype, seed=4)
-    want = ref.scan(x, g, "sigmoid", h0)
+    x, g, h0, dout, dfinal = make(S, N, C, "sigmoid", dtype, seed=4)
+    dout = ref.rounded(dout, dtype)
+    want = ref.scan(x, g, "sigmoid", h0, dout=dout, dfinal=dfinal)
 
     def off(a, kind):
         t = torch.empty(a.size + 1, dtype=TYPES[kind], device="cuda")[1:].view(a.shape)
         return t.copy_(dev(a, kind))
 
     state, out = off(h0, "f32"), off(x, dtype)
-    plan = lna.GatedScan(lna.make_scan_config(S, N, C, in_dtype=dtype, out_dtype=dtype))
-    plan.forward(off(x, dtype), off(g, dtype), h0=state, final=state, out=out)
+    plan = lna.GatedScan(lna.make_scan_config(S, N, C, in_dtype=dtype, out_dtype=dtype,
+                                              grad_dtype=dtype))
+    states = off(np.zeros(plan.states_shape), "f32")
+    plan.forward(off(x, dtype), off(g, dtype), h0=state, states=states, final=state, out=out)
     ref.check("h", out, want["h"], dtype)
     ref.check("final", state, want["final"])
+    last, dx, dg = off(dfinal, "f32"), off(x, dtype), off(g, dtype)
+    plan.backward(off(x, dtype), off(g, dtype), states, off(dout, dtype), dfinal=last,
+                  grads={"dx": dx, "dg": dg, "dh0": last})
+    ref.check("dx", dx, want["dx"], dtype)
+    ref.check("dg", dg, want["dg"], dtype)
+    ref.check("dh0", last, want["dh0"])
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
