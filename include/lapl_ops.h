@@ -105,8 +105,9 @@ lapl_status lapl_scan_device_errors(lapl_scan_handle h, void* stream, unsigned* 
 
 /*
  * Fault injection, for testing that report: wait_ns: the bound of the waits of this plan's calls
- * from now on (0: one second); skip_last = 1: the last round's maps are never sent, so that the
- * waits for them run out (kernels for long sequences only: plan_info teams > 0); 0: normal.
+ * from now on (0: one second); skip_last = n > 0: the maps of the n-th last round (or of the first,
+ * where there are fewer) are never sent, so that the waits for them run out (kernels for long
+ * sequences only: plan_info teams > 0); 0: normal.
  */
 lapl_status lapl_scan_set_fault_injection(lapl_scan_handle h, unsigned long long wait_ns,
                                           int skip_last);

@@ -603,7 +603,7 @@ scan::Args base_args(const lapl_scan_plan& p) {
   a.chunks = (c.tokens + scan::kT - 1) / scan::kT;
   a.reverse = c.reverse;
   a.wait_ns = p.wait_ns;
-  a.skip_last = p.skip_last != 0;
+  a.skip_last = p.skip_last;
   a.x_stride = c.x_stride ? c.x_stride : c.channels;
   a.g_stride = c.g_stride ? c.g_stride : c.channels;
   return a;
@@ -793,7 +793,7 @@ lapl_status lapl_scan_device_errors(lapl_scan_handle p, void* stream, unsigned* 
 
 lapl_status lapl_scan_set_fault_injection(lapl_scan_handle p, unsigned long long wait_ns,
                                           int skip_last) {
-  if (!p || skip_last < 0 || skip_last > 1) return LAPL_ERR_INVALID_ARG;
+  if (!p || skip_last < 0) return LAPL_ERR_INVALID_ARG;
   p->wait_ns = wait_ns ? wait_ns : kWaitNs;
   p->skip_last = skip_last;
   return LAPL_OK;

@@ -32,9 +32,10 @@ struct Args {
   float* dh0;
   long long x_stride, g_stride;
   int sequences, n, c, chunks, reverse;
-  // scan_pipe.cuh: x and g, and dout, copied in less than 16 bytes; the bound of a wait, and whether
-  // the last round's maps are not sent (fault injection for tests).
-  bool fine, fine_dout, skip_last;
+  // scan_pipe.cuh: x and g, and dout, copied in less than 16 bytes; the bound of a wait, and n > 0
+  // where the n-th last round's maps are not sent (fault injection for tests).
+  bool fine, fine_dout;
+  int skip_last;
   unsigned long long wait_ns;
   Geo geo;
 };

@@ -33,8 +33,11 @@
 // another may be at r + T and send up to r + 2T - 1: maps of 2T rounds may be there at once.
 //
 // The receiving warp's wait for the cluster's maps is bounded (one second): when it gives up it sets
-// kErrBitScan in the device error word and goes on without waiting, so that the kernel ends; its
-// outputs are then undefined.  No CTA of a cluster leaves before all have come to their end.
+// kErrBitScan in the device error word and goes on without waiting for maps, so that the kernel ends;
+// its outputs are then undefined.  It still keeps step with its own CTA: its arrival for a round at the
+// barrier of the team's states must not come before the team has left that barrier's round before, which
+// the round's maps tell where they have come and the sending warp's arrival at a barrier of their own
+// where they have not.  No CTA of a cluster leaves before all have come to their end.
 #pragma once
 
 #include "scan.cuh"
@@ -158,25 +161,39 @@ __device__ __forceinline__ Raw<k16, V> read_raw(unsigned at) {
   return r;
 }
 
+__device__ __forceinline__ unsigned long long nanoseconds() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
 // Until the phase of the given parity is complete, or false after `bound` ns.
 __device__ __forceinline__ bool wait_phase(unsigned bar, unsigned parity, unsigned long long bound) {
+  const unsigned at_once = (unsigned)min(bound, 1000000000ull);   // a look may last that long itself
   auto done = [&] {
     unsigned d;
     asm volatile("{\n\t.reg .pred p;\n\t"
-                 "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(d) : "r"(bar), "r"(parity) : "memory");
+                 "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(d) : "r"(bar), "r"(parity), "r"(at_once)
+                 : "memory");
     return d != 0;
   };
-  auto now = [] {
-    unsigned long long t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-  };
   if (done()) return true;
-  const unsigned long long t0 = now();
+  const unsigned long long t0 = nanoseconds();
   while (!done())
-    if (now() - t0 > bound) return false;
+    if (nanoseconds() - t0 > bound) return false;
   return true;
+}
+
+// Named barriers: a team's runs are written; the states that enter its tile are; the sending warp has
+// seen the runs.  (0 is __syncthreads'; there are 16.)
+template <int kTeams>
+__device__ __forceinline__ int runs_bar(int team) { return 1 + team; }
+template <int kTeams>
+__device__ __forceinline__ int states_bar(int team) { return 1 + kTeams + team; }
+template <int kTeams>
+__device__ __forceinline__ int seen_bar(int team) {
+  static_assert(1 + 3 * kTeams <= 16, "named barriers");
+  return 1 + 2 * kTeams + team;
 }
 
 // What a CTA works on.
@@ -249,10 +266,13 @@ __device__ __forceinline__ void send_chain(const Args& a, const Unit<kLanes, V>&
   constexpr int kBy = (kDown ? -kLanes : kLanes) * kMap;   // from a lane's run to its next
   const int lane = threadIdx.x & 31, pos = lane & (kLanes - 1), set = lane / kLanes;
   const int first = (kDown ? kRuns - 1 - set * kWarps : set * kWarps) * kLanes + pos;
+  // Fault injection: a round whose maps are not sent.
+  const int lost_round = a.skip_last ? max(0, a.geo.tiles - a.skip_last) : -1;
   for (int r = 0; r < a.geo.tiles; ++r) {
     const int team = r % kTeams, slot = r % slots_of(kTeams);
     const unsigned runs = smem + l.runs + (team * kWarps * 32 + first) * kMap;
-    bar_sync(1 + team, kWarps * 32 + 32);      // the team's runs are written
+    bar_sync(runs_bar<kTeams>(team), kWarps * 32 + 32);
+    bar_arrive(seen_bar<kTeams>(team), 64);
     Map<V> m[kWarps];
 #pragma unroll
     for (int k = 0; k < kWarps; ++k) get_map(runs + k * kBy, m[k]);
@@ -277,7 +297,7 @@ __device__ __forceinline__ void send_chain(const Args& a, const Unit<kLanes, V>&
       all = {shuffle(all.a, 32 - kLanes + pos), shuffle(all.b, 32 - kLanes + pos)};
     }
     const unsigned to = smem + l.slots + ((slot * u.cluster + u.rank) * kLanes + pos) * kMap;
-    if (!(a.skip_last && r == a.geo.tiles - 1))
+    if (r != lost_round)
       for (int k = set; k < u.cluster; k += kSets)
         send_map(at_rank(to, k), at_rank(bars + slot * 8, k), all);
 #pragma unroll
@@ -286,7 +306,7 @@ __device__ __forceinline__ void send_chain(const Args& a, const Unit<kLanes, V>&
       before.b = fma(m[k].a, before.b, m[k].b);
       before.a = mul(m[k].a, before.a);
     }
-    bar_arrive(1 + kTeams + team, kWarps * 32 + 64);
+    bar_arrive(states_bar<kTeams>(team), kWarps * 32 + 64);
   }
 }
 
@@ -300,9 +320,10 @@ __device__ __forceinline__ Vec<V> first_state(const Args& a, const Unit<kLanes, 
                                       : fill<V>(0.f);
 }
 
-// The receiving warp: the state that enters every round's tile, from the tiles of the cluster.
+// The receiving warp: the state that enters every round's tile, from the tiles of the cluster.  True if
+// a wait gave up.
 template <int kLanes, int V, int kTeams, int kWarps, bool kDown>
-__device__ __forceinline__ void receive_chain(const Args& a, const Unit<kLanes, V>& u, unsigned smem,
+__device__ __forceinline__ bool receive_chain(const Args& a, const Unit<kLanes, V>& u, unsigned smem,
                                               const Layout& l, unsigned bars, Vec<V> carry,
                                               float* finish, unsigned* err) {
   constexpr int kMap = 2 * V * 4;
@@ -312,11 +333,20 @@ __device__ __forceinline__ void receive_chain(const Args& a, const Unit<kLanes, 
   bool lost = false;
   for (int r = 0; r < a.geo.tiles; ++r) {
     const int team = r % kTeams, slot = r % slots_of(kTeams);
-    const unsigned bar = bars + slot * 8;
-    if (lane == 0)
-      asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
-                   ::"r"(bar), "r"(u.cluster * kLanes * kMap) : "memory");
-    if (!lost && !wait_phase(bar, (r / slots_of(kTeams)) & 1, a.wait_ns)) lost = true;
+    const unsigned bar = bars + slot * 8, bytes = u.cluster * kLanes * kMap;
+    if (!lost) {
+      if (lane == 0)
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;"
+                     ::"r"(bar), "r"(bytes) : "memory");
+      lost = __any_sync(0xffffffffu, !wait_phase(bar, (r / slots_of(kTeams)) & 1, a.wait_ns));
+    } else if (lane == 0) {
+      // The slot's phase may have had its one arrival; the bytes that still come are counted off.
+      asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;"
+                   ::"r"(bar), "r"(bytes) : "memory");
+    }
+    // The sending warp has come by this round.  The round's maps, this CTA's among them, say so.
+    if (lost) bar_sync(seen_bar<kTeams>(team), 64);
+    else bar_arrive(seen_bar<kTeams>(team), 64);
     const unsigned slots = smem + l.slots + (slot * u.cluster * kLanes + pos) * kMap;
     Vec<V> enter = carry;
     for (int k = 0; k < u.cluster; ++k) {
@@ -327,10 +357,11 @@ __device__ __forceinline__ void receive_chain(const Args& a, const Unit<kLanes, 
       carry = fma(m.a, carry, m.b);
     }
     if (lane < kLanes) put_state(smem + l.enters + (team * kLanes + pos) * (V * 4), enter);
-    bar_arrive(1 + kTeams + team, kWarps * 32 + 64);
+    bar_arrive(states_bar<kTeams>(team), kWarps * 32 + 64);
   }
   if (lost && lane == 0) atomicOr(err, kErrBitScan);
   if (finish && on && u.rank == 0) store_vec<false>(finish + u.s * a.c + c, carry);
+  return lost;
 }
 
 __device__ __forceinline__ void start_barriers(unsigned bars, int slots) {
@@ -342,6 +373,15 @@ __device__ __forceinline__ void start_barriers(unsigned bars, int slots) {
 }
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// The end of a CTA.  One that gave up a wait may still be sent maps: all are on their way once the
+// cluster has met, and it stays for 0.1 ms more (at most 10,000 looks at the clock), far longer than
+// they take.
+__device__ __forceinline__ void leave(bool lost) {
+  cluster_sync();
+  if (!lost) return;
+  const unsigned long long t0 = nanoseconds();
+  for (int k = 0; k < 10000 && nanoseconds() - t0 < 100000ull; ++k) __nanosleep(100);
 }
 
 template <bool kIn16, bool kOut16, bool kSig, int kLanes, int kStages, int kTeams, int kWarps>
@@ -359,10 +399,11 @@ scan_forward_pipe_kernel(const Args a, unsigned* err) {
   const Vec<V> start = first_state(a, unit, warp == kTeams * kWarps + 1, a.h0);
   start_barriers(bars, slots_of(kTeams));
   cluster_sync();
+  bool lost = false;   // in the receiving warp
   if (warp == kTeams * kWarps) {
     send_chain<kLanes, V, kTeams, kWarps, false>(a, unit, smem, l, bars);
   } else if (warp == kTeams * kWarps + 1) {
-    receive_chain<kLanes, V, kTeams, kWarps, false>(a, unit, smem, l, bars, start, a.final_state, err);
+    lost = receive_chain<kLanes, V, kTeams, kWarps, false>(a, unit, smem, l, bars, start, a.final_state, err);
   } else {
     const int team = warp / kWarps, wt = warp - team * kWarps;   // place in the team
     const int run = wt * (32 / kLanes) + lane / kLanes;
@@ -409,8 +450,8 @@ scan_forward_pipe_kernel(const Args a, unsigned* err) {
         m.b = step<kSig>(gate[k], widen(read_raw<kIn16, V>(from + T::kWarp + k * T::kRow)), m.b);
       }
       put_map(smem + l.runs + (team * kWarps * 32 + wt * 32 + lane) * (2 * V * 4), m);
-      bar_arrive(1 + team, kWarps * 32 + 32);
-      bar_sync(1 + kTeams + team, kWarps * 32 + 64);
+      bar_arrive(runs_bar<kTeams>(team), kWarps * 32 + 32);
+      bar_sync(states_bar<kTeams>(team), kWarps * 32 + 64);
       Vec<V> h;
       get_state(smem + l.enters + (team * kLanes + pos) * (V * 4), h);
       get_map(smem + l.runs + (team * kWarps * 32 + wt * 32 + lane) * (2 * V * 4), m);
@@ -446,7 +487,7 @@ scan_forward_pipe_kernel(const Args a, unsigned* err) {
     }
     copies_left<0>();
   }
-  cluster_sync();
+  leave(lost);
 }
 
 template <bool kIn16, bool kGrad16, bool kSig, int kLanes, int kStages, int kTeams, int kWarps>
@@ -465,10 +506,11 @@ scan_backward_pipe_kernel(const Args a, unsigned* err) {
   const Vec<V> start = first_state(a, unit, warp == kTeams * kWarps + 1, a.dfinal);
   start_barriers(bars, slots_of(kTeams));
   cluster_sync();
+  bool lost = false;   // in the receiving warp
   if (warp == kTeams * kWarps) {
     send_chain<kLanes, V, kTeams, kWarps, true>(a, unit, smem, l, bars);
   } else if (warp == kTeams * kWarps + 1) {
-    receive_chain<kLanes, V, kTeams, kWarps, true>(a, unit, smem, l, bars, start, a.dh0, err);
+    lost = receive_chain<kLanes, V, kTeams, kWarps, true>(a, unit, smem, l, bars, start, a.dh0, err);
   } else {
     const int team = warp / kWarps, wt = warp - team * kWarps;
     const int run = wt * (32 / kLanes) + lane / kLanes;
@@ -526,7 +568,7 @@ scan_backward_pipe_kernel(const Args a, unsigned* err) {
         m.b = decayed<kSig>(gate[k], add(widen(read_raw<kGrad16, V>(from + my_grad + k * TG::kRow)), m.b));
       }
       put_map(smem + l.runs + (team * kWarps * 32 + wt * 32 + lane) * (2 * V * 4), m);
-      bar_arrive(1 + team, kWarps * 32 + 32);
+      bar_arrive(runs_bar<kTeams>(team), kWarps * 32 + 32);
       // The slope of a step in its decay, x_i - h_{i-1} (with -z: the signs cancel) or h_{i-1}, while
       // the chain goes on.
 #pragma unroll
@@ -535,7 +577,7 @@ scan_backward_pipe_kernel(const Args a, unsigned* err) {
         slope[k] = kSig ? sub(x, h) : h;
         h = step<kSig>(gate[k], x, h);
       }
-      bar_sync(1 + kTeams + team, kWarps * 32 + 64);
+      bar_sync(states_bar<kTeams>(team), kWarps * 32 + 64);
       Vec<V> E;
       get_state(smem + l.enters + (team * kLanes + pos) * (V * 4), E);
       get_map(smem + l.runs + (team * kWarps * 32 + wt * 32 + lane) * (2 * V * 4), m);
@@ -570,7 +612,7 @@ scan_backward_pipe_kernel(const Args a, unsigned* err) {
     }
     copies_left<0>();
   }
-  cluster_sync();
+  leave(lost);
 }
 
 using PipeKernel = void (*)(Args, unsigned*);
