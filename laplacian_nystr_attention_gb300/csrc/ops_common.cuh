@@ -62,6 +62,12 @@ __device__ __forceinline__ Vec<1> fma(const Vec<1>& a, const Vec<1>& b, const Ve
   return {{fmaf(a.f[0], b.f[0], c.f[0])}};
 }
 __device__ __forceinline__ Vec<1> mul(const Vec<1>& a, const Vec<1>& b) { return {{a.f[0] * b.f[0]}}; }
+// Products below the normal range are zero.
+__device__ __forceinline__ Vec<1> mul_flush(const Vec<1>& a, const Vec<1>& b) {
+  Vec<1> d;
+  asm("mul.rn.ftz.f32 %0, %1, %2;" : "=f"(d.f[0]) : "f"(a.f[0]), "f"(b.f[0]));
+  return d;
+}
 __device__ __forceinline__ Vec<1> add(const Vec<1>& a, const Vec<1>& b) { return {{a.f[0] + b.f[0]}}; }
 __device__ __forceinline__ Vec<1> sub(const Vec<1>& a, const Vec<1>& b) { return {{a.f[0] - b.f[0]}}; }
 #define LAPL_PACKED(name, op)                                                              \
@@ -74,6 +80,7 @@ __device__ __forceinline__ Vec<1> sub(const Vec<1>& a, const Vec<1>& b) { return
     return d;                                                                                   \
   }
 LAPL_PACKED(mul, "mul.rn")
+LAPL_PACKED(mul_flush, "mul.rn.ftz")
 LAPL_PACKED(add, "add.rn")
 LAPL_PACKED(sub, "sub.rn")
 #undef LAPL_PACKED

@@ -23,9 +23,11 @@
 // backward, of which 7.4 and 12.7 are bytes), odd bf16 channel counts, and rows of odd lengths where
 // they are many (16 x 4096 x 333 fp32: 64 us of 39).
 //
-// The sigmoid gate's steps are written h + z (x - h) with z = 1 - a = 1 / (1 + exp(g)) computed as
-// such: near a = 1 the rounding of a would be a relative error of z of 2^-24 / z, and that error
-// compounds over the 1 / z tokens the state remembers.
+// The sigmoid gate's a and z = 1 - a are computed each for itself: neither is accurate as 1 less the
+// other where it is small.  Near a = 1 the rounding of a is a relative error of z of 2^-24 / z, and that
+// error compounds over the 1 / z tokens the state remembers; what crosses from run to run goes by
+// 1 - A, summed as such (scan.cuh).  Of the two a thread's registers have room for one: between its two
+// walks z x, or in the backward z, waits in shared memory.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -43,10 +45,27 @@ constexpr int kThreads = 256;
 constexpr int kMaxCluster = 16;
 constexpr int kMaxChannels = 64;      // channels of a tile: 32 lanes x 2
 
+// In dynamic shared memory: maps of the runs, by round parity ([2][threads V]); of the cluster's tiles
+// ([2][kMaxCluster][kMaxChannels]); and with the sigmoid gate what a thread keeps of each token from
+// its first walk to the second ([kT][threads] of V values).
+template <int V, bool kCluster>
 struct Shared {
-  float2 run[2][kThreads * 2];                          // maps of the runs, by round parity
-  float2 tile[2][kMaxCluster][kMaxChannels];            // maps of the cluster's tiles
+  unsigned char* base;
+  __device__ __forceinline__ float2* run(int parity) const {
+    return reinterpret_cast<float2*>(base) + parity * (int)blockDim.x * V;
+  }
+  __device__ __forceinline__ float2* tile(int parity, int rank) const {
+    return run(2) + (parity * kMaxCluster + rank) * kMaxChannels;
+  }
+  __device__ __forceinline__ Vec<V>* kept() const {
+    return reinterpret_cast<Vec<V>*>(run(2) + (kCluster ? 2 * kMaxCluster * kMaxChannels : 0)) +
+           threadIdx.x;
+  }
 };
+constexpr unsigned shared_bytes(int threads, int v, bool cluster, bool sig) {
+  return 8u * (2 * threads * v + (cluster ? 2 * kMaxCluster * kMaxChannels : 0)) +
+         (sig ? 4u * v * kT * threads : 0u);
+}
 
 // What a thread is: sequence, channels, place along the tokens.
 struct Place {
@@ -73,15 +92,15 @@ __device__ __forceinline__ Place place_of(const Args& a) {
 // From the run map (A, B) of every thread: the value that enters this thread's run, and `carry`
 // moved past the whole round.  kDown: runs and CTAs in descending order.
 template <int V, bool kCluster, bool kDown>
-__device__ __forceinline__ void exchange(Shared& sm, int parity, const Place& p, int lanes,
+__device__ __forceinline__ void exchange(const Shared<V, kCluster>& sm, int parity, const Place& p, int lanes,
                                          int cluster, const Vec<V>& A, const Vec<V>& B,
                                          Vec<V>& carry, Vec<V>& enter) {
   const int cpb = lanes * V, groups = p.groups;
 #pragma unroll
   for (int v = 0; v < V; ++v)
-    sm.run[parity][p.group * cpb + p.lane * V + v] = make_float2(A.f[v], B.f[v]);
+    sm.run(parity)[p.group * cpb + p.lane * V + v] = make_float2(A.f[v], B.f[v]);
   __syncthreads();
-  const float2* runs = &sm.run[parity][(kDown ? (groups - 1) * cpb : 0) + p.lane * V];
+  const float2* runs = sm.run(parity) + (kDown ? (groups - 1) * cpb : 0) + p.lane * V;
   const int by = kDown ? -cpb : cpb;
   const int mine = kDown ? groups - 1 - p.group : p.group;   // runs before this one
   if constexpr (!kCluster) {
@@ -96,14 +115,14 @@ __device__ __forceinline__ void exchange(Shared& sm, int parity, const Place& p,
   } else {
     // One thread a channel composes the CTA's runs and hands the map to every CTA of the cluster.
     if ((int)threadIdx.x < cpb) {
-      const float2* q = &sm.run[parity][(kDown ? (groups - 1) * cpb : 0) + threadIdx.x];
+      const float2* q = sm.run(parity) + (kDown ? (groups - 1) * cpb : 0) + threadIdx.x;
       float ta = 1.f, tb = 0.f;
 #pragma unroll 4
       for (int k = 0; k < groups; ++k, q += by) {
         tb = fmaf(q->x, tb, q->y);
         ta *= q->x;
       }
-      float2* to = &sm.tile[parity][p.rank][threadIdx.x];
+      float2* to = sm.tile(parity, p.rank) + threadIdx.x;
       for (int r = 0; r < cluster; ++r)
         *cg::this_cluster().map_shared_rank(to, r) = make_float2(ta, tb);
     }
@@ -125,7 +144,7 @@ __device__ __forceinline__ void exchange(Shared& sm, int parity, const Place& p,
       if (r == p.rank) enter = fma(pa, carry, pb);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float2 m = sm.tile[parity][r][p.lane * V + v];
+        const float2 m = sm.tile(parity, r)[p.lane * V + v];
         carry.f[v] = fmaf(m.x, carry.f[v], m.y);
       }
     }
@@ -165,7 +184,9 @@ __device__ __forceinline__ void load_run(Raw<k16, V> (&w)[kT], const void* base,
 template <bool kIn16, bool kOut16, int V, bool kSig, bool kCluster>
 __global__ void __launch_bounds__(kThreads, 3)
 scan_forward_kernel(const Args a) {
-  __shared__ Shared sm;
+  extern __shared__ __align__(16) unsigned char dynamic[];
+  const Shared<V, kCluster> sm = {dynamic};
+  Vec<V>* const kept = sm.kept();
   const Place p = place_of<V>(a);
   Vec<V> carry = fill<V>(0.f);
   if (a.h0 && p.on) carry = widen(load_raw<false, V>(a.h0 + p.s * a.c + p.c));
@@ -176,26 +197,40 @@ scan_forward_kernel(const Args a) {
   for (int t = 0; t < a.geo.tiles; ++t) {
     const Run now = run_of(a, p, t, tile);
     Raw<kIn16, V> rx[kT];
-    Vec<V> gate[kT];
+    Vec<V> decay[kT], B = fill<V>(0.f), h;
+    Factor<kSig, V> A;
     {
       Raw<kIn16, V> rg[kT];
       load_run(rg, a.g, now, a.g_stride, p.c, a.reverse, live);
       load_run(rx, a.x, now, a.x_stride, p.c, a.reverse, live);
+      if constexpr (kSig) {
+        gates<4, kIn16, V>(rg, now.i0, live, [&](int u, const Gate<V>& g) {
+          const Vec<V> b = mul(g.z, widen(rx[u]));
+          A.take(g);
+          B = fma(g.a, B, b);
+          kept[u * blockDim.x] = b;
+          decay[u] = g.a;
+        });
+      } else {
 #pragma unroll
-      for (int u = 0; u < kT; ++u) gate[u] = gate_of<kSig>(rg[u]);
-    }
-    if (now.i0 + kT > live) {
+        for (int u = 0; u < kT; ++u) decay[u] = widen(rg[u]);
+        if (now.i0 + kT > live) {
 #pragma unroll
-      for (int u = 0; u < kT; ++u)
-        if (now.i0 + u >= live) gate[u] = identity_gate<kSig, V>();
-    }
-    Vec<V> A = fill<V>(1.f), B = fill<V>(0.f), h;
+          for (int u = 0; u < kT; ++u)
+            if (now.i0 + u >= live) decay[u] = fill<V>(1.f);
+        }
 #pragma unroll
-    for (int u = 0; u < kT; ++u) {
-      A = decayed<kSig>(gate[u], A);
-      B = step<kSig>(gate[u], widen(rx[u]), B);
+        for (int u = 0; u < kT; ++u) {
+          A.take({decay[u], {}});
+          B = fma(decay[u], B, widen(rx[u]));
+        }
+      }
     }
-    exchange<V, kCluster, false>(sm, t & 1, p, a.geo.lanes, a.geo.cluster, A, B, carry, h);
+    auto next = [&](int u, const Vec<V>& h) {
+      if constexpr (kSig) return fma(decay[u], h, kept[u * blockDim.x]);
+      else return fma(decay[u], h, widen(rx[u]));
+    };
+    exchange<V, kCluster, false>(sm, t & 1, p, a.geo.lanes, a.geo.cluster, A.value(), B, carry, h);
     if (p.on && now.i0 < a.n) {
       if (a.states)
         store_vec<false>(a.states + (p.s * a.chunks + now.i0 / kT) * a.c + p.c, h);
@@ -205,14 +240,14 @@ scan_forward_kernel(const Args a) {
       if (now.i0 + kT <= live) {
 #pragma unroll
         for (int u = 0; u < kT; ++u, q += by) {
-          h = step<kSig>(gate[u], widen(rx[u]), h);
+          h = next(u, h);
           store_vec<kOut16>(q, h);
         }
       } else {
 #pragma unroll
         for (int u = 0; u < kT; ++u, q += by) {
           const int i = now.i0 + u;
-          h = step<kSig>(gate[u], widen(rx[u]), h);
+          h = next(u, h);
           if (i < live)
             store_vec<kOut16>(q, h);
           else if (i < a.n)
@@ -229,7 +264,9 @@ scan_forward_kernel(const Args a) {
 template <bool kIn16, bool kGrad16, int V, bool kSig, bool kCluster>
 __global__ void __launch_bounds__(kThreads, 2)
 scan_backward_kernel(const Args a) {
-  __shared__ Shared sm;
+  extern __shared__ __align__(16) unsigned char dynamic[];
+  const Shared<V, kCluster> sm = {dynamic};
+  Vec<V>* const kept = sm.kept();
   const Place p = place_of<V>(a);
   Vec<V> carry = fill<V>(0.f);
   if (a.dfinal && p.on) carry = widen(load_raw<false, V>(a.dfinal + p.s * a.c + p.c));
@@ -238,7 +275,8 @@ scan_backward_kernel(const Args a) {
   if constexpr (kCluster) cg::this_cluster().sync();
   for (int t = a.geo.tiles - 1; t >= 0; --t) {
     const Run run = run_of(a, p, t, tile);
-    Vec<V> gate[kT], x[kT], dh[kT], h = fill<V>(0.f);
+    Vec<V> decay[kT], slope[kT], dh[kT], h = fill<V>(0.f);
+    Factor<kSig, V> A;
     {
       Raw<kIn16, V> rx[kT], rg[kT];
       Raw<kGrad16, V> rd[kT];
@@ -247,33 +285,39 @@ scan_backward_kernel(const Args a) {
       load_run(rd, a.dout, run, a.c, p.c, a.reverse, live);
       if (p.on && run.i0 < a.n)
         h = widen(load_raw<false, V>(a.states + (p.s * a.chunks + run.i0 / kT) * a.c + p.c));
+      if constexpr (kSig) {
+        gates<4, kIn16, V>(rg, run.i0, live, [&](int u, const Gate<V>& g) {
+          const Vec<V> x = widen(rx[u]);
+          A.take(g);
+          slope[u] = mul(g.z, sub(h, x));
+          h = fma(g.a, h, mul(g.z, x));
+          kept[u * blockDim.x] = g.z;
+          decay[u] = g.a;
+        });
+      } else {
 #pragma unroll
-      for (int u = 0; u < kT; ++u) {
-        x[u] = widen(rx[u]);
-        gate[u] = gate_of<kSig>(rg[u]);
-        dh[u] = widen(rd[u]);
+        for (int u = 0; u < kT; ++u) decay[u] = widen(rg[u]);
+        if (run.i0 + kT > live) {
+#pragma unroll
+          for (int u = 0; u < kT; ++u)
+            if (run.i0 + u >= live) decay[u] = fill<V>(1.f);
+        }
+#pragma unroll
+        for (int u = 0; u < kT; ++u) {
+          slope[u] = h;
+          h = fma(decay[u], h, widen(rx[u]));
+        }
       }
-    }
-    if (run.i0 + kT > live) {
 #pragma unroll
-      for (int u = 0; u < kT; ++u)
-        if (run.i0 + u >= live) gate[u] = identity_gate<kSig, V>();
+      for (int u = 0; u < kT; ++u) dh[u] = widen(rd[u]);
     }
-    // The slope of a step in its decay, x_i - h_{i-1} (with -z: the signs cancel) or h_{i-1}, in x's
-    // place.
-#pragma unroll
-    for (int u = 0; u < kT; ++u) {
-      const Vec<V> before = h;
-      h = step<kSig>(gate[u], x[u], h);
-      x[u] = kSig ? sub(x[u], before) : before;
-    }
-    Vec<V> A = fill<V>(1.f), B = fill<V>(0.f), E;
+    Vec<V> B = fill<V>(0.f), E;
 #pragma unroll
     for (int u = kT - 1; u >= 0; --u) {
-      A = decayed<kSig>(gate[u], A);
-      B = decayed<kSig>(gate[u], add(dh[u], B));
+      if constexpr (!kSig) A.take({decay[u], {}});
+      B = mul(decay[u], add(dh[u], B));
     }
-    exchange<V, kCluster, true>(sm, t & 1, p, a.geo.lanes, a.geo.cluster, A, B, carry, E);
+    exchange<V, kCluster, true>(sm, t & 1, p, a.geo.lanes, a.geo.cluster, A.value(), B, carry, E);
     if (p.on && run.i0 < a.n) {
       constexpr int kBytes = kGrad16 ? 2 : 4;
       const bool whole = run.i0 + kT <= live;
@@ -285,9 +329,10 @@ scan_backward_kernel(const Args a) {
 #pragma unroll
       for (int u = kT - 1; u >= 0; --u, qx += bx, qg += bg) {
         const Vec<V> D = add(dh[u], E);
-        E = decayed<kSig>(gate[u], D);
-        Vec<V> dx, dg;
-        step_gradients<kSig>(gate[u], x[u], D, E, dx, dg);
+        E = mul(decay[u], D);
+        Vec<V> z = {}, dx, dg;
+        if constexpr (kSig) z = kept[u * blockDim.x];
+        step_gradients<kSig>(z, slope[u], D, E, dx, dg);
         const int i = run.i0 + u;
         if (whole || i < live) {
           store_vec<kGrad16>(qx, dx);
@@ -512,6 +557,8 @@ lapl_status launch(lapl_scan_plan* p, scan::Kernel k, scan::Args& a, int v, void
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((long long)p->cfg.sequences * a.geo.blocks * a.geo.cluster));
   cfg.blockDim = dim3((unsigned)a.geo.threads);
+  const bool sig = p->cfg.gate == LAPL_GATE_SIGMOID;
+  cfg.dynamicSmemBytes = scan::shared_bytes(a.geo.threads, v, a.geo.cluster > 1, sig);
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -520,7 +567,11 @@ lapl_status launch(lapl_scan_plan* p, scan::Kernel k, scan::Args& a, int v, void
   cfg.attrs = at;
   cfg.numAttrs = a.geo.cluster > 1 ? 1 : 0;
   cudaError_t e = cudaSuccess;
-  if (a.geo.cluster > 8)
+  if (cfg.dynamicSmemBytes > 48 * 1024)   // the most there is, whatever this plan's takes: it is the kernel's
+    e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k),
+                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)scan::shared_bytes(scan::kThreads, 2, true, true));
+  if (e == cudaSuccess && a.geo.cluster > 8)
     e = cudaFuncSetAttribute(reinterpret_cast<const void*>(k),
                              cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, k, a);

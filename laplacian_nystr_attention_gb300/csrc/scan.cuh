@@ -92,66 +92,105 @@ __device__ __forceinline__ void store_vec(void* p, const Vec<V>& v) {
   }
 }
 
-// A step's decay as it is kept: a (decay gate), or -z (sigmoid gate) with z = 1 - a = 1 / (1 + exp(g)).
-//
-// The hardware's base-2 exponential is good to 2 ulp, but its argument t = g log2 e is rounded, which
-// is a relative error of |t| ulp in exp(g).  The part that the rounding lost, r = g log2 e - t, comes
-// exactly out of one more fused step, and 2^(t + r) = 2^t (1 + r ln 2) puts it back.  g is held within
-// [-87, 88], where neither overflows (z is 1 and 6e-39 there); NaN passes through.
+// A step's decay, and with the sigmoid gate z = 1 - a = 1 / (1 + exp(g)) beside it, each good to some
+// 2^-24 of itself: h = a h + z x keeps what either loses of the other where it is small.  (With z alone
+// and a = 1 - z, gradients through a gate of -10 were off by 5e-4 of themselves, of -17 gone.)
+template <int V>
+struct Gate {
+  Vec<V> a, z;   // z: sigmoid only
+};
+// The hardware's base-2 exponential is good to 2 ulp, but its argument t, g log2 e rounded, is a
+// relative error of |t| ulp in exp(g).  What t lacks, r, comes out of one more step or two, and
+// 2^(t + r) = 2^t (1 + r ln 2) puts it back.  (bf16: log2 e in two parts, of which 16 bits times g are
+// exact; r ln 2 is at most 5e-4, whose square costs 2^-24 and a half at the ends.)  g is held within [-88, 88],
+// where nothing overflows, and everything is scaled by 1/16, so that 16 / (1 + exp(g)) stays in the normal
+// range: a and z below 2^-126 (|g| above 87.3) are zero, and the other one is then 1.  NaN passes
+// through.
 template <bool kSig, bool k16, int V>
-__device__ __forceinline__ Vec<V> gate_of(Raw<k16, V> w) {
+__device__ __forceinline__ Gate<V> gate_of(Raw<k16, V> w) {
   if constexpr (!kSig) {
-    return widen(w);
+    return {widen(w), fill<V>(0.f)};
   } else {
-    Vec<V> g;
+    constexpr float kScale = 0.0625f, kLn2 = 0.693147181f;
+    const Vec<V> sixteenth = fill<V>(kScale);
+    Vec<V> g, t, e, r;   // r: ln 2 / 16 of what t lacks
     if constexpr (k16) {   // both values at once (with one, the other half is 0)
-      asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(w.w[0]) : "r"(0x42b042b0u));
-      asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w.w[0]) : "r"(0xc2aec2aeu));
+      asm("min.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(w.w[0]) : "r"(0x42b042b0u));   // 88
       g = widen(w);
+      t = mul(g, fill<V>(1.44268799f));                       // 0x1.7154p+0, 16 bits
+      r = mul(g, fill<V>(kScale * 4.88849515e-6f));           // (log2 e - that) ln 2
     } else {
       g = widen(w);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        asm("min.NaN.f32 %0, %0, 0f42b00000;" : "+f"(g.f[i]));   // 88
-        asm("max.NaN.f32 %0, %0, 0fc2ae0000;" : "+f"(g.f[i]));   // -87
-      }
+      for (int i = 0; i < V; ++i)
+        asm("min.NaN.xorsign.abs.f32 %0, %0, 0f42b00000;" : "+f"(g.f[i]));
+      t = mul(g, fill<V>(1.44269504f));
+      Vec<V> minus;
+#pragma unroll
+      for (int i = 0; i < V; ++i) minus.f[i] = -t.f[i];
+      // log2 e is 1.44269504f and 1.92596303e-8.
+      r = mul(fma(g, fill<V>(1.92596303e-8f), fma(g, fill<V>(1.44269504f), minus)),
+              fill<V>(kScale * kLn2));
     }
-    const Vec<V> t = mul(g, fill<V>(-1.44269504f));            // -g log2 e, rounded
-    const Vec<V> r = fma(g, fill<V>(1.44269504f), t);
-    Vec<V> e;
 #pragma unroll
-    for (int i = 0; i < V; ++i) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.f[i]) : "f"(-t.f[i]));
-    Vec<V> z = fma(mul(e, fill<V>(-0.693147181f)), r, sub(fill<V>(-1.f), e));   // -1 - exp(g)
+    for (int i = 0; i < V; ++i) asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.f[i]) : "f"(t.f[i]));
+    e = fma(e, r, mul(e, sixteenth));                         // exp(g) / 16
+    Vec<V> u = add(e, sixteenth);
 #pragma unroll
-    for (int i = 0; i < V; ++i) asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(z.f[i]));
-    return z;
+    for (int i = 0; i < V; ++i) asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(u.f[i]));   // 16 / (1 + exp(g))
+    Gate<V> gate = {ops::mul_flush(e, u), ops::mul_flush(u, sixteenth)};
+    // In fp32 also the last bit of an open gate's a, which the tokens that the state remembers
+    // repeat; bf16 inputs leave it (a packed value's four instructions of some fifty).
+    if constexpr (!k16)
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (gate.z.f[i] < 0.5f) gate.a.f[i] = 1.f - gate.z.f[i];
+    return gate;
   }
 }
-// The decay of a step that leaves the state as it is.
+// The factor of a run's map: the product of its decays.  With the sigmoid gate also 1 less it,
+// c = z + a c, a sum of positive numbers: where the gates are nearly open the state remembers 1 / (1 - A)
+// runs, and a rounding of every factor of A would be that much larger in it.
 template <bool kSig, int V>
-__device__ __forceinline__ Vec<V> identity_gate() {
-  return fill<V>(kSig ? 0.f : 1.f);
-}
-// h after a step: h - z (h - x), or a h + x.
-template <bool kSig, int V>
-__device__ __forceinline__ Vec<V> step(const Vec<V>& gate, const Vec<V>& x, const Vec<V>& h) {
-  if constexpr (kSig) return fma(gate, sub(h, x), h);
-  else return fma(gate, h, x);
-}
-// a times v.
-template <bool kSig, int V>
-__device__ __forceinline__ Vec<V> decayed(const Vec<V>& gate, const Vec<V>& v) {
-  if constexpr (kSig) return fma(gate, v, v);
-  else return mul(gate, v);
-}
-// The gradients of a step from D, with E = a D and slope = x_i - h_{i-1} (gate is -z) or h_{i-1}.
-template <bool kSig, int V>
-__device__ __forceinline__ void step_gradients(const Vec<V>& gate, const Vec<V>& slope,
-                                               const Vec<V>& D, const Vec<V>& E, Vec<V>& dx,
-                                               Vec<V>& dg) {
+struct Factor {
+  Vec<V> p = fill<V>(1.f), c = fill<V>(0.f);
+  __device__ __forceinline__ void take(const Gate<V>& gate) {
+    p = mul(gate.a, p);
+    if constexpr (kSig) c = fma(gate.a, c, gate.z);
+  }
+  __device__ __forceinline__ Vec<V> value() const {
+    Vec<V> r = p;
+    if constexpr (kSig)
 #pragma unroll
-  for (int i = 0; i < V; ++i) dx.f[i] = kSig ? -gate.f[i] * D.f[i] : D.f[i];
-  dg = kSig ? mul(mul(gate, slope), E) : mul(slope, D);
+      for (int i = 0; i < V; ++i)
+        if (c.f[i] < 0.5f) r.f[i] = 1.f - c.f[i];
+    return r;
+  }
+};
+// use(u, gate) for each of kT sigmoid gates in turn, those from `live` on as steps that change nothing.
+// kAtOnce at a time, whose latencies overlap.
+template <int kAtOnce, bool k16, int V, class Use>
+__device__ __forceinline__ void gates(const Raw<k16, V> (&w)[kT], int i0, int live, Use use) {
+#pragma unroll
+  for (int u0 = 0; u0 < kT; u0 += kAtOnce) {
+    Gate<V> g[kAtOnce];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) g[u] = gate_of<true>(w[u0 + u]);
+    if (i0 + u0 + kAtOnce > live) {
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u)
+        if (i0 + u0 + u >= live) g[u] = {fill<V>(1.f), fill<V>(0.f)};
+    }
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) use(u0 + u, g[u]);
+  }
+}
+// The gradients of a step from D and E = a D.
+template <bool kSig, int V>
+__device__ __forceinline__ void step_gradients(const Vec<V>& z, const Vec<V>& slope, const Vec<V>& D,
+                                               const Vec<V>& E, Vec<V>& dx, Vec<V>& dg) {
+  dx = kSig ? mul(z, D) : D;
+  dg = mul(slope, kSig ? E : D);
 }
 
 }  // namespace scan

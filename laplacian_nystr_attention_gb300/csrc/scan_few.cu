@@ -77,6 +77,53 @@ struct Spot {
     return s * a.n + (a.reverse ? len - 1 - i : i);
   }
 };
+// The sigmoid gate's smaller side, -z or a by its sign: h + z (x - h) or x - a (x - h), and D - z D or
+// a D, without the rounding of the other one.  A state that is handed on from call to call goes through
+// thousands of steps, and an error of a that they share grows to 2^-24 / z.  (The decay gate: a.)
+template <bool kSig, int V>
+struct Side {
+  Vec<V> n;
+  Side() = default;
+  __device__ __forceinline__ explicit Side(const Gate<V>& gate) : n(gate.a) {
+    if constexpr (kSig)
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (gate.z.f[i] < 0.5f) n.f[i] = -gate.z.f[i];
+  }
+  __device__ __forceinline__ bool open(int i) const { return __float_as_int(n.f[i]) < 0; }
+  // h after a step.
+  __device__ __forceinline__ Vec<V> step(const Vec<V>& x, const Vec<V>& h) const {
+    if constexpr (!kSig) return fma(n, h, x);
+    Vec<V> from;
+#pragma unroll
+    for (int i = 0; i < V; ++i) from.f[i] = open(i) ? h.f[i] : x.f[i];
+    return fma(n, sub(h, x), from);
+  }
+  // The slope of a step in its decay: of a z with the sigmoid gate.
+  __device__ __forceinline__ Vec<V> slope(const Vec<V>& x, const Vec<V>& before) const {
+    return kSig ? sub(before, x) : before;
+  }
+  // From D: a D, and the step's gradients.
+  __device__ __forceinline__ Vec<V> gradients(const Vec<V>& D, const Vec<V>& slope, Vec<V>& dx,
+                                              Vec<V>& dg) const {
+    if constexpr (!kSig) {
+      dx = D;
+      dg = mul(slope, D);
+      return mul(n, D);
+    }
+    Vec<V> less, E;
+#pragma unroll
+    for (int i = 0; i < V; ++i) less.f[i] = fabsf(n.f[i]);
+    const Vec<V> small = mul(less, D), large = sub(D, small);
+    dg = mul(slope, mul(less, large));
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      dx.f[i] = open(i) ? small.f[i] : large.f[i];
+      E.f[i] = open(i) ? large.f[i] : small.f[i];
+    }
+    return E;
+  }
+};
 template <int V>
 __device__ __forceinline__ State<V> zeros() {
   State<V> h;
@@ -129,7 +176,7 @@ __global__ void __launch_bounds__(kThreads) scan_few_kernel(const Args a) {
       if (i < len) {
 #pragma unroll
         for (int k = 0; k < kN; ++k)
-          h.p[k] = step<kSig>(gate_of<kSig>(ng[u].p[k]), widen(nx[u].p[k]), h.p[k]);
+          h.p[k] = Side<kSig, Parts<V>::kW>(gate_of<kSig>(ng[u].p[k])).step(widen(nx[u].p[k]), h.p[k]);
         store_state<kOut16>(a.out, spot.row(a, i) * a.c + c, h);
       } else if (i < a.n) {
         store_state<kOut16>(a.out, (s * a.n + i) * a.c + c, zeros<V>());
@@ -159,16 +206,17 @@ __global__ void __launch_bounds__(kThreads) scan_few_backward_kernel(const Args 
     }
   State<V> h = load_state<V>(a.states, s * a.c + c), E = zeros<V>();   // one kept state a sequence
   if (a.dfinal) E = load_state<V>(a.dfinal, s * a.c + c);
-  State<V> gate[T], slope[T];
+  Side<kSig, Parts<V>::kW> gate[T][kN];
+  State<V> slope[T];
 #pragma unroll
   for (int i = 0; i < T; ++i)
     if (i < len)
 #pragma unroll
       for (int k = 0; k < kN; ++k) {
         const auto in = widen(x[i].p[k]);
-        gate[i].p[k] = gate_of<kSig>(g[i].p[k]);
-        slope[i].p[k] = kSig ? sub(in, h.p[k]) : h.p[k];
-        h.p[k] = step<kSig>(gate[i].p[k], in, h.p[k]);
+        gate[i][k] = Side<kSig, Parts<V>::kW>(gate_of<kSig>(g[i].p[k]));
+        slope[i].p[k] = gate[i][k].slope(in, h.p[k]);
+        h.p[k] = gate[i][k].step(in, h.p[k]);
       }
 #pragma unroll
   for (int i = T - 1; i >= 0; --i) {
@@ -178,8 +226,7 @@ __global__ void __launch_bounds__(kThreads) scan_few_backward_kernel(const Args 
 #pragma unroll
       for (int k = 0; k < kN; ++k) {
         const auto D = add(widen(dh[i].p[k]), E.p[k]);
-        E.p[k] = decayed<kSig>(gate[i].p[k], D);
-        step_gradients<kSig>(gate[i].p[k], slope[i].p[k], D, E.p[k], dx.p[k], dg.p[k]);
+        E.p[k] = gate[i][k].gradients(D, slope[i].p[k], dx.p[k], dg.p[k]);
       }
     const long long row = i < len ? spot.row(a, i) : s * a.n + i;
     store_state<kGrad16>(a.dx, row * a.x_stride + c, dx);

@@ -14,8 +14,10 @@
 //     while the round before is still being received.
 //   * Each warp copies its own tokens ahead into its own ring of stages (cp.async, 16 bytes at a
 //     time): no barrier between warps, and the bytes in flight are those of the ring.  A stage is kept
-//     until its tokens are read a second time, so that registers hold the gates alone (and in the
-//     backward the slopes): holding the tokens as well took 73 us instead of 58 below.
+//     until its tokens are read a second time, so that registers hold the decays alone (and in the
+//     backward the slopes): holding the tokens as well took 73 us instead of 58 below.  With the
+//     sigmoid gate a thread leaves there, in the place of its own g and x, what it needs the second
+//     time: z x, or in the backward z.
 // Two values go through the packed fp32 instructions (bf16 inputs).
 //
 // Measured (of 6.78 TB/s): 32 x 16384 x 64 bf16, sigmoid gate: 38.7 us forward (77%) and 57.5 us backward
@@ -166,6 +168,22 @@ __device__ __forceinline__ unsigned long long nanoseconds() {
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
 }
+// Two words of a stage that are one thread's own, V floats.
+template <int V>
+__device__ __forceinline__ void keep(unsigned at, unsigned apart, const Vec<V>& v) {
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + i * apart), "f"(v.f[i]) : "memory");
+}
+template <int V>
+__device__ __forceinline__ Vec<V> kept(unsigned at, unsigned apart) {
+  Vec<V> v;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v.f[i]) : "r"(at + i * apart) : "memory");
+  return v;
+}
+
 // Until the phase of the given parity is complete, or false after `bound` ns.
 __device__ __forceinline__ bool wait_phase(unsigned bar, unsigned parity, unsigned long long bound) {
   const unsigned at_once = (unsigned)min(bound, 1000000000ull);   // a look may last that long itself
@@ -435,20 +453,39 @@ scan_forward_pipe_kernel(const Args a, unsigned* err) {
       copies_left<kStages - 1>();
       __syncwarp();
       const unsigned from = ring + stage * kStage + my;
-      Vec<V> gate[kT];
+      Vec<V> decay[kT];
+      Map<V> m = {{}, fill<V>(0.f)};
+      Factor<kSig, V> factor;
+      if constexpr (kSig) {
+        Raw<kIn16, V> rg[kT];
 #pragma unroll
-      for (int k = 0; k < kT; ++k) gate[k] = gate_of<kSig>(read_raw<kIn16, V>(from + k * T::kRow));
-      if (i0 + kT > live) {
+        for (int k = 0; k < kT; ++k) rg[k] = read_raw<kIn16, V>(from + k * T::kRow);
+        gates<8, kIn16, V>(rg, i0, live, [&](int k, const Gate<V>& g) {
+          const Vec<V> b = mul(g.z, widen(read_raw<kIn16, V>(from + T::kWarp + k * T::kRow)));
+          factor.take(g);
+          m.b = fma(g.a, m.b, b);
+          keep(from + k * T::kRow, T::kWarp, b);
+          decay[k] = g.a;
+        });
+      } else {
 #pragma unroll
-        for (int k = 0; k < kT; ++k)
-          if (i0 + k >= live) gate[k] = identity_gate<kSig, V>();
+        for (int k = 0; k < kT; ++k) decay[k] = widen(read_raw<kIn16, V>(from + k * T::kRow));
+        if (i0 + kT > live) {
+#pragma unroll
+          for (int k = 0; k < kT; ++k)
+            if (i0 + k >= live) decay[k] = fill<V>(1.f);
+        }
+#pragma unroll
+        for (int k = 0; k < kT; ++k) {
+          factor.take({decay[k], {}});
+          m.b = fma(decay[k], m.b, widen(read_raw<kIn16, V>(from + T::kWarp + k * T::kRow)));
+        }
       }
-      Map<V> m = {fill<V>(1.f), fill<V>(0.f)};
-#pragma unroll
-      for (int k = 0; k < kT; ++k) {
-        m.a = decayed<kSig>(gate[k], m.a);
-        m.b = step<kSig>(gate[k], widen(read_raw<kIn16, V>(from + T::kWarp + k * T::kRow)), m.b);
-      }
+      m.a = factor.value();
+      auto next = [&](int k, const Vec<V>& h) {
+        if constexpr (kSig) return fma(decay[k], h, kept<V>(from + k * T::kRow, T::kWarp));
+        else return fma(decay[k], h, widen(read_raw<kIn16, V>(from + T::kWarp + k * T::kRow)));
+      };
       put_map(smem + l.runs + (team * kWarps * 32 + wt * 32 + lane) * (2 * V * 4), m);
       bar_arrive(runs_bar<kTeams>(team), kWarps * 32 + 32);
       bar_sync(states_bar<kTeams>(team), kWarps * 32 + 64);
@@ -464,14 +501,14 @@ scan_forward_pipe_kernel(const Args a, unsigned* err) {
         if (i0 + kT <= live) {
 #pragma unroll
           for (int k = 0; k < kT; ++k, q += by) {
-            h = step<kSig>(gate[k], widen(read_raw<kIn16, V>(from + T::kWarp + k * T::kRow)), h);
+            h = next(k, h);
             store_vec<kOut16>(q, h);
           }
         } else {
 #pragma unroll
           for (int k = 0; k < kT; ++k, q += by) {
             const int i = i0 + k;
-            h = step<kSig>(gate[k], widen(read_raw<kIn16, V>(from + T::kWarp + k * T::kRow)), h);
+            h = next(k, h);
             if (i < live)
               store_vec<kOut16>(q, h);
             else if (i < a.n)
@@ -552,30 +589,45 @@ scan_backward_pipe_kernel(const Args a, unsigned* err) {
       copies_left<kStages - 1>();
       __syncwarp();
       const unsigned from = ring + stage * kStage;
-      Vec<V> gate[kT], slope[kT], h = next;
+      Vec<V> decay[kT], slope[kT], h = next;
+      Factor<kSig, V> factor;
+      if constexpr (kSig) {
+        Raw<kIn16, V> rg[kT];
 #pragma unroll
-      for (int k = 0; k < kT; ++k) gate[k] = gate_of<kSig>(read_raw<kIn16, V>(from + my + k * T::kRow));
-      next = state(r + kTeams);
-      if (i0 + kT > live) {
+        for (int k = 0; k < kT; ++k) rg[k] = read_raw<kIn16, V>(from + my + k * T::kRow);
+        gates<kT, kIn16, V>(rg, i0, live, [&](int k, const Gate<V>& g) {
+          const Vec<V> x = widen(read_raw<kIn16, V>(from + my + T::kWarp + k * T::kRow));
+          factor.take(g);
+          slope[k] = mul(g.z, sub(h, x));
+          h = fma(g.a, h, mul(g.z, x));
+          keep(from + my + k * T::kRow, T::kWarp, g.z);
+          decay[k] = g.a;
+        });
+      } else {
 #pragma unroll
-        for (int k = 0; k < kT; ++k)
-          if (i0 + k >= live) gate[k] = identity_gate<kSig, V>();
+        for (int k = 0; k < kT; ++k) decay[k] = widen(read_raw<kIn16, V>(from + my + k * T::kRow));
+        if (i0 + kT > live) {
+#pragma unroll
+          for (int k = 0; k < kT; ++k)
+            if (i0 + k >= live) decay[k] = fill<V>(1.f);
+        }
       }
-      Map<V> m = {fill<V>(1.f), fill<V>(0.f)};
+      next = state(r + kTeams);
+      Map<V> m = {{}, fill<V>(0.f)};
 #pragma unroll
       for (int k = kT - 1; k >= 0; --k) {
-        m.a = decayed<kSig>(gate[k], m.a);
-        m.b = decayed<kSig>(gate[k], add(widen(read_raw<kGrad16, V>(from + my_grad + k * TG::kRow)), m.b));
+        if constexpr (!kSig) factor.take({decay[k], {}});
+        m.b = mul(decay[k], add(widen(read_raw<kGrad16, V>(from + my_grad + k * TG::kRow)), m.b));
       }
+      m.a = factor.value();
       put_map(smem + l.runs + (team * kWarps * 32 + wt * 32 + lane) * (2 * V * 4), m);
       bar_arrive(runs_bar<kTeams>(team), kWarps * 32 + 32);
-      // The slope of a step in its decay, x_i - h_{i-1} (with -z: the signs cancel) or h_{i-1}, while
-      // the chain goes on.
+      if constexpr (!kSig) {   // while the chain goes on
 #pragma unroll
-      for (int k = 0; k < kT; ++k) {
-        const Vec<V> x = widen(read_raw<kIn16, V>(from + my + T::kWarp + k * T::kRow));
-        slope[k] = kSig ? sub(x, h) : h;
-        h = step<kSig>(gate[k], x, h);
+        for (int k = 0; k < kT; ++k) {
+          slope[k] = h;
+          h = fma(decay[k], h, widen(read_raw<kIn16, V>(from + my + T::kWarp + k * T::kRow)));
+        }
       }
       bar_sync(states_bar<kTeams>(team), kWarps * 32 + 64);
       Vec<V> E;
@@ -592,9 +644,10 @@ scan_backward_pipe_kernel(const Args a, unsigned* err) {
 #pragma unroll
         for (int k = kT - 1; k >= 0; --k, qx += bx, qg += bg) {
           const Vec<V> D = add(widen(read_raw<kGrad16, V>(from + my_grad + k * TG::kRow)), E);
-          E = decayed<kSig>(gate[k], D);
-          Vec<V> dx, dg;
-          step_gradients<kSig>(gate[k], slope[k], D, E, dx, dg);
+          E = mul(decay[k], D);
+          Vec<V> z = {}, dx, dg;
+          if constexpr (kSig) z = kept<V>(from + my + k * T::kRow, T::kWarp);
+          step_gradients<kSig>(z, slope[k], D, E, dx, dg);
           if (k < left) {
             store_vec<kGrad16>(qx, dx);
             store_vec<kGrad16>(qg, dg);
