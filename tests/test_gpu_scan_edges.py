@@ -151,3 +151,44 @@ def test_a_reset_gate_leaves_nothing_of_a_large_state():
             x[:, at - 1] = 1e8
         h = lna.GatedScan(lna.make_scan_config(1, N, 8)).forward(x, g, h0=h0)
         assert (h[:, at] == x[:, at]).all()
+
+
+# ---- states that are not finite -----------------------------------------------------------
+
+@pytest.mark.parametrize("S,N,C,lens", [(2, 3, 8, [3, 2]), (2, 30, 9, [30, 20]),
+                                        (2, 300, 64, [300, 150]), (2, 1500, 64, [1500, 700])])
+@pytest.mark.parametrize("gate", ["sigmoid", "decay"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_a_state_that_is_not_finite_stays_so(S, N, C, lens, gate, dtype, bad):
+    """From the token on whose x (or, a NaN, whose g) is not finite its channel's states are not
+    finite, to the last one, padding or not; everything else is as without it.  Backward likewise:
+    dg from the next token on; dx and dh0 do not know of it."""
+    import laplacian_nystr_attention_gb300 as lna
+    x, g, dout = (randn(S, N, C, seed=k, dtype=dtype) for k in range(3))
+    if gate == "decay":
+        g = torch.sigmoid(g + 2)
+    plan = lna.GatedScan(lna.make_scan_config(S, N, C, gate=gate, in_dtype=dtype, grad_dtype=dtype))
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+
+    def both():
+        states, final = torch.empty(plan.states_shape, device="cuda"), torch.empty(S, C, device="cuda")
+        h = plan.forward(x, g, lengths=n, states=states, final=final)
+        return [h, final, *plan.backward(x, g, states, dout, lengths=n)]
+
+    want = [t.clone() for t in both()]
+    at, c = lens[1] // 2, C - 1
+    x[1, at, c] = bad
+    h, final, dx, dg, dh0 = both()
+    hit = torch.zeros(S, N, C, dtype=torch.bool, device="cuda")
+    hit[1, at:lens[1], c] = True
+    assert torch.equal(~torch.isfinite(h), hit)
+    assert torch.equal(h[~hit], want[0][~hit])
+    lost = torch.zeros_like(final, dtype=torch.bool)
+    lost[1, c] = True
+    assert torch.equal(~torch.isfinite(final), lost) and torch.equal(final[~lost], want[1][~lost])
+    assert torch.equal(dx, want[2]) and torch.equal(dh0, want[4])
+    if gate == "decay":     # dg is h_{i-1} D
+        hit[1, at, c] = False
+    assert torch.equal(~torch.isfinite(dg), hit)
+    assert torch.equal(dg[~hit], want[3][~hit])
