@@ -12,11 +12,16 @@
 // them into other tensors, of which 239 are the bytes of both passes at that rate; 24 tensors of 2^20
 // values together 8.5 us, the latency of two launches.
 //
-// Squares.  fp32 holds values over 2^-149 .. 2^128, whose squares need twice that range.  Two sums
-// are kept: of (x 2^35)^2, exact enough for every value between 2^-98 and 2^28, and of (x 2^-72)^2
-// for what is larger.  The first is used unless it overflows; then some |x| is 2^24 or more, against
-// which what the second loses is nothing.  Partial sums are fp32 over at most some thousand values
-// of one thread, then pairs of floats.
+// Squares.  fp32 holds values over 2^-149 .. 2^128, whose squares need twice that range.  There are
+// three sums: of (x 2^35)^2, and for where that vanishes or overflows of (x 2^86)^2 and (x 2^-72)^2.  Their
+// squares are normal numbers from |x| = 2^-98, 2^-149 and 2^9 on.  The first is used if it comes out at
+// 2^-86 or more, against which the 2^-150 that each value may have lost is nothing even for 2^40
+// values.  If it does not, the second cannot overflow, and loses nothing.  If it overflows, all squares
+// together are more than 2^58, of which the third loses 2^-6 for each value at most, 2^-24 for 2^40 of
+// them.  A CTA sums the first alone, and the others are that times a power of two, unless it may have lost
+// something that counts, or nearly overflows: then the CTA goes through its pieces again for the other
+// two.  (All three for every value: 90 us instead of 79 for 2^28 bf16 values.)  Partial sums are fp32
+// over the 128 values at most that a thread has of a piece, in two chains, then pairs of floats.
 #include <algorithm>
 #include <new>
 #include <type_traits>
@@ -28,12 +33,20 @@ namespace lapl {
 namespace clip {
 
 constexpr int kThreads = 512;
+constexpr int kCtas = 4;             // of an SM, all resident at once: 32 registers a thread
 constexpr int kMinPiece = 2048, kMaxPiece = 65536;   // values, powers of two
 constexpr int kStart = 2048;   // values that a CTA streams while it starts on a piece
 constexpr int kUnroll = 4;           // 16-byte loads of a thread in flight, or 2 kUnroll of a value
 constexpr int kTable = 1000;         // tensors of a launch: 20 KB of its 32 KB of parameters
 constexpr int kSmallTable = 64;
 constexpr float kLow = 34359738368.f;                // 2^35
+constexpr float kTiny = 77371252455336267181195264.f;   // 2^86
+// A sum of squares times kLow^2 that is used.
+constexpr float kLowUsed = 1.292469707114106e-26f;      // 2^-86
+// A thread's sum for one piece: 128 values may be off by 2^-143 together, 2^-25 of this.
+constexpr float kLowLeast = 3.009265538105056e-36f;     // 2^-118
+// A thread's sum for all its pieces, below which a CTA's does not overflow.
+constexpr float kLowMost = 8.307674973655724e34f;       // 2^116
 constexpr float kHigh = 2.117582368135751e-22f;      // 2^-72
 
 template <int N>
@@ -70,23 +83,26 @@ __device__ __forceinline__ Piece piece_of(const Table<N>& t, int i) {
   return p;
 }
 
+// Squares of even and odd values times scale, and whether there is anything but zeros.
 struct Sums {
-  ops::Vec<2> low, high;   // of even and odd values
-  __device__ __forceinline__ void add(const ops::Vec<2>& x) {
-    const ops::Vec<2> l = ops::mul(x, ops::fill<2>(kLow)), h = ops::mul(x, ops::fill<2>(kHigh));
-    low = ops::fma(l, l, low);
-    high = ops::fma(h, h, high);
+  ops::Vec<2> sum;
+  uint32_t bits;
+  __device__ __forceinline__ void add(const ops::Vec<2>& x, float scale) {
+    const ops::Vec<2> v = ops::mul(x, ops::fill<2>(scale));
+    sum = ops::fma(v, v, sum);
   }
   template <bool kHalf>
-  __device__ __forceinline__ void add(const uint4& v) {
+  __device__ __forceinline__ void add(const uint4& v, float scale) {
+    bits |= v.x | v.y;
+    bits |= v.z | v.w;
     if constexpr (kHalf) {
-      add({bf16_lo(v.x), bf16_hi(v.x)});
-      add({bf16_lo(v.y), bf16_hi(v.y)});
-      add({bf16_lo(v.z), bf16_hi(v.z)});
-      add({bf16_lo(v.w), bf16_hi(v.w)});
+      add({bf16_lo(v.x), bf16_hi(v.x)}, scale);
+      add({bf16_lo(v.y), bf16_hi(v.y)}, scale);
+      add({bf16_lo(v.z), bf16_hi(v.z)}, scale);
+      add({bf16_lo(v.w), bf16_hi(v.w)}, scale);
     } else {
-      add({__uint_as_float(v.x), __uint_as_float(v.y)});
-      add({__uint_as_float(v.z), __uint_as_float(v.w)});
+      add({__uint_as_float(v.x), __uint_as_float(v.y)}, scale);
+      add({__uint_as_float(v.z), __uint_as_float(v.w)}, scale);
     }
   }
 };
@@ -119,23 +135,14 @@ struct Pair {
   __device__ __forceinline__ float value() const { return isfinite(hi) ? hi + lo : hi; }
 };
 struct Pairs {
-  Pair low, high;
-  __device__ __forceinline__ void add(const Pairs& o) {
-    low.add(o.low.hi, o.low.lo);
-    high.add(o.high.hi, o.high.lo);
-  }
+  Pair of[3];   // low, tiny, high
 };
-
 // Sum over the CTA in thread 0 (fixed order).
-__device__ __forceinline__ Pairs block_sum(Pairs s, Pairs* sm) {
-  auto across = [](Pairs s, int n) {
+__device__ __forceinline__ Pair block_sum(Pair s, Pair* sm) {
+  auto across = [](Pair s, int n) {
     for (int o = n / 2; o > 0; o >>= 1) {
-      Pairs other;
-      other.low.hi = __shfl_down_sync(0xffffffffu, s.low.hi, o);
-      other.low.lo = __shfl_down_sync(0xffffffffu, s.low.lo, o);
-      other.high.hi = __shfl_down_sync(0xffffffffu, s.high.hi, o);
-      other.high.lo = __shfl_down_sync(0xffffffffu, s.high.lo, o);
-      s.add(other);
+      const float hi = __shfl_down_sync(0xffffffffu, s.hi, o);
+      s.add(hi, __shfl_down_sync(0xffffffffu, s.lo, o));
     }
     return s;
   };
@@ -148,53 +155,79 @@ __device__ __forceinline__ Pairs block_sum(Pairs s, Pairs* sm) {
 
 // The squares of one piece.
 template <bool kHalf>
-__device__ __forceinline__ Sums squares(const Piece& p) {
+__device__ __forceinline__ Sums squares(const Piece& p, float scale) {
   constexpr int kBytes = kHalf ? 2 : 4;
   // Values before the first 16-byte boundary, 16 bytes at a time, and the rest.
   const int head = min(p.count, (int)((16 - ((uintptr_t)p.in & 15)) & 15) / kBytes);
   const int vectors = (p.count - head) * kBytes / 16;
   Sums s = {};
   each<kUnroll>(reinterpret_cast<const uint4*>(p.in + head * kBytes), vectors,
-              [&](int, const uint4& v) { s.add<kHalf>(v); });
+              [&](int, const uint4& v) { s.add<kHalf>(v, scale); });
   const int body = vectors * 16 / kBytes;
   for (int k = threadIdx.x; k < p.count - body; k += kThreads) {
     const int e = k < head ? k : k + body;
-    if constexpr (kHalf) s.add({ops::bf16_bits(reinterpret_cast<const uint16_t*>(p.in)[e]), 0.f});
-    else s.add({reinterpret_cast<const float*>(p.in)[e], 0.f});
+    const float v = kHalf ? ops::bf16_bits(reinterpret_cast<const uint16_t*>(p.in)[e])
+                          : reinterpret_cast<const float*>(p.in)[e];
+    s.bits |= __float_as_uint(v);
+    s.add({v, 0.f}, scale);
   }
   return s;
 }
 
 template <int N>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kCtas)
 clip_norm_kernel(const __grid_constant__ Table<N> t, Pairs* part) {
-  __shared__ Pairs sm[kThreads / 32];
+  __shared__ Pair sm[kThreads / 32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  Pairs sum = {};
   const int pieces = t.first[t.tensors];
-  for (int i = blockIdx.x; i < pieces; i += gridDim.x) {
-    const Piece p = piece_of(t, i);
-    const Sums s = p.half ? squares<true>(p) : squares<false>(p);
-    sum.low.add(s.low.f[0] + s.low.f[1]);
-    sum.high.add(s.high.f[0] + s.high.f[1]);
+  Pairs& mine = part[blockIdx.x];
+  // One pass, or three.
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const float scale = pass == 0 ? kLow : pass == 1 ? kTiny : kHigh;
+    Pair sum = {};
+    bool unsure = false;
+    for (int i = blockIdx.x; i < pieces; i += gridDim.x) {
+      const Piece p = piece_of(t, i);
+      const Sums s = p.half ? squares<true>(p, scale) : squares<false>(p, scale);
+      const float v = s.sum.f[0] + s.sum.f[1];
+      unsure |= v < kLowLeast && (s.bits & (p.half ? 0x7fff7fffu : 0x7fffffffu)) != 0u;
+      sum.add(v);
+    }
+    const bool more = __syncthreads_or(unsure || !(sum.hi < kLowMost)) || pass > 0;
+    sum = block_sum(sum, sm);
+    if (threadIdx.x == 0) mine.of[pass] = sum;
+    if (!more) {
+      constexpr float kUp = (kTiny / kLow) * (kTiny / kLow), kDown = kHigh / kLow;   // kDown twice
+      if (threadIdx.x == 0) {
+        mine.of[1] = {sum.hi * kUp, sum.lo * kUp};
+        mine.of[2] = {sum.hi * kDown * kDown, sum.lo * kDown * kDown};
+      }
+      return;
+    }
   }
-  sum = block_sum(sum, sm);
-  if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
 
 // The norm from all partials, the same in every thread.
 __device__ __forceinline__ float norm_of(const Pairs* part, int parts) {
-  __shared__ Pairs sm[kThreads / 32];
+  __shared__ Pair sm[kThreads / 32];
   __shared__ float norm;
-  Pairs s = {};
-  for (int k = threadIdx.x; k < parts; k += kThreads) s.add(part[k]);
-  s = block_sum(s, sm);
-  if (threadIdx.x == 0) {
-    const float low = s.low.value();
-    norm = isinf(low) ? sqrtf(s.high.value()) * (1.f / kHigh) : sqrtf(low) * (1.f / kLow);
+  __shared__ int next;
+  // The first sum, and where that is of no use another.
+#pragma unroll 1
+  for (int which = 0;;) {
+    Pair s = {};
+    for (int k = threadIdx.x; k < parts; k += kThreads) s.add(part[k].of[which].hi, part[k].of[which].lo);
+    s = block_sum(s, sm);
+    if (threadIdx.x == 0) {
+      const float v = s.value();
+      norm = sqrtf(v) * (which == 0 ? 1.f / kLow : which == 1 ? 1.f / kTiny : 1.f / kHigh);
+      next = which > 0 || (v >= kLowUsed && v < INFINITY) ? 0 : v < kLowUsed ? 1 : 2;
+    }
+    __syncthreads();
+    which = next;
+    if (which == 0) return norm;
   }
-  __syncthreads();
-  return norm;
 }
 
 __global__ void __launch_bounds__(kThreads)
@@ -417,7 +450,7 @@ lapl_status create(const lapl_clip_config* cfg, int sms, int device, lapl_clip_p
     p->batches.back().index.push_back(i);
     pieces += more;
   }
-  const long long ctas = 4LL * sms;   // of 512 threads: all resident at once
+  const long long ctas = (long long)clip::kCtas * sms;
   for (auto& b : p->batches) {
     // The piece with the least on the longest path: rounds of pieces, and starting on each.  (Of any
     // size, one or two for each CTA, large ones took up to 5% longer.)
