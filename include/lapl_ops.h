@@ -147,7 +147,8 @@ lapl_status lapl_norm_create(const lapl_norm_config* cfg, lapl_norm_handle* out)
  * NULL: s rounded to res_dtype (the norm itself goes by the unrounded s); may be residual itself;
  * rstd: device [B,N] fp32 or NULL; y: device [B,N,W] out_dtype; scales: LAPL_F8E4M3 only: device
  * [B,N, W/scale_group (1 for whole rows)] fp32.  8-bit values are q = round(y / scale) to nearest,
- * ties to even, with scale = max(largest |y| of the group, 2^-100) / 448; y is about q * scale.
+ * ties to even, with scale = max(largest |y| of the group, 2^-100) / 448; y is about q * scale.  A
+ * NaN makes its row's values NaN, and their scales.
  */
 lapl_status lapl_norm_forward(lapl_norm_handle h, const void* x, const void* residual,
                               const float* weight, void* sum, float* rstd, void* y,

@@ -171,13 +171,20 @@ __device__ __forceinline__ void store(void* base, long long e, const Values<VEC>
   }
 }
 
+// The larger one, or NaN if either is.
+__device__ __forceinline__ float larger(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // Sum or largest over the G threads of a row, the same value in each.  `scratch`: one float for
 // each warp of the CTA, of this reduction alone until the next __syncthreads.
 template <bool kMax>
 __device__ __forceinline__ float row_reduce(float v, int g, float* scratch) {
   for (int o = min(g, 32) >> 1; o > 0; o >>= 1) {
     const float other = __shfl_xor_sync(0xffffffffu, v, o);
-    v = kMax ? fmaxf(v, other) : v + other;
+    v = kMax ? larger(v, other) : v + other;
   }
   if (g > 32) {
     const int lane = threadIdx.x & 31;
@@ -187,7 +194,7 @@ __device__ __forceinline__ float row_reduce(float v, int g, float* scratch) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       const float other = __shfl_xor_sync(0xffffffffu, v, o);
-      v = kMax ? fmaxf(v, other) : v + other;
+      v = kMax ? larger(v, other) : v + other;
     }
   }
   return v;
@@ -208,6 +215,19 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d
   const __nv_fp8x2_storage_t hi =
       __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
   return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+
+// v / by from inv, 1 / by rounded to nearest: the product, and what is left of v by a fused step, which
+// corrects it (Markstein's division).  y times 1 / scale alone, or times 448 / largest, would put
+// values near the middle of two e4m3 ones on the wrong side.
+__device__ __forceinline__ float quotient(float v, float by, float inv) {
+  const float q = v * inv;
+  return fmaf(fmaf(-by, q, v), inv, q);
+}
+template <int V>
+__device__ __forceinline__ ops::Vec<V> quotient(const ops::Vec<V>& v, float by, float inv) {
+  const ops::Vec<V> q = ops::mul(v, ops::fill<V>(inv));
+  return ops::fma(ops::fma(ops::fill<V>(-by), q, v), ops::fill<V>(inv), q);
 }
 
 // A row's values one after the other where the heads' lengths are no multiple of 8.
@@ -471,12 +491,12 @@ norm_forward_kernel(const Args a) {
         top[j] = 0.f;
         if (cols.in(j))
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) top[j] = fmaxf(top[j], fabsf(at(s[j], i)));
+          for (int i = 0; i < VEC; ++i) top[j] = larger(top[j], fabsf(at(s[j], i)));
       }
       if (a.group_log2 < 0) {
         float m = 0.f;
 #pragma unroll
-        for (int j = 0; j < NV; ++j) m = fmaxf(m, top[j]);
+        for (int j = 0; j < NV; ++j) m = larger(m, top[j]);
         m = row_reduce<true>(m, a.g, scratch[parity][1]);
 #pragma unroll
         for (int j = 0; j < NV; ++j) top[j] = m;
@@ -487,13 +507,13 @@ norm_forward_kernel(const Args a) {
           if (o < (1 << a.group_log2) / 8)
 #pragma unroll
             for (int j = 0; j < NV; ++j)
-              top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
+              top[j] = larger(top[j], __shfl_xor_sync(0xffffffffu, top[j], o));
       } else {
         // A warp has 32 columns side by side; a row has the CTA to itself.
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
           float m = top[j];
-          for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          for (int o = 16; o > 0; o >>= 1) m = larger(m, __shfl_xor_sync(0xffffffffu, m, o));
           if ((t & 31) == 0 && cols.in(j)) seg[parity][cols.col(j) >> 5] = m;
         }
         __syncthreads();
@@ -502,24 +522,24 @@ norm_forward_kernel(const Args a) {
           if (cols.in(j)) {
             const int each = 1 << (a.group_log2 - 5);
             const int from = (cols.col(j) >> a.group_log2) * each;
-            for (int k = 0; k < each; ++k) top[j] = fmaxf(top[j], seg[parity][from + k]);
+            for (int k = 0; k < each; ++k) top[j] = larger(top[j], seg[parity][from + k]);
           }
       }
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         if (!(live && cols.in(j))) continue;
         const int col = cols.col(j);
-        const float m = fmaxf(top[j], kAmaxFloor);
-        const float inv = kE4m3Max / m;
+        const float scale = quotient(larger(top[j], kAmaxFloor), kE4m3Max, 1.f / kE4m3Max);
+        const float inv = __frcp_rn(scale);
         if (a.group_log2 < 0) {
-          if (t == 0 && j == 0) a.scales[row] = m * (1.f / kE4m3Max);
+          if (t == 0 && j == 0) a.scales[row] = scale;
         } else if ((col & ((1 << a.group_log2) - 1)) == 0) {
-          a.scales[(row0 + col) >> a.group_log2] = m * (1.f / kE4m3Max);
+          a.scales[(row0 + col) >> a.group_log2] = scale;
         }
         unsigned char* p = reinterpret_cast<unsigned char*>(a.y) + row0 + col;
         if constexpr (VEC == 8) {
 #pragma unroll
-          for (int i = 0; i < X::kN; ++i) s[j].v[i] = ops::mul(s[j].v[i], ops::fill<X::kW>(inv));
+          for (int i = 0; i < X::kN; ++i) s[j].v[i] = quotient(s[j].v[i], scale, inv);
           const uint2 q = make_uint2(pack_e4m3(at(s[j], 0), at(s[j], 1), at(s[j], 2), at(s[j], 3)),
                                      pack_e4m3(at(s[j], 4), at(s[j], 5), at(s[j], 6), at(s[j], 7)));
           if (cols.whole(j)) {
@@ -530,7 +550,7 @@ norm_forward_kernel(const Args a) {
               if (cols.valid(j, i)) p[i] = (unsigned char)((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
           }
         } else {
-          *p = (unsigned char)pack_e4m3(at(s[j], 0) * inv, 0.f, 0.f, 0.f);
+          *p = (unsigned char)pack_e4m3(quotient(at(s[j], 0), scale, inv), 0.f, 0.f, 0.f);
         }
       }
     }
