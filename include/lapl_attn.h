@@ -319,7 +319,8 @@ lapl_status lapl_attn_forward_noalloc(lapl_attn_handle h, const void* q, const v
  *   dout            device [B,H,N,d] fp32, dLoss/dO;
  *   dq, dk, dv      device [B,H,N,d] fp32, written (fp32 also for bf16 inputs);
  *   dbias           device [H,m] fp32 or NULL: written with the sum over the batch of
- *                   dLoss/dbias (zeros when whiten = 0);
+ *                   dLoss/dbias (zeros when whiten = 0, and for B == 0, which writes
+ *                   nothing else);
  *   fwd_workspace   the workspace of that forward, which must have been
  *                   lapl_attn_forward_train on the same handle, untouched since: the backward
  *                   reads the landmarks, the Newton-Schulz iterates, A, B, the column

@@ -191,9 +191,6 @@ class LaplacianNystromAttention:
                            self.bwd_workspace_bytes, st.cuda_stream)
         if max_norm is not None:
             all_four = [g["dq"], g["dk"], g["dv"], g["dbias"]]
-            if c.batch == 0:   # an empty batch writes no gradient, and the bias's is zero
-                with torch.cuda.stream(st):
-                    g["dbias"].zero_()
             if getattr(self, "_clip", None) is None:
                 with torch.cuda.device(q.device):
                     self._clip = GradClip([t.numel() for t in all_four], ["f32"] * 4)

@@ -625,7 +625,16 @@ lapl_status lapl_attn_backward(lapl_attn_handle h, const void* q, const void* k,
                                size_t bwd_workspace_bytes, void* stream) {
   if (!h) return LAPL_ERR_INVALID_ARG;
   if (h->geo.cg) return LAPL_ERR_UNSUPPORTED;
-  if (h->geo.bh == 0) return LAPL_OK;
+  if (h->geo.bh == 0) {   // nothing but dbias, an empty sum
+    if (!dbias) return LAPL_OK;
+    if ((uintptr_t)dbias & 3u) return LAPL_ERR_ALIGNMENT;
+    const cudaError_t e =
+        cudaMemsetAsync(dbias, 0, (size_t)h->cfg.heads * h->geo.m * sizeof(float),
+                        static_cast<cudaStream_t>(stream));
+    if (e == cudaSuccess) return LAPL_OK;
+    set_error(h, e, "backward");
+    return LAPL_ERR_CUDA;
+  }
   if (!q || !k || !v || !dout || !dq || !dk || !dv || !fwd_workspace || !bwd_workspace)
     return LAPL_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(dout) || !aligned16(dq) ||
