@@ -35,7 +35,8 @@ from ._lib import (LAPL_F8E4M3, LAPL_GATE_DECAY, LAPL_GATE_SIGMOID, LAPL_SCAN_CH
                    lapl_scan_backward, lapl_scan_config, lapl_scan_create, lapl_scan_destroy,
                    lapl_scan_device_errors, lapl_scan_forward, lapl_scan_last_error,
                    lapl_scan_plan_info_get, lapl_scan_set_fault_injection)
-from .operators import (GatedScan, GradClip, ResidualNorm, make_norm_config, make_scan_config)
+from .operators import (FLOAT_MAX, GatedScan, GradClip, ResidualNorm, make_norm_config,
+                        make_scan_config)
 
 __all__ = [
     "LaplacianNystromAttention", "LaplAttnError", "lapl_attn_config", "lapl_attn_debug",
@@ -180,8 +181,8 @@ class LaplacianNystromAttention:
             self.bwd_workspace_bytes = lapl_attn_backward_workspace_size(self.handle)
             self.bwd_workspace = torch.empty(max(self.bwd_workspace_bytes, 256),
                                              dtype=torch.uint8, device=q.device)
-        if max_norm is not None and not 0 <= max_norm < float("inf"):
-            raise ValueError(f"max_norm must be finite and not negative, got {max_norm}")
+        if max_norm is not None and not 0 <= max_norm <= FLOAT_MAX:
+            raise ValueError(f"max_norm must be finite in fp32 and not negative, got {max_norm}")
         st = stream if stream is not None else torch.cuda.current_stream()
         lapl_attn_backward(self.handle, q.data_ptr(), k.data_ptr(), v.data_ptr(),
                            bias.data_ptr() if bias is not None else None, dout.data_ptr(),

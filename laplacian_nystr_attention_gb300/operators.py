@@ -18,6 +18,8 @@ from ._lib import (LAPL_BF16, LAPL_F32, LAPL_F8E4M3, LAPL_GATE_DECAY, LAPL_GATE_
 
 _DTYPES = {"f32": LAPL_F32, "bf16": LAPL_BF16, "f8": LAPL_F8E4M3}
 _GATES = {"decay": LAPL_GATE_DECAY, "sigmoid": LAPL_GATE_SIGMOID}
+#: The largest fp32 value, and so the largest norm to clip to.
+FLOAT_MAX = 3.4028234663852886e38
 
 
 def make_scan_config(sequences, tokens, channels, gate="sigmoid", reverse=0, in_dtype="f32",

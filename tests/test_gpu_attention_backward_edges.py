@@ -33,3 +33,21 @@ def test_an_empty_batch_gives_a_zero_bias_gradient():
     side.synchronize()
     assert (got[3] == 0).all()
     att.close()
+
+
+@pytest.mark.parametrize("bad", [-1.0, float("nan"), float("inf"), 1e39, -1e39])
+def test_a_max_norm_that_is_none_is_refused_before_the_backward(bad):
+    """What fp32 does not hold, too; no gradient is written."""
+    import laplacian_nystr_attention_gb300 as lna
+    w = WORKLOADS["tiny_f32"]
+    att = lna.LaplacianNystromAttention(lna.make_config(**w.config()))
+    q = torch.randn(w.batch, w.heads, w.n, w.head_dim, device="cuda")
+    att.forward(q, q, q, keep_for_backward=True)
+    grads = {name: torch.full_like(q, 7.0) for name in ("dq", "dk", "dv")}
+    with pytest.raises(ValueError):
+        att.backward(q, q, q, q, grads=grads, max_norm=bad)
+    torch.cuda.synchronize()
+    assert all((t == 7.0).all() for t in grads.values())
+    att.backward(q, q, q, q, grads=grads, max_norm=3.4028234663852886e38)
+    assert torch.isfinite(att.grad_norm)
+    att.close()
