@@ -138,7 +138,10 @@ class _Plan:
 
 class GatedScan(_Plan):
     """h_i = a_i h_{i-1} + x_i ("decay": a = g) or + (1 - a_i) x_i ("sigmoid": a = sigmoid(g)) over
-    the tokens of each sequence, for every channel."""
+    the tokens of each sequence, for every channel.
+
+    Long sequences wait for one another's parts on the GPU, each wait bounded to a second; results
+    of a call whose wait gave up are undefined, and check_device_errors() is what tells."""
 
     _destroy = staticmethod(_lib.lapl_scan_destroy)
 
@@ -213,6 +216,14 @@ class GatedScan(_Plan):
             None if dfinal is None else self._check(dfinal, self._state["dfinal"]),
             at_dx, at_dg, at_dh0, self._raw_stream(self._index))
         return dx, dg, dh0
+
+    def check_device_errors(self, stream=None):
+        """Raises LaplAttnError if a wait on this device has given up since the last time it was
+        asked; waits for the stream's work so far (not while it is captured)."""
+        if stream is not None:
+            with self._on(stream, ()):
+                return self.check_device_errors()
+        _lib.lapl_scan_device_errors(self.handle, self._raw_stream(self._index))
 
     def _like(self, grad, want, like):
         """A gradient and its address: the one given, checked, or a new one in rows as like's."""

@@ -60,6 +60,26 @@ def test_wait_that_gives_up_early(S, N, C, dtype, wait_ns, skip_last):
     assert lna.lapl_scan_device_errors(plan.handle, st) == 0
 
 
+def test_a_wait_that_gave_up_is_told_in_python():
+    import laplacian_nystr_attention_gb300 as lna
+    plan = lna.GatedScan(lna.make_scan_config(2, 5000, 64))
+    x, g = randn(2, 5000, 64), randn(2, 5000, 64, seed=1)
+    plan.forward(x, g)
+    plan.check_device_errors()
+    lna.lapl_scan_set_fault_injection(plan.handle, 2_000_000, 3)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (None, side):
+        plan.forward(x, g, stream=stream)
+        with pytest.raises(lna.LaplAttnError) as e:
+            plan.check_device_errors(stream=stream)
+        assert e.value.status == 6
+        plan.check_device_errors()
+    lna.lapl_scan_set_fault_injection(plan.handle, 0, 0)
+    plan.forward(x, g)
+    plan.check_device_errors()
+
+
 # ---- gates at both ends -------------------------------------------------------------------
 
 def sigmoid_scan(x, g, h0, dout, dfinal):
