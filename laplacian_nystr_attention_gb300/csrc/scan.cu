@@ -126,7 +126,7 @@ __device__ __forceinline__ void exchange(const Shared<V, kCluster>& sm, int pari
       for (int r = 0; r < cluster; ++r)
         *cg::this_cluster().map_shared_rank(to, r) = make_float2(ta, tb);
     }
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
     // Meanwhile, the map of the CTA's runs before this thread's.
     Vec<V> pa = fill<V>(1.f), pb = fill<V>(0.f);
 #pragma unroll 4
@@ -137,7 +137,7 @@ __device__ __forceinline__ void exchange(const Shared<V, kCluster>& sm, int pari
         pa.f[v] *= runs[v].x;
       }
     }
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 #pragma unroll 4
     for (int k = 0; k < cluster; ++k) {
       const int r = kDown ? cluster - 1 - k : k;
