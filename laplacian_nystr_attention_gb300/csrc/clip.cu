@@ -32,6 +32,8 @@
 namespace lapl {
 namespace clip {
 
+using ops::Pair;
+
 constexpr int kThreads = 512;
 constexpr int kCtas = 4;             // of an SM, all resident at once: 32 registers a thread
 constexpr int kMinPiece = 2048, kMaxPiece = 65536;   // values, powers of two
@@ -122,18 +124,6 @@ __device__ __forceinline__ void each(const T* p, int n, Use use) {
   for (; k < n; k += kThreads) use(k, p[k]);
 }
 
-// A sum held as two floats, its value and what that lost (Knuth's two-sum): 48 bits without the
-// double-precision units, of which this GPU has few (sums in double took 36 us of a pass of 57).
-// Where the sum is not finite, hi says so and lo nothing.
-struct Pair {
-  float hi, lo;
-  __device__ __forceinline__ void add(float v, float v_lo = 0.f) {
-    const float s = hi + v, b = s - hi;
-    lo += (hi - (s - b)) + (v - b) + v_lo;
-    hi = s;
-  }
-  __device__ __forceinline__ float value() const { return isfinite(hi) ? hi + lo : hi; }
-};
 struct Pairs {
   Pair of[3];   // low, tiny, high
 };

@@ -68,3 +68,24 @@ def test_8_bit_rows_with_a_nan(group, d):
     assert torch.equal(scales[0, keep], good[1][0, keep])
     assert torch.isnan(q[0, 7].float()).all() and torch.isnan(scales[0, 7]).all()
     assert torch.isnan(q[0, 9, 0].float()) and torch.isnan(scales[0, 9, 0])
+
+
+# ---- sums over rows -----------------------------------------------------------------------
+
+@pytest.mark.parametrize("rows,width", [(32, 64), (16, 100), (3, 256), (300, 1024), (60, 1024),
+                                        (300, 2049), (300, 4096), (150, 16384), (150, 9999)])
+@pytest.mark.parametrize("grad", ["f32", "bf16"])
+def test_dweight_keeps_small_rows_beside_large_ones(rows, width, grad):
+    """A row of 2^30, one of -2^30 and ones: what is left after the large ones cancel is the ones,
+    exactly where each row has threads of its own (sums in fp32 lose tens of them).
+
+    A thread adds its own rows in fp32.  152 CTAs or more share the rows, so that it has at most
+    rows / 152 of them, rounded up, and beside a large one loses the others, 1 each: twice that less
+    one in all."""
+    import laplacian_nystr_attention_gb300 as lna
+    plan = lna.ResidualNorm(lna.make_norm_config(1, 1, rows, width, grad_dtype=grad))
+    dy = torch.ones(1, rows, width, device="cuda", dtype=TYPES[grad])
+    dy[0, 0], dy[0, rows // 2] = 2.0 ** 30, -(2.0 ** 30)
+    total, rstd = torch.ones(1, rows, width, device="cuda"), torch.ones(1, rows, device="cuda")
+    _, _, dweight = plan.backward(total, rstd, None, dy, grads={"dx": None})
+    assert ((dweight - (rows - 2)).abs() <= 2 * (-(-rows // 152) - 1)).all()
