@@ -45,14 +45,14 @@ constexpr int kThreads = 256;
 constexpr int kMaxCluster = 16;
 constexpr int kMaxChannels = 64;      // channels of a tile: 32 lanes x 2
 
-// In dynamic shared memory: maps of the runs, by round parity ([2][threads V]); of the cluster's tiles
+// In dynamic shared memory: maps of the runs, by round parity ([2][kThreads V]); of the cluster's tiles
 // ([2][kMaxCluster][kMaxChannels]); and with the sigmoid gate what a thread keeps of each token from
 // its first walk to the second ([kT][threads] of V values).
 template <int V, bool kCluster>
 struct Shared {
   unsigned char* base;
   __device__ __forceinline__ float2* run(int parity) const {
-    return reinterpret_cast<float2*>(base) + parity * (int)blockDim.x * V;
+    return reinterpret_cast<float2*>(base) + parity * kThreads * V;
   }
   __device__ __forceinline__ float2* tile(int parity, int rank) const {
     return run(2) + (parity * kMaxCluster + rank) * kMaxChannels;
@@ -63,7 +63,7 @@ struct Shared {
   }
 };
 constexpr unsigned shared_bytes(int threads, int v, bool cluster, bool sig) {
-  return 8u * (2 * threads * v + (cluster ? 2 * kMaxCluster * kMaxChannels : 0)) +
+  return 8u * (2 * kThreads * v + (cluster ? 2 * kMaxCluster * kMaxChannels : 0)) +
          (sig ? 4u * v * kT * threads : 0u);
 }
 
