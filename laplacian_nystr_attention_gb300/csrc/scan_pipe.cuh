@@ -168,20 +168,13 @@ __device__ __forceinline__ unsigned long long nanoseconds() {
   asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
   return t;
 }
-// Two words of a stage that are one thread's own, V floats.
+// What a thread keeps of token k, V floats, where the warp's g and x were: 8 tokens in each of the two, of
+// which one is `apart` bytes behind the other.  Whoever keeps the first of a half has met the warp after
+// all of its threads read that half's words.
+constexpr int kHalf = kT / 2;
 template <int V>
-__device__ __forceinline__ void keep(unsigned at, unsigned apart, const Vec<V>& v) {
-#pragma unroll
-  for (int i = 0; i < V; ++i)
-    asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + i * apart), "f"(v.f[i]) : "memory");
-}
-template <int V>
-__device__ __forceinline__ Vec<V> kept(unsigned at, unsigned apart) {
-  Vec<V> v;
-#pragma unroll
-  for (int i = 0; i < V; ++i)
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v.f[i]) : "r"(at + i * apart) : "memory");
-  return v;
+__device__ __forceinline__ unsigned keep_at(unsigned warp_stage, unsigned apart, int k) {
+  return warp_stage + (k < kHalf ? 0u : apart) + (k % kHalf * 32 + ((int)threadIdx.x & 31)) * (V * 4);
 }
 
 // Until the phase of the given parity is complete, or false after `bound` ns.
@@ -460,11 +453,17 @@ scan_forward_pipe_kernel(const Args a, unsigned* err) {
         Raw<kIn16, V> rg[kT];
 #pragma unroll
         for (int k = 0; k < kT; ++k) rg[k] = read_raw<kIn16, V>(from + k * T::kRow);
+        Raw<kIn16, V> rx[kT];
         gates<8, kIn16, V>(rg, i0, live, [&](int k, const Gate<V>& g) {
-          const Vec<V> b = mul(g.z, widen(read_raw<kIn16, V>(from + T::kWarp + k * T::kRow)));
+          if (k % kHalf == 0) {
+#pragma unroll
+            for (int u = k; u < k + kHalf; ++u) rx[u] = read_raw<kIn16, V>(from + T::kWarp + u * T::kRow);
+            __syncwarp();
+          }
+          const Vec<V> b = mul(g.z, widen(rx[k]));
           factor.take(g);
           m.b = fma(g.a, m.b, b);
-          keep(from + k * T::kRow, T::kWarp, b);
+          put_state(keep_at<V>(ring + stage * kStage, T::kWarp, k), b);
           decay[k] = g.a;
         });
       } else {
@@ -483,8 +482,12 @@ scan_forward_pipe_kernel(const Args a, unsigned* err) {
       }
       m.a = factor.value();
       auto next = [&](int k, const Vec<V>& h) {
-        if constexpr (kSig) return fma(decay[k], h, kept<V>(from + k * T::kRow, T::kWarp));
-        else return fma(decay[k], h, widen(read_raw<kIn16, V>(from + T::kWarp + k * T::kRow)));
+        Vec<V> b;
+        if constexpr (kSig) {
+          get_state(keep_at<V>(ring + stage * kStage, T::kWarp, k), b);
+          return fma(decay[k], h, b);
+        }
+        return fma(decay[k], h, widen(read_raw<kIn16, V>(from + T::kWarp + k * T::kRow)));
       };
       put_map(smem + l.runs + (team * kWarps * 32 + wt * 32 + lane) * (2 * V * 4), m);
       bar_arrive(runs_bar<kTeams>(team), kWarps * 32 + 32);
@@ -595,12 +598,19 @@ scan_backward_pipe_kernel(const Args a, unsigned* err) {
         Raw<kIn16, V> rg[kT];
 #pragma unroll
         for (int k = 0; k < kT; ++k) rg[k] = read_raw<kIn16, V>(from + my + k * T::kRow);
+        Raw<kIn16, V> rx[kT];
         gates<kT, kIn16, V>(rg, i0, live, [&](int k, const Gate<V>& g) {
-          const Vec<V> x = widen(read_raw<kIn16, V>(from + my + T::kWarp + k * T::kRow));
+          if (k % kHalf == 0) {
+#pragma unroll
+            for (int u = k; u < k + kHalf; ++u)
+              rx[u] = read_raw<kIn16, V>(from + my + T::kWarp + u * T::kRow);
+            __syncwarp();
+          }
+          const Vec<V> x = widen(rx[k]);
           factor.take(g);
           slope[k] = mul(g.z, sub(h, x));
           h = fma(g.a, h, mul(g.z, x));
-          keep(from + my + k * T::kRow, T::kWarp, g.z);
+          put_state(keep_at<V>(from, T::kWarp, k), g.z);
           decay[k] = g.a;
         });
       } else {
@@ -646,7 +656,7 @@ scan_backward_pipe_kernel(const Args a, unsigned* err) {
           const Vec<V> D = add(widen(read_raw<kGrad16, V>(from + my_grad + k * TG::kRow)), E);
           E = mul(decay[k], D);
           Vec<V> z = {}, dx, dg;
-          if constexpr (kSig) z = kept<V>(from + my + k * T::kRow, T::kWarp);
+          if constexpr (kSig) get_state(keep_at<V>(from, T::kWarp, k), z);
           step_gradients<kSig>(z, slope[k], D, E, dx, dg);
           if (k < left) {
             store_vec<kGrad16>(qx, dx);
