@@ -8,9 +8,9 @@
 // CTA b sums the squares of pieces b, b + grid, ... and writes one partial.  Second pass: every CTA
 // sums all partials in the same order, so each has the same norm to the last bit, and scales its
 // pieces.  HBM-bound: the first pass reads every value, the second reads and writes it.  Measured:
-// 2^28 values (540 MB of bf16 and fp32) 80 us for the norm (the copy's rate), 256 us to clip
+// 2^28 values (540 MB of bf16 and fp32) 82 us for the norm (the copy's rate), 258 us to clip
 // them into other tensors, of which 239 are the bytes of both passes at that rate; 24 tensors of 2^20
-// values together 8.5 us, the latency of two launches.
+// values together 7.7 us, the latency of two launches.
 //
 // Squares.  fp32 holds values over 2^-149 .. 2^128, whose squares need twice that range.  There are
 // three sums: of (x 2^35)^2, and for where that vanishes or overflows of (x 2^86)^2 and (x 2^-72)^2.  Their

@@ -1,9 +1,9 @@
 // norm.cu -- residual addition + root-mean-square norm: the backward kernel, and lapl_norm_* of
 // include/lapl_ops.h (norm_kernels.cuh has the formulas and the work split).
 //
-// HBM-bound: the backward at 32 x 784 rows of 256 fp32 values takes 19.1 us (the bytes: 19.0) and 23.2
+// HBM-bound: the backward at 32 x 784 rows of 256 fp32 values takes 20 us (the bytes: 19.0) and 23.9
 // with the launch that sums dweight's partials; 8193 rows of 2049 bf16 values, whose vectors start
-// anywhere, 35.7 us (69%: issue in 56% of the cycles, the rows' reductions, and 4 us for dweight).
+// anywhere, 36.3 us (68%: issue in 63% of the cycles, the rows' reductions, and 4 us for dweight).
 #include <algorithm>
 #include <new>
 

@@ -24,8 +24,8 @@
 // pointer off 16 bytes) runs with vectors of one value, a row to a CTA.
 //
 // HBM-bound.  Measured (of 6.78 TB/s): the attention's fp32 output at 4 x 8 x 16384 x 64 with a bf16
-// residual 52 us (6.5 TB/s, 95%); rows of 4096 bf16 values to e4m3 by groups of 128 38.1 us (91%; a
-// value's conversions and scaling keep issue at 67%).
+// residual 52 us (6.5 TB/s, 95%); rows of 4096 bf16 values to e4m3 by groups of 128 38.3 us (91%; a
+// value's conversions and division keep issue at 68%).
 #pragma once
 
 #include "ops_common.cuh"

@@ -19,9 +19,9 @@
 // The order of every composition is fixed, so results are the same bit for bit from call to call.
 // What bounds it is the exchange: a round of tiles costs a load, a barrier and a walk one after the
 // other, whatever the bytes.  These kernels take sequences longer than scan_few.cu's few tokens and
-// shorter than scan_pipe.cuh's are made for (512 x 256 x 64 bf16: 14 us forward, 23
-// backward, of which 7.4 and 12.7 are bytes), odd bf16 channel counts, and rows of odd lengths where
-// they are many (16 x 4096 x 333 fp32: 64 us of 39).
+// shorter than scan_pipe.cuh's are made for (512 x 256 x 64 bf16, sigmoid and decay gate: 14.7 and 11.7 us
+// forward, 23.3 and 18.8 backward, of which 7.4 and 12.7 are bytes), odd bf16 channel counts, and rows
+// of odd lengths where they are many (16 x 4096 x 333 fp32: 69 and 62 us of 39).
 //
 // The sigmoid gate's a and z = 1 - a are computed each for itself: neither is accurate as 1 less the
 // other where it is small.  Near a = 1 the rounding of a is a relative error of z of 2^-24 / z, and that
@@ -526,9 +526,10 @@ namespace {
 constexpr unsigned long long kWaitNs = 1000000000ull;   // one second
 
 // Tokens from which the pipelined kernels are taken; shorter sequences leave their teams without work.
-// 32 x 16384 x 64 ones of bf16 fall to half the time; at 800 tokens forward, 40 to 700 sequences of 32
-// to 128 channels, bf16 93 to 114% of the other kernel's time, fp32 97 to 118; backward 63 to 95%, at
-// 512 tokens of bf16 80 to 97%, fp32 94 to 115, at 256 of bf16 100 to 133.
+// In percent of the other kernel's time, 40 to 700 sequences of 32 to 128 channels, both gates, mean and
+// range: forward at 800 tokens bf16 97 (90 to 108), fp32 108 (95 to 123), which breaks even later, at
+// 1600 95 (84 to 101); at 512 117 and 129.  Backward at 800 bf16 82 (61 to 99), fp32 91 (71 to 106), at 512
+// 98 (83 to 120) and 110 (88 to 128), at 256 bf16 118.
 constexpr int kPipeTokens = 768, kPipeTokensBackward16 = 512;
 
 bool whole(std::initializer_list<const void*> pointers, int bytes) {
@@ -684,8 +685,8 @@ lapl_status lapl_scan_create(const lapl_scan_config* cfg, lapl_scan_handle* out)
   }
   for (int v = 1; v <= 2; ++v) p->geo[v - 1] = scan::geometry(*cfg, sms, v);
   // Tokens one after the other in a thread: where there are few, and with threads for the GPU some more
-  // (bf16 and fp32, 8 tokens of 64 x 4096 channels: 42 and 38% of the other kernel's time, of 1 x 4096,
-  // 110 and 117; 32 tokens of 64 x 4096: 94 and 80, of 256 x 512: 107 and 98).
+  // (sigmoid gate, bf16 and fp32, 8 tokens of 64 x 4096 channels: 50 and 54% of the other kernel's time, of
+  // 1 x 4096, 100 and 115; 32 tokens of 64 x 4096: 101 and 84, of 256 x 512: 107 and 98).
   p->few = cfg->tokens <= 8 ||
            (cfg->tokens <= 32 && (long long)cfg->sequences * cfg->channels >= 1600LL * sms);
   // Long sequences: the pipelined kernels, for bf16 inputs in pairs of channels.
@@ -747,8 +748,8 @@ lapl_status lapl_scan_forward(lapl_scan_handle p, const void* x, const void* g, 
     const int pair = c.in_dtype == LAPL_BF16 ? 2 : 1;
     a.fine = !coarse(x, a.x_stride, ib) || !coarse(g, a.g_stride, ib);
     // Without 16-byte pieces, and with sequences and channels for nearly the whole GPU, the other
-    // kernel is the faster one (16 x 4096 x 333 fp32, clusters of 2: 64 against 83 us; 5 x 8484 x 23,
-    // of 16: 17 against 9).
+    // kernel is the faster one (sigmoid gate, 16 x 4096 x 333 fp32, clusters of 2: 68 against 87 us;
+    // 5 x 8484 x 23, of 16: 12 against 8; 2 x 9001 x 257: 25 against 19).
     const bool other = a.fine && p->geo[pair - 1].cluster <= 2;
     if (!other && whole({x, g}, 4) && whole({out}, pair * ob) &&
         whole({h0, states, final_state}, pair * 4))
@@ -793,8 +794,8 @@ lapl_status lapl_scan_backward(lapl_scan_handle p, const void* x, const void* g,
     const int pair = c.in_dtype == LAPL_BF16 ? 2 : 1;
     a.fine = !coarse(x, a.x_stride, ib) || !coarse(g, a.g_stride, ib);
     a.fine_dout = !coarse(dout, a.c, gb);
-    // As forward, for the whole GPU (24 x 4096 x 333 fp32: 140 against 162 us; 16 x 4096 x 333, clusters
-    // of 2: 141 against 126).
+    // As forward, for the whole GPU (sigmoid gate, 24 x 4096 x 333 fp32: 151 against 166 us; 64 x 1024 x
+    // 99: 35 against 47; 16 x 4096 x 333, clusters of 2: 142 against 127).
     const bool other = a.fine && p->geo[pair - 1].cluster == 1;
     if (!other && whole({x, g}, 4) && whole({dout, dx, dg}, pair * gb) &&
         whole({states, dfinal, dh0}, pair * 4) && !(a.fine_dout && pair * gb < 4))

@@ -102,10 +102,10 @@ struct Gate {
 // The hardware's base-2 exponential is good to 2 ulp, but its argument t, g log2 e rounded, is a
 // relative error of |t| ulp in exp(g).  What t lacks, r, comes out of one more step or two, and
 // 2^(t + r) = 2^t (1 + r ln 2) puts it back.  (bf16: log2 e in two parts, of which 16 bits times g are
-// exact; r ln 2 is at most 5e-4, whose square costs 2^-24 and a half at the ends.)  g is held within [-88, 88],
-// where nothing overflows, and everything is scaled by 1/16, so that 16 / (1 + exp(g)) stays in the normal
-// range: a and z below 2^-126 (|g| above 87.3) are zero, and the other one is then 1.  NaN passes
-// through.
+// exact; r ln 2 is at most 5e-4, whose square costs 2^-24 and a half at the ends.)  g is held within
+// [-88, 88], where nothing overflows, and everything is scaled by 1/16, so that 16 / (1 + exp(g)) stays in
+// the normal range: a and z below 2^-126 (|g| above 87.3) are zero, and the other one is then 1.  NaN
+// passes through.
 template <bool kSig, bool k16, int V>
 __device__ __forceinline__ Gate<V> gate_of(Raw<k16, V> w) {
   if constexpr (!kSig) {

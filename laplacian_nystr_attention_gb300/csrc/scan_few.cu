@@ -3,11 +3,11 @@
 //
 // A thread has all tokens of four channels (one where rows or pointers are not multiples of four
 // elements) and goes through the steps with the state in registers: of up to four tokens it reads all
-// at once, of more some at a time with the next ones on their way.  128 x 1 x 4096 bf16 takes 2.4 us where
-// the kernel for longer sequences, 32 threads a CTA and 16 tokens a thread, takes 15.8; 64 x 1 x 512 1.7
-// and 2.9; 20000 x 2 x 512 34 (89% of the copy's rate) and 317; 64 x 8 x 4096 4.1 and 9.8.  The backward
-// of up to eight tokens holds them all: 64 x 1 x 4096 2.0 and 10.7 us, 64 x 8 x 4096 6.9 and 13.2.  What
-// bounds them is the launch, then the bytes.
+// at once, of more some at a time with the next ones on their way.  With the sigmoid gate 128 x 1 x 4096
+// bf16 takes 2.5 us where the kernel for longer sequences, 32 threads a CTA and 16 tokens a thread, takes
+// 13; 64 x 1 x 512 1.7 and 3.3; 20000 x 2 x 512 31 (78% of the copy's rate) and 231; 64 x 8 x 4096 4.3 and
+// 8.5.  The backward of up to eight tokens holds them all: 64 x 1 x 4096 2.1 and 9.6 us, 64 x 8 x 4096 8.4
+// and 11.  What bounds them is the launch, then the bytes, and with many tokens a thread its own steps.
 #include "scan_few.cuh"
 
 namespace lapl {

@@ -15,17 +15,20 @@
 //   * Each warp copies its own tokens ahead into its own ring of stages (cp.async, 16 bytes at a
 //     time): no barrier between warps, and the bytes in flight are those of the ring.  A stage is kept
 //     until its tokens are read a second time, so that registers hold the decays alone (and in the
-//     backward the slopes): holding the tokens as well took 73 us instead of 58 below.  With the
+//     backward the slopes): holding the tokens as well took 73 us instead of 58 once.  With the
 //     sigmoid gate a thread leaves there, in the place of its own g and x, what it needs the second
 //     time: z x, or in the backward z.
 // Two values go through the packed fp32 instructions (bf16 inputs).
 //
-// Measured (of 6.78 TB/s): 32 x 16384 x 64 bf16, sigmoid gate: 38.7 us forward (77%) and 57.5 us backward
-// (88%), decay gate 33.3 (89%) and 56.1 (90%); 4 x 8192 x 512 fp32: 33.0 and 54.6 us (90 and 92%).  bf16
-// with the sigmoid gate is bound by issue and by the chain, the others by memory.  Teams of four warps
-// put one on each scheduler, so that all four end together: with three teams of six the slowest
-// scheduler held up the chain (50.8 against 44.0 us).  Sequences and channels too few for the GPU's
-// clusters cost the rest: 8 x 65536 x 64 bf16 runs in 32-byte pieces of a row on 128 SMs, 44.7 us (69%).
+// Measured (of 6.78 TB/s): 32 x 16384 x 64 bf16, sigmoid gate: 40.3 us forward (74%) and 60.7 us backward
+// (84%), decay gate 33.7 (88%) and 55.2 (92%); 4 x 8192 x 512 fp32, sigmoid: 34.7 and 53.6 us (86 and
+// 93%).  bf16 with the sigmoid gate is bound by issue and by the chain, the others by memory.  Teams of
+// four warps put one on each scheduler, so that all four end together: with three teams of six the
+// slowest scheduler held up the chain (50.8 us where four of four took 44.0).  Sequences and channels too
+// few for the GPU's clusters cost the rest: 8 x 65536 x 64 bf16 runs in 32-byte pieces of a row on 128
+// SMs, 47.5 us (65%) with the sigmoid gate and the states kept.  That gate's numbers are worked out for 8
+// tokens at a time, 16 in the backward: of 2, 4, 8 and 16 the best (forward 49.5, 48.6, 48.1 and 49.4 us
+// there; backward 64.4, 63.5, 63.5 and 61.9 at 32 x 16384 x 64).
 //
 // Copies are of 16 bytes where rows and pointers allow it, else of each thread's own 4 or 8 (which
 // takes more instructions).  scan.cu's kernels take short sequences and what is odd beyond that; where
