@@ -182,7 +182,7 @@ __device__ __forceinline__ unsigned keep_at(unsigned warp_stage, unsigned apart,
 
 // Until the phase of the given parity is complete, or false after `bound` ns.
 __device__ __forceinline__ bool wait_phase(unsigned bar, unsigned parity, unsigned long long bound) {
-  const unsigned at_once = (unsigned)min(bound, 1000000000ull);   // a look may last that long itself
+  const unsigned at_once = (unsigned)min(bound, 1000000ull);   // a look may last that long: up to 1 ms
   auto done = [&] {
     unsigned d;
     asm volatile("{\n\t.reg .pred p;\n\t"
