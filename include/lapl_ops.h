@@ -35,8 +35,8 @@ enum { LAPL_F8E4M3 = 2 };
  *   LAPL_GATE_DECAY:    h_i = a_i h_{i-1} + x_i,              a_i = g_i, which must be in [-1, 1]
  *   LAPL_GATE_SIGMOID:  h_i = a_i h_{i-1} + (1 - a_i) x_i,    a_i = 1 / (1 + exp(-g_i))
  * with h_{-1} = h0 (zeros if NULL).  The processing order is the tokens' order, or with reverse
- * the opposite one, from token len-1 down to token 0.  Arithmetic and states are fp32; decays, and
- * with the sigmoid gate 1 - a, below 2^-126 count as zero.  A state that is not finite leaves the
+ * the opposite one, from token len-1 down to token 0.  Arithmetic and states are fp32; with the
+ * sigmoid gate an a or a 1 - a below 2^-126 counts as zero.  A state that is not finite leaves the
  * later ones of its sequence and channel, the final one among them, not finite: infinite or NaN.
  */
 typedef enum { LAPL_GATE_DECAY = 0, LAPL_GATE_SIGMOID = 1 } lapl_gate;
