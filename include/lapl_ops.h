@@ -175,8 +175,9 @@ lapl_status lapl_norm_destroy(lapl_norm_handle h);
  *
  * norm = sqrt(sum of the squares of every value of every tensor), out = value * scale with
  * scale = max_norm / norm where norm > max_norm, and 1 otherwise.  Squares neither overflow nor
- * vanish: any norm that fp32 holds, down to its smallest values, comes out right.  A norm that is not finite is reported as
- * such and leaves every value as it is.  A scale below 2^-126 has fewer bits than others.
+ * vanish: any norm that fp32 holds, down to its smallest values, comes out right.  A norm that is
+ * not finite is reported as such and leaves every value as it is.  A scale below 2^-126 has fewer
+ * bits than others.
  */
 typedef struct {
   int tensors;             /* T >= 0                                                            */

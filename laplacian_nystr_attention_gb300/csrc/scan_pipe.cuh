@@ -16,7 +16,7 @@
 //     time): no barrier between warps, and the bytes in flight are those of the ring.  A stage is kept
 //     until its tokens are read a second time, so that registers hold the decays alone (and in the
 //     backward the slopes): holding the tokens as well took 73 us instead of 58 once.  With the
-//     sigmoid gate a thread leaves there, in the place of its own g and x, what it needs the second
+//     sigmoid gate a thread leaves there, in the place of the warp's g and x, what it needs the second
 //     time: z x, or in the backward z.
 // Two values go through the packed fp32 instructions (bf16 inputs).
 //
