@@ -8,8 +8,9 @@ Linear Attention with Laplacian Kernel", explainer pages.)
 The compute lives in liblapl_attn.so (hand-written CUDA kernels, C ABI in
 include/lapl_attn.h).  ``_lib`` binds that ABI with the same names; ``LaplacianNystromAttention``
 below is a convenience layer that uses PyTorch only to allocate device memory and to pick the
-current CUDA stream.  ``GatedScan``, ``ResidualNorm`` and ``GradClip`` (operators.py) are the same
-for the operators beside the attention (C ABI in include/lapl_ops.h).
+current CUDA stream.  ``GatedScan``, ``ResidualNorm``, ``GradClip``, ``HeadRotary``,
+``DecayAttention`` and ``AdamW`` (operators.py) are the same for the operators beside the attention
+(C ABI in include/lapl_ops.h).
 """
 from __future__ import annotations
 
@@ -35,7 +36,16 @@ from ._lib import (LAPL_F8E4M3, LAPL_GATE_DECAY, LAPL_GATE_SIGMOID, LAPL_SCAN_CH
                    lapl_scan_backward, lapl_scan_config, lapl_scan_create, lapl_scan_destroy,
                    lapl_scan_device_errors, lapl_scan_forward, lapl_scan_last_error,
                    lapl_scan_plan_info_get, lapl_scan_set_fault_injection)
-from .operators import (FLOAT_MAX, GatedScan, GradClip, ResidualNorm, make_norm_config,
+from ._lib import (LAPL_ADAMW_BLOCK, LAPL_DECAY_MAX_DIM, LAPL_ROPE_MAX_DIM, lapl_adamw_config,
+                   lapl_adamw_create, lapl_adamw_destroy, lapl_adamw_last_error, lapl_adamw_step,
+                   lapl_decay_backward, lapl_decay_config, lapl_decay_create, lapl_decay_destroy,
+                   lapl_decay_device_errors, lapl_decay_forward, lapl_decay_last_error,
+                   lapl_decay_plan_info_get, lapl_decay_set_fault_injection,
+                   lapl_decay_workspace_size, lapl_rope_backward, lapl_rope_config,
+                   lapl_rope_create, lapl_rope_destroy, lapl_rope_forward, lapl_rope_last_error,
+                   lapl_rope_workspace_size)
+from .operators import (FLOAT_MAX, AdamW, DecayAttention, GatedScan, GradClip, HeadRotary,
+                        ResidualNorm, make_decay_config, make_norm_config, make_rope_config,
                         make_scan_config)
 
 __all__ = [
@@ -58,6 +68,15 @@ __all__ = [
     "lapl_norm_backward", "lapl_norm_last_error", "lapl_norm_destroy",
     "lapl_clip_config", "lapl_clip_create", "lapl_clip_workspace_size", "lapl_clip_norm",
     "lapl_clip_apply", "lapl_clip_last_error", "lapl_clip_destroy",
+    "HeadRotary", "DecayAttention", "AdamW", "make_rope_config", "make_decay_config",
+    "LAPL_ADAMW_BLOCK", "LAPL_DECAY_MAX_DIM", "LAPL_ROPE_MAX_DIM",
+    "lapl_rope_config", "lapl_rope_create", "lapl_rope_forward", "lapl_rope_workspace_size",
+    "lapl_rope_backward", "lapl_rope_last_error", "lapl_rope_destroy",
+    "lapl_decay_config", "lapl_decay_create", "lapl_decay_workspace_size", "lapl_decay_forward",
+    "lapl_decay_backward", "lapl_decay_plan_info_get", "lapl_decay_device_errors",
+    "lapl_decay_set_fault_injection", "lapl_decay_last_error", "lapl_decay_destroy",
+    "lapl_adamw_config", "lapl_adamw_create", "lapl_adamw_step", "lapl_adamw_last_error",
+    "lapl_adamw_destroy",
 ]
 
 _DTYPES = {"f32": LAPL_F32, "bf16": LAPL_BF16}

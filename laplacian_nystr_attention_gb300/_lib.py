@@ -32,6 +32,9 @@ LAPL_F8E4M3 = 2
 LAPL_GATE_DECAY = 0
 LAPL_GATE_SIGMOID = 1
 LAPL_SCAN_CHUNK = 16
+LAPL_ADAMW_BLOCK = 256
+LAPL_ROPE_MAX_DIM = 256
+LAPL_DECAY_MAX_DIM = 128
 
 
 class lapl_attn_config(ctypes.Structure):
@@ -80,6 +83,37 @@ class lapl_norm_config(ctypes.Structure):
 class lapl_clip_config(ctypes.Structure):
     _fields_ = [("tensors", ctypes.c_int), ("counts", ctypes.POINTER(ctypes.c_longlong)),
                 ("dtypes", ctypes.POINTER(ctypes.c_int))]
+
+
+class lapl_rope_config(ctypes.Structure):
+    _fields_ = ([(name, ctypes.c_int) for name in
+                 ("batch", "tokens", "q_heads", "k_heads", "v_heads", "head_dim", "axes")]
+                + [("pairs", ctypes.POINTER(ctypes.c_int)),
+                   ("frequencies", ctypes.POINTER(ctypes.c_double)), ("interleaved", ctypes.c_int),
+                   ("norm", ctypes.c_int), ("eps", ctypes.c_float)]
+                + [(name, ctypes.c_int) for name in
+                   ("in_dtype", "out_dtype", "grad_dtype", "q_stride", "k_stride", "v_stride")])
+
+
+class lapl_decay_config(ctypes.Structure):
+    _fields_ = ([(name, ctypes.c_int) for name in
+                 ("batch", "heads", "tokens", "key_dim", "value_dim")]
+                + [("scale", ctypes.c_float)]
+                + [(name, ctypes.c_int) for name in
+                   ("reverse", "in_dtype", "out_dtype", "grad_dtype")])
+
+
+class lapl_decay_plan_info(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int) for name in
+                ("tensor_cores", "segments", "backward_tensor_cores", "backward_segments")]
+
+
+class lapl_adamw_config(ctypes.Structure):
+    _fields_ = [("tensors", ctypes.c_int), ("counts", ctypes.POINTER(ctypes.c_longlong)),
+                ("dtypes", ctypes.POINTER(ctypes.c_int)),
+                ("grad_dtypes", ctypes.POINTER(ctypes.c_int)),
+                ("weight_decay", ctypes.POINTER(ctypes.c_float)), ("beta1", ctypes.c_double),
+                ("beta2", ctypes.c_double), ("eps", ctypes.c_double), ("state_bits", ctypes.c_int)]
 
 
 class LaplAttnError(RuntimeError):
@@ -141,6 +175,28 @@ def _load():
                              sz, vp], st),
         "lapl_clip_last_error": ([H], ctypes.c_char_p),
         "lapl_clip_destroy": ([H], st),
+        "lapl_rope_create": ([ctypes.POINTER(lapl_rope_config), ctypes.POINTER(H)], st),
+        "lapl_rope_forward": ([H, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp], st),
+        "lapl_rope_workspace_size": ([H, ctypes.POINTER(sz)], st),
+        "lapl_rope_backward": ([H, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+                               st),
+        "lapl_rope_last_error": ([H], ctypes.c_char_p),
+        "lapl_rope_destroy": ([H], st),
+        "lapl_decay_create": ([ctypes.POINTER(lapl_decay_config), ctypes.POINTER(H)], st),
+        "lapl_decay_workspace_size": ([H, ctypes.POINTER(sz), ctypes.POINTER(sz)], st),
+        "lapl_decay_forward": ([H, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp], st),
+        "lapl_decay_backward": ([H, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp], st),
+        "lapl_decay_plan_info_get": ([H, ctypes.POINTER(lapl_decay_plan_info)], st),
+        "lapl_decay_device_errors": ([H, vp, ctypes.POINTER(ctypes.c_uint)], st),
+        "lapl_decay_set_fault_injection": ([H, ctypes.c_ulonglong, ctypes.c_int], st),
+        "lapl_decay_last_error": ([H], ctypes.c_char_p),
+        "lapl_decay_destroy": ([H], st),
+        "lapl_adamw_create": ([ctypes.POINTER(lapl_adamw_config), ctypes.POINTER(H)], st),
+        "lapl_adamw_step": ([H] + [ctypes.POINTER(vp)] * 7
+                            + [ctypes.c_float, vp, ctypes.c_longlong, vp, vp, ctypes.c_float, vp],
+                            st),
+        "lapl_adamw_last_error": ([H], ctypes.c_char_p),
+        "lapl_adamw_destroy": ([H], st),
     }
     for name, (args, res) in sigs.items():
         fn = getattr(lib, name)
@@ -166,7 +222,13 @@ EXPORTED = ["lapl_attn_version", "lapl_attn_status_string", "lapl_attn_last_erro
             "lapl_norm_create", "lapl_norm_forward", "lapl_norm_workspace_size",
             "lapl_norm_backward", "lapl_norm_last_error", "lapl_norm_destroy",
             "lapl_clip_create", "lapl_clip_workspace_size", "lapl_clip_norm", "lapl_clip_apply",
-            "lapl_clip_last_error", "lapl_clip_destroy"]
+            "lapl_clip_last_error", "lapl_clip_destroy",
+            "lapl_rope_create", "lapl_rope_forward", "lapl_rope_workspace_size",
+            "lapl_rope_backward", "lapl_rope_last_error", "lapl_rope_destroy",
+            "lapl_decay_create", "lapl_decay_workspace_size", "lapl_decay_forward",
+            "lapl_decay_backward", "lapl_decay_plan_info_get", "lapl_decay_device_errors",
+            "lapl_decay_set_fault_injection", "lapl_decay_last_error", "lapl_decay_destroy",
+            "lapl_adamw_create", "lapl_adamw_step", "lapl_adamw_last_error", "lapl_adamw_destroy"]
 
 
 def status_string(status: int) -> str:
@@ -429,3 +491,123 @@ def lapl_clip_last_error(handle) -> str:
 
 def lapl_clip_destroy(handle) -> None:
     _check(LIB.lapl_clip_destroy(handle), "lapl_clip_destroy")
+
+
+# ---- include/lapl_ops.h: heads with a norm and rotary positions -----------------------------
+def lapl_rope_create(cfg: lapl_rope_config):
+    h = ctypes.c_void_p()
+    _check(LIB.lapl_rope_create(ctypes.byref(cfg), ctypes.byref(h)), "lapl_rope_create")
+    return h
+
+
+def lapl_rope_forward(handle, q, k, v, positions, q_weight, k_weight, q_out, k_out, v_out,
+                      stream) -> None:
+    _check(LIB.lapl_rope_forward(handle, q, k, v, positions, q_weight, k_weight, q_out, k_out,
+                                 v_out, stream), "lapl_rope_forward", handle,
+           "lapl_rope_last_error")
+
+
+def lapl_rope_workspace_size(handle) -> int:
+    n = ctypes.c_size_t()
+    _check(LIB.lapl_rope_workspace_size(handle, ctypes.byref(n)), "lapl_rope_workspace_size",
+           handle, "lapl_rope_last_error")
+    return n.value
+
+
+def lapl_rope_backward(handle, q, k, positions, q_weight, k_weight, dq_out, dk_out, dv_out, dq, dk,
+                       dv, dq_weight, dk_weight, workspace, workspace_bytes, stream) -> None:
+    _check(LIB.lapl_rope_backward(handle, q, k, positions, q_weight, k_weight, dq_out, dk_out,
+                                  dv_out, dq, dk, dv, dq_weight, dk_weight, workspace,
+                                  workspace_bytes, stream), "lapl_rope_backward", handle,
+           "lapl_rope_last_error")
+
+
+def lapl_rope_last_error(handle) -> str:
+    return LIB.lapl_rope_last_error(handle).decode()
+
+
+def lapl_rope_destroy(handle) -> None:
+    _check(LIB.lapl_rope_destroy(handle), "lapl_rope_destroy")
+
+
+# ---- include/lapl_ops.h: linear attention with a decay for each head ------------------------
+def lapl_decay_create(cfg: lapl_decay_config):
+    h = ctypes.c_void_p()
+    _check(LIB.lapl_decay_create(ctypes.byref(cfg), ctypes.byref(h)), "lapl_decay_create")
+    return h
+
+
+def lapl_decay_workspace_size(handle) -> tuple:
+    """(the forward's bytes, the backward's)."""
+    n, m = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(LIB.lapl_decay_workspace_size(handle, ctypes.byref(n), ctypes.byref(m)),
+           "lapl_decay_workspace_size", handle, "lapl_decay_last_error")
+    return n.value, m.value
+
+
+def lapl_decay_forward(handle, q, k, v, log_decay, state, lengths, out, final_state, workspace,
+                       workspace_bytes, stream) -> None:
+    _check(LIB.lapl_decay_forward(handle, q, k, v, log_decay, state, lengths, out, final_state,
+                                  workspace, workspace_bytes, stream), "lapl_decay_forward", handle,
+           "lapl_decay_last_error")
+
+
+def lapl_decay_backward(handle, q, k, v, log_decay, state, lengths, dout, dfinal, dq, dk, dv, dstate,
+                        workspace, workspace_bytes, stream) -> None:
+    _check(LIB.lapl_decay_backward(handle, q, k, v, log_decay, state, lengths, dout, dfinal, dq, dk,
+                                   dv, dstate, workspace, workspace_bytes, stream),
+           "lapl_decay_backward", handle, "lapl_decay_last_error")
+
+
+def lapl_decay_plan_info_get(handle) -> dict:
+    info = lapl_decay_plan_info()
+    _check(LIB.lapl_decay_plan_info_get(handle, ctypes.byref(info)), "lapl_decay_plan_info_get",
+           handle, "lapl_decay_last_error")
+    return {name: int(getattr(info, name)) for name, _ in lapl_decay_plan_info._fields_}
+
+
+def lapl_decay_device_errors(handle, stream) -> int:
+    """Read and clear the device error word (synchronises `stream`); raises on a set flag."""
+    flags = ctypes.c_uint(0)
+    _check(LIB.lapl_decay_device_errors(handle, stream, ctypes.byref(flags)),
+           "lapl_decay_device_errors", handle, "lapl_decay_last_error")
+    return flags.value
+
+
+def lapl_decay_set_fault_injection(handle, wait_ns: int, skip_last: int) -> None:
+    _check(LIB.lapl_decay_set_fault_injection(handle, int(wait_ns), int(skip_last)),
+           "lapl_decay_set_fault_injection", handle, "lapl_decay_last_error")
+
+
+def lapl_decay_last_error(handle) -> str:
+    return LIB.lapl_decay_last_error(handle).decode()
+
+
+def lapl_decay_destroy(handle) -> None:
+    _check(LIB.lapl_decay_destroy(handle), "lapl_decay_destroy")
+
+
+# ---- include/lapl_ops.h: AdamW step ---------------------------------------------------------
+def lapl_adamw_create(cfg: lapl_adamw_config):
+    h = ctypes.c_void_p()
+    _check(LIB.lapl_adamw_create(ctypes.byref(cfg), ctypes.byref(h)), "lapl_adamw_create")
+    return h
+
+
+def lapl_adamw_step(handle, params, grads, masters, m, v, m_scales, v_scales, lr, lr_device, step,
+                    step_device, norm, max_norm, stream) -> None:
+    """params, grads, m, v: the tensors' device addresses, one for each of the plan's tensors;
+    masters, m_scales, v_scales: the same, or None."""
+    lists = [None if a is None else _pointers(a)
+             for a in (params, grads, masters, m, v, m_scales, v_scales)]
+    _check(LIB.lapl_adamw_step(handle, *lists, float(lr), lr_device, int(step), step_device, norm,
+                               float(max_norm), stream), "lapl_adamw_step", handle,
+           "lapl_adamw_last_error")
+
+
+def lapl_adamw_last_error(handle) -> str:
+    return LIB.lapl_adamw_last_error(handle).decode()
+
+
+def lapl_adamw_destroy(handle) -> None:
+    _check(LIB.lapl_adamw_destroy(handle), "lapl_adamw_destroy")

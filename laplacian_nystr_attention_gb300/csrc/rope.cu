@@ -1,0 +1,718 @@
+// rope.cu -- a projection's rows as heads, with the norm of each query and key head and the rotary
+// positions: lapl_rope_* of include/lapl_ops.h.
+//
+//   y = R(x rstd w),  rstd = 1 / sqrt(mean(x^2) + eps);  backward, with g = R^T dy, t = g w, u = x rstd:
+//   dx = rstd (t - u mean(t u)),  dw = sum over rows of g u.
+//
+// HBM-bound: every value is read and written once.  A CTA takes a few tokens, all their heads: the
+// tokens' cosines and sines are formed once, in shared memory, for all heads of q and k.  A group of
+// lanes takes a row (a token's head); a lane has two vectors of it that hold whole pairs (of a head's two
+// halves, or next to each other), so that turning needs no exchange and the norm one sum over the group.
+// Rows are taken token after token within a head, so that what a CTA writes to a head is one run.
+//
+// Angles.  A position times a frequency in fp32 is off by 2^-24 of itself: half a radian at 2^23.  A
+// frequency is held as a 64-bit fraction of a turn instead, whose product with a 32-bit position, modulo
+// a turn, is one integer multiplication and off by 2^-33 of a turn.
+#include <algorithm>
+#include <cmath>
+#include <new>
+#include <vector>
+
+#include "ops_common.cuh"
+
+namespace lapl {
+namespace rope {
+
+constexpr int kThreads = 256;
+constexpr int kMaxPairs = LAPL_ROPE_MAX_DIM / 2;
+constexpr int kMaxTokens = 8;      // tokens of a CTA at a time
+constexpr int kRows = 2;           // rows of a group in flight
+
+struct Part {            // q, k or v
+  const void* in;        // rows [B,N,heads*d]  (backward: what it was, or null without a norm)
+  void* out;             // [B,heads,N,d]       (backward: null)
+  const void* grad;      // backward: gradient [B,heads,N,d]
+  void* din;             // backward: gradient of the rows
+  const float* weight;
+  int heads;
+  int stride;
+};
+struct Args {
+  Part part[3];
+  const int* positions;
+  float* partial;        // backward: [CTAs][2][d] sums as pairs of floats
+  unsigned long long turn[kMaxPairs];   // frequencies, in 2^-64 of a turn
+  long long rows;        // B * N tokens
+  int tokens, d, pairs, axes, first1, first2;   // first1, first2: first pairs of axes 1 and 2
+  int at_once;           // tokens of a CTA at a time
+  int lanes_log2;        // lanes of a row
+  int norm;
+  float eps;
+};
+
+// V values as floats, in memory of either type.
+template <int V, bool kHalf>
+__device__ __forceinline__ void load(float (&x)[V], const void* p, long long at) {
+  if constexpr (kHalf) {
+    const uint16_t* q = static_cast<const uint16_t*>(p) + at;
+    if constexpr (V == 4) {
+      const uint2 w = *reinterpret_cast<const uint2*>(q);
+      x[0] = bf16_lo(w.x), x[1] = bf16_hi(w.x), x[2] = bf16_lo(w.y), x[3] = bf16_hi(w.y);
+    } else if constexpr (V == 2) {
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(q);
+      x[0] = bf16_lo(w), x[1] = bf16_hi(w);
+    } else {
+      x[0] = ops::bf16_bits(*q);
+    }
+  } else {
+    const float* q = static_cast<const float*>(p) + at;
+    if constexpr (V == 4) {
+      const float4 w = *reinterpret_cast<const float4*>(q);
+      x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
+    } else if constexpr (V == 2) {
+      const float2 w = *reinterpret_cast<const float2*>(q);
+      x[0] = w.x, x[1] = w.y;
+    } else {
+      x[0] = *q;
+    }
+  }
+}
+template <int V, bool kHalf>
+__device__ __forceinline__ void store(void* p, long long at, const float (&x)[V]) {
+  if constexpr (kHalf) {
+    uint16_t* q = static_cast<uint16_t*>(p) + at;
+    if constexpr (V == 4)
+      *reinterpret_cast<uint2*>(q) =
+          make_uint2(ops::pack_bf16(x[0], x[1]), ops::pack_bf16(x[2], x[3]));
+    else if constexpr (V == 2) *reinterpret_cast<uint32_t*>(q) = ops::pack_bf16(x[0], x[1]);
+    else *q = (uint16_t)ops::pack_bf16(x[0], 0.f);
+  } else {
+    float* q = static_cast<float*>(p) + at;
+    if constexpr (V == 4) *reinterpret_cast<float4*>(q) = make_float4(x[0], x[1], x[2], x[3]);
+    else if constexpr (V == 2) *reinterpret_cast<float2*>(q) = make_float2(x[0], x[1]);
+    else *q = x[0];
+  }
+}
+
+// The two vectors of a lane's slot j: where they start in a head and whether they are there.  The
+// first pairs / V slots are turned; the rest hold the values after them, two vectors to a slot.
+template <int V, bool kInterleaved>
+struct Slot {
+  int at[2];
+  bool on[2];
+  int pair;   // first pair, or -1
+  __device__ __forceinline__ Slot(int s, int d, int pairs) {
+    const int turned = pairs / V;
+    if (s < turned) {
+      at[0] = kInterleaved ? 2 * V * s : V * s;
+      at[1] = at[0] + (kInterleaved ? V : pairs);
+      on[0] = on[1] = true;
+      pair = V * s;
+    } else {
+      at[0] = 2 * pairs + 2 * V * (s - turned);
+      at[1] = at[0] + V;
+      on[0] = at[0] < d;
+      on[1] = at[1] < d;
+      pair = -1;
+    }
+  }
+};
+
+// Turns a slot's pairs (back with kBack).
+template <int V, bool kInterleaved, bool kBack>
+__device__ __forceinline__ void turn(float (&a)[V], float (&b)[V], const float2* cs) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float2 t = cs[i];
+    const float c = t.x, s = kBack ? -t.y : t.y;
+    // Pair i of the slot: of both vectors, or of the first and then of the second.
+    float& x = kInterleaved && V > 1 ? (i < V / 2 ? a[2 * i] : b[2 * i - V]) : a[i];
+    float& y = kInterleaved && V > 1 ? (i < V / 2 ? a[2 * i + 1] : b[2 * i - V + 1]) : b[i];
+    const float p = x, q = y;
+    x = fmaf(p, c, -(q * s));
+    y = fmaf(q, c, p * s);
+  }
+}
+
+// cos and sin of `count` tokens' pairs from token `first` on.
+__device__ __forceinline__ void fill_turns(float2* cs, const Args& a, long long first, int count) {
+  for (int i = threadIdx.x; i < count * a.pairs; i += kThreads) {
+    const int t = i / a.pairs, p = i - t * a.pairs;
+    const int axis = (p >= a.first1) + (p >= a.first2);
+    const long long pos = a.positions[(first + t) * a.axes + axis];
+    const long long part = (long long)(a.turn[p] * (unsigned long long)pos);   // signed: -1/2 .. 1/2
+    float s, c;
+    sincospif(__ll2float_rn(part) * 1.0842021724855044e-19f, &s, &c);   // 2^-63: half turns
+    cs[i] = make_float2(c, s);
+  }
+}
+
+__device__ __forceinline__ float group_sum(float v, int lanes) {
+  for (int o = lanes / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Where a token's part begins: of the rows, and of the heads' planes.
+struct Place {
+  long long in, out;
+  __device__ __forceinline__ Place(const Args& a, const Part& p, long long token, int head) {
+    const unsigned b = (unsigned)token / (unsigned)a.tokens, n = (unsigned)token - b * (unsigned)a.tokens;
+    in = token * p.stride + (long long)head * a.d;
+    out = (((long long)b * p.heads + head) * a.tokens + n) * a.d;
+  }
+};
+
+template <int V, int NS, bool kInterleaved, bool kHalfIn, bool kHalfOut>
+__global__ void __launch_bounds__(kThreads)
+rope_forward_kernel(const __grid_constant__ Args a) {
+  extern __shared__ float2 cs[];
+  const int lanes = 1 << a.lanes_log2, lane = threadIdx.x & (lanes - 1);
+  const int group = threadIdx.x >> a.lanes_log2, groups = kThreads >> a.lanes_log2;
+  const float inv_d = 1.f / (float)a.d;
+  for (long long first = (long long)blockIdx.x * a.at_once; first < a.rows;
+       first += (long long)gridDim.x * a.at_once) {
+    const int count = (int)min((long long)a.at_once, a.rows - first);
+    __syncthreads();   // the last tokens' turns are used up
+    fill_turns(cs, a, first, count);
+    __syncthreads();
+#pragma unroll 1
+    for (int which = 0; which < 3; ++which) {
+      const Part& p = a.part[which];
+      const int rows = p.heads * count;
+      const bool norm = a.norm && which < 2;
+      for (int r0 = group; r0 - group < rows; r0 += kRows * groups) {
+        float x[kRows][NS][2][V];
+        int token[kRows];
+        Place place[kRows] = {Place(a, p, first, 0), Place(a, p, first, 0)};
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+          const int r = r0 + u * groups;
+          const int head = r / count;
+          token[u] = r - head * count;
+          place[u] = Place(a, p, first + token[u], head);
+#pragma unroll
+          for (int j = 0; j < NS; ++j) {
+            const Slot<V, kInterleaved> s(lane + j * lanes, a.d, a.pairs);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              if (r < rows && s.on[h]) {
+                load<V, kHalfIn>(x[u][j][h], p.in, place[u].in + s.at[h]);
+              } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i) x[u][j][h][i] = 0.f;
+              }
+            }
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+          float rstd = 1.f;
+          if (norm) {
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < NS; ++j)
+#pragma unroll
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < V; ++i) sum = fmaf(x[u][j][h][i], x[u][j][h][i], sum);
+            rstd = 1.f / sqrtf(fmaf(group_sum(sum, lanes), inv_d, a.eps));
+          }
+          if (r0 + u * groups >= rows) continue;
+#pragma unroll
+          for (int j = 0; j < NS; ++j) {
+            const Slot<V, kInterleaved> s(lane + j * lanes, a.d, a.pairs);
+            if (norm) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                float w[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) w[i] = 1.f;
+                if (p.weight && s.on[h]) {
+#pragma unroll
+                  for (int i = 0; i < V; ++i) w[i] = p.weight[s.at[h] + i];
+                }
+#pragma unroll
+                for (int i = 0; i < V; ++i) x[u][j][h][i] *= rstd * w[i];
+              }
+            }
+            if (which < 2 && s.pair >= 0)
+              turn<V, kInterleaved, false>(x[u][j][0], x[u][j][1],
+                                           cs + token[u] * a.pairs + s.pair);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if (s.on[h]) store<V, kHalfOut>(p.out, place[u].out + s.at[h], x[u][j][h]);
+          }
+        }
+      }
+    }
+  }
+}
+
+// Sum of a weight's gradient over the CTA's groups, in pairs of floats, to its partial.
+template <int V, int NS, bool kInterleaved>
+__device__ __forceinline__ void write_partial(const Args& a, int which, const ops::Pair (&dw)[NS][2][V],
+                                              float2* scratch, int lane, int lanes, int group,
+                                              int groups) {
+  // One group after another adds to the CTA's sums.
+  float2* sums = scratch;
+  for (int i = threadIdx.x; i < a.d; i += kThreads) sums[i] = make_float2(0.f, 0.f);
+  for (int g = 0; g < groups; ++g) {
+    __syncthreads();
+    if (g != group) continue;
+#pragma unroll
+    for (int j = 0; j < NS; ++j) {
+      const Slot<V, kInterleaved> s(lane + j * lanes, a.d, a.pairs);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (s.on[h]) {
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const float2 old = sums[s.at[h] + i];
+            ops::Pair v = {old.x, old.y};
+            v.add(dw[j][h][i].hi, dw[j][h][i].lo);
+            sums[s.at[h] + i] = make_float2(v.hi, v.lo);
+          }
+        }
+    }
+  }
+  __syncthreads();
+  float2* out = reinterpret_cast<float2*>(a.partial) + ((long long)blockIdx.x * 2 + which) * a.d;
+  for (int i = threadIdx.x; i < a.d; i += kThreads) out[i] = sums[i];
+  __syncthreads();
+}
+
+template <int V, int NS, bool kInterleaved, bool kHalfIn, bool kHalfGrad>
+__global__ void __launch_bounds__(kThreads)
+rope_backward_kernel(const __grid_constant__ Args a) {
+  extern __shared__ float2 cs[];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int lanes = 1 << a.lanes_log2, lane = threadIdx.x & (lanes - 1);
+  const int group = threadIdx.x >> a.lanes_log2, groups = kThreads >> a.lanes_log2;
+  const float inv_d = 1.f / (float)a.d;
+  // One part after another over all of the CTA's tokens: one weight's sums at a time.
+#pragma unroll 1
+  for (int which = 0; which < 3; ++which) {
+    const Part& p = a.part[which];
+    if (p.heads == 0) continue;
+    const bool norm = a.norm && which < 2;
+    ops::Pair dw[NS][2][V];
+#pragma unroll
+    for (int j = 0; j < NS; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < V; ++i) dw[j][h][i] = {0.f, 0.f};
+    for (long long first = (long long)blockIdx.x * a.at_once; first < a.rows;
+         first += (long long)gridDim.x * a.at_once) {
+      const int count = (int)min((long long)a.at_once, a.rows - first);
+      if (which < 2 && a.pairs) {
+        __syncthreads();   // the last tokens' turns are used up
+        fill_turns(cs, a, first, count);
+        __syncthreads();
+      }
+      const int rows = p.heads * count;
+      for (int r = group; r - group < rows; r += groups) {
+        const int head = r / count, token = r - head * count;
+        const Place place(a, p, first + token, head);
+        float x[NS][2][V], g[NS][2][V];
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+          const Slot<V, kInterleaved> s(lane + j * lanes, a.d, a.pairs);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const bool on = r < rows && s.on[h];
+#pragma unroll
+            for (int i = 0; i < V; ++i) x[j][h][i] = g[j][h][i] = 0.f;
+            if (on) load<V, kHalfGrad>(g[j][h], p.grad, place.out + s.at[h]);
+            if (on && norm) load<V, kHalfIn>(x[j][h], p.in, place.in + s.at[h]);
+          }
+        }
+        if (which < 2) {
+#pragma unroll
+          for (int j = 0; j < NS; ++j) {
+            const Slot<V, kInterleaved> s(lane + j * lanes, a.d, a.pairs);
+            if (r < rows && s.pair >= 0)
+              turn<V, kInterleaved, true>(g[j][0], g[j][1], cs + token * a.pairs + s.pair);
+          }
+        }
+        if (norm) {
+          float sum = 0.f;
+#pragma unroll
+          for (int j = 0; j < NS; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int i = 0; i < V; ++i) sum = fmaf(x[j][h][i], x[j][h][i], sum);
+          const float rstd = 1.f / sqrtf(fmaf(group_sum(sum, lanes), inv_d, a.eps));
+          float dot = 0.f;
+#pragma unroll
+          for (int j = 0; j < NS; ++j) {
+            const Slot<V, kInterleaved> s(lane + j * lanes, a.d, a.pairs);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int i = 0; i < V; ++i) {
+                const float u = x[j][h][i] * rstd;
+                x[j][h][i] = u;
+                if (r < rows) dw[j][h][i].add(g[j][h][i] * u);
+                if (p.weight && s.on[h]) g[j][h][i] *= p.weight[s.at[h] + i];
+                dot = fmaf(g[j][h][i], u, dot);
+              }
+          }
+          dot = group_sum(dot, lanes) * inv_d;
+#pragma unroll
+          for (int j = 0; j < NS; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int i = 0; i < V; ++i)
+                g[j][h][i] = rstd * fmaf(-x[j][h][i], dot, g[j][h][i]);
+        }
+        if (r < rows) {
+#pragma unroll
+          for (int j = 0; j < NS; ++j) {
+            const Slot<V, kInterleaved> s(lane + j * lanes, a.d, a.pairs);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if (s.on[h]) store<V, kHalfGrad>(p.din, place.in + s.at[h], g[j][h]);
+          }
+        }
+      }
+    }
+    if (a.partial && which < 2) {
+      __syncthreads();
+      write_partial<V, NS, kInterleaved>(a, which, dw, cs, lane, lanes, group, groups);
+    }
+  }
+}
+
+// The weights' gradients from all partials: a warp for each of 2 d values, in a fixed order.
+__global__ void __launch_bounds__(kThreads)
+rope_weights_kernel(const float2* partial, int parts, int d, float* dq, float* dk) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // the partials are written
+  const int lane = threadIdx.x & 31, i = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  float* out = i < d ? dq : dk;
+  if (i >= 2 * d || !out) return;
+  ops::Pair s = {0.f, 0.f};
+  for (int k = lane; k < parts; k += 32) {
+    const float2 v = partial[(long long)k * 2 * d + i];
+    s.add(v.x, v.y);
+  }
+  for (int o = 16; o > 0; o >>= 1) {
+    const float hi = __shfl_down_sync(0xffffffffu, s.hi, o);
+    s.add(hi, __shfl_down_sync(0xffffffffu, s.lo, o));
+  }
+  if (lane == 0) out[i < d ? i : i - d] = s.value();
+}
+
+// kernel<...>(V, slots of a lane, interleaved, types) as a function pointer.
+using Kernel = void (*)(const Args);
+template <bool kBackward, int V, int NS, bool kInterleaved>
+Kernel by_type(bool half_in, bool half_out) {
+  if constexpr (kBackward) {
+    if (half_in) return half_out ? rope_backward_kernel<V, NS, kInterleaved, true, true>
+                                 : rope_backward_kernel<V, NS, kInterleaved, true, false>;
+    return half_out ? rope_backward_kernel<V, NS, kInterleaved, false, true>
+                    : rope_backward_kernel<V, NS, kInterleaved, false, false>;
+  } else {
+    if (half_in) return half_out ? rope_forward_kernel<V, NS, kInterleaved, true, true>
+                                 : rope_forward_kernel<V, NS, kInterleaved, true, false>;
+    return half_out ? rope_forward_kernel<V, NS, kInterleaved, false, true>
+                    : rope_forward_kernel<V, NS, kInterleaved, false, false>;
+  }
+}
+template <bool kBackward, bool kInterleaved>
+Kernel by_shape(int vec, int ns, bool half_in, bool half_out) {
+  if (vec == 4) return by_type<kBackward, 4, 1, kInterleaved>(half_in, half_out);
+  if (vec == 2 && ns == 1) return by_type<kBackward, 2, 1, kInterleaved>(half_in, half_out);
+  if (vec == 2) return by_type<kBackward, 2, 2, kInterleaved>(half_in, half_out);
+  if (ns == 1) return by_type<kBackward, 1, 1, kInterleaved>(half_in, half_out);
+  if (ns == 2) return by_type<kBackward, 1, 2, kInterleaved>(half_in, half_out);
+  return by_type<kBackward, 1, 4, kInterleaved>(half_in, half_out);
+}
+
+}  // namespace rope
+}  // namespace lapl
+
+struct lapl_rope_plan {
+  lapl_rope_config cfg;
+  lapl::rope::Args args;    // sizes, strides and turns
+  int sms, device;
+  char last_error[lapl::ops::kErrorText];
+};
+
+using namespace lapl;
+
+namespace {
+
+constexpr int kBackwardCtas = 4;   // of an SM
+
+lapl_status validate(const lapl_rope_config* c) {
+  if (!c || c->batch < 0 || c->tokens < 1 || c->q_heads < 1 || c->k_heads < 0 || c->v_heads < 0 ||
+      c->head_dim < 1 || c->axes < 1 || c->axes > 3 || !c->pairs)
+    return LAPL_ERR_INVALID_ARG;
+  if (c->interleaved < 0 || c->interleaved > 1 || c->norm < 0 || c->norm > 1 || !(c->eps >= 0.f) ||
+      !std::isfinite(c->eps))
+    return LAPL_ERR_INVALID_ARG;
+  if (!ops::is_float_dtype(c->in_dtype) || !ops::is_float_dtype(c->out_dtype) ||
+      !ops::is_float_dtype(c->grad_dtype))
+    return LAPL_ERR_INVALID_ARG;
+  if (c->head_dim > LAPL_ROPE_MAX_DIM || c->q_heads > 4096 || c->k_heads > 4096 || c->v_heads > 4096 ||
+      (long long)c->batch * c->tokens > (1LL << 31) - 1)
+    return LAPL_ERR_UNSUPPORTED;
+  int pairs = 0;
+  for (int i = 0; i < c->axes; ++i) {
+    if (c->pairs[i] < 0 || c->pairs[i] > LAPL_ROPE_MAX_DIM) return LAPL_ERR_INVALID_ARG;
+    pairs += c->pairs[i];
+  }
+  if (2 * pairs > c->head_dim || (pairs > 0 && !c->frequencies)) return LAPL_ERR_INVALID_ARG;
+  for (int i = 0; i < pairs; ++i)
+    if (!std::isfinite(c->frequencies[i])) return LAPL_ERR_INVALID_ARG;
+  const int heads[3] = {c->q_heads, c->k_heads, c->v_heads};
+  const int strides[3] = {c->q_stride, c->k_stride, c->v_stride};
+  for (int i = 0; i < 3; ++i) {
+    if (strides[i] < 0) return LAPL_ERR_INVALID_ARG;
+    if (heads[i] > 0 && strides[i] != 0 && strides[i] < heads[i] * c->head_dim)
+      return LAPL_ERR_INVALID_ARG;
+  }
+  return LAPL_OK;
+}
+
+// radians as a fraction of a turn, in 2^-64.
+unsigned long long turns(double radians) {
+  const long double t = (long double)radians / 6.283185307179586476925286766559005768L;
+  const long double part = t - std::floor(t);
+  const long double scaled = part * 18446744073709551616.0L;
+  return scaled >= 18446744073709551616.0L ? 0ull : (unsigned long long)scaled;
+}
+
+bool rows_fit(const void* p, int stride, int dtype, int vec) {
+  return p == nullptr || (ops::aligned(p, (size_t)ops::dtype_bytes(dtype) * vec) && stride % vec == 0);
+}
+bool heads_fit(const void* p, int dtype, int vec) {
+  return p == nullptr || ops::aligned(p, (size_t)ops::dtype_bytes(dtype) * vec);
+}
+
+// Widest vectors that hold whole pairs and that every row and head starts on.
+int vector_of(const lapl_rope_plan& p, const rope::Args& a, bool backward) {
+  const lapl_rope_config& c = p.cfg;
+  for (int vec = 4; vec > 1; vec /= 2) {
+    bool fits = a.d % vec == 0 && a.pairs % vec == 0;
+    for (int i = 0; i < 3 && fits; ++i) {
+      const rope::Part& t = a.part[i];
+      if (t.heads == 0) continue;
+      fits = rows_fit(t.in, t.stride, c.in_dtype, vec);
+      if (!backward) fits = fits && heads_fit(t.out, c.out_dtype, vec);
+      else fits = fits && heads_fit(t.grad, c.grad_dtype, vec) && rows_fit(t.din, t.stride, c.grad_dtype, vec);
+    }
+    if (fits) return vec;
+  }
+  return 1;
+}
+
+cudaError_t launch(const lapl_rope_plan& p, rope::Args& a, bool backward, int* ctas, cudaStream_t st) {
+  const lapl_rope_config& c = p.cfg;
+  const int vec = vector_of(p, a, backward);
+  const int rest = a.d - 2 * a.pairs;
+  const int slots = a.pairs / vec + (rest + 2 * vec - 1) / (2 * vec);
+  int lanes_log2 = 0;
+  while (lanes_log2 < 5 && (1 << lanes_log2) < slots) ++lanes_log2;
+  const int ns = (slots + 31) / 32;
+  a.lanes_log2 = lanes_log2;
+  // Fewer tokens to a CTA where that many would not give one to every SM.
+  int at_once = rope::kMaxTokens;
+  while (at_once > 1 && a.rows < (long long)at_once * 2 * p.sms) at_once /= 2;
+  a.at_once = at_once;
+  const long long tiles = (a.rows + at_once - 1) / at_once;
+  const long long most = backward ? (long long)kBackwardCtas * p.sms : 1LL << 30;
+  const int grid = (int)std::min(tiles, most);
+  *ctas = grid;
+  const int ns_rounded = ns <= 1 ? 1 : ns == 2 ? 2 : 4;
+  const bool hi = c.in_dtype == LAPL_BF16;
+  const bool ho = (backward ? c.grad_dtype : c.out_dtype) == LAPL_BF16;
+  rope::Kernel k;
+  if (backward)
+    k = c.interleaved ? rope::by_shape<true, true>(vec, ns_rounded, hi, ho)
+                      : rope::by_shape<true, false>(vec, ns_rounded, hi, ho);
+  else
+    k = c.interleaved ? rope::by_shape<false, true>(vec, ns_rounded, hi, ho)
+                      : rope::by_shape<false, false>(vec, ns_rounded, hi, ho);
+  // The turns, and in the backward in the same place a weight's sums.
+  const size_t smem = sizeof(float2) * std::max(a.pairs * at_once, backward ? a.d : 0);
+  k<<<grid, rope::kThreads, smem, st>>>(a);
+  return cudaGetLastError();
+}
+
+lapl_status check_pointers(std::initializer_list<std::pair<const void*, int>> list) {
+  for (const auto& x : list)
+    if (!ops::aligned(x.first, x.second)) return LAPL_ERR_ALIGNMENT;
+  return LAPL_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+lapl_status lapl_rope_create(const lapl_rope_config* cfg, lapl_rope_handle* out) {
+  if (!out) return LAPL_ERR_INVALID_ARG;
+  *out = nullptr;
+  const lapl_status st = validate(cfg);
+  if (st != LAPL_OK) return st;
+  int sms = 0, device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
+  if (e != cudaSuccess) return LAPL_ERR_CUDA;
+  lapl_rope_plan* p = new (std::nothrow) lapl_rope_plan();
+  if (!p) return LAPL_ERR_INVALID_ARG;
+  p->cfg = *cfg;
+  p->sms = sms;
+  p->device = device;
+  rope::Args& a = p->args;
+  a = {};
+  int pairs[3] = {0, 0, 0};
+  for (int i = 0; i < cfg->axes; ++i) pairs[i] = cfg->pairs[i];
+  a.pairs = pairs[0] + pairs[1] + pairs[2];
+  a.first1 = pairs[0];
+  a.first2 = pairs[0] + pairs[1];
+  if (cfg->axes < 3) a.first2 = rope::kMaxPairs;
+  if (cfg->axes < 2) a.first1 = rope::kMaxPairs;
+  for (int i = 0; i < a.pairs; ++i) a.turn[i] = turns(cfg->frequencies[i]);
+  p->cfg.pairs = nullptr;          // the caller's, for the call only
+  p->cfg.frequencies = nullptr;
+  a.rows = (long long)cfg->batch * cfg->tokens;
+  a.tokens = cfg->tokens;
+  a.d = cfg->head_dim;
+  a.axes = cfg->axes;
+  a.norm = cfg->norm;
+  a.eps = cfg->eps;
+  const int heads[3] = {cfg->q_heads, cfg->k_heads, cfg->v_heads};
+  const int strides[3] = {cfg->q_stride, cfg->k_stride, cfg->v_stride};
+  for (int i = 0; i < 3; ++i) {
+    a.part[i].heads = heads[i];
+    a.part[i].stride = strides[i] ? strides[i] : heads[i] * cfg->head_dim;
+  }
+  *out = p;
+  return LAPL_OK;
+}
+
+lapl_status lapl_rope_workspace_size(lapl_rope_handle p, size_t* bytes) {
+  if (!p || !bytes) return LAPL_ERR_INVALID_ARG;
+  *bytes = align_up((size_t)kBackwardCtas * p->sms * 2 * p->cfg.head_dim * sizeof(float2), kAlign);
+  return LAPL_OK;
+}
+
+lapl_status lapl_rope_forward(lapl_rope_handle p, const void* q, const void* k, const void* v,
+                              const int* positions, const float* q_weight, const float* k_weight,
+                              void* q_out, void* k_out, void* v_out, void* stream) {
+  if (!p) return LAPL_ERR_INVALID_ARG;
+  const lapl_rope_config& c = p->cfg;
+  if (!c.norm && (q_weight || k_weight)) return LAPL_ERR_INVALID_ARG;
+  if (c.batch > 0) {
+    if (!q || !q_out || (c.k_heads && (!k || !k_out)) || (c.v_heads && (!v || !v_out)) ||
+        (p->args.pairs && !positions))
+      return LAPL_ERR_INVALID_ARG;
+  }
+  const int i = ops::dtype_bytes(c.in_dtype), o = ops::dtype_bytes(c.out_dtype);
+  lapl_status st = check_pointers({{q, i}, {k, i}, {v, i}, {positions, 4}, {q_weight, 4}, {k_weight, 4},
+                                   {q_out, o}, {k_out, o}, {v_out, o}});
+  if (st != LAPL_OK) return st;
+  st = ops::check_device(p->device, p->last_error, "rope_forward/device");
+  if (st != LAPL_OK || c.batch == 0) return st;
+  rope::Args a = p->args;
+  const void* in[3] = {q, k, v};
+  void* out[3] = {q_out, k_out, v_out};
+  const float* weight[3] = {q_weight, k_weight, nullptr};
+  for (int n = 0; n < 3; ++n) {
+    a.part[n].in = a.part[n].heads ? in[n] : nullptr;
+    a.part[n].out = a.part[n].heads ? out[n] : nullptr;
+    a.part[n].weight = weight[n];
+  }
+  a.positions = positions;
+  int ctas = 0;
+  const cudaError_t e = launch(*p, a, false, &ctas, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) {
+    ops::set_error(p->last_error, e, "rope_forward");
+    return LAPL_ERR_CUDA;
+  }
+  return LAPL_OK;
+}
+
+lapl_status lapl_rope_backward(lapl_rope_handle p, const void* q, const void* k,
+                               const int* positions, const float* q_weight, const float* k_weight,
+                               const void* dq_out, const void* dk_out, const void* dv_out, void* dq,
+                               void* dk, void* dv, float* dq_weight, float* dk_weight,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  if (!p) return LAPL_ERR_INVALID_ARG;
+  const lapl_rope_config& c = p->cfg;
+  if (!c.norm && (q_weight || k_weight || dq_weight || dk_weight)) return LAPL_ERR_INVALID_ARG;
+  if (c.batch > 0) {
+    if (!dq_out || !dq || (c.k_heads && (!dk_out || !dk)) || (c.v_heads && (!dv_out || !dv)) ||
+        (p->args.pairs && !positions) || (c.norm && (!q || (c.k_heads && !k))))
+      return LAPL_ERR_INVALID_ARG;
+  }
+  const bool weights = dq_weight || dk_weight;
+  const int i = ops::dtype_bytes(c.in_dtype), g = ops::dtype_bytes(c.grad_dtype);
+  lapl_status st = check_pointers({{q, i}, {k, i}, {positions, 4}, {q_weight, 4}, {k_weight, 4},
+                                   {dq_out, g}, {dk_out, g}, {dv_out, g}, {dq, g}, {dk, g}, {dv, g},
+                                   {dq_weight, 4}, {dk_weight, 4}});
+  if (st != LAPL_OK) return st;
+  if (weights) {
+    size_t need = 0;
+    lapl_rope_workspace_size(p, &need);
+    if (!workspace) return LAPL_ERR_INVALID_ARG;
+    if (!ops::aligned(workspace, 16)) return LAPL_ERR_ALIGNMENT;
+    if (workspace_bytes < need) return LAPL_ERR_WORKSPACE;
+  }
+  st = ops::check_device(p->device, p->last_error, "rope_backward/device");
+  if (st != LAPL_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  int ctas = 0;
+  if (c.batch > 0) {
+    rope::Args a = p->args;
+    const void* in[3] = {q, k, nullptr};
+    const void* grad[3] = {dq_out, dk_out, dv_out};
+    void* din[3] = {dq, dk, dv};
+    const float* weight[3] = {q_weight, k_weight, nullptr};
+    for (int n = 0; n < 3; ++n) {
+      rope::Part& t = a.part[n];
+      t.in = t.heads && c.norm ? in[n] : nullptr;
+      t.grad = t.heads ? grad[n] : nullptr;
+      t.din = t.heads ? din[n] : nullptr;
+      t.weight = weight[n];
+    }
+    a.positions = positions;
+    a.partial = weights ? static_cast<float*>(workspace) : nullptr;
+    e = launch(*p, a, true, &ctas, s);
+  }
+  if (e == cudaSuccess && weights) {
+    float* dkw = c.k_heads ? dk_weight : nullptr;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((2 * c.head_dim + rope::kThreads / 32 - 1) / (rope::kThreads / 32)));
+    cfg.blockDim = dim3(rope::kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = c.batch > 0 ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, rope::rope_weights_kernel, static_cast<const float2*>(workspace), ctas,
+                           c.head_dim, dq_weight, dkw);
+    if (e == cudaSuccess && dk_weight && !dkw)   // no key heads: nothing that depends on it
+      e = cudaMemsetAsync(dk_weight, 0, sizeof(float) * c.head_dim, s);
+  }
+  if (e != cudaSuccess) {
+    ops::set_error(p->last_error, e, "rope_backward");
+    return LAPL_ERR_CUDA;
+  }
+  return LAPL_OK;
+}
+
+const char* lapl_rope_last_error(lapl_rope_handle p) { return p ? p->last_error : ""; }
+
+lapl_status lapl_rope_destroy(lapl_rope_handle p) {
+  delete p;
+  return LAPL_OK;
+}
+
+}  // extern "C"
