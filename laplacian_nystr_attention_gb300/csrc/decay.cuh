@@ -94,6 +94,9 @@ struct Fade {
     if (x > -0.5f) factor = 1.f;
   }
   __device__ __forceinline__ float operator()(float s) const { return fmaf(s, less, s * factor); }
+  __device__ __forceinline__ ops::Vec<2> operator()(const ops::Vec<2>& s) const {
+    return ops::fma(s, ops::fill<2>(less), ops::mul(s, ops::fill<2>(factor)));
+  }
 };
 
 // All launches of the passes token by token, for any sizes and types (decay_rows.cu).

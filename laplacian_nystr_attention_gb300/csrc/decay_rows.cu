@@ -218,12 +218,10 @@ decay_rows_kernel(const __grid_constant__ Args a, int pass0) {
     }
     if (held) {
       const Fade fade(l, n);
-      const Vec<2> factor = ops::fill<2>(fade.factor), less = ops::fill<2>(fade.less);
 #pragma unroll
       for (int c = 0; c < kCols; ++c)
 #pragma unroll
-        for (int i = 0; i < KD / 2; ++i)
-          S[c][i] = ops::fma(S[c][i], less, ops::mul(S[c][i], factor));
+        for (int i = 0; i < KD / 2; ++i) S[c][i] = fade(S[c][i]);
     }
   }
   // Where the state goes: this segment's own, or after the last segment the sequence's.

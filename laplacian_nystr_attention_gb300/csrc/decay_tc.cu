@@ -11,16 +11,18 @@
 //   outer   X S
 //   add     Y^T Z'         Z' = Z with each token's decay to the chunk's end
 // x, y and z enter as they are.  What is computed is split into bf16 parts, so that no product loses
-// what fp32 holds: P and S into two (2^-17 of a value is left out, against 2^-9 of the output's own
-// rounding), Z' into three (2^-25), as the state's errors are carried along.
+// what fp32 holds: P and S into two, which leave out 2^-16 of a value at most (2.5e-6 on average; the
+// output's own rounding is 2^-8), Z' into three (2^-24), as what the state loses is carried along (two
+// parts: a state 2.4e-6 off instead of 0.7e-6).
 //
 // One CTA of an SM works through a segment of a sequence; its warps:
 //   0-7    scores to P (warp w: rows 32 (w % 4) and up, every other block of 32 columns), and the
-//          outputs: both accumulators, the decays, through shared memory to whole runs of rows
+//          outputs: both accumulators, the decays, through shared memory to whole runs of rows.  Warp 0:
+//          the copies of X, Y and Z tiles by TMA, 128-byte swizzle, a chunk ahead
 //   8-11   the state, fp32 in registers: g^n S + add, and its two parts as an operand
-//   12-15  Z' from Z
-//   16     copies: X, Y and Z tiles by TMA, 128-byte swizzle, up to 3 chunks ahead
-//   17     one thread issues the products
+//   8-14   Z' from Z
+//   15     the products
+// (16 warps, so that each may have 128 registers: with 18 it was 96, and spills.)
 // Before it, where a sequence has several segments: decay_sums_kernel forms each segment's own
 // contribution to the state (add, with decays to the segment's end) and decay_carry_kernel the states
 // before each.
@@ -40,8 +42,9 @@ constexpr int kD = 64;                        // padded row length
 constexpr unsigned kTile = kChunk * kD * 2;   // bytes of a tile of X, Y, Z or a part of Z'
 constexpr unsigned kState = kD * kD * 2;      // bytes of a part of S
 constexpr int kParts = 3;                     // of Z'
-constexpr int kMaxStages = 4;
-constexpr int kPowers = 32;
+constexpr int kPieces = kChunk * kD / 8;      // of a tile, of 16 bytes
+constexpr int kStages = 2;                    // of X, Y and Z, and of Z'
+constexpr int kAhead = 2;                     // chunks from a copy to the prefetch into L2 beside it
 
 // Columns of tensor memory.
 constexpr unsigned kScores = 0, kInner = 256, kOuter = 320, kAdd = 384, kColumns = 512;
@@ -52,7 +55,6 @@ struct TcArgs {
   unsigned* err;
   unsigned long long wait_ns;
   int skip_last;
-  int stages;
 };
 
 // The chunks of a segment of one sequence, in processing order.
@@ -73,45 +75,71 @@ struct Chunks {
   __device__ __forceinline__ int tokens(int i) const { return min(kChunk, len - place(i) * kChunk); }
 };
 
-// The tokens of Z, times weight(row), as kParts tiles; rows from n on as zeros, in Z and Y too, whose
-// products with zeros would not be zeros for what is not finite there.  A thread has 16 / kShare pieces
-// of 8 values of a row of 64.
-template <int kShare, class Weight>
-__device__ __forceinline__ void weigh(unsigned char* y, unsigned char* z, unsigned char* to, int row,
-                                      int share, int n, Weight weight) {
-  const float w = weight(row);
-  const Vec<2> w2 = ops::fill<2>(w);
-  const unsigned at = (unsigned)row * 128u;
-#pragma unroll
-  for (int c = 0; c < 8 / kShare; ++c) {
-    const unsigned piece = at + ((unsigned)((share * (8 / kShare) + c) ^ (row & 7)) << 4);
+// A place in a ring of stages, and the parity of the stage's current phase (kept by adding: a remainder by
+// a number of stages that is no constant took the products' thread 100 clocks).
+struct Ring {
+  int stage = 0;
+  unsigned phase = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++stage == stages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+// The tokens of Z, times late[row] and by, as kParts tiles; rows from n on as zeros, in Z and Y too, whose
+// products with zeros would not be zeros for what is not finite there.  Pieces kFirst to kLast of 8 values,
+// 8 to a row.
+template <int kThreads, int kFirst, int kLast>
+__device__ __forceinline__ void weigh(unsigned char* y, unsigned char* z, unsigned char* to, int thread,
+                                      int n, const float* late, float by) {
+#pragma unroll 2
+  for (int i = kFirst + thread; i < kLast; i += kThreads) {
+    const int row = i >> 3;
+    const unsigned at = (unsigned)row * 128u + ((unsigned)((i ^ row) & 7) << 4);
     uint4 part[kParts] = {};
     if (row < n) {
-      const uint4 v = *reinterpret_cast<const uint4*>(z + piece);
+      const uint4 v = *reinterpret_cast<const uint4*>(z + at);
+      const Vec<2> w = ops::fill<2>(late[row] * by);
       const uint32_t in[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        Vec<2> f = ops::mul({{bf16_lo(in[e]), bf16_hi(in[e])}}, w2);
+        Vec<2> f = ops::mul({{bf16_lo(in[e]), bf16_hi(in[e])}}, w);
 #pragma unroll
         for (int k = 0; k < kParts; ++k) (&part[k].x)[e] = take(f);
       }
     } else {
-      *reinterpret_cast<uint4*>(z + piece) = make_uint4(0, 0, 0, 0);
-      *reinterpret_cast<uint4*>(y + piece) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(z + at) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(y + at) = make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
-    for (int k = 0; k < kParts; ++k) *reinterpret_cast<uint4*>(to + k * kTile + piece) = part[k];
+    for (int k = 0; k < kParts; ++k) *reinterpret_cast<uint4*>(to + k * kTile + at) = part[k];
   }
 }
 
-// add: D = Y^T Z' over a chunk; rows 64 and up of D are rows 0 and up again (lbo = 0).
-__device__ __forceinline__ void issue_add(unsigned d, unsigned y, unsigned parts) {
+// add: D = Y^T Z' over a chunk, the first part in columns 0-63, the others' sum in 64-127; rows 64 and up
+// are rows 0 and up again (lbo = 0).
+__device__ __forceinline__ void issue_add(unsigned d, uint64_t y, uint64_t parts) {
 #pragma unroll
-  for (int k = 0; k < kParts; ++k)
+  for (int s = 0; s < kChunk / 16; ++s)
+    mma(d, y + s * 2048 / 16, parts + s * 2048 / 16, instruction(2 * kD, true, true), s > 0);
 #pragma unroll
-    for (int s = 0; s < kChunk / 16; ++s)
-      mma(d, operand(y + s * 2048, 0), operand(parts + k * kTile + s * 2048, 0),
-          instruction(kD, true, true), k > 0 || s > 0);
+  for (int s = 0; s < kChunk / 16; ++s)
+    mma(d + kD, y + s * 2048 / 16, parts + (2 * kTile + s * 2048) / 16, instruction(kD, true, true),
+        true);
+}
+constexpr unsigned kAddColumns = 2 * kD;
+// Both sums, 32 columns of each.
+__device__ __forceinline__ void load_add(unsigned addr, Vec<2> (&sum)[16]) {
+  unsigned d[2][32];
+  tmem_load32(addr, d[0]);
+  tmem_load32(addr + kD, d[1]);
+  tmem_loaded();
+#pragma unroll
+  for (int c = 0; c < 16; ++c)
+    sum[c] = ops::add({{__uint_as_float(d[0][2 * c]), __uint_as_float(d[0][2 * c + 1])}},
+                      {{__uint_as_float(d[1][2 * c]), __uint_as_float(d[1][2 * c + 1])}});
 }
 
 // A state's values of tensor-memory lane `lane`: row lane % 64, columns from 32 (lane / 64) on.
@@ -122,24 +150,47 @@ struct Place64 {
 
 // ---- outputs ----------------------------------------------------------------------------
 
-constexpr int kOutWarps = 18, kOutThreads = 32 * kOutWarps;
-constexpr int kCopyWarp = 16, kIssueWarp = 17;
+constexpr int kOutWarps = 16, kOutThreads = 32 * kOutWarps;
+constexpr int kStateWarp = 8, kWeighWarp = 12, kIssueWarp = 15;
+// Pieces of Z' that the warps from kWeighWarp on weigh; the state's warps weigh the rest, after the state.
+constexpr int kWeighPieces = 640;
+
+// Decays from a column of a block of 32 scores to a row, in processing order: within a block on the
+// diagonal, near[31 + row - column], zero for columns after the row; in others g^(row - last column),
+// times far[column].  (Last: of the block, in processing order; the order may be against the columns'.)
+// late[row]: from a whole chunk's token to its end, times zs; of n tokens, late + 128 - n (late, against the
+// order).
+struct Decays {
+  float far[32];
+  float near[64];
+  float late[kChunk];
+  __device__ __forceinline__ void fill(float log2g, int reverse, float zs, int i) {   // i < kChunk
+    if (i < 32) far[i] = power(log2g, reverse ? i : 31 - i);
+    const int back = (i - 31) * (reverse ? -1 : 1);
+    if (i < 64) near[i] = back >= 0 && i < 63 ? power(log2g, back) : 0.f;
+    late[i] = zs * power(log2g, reverse ? i : kChunk - 1 - i);
+  }
+  __device__ __forceinline__ const float* late_of(int n, int reverse) const {
+    return reverse ? late : late + kChunk - n;
+  }
+};
 
 struct OutLayout {
-  unsigned stage, parts, state, staging, powers, bars, total;
-  __host__ __device__ OutLayout(int stages, bool out_half) {
+  unsigned stage, parts, state, staging, decays, bars, total;
+  __host__ __device__ OutLayout() {
     stage = 0;
-    parts = stages * 3 * kTile;
-    state = parts + kParts * kTile;
+    parts = kStages * 3 * kTile;
+    state = parts + kStages * kParts * kTile;
     staging = state + 2 * kState;
-    powers = staging + 8 * 32 * 32 * (out_half ? 2 : 4);
-    bars = powers + kPowers * 4;
+    decays = staging + 8 * 2048;
+    bars = decays + sizeof(Decays);
     total = bars + 8 * 32;
   }
 };
 enum Bar {
-  kFull = 0, kEmpty = kFull + kMaxStages, kScoresFull = kEmpty + kMaxStages, kPReady = kScoresFull + 2,
-  kOFull = kPReady + 2, kOFree, kZReady, kAddFull, kAddFree, kSReady, kSFree, kDone, kBars
+  kFull = 0, kScoresFull = kFull + kStages, kPReady = kScoresFull + 2,
+  kZReady = kPReady + 2, kOFull = kZReady + 2, kOFree, kAddFull, kAddFree,
+  kSReady, kSFree, kDone, kBars
 };
 static_assert(kBars < 32, "room of the barriers");
 
@@ -150,12 +201,16 @@ decay_chunks_kernel(const __grid_constant__ TcArgs t) {
   const int which = blockIdx.z;
   const Pass& p = a.pass[which];
   const int bh = blockIdx.x / a.segments, segment = blockIdx.x % a.segments;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31;
+  // The products are issued beside the warps of the rows with the fewest scores: a scheduler's other warps
+  // hold the issuing one up.
+  int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+  if (warp >= kWeighWarp && !p.reverse) warp = warp == kWeighWarp ? kIssueWarp : warp - 1;
   const Chunks chunks(a, p, bh, segment);
-  const int n = chunks.count, stages = t.stages;
+  const int n = chunks.count;
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  const OutLayout at(stages, p.out_half);
-  float* powers = reinterpret_cast<float*>(smem + at.powers);
+  const OutLayout at;
+  Decays& decays = *reinterpret_cast<Decays*>(smem + at.decays);
   const unsigned bars = smem_u32(smem + at.bars);
   auto bar = [&](int b) { return bars + 8u * (unsigned)b; };
   unsigned* slot = reinterpret_cast<unsigned*>(smem + at.bars + 8 * kBars);
@@ -169,17 +224,14 @@ decay_chunks_kernel(const __grid_constant__ TcArgs t) {
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kMaxStages; ++s) {
-      mbar_init(bar(kFull + s), 1);
-      mbar_init(bar(kEmpty + s), 1);
-    }
     for (int s = 0; s < 2; ++s) {
+      mbar_init(bar(kFull + s), 1);
       mbar_init(bar(kScoresFull + s), 1);
       mbar_init(bar(kPReady + s), 8);
+      mbar_init(bar(kZReady + s), kIssueWarp - kStateWarp);
     }
     mbar_init(bar(kOFull), 1);
     mbar_init(bar(kOFree), 8);
-    mbar_init(bar(kZReady), 4);
     mbar_init(bar(kAddFull), 1);
     mbar_init(bar(kAddFree), 4);
     mbar_init(bar(kSReady), 4);
@@ -187,14 +239,53 @@ decay_chunks_kernel(const __grid_constant__ TcArgs t) {
     mbar_init(bar(kDone), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (threadIdx.x >= 32 && threadIdx.x < 32 + kPowers)
-    powers[threadIdx.x - 32] = power(l2, threadIdx.x - 32);
+  if (threadIdx.x >= 128 && threadIdx.x < 128 + kChunk)
+    decays.fill(l2, p.reverse, p.zs, threadIdx.x - 128);
   fence_before();
   __syncthreads();
   fence_after();
   const unsigned tmem = *slot;
   bool ok = true;
   const unsigned long long wait_ns = t.wait_ns;
+
+  // The copies of chunk i, by one lane of a warp; the chunks after the next are on their way into L2.
+  auto copy = [&](int i, bool leader) {
+    if (i >= n || (t.skip_last && i == n - 1)) return;   // (fault injection: never copied)
+    if (leader) {
+      const unsigned dst = smem_u32(smem + at.stage + (i & 1) * 3 * kTile), full = bar(kFull + (i & 1));
+      const int token = chunks.place(i) * kChunk;
+      mbar_expect_tx(full, 3 * kTile);
+      tma_load_3d(dst, &t.x[which], 0, token, bh, full);
+      tma_load_3d(dst + kTile, &t.y[which], 0, token, bh, full);
+      tma_load_3d(dst + 2 * kTile, &t.z[which], 0, token, bh, full);
+      if (i + kAhead < n) {
+        const int later = chunks.place(i + kAhead) * kChunk;
+        tma_prefetch_3d(&t.x[which], 0, later, bh);
+        tma_prefetch_3d(&t.y[which], 0, later, bh);
+        tma_prefetch_3d(&t.z[which], 0, later, bh);
+      }
+    }
+  };
+  // Z' of chunk i, by the warps from kStateWarp on.
+  auto weigh_chunk = [&](int i) {
+    const int b = i & 1;
+    if (!warp_wait(bar(kFull + b), (i >> 1) & 1, wait_ns)) return false;
+    // (All that read the chunk before the last's Z' is done: what was copied for this one waited for it.)
+    const int tokens = chunks.tokens(i);
+    unsigned char* stage = smem + at.stage + b * 3 * kTile;
+    unsigned char* to = smem + at.parts + b * kParts * kTile;
+    const float* late = decays.late_of(tokens, p.reverse);
+    if (warp < kWeighWarp)
+      weigh<32 * (kWeighWarp - kStateWarp), kWeighPieces, kPieces>(
+          stage + kTile, stage + 2 * kTile, to, threadIdx.x - 32 * kStateWarp, tokens, late, 1.f);
+    else
+      weigh<32 * (kIssueWarp - kWeighWarp), 0, kWeighPieces>(
+          stage + kTile, stage + 2 * kTile, to, 32 * (warp - kWeighWarp) + lane, tokens, late, 1.f);
+    fence_async();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(kZReady + b));
+    return true;
+  };
 
   if (warp < 8) {
     // ---------------- P and outputs ----------------
@@ -203,15 +294,14 @@ decay_chunks_kernel(const __grid_constant__ TcArgs t) {
     const int row = 32 * quad + lane;
     const float f = p.zs * p.os;
     const bool half = p.out_half;
-    unsigned char* staging = smem + at.staging + warp * (half ? 2048 : 4096);
+    unsigned char* staging = smem + at.staging + warp * 2048;
     auto scores_to_p = [&](int i) {
       if (!warp_wait(bar(kScoresFull + (i & 1)), (i >> 1) & 1, wait_ns)) return false;
       fence_after();
       const unsigned base = tmem + kScores + 128u * (i & 1) + lanes;
       const int tokens = chunks.tokens(i);
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int j = 2 * b + odd;          // block of 32 columns
+#pragma unroll 1
+      for (int j = odd; j < 4; j += 2) {    // blocks of 32 columns
         unsigned hi[16], lo[16];
         const bool none = p.reverse ? j < quad : j > quad;
         if (none || 32 * j >= tokens) {
@@ -220,32 +310,35 @@ decay_chunks_kernel(const __grid_constant__ TcArgs t) {
         } else {
           unsigned s[32];
           tmem_load32(base + 32 * j, s);
-          // A block off the diagonal: g^(row - its last column) g^(last column - column).
-          const int ahead = p.reverse ? 32 * j - row : row - (32 * j + 31);
-          const float rowf = j == quad ? f : f * power(l2, ahead);
+          Vec<2> v[16];
+          if (j == quad) {
+            const float* near = decays.near + 31 + lane;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = ops::mul({{near[-2 * e], near[-2 * e - 1]}}, ops::fill<2>(f));
+          } else {
+            const float g = f * power(l2, p.reverse ? 32 * j - row : row - (32 * j + 31));
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const float4 w = *reinterpret_cast<const float4*>(decays.far + 2 * e);
+              v[e] = ops::mul({{w.x, w.y}}, ops::fill<2>(g));
+              v[e + 1] = ops::mul({{w.z, w.w}}, ops::fill<2>(g));
+            }
+          }
           tmem_loaded();
 #pragma unroll
+          for (int e = 0; e < 16; ++e)
+            v[e] = ops::mul(v[e], {{__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])}});
+          if (32 * j + 32 > tokens) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              if (32 * j + 2 * e >= tokens) v[e].f[0] = 0.f;
+              if (32 * j + 2 * e + 1 >= tokens) v[e].f[1] = 0.f;
+            }
+          }
+#pragma unroll
           for (int e = 0; e < 16; ++e) {
-            Vec<2> v = {{__uint_as_float(s[2 * e]), __uint_as_float(s[2 * e + 1])}};
-            Vec<2> w;
-            if (j == quad) {
-              const int d0 = p.reverse ? 2 * e - lane : lane - 2 * e;
-              const int d1 = p.reverse ? d0 + 1 : d0 - 1;
-              w = ops::mul({{powers[d0 & 31], powers[d1 & 31]}}, ops::fill<2>(rowf));
-              v = ops::mul(v, w);
-              if (d0 < 0) v.f[0] = 0.f;
-              if (d1 < 0) v.f[1] = 0.f;
-            } else {
-              w = p.reverse ? Vec<2>{{powers[2 * e], powers[2 * e + 1]}}
-                            : Vec<2>{{powers[31 - 2 * e], powers[30 - 2 * e]}};
-              v = ops::mul(v, ops::mul(w, ops::fill<2>(rowf)));
-            }
-            if (tokens < kChunk) {
-              if (32 * j + 2 * e >= tokens) v.f[0] = 0.f;
-              if (32 * j + 2 * e + 1 >= tokens) v.f[1] = 0.f;
-            }
-            hi[e] = take(v);
-            lo[e] = ops::pack_bf16(v.f[0], v.f[1]);
+            hi[e] = take(v[e]);
+            lo[e] = ops::pack_bf16(v[e].f[0], v[e].f[1]);
           }
         }
         tmem_store16(base + 32 * j, hi);
@@ -257,79 +350,89 @@ decay_chunks_kernel(const __grid_constant__ TcArgs t) {
       if (lane == 0) mbar_arrive(bar(kPReady + (i & 1)));
       return true;
     };
+    // Outputs go through shared memory, 64 bytes of a row at a time (32 columns in bf16, or 16), to 8 rows at
+    // once.
+    const int piece = lane & 3, row0 = lane >> 2;
+    auto stage = [&](const Vec<2>* o) {   // 32 bf16 columns, or 16
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          (&v.x)[e] = half ? ops::pack_bf16(o[4 * c + e].f[0], o[4 * c + e].f[1])
+                           : __float_as_uint(o[2 * c + (e >> 1)].f[e & 1]);
+        *reinterpret_cast<uint4*>(staging + (lane * 4 + (c ^ ((lane >> 1) & 3))) * 16) = v;
+      }
+      __syncwarp();
+    };
+    auto flush = [&](int i, int col) {
+      const long long first = (long long)bh * a.tokens;
+      const int size = half ? 2 : 4, token0 = chunks.place(i) * kChunk + 32 * quad;
+      col += piece * (16 / size);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = row0 + 8 * k, token = token0 + r;
+        const uint4 v =
+            *reinterpret_cast<const uint4*>(staging + (r * 4 + (piece ^ ((r >> 1) & 3))) * 16);
+        if (token < a.tokens && col < p.b)
+          *reinterpret_cast<uint4*>(static_cast<char*>(p.out) + ((first + token) * p.b + col) * size) = v;
+      }
+      __syncwarp();
+    };
     auto outputs = [&](int i) {
       if (!warp_wait(bar(kOFull), i & 1, wait_ns)) return false;
       fence_after();
+      // All that reads the chunk's stage is done: the copies of the one after the next take it.
+      if (warp == 0 && i + kStages < n) copy(i + kStages, elect());
       unsigned inner[32], outer[32];
       tmem_load32(tmem + kInner + 32 * odd + lanes, inner);
       tmem_load32(tmem + kOuter + 32 * odd + lanes, outer);
-      const int tokens = chunks.tokens(i), place = chunks.place(i) * kChunk;
+      const int tokens = chunks.tokens(i);
       const bool undecayed = p.undecayed && chunks.first + i == 0;
       const int steps = (p.reverse ? tokens - row : row + 1) - undecayed;
-      const float g = row < tokens ? p.os * power(l2, steps) : 0.f;
+      const bool live = row < tokens;
+      const Vec<2> g = ops::fill<2>(live ? p.os * power(l2, steps) : 0.f);
       tmem_loaded();
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kOFree));
-      const bool live = row < tokens;
-      if (half) {
+      Vec<2> o[16];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint4 v;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int k = 8 * c + 2 * e;
-            const Vec<2> o = ops::fma({{__uint_as_float(outer[k]), __uint_as_float(outer[k + 1])}},
-                                      ops::fill<2>(g),
-                                      {{__uint_as_float(inner[k]), __uint_as_float(inner[k + 1])}});
-            (&v.x)[e] = live ? ops::pack_bf16(o.f[0], o.f[1]) : 0u;
-          }
-          *reinterpret_cast<uint4*>(staging + (lane * 4 + (c ^ ((lane >> 1) & 3))) * 16) = v;
-        }
-      } else {
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          float v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int k = 4 * c + e;
-            v[e] = live ? fmaf(__uint_as_float(outer[k]), g, __uint_as_float(inner[k])) : 0.f;
-          }
-          *reinterpret_cast<float4*>(staging + (lane * 8 + (c ^ (lane & 7))) * 16) =
-              make_float4(v[0], v[1], v[2], v[3]);
-        }
+      for (int e = 0; e < 16; ++e) {
+        o[e] = ops::fma({{__uint_as_float(outer[2 * e]), __uint_as_float(outer[2 * e + 1])}}, g,
+                        {{__uint_as_float(inner[2 * e]), __uint_as_float(inner[2 * e + 1])}});
+        if (!live) o[e] = ops::fill<2>(0.f);
       }
-      __syncwarp();
-      // 64 or 128 bytes of a row at a time, rows side by side.
-      const int pieces = half ? 4 : 8, per = half ? 8 : 4;
-      const int piece = lane % pieces, row0 = lane / pieces;
-      const int col = 32 * odd + piece * per;
-      const long long first = (long long)bh * a.tokens;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (k >= pieces) break;
-        const int r = row0 + k * (32 / pieces);
-        const int sw = half ? piece ^ ((r >> 1) & 3) : piece ^ (r & 7);
-        const uint4 v = *reinterpret_cast<const uint4*>(staging + (r * pieces + sw) * 16);
-        const int token = place + 32 * quad + r;
-        if (token < a.tokens && col < p.b) {
-          const long long to = ((first + token) * p.b + col) * (half ? 2 : 4);
-          *reinterpret_cast<uint4*>(static_cast<char*>(p.out) + to) = v;
-        }
+      stage(o);
+      if (!half) {
+        flush(i, 32 * odd);
+        stage(o + 8);
+        flush(i, 32 * odd + 16);
       }
-      __syncwarp();
       return true;
     };
-    for (int i = 0; i <= n && ok; ++i) {
-      if (i < n) ok = scores_to_p(i);
-      if (ok && i > 0) ok = outputs(i - 1);
+    // (bf16 rows leave shared memory after the next chunk's P, on which the products wait.)
+    if (warp == 0)
+      for (int i = 0; i < min(n, kStages); ++i) copy(i, elect());
+    int done = 0;
+    for (int i = 0; i < n && ok; ++i) {
+      ok = scores_to_p(i);
+      if (!ok) break;
+      if (half && i > 0) flush(i - 1, 32 * odd);
+      ok = outputs(i);
+      if (ok) done = i + 1;
     }
+    // Every copy lands before the CTA may finish: those of the chunks not done, made so far.
+    if (!ok && warp == 0)
+      for (int i = done; i < min(n, done + kStages); ++i)
+        mbar_wait(bar(kFull + (i & 1)), (i >> 1) & 1, wait_ns);
+    if (half && ok && n > 0) flush(n - 1, 32 * odd);
   } else if (warp < 12) {
     // ---------------- the state ----------------
     const int tl = threadIdx.x - 256;
     const Place64 place(tl);
     const unsigned lanes = (unsigned)(32 * (warp & 3)) << 16;
-    float S[32];
+    Vec<2> S[16];
     const float* from = nullptr;
     long long row_step = p.b, col_step = 1;
     if (p.states) {
@@ -340,9 +443,9 @@ decay_chunks_kernel(const __grid_constant__ TcArgs t) {
     }
 #pragma unroll
     for (int c = 0; c < 32; ++c) {
-      S[c] = 0.f;
+      S[c / 2].f[c & 1] = 0.f;
       if (from && place.row < p.a && place.col + c < p.b)
-        S[c] = from[place.row * row_step + (place.col + c) * col_step];
+        S[c / 2].f[c & 1] = from[place.row * row_step + (place.col + c) * col_step];
     }
     unsigned char* operand_at = smem + at.state + place.row * 128;
     auto publish = [&] {
@@ -351,7 +454,7 @@ decay_chunks_kernel(const __grid_constant__ TcArgs t) {
         uint4 hi, lo;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          Vec<2> v = {{S[8 * c + 2 * e], S[8 * c + 2 * e + 1]}};
+          Vec<2> v = S[4 * c + e];
           (&hi.x)[e] = take(v);
           (&lo.x)[e] = ops::pack_bf16(v.f[0], v.f[1]);
         }
@@ -363,24 +466,27 @@ decay_chunks_kernel(const __grid_constant__ TcArgs t) {
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kSReady));
     };
-    if (n > 0) publish();
-    for (int i = 0; i < n; ++i) {
+    if (n > 0) {
+      publish();
+      ok = weigh_chunk(0);
+    }
+    for (int i = 0; i < n && ok; ++i) {
       ok = warp_wait(bar(kAddFull), i & 1, wait_ns);
       if (!ok) break;
       fence_after();
-      unsigned d[32];
-      tmem_load32(tmem + kAdd + place.col + lanes, d);
       const Fade fade(l, chunks.tokens(i) - (p.undecayed && chunks.first + i == 0));
-      tmem_loaded();
+      Vec<2> add[16];
+      load_add(tmem + kAdd + place.col + lanes, add);
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kAddFree));
 #pragma unroll
-      for (int c = 0; c < 32; ++c) S[c] = fade(S[c]) + __uint_as_float(d[c]);
+      for (int c = 0; c < 16; ++c) S[c] = ops::add(fade(S[c]), add[c]);
       if (i + 1 < n) {
         ok = warp_wait(bar(kSFree), i & 1, wait_ns);
         if (!ok) break;
         publish();
+        ok = weigh_chunk(i + 1);
       }
     }
     if (ok && p.last && segment == a.segments - 1) {
@@ -388,99 +494,71 @@ decay_chunks_kernel(const __grid_constant__ TcArgs t) {
       float* to = p.last + (long long)bh * p.a * p.b + (long long)place.row * p.b + place.col;
 #pragma unroll
       for (int c = 0; c < 32; ++c)
-        if (place.row < p.a && place.col + c < p.b) to[c] = S[c] * g;
+        if (place.row < p.a && place.col + c < p.b) to[c] = S[c / 2].f[c & 1] * g;
     }
-  } else if (warp < 16) {
+  } else if (warp < kIssueWarp) {
     // ---------------- Z' ----------------
-    const int row = threadIdx.x - 384;
-    const float whole = p.zs * power(l2, p.reverse ? row : kChunk - 1 - row);
-    for (int i = 0; i < n; ++i) {
-      const int s = i % stages, tokens = chunks.tokens(i);
-      ok = warp_wait(bar(kFull + s), (i / stages) & 1, wait_ns);
-      if (ok && i > 0) ok = warp_wait(bar(kAddFull), (i - 1) & 1, wait_ns);
-      if (!ok) break;
-      unsigned char* stage = smem + at.stage + s * 3 * kTile;
-      weigh<1>(stage + kTile, stage + 2 * kTile, smem + at.parts, row, 0, tokens, [&](int r) {
-        return tokens == kChunk || p.reverse ? whole : p.zs * power(l2, max(0, tokens - 1 - r));
-      });
-      fence_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kZReady));
-    }
-  } else if (warp == kCopyWarp) {
-    // ---------------- copies ----------------
-    if (lane == 0) {
-      int issued = 0;
-      for (int i = 0; i < n; ++i) {
-        const int s = i % stages;
-        if (i >= stages && !mbar_wait(bar(kEmpty + s), ((i / stages) - 1) & 1, wait_ns)) {
-          ok = false;
-          break;
-        }
-        if (t.skip_last && i == n - 1) break;   // fault injection: never copied
-        const unsigned dst = smem_u32(smem + at.stage + s * 3 * kTile);
-        const int token = chunks.place(i) * kChunk;
-        mbar_expect_tx(bar(kFull + s), 3 * kTile);
-        tma_load_3d(dst, &t.x[which], 0, token, bh, bar(kFull + s));
-        tma_load_3d(dst + kTile, &t.y[which], 0, token, bh, bar(kFull + s));
-        tma_load_3d(dst + 2 * kTile, &t.z[which], 0, token, bh, bar(kFull + s));
-        issued = i + 1;
-      }
-      // Every copy lands before the CTA may finish.
-      for (int i = max(0, issued - stages); i < issued; ++i)
-        mbar_wait(bar(kFull + i % stages), (i / stages) & 1, wait_ns);
-    }
-  } else if (lane == 0) {
+    for (int i = 0; i < n && ok; ++i) ok = weigh_chunk(i);
+  } else {
     // ---------------- products ----------------
-    auto stage_at = [&](int i) { return smem_u32(smem + at.stage + (i % stages) * 3 * kTile); };
+    const bool leader = elect();
+    const unsigned stage0 = smem_u32(smem + at.stage);
     auto scores = [&](int i) {
-      if (!mbar_wait(bar(kFull + i % stages), (i / stages) & 1, wait_ns)) return false;
-      // The tile of P that the scores overwrite: its product is done.
-      if (i >= 2 && !mbar_wait(bar(kOFull), (i - 2) & 1, wait_ns)) return false;
+      if (!warp_wait(bar(kFull + (i & 1)), (i >> 1) & 1, wait_ns)) return false;
       fence_after();
-      const unsigned x = stage_at(i);
-#pragma unroll
-      for (int s = 0; s < kD / 16; ++s)
-        mma(tmem + kScores + 128u * (i & 1), operand(x + s * 32, 0), operand(x + kTile + s * 32, 0),
-            instruction(kChunk, false, false), s > 0);
-      commit(bar(kScoresFull + (i & 1)));
-      return true;
-    };
-    const unsigned parts = smem_u32(smem + at.parts), state = smem_u32(smem + at.state);
-    if (n > 0) ok = scores(0);
-    for (int i = 0; i < n && ok; ++i) {
-      const unsigned x = stage_at(i), y = x + kTile, z = x + 2 * kTile;
-      ok = mbar_wait(bar(kZReady), i & 1, wait_ns) &&
-           (i == 0 || mbar_wait(bar(kAddFree), (i - 1) & 1, wait_ns));
-      if (!ok) break;
-      fence_after();
-      issue_add(tmem + kAdd, y, parts);
-      commit(bar(kAddFull));
-      if (i + 1 < n) ok = scores(i + 1);
-      ok = ok && mbar_wait(bar(kSReady), i & 1, wait_ns) &&
-           (i == 0 || mbar_wait(bar(kOFree), (i - 1) & 1, wait_ns));
-      if (!ok) break;
-      fence_after();
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
+      if (leader) {
+        const uint64_t x = operand(stage0 + (i & 1) * 3 * kTile, 0);
 #pragma unroll
         for (int s = 0; s < kD / 16; ++s)
-          mma(tmem + kOuter, operand(x + s * 32, 0), operand(state + k * kState + s * 2048, 0),
-              instruction(kD, false, true), k > 0 || s > 0);
-      commit(bar(kSFree));
-      ok = mbar_wait(bar(kPReady + (i & 1)), (i >> 1) & 1, wait_ns);
+          mma(tmem + kScores + 128u * (i & 1), x + 2 * s, x + kTile / 16 + 2 * s,
+              instruction(kChunk, false, false), s > 0);
+        commit(bar(kScoresFull + (i & 1)));
+      }
+      return true;
+    };
+    const uint64_t state = operand(smem_u32(smem + at.state), 0);
+    if (n > 0) ok = scores(0);
+    for (int i = 0; i < n && ok; ++i) {
+      const uint64_t x = operand(stage0 + (i & 1) * 3 * kTile, 0);
+      const uint64_t y = x + kTile / 16, z = y + kTile / 16;
+      ok = warp_wait(bar(kZReady + (i & 1)), (i >> 1) & 1, wait_ns) &&
+           (i == 0 || warp_wait(bar(kAddFree), (i - 1) & 1, wait_ns));
       if (!ok) break;
       fence_after();
+      if (leader) {
+        issue_add(tmem + kAdd, y, operand(smem_u32(smem + at.parts + (i & 1) * kParts * kTile), kTile));
+        commit(bar(kAddFull));
+      }
+      ok = warp_wait(bar(kSReady), i & 1, wait_ns) &&
+           (i == 0 || warp_wait(bar(kOFree), (i - 1) & 1, wait_ns));
+      if (!ok) break;
+      fence_after();
+      if (leader) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+        for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int s = 0; s < kChunk / 16; ++s)
-          mma_tmem(tmem + kInner, tmem + kScores + 128u * (i & 1) + 32 * (s / 2) + 16 * k + 8 * (s & 1),
-                   operand(z + s * 2048, 0), instruction(kD, false, true), k > 0 || s > 0);
-      commit(bar(kOFull));
-      commit(bar(kEmpty + i % stages));
+          for (int s = 0; s < kD / 16; ++s)
+            mma(tmem + kOuter, x + 2 * s, state + (k * kState + s * 2048) / 16,
+                instruction(kD, false, true), k > 0 || s > 0);
+        commit(bar(kSFree));
+      }
+      ok = warp_wait(bar(kPReady + (i & 1)), (i >> 1) & 1, wait_ns);
+      if (!ok) break;
+      fence_after();
+      if (leader) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int s = 0; s < kChunk / 16; ++s)
+            mma_tmem(tmem + kInner,
+                     tmem + kScores + 128u * (i & 1) + 32 * (s / 2) + 16 * k + 8 * (s & 1),
+                     z + s * 2048 / 16, instruction(kD, false, true), k > 0 || s > 0);
+        commit(bar(kOFull));
+      }
+      // The next chunk's scores, whose tile of P the last chunk's product has read: kOFree told.
+      ok = i + 1 == n || scores(i + 1);
     }
-    commit(bar(kDone));
+    if (leader) commit(bar(kDone));
   }
 
   // Agree on failures; then whatever the tensor core still does ends before its memory goes.
@@ -515,11 +593,12 @@ constexpr int kSumWarps = 14, kSumThreads = 32 * kSumWarps;
 constexpr int kSumStages = 4;
 
 struct SumLayout {
-  unsigned stage, parts, bars, total;
+  unsigned stage, parts, late, bars, total;
   __host__ __device__ SumLayout() {
     stage = 0;
     parts = kSumStages * 2 * kTile;
-    bars = parts + 2 * kParts * kTile;
+    late = parts + 2 * kParts * kTile;
+    bars = late + kChunk * 4;
     total = bars + 8 * 32;
   }
 };
@@ -530,7 +609,7 @@ enum SumBar {
 static_assert(kSumBars < 32, "room of the barriers");
 
 // Sum over a segment's tokens of y z^T with their decays to the segment's end.  Warps 0-7: Z'; 8-11: sums
-// in registers (a chunk's products in tensor memory, whose adding rounds down, only); 12 copies, 13 issues.
+// in registers (in tensor memory, whose adding cuts off, a chunk's products only); 12 copies, 13 issues.
 __global__ void __launch_bounds__(kSumThreads, 1)
 decay_sums_kernel(const __grid_constant__ TcArgs t) {
   extern __shared__ unsigned char smem_raw[];
@@ -538,7 +617,7 @@ decay_sums_kernel(const __grid_constant__ TcArgs t) {
   const int which = blockIdx.z;
   const Pass& p = a.pass[which];
   const int bh = blockIdx.x / (a.segments - 1), segment = blockIdx.x % (a.segments - 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const Chunks chunks(a, p, bh, segment);
   const int n = chunks.count;
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -547,7 +626,7 @@ decay_sums_kernel(const __grid_constant__ TcArgs t) {
   auto bar = [&](int b) { return bars + 8u * (unsigned)b; };
   unsigned* slot = reinterpret_cast<unsigned*>(smem + at.bars + 8 * kSumBars);
   const float l2 = log_decay(a, bh) * kLog2e;
-  constexpr unsigned kSumColumns = 128;
+  constexpr unsigned kSumColumns = 2 * kAddColumns;
 
   if (warp == 13) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -569,6 +648,11 @@ decay_sums_kernel(const __grid_constant__ TcArgs t) {
     mbar_init(bar(kSumEnd), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  float* late = reinterpret_cast<float*>(smem + at.late);
+  if (threadIdx.x >= 128 && threadIdx.x < 128 + kChunk) {
+    const int i = threadIdx.x - 128;
+    late[i] = p.zs * power(l2, p.reverse ? i : kChunk - 1 - i);
+  }
   fence_before();
   __syncthreads();
   fence_after();
@@ -577,20 +661,19 @@ decay_sums_kernel(const __grid_constant__ TcArgs t) {
   const unsigned long long wait_ns = t.wait_ns;
 
   if (warp < 8) {
-    const int row = threadIdx.x >> 1, share = threadIdx.x & 1;
-    int after = 0;   // tokens of the segment after the chunk
+    // Decays to the segment's end: to the chunk's, times those of the tokens after it.
+    int after = 0;
     for (int i = 0; i < n; ++i) after += chunks.tokens(i);
-    for (int i = 0; i < n; ++i) {
-      const int s = i % kSumStages, tokens = chunks.tokens(i);
+    Ring ring;
+    for (int i = 0; i < n; ++i, ring.next(kSumStages)) {
+      const int tokens = chunks.tokens(i);
       after -= tokens;
-      ok = warp_wait(bar(kSumFull + s), (i / kSumStages) & 1, wait_ns);
+      ok = warp_wait(bar(kSumFull + ring.stage), ring.phase, wait_ns);
       if (ok && i > 1) ok = warp_wait(bar(kSumDone + (i & 1)), ((i >> 1) - 1) & 1, wait_ns);
       if (!ok) break;
-      unsigned char* stage = smem + at.stage + s * 2 * kTile;
-      weigh<2>(stage, stage + kTile, smem + at.parts + (i & 1) * kParts * kTile, row, share, tokens,
-               [&](int r) {
-                 return p.zs * power(l2, after + (p.reverse ? r : max(0, tokens - 1 - r)));
-               });
+      unsigned char* stage = smem + at.stage + ring.stage * 2 * kTile;
+      weigh<256, 0, kPieces>(stage, stage + kTile, smem + at.parts + (i & 1) * kParts * kTile, threadIdx.x, tokens,
+                 p.reverse ? late : late + kChunk - tokens, power(l2, after));
       fence_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kSumReady + (i & 1)));
@@ -598,56 +681,59 @@ decay_sums_kernel(const __grid_constant__ TcArgs t) {
   } else if (warp < 12) {
     const Place64 place(threadIdx.x - 256);
     const unsigned lanes = (unsigned)(32 * (warp & 3)) << 16;
-    float S[32] = {};
+    Vec<2> S[16];
+#pragma unroll
+    for (int c = 0; c < 16; ++c) S[c] = ops::fill<2>(0.f);
     for (int i = 0; i < n; ++i) {
       ok = warp_wait(bar(kSumDone + (i & 1)), (i >> 1) & 1, wait_ns);
       if (!ok) break;
       fence_after();
-      unsigned d[32];
-      tmem_load32(tmem + 64u * (i & 1) + place.col + lanes, d);
-      tmem_loaded();
+      Vec<2> add[16];
+      load_add(tmem + kAddColumns * (i & 1) + place.col + lanes, add);
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kSumFree + (i & 1)));
 #pragma unroll
-      for (int c = 0; c < 32; ++c) S[c] += __uint_as_float(d[c]);
+      for (int c = 0; c < 16; ++c) S[c] = ops::add(S[c], add[c]);
     }
     float* to = p.states + (((long long)bh * a.segments + segment) * p.a + place.row) * p.b + place.col;
 #pragma unroll
     for (int c = 0; c < 32; ++c)
-      if (place.row < p.a && place.col + c < p.b) to[c] = S[c];
+      if (place.row < p.a && place.col + c < p.b) to[c] = S[c / 2].f[c & 1];
   } else if (warp == 12) {
-    if (lane == 0) {
-      int issued = 0;
-      for (int i = 0; i < n; ++i) {
-        const int s = i % kSumStages;
-        if (i >= kSumStages && !mbar_wait(bar(kSumEmpty + s), ((i / kSumStages) - 1) & 1, wait_ns)) {
-          ok = false;
-          break;
-        }
-        if (t.skip_last && i == n - 1) break;   // fault injection: never copied
-        const unsigned dst = smem_u32(smem + at.stage + s * 2 * kTile);
-        const int token = chunks.place(i) * kChunk;
+    const bool leader = elect();
+    int issued = 0;
+    for (int i = 0; i < n; ++i) {
+      const int s = i % kSumStages;
+      if (i >= kSumStages) ok = warp_wait(bar(kSumEmpty + s), ((i / kSumStages) - 1) & 1, wait_ns);
+      if (!ok) break;
+      const unsigned dst = smem_u32(smem + at.stage + s * 2 * kTile);
+      const int token = chunks.place(i) * kChunk;
+      if (leader) {
         mbar_expect_tx(bar(kSumFull + s), 2 * kTile);
         tma_load_3d(dst, &t.y[which], 0, token, bh, bar(kSumFull + s));
         tma_load_3d(dst + kTile, &t.z[which], 0, token, bh, bar(kSumFull + s));
-        issued = i + 1;
       }
-      for (int i = max(0, issued - kSumStages); i < issued; ++i)
-        mbar_wait(bar(kSumFull + i % kSumStages), (i / kSumStages) & 1, wait_ns);
+      issued = i + 1;
     }
-  } else if (lane == 0) {
+    for (int i = max(0, issued - kSumStages); i < issued; ++i)
+      mbar_wait(bar(kSumFull + i % kSumStages), (i / kSumStages) & 1, wait_ns);
+  } else {
+    const bool leader = elect();
     for (int i = 0; i < n; ++i) {
-      ok = mbar_wait(bar(kSumReady + (i & 1)), (i >> 1) & 1, wait_ns) &&
-           (i < 2 || mbar_wait(bar(kSumFree + (i & 1)), ((i >> 1) - 1) & 1, wait_ns));
+      ok = warp_wait(bar(kSumReady + (i & 1)), (i >> 1) & 1, wait_ns) &&
+           (i < 2 || warp_wait(bar(kSumFree + (i & 1)), ((i >> 1) - 1) & 1, wait_ns));
       if (!ok) break;
       fence_after();
-      issue_add(tmem + 64u * (i & 1), smem_u32(smem + at.stage + (i % kSumStages) * 2 * kTile),
-                smem_u32(smem + at.parts + (i & 1) * kParts * kTile));
-      commit(bar(kSumDone + (i & 1)));
-      commit(bar(kSumEmpty + i % kSumStages));
+      if (leader) {
+        issue_add(tmem + kAddColumns * (i & 1),
+                  operand(smem_u32(smem + at.stage + (i % kSumStages) * 2 * kTile), 0),
+                  operand(smem_u32(smem + at.parts + (i & 1) * kParts * kTile), kTile));
+        commit(bar(kSumDone + (i & 1)));
+        commit(bar(kSumEmpty + i % kSumStages));
+      }
     }
-    commit(bar(kSumEnd));
+    if (leader) commit(bar(kSumEnd));
   }
 
   ok = __syncthreads_and(ok ? 1 : 0) != 0;
@@ -691,33 +777,27 @@ cudaError_t launch_tc(const Args& a, int passes, int bh, unsigned* err, unsigned
   t.err = err;
   t.wait_ns = wait_ns;
   t.skip_last = skip_last;
-  bool out_half = true;
   for (int i = 0; i < passes; ++i) {
     const Pass& p = a.pass[i];
-    out_half = out_half && p.out_half;
     if (!encode(&t.x[i], p.x, p.a, a.tokens, bh) || !encode(&t.y[i], p.y, p.a, a.tokens, bh) ||
         !encode(&t.z[i], p.z, p.b, a.tokens, bh))
       return cudaErrorInvalidValue;
   }
-  t.stages = 3;
-  while (t.stages > 2 && OutLayout(t.stages, out_half).total + 1024 > kSmemMost) --t.stages;
   cudaError_t e = cudaSuccess;
   if (a.segments > 1) {
-    t.skip_last = 0;   // (the outputs' kernel is the one that is told to)
     const unsigned smem = SumLayout().total + 1024;
     e = cudaFuncSetAttribute(decay_sums_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
     if (e != cudaSuccess) return e;
     decay_sums_kernel<<<dim3((unsigned)(bh * (a.segments - 1)), 1, (unsigned)passes), kSumThreads, smem,
                         st>>>(t);
     e = cudaGetLastError();
-    t.skip_last = skip_last;
   }
   if (e == cudaSuccess && a.pass[0].states) e = launch_carry(a, passes, bh, st);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(decay_chunks_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
   if (e != cudaSuccess) return e;
   decay_chunks_kernel<<<dim3((unsigned)(bh * a.segments), 1, (unsigned)passes), kOutThreads,
-                        OutLayout(t.stages, out_half).total + 1024, st>>>(t);
+                        OutLayout().total + 1024, st>>>(t);
   return cudaGetLastError();
 }
 
