@@ -38,12 +38,13 @@ lapl_status validate(const lapl_decay_config* c) {
   return LAPL_OK;
 }
 
-// Segments of a sequence token by token.  A segment's warps walk its tokens alone; about 8 warps of an
-// SM are resident.  More than one segment costs the launch that forms their states, about 0.6 of the
-// other's time.
+// Segments of a sequence token by token.  A segment's warps walk its tokens alone; by registers 16, 12 or
+// 8 warps of an SM are resident.  More than one segment costs the launch that forms their states, about 0.6 of
+// the other's time, and the launches' own time, about that of 64 tokens.
 int row_segments(int tokens, long long bh, int rows, int cols, int sms) {
-  const int per_warp = rows <= 64 && cols > 32 ? 64 : 32;
-  const long long warps = bh * ((cols + per_warp - 1) / per_warp), room = 8LL * sms;
+  const int per_warp = rows <= 32 && cols > 32 ? 64 : 32;
+  const long long warps = bh * ((cols + per_warp - 1) / per_warp);
+  const long long room = (long long)(rows <= 64 ? 16 : rows <= 96 ? 12 : 8) * sms;
   int best = 1;
   double least = 0;
   for (int g = 1; g <= 64 && (g == 1 || tokens / g >= 32); ++g) {
@@ -75,7 +76,7 @@ int chunk_segments(int tokens, long long bh, int sms) {
 
 // Tokens of a segment: whole stages or chunks.
 int per_segment(int tokens, int segments, int step) {
-  return ((tokens + segments - 1) / segments + step - 1) / step * step;
+  return ((tokens + segments - 1) / segments + step - 1) / step * step;   // (step: of a stage or chunk)
 }
 
 bool tc_sizes(const lapl_decay_config& c) {

@@ -87,6 +87,7 @@ __device__ __forceinline__ float log_decay(const Args& a, int bh) {
 // m = exp(l n) - 1, whose rounding counts for less.
 struct Fade {
   float factor, less;   // less: m, or 0 where the factor is used
+  Fade() = default;
   __device__ __forceinline__ Fade(float l, int n) {
     const float x = l * (float)n;
     factor = exp2f(x * kLog2e);

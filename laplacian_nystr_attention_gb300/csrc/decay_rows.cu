@@ -1,13 +1,16 @@
 // decay_rows.cu -- a pass of the linear attention with decays token by token (decay.cuh has the
 // formulas): any sizes, types and alignment, and single tokens.
 //
-// A warp holds kCols columns of a sequence's state for each lane, all rows of them, in registers; a
-// token costs it a fused multiply-add for y_i z_j and one for x_i S_ij for each value, two rows at a
-// time in packed fp32 instructions.  The decay costs nothing: within a stage of kTok tokens the state
-// is held times g^-i (z times that instead, and outputs times g^i), and put right at the stage's end.
-// Where g^-kTok is large (over 2^4; a larger one could overflow what the sums do not) the state is
-// multiplied at every token.  The warps of a CTA take the same sequence's next columns, so that x and
-// y are read and widened to fp32 once; tokens are copied a stage ahead.
+// A warp holds 8 kCols columns of a sequence's state, all rows of them, in registers: a lane kCols columns of
+// a quarter of the rows.  A token costs it a fused multiply-add for y_i z_j and one for x_i S_ij for each value,
+// two rows at a time in packed fp32 instructions; the quarters' outputs meet in six shuffles.  (With whole
+// columns in a lane every lane read all of x and y: 32 reads of 16 bytes a token at 64 x 64 instead of 10, and
+// shared memory, 4 clocks for each, took three times as long as the arithmetic.)  The decay costs
+// nothing: within a stage of kTok tokens the state is held times g^-i (z times that instead, and outputs
+// times g^i), and put right at the stage's end.  Where g^-kTok is large (over 2^4; a larger one could
+// overflow what the sums do not) the state is multiplied at every token.  The warps of a CTA take the
+// same sequence's next columns, so that x and y are read and widened to fp32 once; tokens are copied a
+// stage ahead.
 //
 // Bound by fp32 arithmetic for long sequences (2 a b multiply-adds a token, 3 with segments), by the
 // bytes of the states for single tokens.
@@ -21,8 +24,32 @@ namespace {
 
 using ops::Vec;
 
-constexpr int kTok = 16;          // tokens of a stage
+constexpr int kTok = 12;          // tokens of a stage (16: at 64 x 64 in fp32 room for 7 of 8 CTAs)
 constexpr float kMostUp = 4.f;    // log2 of the largest g^-kTok that the state is held times
+
+// Two floats in a register pair as the packed instructions take them.  (As two floats that happen to be
+// neighbours, half of a token's instructions were moves.)
+using Two = unsigned long long;
+__device__ __forceinline__ Two two(float a, float b) {
+  Two r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ Vec<2> apart(Two v) {
+  Vec<2> r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.f[0]), "=f"(r.f[1]) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ Two fma(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ Two mul(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
 // Copies `bytes` (a run of whole elements) to shared memory, in the widest pieces that both sides
 // start on; `there`: dst is as far into 16 bytes as src.
@@ -61,53 +88,104 @@ __device__ __forceinline__ long long first_token(const Pass& p, int len, int i0,
   return p.reverse ? len - i0 - n : i0;
 }
 
+// Sums over the four quarters of the warp, kCols / 4 of each lane's kCols: those from column
+// (lane / 16) kCols / 2 + (lane / 8 % 2) kCols / 4 on.
+template <int kCols>
+__device__ __forceinline__ void across_quarters(float (&v)[kCols], int lane) {
+  const bool upper = lane & 16, odd = lane & 8;
+#pragma unroll
+  for (int c = 0; c < kCols / 2; ++c) {
+    const float other = __shfl_xor_sync(0xffffffffu, upper ? v[c] : v[c + kCols / 2], 16);
+    v[c] = (upper ? v[c + kCols / 2] : v[c]) + other;
+  }
+#pragma unroll
+  for (int c = 0; c < kCols / 4; ++c) {
+    const float other = __shfl_xor_sync(0xffffffffu, odd ? v[c] : v[c + kCols / 4], 8);
+    v[c] = (odd ? v[c + kCols / 4] : v[c]) + other;
+  }
+}
+
+// Registers for as many warps as a lane's part of the state allows: a warp issues every 4 to 5 clocks.
 template <int KD, int kCols, bool kOut>
-__global__ void __launch_bounds__(128, 2)
+__global__ void __launch_bounds__(128, KD * kCols <= 256 ? 4 : KD * kCols <= 384 ? 3 : 2)
 decay_rows_kernel(const __grid_constant__ Args a, int pass0) {
   extern __shared__ __align__(16) unsigned char smem[];
+  constexpr int kRows = KD / 4, kPairs = kRows / 2;   // of a lane
+  constexpr int kWide = 8 * kCols;                    // columns of a warp
   const Pass& p = a.pass[pass0 + blockIdx.z];
   const int bh = blockIdx.x / a.segments, segment = blockIdx.x % a.segments;
   const Range range(a, bh, segment);
   const int live = range.live(a, p);
   if (!kOut && segment == a.segments - 1) return;   // no segment comes after it
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, threads = blockDim.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, threads = blockDim.x, warps = threads / 32;
   const int rows = p.a, cols = p.b;
-  int col[kCols];
-#pragma unroll
-  for (int c = 0; c < kCols; ++c) col[c] = (warp * 32 + lane) * kCols + c;
-  // Shared memory: two raw stages (x, y, z as they are), then one stage in fp32.
+  const int row0 = (lane >> 3) * kRows, col0 = warp * kWide + (lane & 7) * kCols;
+  // First of the columns whose outputs are left to the lane.
+  const int out_col = col0 + ((lane >> 4) & 1) * (kCols / 2) + ((lane >> 3) & 1) * (kCols / 4);
+  // Shared memory: two raw stages (x, y, z as they are), then one stage in fp32, padded.
   const int xb = p.x_half ? 2 : 4, yb = p.y_half ? 2 : 4, zb = p.z_half ? 2 : 4;
   const unsigned raw_x = kOut ? (unsigned)((kTok * rows * xb + 15) & ~15) : 0u;
   const unsigned raw_y = (unsigned)((kTok * rows * yb + 15) & ~15);
   const unsigned raw_z = (unsigned)((kTok * cols * zb + 15) & ~15);
   const unsigned raw = raw_x + raw_y + raw_z;
+  const int wide = warps * kWide;
+  // Rows of fp32 that need no padding are read as they were copied.
+  const bool x_as_is = !p.x_half && rows == KD, y_as_is = !p.y_half && rows == KD;
   float* fx = reinterpret_cast<float*>(smem + 2 * raw);       // [kTok][KD]
-  float* fy = fx + (kOut ? kTok * KD : 0);                    // [kTok][KD]
-  float* fz = fy + kTok * KD;                                 // [kTok][cols]
+  float* fy = fx + (kOut && !x_as_is ? kTok * KD : 0);        // [kTok][KD]
+  float* fz = fy + (y_as_is ? 0 : kTok * KD);                 // [kTok][wide], times its decay
+  float* down = fz + kTok * wide;                             // [kTok] of outputs
 
   const float l = log_decay(a, bh), l2 = l * kLog2e;
   const bool held = -l2 * kTok <= kMostUp;
 
-  Vec<2> S[kCols][KD / 2];
+  Two S[kPairs][kCols];
 #pragma unroll
-  for (int c = 0; c < kCols; ++c)
+  for (int i = 0; i < kPairs; ++i)
 #pragma unroll
-    for (int i = 0; i < KD / 2; ++i) S[c][i] = ops::fill<2>(0.f);
+    for (int c = 0; c < kCols; ++c) S[i][c] = 0;
+  // Calls use(value, row, column) for every value of the lane's that is there.
+  auto each_value = [&](auto use) {
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i)
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) {
+        Vec<2> v = apart(S[i][c]);
+        if (col0 + c < cols) {
+          if (row0 + 2 * i < rows) use(v.f[0], row0 + 2 * i, col0 + c);
+          if (row0 + 2 * i + 1 < rows) use(v.f[1], row0 + 2 * i + 1, col0 + c);
+        }
+        S[i][c] = two(v.f[0], v.f[1]);
+      }
+  };
+  // The same for four columns, where rows are whole vectors.
+  auto each_four = [&](auto use) {
+#pragma unroll
+    for (int i = 0; i < kPairs; ++i)
+#pragma unroll
+      for (int c = 0; c < kCols; c += 4) {
+        Vec<2> v[4] = {apart(S[i][c]), apart(S[i][c + 1]), apart(S[i][c + 2]), apart(S[i][c + 3])};
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (row0 + 2 * i + e < rows && col0 + c < cols)
+            use(v[0].f[e], v[1].f[e], v[2].f[e], v[3].f[e], (row0 + 2 * i + e) * cols + col0 + c);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) S[i][c + k] = two(v[k].f[0], v[k].f[1]);
+      }
+  };
   if (kOut) {
-    const float* from = nullptr;
-    long long row_step = cols, col_step = 1;
-    if (p.states) {
-      from = p.states + ((long long)bh * a.segments + segment) * rows * cols;
-    } else if (p.first) {
-      from = p.first + (long long)bh * rows * cols;
-      if (p.first_across) row_step = 1, col_step = rows;
-    }
-    if (from) {
-#pragma unroll
-      for (int c = 0; c < kCols; ++c)
-#pragma unroll
-        for (int i = 0; i < KD; ++i)
-          if (i < rows && col[c] < cols) S[c][i / 2].f[i & 1] = from[i * row_step + col[c] * col_step];
+    const long long at = (long long)bh * rows * cols;
+    const float* from = p.states ? p.states + ((long long)bh * a.segments + segment) * rows * cols
+                        : p.first ? p.first + at : nullptr;
+    if (from && !p.states && p.first_across) {
+      each_value([&](float& v, int row, int col) { v = from[col * rows + row]; });
+    } else if (from && cols % 4 == 0 && ((uintptr_t)from & 15) == 0) {
+      each_four([&](float& v0, float& v1, float& v2, float& v3, int i) {
+        const float4 f = *reinterpret_cast<const float4*>(from + i);
+        v0 = f.x, v1 = f.y, v2 = f.z, v3 = f.w;
+      });
+    } else if (from) {
+      each_value([&](float& v, int row, int col) { v = from[row * cols + col]; });
     }
   }
 
@@ -126,16 +204,21 @@ decay_rows_kernel(const __grid_constant__ Args a, int pass0) {
     }
     ops::close_copies();
   };
-  // One stage's rows in fp32, in processing order; `pad`: to KD with zeros.
-  auto widen = [&](float* to, const unsigned char* from, int half, int n, int width, int pad) {
-    for (int i = threadIdx.x; i < n * pad; i += threads) {
-      const int t = i / pad, e = i - t * pad;
-      const int src = (p.reverse ? n - 1 - t : t) * width + e;
-      float v = 0.f;
-      if (e < width)
-        v = half ? ops::bf16_bits(reinterpret_cast<const uint16_t*>(from)[src])
-                 : reinterpret_cast<const float*>(from)[src];
-      to[i] = v;
+  // Value e of row t of a raw stage.
+  auto value = [&](const unsigned char* from, int half, int width, int t, int e) {
+    return half ? ops::bf16_bits(reinterpret_cast<const uint16_t*>(from)[t * width + e])
+                : reinterpret_cast<const float*>(from)[t * width + e];
+  };
+  // One stage's rows in fp32, padded to KD with zeros; a warp takes a row.
+  auto widen = [&](float* to, const unsigned char* from, int half, int n) {
+#pragma unroll 4
+    for (int t = warp; t < n; t += warps) {
+#pragma unroll
+      for (int j = 0; j < (KD + 31) / 32; ++j) {
+        const int e = lane + 32 * j;
+        if (KD % 32 && e >= KD) break;
+        to[t * KD + e] = e < rows ? value(from, half, rows, t, e) : 0.f;
+      }
     }
   };
 
@@ -144,84 +227,105 @@ decay_rows_kernel(const __grid_constant__ Args a, int pass0) {
   bool first = kOut && p.undecayed && segment == 0;
   for (int i0 = range.begin; i0 < range.begin + live; i0 += kTok, stage ^= 1) {
     const int n = min(kTok, range.begin + live - i0);
+    ops::copies_left<0>();
+    __syncthreads();   // this stage's copies are there; the last one's values are used up
     copy(i0 + kTok, stage ^ 1);
-    ops::copies_left<1>();
-    __syncthreads();   // this stage's copies are there; the last one's fp32 values are used up
     const unsigned char* from = smem + stage * raw;
-    if (kOut) widen(fx, from, p.x_half, n, rows, KD);
-    widen(fy, from + raw_x, p.y_half, n, rows, KD);
-    widen(fz, from + raw_x + raw_y, p.z_half, n, cols, cols);
+    if (kOut && !x_as_is) widen(fx, from, p.x_half, n);
+    if (!y_as_is) widen(fy, from + raw_x, p.y_half, n);
+    // (The stage's rows lie as in memory: row `at` is token n - 1 - at against the order.)
+#pragma unroll 4
+    for (int at = warp; at < n; at += warps) {
+      const int t = p.reverse ? n - 1 - at : at;
+      const float w = held ? p.zs * exp2f(-l2 * (float)(t + 1)) : p.zs;
+      for (int e = lane; e < wide; e += 32)
+        fz[at * wide + e] = e < cols ? w * value(from + raw_x + raw_y, p.z_half, cols, at, e) : 0.f;
+    }
+    if (kOut && threadIdx.x < kTok)
+      down[threadIdx.x] = held ? p.os * exp2f(l2 * (float)(threadIdx.x + 1)) : p.os;
     __syncthreads();
-    // The state's factor: it is S times `up` (held), which a token multiplies by 1 / g.
+    // Rows go up or down in memory.
+    const int at0 = p.reverse ? n - 1 : 0, up = p.reverse ? -1 : 1;
+    const float* sx = (x_as_is ? reinterpret_cast<const float*>(from) : fx) + row0 + at0 * KD;
+    const float* sy = (y_as_is ? reinterpret_cast<const float*>(from + raw_x) : fy) + row0 + at0 * KD;
+    const float* sz = fz + col0 + at0 * wide;
+    long long to = 0;
+    if (kOut)
+      to = ((long long)bh * a.tokens + (p.reverse ? range.len - 1 - i0 : i0)) * cols + out_col;
     if (held && first) {
 #pragma unroll
-      for (int c = 0; c < kCols; ++c)
+      for (int i = 0; i < kPairs; ++i)
 #pragma unroll
-        for (int i = 0; i < KD / 2; ++i) S[c][i] = ops::mul(S[c][i], ops::fill<2>(exp2f(-l2)));
+        for (int c = 0; c < kCols; ++c) S[i][c] = mul(S[i][c], two(exp2f(-l2), exp2f(-l2)));
       first = false;
     }
     const float g = exp2f(l2);
 #pragma unroll 1
-    for (int t = 0; t < n; ++t) {
-      const float up = held ? exp2f(-l2 * (float)(t + 1)) : 1.f;
-      const float down = held ? exp2f(l2 * (float)(t + 1)) : 1.f;
-      if (!held && !first) {
+    for (int t = 0; t < n; ++t, sx += up * KD, sy += up * KD, sz += up * wide, to += up * cols) {
+      if (!held) {
+        if (!first) {
 #pragma unroll
-        for (int c = 0; c < kCols; ++c)
+          for (int i = 0; i < kPairs; ++i)
 #pragma unroll
-          for (int i = 0; i < KD / 2; ++i) S[c][i] = ops::mul(S[c][i], ops::fill<2>(g));
-      }
-      first = false;
-      Vec<2> z[kCols], o[kCols][2];
-#pragma unroll
-      for (int c = 0; c < kCols; ++c) {
-        z[c] = ops::fill<2>(col[c] < cols ? fz[t * cols + col[c]] * p.zs * up : 0.f);
-        o[c][0] = o[c][1] = ops::fill<2>(0.f);
-      }
-      const float4* y4 = reinterpret_cast<const float4*>(fy + t * KD);
-      const float4* x4 = reinterpret_cast<const float4*>(fx + t * KD);
-#pragma unroll
-      for (int i = 0; i < KD / 4; ++i) {
-        const float4 y = y4[i];
-        const Vec<2> y0 = {{y.x, y.y}}, y1 = {{y.z, y.w}};
-#pragma unroll
-        for (int c = 0; c < kCols; ++c) {
-          S[c][2 * i] = ops::fma(y0, z[c], S[c][2 * i]);
-          S[c][2 * i + 1] = ops::fma(y1, z[c], S[c][2 * i + 1]);
+            for (int c = 0; c < kCols; ++c) S[i][c] = mul(S[i][c], two(g, g));
         }
-        if (kOut) {
-          const float4 x = x4[i];
-          const Vec<2> x0 = {{x.x, x.y}}, x1 = {{x.z, x.w}};
+        first = false;
+      }
+      Two z[kCols], o[kCols];
 #pragma unroll
-          for (int c = 0; c < kCols; ++c) {
-            o[c][0] = ops::fma(x0, S[c][2 * i], o[c][0]);
-            o[c][1] = ops::fma(x1, S[c][2 * i + 1], o[c][1]);
-          }
+      for (int c = 0; c < kCols; c += 4) {
+        const float4 f = *reinterpret_cast<const float4*>(sz + c);
+        z[c] = two(f.x, f.x), z[c + 1] = two(f.y, f.y);
+        z[c + 2] = two(f.z, f.z), z[c + 3] = two(f.w, f.w);
+      }
+      const ulonglong2* y2 = reinterpret_cast<const ulonglong2*>(sy);
+      const ulonglong2* x2 = reinterpret_cast<const ulonglong2*>(sx);
+#pragma unroll
+      for (int i = 0; i < kPairs; i += 2) {
+        const ulonglong2 y = y2[i / 2];
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) S[i][c] = fma(y.x, z[c], S[i][c]);
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) S[i + 1][c] = fma(y.y, z[c], S[i + 1][c]);
+        if (kOut) {
+          const ulonglong2 x = x2[i / 2];
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) o[c] = i == 0 ? mul(x.x, S[i][c]) : fma(x.x, S[i][c], o[c]);
+#pragma unroll
+          for (int c = 0; c < kCols; ++c) o[c] = fma(x.y, S[i + 1][c], o[c]);
         }
       }
       if (kOut) {
-        const int i = i0 + t;
-        const long long row =
-            ((long long)bh * a.tokens + (p.reverse ? range.len - 1 - i : i)) * cols;
-        const float f = p.os * down;
         float v[kCols];
 #pragma unroll
-        for (int c = 0; c < kCols; ++c)
-          v[c] = f * ((o[c][0].f[0] + o[c][0].f[1]) + (o[c][1].f[0] + o[c][1].f[1]));
+        for (int c = 0; c < kCols; ++c) {
+          const Vec<2> both = apart(o[c]);
+          v[c] = both.f[0] + both.f[1];
+        }
+        across_quarters(v, lane);
+        const float f = down[t];
+        if (out_col < cols) {
+          if (p.out_half) {
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + to;
 #pragma unroll
-        for (int c = 0; c < kCols; ++c)
-          if (col[c] < cols) {
-            if (p.out_half) static_cast<__nv_bfloat16*>(p.out)[row + col[c]] = __float2bfloat16_rn(v[c]);
-            else static_cast<float*>(p.out)[row + col[c]] = v[c];
+            for (int c = 0; c < kCols / 4; ++c)
+              if (c == 0 || out_col + c < cols) out[c] = __float2bfloat16_rn(f * v[c]);
+          } else {
+            float* out = static_cast<float*>(p.out) + to;
+#pragma unroll
+            for (int c = 0; c < kCols / 4; ++c)
+              if (c == 0 || out_col + c < cols) out[c] = f * v[c];
           }
+        }
       }
     }
     if (held) {
       const Fade fade(l, n);
+      const Two less = two(fade.less, fade.less), factor = two(fade.factor, fade.factor);
 #pragma unroll
-      for (int c = 0; c < kCols; ++c)
+      for (int i = 0; i < kPairs; ++i)
 #pragma unroll
-        for (int i = 0; i < KD / 2; ++i) S[c][i] = fade(S[c][i]);
+        for (int c = 0; c < kCols; ++c) S[i][c] = fma(S[i][c], less, mul(S[i][c], factor));
     }
   }
   // Where the state goes: this segment's own, or after the last segment the sequence's.
@@ -233,18 +337,17 @@ decay_rows_kernel(const __grid_constant__ Args a, int pass0) {
     to = p.last + (long long)bh * rows * cols;
     if (p.undecayed && range.len > 0) f = exp2f(l2);
   }
-  if (to) {
-#pragma unroll
-    for (int c = 0; c < kCols; ++c)
-#pragma unroll
-      for (int i = 0; i < KD; ++i)
-        if (i < rows && col[c] < cols) to[(long long)i * cols + col[c]] = S[c][i / 2].f[i & 1] * f;
-  }
+  if (to && cols % 4 == 0 && ((uintptr_t)to & 15) == 0)
+    each_four([&](float v0, float v1, float v2, float v3, int i) {
+      *reinterpret_cast<float4*>(to + i) = make_float4(v0 * f, v1 * f, v2 * f, v3 * f);
+    });
+  else if (to)
+    each_value([&](float v, int row, int col) { to[row * cols + col] = v * f; });
   // Zeros for the segment's padding.
   if (kOut) {
-    const long long row0 = (long long)bh * a.tokens;
-    const long long from = (row0 + max(range.begin, range.len)) * cols;
-    const long long to_end = (row0 + range.end) * cols;
+    const long long start = (long long)bh * a.tokens;
+    const long long from = (start + max(range.begin, range.len)) * cols;
+    const long long to_end = (start + range.end) * cols;
     for (long long i = from + threadIdx.x; i < to_end; i += threads) {
       if (p.out_half) static_cast<uint16_t*>(p.out)[i] = 0;
       else static_cast<float*>(p.out)[i] = 0.f;
@@ -253,21 +356,27 @@ decay_rows_kernel(const __grid_constant__ Args a, int pass0) {
 }
 
 // The state before each segment, from every segment's own (in place): a thread for each value.
+constexpr int kMostSegments = 64;
 __global__ void __launch_bounds__(256)
 decay_carry_kernel(const __grid_constant__ Args a, int tiles) {
+  __shared__ Fade fades[kMostSegments];
   const Pass& p = a.pass[blockIdx.z];
   const int size = p.a * p.b, bh = blockIdx.x / tiles;
   const int i = (blockIdx.x - bh * tiles) * 256 + threadIdx.x;
+  // The segments with tokens come first.
+  if (threadIdx.x < a.segments) {
+    const int live = Range(a, bh, threadIdx.x).live(a, p);
+    fades[threadIdx.x] = Fade(log_decay(a, bh), live - (p.undecayed && threadIdx.x == 0 && live > 0));
+  }
+  __syncthreads();
   if (i >= size) return;
-  const float l = log_decay(a, bh);
   float s = 0.f;
   if (p.first) {
     const int row = i / p.b, col = i - row * p.b;
     s = p.first[(long long)bh * size + (p.first_across ? col * p.a + row : i)];
   }
   float* at = p.states + (long long)bh * a.segments * size + i;
-  bool undecayed = p.undecayed;
-  constexpr int kAhead = 8;   // loads in flight
+  constexpr int kAhead = 32;   // loads in flight (8: 11 us instead of 6 for 32 x 19 states of 64 x 64)
   for (int g0 = 0; g0 < a.segments; g0 += kAhead) {
     float own[kAhead];
 #pragma unroll
@@ -276,13 +385,14 @@ decay_carry_kernel(const __grid_constant__ Args a, int tiles) {
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       if (g0 + u >= a.segments) break;
-      const int live = Range(a, bh, g0 + u).live(a, p);
       at[(long long)(g0 + u) * size] = s;
-      if (live > 0) s = Fade(l, live - undecayed)(s) + own[u];
-      if (live > 0) undecayed = false;
+      s = fades[g0 + u](s) + own[u];   // (a segment without tokens: s, and its own state is zeros)
     }
   }
 }
+
+// The most shared memory of any pass: two stages of fp32 rows of 128, one of them padded.
+constexpr int kMostSmem = kTok * 4 * (2 * 3 * 128 + 3 * 128 + 1);
 
 template <int KD, int kCols>
 cudaError_t launch_pass(const Args& a, int pass0, int passes, int bh, bool out, int warps, size_t smem,
@@ -291,7 +401,7 @@ cudaError_t launch_pass(const Args& a, int pass0, int passes, int bh, bool out, 
   if (smem > 48 * 1024) {
     // As large as any call needs: calls at once do not set it lower for each other.
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kTok * (KD + KD + 128) * 4 * 3);
+                                               kMostSmem);
     if (e != cudaSuccess) return e;
   }
   kernel<<<dim3((unsigned)(bh * a.segments), 1, (unsigned)passes), 32 * warps, smem, st>>>(a, pass0);
@@ -299,7 +409,9 @@ cudaError_t launch_pass(const Args& a, int pass0, int passes, int bh, bool out, 
 }
 
 // Rows of a pass as the kernels pad them.
-int padded(int rows) { return rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+int padded(int rows) {
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 48 ? 48 : rows <= 64 ? 64 : rows <= 96 ? 96 : 128;
+}
 
 }  // namespace
 
@@ -325,25 +437,33 @@ cudaError_t launch_rows(const Args& a, int passes, int bh, cudaStream_t st) {
       while (i + n < passes && padded(a.pass[i + n].a) == kd) ++n;
       int cols = 0;
       size_t smem = 0;
+      const bool out = stage == 2;
       for (int j = i; j < i + n; ++j) {
         const Pass& p = a.pass[j];
         cols = std::max(cols, p.b);
         const size_t x = stage == 2 ? align_up((size_t)kTok * p.a * (p.x_half ? 2 : 4), 16) : 0;
         const size_t y = align_up((size_t)kTok * p.a * (p.y_half ? 2 : 4), 16);
         const size_t z = align_up((size_t)kTok * p.b * (p.z_half ? 2 : 4), 16);
-        smem = std::max(smem, 2 * (x + y + z) +
-                                  sizeof(float) * kTok * ((stage == 2 ? 2 : 1) * kd + p.b));
+        const size_t padded_x = out && (p.x_half || p.a != kd) ? kd : 0;
+        const size_t padded_y = p.y_half || p.a != kd ? kd : 0;
+        smem = std::max(smem, 2 * (x + y + z) + sizeof(float) * kTok * (padded_x + padded_y));
       }
       cudaError_t e;
-      const bool out = stage == 2;
-      if (kd == 128) {
-        e = launch_pass<128, 1>(a, i, n, bh, out, (cols + 31) / 32, smem, st);
-      } else if (kd == 64) {
-        e = cols > 32 ? launch_pass<64, 2>(a, i, n, bh, out, (cols + 63) / 64, smem, st)
-                      : launch_pass<64, 1>(a, i, n, bh, out, 1, smem, st);
-      } else {
-        e = cols > 32 ? launch_pass<32, 2>(a, i, n, bh, out, (cols + 63) / 64, smem, st)
-                      : launch_pass<32, 1>(a, i, n, bh, out, 1, smem, st);
+      // A lane's 8 columns where that is no more than half of them padding, and where it has registers.
+      const bool wide = cols > 32 && kd <= 32;
+      const int warps = wide ? (cols + 63) / 64 : (cols + 31) / 32;
+      smem += sizeof(float) * kTok * (warps * (wide ? 64 : 32) + 1);
+      switch (kd * 2 + wide) {
+        case 32: e = launch_pass<16, 4>(a, i, n, bh, out, warps, smem, st); break;
+        case 33: e = launch_pass<16, 8>(a, i, n, bh, out, warps, smem, st); break;
+        case 64: e = launch_pass<32, 4>(a, i, n, bh, out, warps, smem, st); break;
+        case 65: e = launch_pass<32, 8>(a, i, n, bh, out, warps, smem, st); break;
+        case 96: e = launch_pass<48, 4>(a, i, n, bh, out, warps, smem, st); break;
+        case 97: e = launch_pass<48, 8>(a, i, n, bh, out, warps, smem, st); break;
+        case 128: e = launch_pass<64, 4>(a, i, n, bh, out, warps, smem, st); break;
+        case 129: e = launch_pass<64, 8>(a, i, n, bh, out, warps, smem, st); break;
+        case 192: e = launch_pass<96, 4>(a, i, n, bh, out, warps, smem, st); break;
+        default: e = launch_pass<128, 4>(a, i, n, bh, out, warps, smem, st); break;
       }
       if (e != cudaSuccess) return e;
       i += n;

@@ -25,8 +25,10 @@ namespace rope {
 
 constexpr int kThreads = 256;
 constexpr int kMaxPairs = LAPL_ROPE_MAX_DIM / 2;
-constexpr int kMaxTokens = 8;      // tokens of a CTA at a time
-constexpr int kRows = 2;           // rows of a group in flight
+constexpr int kMaxTokens = 8;      // tokens of a CTA at a time, a power of two
+// Rows of a group in flight, forward.
+constexpr int rows_of(int vec) { return vec == 8 ? 3 : 4; }
+constexpr int kBackRows = 2;       // and backward, of two tensors
 
 struct Part {            // q, k or v
   const void* in;        // rows [B,N,heads*d]  (backward: what it was, or null without a norm)
@@ -44,53 +46,54 @@ struct Args {
   unsigned long long turn[kMaxPairs];   // frequencies, in 2^-64 of a turn
   long long rows;        // B * N tokens
   int tokens, d, pairs, axes, first1, first2;   // first1, first2: first pairs of axes 1 and 2
-  int at_once;           // tokens of a CTA at a time
+  int at_once;           // tokens of a CTA at a time, a power of two
   int lanes_log2;        // lanes of a row
   int norm;
   float eps;
 };
 
-// V values as floats, in memory of either type.
+// V values as they are in memory, in words of 32 bits (one bf16 value: in the low half).
 template <int V, bool kHalf>
-__device__ __forceinline__ void load(float (&x)[V], const void* p, long long at) {
-  if constexpr (kHalf) {
-    const uint16_t* q = static_cast<const uint16_t*>(p) + at;
-    if constexpr (V == 4) {
-      const uint2 w = *reinterpret_cast<const uint2*>(q);
-      x[0] = bf16_lo(w.x), x[1] = bf16_hi(w.x), x[2] = bf16_lo(w.y), x[3] = bf16_hi(w.y);
-    } else if constexpr (V == 2) {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(q);
-      x[0] = bf16_lo(w), x[1] = bf16_hi(w);
+struct Raw {
+  static constexpr int kWords = kHalf ? (V + 1) / 2 : V;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const void* p, long long at) {
+    constexpr int kBytes = V * (kHalf ? 2 : 4);
+    const char* q = static_cast<const char*>(p) + at * (kHalf ? 2 : 4);
+    if constexpr (kBytes == 2) {
+      w[0] = *reinterpret_cast<const uint16_t*>(q);
+    } else if constexpr (kBytes == 4) {
+      w[0] = *reinterpret_cast<const uint32_t*>(q);
+    } else if constexpr (kBytes == 8) {
+      const uint2 v = *reinterpret_cast<const uint2*>(q);
+      w[0] = v.x, w[1] = v.y;
     } else {
-      x[0] = ops::bf16_bits(*q);
-    }
-  } else {
-    const float* q = static_cast<const float*>(p) + at;
-    if constexpr (V == 4) {
-      const float4 w = *reinterpret_cast<const float4*>(q);
-      x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
-    } else if constexpr (V == 2) {
-      const float2 w = *reinterpret_cast<const float2*>(q);
-      x[0] = w.x, x[1] = w.y;
-    } else {
-      x[0] = *q;
+      const uint4 v = *reinterpret_cast<const uint4*>(q);
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
     }
   }
-}
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ float value(int i) const {
+    if constexpr (!kHalf) return __uint_as_float(w[i]);
+    return i & 1 ? bf16_hi(w[i / 2]) : bf16_lo(w[i / 2]);
+  }
+};
 template <int V, bool kHalf>
 __device__ __forceinline__ void store(void* p, long long at, const float (&x)[V]) {
-  if constexpr (kHalf) {
-    uint16_t* q = static_cast<uint16_t*>(p) + at;
-    if constexpr (V == 4)
-      *reinterpret_cast<uint2*>(q) =
-          make_uint2(ops::pack_bf16(x[0], x[1]), ops::pack_bf16(x[2], x[3]));
-    else if constexpr (V == 2) *reinterpret_cast<uint32_t*>(q) = ops::pack_bf16(x[0], x[1]);
-    else *q = (uint16_t)ops::pack_bf16(x[0], 0.f);
+  char* q = static_cast<char*>(p) + at * (kHalf ? 2 : 4);
+  if constexpr (kHalf && V == 1) {
+    *reinterpret_cast<uint16_t*>(q) = (uint16_t)ops::pack_bf16(x[0], 0.f);
   } else {
-    float* q = static_cast<float*>(p) + at;
-    if constexpr (V == 4) *reinterpret_cast<float4*>(q) = make_float4(x[0], x[1], x[2], x[3]);
-    else if constexpr (V == 2) *reinterpret_cast<float2*>(q) = make_float2(x[0], x[1]);
-    else *q = x[0];
+    uint32_t w[Raw<V, kHalf>::kWords];
+#pragma unroll
+    for (int i = 0; i < Raw<V, kHalf>::kWords; ++i)
+      w[i] = kHalf ? ops::pack_bf16(x[2 * i % V], x[(2 * i + 1) % V]) : __float_as_uint(x[i % V]);
+    if constexpr (sizeof(w) == 4) *reinterpret_cast<uint32_t*>(q) = w[0];
+    else if constexpr (sizeof(w) == 8) *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint4*>(q) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -152,96 +155,109 @@ __device__ __forceinline__ float group_sum(float v, int lanes) {
   return v;
 }
 
-// Where a token's part begins: of the rows, and of the heads' planes.
+// A group's token of the CTA's tokens from `first` on, and its places in all parts: of head 0, and from
+// there to the next heads.
 struct Place {
-  long long in, out;
-  __device__ __forceinline__ Place(const Args& a, const Part& p, long long token, int head) {
-    const unsigned b = (unsigned)token / (unsigned)a.tokens, n = (unsigned)token - b * (unsigned)a.tokens;
-    in = token * p.stride + (long long)head * a.d;
-    out = (((long long)b * p.heads + head) * a.tokens + n) * a.d;
+  bool live;
+  int token;            // of the CTA's
+  long long in[3], out[3];
+  __device__ __forceinline__ Place(const Args& a, long long first, int token_of_group) {
+    token = token_of_group;
+    const unsigned at = (unsigned)first + (unsigned)token;
+    live = at < (unsigned long long)a.rows;
+    const unsigned b = at / (unsigned)a.tokens, n = at - b * (unsigned)a.tokens;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      in[i] = (long long)at * a.part[i].stride;
+      out[i] = ((long long)b * a.part[i].heads * a.tokens + n) * a.d;
+    }
   }
 };
 
 template <int V, int NS, bool kInterleaved, bool kHalfIn, bool kHalfOut>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 3)
 rope_forward_kernel(const __grid_constant__ Args a) {
   extern __shared__ float2 cs[];
+  constexpr int kRows = rows_of(V);
   const int lanes = 1 << a.lanes_log2, lane = threadIdx.x & (lanes - 1);
   const int group = threadIdx.x >> a.lanes_log2, groups = kThreads >> a.lanes_log2;
   const float inv_d = 1.f / (float)a.d;
+  // A group has one of the tokens, and every step-th head of it.
+  const int token = group & (a.at_once - 1), head0 = group / a.at_once, step = groups / a.at_once;
+  const int heads_q = a.part[0].heads, heads_qk = heads_q + a.part[1].heads;
+  const int heads = heads_qk + a.part[2].heads;
+  const long long plane = (long long)a.tokens * a.d;
+  const Slot<V, kInterleaved> slot0(lane, a.d, a.pairs);
   for (long long first = (long long)blockIdx.x * a.at_once; first < a.rows;
        first += (long long)gridDim.x * a.at_once) {
     const int count = (int)min((long long)a.at_once, a.rows - first);
-    __syncthreads();   // the last tokens' turns are used up
-    fill_turns(cs, a, first, count);
-    __syncthreads();
-#pragma unroll 1
-    for (int which = 0; which < 3; ++which) {
-      const Part& p = a.part[which];
-      const int rows = p.heads * count;
-      const bool norm = a.norm && which < 2;
-      for (int r0 = group; r0 - group < rows; r0 += kRows * groups) {
-        float x[kRows][NS][2][V];
-        int token[kRows];
-        Place place[kRows] = {Place(a, p, first, 0), Place(a, p, first, 0)};
+    const Place place(a, first, token);
+    Raw<V, kHalfIn> raw[kRows][NS][2];
+    auto load = [&](int h0) {
 #pragma unroll
-        for (int u = 0; u < kRows; ++u) {
-          const int r = r0 + u * groups;
-          const int head = r / count;
-          token[u] = r - head * count;
-          place[u] = Place(a, p, first + token[u], head);
+      for (int u = 0; u < kRows; ++u) {
+        const int h = h0 + u * step, which = (h >= heads_q) + (h >= heads_qk);
+        const int head = h - (which == 0 ? 0 : which == 1 ? heads_q : heads_qk);
+        const long long at = (which == 0 ? place.in[0] : which == 1 ? place.in[1] : place.in[2]) +
+                             (long long)head * a.d;
 #pragma unroll
-          for (int j = 0; j < NS; ++j) {
-            const Slot<V, kInterleaved> s(lane + j * lanes, a.d, a.pairs);
+        for (int j = 0; j < NS; ++j) {
+          const Slot<V, kInterleaved> s = NS == 1 ? slot0 : Slot<V, kInterleaved>(lane + j * lanes, a.d, a.pairs);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              if (r < rows && s.on[h]) {
-                load<V, kHalfIn>(x[u][j][h], p.in, place[u].in + s.at[h]);
-              } else {
-#pragma unroll
-                for (int i = 0; i < V; ++i) x[u][j][h][i] = 0.f;
-              }
-            }
+          for (int e = 0; e < 2; ++e) {
+            if (place.live && h < heads && s.on[e]) raw[u][j][e].load(a.part[which].in, at + s.at[e]);
+            else raw[u][j][e].zero();
           }
         }
+      }
+    };
+    load(head0);   // on their way while the turns are formed
+    if (a.pairs) {
+      __syncthreads();   // the last tokens' turns are used up
+      fill_turns(cs, a, first, count);
+      __syncthreads();
+    }
+#pragma unroll 1
+    for (int h0 = head0; h0 - head0 < heads; h0 += kRows * step) {
+      if (h0 != head0) load(h0);
 #pragma unroll
-        for (int u = 0; u < kRows; ++u) {
-          float rstd = 1.f;
-          if (norm) {
-            float sum = 0.f;
+      for (int u = 0; u < kRows; ++u) {
+        const int h = h0 + u * step, which = (h >= heads_q) + (h >= heads_qk);
+        const int head = h - (which == 0 ? 0 : which == 1 ? heads_q : heads_qk);
+        float x[NS][2][V];
+        float sum = 0.f;
 #pragma unroll
-            for (int j = 0; j < NS; ++j)
+        for (int j = 0; j < NS; ++j)
 #pragma unroll
-              for (int h = 0; h < 2; ++h)
+          for (int e = 0; e < 2; ++e)
 #pragma unroll
-                for (int i = 0; i < V; ++i) sum = fmaf(x[u][j][h][i], x[u][j][h][i], sum);
-            rstd = 1.f / sqrtf(fmaf(group_sum(sum, lanes), inv_d, a.eps));
-          }
-          if (r0 + u * groups >= rows) continue;
-#pragma unroll
-          for (int j = 0; j < NS; ++j) {
-            const Slot<V, kInterleaved> s(lane + j * lanes, a.d, a.pairs);
-            if (norm) {
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                float w[V];
-#pragma unroll
-                for (int i = 0; i < V; ++i) w[i] = 1.f;
-                if (p.weight && s.on[h]) {
-#pragma unroll
-                  for (int i = 0; i < V; ++i) w[i] = p.weight[s.at[h] + i];
-                }
-#pragma unroll
-                for (int i = 0; i < V; ++i) x[u][j][h][i] *= rstd * w[i];
-              }
+            for (int i = 0; i < V; ++i) {
+              x[j][e][i] = raw[u][j][e].value(i);
+              sum = fmaf(x[j][e][i], x[j][e][i], sum);
             }
-            if (which < 2 && s.pair >= 0)
-              turn<V, kInterleaved, false>(x[u][j][0], x[u][j][1],
-                                           cs + token[u] * a.pairs + s.pair);
+        const bool norm = a.norm && which < 2;
+        float rstd = 1.f;
+        if (a.norm) rstd = 1.f / sqrtf(fmaf(group_sum(sum, lanes), inv_d, a.eps));
+        if (!place.live || h >= heads) continue;
+        const float* weight = a.part[which].weight;
+        const long long at = (which == 0 ? place.out[0] : which == 1 ? place.out[1] : place.out[2]) + head * plane;
+        void* out = a.part[which].out;
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              if (s.on[h]) store<V, kHalfOut>(p.out, place[u].out + s.at[h], x[u][j][h]);
+        for (int j = 0; j < NS; ++j) {
+          const Slot<V, kInterleaved> s = NS == 1 ? slot0 : Slot<V, kInterleaved>(lane + j * lanes, a.d, a.pairs);
+          if (norm) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+              for (int i = 0; i < V; ++i)
+                x[j][e][i] *= rstd * (weight && s.on[e] ? weight[s.at[e] + i] : 1.f);
+            }
           }
+          if (which < 2 && s.pair >= 0)
+            turn<V, kInterleaved, false>(x[j][0], x[j][1], cs + place.token * a.pairs + s.pair);
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (s.on[e]) store<V, kHalfOut>(out, at + s.at[e], x[j][e]);
         }
       }
     }
@@ -251,10 +267,9 @@ rope_forward_kernel(const __grid_constant__ Args a) {
 // Sum of a weight's gradient over the CTA's groups, in pairs of floats, to its partial.
 template <int V, int NS, bool kInterleaved>
 __device__ __forceinline__ void write_partial(const Args& a, int which, const ops::Pair (&dw)[NS][2][V],
-                                              float2* scratch, int lane, int lanes, int group,
-                                              int groups) {
+                                              float2* sums, int lane, int lanes, int group, int groups) {
   // One group after another adds to the CTA's sums.
-  float2* sums = scratch;
+  __syncthreads();
   for (int i = threadIdx.x; i < a.d; i += kThreads) sums[i] = make_float2(0.f, 0.f);
   for (int g = 0; g < groups; ++g) {
     __syncthreads();
@@ -278,9 +293,9 @@ __device__ __forceinline__ void write_partial(const Args& a, int which, const op
   __syncthreads();
   float2* out = reinterpret_cast<float2*>(a.partial) + ((long long)blockIdx.x * 2 + which) * a.d;
   for (int i = threadIdx.x; i < a.d; i += kThreads) out[i] = sums[i];
-  __syncthreads();
 }
 
+// dw: a tile's heads are summed in fp32 (some of them to a group), tiles in pairs of floats.
 template <int V, int NS, bool kInterleaved, bool kHalfIn, bool kHalfGrad>
 __global__ void __launch_bounds__(kThreads)
 rope_backward_kernel(const __grid_constant__ Args a) {
@@ -289,100 +304,129 @@ rope_backward_kernel(const __grid_constant__ Args a) {
   const int lanes = 1 << a.lanes_log2, lane = threadIdx.x & (lanes - 1);
   const int group = threadIdx.x >> a.lanes_log2, groups = kThreads >> a.lanes_log2;
   const float inv_d = 1.f / (float)a.d;
-  // One part after another over all of the CTA's tokens: one weight's sums at a time.
-#pragma unroll 1
-  for (int which = 0; which < 3; ++which) {
-    const Part& p = a.part[which];
-    if (p.heads == 0) continue;
-    const bool norm = a.norm && which < 2;
-    ops::Pair dw[NS][2][V];
+  const int token = group & (a.at_once - 1), head0 = group / a.at_once, step = groups / a.at_once;
+  const long long plane = (long long)a.tokens * a.d;
+  ops::Pair dw[2][NS][2][V];
+#pragma unroll
+  for (int w = 0; w < 2; ++w)
 #pragma unroll
     for (int j = 0; j < NS; ++j)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int i = 0; i < V; ++i) dw[j][h][i] = {0.f, 0.f};
-    for (long long first = (long long)blockIdx.x * a.at_once; first < a.rows;
-         first += (long long)gridDim.x * a.at_once) {
-      const int count = (int)min((long long)a.at_once, a.rows - first);
-      if (which < 2 && a.pairs) {
-        __syncthreads();   // the last tokens' turns are used up
-        fill_turns(cs, a, first, count);
-        __syncthreads();
-      }
-      const int rows = p.heads * count;
-      for (int r = group; r - group < rows; r += groups) {
-        const int head = r / count, token = r - head * count;
-        const Place place(a, p, first + token, head);
-        float x[NS][2][V], g[NS][2][V];
+        for (int i = 0; i < V; ++i) dw[w][j][e][i] = {0.f, 0.f};
+  for (long long first = (long long)blockIdx.x * a.at_once; first < a.rows;
+       first += (long long)gridDim.x * a.at_once) {
+    const int count = (int)min((long long)a.at_once, a.rows - first);
+    if (a.pairs) {
+      __syncthreads();   // the last tokens' turns are used up
+      fill_turns(cs, a, first, count);
+      __syncthreads();
+    }
+    const Place place(a, first, token);
 #pragma unroll
-        for (int j = 0; j < NS; ++j) {
-          const Slot<V, kInterleaved> s(lane + j * lanes, a.d, a.pairs);
+    for (int which = 0; which < 3; ++which) {
+      const Part& p = a.part[which];
+      const bool norm = which < 2 && a.norm;
+      float tile[NS][2][V];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const bool on = r < rows && s.on[h];
+      for (int j = 0; j < NS; ++j)
 #pragma unroll
-            for (int i = 0; i < V; ++i) x[j][h][i] = g[j][h][i] = 0.f;
-            if (on) load<V, kHalfGrad>(g[j][h], p.grad, place.out + s.at[h]);
-            if (on && norm) load<V, kHalfIn>(x[j][h], p.in, place.in + s.at[h]);
-          }
-        }
-        if (which < 2) {
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int i = 0; i < V; ++i) tile[j][e][i] = 0.f;
+#pragma unroll 1
+      for (int h0 = head0; h0 - head0 < p.heads; h0 += kBackRows * step) {
+        Raw<V, kHalfGrad> rg[kBackRows][NS][2];
+        Raw<V, kHalfIn> rx[kBackRows][NS][2];
+#pragma unroll
+        for (int u = 0; u < kBackRows; ++u) {
+          const int h = h0 + u * step;
 #pragma unroll
           for (int j = 0; j < NS; ++j) {
             const Slot<V, kInterleaved> s(lane + j * lanes, a.d, a.pairs);
-            if (r < rows && s.pair >= 0)
-              turn<V, kInterleaved, true>(g[j][0], g[j][1], cs + token * a.pairs + s.pair);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const bool on = place.live && h < p.heads && s.on[e];
+              rg[u][j][e].zero();
+              rx[u][j][e].zero();
+              if (on) rg[u][j][e].load(p.grad, place.out[which] + h * plane + s.at[e]);
+              if (on && norm) rx[u][j][e].load(p.in, place.in[which] + (long long)h * a.d + s.at[e]);
+            }
           }
         }
-        if (norm) {
+#pragma unroll
+        for (int u = 0; u < kBackRows; ++u) {
+          const int h = h0 + u * step;
+          const bool live = place.live && h < p.heads;
+          float x[NS][2][V], g[NS][2][V];
           float sum = 0.f;
 #pragma unroll
-          for (int j = 0; j < NS; ++j)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int i = 0; i < V; ++i) sum = fmaf(x[j][h][i], x[j][h][i], sum);
-          const float rstd = 1.f / sqrtf(fmaf(group_sum(sum, lanes), inv_d, a.eps));
-          float dot = 0.f;
-#pragma unroll
           for (int j = 0; j < NS; ++j) {
             const Slot<V, kInterleaved> s(lane + j * lanes, a.d, a.pairs);
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int e = 0; e < 2; ++e)
 #pragma unroll
               for (int i = 0; i < V; ++i) {
-                const float u = x[j][h][i] * rstd;
-                x[j][h][i] = u;
-                if (r < rows) dw[j][h][i].add(g[j][h][i] * u);
-                if (p.weight && s.on[h]) g[j][h][i] *= p.weight[s.at[h] + i];
-                dot = fmaf(g[j][h][i], u, dot);
+                g[j][e][i] = rg[u][j][e].value(i);
+                x[j][e][i] = rx[u][j][e].value(i);
+                sum = fmaf(x[j][e][i], x[j][e][i], sum);
               }
+            if (which < 2 && live && s.pair >= 0)
+              turn<V, kInterleaved, true>(g[j][0], g[j][1], cs + place.token * a.pairs + s.pair);
           }
-          dot = group_sum(dot, lanes) * inv_d;
+          if (norm) {
+            const float rstd = 1.f / sqrtf(fmaf(group_sum(sum, lanes), inv_d, a.eps));
+            float dot = 0.f;
 #pragma unroll
-          for (int j = 0; j < NS; ++j)
+            for (int j = 0; j < NS; ++j) {
+              const Slot<V, kInterleaved> s(lane + j * lanes, a.d, a.pairs);
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+              for (int e = 0; e < 2; ++e)
 #pragma unroll
-              for (int i = 0; i < V; ++i)
-                g[j][h][i] = rstd * fmaf(-x[j][h][i], dot, g[j][h][i]);
-        }
-        if (r < rows) {
+                for (int i = 0; i < V; ++i) {
+                  const float u_ = x[j][e][i] * rstd;
+                  x[j][e][i] = u_;
+                  if (live) tile[j][e][i] = fmaf(g[j][e][i], u_, tile[j][e][i]);
+                  if (p.weight && s.on[e]) g[j][e][i] *= p.weight[s.at[e] + i];
+                  dot = fmaf(g[j][e][i], u_, dot);
+                }
+            }
+            dot = group_sum(dot, lanes) * inv_d;
 #pragma unroll
-          for (int j = 0; j < NS; ++j) {
-            const Slot<V, kInterleaved> s(lane + j * lanes, a.d, a.pairs);
+            for (int j = 0; j < NS; ++j)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-              if (s.on[h]) store<V, kHalfGrad>(p.din, place.in + s.at[h], g[j][h]);
+              for (int e = 0; e < 2; ++e)
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                  g[j][e][i] = rstd * fmaf(-x[j][e][i], dot, g[j][e][i]);
+          }
+          if (live) {
+#pragma unroll
+            for (int j = 0; j < NS; ++j) {
+              const Slot<V, kInterleaved> s(lane + j * lanes, a.d, a.pairs);
+#pragma unroll
+              for (int e = 0; e < 2; ++e)
+                if (s.on[e])
+                  store<V, kHalfGrad>(p.din, place.in[which] + (long long)h * a.d + s.at[e], g[j][e]);
+            }
           }
         }
       }
+      if (which < 2 && a.partial) {
+#pragma unroll
+        for (int j = 0; j < NS; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int i = 0; i < V; ++i) dw[which & 1][j][e][i].add(tile[j][e][i]);
+      }
     }
-    if (a.partial && which < 2) {
-      __syncthreads();
-      write_partial<V, NS, kInterleaved>(a, which, dw, cs, lane, lanes, group, groups);
-    }
+  }
+  if (a.partial) {
+#pragma unroll
+    for (int which = 0; which < 2; ++which)
+      write_partial<V, NS, kInterleaved>(a, which, dw[which], cs, lane, lanes, group, groups);
   }
 }
 
@@ -423,6 +467,9 @@ Kernel by_type(bool half_in, bool half_out) {
 }
 template <bool kBackward, bool kInterleaved>
 Kernel by_shape(int vec, int ns, bool half_in, bool half_out) {
+  if constexpr (!kBackward) {   // 16 bytes of both types
+    if (vec == 8) return rope_forward_kernel<8, 1, kInterleaved, true, true>;
+  }
   if (vec == 4) return by_type<kBackward, 4, 1, kInterleaved>(half_in, half_out);
   if (vec == 2 && ns == 1) return by_type<kBackward, 2, 1, kInterleaved>(half_in, half_out);
   if (vec == 2) return by_type<kBackward, 2, 2, kInterleaved>(half_in, half_out);
@@ -496,7 +543,8 @@ bool heads_fit(const void* p, int dtype, int vec) {
 // Widest vectors that hold whole pairs and that every row and head starts on.
 int vector_of(const lapl_rope_plan& p, const rope::Args& a, bool backward) {
   const lapl_rope_config& c = p.cfg;
-  for (int vec = 4; vec > 1; vec /= 2) {
+  const bool half = !backward && c.in_dtype == LAPL_BF16 && c.out_dtype == LAPL_BF16;
+  for (int vec = half ? 8 : 4; vec > 1; vec /= 2) {
     bool fits = a.d % vec == 0 && a.pairs % vec == 0;
     for (int i = 0; i < 3 && fits; ++i) {
       const rope::Part& t = a.part[i];
