@@ -144,32 +144,51 @@ __device__ __forceinline__ void store_bf16(uint16_t* p, const float (&x)[kPer], 
   }
 }
 
-// Largest absolute value of the warp's; a NaN among them wins (fmaxf would lose it).
-__device__ __forceinline__ float block_max(const float (&x)[kPer]) {
-  float top = 0.f;
+// Largest absolute value of the warp's, and at least `least`; a NaN among them wins, as its bits are larger
+// than any number's.
+__device__ __forceinline__ float block_max(const float (&x)[kPer], float least) {
+  unsigned top = __float_as_uint(least);
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(fabsf(x[i])));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float other = __shfl_xor_sync(0xffffffffu, top, o);
-    asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(other));
-  }
-  return top;
+  for (int i = 0; i < kPer; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, top));
+}
+__device__ __forceinline__ float fast_sqrt(float v) {   // off by a unit
+  float r;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
 }
 
-// x as codes with a scale; kRoot: what is above zero gets a code above zero.
+// x, or with kRoot the root of x, as codes with a scale; kRoot: what is above zero gets a code above zero.
+// Where x / scale falls is clear from x (or its root, off by a unit) times the scale's reciprocal, off by 4
+// units together at most, but next to the middle between two codes, and where codes have fewer bits: there
+// the root and the division are formed exactly.  (For each code they were half of the kernel's
+// instructions, whose issue bounds it: 2^27 values 494 us and 715, root and divisions for each.)
 template <bool kVector, bool kRoot>
-__device__ __forceinline__ void store_f8(uint8_t* p, float* scale_at, const float (&x)[kPer], int lane,
-                                         int n) {
-  float top = block_max(x);
-  asm("max.NaN.f32 %0, %0, %1;" : "+f"(top) : "f"(kAmaxFloor));
-  const float scale = __fmul_rn(top, 1.f / kF8Max);
+__device__ __forceinline__ void store_f8(uint8_t* p, float* scale_at, const float (&x)[kPer],
+                                         const float (&root)[kPer], int lane, int n) {
+  // The root of the largest is the largest root.
+  const float top = block_max(x, kRoot ? 0.f : kAmaxFloor);
+  // (The root of anything above zero is above the floor.)
+  const float most = !kRoot ? top : top > 0.f ? __fsqrt_rn(top) : isnan(top) ? top : kAmaxFloor;
+  const float scale = __fmul_rn(most, 1.f / kF8Max);
   if (lane == 0) *scale_at = scale;
+  const float inverse = 1.f / scale;   // (scale is at least 2^-109)
   float q[kPer];
+  bool exactly = false;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    q[i] = __fdiv_rn(x[i], scale);
-    if (kRoot && x[i] > 0.f && q[i] < kF8Least) q[i] = kF8Least;
+    q[i] = (kRoot ? root[i] : x[i]) * inverse;
+    const int off = (int)(__float_as_uint(q[i]) & 0xFFFFFu) - (0x80000 - 8);
+    exactly |= (unsigned)off <= 16u || (q[i] != 0.f && fabsf(q[i]) < 0.015626f);
+  }
+  if (exactly) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) q[i] = __fdiv_rn(kRoot ? __fsqrt_rn(x[i]) : x[i], scale);
+  }
+  if (kRoot) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (x[i] > 0.f) q[i] = fmaxf(q[i], kF8Least);
   }
 #pragma unroll
   for (int i = 0; i < kPer; i += kVector ? 4 : 1) {
@@ -207,28 +226,36 @@ __device__ __forceinline__ void update(const Table<N>& t, int k, long long at, l
     load_f32<kVector>(x.v, static_cast<const float*>(t.v[k]) + at, lane, n);
   }
   float r[kPer];
+  // The states' products and sums are rounded one by one, as the formulas read, and not contracted: a code
+  // next to a border must not depend on how a compiler joins them.
+  auto each = [](float v) { return ops::fill<2>(v); };
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
+  for (int i = 0; i < kPer; i += 2) {
+    ops::Vec<2> m = {{x.m[i], x.m[i + 1]}}, v = {{x.v[i], x.v[i + 1]}};
     if constexpr (k8) {
-      x.m[i] = __fmul_rn(x.m[i], m_scale);
-      x.v[i] = __fmul_rn(x.v[i], v_scale);
-      x.v[i] = __fmul_rn(x.v[i], x.v[i]);
+      m = ops::mul(m, each(m_scale));
+      v = ops::mul(v, each(v_scale));
+      v = ops::mul(v, v);
     }
-    // The states' products and sums are rounded one by one, as the formulas read, and not contracted:
-    // a code next to a border must not depend on how a compiler joins them.
-    const float g = __fmul_rn(x.g[i], clip);
-    x.m[i] = __fadd_rn(__fmul_rn(s.beta1, x.m[i]), __fmul_rn(s.one_beta1, g));
-    x.v[i] = __fadd_rn(__fmul_rn(s.beta2, x.v[i]), __fmul_rn(__fmul_rn(s.one_beta2, g), g));
-    r[i] = __fsqrt_rn(x.v[i]);
-    // lr m / late1 / (sqrt(v / late2) + eps), with a = lr / late1 and root = 1 / sqrt(late2).
-    x.w[i] = x.w[i] * keep - a * x.m[i] / fmaf(r[i], root, s.eps);
+    const ops::Vec<2> g = ops::mul({{x.g[i], x.g[i + 1]}}, each(clip));
+    m = ops::add(ops::mul(each(s.beta1), m), ops::mul(each(s.one_beta1), g));
+    v = ops::add(ops::mul(each(s.beta2), v), ops::mul(ops::mul(each(s.one_beta2), g), g));
+    const ops::Vec<2> am = ops::mul(m, each(a)), kept = ops::mul({{x.w[i], x.w[i + 1]}}, each(keep));
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      x.m[i + e] = m.f[e];
+      x.v[i + e] = v.f[e];
+      r[i + e] = fast_sqrt(v.f[e]);
+      // lr m / late1 / (sqrt(v / late2) + eps), with a = lr / late1 and root = 1 / sqrt(late2).
+      x.w[i + e] = kept.f[e] - __fdividef(am.f[e], fmaf(r[i + e], root, s.eps));
+    }
   }
   if (master) store_f32<kVector>(master + at, x.w, lane, n);
   if (half) store_bf16<kVector>(static_cast<uint16_t*>(t.param[k]) + at, x.w, lane, n);
   else store_f32<kVector>(static_cast<float*>(t.param[k]) + at, x.w, lane, n);
   if constexpr (k8) {
-    store_f8<kVector, false>(static_cast<uint8_t*>(t.m[k]) + at, t.m_scale[k] + block, x.m, lane, n);
-    store_f8<kVector, true>(static_cast<uint8_t*>(t.v[k]) + at, t.v_scale[k] + block, r, lane, n);
+    store_f8<kVector, false>(static_cast<uint8_t*>(t.m[k]) + at, t.m_scale[k] + block, x.m, r, lane, n);
+    store_f8<kVector, true>(static_cast<uint8_t*>(t.v[k]) + at, t.v_scale[k] + block, x.v, r, lane, n);
   } else {
     store_f32<kVector>(static_cast<float*>(t.m[k]) + at, x.m, lane, n);
     store_f32<kVector>(static_cast<float*>(t.v[k]) + at, x.v, lane, n);
@@ -236,7 +263,7 @@ __device__ __forceinline__ void update(const Table<N>& t, int k, long long at, l
 }
 
 template <bool k8, int N>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, kCtas)
 adamw_kernel(const __grid_constant__ Table<N> t, const __grid_constant__ Step s) {
   float clip = 1.f;
   if (s.norm) {

@@ -39,17 +39,21 @@ lapl_status validate(const lapl_decay_config* c) {
 }
 
 // Segments of a sequence token by token.  A segment's warps walk its tokens alone; by registers 16, 12 or
-// 8 warps of an SM are resident.  More than one segment costs the launch that forms their states, about 0.6 of
-// the other's time, and the launches' own time, about that of 64 tokens.
+// 8 warps of an SM are resident.  Times in us, about as measured: a token of the outputs 0.35, of the
+// segments' sums 0.2, a launch 3, its CTAs 2, and 0.05 for each segment.  (16 sequences of 3136 tokens of
+// 32 x 32 in fp32: 58 us in 64 segments, 85 in 32, 149 in 16.)
 int row_segments(int tokens, long long bh, int rows, int cols, int sms) {
   const int per_warp = rows <= 32 && cols > 32 ? 64 : 32;
   const long long warps = bh * ((cols + per_warp - 1) / per_warp);
-  const long long room = (long long)(rows <= 64 ? 16 : rows <= 96 ? 12 : 8) * sms;
+  const long long room = (rows <= 64 ? 16LL : 48LL) * sms;
   int best = 1;
   double least = 0;
-  for (int g = 1; g <= 64 && (g == 1 || tokens / g >= 32); ++g) {
+  for (int g = 1; g <= decay::kMostSegments && (g == 1 || tokens / g >= 16); ++g) {
     const double waves = (double)((warps * g + room - 1) / room);
-    const double time = (g > 1 ? 1.6 : 1.0) * waves * ((tokens + g - 1) / g) + (g > 1 ? 64.0 : 0.0);
+    const int per = (tokens + g - 1) / g;
+    const double token = std::max(rows, 16) / 32.0;
+    double time = waves * (2.0 + 0.35 * token * per);
+    if (g > 1) time += waves * (2.0 + 0.2 * token * per) + 6.0 + 0.05 * g;
     if (g == 1 || time < least) least = time, best = g;
   }
   return best;

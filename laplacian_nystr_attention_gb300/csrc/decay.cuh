@@ -46,6 +46,7 @@ struct Pass {
 
 constexpr int kMaxPasses = 3;
 constexpr int kTcChunk = 128;   // tokens of a chunk on the tensor cores
+constexpr int kMostSegments = 128;
 struct Args {
   Pass pass[kMaxPasses];
   const float* log_decay;   // [H]

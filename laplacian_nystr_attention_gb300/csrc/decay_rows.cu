@@ -356,7 +356,6 @@ decay_rows_kernel(const __grid_constant__ Args a, int pass0) {
 }
 
 // The state before each segment, from every segment's own (in place): a thread for each value.
-constexpr int kMostSegments = 64;
 __global__ void __launch_bounds__(256)
 decay_carry_kernel(const __grid_constant__ Args a, int tiles) {
   __shared__ Fade fades[kMostSegments];

@@ -121,13 +121,31 @@ struct Slot {
   }
 };
 
+// V floats of shared memory that start on a vector.
+template <int V>
+__device__ __forceinline__ void read(float (&x)[V], const float* p) {
+  if constexpr (V % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(p + i);
+      x[i] = f.x, x[i + 1] = f.y, x[i + 2] = f.z, x[i + 3] = f.w;
+    }
+  } else if constexpr (V == 2) {
+    const float2 f = *reinterpret_cast<const float2*>(p);
+    x[0] = f.x, x[1] = f.y;
+  } else {
+    x[0] = *p;
+  }
+}
+
 // Turns a slot's pairs (back with kBack).
 template <int V, bool kInterleaved, bool kBack>
 __device__ __forceinline__ void turn(float (&a)[V], float (&b)[V], const float2* cs) {
+  float t[2 * V];
+  read<2 * V>(t, reinterpret_cast<const float*>(cs));
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const float2 t = cs[i];
-    const float c = t.x, s = kBack ? -t.y : t.y;
+    const float c = t[2 * i], s = kBack ? -t[2 * i + 1] : t[2 * i + 1];
     // Pair i of the slot: of both vectors, or of the first and then of the second.
     float& x = kInterleaved && V > 1 ? (i < V / 2 ? a[2 * i] : b[2 * i - V]) : a[i];
     float& y = kInterleaved && V > 1 ? (i < V / 2 ? a[2 * i + 1] : b[2 * i - V + 1]) : b[i];
@@ -137,16 +155,30 @@ __device__ __forceinline__ void turn(float (&a)[V], float (&b)[V], const float2*
   }
 }
 
-// cos and sin of `count` tokens' pairs from token `first` on.
+// cos and sin of `count` tokens' pairs from token `first` on, zeros for the others of the CTA's.
 __device__ __forceinline__ void fill_turns(float2* cs, const Args& a, long long first, int count) {
-  for (int i = threadIdx.x; i < count * a.pairs; i += kThreads) {
+  for (int i = threadIdx.x; i < a.at_once * a.pairs; i += kThreads) {
     const int t = i / a.pairs, p = i - t * a.pairs;
+    if (t >= count) {
+      cs[i] = make_float2(0.f, 0.f);
+      continue;
+    }
     const int axis = (p >= a.first1) + (p >= a.first2);
     const long long pos = a.positions[(first + t) * a.axes + axis];
     const long long part = (long long)(a.turn[p] * (unsigned long long)pos);   // signed: -1/2 .. 1/2
     float s, c;
     sincospif(__ll2float_rn(part) * 1.0842021724855044e-19f, &s, &c);   // 2^-63: half turns
     cs[i] = make_float2(c, s);
+  }
+}
+
+// Both weights in shared memory, ones where there are none, [2][padded].
+__host__ __device__ __forceinline__ int padded(int d) { return (d + 7) & ~7; }
+__device__ __forceinline__ void fill_weights(float* w, const Args& a) {
+  for (int i = threadIdx.x; i < 2 * padded(a.d); i += kThreads) {
+    const int which = i >= padded(a.d), e = i - which * padded(a.d);
+    const float* from = which ? a.part[1].weight : a.part[0].weight;
+    w[i] = from && e < a.d ? from[e] : 1.f;
   }
 }
 
@@ -177,8 +209,15 @@ struct Place {
 template <int V, int NS, bool kInterleaved, bool kHalfIn, bool kHalfOut>
 __global__ void __launch_bounds__(kThreads, 3)
 rope_forward_kernel(const __grid_constant__ Args a) {
-  extern __shared__ float2 cs[];
+  extern __shared__ __align__(16) float smem[];
   constexpr int kRows = rows_of(V);
+  const int pad = padded(a.d);
+  const float* weights = smem;
+  float2* cs = reinterpret_cast<float2*>(smem + 2 * pad);
+  if (a.norm) {
+    fill_weights(smem, a);
+    __syncthreads();
+  }
   const int lanes = 1 << a.lanes_log2, lane = threadIdx.x & (lanes - 1);
   const int group = threadIdx.x >> a.lanes_log2, groups = kThreads >> a.lanes_log2;
   const float inv_d = 1.f / (float)a.d;
@@ -239,7 +278,7 @@ rope_forward_kernel(const __grid_constant__ Args a) {
         float rstd = 1.f;
         if (a.norm) rstd = 1.f / sqrtf(fmaf(group_sum(sum, lanes), inv_d, a.eps));
         if (!place.live || h >= heads) continue;
-        const float* weight = a.part[which].weight;
+        const float* weight = weights + (which ? pad : 0);
         const long long at = (which == 0 ? place.out[0] : which == 1 ? place.out[1] : place.out[2]) + head * plane;
         void* out = a.part[which].out;
 #pragma unroll
@@ -248,9 +287,10 @@ rope_forward_kernel(const __grid_constant__ Args a) {
           if (norm) {
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
+              float w[V];
+              read<V>(w, weight + (s.on[e] ? s.at[e] : 0));
 #pragma unroll
-              for (int i = 0; i < V; ++i)
-                x[j][e][i] *= rstd * (weight && s.on[e] ? weight[s.at[e] + i] : 1.f);
+              for (int i = 0; i < V; ++i) x[j][e][i] *= rstd * w[i];
             }
           }
           if (which < 2 && s.pair >= 0)
@@ -264,97 +304,119 @@ rope_forward_kernel(const __grid_constant__ Args a) {
   }
 }
 
-// Sum of a weight's gradient over the CTA's groups, in pairs of floats, to its partial.
+// Adds what the CTA's threads have of a weight's gradient to its sums in shared memory, in pairs of
+// floats and a fixed order: a warp's groups by shuffles, then warp after warp.
 template <int V, int NS, bool kInterleaved>
-__device__ __forceinline__ void write_partial(const Args& a, int which, const ops::Pair (&dw)[NS][2][V],
-                                              float2* sums, int lane, int lanes, int group, int groups) {
-  // One group after another adds to the CTA's sums.
-  __syncthreads();
-  for (int i = threadIdx.x; i < a.d; i += kThreads) sums[i] = make_float2(0.f, 0.f);
-  for (int g = 0; g < groups; ++g) {
-    __syncthreads();
-    if (g != group) continue;
+__device__ __forceinline__ void add_to_sums(const Args& a, const float (&dw)[NS][2][V], float2* sums,
+                                            int lane, int lanes) {
+  const int warp = threadIdx.x >> 5;
 #pragma unroll
-    for (int j = 0; j < NS; ++j) {
-      const Slot<V, kInterleaved> s(lane + j * lanes, a.d, a.pairs);
+  for (int j = 0; j < NS; ++j) {
+    const Slot<V, kInterleaved> s(lane + j * lanes, a.d, a.pairs);
+    ops::Pair v[2][V];
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (s.on[h]) {
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        v[e][i] = {dw[j][e][i], 0.f};
+        for (int o = lanes; o < 32; o *= 2) {
+          const float hi = __shfl_xor_sync(0xffffffffu, v[e][i].hi, o);
+          v[e][i].add(hi, __shfl_xor_sync(0xffffffffu, v[e][i].lo, o));
+        }
+      }
+    for (int w = 0; w < kThreads / 32; ++w) {
+      __syncthreads();
+      if (w != warp || (threadIdx.x & 31) >= lanes) continue;
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (s.on[e]) {
 #pragma unroll
           for (int i = 0; i < V; ++i) {
-            const float2 old = sums[s.at[h] + i];
-            ops::Pair v = {old.x, old.y};
-            v.add(dw[j][h][i].hi, dw[j][h][i].lo);
-            sums[s.at[h] + i] = make_float2(v.hi, v.lo);
+            const float2 old = sums[s.at[e] + i];
+            ops::Pair sum = {old.x, old.y};
+            sum.add(v[e][i].hi, v[e][i].lo);
+            sums[s.at[e] + i] = make_float2(sum.hi, sum.lo);
           }
         }
     }
   }
-  __syncthreads();
-  float2* out = reinterpret_cast<float2*>(a.partial) + ((long long)blockIdx.x * 2 + which) * a.d;
-  for (int i = threadIdx.x; i < a.d; i += kThreads) out[i] = sums[i];
 }
 
-// dw: a tile's heads are summed in fp32 (some of them to a group), tiles in pairs of floats.
+// dw: a thread's rows are summed in fp32, kTiles CTA's tokens of them at most, what follows in pairs of floats.
+constexpr int kTiles = 32;
 template <int V, int NS, bool kInterleaved, bool kHalfIn, bool kHalfGrad>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 rope_backward_kernel(const __grid_constant__ Args a) {
-  extern __shared__ float2 cs[];
+  extern __shared__ __align__(16) float smem[];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int pad = padded(a.d);
+  float2* cs = reinterpret_cast<float2*>(smem + 2 * pad);
+  float2* sums = cs + a.pairs * a.at_once;   // [2][d]
+  if (a.norm) {
+    fill_weights(smem, a);
+    __syncthreads();
+  }
   const int lanes = 1 << a.lanes_log2, lane = threadIdx.x & (lanes - 1);
   const int group = threadIdx.x >> a.lanes_log2, groups = kThreads >> a.lanes_log2;
   const float inv_d = 1.f / (float)a.d;
   const int token = group & (a.at_once - 1), head0 = group / a.at_once, step = groups / a.at_once;
   const long long plane = (long long)a.tokens * a.d;
-  ops::Pair dw[2][NS][2][V];
+  const Slot<V, kInterleaved> slot0(lane, a.d, a.pairs);
+  auto slot = [&](int j) { return NS == 1 ? slot0 : Slot<V, kInterleaved>(lane + j * lanes, a.d, a.pairs); };
+  if (a.partial)
+    for (int i = threadIdx.x; i < 2 * a.d; i += kThreads) sums[i] = make_float2(0.f, 0.f);
+  float dw[2][NS][2][V];
+  auto clear = [&] {
 #pragma unroll
-  for (int w = 0; w < 2; ++w)
-#pragma unroll
-    for (int j = 0; j < NS; ++j)
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int i = 0; i < V; ++i) dw[w][j][e][i] = {0.f, 0.f};
-  for (long long first = (long long)blockIdx.x * a.at_once; first < a.rows;
-       first += (long long)gridDim.x * a.at_once) {
-    const int count = (int)min((long long)a.at_once, a.rows - first);
-    if (a.pairs) {
-      __syncthreads();   // the last tokens' turns are used up
-      fill_turns(cs, a, first, count);
-      __syncthreads();
-    }
-    const Place place(a, first, token);
-#pragma unroll
-    for (int which = 0; which < 3; ++which) {
-      const Part& p = a.part[which];
-      const bool norm = which < 2 && a.norm;
-      float tile[NS][2][V];
+    for (int w = 0; w < 2; ++w)
 #pragma unroll
       for (int j = 0; j < NS; ++j)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
-          for (int i = 0; i < V; ++i) tile[j][e][i] = 0.f;
-#pragma unroll 1
-      for (int h0 = head0; h0 - head0 < p.heads; h0 += kBackRows * step) {
-        Raw<V, kHalfGrad> rg[kBackRows][NS][2];
-        Raw<V, kHalfIn> rx[kBackRows][NS][2];
+          for (int i = 0; i < V; ++i) dw[w][j][e][i] = 0.f;
+  };
+  clear();
+  int tiles = 0;
+  for (long long first = (long long)blockIdx.x * a.at_once; first < a.rows;
+       first += (long long)gridDim.x * a.at_once) {
+    const int count = (int)min((long long)a.at_once, a.rows - first);
+    const Place place(a, first, token);
+    Raw<V, kHalfGrad> rg[kBackRows][NS][2];
+    Raw<V, kHalfIn> rx[kBackRows][NS][2];
+    auto load = [&](int which, int h0) {
+      const Part& p = a.part[which];
 #pragma unroll
-        for (int u = 0; u < kBackRows; ++u) {
-          const int h = h0 + u * step;
+      for (int u = 0; u < kBackRows; ++u) {
+        const int h = h0 + u * step;
 #pragma unroll
-          for (int j = 0; j < NS; ++j) {
-            const Slot<V, kInterleaved> s(lane + j * lanes, a.d, a.pairs);
+        for (int j = 0; j < NS; ++j) {
+          const Slot<V, kInterleaved> s = slot(j);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const bool on = place.live && h < p.heads && s.on[e];
-              rg[u][j][e].zero();
-              rx[u][j][e].zero();
-              if (on) rg[u][j][e].load(p.grad, place.out[which] + h * plane + s.at[e]);
-              if (on && norm) rx[u][j][e].load(p.in, place.in[which] + (long long)h * a.d + s.at[e]);
-            }
+          for (int e = 0; e < 2; ++e) {
+            const bool on = place.live && h < p.heads && s.on[e];
+            rg[u][j][e].zero();
+            rx[u][j][e].zero();
+            if (on) rg[u][j][e].load(p.grad, place.out[which] + h * plane + s.at[e]);
+            if (on && which < 2 && a.norm)
+              rx[u][j][e].load(p.in, place.in[which] + (long long)h * a.d + s.at[e]);
           }
         }
+      }
+    };
+    load(0, head0);   // on their way while the turns are formed
+    if (a.pairs) {
+      __syncthreads();   // the last tokens' turns are used up
+      fill_turns(cs, a, first, count);
+      __syncthreads();
+    }
+#pragma unroll
+    for (int which = 0; which < 3; ++which) {
+      const Part& p = a.part[which];
+      const bool norm = which < 2 && a.norm;
+#pragma unroll 1
+      for (int h0 = head0; h0 - head0 < p.heads; h0 += kBackRows * step) {
+        if (which > 0 || h0 != head0) load(which, h0);
 #pragma unroll
         for (int u = 0; u < kBackRows; ++u) {
           const int h = h0 + u * step;
@@ -363,7 +425,7 @@ rope_backward_kernel(const __grid_constant__ Args a) {
           float sum = 0.f;
 #pragma unroll
           for (int j = 0; j < NS; ++j) {
-            const Slot<V, kInterleaved> s(lane + j * lanes, a.d, a.pairs);
+            const Slot<V, kInterleaved> s = slot(j);
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll
@@ -372,25 +434,30 @@ rope_backward_kernel(const __grid_constant__ Args a) {
                 x[j][e][i] = rx[u][j][e].value(i);
                 sum = fmaf(x[j][e][i], x[j][e][i], sum);
               }
-            if (which < 2 && live && s.pair >= 0)
+            if (which < 2 && s.pair >= 0)
               turn<V, kInterleaved, true>(g[j][0], g[j][1], cs + place.token * a.pairs + s.pair);
           }
           if (norm) {
-            const float rstd = 1.f / sqrtf(fmaf(group_sum(sum, lanes), inv_d, a.eps));
+            // (Rows that are not there: all zeros, whose rstd may be infinite.)
+            const float mean = fmaf(group_sum(sum, lanes), inv_d, a.eps);
+            const float rstd = live ? 1.f / sqrtf(mean) : 0.f;
             float dot = 0.f;
 #pragma unroll
             for (int j = 0; j < NS; ++j) {
-              const Slot<V, kInterleaved> s(lane + j * lanes, a.d, a.pairs);
+              const Slot<V, kInterleaved> s = slot(j);
 #pragma unroll
-              for (int e = 0; e < 2; ++e)
+              for (int e = 0; e < 2; ++e) {
+                float w[V];
+                read<V>(w, smem + (which ? pad : 0) + (s.on[e] ? s.at[e] : 0));
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                  const float u_ = x[j][e][i] * rstd;
-                  x[j][e][i] = u_;
-                  if (live) tile[j][e][i] = fmaf(g[j][e][i], u_, tile[j][e][i]);
-                  if (p.weight && s.on[e]) g[j][e][i] *= p.weight[s.at[e] + i];
-                  dot = fmaf(g[j][e][i], u_, dot);
+                  const float v = x[j][e][i] * rstd;
+                  x[j][e][i] = v;
+                  dw[which & 1][j][e][i] = fmaf(g[j][e][i], v, dw[which & 1][j][e][i]);
+                  g[j][e][i] *= w[i];
+                  dot = fmaf(g[j][e][i], v, dot);
                 }
+              }
             }
             dot = group_sum(dot, lanes) * inv_d;
 #pragma unroll
@@ -404,7 +471,7 @@ rope_backward_kernel(const __grid_constant__ Args a) {
           if (live) {
 #pragma unroll
             for (int j = 0; j < NS; ++j) {
-              const Slot<V, kInterleaved> s(lane + j * lanes, a.d, a.pairs);
+              const Slot<V, kInterleaved> s = slot(j);
 #pragma unroll
               for (int e = 0; e < 2; ++e)
                 if (s.on[e])
@@ -413,20 +480,19 @@ rope_backward_kernel(const __grid_constant__ Args a) {
           }
         }
       }
-      if (which < 2 && a.partial) {
+    }
+    if (a.partial && (++tiles == kTiles || first + (long long)gridDim.x * a.at_once >= a.rows)) {
 #pragma unroll
-        for (int j = 0; j < NS; ++j)
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int i = 0; i < V; ++i) dw[which & 1][j][e][i].add(tile[j][e][i]);
-      }
+      for (int which = 0; which < 2; ++which)
+        add_to_sums<V, NS, kInterleaved>(a, dw[which], sums + which * a.d, lane, lanes);
+      clear();
+      tiles = 0;
     }
   }
   if (a.partial) {
-#pragma unroll
-    for (int which = 0; which < 2; ++which)
-      write_partial<V, NS, kInterleaved>(a, which, dw[which], cs, lane, lanes, group, groups);
+    __syncthreads();
+    float2* out = reinterpret_cast<float2*>(a.partial) + (long long)blockIdx.x * 2 * a.d;
+    for (int i = threadIdx.x; i < 2 * a.d; i += kThreads) out[i] = sums[i];
   }
 }
 
@@ -467,9 +533,10 @@ Kernel by_type(bool half_in, bool half_out) {
 }
 template <bool kBackward, bool kInterleaved>
 Kernel by_shape(int vec, int ns, bool half_in, bool half_out) {
-  if constexpr (!kBackward) {   // 16 bytes of both types
-    if (vec == 8) return rope_forward_kernel<8, 1, kInterleaved, true, true>;
-  }
+  // 16 bytes of both types.
+  if (vec == 8)
+    return kBackward ? rope_backward_kernel<8, 1, kInterleaved, true, true>
+                     : rope_forward_kernel<8, 1, kInterleaved, true, true>;
   if (vec == 4) return by_type<kBackward, 4, 1, kInterleaved>(half_in, half_out);
   if (vec == 2 && ns == 1) return by_type<kBackward, 2, 1, kInterleaved>(half_in, half_out);
   if (vec == 2) return by_type<kBackward, 2, 2, kInterleaved>(half_in, half_out);
@@ -492,7 +559,7 @@ using namespace lapl;
 
 namespace {
 
-constexpr int kBackwardCtas = 4;   // of an SM
+constexpr int kBackwardCtas = 2;   // of an SM, all resident at once
 
 lapl_status validate(const lapl_rope_config* c) {
   if (!c || c->batch < 0 || c->tokens < 1 || c->q_heads < 1 || c->k_heads < 0 || c->v_heads < 0 ||
@@ -543,7 +610,7 @@ bool heads_fit(const void* p, int dtype, int vec) {
 // Widest vectors that hold whole pairs and that every row and head starts on.
 int vector_of(const lapl_rope_plan& p, const rope::Args& a, bool backward) {
   const lapl_rope_config& c = p.cfg;
-  const bool half = !backward && c.in_dtype == LAPL_BF16 && c.out_dtype == LAPL_BF16;
+  const bool half = c.in_dtype == LAPL_BF16 && (backward ? c.grad_dtype : c.out_dtype) == LAPL_BF16;
   for (int vec = half ? 8 : 4; vec > 1; vec /= 2) {
     bool fits = a.d % vec == 0 && a.pairs % vec == 0;
     for (int i = 0; i < 3 && fits; ++i) {
@@ -585,8 +652,9 @@ cudaError_t launch(const lapl_rope_plan& p, rope::Args& a, bool backward, int* c
   else
     k = c.interleaved ? rope::by_shape<false, true>(vec, ns_rounded, hi, ho)
                       : rope::by_shape<false, false>(vec, ns_rounded, hi, ho);
-  // The turns, and in the backward in the same place a weight's sums.
-  const size_t smem = sizeof(float2) * std::max(a.pairs * at_once, backward ? a.d : 0);
+  // Both weights, the turns, and in the backward both weights' sums.
+  const size_t smem =
+      sizeof(float2) * (rope::padded(a.d) + a.pairs * at_once + (backward ? 2 * a.d : 0));
   k<<<grid, rope::kThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
