@@ -25,10 +25,11 @@ namespace rope {
 
 constexpr int kThreads = 256;
 constexpr int kMaxPairs = LAPL_ROPE_MAX_DIM / 2;
-constexpr int kMaxTokens = 8;      // tokens of a CTA at a time, a power of two
+constexpr int kTokens = 16, kMaxTokens = 32;   // tokens of a CTA at a time, powers of two
 // Rows of a group in flight, forward.
 constexpr int rows_of(int vec) { return vec == 8 ? 3 : 4; }
-constexpr int kBackRows = 2;       // and backward, of two tensors
+constexpr int back_rows_of(int vec) { return vec == 8 ? 1 : 2; }   // and backward, of two tensors
+constexpr int kBackCtas = 2;   // CTAs of an SM, by registers (3 with 80 registers: spills, and no faster)
 
 struct Part {            // q, k or v
   const void* in;        // rows [B,N,heads*d]  (backward: what it was, or null without a norm)
@@ -97,29 +98,45 @@ __device__ __forceinline__ void store(void* p, long long at, const float (&x)[V]
   }
 }
 
-// The two vectors of a lane's slot j: where they start in a head and whether they are there.  The
-// first pairs / V slots are turned; the rest hold the values after them, two vectors to a slot.
+// The two vectors of a lane's slot: where they start in a head, whether they are there, and the first
+// pair that each turns, or -1.  Pairs of a head's halves: the first pairs / V slots are turned, a vector of
+// one half and one of the other; the rest hold the values after them.  Interleaved: a head's vectors in
+// their order, which hold whole pairs each.
 template <int V, bool kInterleaved>
 struct Slot {
   int at[2];
   bool on[2];
-  int pair;   // first pair, or -1
+  int pair[2];
   __device__ __forceinline__ Slot(int s, int d, int pairs) {
-    const int turned = pairs / V;
-    if (s < turned) {
-      at[0] = kInterleaved ? 2 * V * s : V * s;
-      at[1] = at[0] + (kInterleaved ? V : pairs);
+    if (kInterleaved && V > 1) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        at[e] = V * (2 * s + e);
+        on[e] = at[e] < d;
+        pair[e] = at[e] < 2 * pairs ? at[e] / 2 : -1;
+      }
+    } else if (s < pairs / V) {
+      at[0] = kInterleaved ? 2 * s : V * s;
+      at[1] = kInterleaved ? 2 * s + 1 : at[0] + pairs;
       on[0] = on[1] = true;
-      pair = V * s;
+      pair[0] = pair[1] = V * s;
     } else {
-      at[0] = 2 * pairs + 2 * V * (s - turned);
+      at[0] = 2 * pairs + 2 * V * (s - pairs / V);
       at[1] = at[0] + V;
       on[0] = at[0] < d;
       on[1] = at[1] < d;
-      pair = -1;
+      pair[0] = pair[1] = -1;
     }
   }
 };
+
+// Where the cosine and sine of the CTA's i-th (token, pair) are: 16-byte units of two pairs, spread so that
+// eight lanes' units a vector or two apart lie in different banks.
+__device__ __forceinline__ int turn_at(int i) {
+  const int u = i >> 1;
+  return (u ^ ((u >> 2) & 7)) * 2 + (i & 1);
+}
+__host__ __device__ __forceinline__ int turns_of(int n) { return (n + 15) & ~15; }   // room
 
 // V floats of shared memory that start on a vector.
 template <int V>
@@ -138,20 +155,47 @@ __device__ __forceinline__ void read(float (&x)[V], const float* p) {
   }
 }
 
-// Turns a slot's pairs (back with kBack).
+// Turns x, y by the angle.
+template <bool kBack>
+__device__ __forceinline__ void turn_one(float& x, float& y, float c, float s) {
+  if (kBack) s = -s;
+  const float p = x, q = y;
+  x = fmaf(p, c, -(q * s));
+  y = fmaf(q, c, p * s);
+}
+// Turns a slot's pairs (back with kBack); first: the token's first place among the turns.
 template <int V, bool kInterleaved, bool kBack>
-__device__ __forceinline__ void turn(float (&a)[V], float (&b)[V], const float2* cs) {
-  float t[2 * V];
-  read<2 * V>(t, reinterpret_cast<const float*>(cs));
+__device__ __forceinline__ void turn(float (&a)[V], float (&b)[V], const Slot<V, kInterleaved>& s,
+                                     const float2* cs, int first) {
+  if constexpr (V == 1) {
+    if (s.pair[0] < 0) return;
+    const float2 t = cs[turn_at(first + s.pair[0])];
+    turn_one<kBack>(a[0], b[0], t.x, t.y);
+  } else if constexpr (kInterleaved) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const float c = t[2 * i], s = kBack ? -t[2 * i + 1] : t[2 * i + 1];
-    // Pair i of the slot: of both vectors, or of the first and then of the second.
-    float& x = kInterleaved && V > 1 ? (i < V / 2 ? a[2 * i] : b[2 * i - V]) : a[i];
-    float& y = kInterleaved && V > 1 ? (i < V / 2 ? a[2 * i + 1] : b[2 * i - V + 1]) : b[i];
-    const float p = x, q = y;
-    x = fmaf(p, c, -(q * s));
-    y = fmaf(q, c, p * s);
+    for (int e = 0; e < 2; ++e) {
+      if (s.pair[e] < 0) continue;
+      float (&x)[V] = e ? b : a;
+      if constexpr (V == 2) {
+        const float2 t = cs[turn_at(first + s.pair[e])];
+        turn_one<kBack>(x[0], x[1], t.x, t.y);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V / 2; i += 2) {
+          const float2 t = cs[turn_at(first + s.pair[e] + i)], u = cs[turn_at(first + s.pair[e] + i + 1)];
+          turn_one<kBack>(x[2 * i], x[2 * i + 1], t.x, t.y);
+          turn_one<kBack>(x[2 * i + 2], x[2 * i + 3], u.x, u.y);
+        }
+      }
+    }
+  } else {
+    if (s.pair[0] < 0) return;
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {   // (a token's pairs are a multiple of V: even places)
+      const float4 t = *reinterpret_cast<const float4*>(cs + turn_at(first + s.pair[0] + i));
+      turn_one<kBack>(a[i], b[i], t.x, t.y);
+      turn_one<kBack>(a[i + 1], b[i + 1], t.z, t.w);
+    }
   }
 }
 
@@ -160,7 +204,7 @@ __device__ __forceinline__ void fill_turns(float2* cs, const Args& a, long long 
   for (int i = threadIdx.x; i < a.at_once * a.pairs; i += kThreads) {
     const int t = i / a.pairs, p = i - t * a.pairs;
     if (t >= count) {
-      cs[i] = make_float2(0.f, 0.f);
+      cs[turn_at(i)] = make_float2(0.f, 0.f);
       continue;
     }
     const int axis = (p >= a.first1) + (p >= a.first2);
@@ -168,7 +212,7 @@ __device__ __forceinline__ void fill_turns(float2* cs, const Args& a, long long 
     const long long part = (long long)(a.turn[p] * (unsigned long long)pos);   // signed: -1/2 .. 1/2
     float s, c;
     sincospif(__ll2float_rn(part) * 1.0842021724855044e-19f, &s, &c);   // 2^-63: half turns
-    cs[i] = make_float2(c, s);
+    cs[turn_at(i)] = make_float2(c, s);
   }
 }
 
@@ -235,6 +279,7 @@ rope_forward_kernel(const __grid_constant__ Args a) {
     auto load = [&](int h0) {
 #pragma unroll
       for (int u = 0; u < kRows; ++u) {
+        if (h0 - head0 + u * step >= heads) break;   // (no group has a row there)
         const int h = h0 + u * step, which = (h >= heads_q) + (h >= heads_qk);
         const int head = h - (which == 0 ? 0 : which == 1 ? heads_q : heads_qk);
         const long long at = (which == 0 ? place.in[0] : which == 1 ? place.in[1] : place.in[2]) +
@@ -261,6 +306,7 @@ rope_forward_kernel(const __grid_constant__ Args a) {
       if (h0 != head0) load(h0);
 #pragma unroll
       for (int u = 0; u < kRows; ++u) {
+        if (h0 - head0 + u * step >= heads) break;
         const int h = h0 + u * step, which = (h >= heads_q) + (h >= heads_qk);
         const int head = h - (which == 0 ? 0 : which == 1 ? heads_q : heads_qk);
         float x[NS][2][V];
@@ -276,7 +322,7 @@ rope_forward_kernel(const __grid_constant__ Args a) {
             }
         const bool norm = a.norm && which < 2;
         float rstd = 1.f;
-        if (a.norm) rstd = 1.f / sqrtf(fmaf(group_sum(sum, lanes), inv_d, a.eps));
+        if (a.norm) rstd = rsqrtf(fmaf(group_sum(sum, lanes), inv_d, a.eps));   // off by 2 units
         if (!place.live || h >= heads) continue;
         const float* weight = weights + (which ? pad : 0);
         const long long at = (which == 0 ? place.out[0] : which == 1 ? place.out[1] : place.out[2]) + head * plane;
@@ -293,8 +339,8 @@ rope_forward_kernel(const __grid_constant__ Args a) {
               for (int i = 0; i < V; ++i) x[j][e][i] *= rstd * w[i];
             }
           }
-          if (which < 2 && s.pair >= 0)
-            turn<V, kInterleaved, false>(x[j][0], x[j][1], cs + place.token * a.pairs + s.pair);
+          if (which < 2)
+            turn<V, kInterleaved, false>(x[j][0], x[j][1], s, cs, place.token * a.pairs);
 #pragma unroll
           for (int e = 0; e < 2; ++e)
             if (s.on[e]) store<V, kHalfOut>(out, at + s.at[e], x[j][e]);
@@ -345,13 +391,14 @@ __device__ __forceinline__ void add_to_sums(const Args& a, const float (&dw)[NS]
 // dw: a thread's rows are summed in fp32, kTiles CTA's tokens of them at most, what follows in pairs of floats.
 constexpr int kTiles = 32;
 template <int V, int NS, bool kInterleaved, bool kHalfIn, bool kHalfGrad>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, kBackCtas)
 rope_backward_kernel(const __grid_constant__ Args a) {
+  constexpr int kBackRows = back_rows_of(V);
   extern __shared__ __align__(16) float smem[];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int pad = padded(a.d);
   float2* cs = reinterpret_cast<float2*>(smem + 2 * pad);
-  float2* sums = cs + a.pairs * a.at_once;   // [2][d]
+  float2* sums = cs + turns_of(a.pairs * a.at_once);   // [2][d]
   if (a.norm) {
     fill_weights(smem, a);
     __syncthreads();
@@ -388,6 +435,7 @@ rope_backward_kernel(const __grid_constant__ Args a) {
       const Part& p = a.part[which];
 #pragma unroll
       for (int u = 0; u < kBackRows; ++u) {
+        if (h0 - head0 + u * step >= p.heads) break;   // (no group has a row there)
         const int h = h0 + u * step;
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
@@ -419,6 +467,7 @@ rope_backward_kernel(const __grid_constant__ Args a) {
         if (which > 0 || h0 != head0) load(which, h0);
 #pragma unroll
         for (int u = 0; u < kBackRows; ++u) {
+          if (h0 - head0 + u * step >= p.heads) break;
           const int h = h0 + u * step;
           const bool live = place.live && h < p.heads;
           float x[NS][2][V], g[NS][2][V];
@@ -434,13 +483,13 @@ rope_backward_kernel(const __grid_constant__ Args a) {
                 x[j][e][i] = rx[u][j][e].value(i);
                 sum = fmaf(x[j][e][i], x[j][e][i], sum);
               }
-            if (which < 2 && s.pair >= 0)
-              turn<V, kInterleaved, true>(g[j][0], g[j][1], cs + place.token * a.pairs + s.pair);
+            if (which < 2)
+              turn<V, kInterleaved, true>(g[j][0], g[j][1], s, cs, place.token * a.pairs);
           }
           if (norm) {
             // (Rows that are not there: all zeros, whose rstd may be infinite.)
             const float mean = fmaf(group_sum(sum, lanes), inv_d, a.eps);
-            const float rstd = live ? 1.f / sqrtf(mean) : 0.f;
+            const float rstd = live ? rsqrtf(mean) : 0.f;
             float dot = 0.f;
 #pragma unroll
             for (int j = 0; j < NS; ++j) {
@@ -559,8 +608,6 @@ using namespace lapl;
 
 namespace {
 
-constexpr int kBackwardCtas = 2;   // of an SM, all resident at once
-
 lapl_status validate(const lapl_rope_config* c) {
   if (!c || c->batch < 0 || c->tokens < 1 || c->q_heads < 1 || c->k_heads < 0 || c->v_heads < 0 ||
       c->head_dim < 1 || c->axes < 1 || c->axes > 3 || !c->pairs)
@@ -612,7 +659,7 @@ int vector_of(const lapl_rope_plan& p, const rope::Args& a, bool backward) {
   const lapl_rope_config& c = p.cfg;
   const bool half = c.in_dtype == LAPL_BF16 && (backward ? c.grad_dtype : c.out_dtype) == LAPL_BF16;
   for (int vec = half ? 8 : 4; vec > 1; vec /= 2) {
-    bool fits = a.d % vec == 0 && a.pairs % vec == 0;
+    bool fits = a.d % vec == 0 && (c.interleaved ? 2 * a.pairs : a.pairs) % vec == 0;
     for (int i = 0; i < 3 && fits; ++i) {
       const rope::Part& t = a.part[i];
       if (t.heads == 0) continue;
@@ -629,17 +676,22 @@ cudaError_t launch(const lapl_rope_plan& p, rope::Args& a, bool backward, int* c
   const lapl_rope_config& c = p.cfg;
   const int vec = vector_of(p, a, backward);
   const int rest = a.d - 2 * a.pairs;
-  const int slots = a.pairs / vec + (rest + 2 * vec - 1) / (2 * vec);
+  const int slots = c.interleaved && vec > 1 ? (a.d + 2 * vec - 1) / (2 * vec)
+                                             : a.pairs / vec + (rest + 2 * vec - 1) / (2 * vec);
   int lanes_log2 = 0;
   while (lanes_log2 < 5 && (1 << lanes_log2) < slots) ++lanes_log2;
   const int ns = (slots + 31) / 32;
   a.lanes_log2 = lanes_log2;
-  // Fewer tokens to a CTA where that many would not give one to every SM.
-  int at_once = rope::kMaxTokens;
+  // More tokens to a CTA where its groups of lanes would be more than their heads; fewer where that many
+  // would not give a CTA to every SM.
+  const int groups = rope::kThreads >> lanes_log2;
+  const int heads = a.part[0].heads + (backward ? 0 : a.part[1].heads + a.part[2].heads);
+  int at_once = std::min(rope::kTokens, groups);   // a group has one token of the CTA's at most
+  while (at_once < std::min(rope::kMaxTokens, groups) && groups / at_once > heads) at_once *= 2;
   while (at_once > 1 && a.rows < (long long)at_once * 2 * p.sms) at_once /= 2;
   a.at_once = at_once;
   const long long tiles = (a.rows + at_once - 1) / at_once;
-  const long long most = backward ? (long long)kBackwardCtas * p.sms : 1LL << 30;
+  const long long most = backward ? (long long)rope::kBackCtas * p.sms : 1LL << 30;
   const int grid = (int)std::min(tiles, most);
   *ctas = grid;
   const int ns_rounded = ns <= 1 ? 1 : ns == 2 ? 2 : 4;
@@ -654,7 +706,8 @@ cudaError_t launch(const lapl_rope_plan& p, rope::Args& a, bool backward, int* c
                       : rope::by_shape<false, false>(vec, ns_rounded, hi, ho);
   // Both weights, the turns, and in the backward both weights' sums.
   const size_t smem =
-      sizeof(float2) * (rope::padded(a.d) + a.pairs * at_once + (backward ? 2 * a.d : 0));
+      sizeof(float2) *
+                      (rope::padded(a.d) + rope::turns_of(a.pairs * at_once) + (backward ? 2 * a.d : 0));
   k<<<grid, rope::kThreads, smem, st>>>(a);
   return cudaGetLastError();
 }
@@ -713,7 +766,7 @@ lapl_status lapl_rope_create(const lapl_rope_config* cfg, lapl_rope_handle* out)
 
 lapl_status lapl_rope_workspace_size(lapl_rope_handle p, size_t* bytes) {
   if (!p || !bytes) return LAPL_ERR_INVALID_ARG;
-  *bytes = align_up((size_t)kBackwardCtas * p->sms * 2 * p->cfg.head_dim * sizeof(float2), kAlign);
+  *bytes = align_up((size_t)rope::kBackCtas * p->sms * 2 * p->cfg.head_dim * sizeof(float2), kAlign);
   return LAPL_OK;
 }
 

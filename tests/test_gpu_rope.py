@@ -147,6 +147,15 @@ def test_tokens(N):
     run(B=3, N=N, heads=(2, 1, 1), d=32, pairs=(8, 8), seed=N)
 
 
+@pytest.mark.parametrize("d,pairs", [(90, (9, 13, 13)), (250, (125,)), (256, (128,)), (256, (40,)),
+                                     (4, (2,)), (1, (0,))])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_many_tokens_of_wide_and_narrow_heads(d, pairs, dtype):
+    """Over 32 tokens for each of the GPU's SMs, with as many lanes to a head as there can be, or one."""
+    for interleaved in (False, True):
+        run(B=3, N=3400, heads=(1, 1, 1), d=d, pairs=pairs, dtype=dtype, interleaved=interleaved)
+
+
 @pytest.mark.parametrize("far", [0, 1 << 24, (1 << 31) - 60, -(1 << 31) + 60])
 @pytest.mark.parametrize("pairs", [(8,), (4, 4)])
 def test_far_positions(far, pairs):
