@@ -62,17 +62,21 @@ int row_segments(int tokens, long long bh, int rows, int cols, int sms) {
 // Shortest sequences for the tensor cores.
 constexpr int kLeastTokens = 64;
 
-// Segments of a sequence in chunks: a CTA of an SM walks its chunks.  Times in us, as measured: a chunk of the
-// outputs 2.05 and 4.5 for a CTA; of the segments' sums 1.25 and 3; the launch between 4, and 0.4 for
-// each segment.  (4 x 8 sequences of 128 chunks: 110 us in 4 segments, 249 in 1, 121 in 9.)
-int chunk_segments(int tokens, long long bh, int sms) {
+// Segments of a sequence in chunks: a CTA of an SM walks its chunks, of 64 columns of the state.  Times in
+// us, as measured, for rows of up to 64 values and for longer ones: a chunk of the outputs and what a CTA
+// has besides, the same of the segments' sums; the launch between 4, and 0.4 for each segment.  (4 x 8
+// sequences of 128 chunks of 64 x 64: 110 us in 4 segments, 249 in 1, 121 in 9.)
+int chunk_segments(int tokens, long long bh, int rows, int cols, int sms) {
+  static const double kTimes[2][4] = {{2.05, 4.5, 1.25, 3.0}, {3.6, 6.0, 1.9, 4.0}};
+  const double* t = kTimes[rows > 64];
   const int chunks = (tokens + decay::kTcChunk - 1) / decay::kTcChunk;
+  bh *= (cols + 63) / 64;
   int best = 1;
   double least = 0;
   for (int g = 1; g <= 64 && g <= chunks; ++g) {
     const int per = (chunks + g - 1) / g, n = (chunks + per - 1) / per;
-    double time = (double)((bh * n + sms - 1) / sms) * (4.5 + 2.05 * per);
-    if (n > 1) time += (double)((bh * (n - 1) + sms - 1) / sms) * (3.0 + 1.25 * per) + 4.0 + 0.4 * n;
+    double time = (double)((bh * n + sms - 1) / sms) * (t[1] + t[0] * per);
+    if (n > 1) time += (double)((bh * (n - 1) + sms - 1) / sms) * (t[3] + t[2] * per) + 4.0 + 0.4 * n;
     if (g == 1 || time < least) least = time, best = n;
   }
   return best;
@@ -84,8 +88,8 @@ int per_segment(int tokens, int segments, int step) {
 }
 
 bool tc_sizes(const lapl_decay_config& c) {
-  return c.in_dtype == LAPL_BF16 && c.tokens >= kLeastTokens && c.key_dim <= 64 && c.value_dim <= 64 &&
-         c.key_dim % 8 == 0 && c.value_dim % 8 == 0;
+  return c.in_dtype == LAPL_BF16 && c.tokens >= kLeastTokens && c.key_dim % 8 == 0 &&
+         c.value_dim % 8 == 0;
 }
 
 size_t states_bytes(const lapl_decay_plan& p, int segments) {
@@ -151,9 +155,11 @@ lapl_status lapl_decay_create(const lapl_decay_config* cfg, lapl_decay_handle* o
   p->info.tensor_cores = tc_sizes(*cfg);
   p->info.backward_tensor_cores = tc_sizes(*cfg) && cfg->grad_dtype == LAPL_BF16;
   p->info.segments =
-      p->info.tensor_cores ? chunk_segments(cfg->tokens, p->bh, sms) : p->row_segments;
+      p->info.tensor_cores
+          ? chunk_segments(cfg->tokens, p->bh, cfg->key_dim, cfg->value_dim, sms)
+          : p->row_segments;
   p->info.backward_segments = p->info.backward_tensor_cores
-                                  ? chunk_segments(cfg->tokens, 3LL * p->bh, sms)
+                                  ? chunk_segments(cfg->tokens, 3LL * p->bh, most, most, sms)
                                   : p->backward_row_segments;
   *out = p;
   return LAPL_OK;

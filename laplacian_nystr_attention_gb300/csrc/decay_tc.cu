@@ -1,5 +1,5 @@
 // decay_tc.cu -- a pass of the linear attention with decays in chunks of 128 tokens on the tensor
-// cores (decay.cuh has the formulas): bf16 rows of up to 64 values.
+// cores (decay.cuh has the formulas): bf16 rows, 64 columns of the state to a CTA.
 //
 // With g the head's decay, a chunk of n tokens (m = 0 .. n-1 in processing order) and the state S before
 // it, the chunk's outputs and the state after it are
@@ -38,13 +38,15 @@ using namespace tc;
 using ops::Vec;
 
 constexpr int kChunk = kTcChunk;
-constexpr int kD = 64;                        // padded row length
-constexpr unsigned kTile = kChunk * kD * 2;   // bytes of a tile of X, Y, Z or a part of Z'
-constexpr unsigned kState = kD * kD * 2;      // bytes of a part of S
+constexpr int kD = 64;                        // columns of a tile of X, Y or Z
+constexpr unsigned kTile = kChunk * kD * 2;   // bytes of one, or of a part of Z'
 constexpr int kParts = 3;                     // of Z'
 constexpr int kPieces = kChunk * kD / 8;      // of a tile, of 16 bytes
-constexpr int kStages = 2;                    // of X, Y and Z, and of Z'
 constexpr int kAhead = 2;                     // chunks from a copy to the prefetch into L2 beside it
+// kBoxes: tiles that rows of X and Y take, padded: 1 (up to 64 values) or 2 (up to 128).  Z is one, the
+// pass's columns in steps of 64.
+// Stages of X, Y and Z, and of Z': of the longer rows shared memory holds one.
+constexpr int stages_of(int boxes) { return boxes == 1 ? 2 : 1; }
 
 // Columns of tensor memory.
 constexpr unsigned kScores = 0, kInner = 256, kOuter = 320, kAdd = 384, kColumns = 512;
@@ -91,7 +93,7 @@ struct Ring {
 // The tokens of Z, times late[row] and by, as kParts tiles; rows from n on as zeros, in Z and Y too, whose
 // products with zeros would not be zeros for what is not finite there.  Pieces kFirst to kLast of 8 values,
 // 8 to a row.
-template <int kThreads, int kFirst, int kLast>
+template <int kBoxes, int kThreads, int kFirst, int kLast>
 __device__ __forceinline__ void weigh(unsigned char* y, unsigned char* z, unsigned char* to, int thread,
                                       int n, const float* late, float by) {
 #pragma unroll 2
@@ -111,15 +113,16 @@ __device__ __forceinline__ void weigh(unsigned char* y, unsigned char* z, unsign
       }
     } else {
       *reinterpret_cast<uint4*>(z + at) = make_uint4(0, 0, 0, 0);
-      *reinterpret_cast<uint4*>(y + at) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int k = 0; k < kBoxes; ++k) *reinterpret_cast<uint4*>(y + k * kTile + at) = make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int k = 0; k < kParts; ++k) *reinterpret_cast<uint4*>(to + k * kTile + at) = part[k];
   }
 }
 
-// add: D = Y^T Z' over a chunk, the first part in columns 0-63, the others' sum in 64-127; rows 64 and up
-// are rows 0 and up again (lbo = 0).
+// add: D = Y^T Z' over a chunk, the first part in columns 0-63, the others' sum in 64-127.  With one box of Y
+// rows 64 and up are rows 0 and up again (y's lbo = 0).
 __device__ __forceinline__ void issue_add(unsigned d, uint64_t y, uint64_t parts) {
 #pragma unroll
   for (int s = 0; s < kChunk / 16; ++s)
@@ -130,23 +133,32 @@ __device__ __forceinline__ void issue_add(unsigned d, uint64_t y, uint64_t parts
         true);
 }
 constexpr unsigned kAddColumns = 2 * kD;
-// Both sums, 32 columns of each.
-__device__ __forceinline__ void load_add(unsigned addr, Vec<2> (&sum)[16]) {
-  unsigned d[2][32];
-  tmem_load32(addr, d[0]);
-  tmem_load32(addr + kD, d[1]);
-  tmem_loaded();
-#pragma unroll
-  for (int c = 0; c < 16; ++c)
-    sum[c] = ops::add({{__uint_as_float(d[0][2 * c]), __uint_as_float(d[0][2 * c + 1])}},
-                      {{__uint_as_float(d[1][2 * c]), __uint_as_float(d[1][2 * c + 1])}});
-}
-
-// A state's values of tensor-memory lane `lane`: row lane % 64, columns from 32 (lane / 64) on.
-struct Place64 {
+// A thread's part of the state: the row of its tensor-memory lane, all 64 columns of it, or with 64 rows, which
+// the lanes hold twice, half of them.
+template <int kBoxes>
+struct Place {
+  static constexpr int kCols = 32 * kBoxes;
   int row, col;
-  __device__ __forceinline__ explicit Place64(int lane) : row(lane & 63), col((lane >> 6) * 32) {}
+  __device__ __forceinline__ explicit Place(int lane)
+      : row(kBoxes == 2 ? lane : lane & 63), col(kBoxes == 2 ? 0 : (lane >> 6) * 32) {}
 };
+// Calls use(16 columns at a time: which, both sums' sums in pairs) for kCols columns.
+template <int kCols, class Use>
+__device__ __forceinline__ void each_add(unsigned addr, Use use) {
+#pragma unroll
+  for (int q = 0; q < kCols / 16; ++q) {
+    unsigned d[2][16];
+    tmem_load16(addr + 16 * q, d[0]);
+    tmem_load16(addr + kD + 16 * q, d[1]);
+    tmem_loaded();
+    Vec<2> sum[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      sum[c] = ops::add({{__uint_as_float(d[0][2 * c]), __uint_as_float(d[0][2 * c + 1])}},
+                        {{__uint_as_float(d[1][2 * c]), __uint_as_float(d[1][2 * c + 1])}});
+    use(q, sum);
+  }
+}
 
 // ---- outputs ----------------------------------------------------------------------------
 
@@ -175,11 +187,15 @@ struct Decays {
   }
 };
 
+template <int kBoxes>
 struct OutLayout {
+  static constexpr int kStages = stages_of(kBoxes);
+  static constexpr unsigned kStage = (2 * kBoxes + 1) * kTile;   // X, Y and Z
+  static constexpr unsigned kState = kBoxes * kD * kD * 2;       // a part of S
   unsigned stage, parts, state, staging, decays, bars, total;
   __host__ __device__ OutLayout() {
     stage = 0;
-    parts = kStages * 3 * kTile;
+    parts = kStages * kStage;
     state = parts + kStages * kParts * kTile;
     staging = state + 2 * kState;
     decays = staging + 8 * 2048;
@@ -188,18 +204,23 @@ struct OutLayout {
   }
 };
 enum Bar {
-  kFull = 0, kScoresFull = kFull + kStages, kPReady = kScoresFull + 2,
+  kFull = 0, kScoresFull = kFull + 2, kPReady = kScoresFull + 2,
   kZReady = kPReady + 2, kOFull = kZReady + 2, kOFree, kAddFull, kAddFree,
   kSReady, kSFree, kDone, kBars
 };
 static_assert(kBars < 32, "room of the barriers");
 
+template <int kBoxes>
 __global__ void __launch_bounds__(kOutThreads, 1)
 decay_chunks_kernel(const __grid_constant__ TcArgs t) {
+  using Layout = OutLayout<kBoxes>;
+  constexpr int kStages = Layout::kStages;
+  constexpr unsigned kStage = Layout::kStage, kState = Layout::kState;
   extern __shared__ unsigned char smem_raw[];
   const Args& a = t.a;
-  const int which = blockIdx.z;
+  const int which = blockIdx.z, col0 = blockIdx.y * kD;
   const Pass& p = a.pass[which];
+  if (col0 >= p.b) return;   // (a pass with fewer columns than the launch's widest)
   const int bh = blockIdx.x / a.segments, segment = blockIdx.x % a.segments;
   const int lane = threadIdx.x & 31;
   // The products are issued beside the warps of the rows with the fewest scores: a scheduler's other warps
@@ -209,7 +230,7 @@ decay_chunks_kernel(const __grid_constant__ TcArgs t) {
   const Chunks chunks(a, p, bh, segment);
   const int n = chunks.count;
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  const OutLayout at;
+  const Layout at;
   Decays& decays = *reinterpret_cast<Decays*>(smem + at.decays);
   const unsigned bars = smem_u32(smem + at.bars);
   auto bar = [&](int b) { return bars + 8u * (unsigned)b; };
@@ -248,39 +269,49 @@ decay_chunks_kernel(const __grid_constant__ TcArgs t) {
   bool ok = true;
   const unsigned long long wait_ns = t.wait_ns;
 
+  // A chunk's stage, and the parity of its phase.
+  auto stage_of = [](int i) { return kStages == 2 ? i & 1 : 0; };
+  auto phase_of = [](int i) { return kStages == 2 ? (i >> 1) & 1 : i & 1; };
   // The copies of chunk i, by one lane of a warp; the chunks after the next are on their way into L2.
   auto copy = [&](int i, bool leader) {
     if (i >= n || (t.skip_last && i == n - 1)) return;   // (fault injection: never copied)
     if (leader) {
-      const unsigned dst = smem_u32(smem + at.stage + (i & 1) * 3 * kTile), full = bar(kFull + (i & 1));
+      const unsigned dst = smem_u32(smem + at.stage + stage_of(i) * kStage), full = bar(kFull + stage_of(i));
       const int token = chunks.place(i) * kChunk;
-      mbar_expect_tx(full, 3 * kTile);
-      tma_load_3d(dst, &t.x[which], 0, token, bh, full);
-      tma_load_3d(dst + kTile, &t.y[which], 0, token, bh, full);
-      tma_load_3d(dst + 2 * kTile, &t.z[which], 0, token, bh, full);
+      mbar_expect_tx(full, kStage);
+#pragma unroll
+      for (int k = 0; k < kBoxes; ++k) {
+        tma_load_3d(dst + k * kTile, &t.x[which], k * kD, token, bh, full);
+        tma_load_3d(dst + (kBoxes + k) * kTile, &t.y[which], k * kD, token, bh, full);
+      }
+      tma_load_3d(dst + 2 * kBoxes * kTile, &t.z[which], col0, token, bh, full);
       if (i + kAhead < n) {
         const int later = chunks.place(i + kAhead) * kChunk;
-        tma_prefetch_3d(&t.x[which], 0, later, bh);
-        tma_prefetch_3d(&t.y[which], 0, later, bh);
-        tma_prefetch_3d(&t.z[which], 0, later, bh);
+#pragma unroll
+        for (int k = 0; k < kBoxes; ++k) {
+          tma_prefetch_3d(&t.x[which], k * kD, later, bh);
+          tma_prefetch_3d(&t.y[which], k * kD, later, bh);
+        }
+        tma_prefetch_3d(&t.z[which], col0, later, bh);
       }
     }
   };
   // Z' of chunk i, by the warps from kStateWarp on.
   auto weigh_chunk = [&](int i) {
-    const int b = i & 1;
-    if (!warp_wait(bar(kFull + b), (i >> 1) & 1, wait_ns)) return false;
-    // (All that read the chunk before the last's Z' is done: what was copied for this one waited for it.)
+    const int b = stage_of(i);
+    if (!warp_wait(bar(kFull + b), phase_of(i), wait_ns)) return false;
+    // (All that read the Z' before in this place is done: what was copied for this one waited for it.)
     const int tokens = chunks.tokens(i);
-    unsigned char* stage = smem + at.stage + b * 3 * kTile;
+    unsigned char* y = smem + at.stage + b * kStage + kBoxes * kTile;
+    unsigned char* z = y + kBoxes * kTile;
     unsigned char* to = smem + at.parts + b * kParts * kTile;
     const float* late = decays.late_of(tokens, p.reverse);
     if (warp < kWeighWarp)
-      weigh<32 * (kWeighWarp - kStateWarp), kWeighPieces, kPieces>(
-          stage + kTile, stage + 2 * kTile, to, threadIdx.x - 32 * kStateWarp, tokens, late, 1.f);
+      weigh<kBoxes, 32 * (kWeighWarp - kStateWarp), kWeighPieces, kPieces>(
+          y, z, to, threadIdx.x - 32 * kStateWarp, tokens, late, 1.f);
     else
-      weigh<32 * (kIssueWarp - kWeighWarp), 0, kWeighPieces>(
-          stage + kTile, stage + 2 * kTile, to, 32 * (warp - kWeighWarp) + lane, tokens, late, 1.f);
+      weigh<kBoxes, 32 * (kIssueWarp - kWeighWarp), 0, kWeighPieces>(
+          y, z, to, 32 * (warp - kWeighWarp) + lane, tokens, late, 1.f);
     fence_async();
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(kZReady + b));
@@ -368,7 +399,7 @@ decay_chunks_kernel(const __grid_constant__ TcArgs t) {
     auto flush = [&](int i, int col) {
       const long long first = (long long)bh * a.tokens;
       const int size = half ? 2 : 4, token0 = chunks.place(i) * kChunk + 32 * quad;
-      col += piece * (16 / size);
+      col += col0 + piece * (16 / size);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int r = row0 + 8 * k, token = token0 + r;
@@ -425,14 +456,17 @@ decay_chunks_kernel(const __grid_constant__ TcArgs t) {
     // Every copy lands before the CTA may finish: those of the chunks not done, made so far.
     if (!ok && warp == 0)
       for (int i = done; i < min(n, done + kStages); ++i)
-        mbar_wait(bar(kFull + (i & 1)), (i >> 1) & 1, wait_ns);
+        mbar_wait(bar(kFull + stage_of(i)), phase_of(i), wait_ns);
     if (half && ok && n > 0) flush(n - 1, 32 * odd);
   } else if (warp < 12) {
     // ---------------- the state ----------------
     const int tl = threadIdx.x - 256;
-    const Place64 place(tl);
+    using Mine = Place<kBoxes>;
+    constexpr int kCols = Mine::kCols;
+    const Mine place(tl);
+    const int col = col0 + place.col;   // of the pass
     const unsigned lanes = (unsigned)(32 * (warp & 3)) << 16;
-    Vec<2> S[16];
+    Vec<2> S[kCols / 2];
     const float* from = nullptr;
     long long row_step = p.b, col_step = 1;
     if (p.states) {
@@ -442,15 +476,15 @@ decay_chunks_kernel(const __grid_constant__ TcArgs t) {
       if (p.first_across) row_step = 1, col_step = p.a;
     }
 #pragma unroll
-    for (int c = 0; c < 32; ++c) {
+    for (int c = 0; c < kCols; ++c) {
       S[c / 2].f[c & 1] = 0.f;
-      if (from && place.row < p.a && place.col + c < p.b)
-        S[c / 2].f[c & 1] = from[place.row * row_step + (place.col + c) * col_step];
+      if (from && place.row < p.a && col + c < p.b)
+        S[c / 2].f[c & 1] = from[place.row * row_step + (col + c) * col_step];
     }
     unsigned char* operand_at = smem + at.state + place.row * 128;
     auto publish = [&] {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < kCols / 8; ++c) {
         uint4 hi, lo;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -475,13 +509,13 @@ decay_chunks_kernel(const __grid_constant__ TcArgs t) {
       if (!ok) break;
       fence_after();
       const Fade fade(l, chunks.tokens(i) - (p.undecayed && chunks.first + i == 0));
-      Vec<2> add[16];
-      load_add(tmem + kAdd + place.col + lanes, add);
+      each_add<kCols>(tmem + kAdd + place.col + lanes, [&](int q, const Vec<2> (&add)[8]) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) S[8 * q + c] = ops::add(fade(S[8 * q + c]), add[c]);
+      });
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kAddFree));
-#pragma unroll
-      for (int c = 0; c < 16; ++c) S[c] = ops::add(fade(S[c]), add[c]);
       if (i + 1 < n) {
         ok = warp_wait(bar(kSFree), i & 1, wait_ns);
         if (!ok) break;
@@ -491,10 +525,10 @@ decay_chunks_kernel(const __grid_constant__ TcArgs t) {
     }
     if (ok && p.last && segment == a.segments - 1) {
       const float g = p.undecayed && chunks.len > 0 ? exp2f(l2) : 1.f;
-      float* to = p.last + (long long)bh * p.a * p.b + (long long)place.row * p.b + place.col;
+      float* to = p.last + (long long)bh * p.a * p.b + (long long)place.row * p.b + col;
 #pragma unroll
-      for (int c = 0; c < 32; ++c)
-        if (place.row < p.a && place.col + c < p.b) to[c] = S[c / 2].f[c & 1] * g;
+      for (int c = 0; c < kCols; ++c)
+        if (place.row < p.a && col + c < p.b) to[c] = S[c / 2].f[c & 1] * g;
     }
   } else if (warp < kIssueWarp) {
     // ---------------- Z' ----------------
@@ -503,14 +537,16 @@ decay_chunks_kernel(const __grid_constant__ TcArgs t) {
     // ---------------- products ----------------
     const bool leader = elect();
     const unsigned stage0 = smem_u32(smem + at.stage);
+    // k-th 16 values of rows of X or Y.
+    auto step = [](int k) { return (uint64_t)((k / 4) * (kTile / 16) + 2 * (k % 4)); };
     auto scores = [&](int i) {
-      if (!warp_wait(bar(kFull + (i & 1)), (i >> 1) & 1, wait_ns)) return false;
+      if (!warp_wait(bar(kFull + stage_of(i)), phase_of(i), wait_ns)) return false;
       fence_after();
       if (leader) {
-        const uint64_t x = operand(stage0 + (i & 1) * 3 * kTile, 0);
+        const uint64_t x = operand(stage0 + stage_of(i) * kStage, 0);
 #pragma unroll
-        for (int s = 0; s < kD / 16; ++s)
-          mma(tmem + kScores + 128u * (i & 1), x + 2 * s, x + kTile / 16 + 2 * s,
+        for (int s = 0; s < kBoxes * kD / 16; ++s)
+          mma(tmem + kScores + 128u * (i & 1), x + step(s), x + kBoxes * (kTile / 16) + step(s),
               instruction(kChunk, false, false), s > 0);
         commit(bar(kScoresFull + (i & 1)));
       }
@@ -519,14 +555,16 @@ decay_chunks_kernel(const __grid_constant__ TcArgs t) {
     const uint64_t state = operand(smem_u32(smem + at.state), 0);
     if (n > 0) ok = scores(0);
     for (int i = 0; i < n && ok; ++i) {
-      const uint64_t x = operand(stage0 + (i & 1) * 3 * kTile, 0);
-      const uint64_t y = x + kTile / 16, z = y + kTile / 16;
-      ok = warp_wait(bar(kZReady + (i & 1)), (i >> 1) & 1, wait_ns) &&
+      const unsigned at_x = stage0 + stage_of(i) * kStage;
+      const uint64_t x = operand(at_x, 0), z = x + 2 * kBoxes * (kTile / 16);
+      const uint64_t y = operand(at_x + kBoxes * kTile, kBoxes == 2 ? kTile : 0);
+      ok = warp_wait(bar(kZReady + stage_of(i)), phase_of(i), wait_ns) &&
            (i == 0 || warp_wait(bar(kAddFree), (i - 1) & 1, wait_ns));
       if (!ok) break;
       fence_after();
       if (leader) {
-        issue_add(tmem + kAdd, y, operand(smem_u32(smem + at.parts + (i & 1) * kParts * kTile), kTile));
+        issue_add(tmem + kAdd, y,
+                  operand(smem_u32(smem + at.parts + stage_of(i) * kParts * kTile), kTile));
         commit(bar(kAddFull));
       }
       ok = warp_wait(bar(kSReady), i & 1, wait_ns) &&
@@ -537,8 +575,8 @@ decay_chunks_kernel(const __grid_constant__ TcArgs t) {
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-          for (int s = 0; s < kD / 16; ++s)
-            mma(tmem + kOuter, x + 2 * s, state + (k * kState + s * 2048) / 16,
+          for (int s = 0; s < kBoxes * kD / 16; ++s)
+            mma(tmem + kOuter, x + step(s), state + (k * kState + s * 2048) / 16,
                 instruction(kD, false, true), k > 0 || s > 0);
         commit(bar(kSFree));
       }
@@ -575,7 +613,7 @@ decay_chunks_kernel(const __grid_constant__ TcArgs t) {
                  : "memory");
   }
   // Zeros for the chunks that are all padding.
-  {
+  if (col0 == 0) {
     const long long row0 = (long long)bh * a.tokens;
     const int begin = max(segment * a.per_segment, chunks.all * kChunk);
     const int end = min((segment + 1) * a.per_segment, a.tokens);
@@ -590,38 +628,45 @@ decay_chunks_kernel(const __grid_constant__ TcArgs t) {
 // ---- segments' own states ------------------------------------------------------------------
 
 constexpr int kSumWarps = 14, kSumThreads = 32 * kSumWarps;
-constexpr int kSumStages = 4;
 
+template <int kBoxes>
 struct SumLayout {
+  static constexpr int kStages = kBoxes == 1 ? 4 : 2;
+  static constexpr unsigned kStage = (kBoxes + 1) * kTile;   // Y and Z
   unsigned stage, parts, late, bars, total;
   __host__ __device__ SumLayout() {
     stage = 0;
-    parts = kSumStages * 2 * kTile;
+    parts = kStages * kStage;
     late = parts + 2 * kParts * kTile;
     bars = late + kChunk * 4;
     total = bars + 8 * 32;
   }
 };
 enum SumBar {
-  kSumFull = 0, kSumEmpty = kSumFull + kSumStages, kSumReady = kSumEmpty + kSumStages,
+  kSumFull = 0, kSumEmpty = kSumFull + 4, kSumReady = kSumEmpty + 4,
   kSumDone = kSumReady + 2, kSumFree = kSumDone + 2, kSumEnd = kSumFree + 2, kSumBars
 };
 static_assert(kSumBars < 32, "room of the barriers");
 
 // Sum over a segment's tokens of y z^T with their decays to the segment's end.  Warps 0-7: Z'; 8-11: sums
 // in registers (in tensor memory, whose adding cuts off, a chunk's products only); 12 copies, 13 issues.
+template <int kBoxes>
 __global__ void __launch_bounds__(kSumThreads, 1)
 decay_sums_kernel(const __grid_constant__ TcArgs t) {
+  using Layout = SumLayout<kBoxes>;
+  constexpr int kSumStages = Layout::kStages;
+  constexpr unsigned kStage = Layout::kStage;
   extern __shared__ unsigned char smem_raw[];
   const Args& a = t.a;
-  const int which = blockIdx.z;
+  const int which = blockIdx.z, col0 = blockIdx.y * kD;
   const Pass& p = a.pass[which];
+  if (col0 >= p.b) return;   // (a pass with fewer columns than the launch's widest)
   const int bh = blockIdx.x / (a.segments - 1), segment = blockIdx.x % (a.segments - 1);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const Chunks chunks(a, p, bh, segment);
   const int n = chunks.count;
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  const SumLayout at;
+  const Layout at;
   const unsigned bars = smem_u32(smem + at.bars);
   auto bar = [&](int b) { return bars + 8u * (unsigned)b; };
   unsigned* slot = reinterpret_cast<unsigned*>(smem + at.bars + 8 * kSumBars);
@@ -671,35 +716,40 @@ decay_sums_kernel(const __grid_constant__ TcArgs t) {
       ok = warp_wait(bar(kSumFull + ring.stage), ring.phase, wait_ns);
       if (ok && i > 1) ok = warp_wait(bar(kSumDone + (i & 1)), ((i >> 1) - 1) & 1, wait_ns);
       if (!ok) break;
-      unsigned char* stage = smem + at.stage + ring.stage * 2 * kTile;
-      weigh<256, 0, kPieces>(stage, stage + kTile, smem + at.parts + (i & 1) * kParts * kTile, threadIdx.x, tokens,
+      unsigned char* y = smem + at.stage + ring.stage * kStage;
+      weigh<kBoxes, 256, 0, kPieces>(
+          y, y + kBoxes * kTile, smem + at.parts + (i & 1) * kParts * kTile, threadIdx.x, tokens,
                  p.reverse ? late : late + kChunk - tokens, power(l2, after));
       fence_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kSumReady + (i & 1)));
     }
   } else if (warp < 12) {
-    const Place64 place(threadIdx.x - 256);
+    using Mine = Place<kBoxes>;
+    constexpr int kCols = Mine::kCols;
+    const Mine place(threadIdx.x - 256);
+    const int col = col0 + place.col;   // of the pass
     const unsigned lanes = (unsigned)(32 * (warp & 3)) << 16;
-    Vec<2> S[16];
+    Vec<2> S[kCols / 2];
 #pragma unroll
-    for (int c = 0; c < 16; ++c) S[c] = ops::fill<2>(0.f);
+    for (int c = 0; c < kCols / 2; ++c) S[c] = ops::fill<2>(0.f);
     for (int i = 0; i < n; ++i) {
       ok = warp_wait(bar(kSumDone + (i & 1)), (i >> 1) & 1, wait_ns);
       if (!ok) break;
       fence_after();
-      Vec<2> add[16];
-      load_add(tmem + kAddColumns * (i & 1) + place.col + lanes, add);
+      each_add<kCols>(tmem + kAddColumns * (i & 1) + place.col + lanes,
+                      [&](int q, const Vec<2> (&add)[8]) {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) S[8 * q + c] = ops::add(S[8 * q + c], add[c]);
+                      });
       fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(kSumFree + (i & 1)));
-#pragma unroll
-      for (int c = 0; c < 16; ++c) S[c] = ops::add(S[c], add[c]);
     }
-    float* to = p.states + (((long long)bh * a.segments + segment) * p.a + place.row) * p.b + place.col;
+    float* to = p.states + (((long long)bh * a.segments + segment) * p.a + place.row) * p.b + col;
 #pragma unroll
-    for (int c = 0; c < 32; ++c)
-      if (place.row < p.a && place.col + c < p.b) to[c] = S[c / 2].f[c & 1];
+    for (int c = 0; c < kCols; ++c)
+      if (place.row < p.a && col + c < p.b) to[c] = S[c / 2].f[c & 1];
   } else if (warp == 12) {
     const bool leader = elect();
     int issued = 0;
@@ -707,12 +757,14 @@ decay_sums_kernel(const __grid_constant__ TcArgs t) {
       const int s = i % kSumStages;
       if (i >= kSumStages) ok = warp_wait(bar(kSumEmpty + s), ((i / kSumStages) - 1) & 1, wait_ns);
       if (!ok) break;
-      const unsigned dst = smem_u32(smem + at.stage + s * 2 * kTile);
+      const unsigned dst = smem_u32(smem + at.stage + s * kStage);
       const int token = chunks.place(i) * kChunk;
       if (leader) {
-        mbar_expect_tx(bar(kSumFull + s), 2 * kTile);
-        tma_load_3d(dst, &t.y[which], 0, token, bh, bar(kSumFull + s));
-        tma_load_3d(dst + kTile, &t.z[which], 0, token, bh, bar(kSumFull + s));
+        mbar_expect_tx(bar(kSumFull + s), kStage);
+#pragma unroll
+        for (int k = 0; k < kBoxes; ++k)
+          tma_load_3d(dst + k * kTile, &t.y[which], k * kD, token, bh, bar(kSumFull + s));
+        tma_load_3d(dst + kBoxes * kTile, &t.z[which], col0, token, bh, bar(kSumFull + s));
       }
       issued = i + 1;
     }
@@ -727,7 +779,7 @@ decay_sums_kernel(const __grid_constant__ TcArgs t) {
       fence_after();
       if (leader) {
         issue_add(tmem + kAddColumns * (i & 1),
-                  operand(smem_u32(smem + at.stage + (i % kSumStages) * 2 * kTile), 0),
+                  operand(smem_u32(smem + at.stage + (i % kSumStages) * kStage), kBoxes == 2 ? kTile : 0),
                   operand(smem_u32(smem + at.parts + (i & 1) * kParts * kTile), kTile));
         commit(bar(kSumDone + (i & 1)));
         commit(bar(kSumEmpty + i % kSumStages));
@@ -751,6 +803,7 @@ decay_sums_kernel(const __grid_constant__ TcArgs t) {
 }
 
 constexpr unsigned kSmemMost = 227 * 1024;
+static_assert(sizeof(Decays) == 896, "room of the decays");
 
 bool encode(CUtensorMap* map, const void* base, int width, int tokens, int bh) {
   return tma_encode_3d_sw128(map, base, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (uint64_t)width,
@@ -763,12 +816,42 @@ bool encode(CUtensorMap* map, const void* base, int width, int tokens, int bh) {
 bool tc_fits(const Args& a, int passes) {
   for (int i = 0; i < passes; ++i) {
     const Pass& p = a.pass[i];
-    if (!p.x_half || !p.y_half || !p.z_half || p.a > kD || p.b > kD || p.a % 8 || p.b % 8) return false;
+    if (!p.x_half || !p.y_half || !p.z_half || p.a > 2 * kD || p.b > 2 * kD || p.a % 8 || p.b % 8) return false;
     for (const void* q : {p.x, p.y, p.z, static_cast<const void*>(p.out)})
       if (!ops::aligned(q, 16)) return false;
   }
   return true;
 }
+
+namespace {
+
+template <int kBoxes>
+cudaError_t launch_boxes(const TcArgs& t, int passes, int bh, int tiles, cudaStream_t st) {
+  const Args& a = t.a;
+  const unsigned sums = SumLayout<kBoxes>().total + 1024, outs = OutLayout<kBoxes>().total + 1024;
+  static_assert(OutLayout<kBoxes>::kStages * (OutLayout<kBoxes>::kStage + kParts * kTile) +
+                        2 * OutLayout<kBoxes>::kState + 8 * 2048 + 896 + 256 + 1024 <= kSmemMost,
+                "shared memory of the outputs' kernel");
+  cudaError_t e = cudaSuccess;
+  if (a.segments > 1) {
+    e = cudaFuncSetAttribute(decay_sums_kernel<kBoxes>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kSmemMost);
+    if (e != cudaSuccess) return e;
+    decay_sums_kernel<kBoxes><<<dim3((unsigned)(bh * (a.segments - 1)), (unsigned)tiles, (unsigned)passes),
+                                kSumThreads, sums, st>>>(t);
+    e = cudaGetLastError();
+  }
+  if (e == cudaSuccess && a.pass[0].states) e = launch_carry(a, passes, bh, st);
+  if (e != cudaSuccess) return e;
+  e = cudaFuncSetAttribute(decay_chunks_kernel<kBoxes>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           kSmemMost);
+  if (e != cudaSuccess) return e;
+  decay_chunks_kernel<kBoxes><<<dim3((unsigned)(bh * a.segments), (unsigned)tiles, (unsigned)passes),
+                                kOutThreads, outs, st>>>(t);
+  return cudaGetLastError();
+}
+
+}  // namespace
 
 cudaError_t launch_tc(const Args& a, int passes, int bh, unsigned* err, unsigned long long wait_ns,
                       int skip_last, cudaStream_t st) {
@@ -777,28 +860,18 @@ cudaError_t launch_tc(const Args& a, int passes, int bh, unsigned* err, unsigned
   t.err = err;
   t.wait_ns = wait_ns;
   t.skip_last = skip_last;
+  int rows = 0, cols = 0;
   for (int i = 0; i < passes; ++i) {
     const Pass& p = a.pass[i];
+    rows = std::max(rows, p.a);
+    cols = std::max(cols, p.b);
     if (!encode(&t.x[i], p.x, p.a, a.tokens, bh) || !encode(&t.y[i], p.y, p.a, a.tokens, bh) ||
         !encode(&t.z[i], p.z, p.b, a.tokens, bh))
       return cudaErrorInvalidValue;
   }
-  cudaError_t e = cudaSuccess;
-  if (a.segments > 1) {
-    const unsigned smem = SumLayout().total + 1024;
-    e = cudaFuncSetAttribute(decay_sums_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
-    if (e != cudaSuccess) return e;
-    decay_sums_kernel<<<dim3((unsigned)(bh * (a.segments - 1)), 1, (unsigned)passes), kSumThreads, smem,
-                        st>>>(t);
-    e = cudaGetLastError();
-  }
-  if (e == cudaSuccess && a.pass[0].states) e = launch_carry(a, passes, bh, st);
-  if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(decay_chunks_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost);
-  if (e != cudaSuccess) return e;
-  decay_chunks_kernel<<<dim3((unsigned)(bh * a.segments), 1, (unsigned)passes), kOutThreads,
-                        OutLayout().total + 1024, st>>>(t);
-  return cudaGetLastError();
+  const int tiles = (cols + kD - 1) / kD;
+  return rows <= kD ? launch_boxes<1>(t, passes, bh, tiles, st)
+                    : launch_boxes<2>(t, passes, bh, tiles, st);
 }
 
 }  // namespace decay

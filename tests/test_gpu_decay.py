@@ -107,7 +107,8 @@ def test_dimensions(a, b, dtype):
 
 
 @pytest.mark.parametrize("reverse", [False, True])
-@pytest.mark.parametrize("dtype,a,b", [("bf16", 64, 64), ("bf16", 32, 24), ("f32", 32, 40)])
+@pytest.mark.parametrize("dtype,a,b", [("bf16", 64, 64), ("bf16", 32, 24), ("f32", 32, 40),
+                                       ("bf16", 128, 128), ("bf16", 56, 88)])
 def test_padding(dtype, a, b, reverse):
     """Lengths of 0, 1, whole chunks, past the end and below 0; what lies in the padding is not
     read, whatever it is, and outputs are zero there."""
@@ -142,7 +143,8 @@ def test_decays(dtype, logs):
 
 
 @pytest.mark.parametrize("dtype,a,b", [("bf16", 64, 64), ("bf16", 64, 48), ("f32", 32, 32),
-                                       ("bf16", 128, 64)])
+                                       ("bf16", 128, 64), ("bf16", 64, 128), ("bf16", 128, 128),
+                                       ("f32", 96, 128)])
 @pytest.mark.parametrize("B,N", [(1, 3000), (5, 1111)])
 def test_segments(dtype, a, b, B, N):
     """Long sequences in several segments, both ways, with lengths that end in each of them."""
@@ -163,7 +165,8 @@ def test_pointers_off_sixteen_bytes(dtype, N):
 
 
 @pytest.mark.parametrize("dtype,a,N", [("f32", 64, 33), ("bf16", 64, 33), ("bf16", 64, 200),
-                                       ("bf16", 64, 3000), ("f32", 16, 3000)])
+                                       ("bf16", 64, 3000), ("f32", 16, 3000),
+                                       ("bf16", 128, 1000)])
 def test_states_in_place(dtype, a, N):
     """The final state over the first one, and the first's gradient over the final's."""
     import laplacian_nystr_attention_gb300 as lna
