@@ -227,28 +227,21 @@ __device__ __forceinline__ void update(const Table<N>& t, int k, long long at, l
   }
   float r[kPer];
   // The states' products and sums are rounded one by one, as the formulas read, and not contracted: a code
-  // next to a border must not depend on how a compiler joins them.
-  auto each = [](float v) { return ops::fill<2>(v); };
+  // next to a border must not depend on how a compiler joins them.  (Packed instructions of two values do
+  // get joined.)
 #pragma unroll
-  for (int i = 0; i < kPer; i += 2) {
-    ops::Vec<2> m = {{x.m[i], x.m[i + 1]}}, v = {{x.v[i], x.v[i + 1]}};
+  for (int i = 0; i < kPer; ++i) {
     if constexpr (k8) {
-      m = ops::mul(m, each(m_scale));
-      v = ops::mul(v, each(v_scale));
-      v = ops::mul(v, v);
+      x.m[i] = __fmul_rn(x.m[i], m_scale);
+      x.v[i] = __fmul_rn(x.v[i], v_scale);
+      x.v[i] = __fmul_rn(x.v[i], x.v[i]);
     }
-    const ops::Vec<2> g = ops::mul({{x.g[i], x.g[i + 1]}}, each(clip));
-    m = ops::add(ops::mul(each(s.beta1), m), ops::mul(each(s.one_beta1), g));
-    v = ops::add(ops::mul(each(s.beta2), v), ops::mul(ops::mul(each(s.one_beta2), g), g));
-    const ops::Vec<2> am = ops::mul(m, each(a)), kept = ops::mul({{x.w[i], x.w[i + 1]}}, each(keep));
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      x.m[i + e] = m.f[e];
-      x.v[i + e] = v.f[e];
-      r[i + e] = fast_sqrt(v.f[e]);
-      // lr m / late1 / (sqrt(v / late2) + eps), with a = lr / late1 and root = 1 / sqrt(late2).
-      x.w[i + e] = kept.f[e] - __fdividef(am.f[e], fmaf(r[i + e], root, s.eps));
-    }
+    const float g = __fmul_rn(x.g[i], clip);
+    x.m[i] = __fadd_rn(__fmul_rn(s.beta1, x.m[i]), __fmul_rn(s.one_beta1, g));
+    x.v[i] = __fadd_rn(__fmul_rn(s.beta2, x.v[i]), __fmul_rn(__fmul_rn(s.one_beta2, g), g));
+    r[i] = fast_sqrt(x.v[i]);
+    // lr m / late1 / (sqrt(v / late2) + eps), with a = lr / late1 and root = 1 / sqrt(late2).
+    x.w[i] = x.w[i] * keep - __fdividef(a * x.m[i], fmaf(r[i], root, s.eps));
   }
   if (master) store_f32<kVector>(master + at, x.w, lane, n);
   if (half) store_bf16<kVector>(static_cast<uint16_t*>(t.param[k]) + at, x.w, lane, n);

@@ -42,7 +42,7 @@ lapl_status validate(const lapl_decay_config* c) {
 // 8 warps of an SM are resident.  Times in us, about as measured: a token of the outputs 0.35, of the
 // segments' sums 0.2, a launch 3, its CTAs 2, and 0.05 for each segment.  (16 sequences of 3136 tokens of
 // 32 x 32 in fp32: 58 us in 64 segments, 85 in 32, 149 in 16.)
-int row_segments(int tokens, long long bh, int rows, int cols, int sms) {
+int row_segments(int tokens, long long bh, int rows, int cols, int sms, double* us) {
   const int per_warp = rows <= 32 && cols > 32 ? 64 : 32;
   const long long warps = bh * ((cols + per_warp - 1) / per_warp);
   const long long room = (rows <= 64 ? 16LL : 48LL) * sms;
@@ -56,17 +56,15 @@ int row_segments(int tokens, long long bh, int rows, int cols, int sms) {
     if (g > 1) time += waves * (2.0 + 0.2 * token * per) + 6.0 + 0.05 * g;
     if (g == 1 || time < least) least = time, best = g;
   }
+  *us = least;
   return best;
 }
-
-// Shortest sequences for the tensor cores.
-constexpr int kLeastTokens = 64;
 
 // Segments of a sequence in chunks: a CTA of an SM walks its chunks, of 64 columns of the state.  Times in
 // us, as measured, for rows of up to 64 values and for longer ones: a chunk of the outputs and what a CTA
 // has besides, the same of the segments' sums; the launch between 4, and 0.4 for each segment.  (4 x 8
 // sequences of 128 chunks of 64 x 64: 110 us in 4 segments, 249 in 1, 121 in 9.)
-int chunk_segments(int tokens, long long bh, int rows, int cols, int sms) {
+int chunk_segments(int tokens, long long bh, int rows, int cols, int sms, double* us) {
   static const double kTimes[2][4] = {{2.05, 4.5, 1.25, 3.0}, {3.6, 6.0, 1.9, 4.0}};
   const double* t = kTimes[rows > 64];
   const int chunks = (tokens + decay::kTcChunk - 1) / decay::kTcChunk;
@@ -79,6 +77,7 @@ int chunk_segments(int tokens, long long bh, int rows, int cols, int sms) {
     if (n > 1) time += (double)((bh * (n - 1) + sms - 1) / sms) * (t[3] + t[2] * per) + 4.0 + 0.4 * n;
     if (g == 1 || time < least) least = time, best = n;
   }
+  *us = least;
   return best;
 }
 
@@ -88,8 +87,19 @@ int per_segment(int tokens, int segments, int step) {
 }
 
 bool tc_sizes(const lapl_decay_config& c) {
-  return c.in_dtype == LAPL_BF16 && c.tokens >= kLeastTokens && c.key_dim % 8 == 0 &&
-         c.value_dim % 8 == 0;
+  return c.in_dtype == LAPL_BF16 && c.key_dim % 8 == 0 && c.value_dim % 8 == 0;
+}
+
+// Segments of sequences by both kernels, and whether the tensor cores are faster where they can run: for
+// short sequences, up to one chunk, a CTA's own time against that of the tokens one by one.  (64 x 64 bf16:
+// 8 sequences of 16 tokens 8.3 us and 11.0, 512 of them 26 and 12.7, of 48 30 and 30.)
+void choose(const lapl_decay_config& c, long long bh, int rows, int cols, int sms, bool tc_can, int* row,
+            int* segments, int* tc) {
+  double row_us = 0, tc_us = 0;
+  *row = row_segments(c.tokens, bh, rows, cols, sms, &row_us);
+  const int chunked = chunk_segments(c.tokens, bh, rows, cols, sms, &tc_us);
+  *tc = tc_can && tc_us < row_us;
+  *segments = *tc ? chunked : *row;
 }
 
 size_t states_bytes(const lapl_decay_plan& p, int segments) {
@@ -148,19 +158,12 @@ lapl_status lapl_decay_create(const lapl_decay_config* cfg, lapl_decay_handle* o
   p->device = device;
   p->dev_err = dev_err;
   p->wait_ns = kWaitNs;
-  p->row_segments = row_segments(cfg->tokens, p->bh, cfg->key_dim, cfg->value_dim, sms);
+  choose(*cfg, p->bh, cfg->key_dim, cfg->value_dim, sms, tc_sizes(*cfg), &p->row_segments,
+         &p->info.segments, &p->info.tensor_cores);
   // The backward's three passes go side by side.
   const int most = std::max(cfg->key_dim, cfg->value_dim);
-  p->backward_row_segments = row_segments(cfg->tokens, 3LL * p->bh, most, most, sms);
-  p->info.tensor_cores = tc_sizes(*cfg);
-  p->info.backward_tensor_cores = tc_sizes(*cfg) && cfg->grad_dtype == LAPL_BF16;
-  p->info.segments =
-      p->info.tensor_cores
-          ? chunk_segments(cfg->tokens, p->bh, cfg->key_dim, cfg->value_dim, sms)
-          : p->row_segments;
-  p->info.backward_segments = p->info.backward_tensor_cores
-                                  ? chunk_segments(cfg->tokens, 3LL * p->bh, most, most, sms)
-                                  : p->backward_row_segments;
+  choose(*cfg, 3LL * p->bh, most, most, sms, tc_sizes(*cfg) && cfg->grad_dtype == LAPL_BF16,
+         &p->backward_row_segments, &p->info.backward_segments, &p->info.backward_tensor_cores);
   *out = p;
   return LAPL_OK;
 }

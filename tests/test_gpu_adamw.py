@@ -165,6 +165,47 @@ def test_small_and_large_gradients(scale):
 
 
 @pytest.mark.parametrize("bits", [32, 8])
+def test_states_are_rounded_one_by_one(bits):
+    """Every product and sum of the states rounded to fp32, bit for bit, and the codes of what that
+    gives: nothing is contracted."""
+    import laplacian_nystr_attention_gb300 as lna
+    n, f = 256 * 400, np.float32
+    rng = np.random.default_rng(9)
+    g, m, v = (rng.standard_normal(n).astype(f) for _ in range(3))
+    v = v * v
+    norm, most = f(7.0), f(3.0)
+    plan = lna.AdamW([n], ["f32"], betas=(0.9, 0.95), state_bits=bits)
+    s = {k: [torch.from_numpy(a.copy()).cuda()] for k, a in (("m", m), ("v", v))}
+    if bits == 8:
+        s = {}
+        for k, a in (("m", m), ("v", np.sqrt(v))):
+            scale = np.abs(a).reshape(-1, 256).max(1) * f(1 / 448)
+            q = torch.from_numpy(a / scale.repeat(256)).to(torch.float8_e4m3fn)
+            held = q.float().numpy() * scale.repeat(256)
+            s[k], s[k + "_scales"] = [q.cuda()], [torch.from_numpy(scale).cuda()]
+            if k == "m":
+                m = held
+            else:
+                v = held * held
+    plan.step([torch.zeros(n, device="cuda")], [torch.from_numpy(g).cuda()], step=3, lr=0.1,
+              norm=torch.tensor(norm, device="cuda"), max_norm=float(most), **s)
+    g = g * (most * (f(1) / norm))
+    m = f(0.9) * m + f(1 - 0.9) * g
+    v = f(0.95) * v + f(1 - 0.95) * g * g
+    if bits == 32:
+        assert np.array_equal(s["m"][0].cpu().numpy(), m) and np.array_equal(s["v"][0].cpu().numpy(), v)
+        return
+    for k, a in (("m", m), ("v", np.sqrt(v))):
+        scale = np.abs(a).reshape(-1, 256).max(1) * f(1 / 448)
+        assert np.array_equal(s[k + "_scales"][0].cpu().numpy(), scale)
+        q = a / scale.repeat(256)
+        if k == "v":
+            q = np.where(a > 0, np.maximum(q, f(2.0 ** -9)), q)
+        want = torch.from_numpy(q).to(torch.float8_e4m3fn)
+        assert torch.equal(s[k][0].cpu().view(torch.uint8), want.view(torch.uint8))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
 @pytest.mark.parametrize("norm", [float("inf"), float("nan")])
 def test_a_norm_that_is_not_finite_changes_nothing(bits, norm):
     import laplacian_nystr_attention_gb300 as lna

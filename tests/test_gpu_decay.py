@@ -94,7 +94,8 @@ def test_types(dtype, other):
 @pytest.mark.parametrize("N", [1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 255, 257, 400])
 @pytest.mark.parametrize("reverse", [False, True])
 def test_lengths_of_sequences(N, reverse):
-    run(1, 2, N, 64, 64, "bf16", reverse=reverse, seed=N, tc=N >= 64)
+    run(1, 2, N, 64, 64, "bf16", reverse=reverse, seed=N, tc={1: False, 2: False}.get(
+        N, True if N >= 63 else None))
     run(1, 2, N, 24, 40, "f32", reverse=reverse, seed=N, tc=False)
 
 
