@@ -278,9 +278,10 @@ lapl_status lapl_decay_device_errors(lapl_decay_handle p, void* stream, unsigned
   *flags = word;
   if (!word) return LAPL_OK;
   snprintf(p->last_error, sizeof(p->last_error),
-           "device error flags 0x%x: a bounded wait gave up in:%s%s", word,
+           "device error flags 0x%x: a bounded wait gave up in:%s%s%s", word,
            (word & kErrBitDecay) ? " the linear attention's tensor-core kernels;" : "",
-           (word & ~kErrBitDecay) ? " a kernel of another operator;" : "");
+           (word & kErrBitScan) ? " the recurrence's exchange between CTAs;" : "",
+           (word & ~(kErrBitDecay | kErrBitScan)) ? " a kernel of the attention;" : "");
   return LAPL_ERR_DEVICE_TIMEOUT;
 }
 

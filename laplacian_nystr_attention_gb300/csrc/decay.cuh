@@ -19,9 +19,6 @@
 
 namespace lapl {
 
-// A bit of the device error word beside the others: the tensor-core kernels of the linear attention.
-constexpr unsigned kErrBitDecay = 16u;
-
 namespace decay {
 
 // Smallest log_decay: it underflows at the first step, and stays finite times any length.

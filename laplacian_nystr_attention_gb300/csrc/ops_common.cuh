@@ -13,6 +13,8 @@ namespace lapl {
 // A bit of the device error word beside those of common.cuh: the exchange between CTAs of the gated
 // linear recurrence.
 constexpr unsigned kErrBitScan = 8u;
+// And the tensor-core kernels of the linear attention with decays.
+constexpr unsigned kErrBitDecay = 16u;
 
 namespace ops {
 

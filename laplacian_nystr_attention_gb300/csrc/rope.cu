@@ -388,8 +388,8 @@ __device__ __forceinline__ void add_to_sums(const Args& a, const float (&dw)[NS]
   }
 }
 
-// dw: a thread's rows are summed in fp32, kTiles CTA's tokens of them at most, what follows in pairs of floats.
-constexpr int kTiles = 32;
+// dw: a thread's rows are summed in fp32, some kSummed of them, what follows in pairs of floats.
+constexpr int kSummed = 64;
 template <int V, int NS, bool kInterleaved, bool kHalfIn, bool kHalfGrad>
 __global__ void __launch_bounds__(kThreads, kBackCtas)
 rope_backward_kernel(const __grid_constant__ Args a) {
@@ -424,7 +424,8 @@ rope_backward_kernel(const __grid_constant__ Args a) {
           for (int i = 0; i < V; ++i) dw[w][j][e][i] = 0.f;
   };
   clear();
-  int tiles = 0;
+  const int rows_of_tile = (max(a.part[0].heads, a.part[1].heads) + step - 1) / step;
+  int summed = 0;
   for (long long first = (long long)blockIdx.x * a.at_once; first < a.rows;
        first += (long long)gridDim.x * a.at_once) {
     const int count = (int)min((long long)a.at_once, a.rows - first);
@@ -530,12 +531,13 @@ rope_backward_kernel(const __grid_constant__ Args a) {
         }
       }
     }
-    if (a.partial && (++tiles == kTiles || first + (long long)gridDim.x * a.at_once >= a.rows)) {
+    summed += rows_of_tile;
+    if (a.partial && (summed >= kSummed || first + (long long)gridDim.x * a.at_once >= a.rows)) {
 #pragma unroll
       for (int which = 0; which < 2; ++which)
         add_to_sums<V, NS, kInterleaved>(a, dw[which], sums + which * a.d, lane, lanes);
       clear();
-      tiles = 0;
+      summed = 0;
     }
   }
   if (a.partial) {

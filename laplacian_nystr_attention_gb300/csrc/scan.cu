@@ -837,9 +837,10 @@ lapl_status lapl_scan_device_errors(lapl_scan_handle p, void* stream, unsigned* 
   *flags = word;
   if (!word) return LAPL_OK;
   snprintf(p->last_error, sizeof(p->last_error),
-           "device error flags 0x%x: a bounded wait gave up in:%s%s", word,
+           "device error flags 0x%x: a bounded wait gave up in:%s%s%s", word,
            (word & kErrBitScan) ? " the recurrence's exchange between CTAs;" : "",
-           (word & ~kErrBitScan) ? " a kernel of the attention;" : "");
+           (word & kErrBitDecay) ? " the linear attention with decays;" : "",
+           (word & ~(kErrBitScan | kErrBitDecay)) ? " a kernel of the attention;" : "");
   return LAPL_ERR_DEVICE_TIMEOUT;
 }
 
