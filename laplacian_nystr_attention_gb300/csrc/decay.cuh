@@ -98,10 +98,34 @@ struct Fade {
   }
 };
 
+// The next launch's CTAs may be placed from here on; they wait themselves for what they need.
+__device__ __forceinline__ void release_next() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+// Until the launch before has ended, where this one was placed early.
+__device__ __forceinline__ void await_last() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// early: placed while the launch before runs.
+template <class... P, class... A>
+cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, bool early, cudaStream_t st,
+                   const A&... a) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = early ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, a...);
+}
+
 // All launches of the passes token by token, for any sizes and types (decay_rows.cu).
 cudaError_t launch_rows(const Args& a, int passes, int bh, cudaStream_t st);
-// The launch that turns segments' own states into those before each.
-cudaError_t launch_carry(const Args& a, int passes, int bh, cudaStream_t st);
+// The launch that turns segments' own states into those before each; early: right after theirs.
+cudaError_t launch_carry(const Args& a, int passes, int bh, bool early, cudaStream_t st);
 // All launches of the passes in chunks on the tensor cores (decay_tc.cu), where types, sizes and
 // alignment allow that.
 bool tc_fits(const Args& a, int passes);

@@ -116,6 +116,7 @@ decay_rows_kernel(const __grid_constant__ Args a, int pass0) {
   const int bh = blockIdx.x / a.segments, segment = blockIdx.x % a.segments;
   const Range range(a, bh, segment);
   const int live = range.live(a, p);
+  if (!kOut) release_next();
   if (!kOut && segment == a.segments - 1) return;   // no segment comes after it
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, threads = blockDim.x, warps = threads / 32;
   const int rows = p.a, cols = p.b;
@@ -173,22 +174,6 @@ decay_rows_kernel(const __grid_constant__ Args a, int pass0) {
         for (int k = 0; k < 4; ++k) S[i][c + k] = two(v[k].f[0], v[k].f[1]);
       }
   };
-  if (kOut) {
-    const long long at = (long long)bh * rows * cols;
-    const float* from = p.states ? p.states + ((long long)bh * a.segments + segment) * rows * cols
-                        : p.first ? p.first + at : nullptr;
-    if (from && !p.states && p.first_across) {
-      each_value([&](float& v, int row, int col) { v = from[col * rows + row]; });
-    } else if (from && cols % 4 == 0 && ((uintptr_t)from & 15) == 0) {
-      each_four([&](float& v0, float& v1, float& v2, float& v3, int i) {
-        const float4 f = *reinterpret_cast<const float4*>(from + i);
-        v0 = f.x, v1 = f.y, v2 = f.z, v3 = f.w;
-      });
-    } else if (from) {
-      each_value([&](float& v, int row, int col) { v = from[row * cols + col]; });
-    }
-  }
-
   auto copy = [&](int i0, int stage) {
     const int n = min(kTok, range.begin + live - i0);
     if (n > 0) {
@@ -223,6 +208,22 @@ decay_rows_kernel(const __grid_constant__ Args a, int pass0) {
   };
 
   copy(range.begin, 0);
+  if (kOut) {
+    if (p.states) await_last();   // the states before each segment are there
+    const long long at = (long long)bh * rows * cols;
+    const float* from = p.states ? p.states + ((long long)bh * a.segments + segment) * rows * cols
+                        : p.first ? p.first + at : nullptr;
+    if (from && !p.states && p.first_across) {
+      each_value([&](float& v, int row, int col) { v = from[col * rows + row]; });
+    } else if (from && cols % 4 == 0 && ((uintptr_t)from & 15) == 0) {
+      each_four([&](float& v0, float& v1, float& v2, float& v3, int i) {
+        const float4 f = *reinterpret_cast<const float4*>(from + i);
+        v0 = f.x, v1 = f.y, v2 = f.z, v3 = f.w;
+      });
+    } else if (from) {
+      each_value([&](float& v, int row, int col) { v = from[row * cols + col]; });
+    }
+  }
   int stage = 0;
   bool first = kOut && p.undecayed && segment == 0;
   for (int i0 = range.begin; i0 < range.begin + live; i0 += kTok, stage ^= 1) {
@@ -362,12 +363,14 @@ decay_carry_kernel(const __grid_constant__ Args a, int tiles) {
   const Pass& p = a.pass[blockIdx.z];
   const int size = p.a * p.b, bh = blockIdx.x / tiles;
   const int i = (blockIdx.x - bh * tiles) * 256 + threadIdx.x;
+  release_next();
   // The segments with tokens come first.
   if (threadIdx.x < a.segments) {
     const int live = Range(a, bh, threadIdx.x).live(a, p);
     fades[threadIdx.x] = Fade(log_decay(a, bh), live - (p.undecayed && threadIdx.x == 0 && live > 0));
   }
   __syncthreads();
+  await_last();   // the segments' own states are there
   if (i >= size) return;
   float s = 0.f;
   if (p.first) {
@@ -395,7 +398,7 @@ constexpr int kMostSmem = kTok * 4 * (2 * 3 * 128 + 3 * 128 + 1);
 
 template <int KD, int kCols>
 cudaError_t launch_pass(const Args& a, int pass0, int passes, int bh, bool out, int warps, size_t smem,
-                        cudaStream_t st) {
+                        bool early, cudaStream_t st) {
   auto kernel = out ? decay_rows_kernel<KD, kCols, true> : decay_rows_kernel<KD, kCols, false>;
   if (smem > 48 * 1024) {
     // As large as any call needs: calls at once do not set it lower for each other.
@@ -403,8 +406,8 @@ cudaError_t launch_pass(const Args& a, int pass0, int passes, int bh, bool out, 
                                                kMostSmem);
     if (e != cudaSuccess) return e;
   }
-  kernel<<<dim3((unsigned)(bh * a.segments), 1, (unsigned)passes), 32 * warps, smem, st>>>(a, pass0);
-  return cudaGetLastError();
+  return launch(kernel, dim3((unsigned)(bh * a.segments), 1, (unsigned)passes), 32 * warps, smem, early, st,
+                a, pass0);
 }
 
 // Rows of a pass as the kernels pad them.
@@ -414,18 +417,18 @@ int padded(int rows) {
 
 }  // namespace
 
-cudaError_t launch_carry(const Args& a, int passes, int bh, cudaStream_t st) {
+cudaError_t launch_carry(const Args& a, int passes, int bh, bool early, cudaStream_t st) {
   int most = 0;
   for (int i = 0; i < passes; ++i) most = std::max(most, a.pass[i].a * a.pass[i].b);
   const int tiles = (most + 255) / 256;
-  decay_carry_kernel<<<dim3((unsigned)(bh * tiles), 1, (unsigned)passes), 256, 0, st>>>(a, tiles);
-  return cudaGetLastError();
+  return launch(decay_carry_kernel, dim3((unsigned)(bh * tiles), 1, (unsigned)passes), 256, 0, early, st, a,
+                tiles);
 }
 
 cudaError_t launch_rows(const Args& a, int passes, int bh, cudaStream_t st) {
   for (int stage = a.segments > 1 ? 0 : a.pass[0].states ? 1 : 2; stage < 3; ++stage) {
     if (stage == 1) {
-      const cudaError_t e = launch_carry(a, passes, bh, st);
+      const cudaError_t e = launch_carry(a, passes, bh, a.segments > 1, st);
       if (e != cudaSuccess) return e;
       continue;
     }
@@ -436,7 +439,7 @@ cudaError_t launch_rows(const Args& a, int passes, int bh, cudaStream_t st) {
       while (i + n < passes && padded(a.pass[i + n].a) == kd) ++n;
       int cols = 0;
       size_t smem = 0;
-      const bool out = stage == 2;
+      const bool out = stage == 2, early = out && i == 0 && a.pass[0].states;   // right after the carry
       for (int j = i; j < i + n; ++j) {
         const Pass& p = a.pass[j];
         cols = std::max(cols, p.b);
@@ -453,16 +456,16 @@ cudaError_t launch_rows(const Args& a, int passes, int bh, cudaStream_t st) {
       const int warps = wide ? (cols + 63) / 64 : (cols + 31) / 32;
       smem += sizeof(float) * kTok * (warps * (wide ? 64 : 32) + 1);
       switch (kd * 2 + wide) {
-        case 32: e = launch_pass<16, 4>(a, i, n, bh, out, warps, smem, st); break;
-        case 33: e = launch_pass<16, 8>(a, i, n, bh, out, warps, smem, st); break;
-        case 64: e = launch_pass<32, 4>(a, i, n, bh, out, warps, smem, st); break;
-        case 65: e = launch_pass<32, 8>(a, i, n, bh, out, warps, smem, st); break;
-        case 96: e = launch_pass<48, 4>(a, i, n, bh, out, warps, smem, st); break;
-        case 97: e = launch_pass<48, 8>(a, i, n, bh, out, warps, smem, st); break;
-        case 128: e = launch_pass<64, 4>(a, i, n, bh, out, warps, smem, st); break;
-        case 129: e = launch_pass<64, 8>(a, i, n, bh, out, warps, smem, st); break;
-        case 192: e = launch_pass<96, 4>(a, i, n, bh, out, warps, smem, st); break;
-        default: e = launch_pass<128, 4>(a, i, n, bh, out, warps, smem, st); break;
+        case 32: e = launch_pass<16, 4>(a, i, n, bh, out, warps, smem, early, st); break;
+        case 33: e = launch_pass<16, 8>(a, i, n, bh, out, warps, smem, early, st); break;
+        case 64: e = launch_pass<32, 4>(a, i, n, bh, out, warps, smem, early, st); break;
+        case 65: e = launch_pass<32, 8>(a, i, n, bh, out, warps, smem, early, st); break;
+        case 96: e = launch_pass<48, 4>(a, i, n, bh, out, warps, smem, early, st); break;
+        case 97: e = launch_pass<48, 8>(a, i, n, bh, out, warps, smem, early, st); break;
+        case 128: e = launch_pass<64, 4>(a, i, n, bh, out, warps, smem, early, st); break;
+        case 129: e = launch_pass<64, 8>(a, i, n, bh, out, warps, smem, early, st); break;
+        case 192: e = launch_pass<96, 4>(a, i, n, bh, out, warps, smem, early, st); break;
+        default: e = launch_pass<128, 4>(a, i, n, bh, out, warps, smem, early, st); break;
       }
       if (e != cudaSuccess) return e;
       i += n;

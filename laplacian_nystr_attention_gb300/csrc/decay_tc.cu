@@ -469,6 +469,7 @@ decay_chunks_kernel(const __grid_constant__ TcArgs t) {
     Vec<2> S[kCols / 2];
     const float* from = nullptr;
     long long row_step = p.b, col_step = 1;
+    if (p.states) await_last();   // the states before each segment are there
     if (p.states) {
       from = p.states + ((long long)bh * a.segments + segment) * p.a * p.b;
     } else if (p.first) {
@@ -660,6 +661,7 @@ decay_sums_kernel(const __grid_constant__ TcArgs t) {
   const Args& a = t.a;
   const int which = blockIdx.z, col0 = blockIdx.y * kD;
   const Pass& p = a.pass[which];
+  release_next();
   if (col0 >= p.b) return;   // (a pass with fewer columns than the launch's widest)
   const int bh = blockIdx.x / (a.segments - 1), segment = blockIdx.x % (a.segments - 1);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -837,18 +839,18 @@ cudaError_t launch_boxes(const TcArgs& t, int passes, int bh, int tiles, cudaStr
     e = cudaFuncSetAttribute(decay_sums_kernel<kBoxes>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kSmemMost);
     if (e != cudaSuccess) return e;
-    decay_sums_kernel<kBoxes><<<dim3((unsigned)(bh * (a.segments - 1)), (unsigned)tiles, (unsigned)passes),
-                                kSumThreads, sums, st>>>(t);
-    e = cudaGetLastError();
+    e = launch(decay_sums_kernel<kBoxes>,
+               dim3((unsigned)(bh * (a.segments - 1)), (unsigned)tiles, (unsigned)passes), kSumThreads, sums,
+               false, st, t);
   }
-  if (e == cudaSuccess && a.pass[0].states) e = launch_carry(a, passes, bh, st);
+  if (e == cudaSuccess && a.pass[0].states) e = launch_carry(a, passes, bh, a.segments > 1, st);
   if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(decay_chunks_kernel<kBoxes>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            kSmemMost);
   if (e != cudaSuccess) return e;
-  decay_chunks_kernel<kBoxes><<<dim3((unsigned)(bh * a.segments), (unsigned)tiles, (unsigned)passes),
-                                kOutThreads, outs, st>>>(t);
-  return cudaGetLastError();
+  return launch(decay_chunks_kernel<kBoxes>,
+                dim3((unsigned)(bh * a.segments), (unsigned)tiles, (unsigned)passes), kOutThreads, outs,
+                a.pass[0].states != nullptr, st, t);
 }
 
 }  // namespace
