@@ -24,7 +24,10 @@ namespace {
 
 using ops::Vec;
 
-constexpr int kTok = 12;          // tokens of a stage (16: at 64 x 64 in fp32 room for 7 of 8 CTAs)
+// Tokens of a stage: as many as leave room in shared memory for the warps that registers do (64 x 64 in fp32
+// with 16: 7 of 8 CTAs, and 646 us for what takes 501).
+constexpr int kMostTok = 16;
+constexpr int tokens_of(int kd) { return kd <= 32 ? 16 : 12; }
 constexpr float kMostUp = 4.f;    // log2 of the largest g^-kTok that the state is held times
 
 // Two floats in a register pair as the packed instructions take them.  (As two floats that happen to be
@@ -110,6 +113,7 @@ template <int KD, int kCols, bool kOut>
 __global__ void __launch_bounds__(128, KD * kCols <= 256 ? 4 : KD * kCols <= 384 ? 3 : 2)
 decay_rows_kernel(const __grid_constant__ Args a, int pass0) {
   extern __shared__ __align__(16) unsigned char smem[];
+  constexpr int kTok = tokens_of(KD);
   constexpr int kRows = KD / 4, kPairs = kRows / 2;   // of a lane
   constexpr int kWide = 8 * kCols;                    // columns of a warp
   const Pass& p = a.pass[pass0 + blockIdx.z];
@@ -129,16 +133,24 @@ decay_rows_kernel(const __grid_constant__ Args a, int pass0) {
   const unsigned raw_y = (unsigned)((kTok * rows * yb + 15) & ~15);
   const unsigned raw_z = (unsigned)((kTok * cols * zb + 15) & ~15);
   const unsigned raw = raw_x + raw_y + raw_z;
-  const int wide = warps * kWide;
   // Rows of fp32 that need no padding are read as they were copied.
+  const int wide = warps * kWide;
   const bool x_as_is = !p.x_half && rows == KD, y_as_is = !p.y_half && rows == KD;
+  const bool z_as_is = !p.z_half && cols == wide;
   float* fx = reinterpret_cast<float*>(smem + 2 * raw);       // [kTok][KD]
   float* fy = fx + (kOut && !x_as_is ? kTok * KD : 0);        // [kTok][KD]
-  float* fz = fy + (y_as_is ? 0 : kTok * KD);                 // [kTok][wide], times its decay
-  float* down = fz + kTok * wide;                             // [kTok] of outputs
+  float* fz = fy + (y_as_is ? 0 : kTok * KD);                 // [kTok][wide]
+  float* up = fz + (z_as_is ? 0 : kTok * wide);               // [kTok] what z is multiplied by,
+  float* down = up + kTok;                                    // [kTok] and what outputs are
 
   const float l = log_decay(a, bh), l2 = l * kLog2e;
-  const bool held = -l2 * kTok <= kMostUp;
+  const bool held = -l2 * kMostTok <= kMostUp;
+  if (threadIdx.x < kTok) {
+    const float n = (float)(threadIdx.x + 1);
+    up[threadIdx.x] = held ? p.zs * exp2f(-l2 * n) : p.zs;
+    down[threadIdx.x] = held ? p.os * exp2f(l2 * n) : p.os;
+  }
+  const Fade whole(l, kTok);
 
   Two S[kPairs][kCols];
 #pragma unroll
@@ -234,22 +246,19 @@ decay_rows_kernel(const __grid_constant__ Args a, int pass0) {
     const unsigned char* from = smem + stage * raw;
     if (kOut && !x_as_is) widen(fx, from, p.x_half, n);
     if (!y_as_is) widen(fy, from + raw_x, p.y_half, n);
-    // (The stage's rows lie as in memory: row `at` is token n - 1 - at against the order.)
+    if (!z_as_is) {
 #pragma unroll 4
-    for (int at = warp; at < n; at += warps) {
-      const int t = p.reverse ? n - 1 - at : at;
-      const float w = held ? p.zs * exp2f(-l2 * (float)(t + 1)) : p.zs;
-      for (int e = lane; e < wide; e += 32)
-        fz[at * wide + e] = e < cols ? w * value(from + raw_x + raw_y, p.z_half, cols, at, e) : 0.f;
+      for (int t = warp; t < n; t += warps)
+        for (int e = lane; e < wide; e += 32)
+          fz[t * wide + e] = e < cols ? value(from + raw_x + raw_y, p.z_half, cols, t, e) : 0.f;
     }
-    if (kOut && threadIdx.x < kTok)
-      down[threadIdx.x] = held ? p.os * exp2f(l2 * (float)(threadIdx.x + 1)) : p.os;
     __syncthreads();
     // Rows go up or down in memory.
-    const int at0 = p.reverse ? n - 1 : 0, up = p.reverse ? -1 : 1;
+    const int at0 = p.reverse ? n - 1 : 0, step = p.reverse ? -1 : 1;
     const float* sx = (x_as_is ? reinterpret_cast<const float*>(from) : fx) + row0 + at0 * KD;
     const float* sy = (y_as_is ? reinterpret_cast<const float*>(from + raw_x) : fy) + row0 + at0 * KD;
-    const float* sz = fz + col0 + at0 * wide;
+    const float* sz =
+        (z_as_is ? reinterpret_cast<const float*>(from + raw_x + raw_y) : fz) + col0 + at0 * wide;
     long long to = 0;
     if (kOut)
       to = ((long long)bh * a.tokens + (p.reverse ? range.len - 1 - i0 : i0)) * cols + out_col;
@@ -262,7 +271,7 @@ decay_rows_kernel(const __grid_constant__ Args a, int pass0) {
     }
     const float g = exp2f(l2);
 #pragma unroll 1
-    for (int t = 0; t < n; ++t, sx += up * KD, sy += up * KD, sz += up * wide, to += up * cols) {
+    for (int t = 0; t < n; ++t, sx += step * KD, sy += step * KD, sz += step * wide, to += step * cols) {
       if (!held) {
         if (!first) {
 #pragma unroll
@@ -273,11 +282,13 @@ decay_rows_kernel(const __grid_constant__ Args a, int pass0) {
         first = false;
       }
       Two z[kCols], o[kCols];
+      const float w = up[t];
 #pragma unroll
       for (int c = 0; c < kCols; c += 4) {
         const float4 f = *reinterpret_cast<const float4*>(sz + c);
-        z[c] = two(f.x, f.x), z[c + 1] = two(f.y, f.y);
-        z[c + 2] = two(f.z, f.z), z[c + 3] = two(f.w, f.w);
+        const float z0 = f.x * w, z1 = f.y * w, z2 = f.z * w, z3 = f.w * w;
+        z[c] = two(z0, z0), z[c + 1] = two(z1, z1);
+        z[c + 2] = two(z2, z2), z[c + 3] = two(z3, z3);
       }
       const ulonglong2* y2 = reinterpret_cast<const ulonglong2*>(sy);
       const ulonglong2* x2 = reinterpret_cast<const ulonglong2*>(sx);
@@ -321,7 +332,7 @@ decay_rows_kernel(const __grid_constant__ Args a, int pass0) {
       }
     }
     if (held) {
-      const Fade fade(l, n);
+      const Fade fade = n == kTok ? whole : Fade(l, n);
       const Two less = two(fade.less, fade.less), factor = two(fade.factor, fade.factor);
 #pragma unroll
       for (int i = 0; i < kPairs; ++i)
@@ -394,7 +405,7 @@ decay_carry_kernel(const __grid_constant__ Args a, int tiles) {
 }
 
 // The most shared memory of any pass: two stages of fp32 rows of 128, one of them padded.
-constexpr int kMostSmem = kTok * 4 * (2 * 3 * 128 + 3 * 128 + 1);
+constexpr int kMostSmem = tokens_of(128) * 4 * (2 * 3 * 128 + 3 * 128 + 2);
 
 template <int KD, int kCols>
 cudaError_t launch_pass(const Args& a, int pass0, int passes, int bh, bool out, int warps, size_t smem,
@@ -412,7 +423,7 @@ cudaError_t launch_pass(const Args& a, int pass0, int passes, int bh, bool out, 
 
 // Rows of a pass as the kernels pad them.
 int padded(int rows) {
-  return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 48 ? 48 : rows <= 64 ? 64 : rows <= 96 ? 96 : 128;
+  return rows <= 64 ? (rows + 15) / 16 * 16 : rows <= 80 ? 80 : rows <= 96 ? 96 : 128;
 }
 
 }  // namespace
@@ -434,7 +445,7 @@ cudaError_t launch_rows(const Args& a, int passes, int bh, cudaStream_t st) {
     }
     // Passes of the same padded rows in one launch.
     for (int i = 0; i < passes;) {
-      const int kd = padded(a.pass[i].a);
+      const int kd = padded(a.pass[i].a), tok = tokens_of(kd);
       int n = 1;
       while (i + n < passes && padded(a.pass[i + n].a) == kd) ++n;
       int cols = 0;
@@ -443,27 +454,26 @@ cudaError_t launch_rows(const Args& a, int passes, int bh, cudaStream_t st) {
       for (int j = i; j < i + n; ++j) {
         const Pass& p = a.pass[j];
         cols = std::max(cols, p.b);
-        const size_t x = stage == 2 ? align_up((size_t)kTok * p.a * (p.x_half ? 2 : 4), 16) : 0;
-        const size_t y = align_up((size_t)kTok * p.a * (p.y_half ? 2 : 4), 16);
-        const size_t z = align_up((size_t)kTok * p.b * (p.z_half ? 2 : 4), 16);
+        const size_t x = stage == 2 ? align_up((size_t)tok * p.a * (p.x_half ? 2 : 4), 16) : 0;
+        const size_t y = align_up((size_t)tok * p.a * (p.y_half ? 2 : 4), 16);
+        const size_t z = align_up((size_t)tok * p.b * (p.z_half ? 2 : 4), 16);
         const size_t padded_x = out && (p.x_half || p.a != kd) ? kd : 0;
         const size_t padded_y = p.y_half || p.a != kd ? kd : 0;
-        smem = std::max(smem, 2 * (x + y + z) + sizeof(float) * kTok * (padded_x + padded_y));
+        smem = std::max(smem, 2 * (x + y + z) + sizeof(float) * tok * (padded_x + padded_y));
       }
       cudaError_t e;
       // A lane's 8 columns where that is no more than half of them padding, and where it has registers.
       const bool wide = cols > 32 && kd <= 32;
       const int warps = wide ? (cols + 63) / 64 : (cols + 31) / 32;
-      smem += sizeof(float) * kTok * (warps * (wide ? 64 : 32) + 1);
+      smem += sizeof(float) * tok * (warps * (wide ? 64 : 32) + 2);
       switch (kd * 2 + wide) {
         case 32: e = launch_pass<16, 4>(a, i, n, bh, out, warps, smem, early, st); break;
         case 33: e = launch_pass<16, 8>(a, i, n, bh, out, warps, smem, early, st); break;
         case 64: e = launch_pass<32, 4>(a, i, n, bh, out, warps, smem, early, st); break;
         case 65: e = launch_pass<32, 8>(a, i, n, bh, out, warps, smem, early, st); break;
         case 96: e = launch_pass<48, 4>(a, i, n, bh, out, warps, smem, early, st); break;
-        case 97: e = launch_pass<48, 8>(a, i, n, bh, out, warps, smem, early, st); break;
         case 128: e = launch_pass<64, 4>(a, i, n, bh, out, warps, smem, early, st); break;
-        case 129: e = launch_pass<64, 8>(a, i, n, bh, out, warps, smem, early, st); break;
+        case 160: e = launch_pass<80, 4>(a, i, n, bh, out, warps, smem, early, st); break;
         case 192: e = launch_pass<96, 4>(a, i, n, bh, out, warps, smem, early, st); break;
         default: e = launch_pass<128, 4>(a, i, n, bh, out, warps, smem, early, st); break;
       }
