@@ -41,7 +41,7 @@ lapl_status validate(const lapl_decay_config* c) {
 // Segments of a sequence token by token.  A segment's warps walk its tokens alone; by registers 16, 12 or
 // 8 warps of an SM are resident.  Times in us, about as measured: a token of the outputs 0.35, of the
 // segments' sums 0.2, a launch 3, its CTAs 2, and 0.05 for each segment.  (16 sequences of 3136 tokens of
-// 32 x 32 in fp32: 58 us in 64 segments, 85 in 32, 149 in 16.)
+// 32 x 32 in fp32: 33 us in 98 segments, 45 in 64, 68 in 32, 120 in 16.)
 int row_segments(int tokens, long long bh, int rows, int cols, int sms, double* us) {
   const int per_warp = rows <= 32 && cols > 32 ? 64 : 32;
   const long long warps = bh * ((cols + per_warp - 1) / per_warp);
