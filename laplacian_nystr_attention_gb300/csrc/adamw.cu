@@ -6,7 +6,9 @@
 // run of memory, and a block's largest value is one reduction over the warp.  Blocks that end early
 // and tensors off 16 bytes (8-bit states: off 4) go value by value, lane by lane.
 // HBM-bound: every value's weight, gradient and states are read and written once (28 bytes with fp32
-// states, 16 with 8-bit ones, of fp32 weights).
+// states, 16 with 8-bit ones, of fp32 weights).  Measured, of 6.8 TB/s: 2^20 fp32 values in 24 tensors 5.9 us
+// (5.0 TB/s); 2^27 bf16 weights with masters and 8-bit states 490 us (4.4 TB/s), with instructions issued in
+// 63% of the cycles: roots, divisions and conversions of 8-bit states.
 #include <algorithm>
 #include <cmath>
 #include <new>
@@ -162,7 +164,7 @@ __device__ __forceinline__ float fast_sqrt(float v) {   // off by a unit
 // Where x / scale falls is clear from x (or its root, off by a unit) times the scale's reciprocal, off by 4
 // units together at most, but next to the middle between two codes, and where codes have fewer bits: there
 // the root and the division are formed exactly.  (For each code they were half of the kernel's
-// instructions, whose issue bounds it: 2^27 values 494 us and 715, root and divisions for each.)
+// instructions, whose issue bounds it: 2^27 values 490 us and 715, root and divisions for each.)
 template <bool kVector, bool kRoot>
 __device__ __forceinline__ void store_f8(uint8_t* p, float* scale_at, const float (&x)[kPer],
                                          const float (&root)[kPer], int lane, int n) {

