@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "liblapl_attn.so")
@@ -192,7 +193,7 @@ def _load():
         "lapl_decay_last_error": ([H], ctypes.c_char_p),
         "lapl_decay_destroy": ([H], st),
         "lapl_adamw_create": ([ctypes.POINTER(lapl_adamw_config), ctypes.POINTER(H)], st),
-        "lapl_adamw_step": ([H] + [ctypes.POINTER(vp)] * 7
+        "lapl_adamw_step": ([H] + [vp] * 7
                             + [ctypes.c_float, vp, ctypes.c_longlong, vp, vp, ctypes.c_float, vp],
                             st),
         "lapl_adamw_last_error": ([H], ctypes.c_char_p),
@@ -597,10 +598,14 @@ def lapl_adamw_create(cfg: lapl_adamw_config):
 def lapl_adamw_step(handle, params, grads, masters, m, v, m_scales, v_scales, lr, lr_device, step,
                     step_device, norm, max_norm, stream) -> None:
     """params, grads, m, v: the tensors' device addresses, one for each of the plan's tensors;
-    masters, m_scales, v_scales: the same, or None."""
-    lists = [None if a is None else _pointers(a)
+    masters, m_scales, v_scales: the same (masters: None for what has none), or None."""
+    if masters is not None:
+        masters = [at or 0 for at in masters]
+    # (An array takes a quarter of a ctypes array's time to fill.)
+    lists = [None if a is None else array("Q", a)
              for a in (params, grads, masters, m, v, m_scales, v_scales)]
-    _check(LIB.lapl_adamw_step(handle, *lists, float(lr), lr_device, int(step), step_device, norm,
+    tables = [None if a is None else a.buffer_info()[0] for a in lists]
+    _check(LIB.lapl_adamw_step(handle, *tables, float(lr), lr_device, int(step), step_device, norm,
                                float(max_norm), stream), "lapl_adamw_step", handle,
            "lapl_adamw_last_error")
 

@@ -15,7 +15,7 @@
 // a turn, is one integer multiplication and off by 2^-33 of a turn.
 //
 // Measured, of 6.8 TB/s: 4 x 16384 tokens of 24 heads of 64, bf16, forward 98 us (4.1 TB/s of 403 MB) with
-// instructions issued in 63% of the cycles, some 25 a value; backward 154 us (3.5 TB/s of 537 MB), 43%, waiting
+// instructions issued in 63% of the cycles, some 25 a value; backward 134 us (4.0 TB/s of 537 MB), waiting
 // for loads with the 16 warps of an SM that registers allow.  8 x 3136 tokens of 6 heads of 32 in fp32 15 us,
 // a token 3.8 us.
 #include <algorithm>
@@ -403,7 +403,6 @@ template <int V, int NS, bool kInterleaved, bool kHalfIn, bool kHalfGrad>
 __global__ void __launch_bounds__(kThreads, kBackCtas)
 rope_backward_kernel(const __grid_constant__ Args a) {
   constexpr int kBackRows = back_rows_of(V);
-  constexpr bool kPrefetch = kBackRows == 1;
   extern __shared__ __align__(16) float smem[];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int pad = padded(a.d);
@@ -463,7 +462,8 @@ rope_backward_kernel(const __grid_constant__ Args a) {
         }
       }
     };
-    // The same rows into L2.
+    // Rows into L2, on their way while the ones before are worked on, which a thread's registers have no room
+    // for (without it 155 us instead of 134 of 4 x 16384 tokens of 24 heads of 64).
     auto prefetch = [&](int which, int h) {
       const Part& p = a.part[which];
 #pragma unroll
@@ -491,9 +491,11 @@ rope_backward_kernel(const __grid_constant__ Args a) {
 #pragma unroll 1
       for (int h0 = head0; h0 - head0 < p.heads; h0 += kBackRows * step) {
         if (which > 0 || h0 != head0) load(which, h0);
-        if (kPrefetch) {
-          if (h0 - head0 + step < p.heads) prefetch(which, h0 + step);
-          else if (which < 2) prefetch(which + 1, head0);
+#pragma unroll
+        for (int u = 0; u < kBackRows; ++u) {
+          const int h = h0 + (kBackRows + u) * step;
+          if (h0 + kBackRows * step - head0 < p.heads) prefetch(which, h);
+          else if (which < 2) prefetch(which + 1, head0 + u * step);
         }
 #pragma unroll
         for (int u = 0; u < kBackRows; ++u) {
