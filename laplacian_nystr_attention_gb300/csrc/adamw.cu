@@ -7,8 +7,8 @@
 // and tensors off 16 bytes (8-bit states: off 4) go value by value, lane by lane.
 // HBM-bound: every value's weight, gradient and states are read and written once (28 bytes with fp32
 // states, 16 with 8-bit ones, of fp32 weights).  Measured, of 6.8 TB/s: 2^20 fp32 values in 24 tensors 5.9 us
-// (5.0 TB/s); 2^27 bf16 weights with masters and 8-bit states 490 us (4.4 TB/s), with instructions issued in
-// 63% of the cycles: roots, divisions and conversions of 8-bit states.
+// (5.0 TB/s); 2^27 bf16 weights with masters and 8-bit states 445 us (4.8 TB/s), with instructions issued in
+// two thirds of the cycles: roots, divisions and conversions of 8-bit states.
 #include <algorithm>
 #include <cmath>
 #include <new>
@@ -164,7 +164,8 @@ __device__ __forceinline__ float fast_sqrt(float v) {   // off by a unit
 // Where x / scale falls is clear from x (or its root, off by a unit) times the scale's reciprocal, off by 4
 // units together at most, but next to the middle between two codes, and where codes have fewer bits: there
 // the root and the division are formed exactly.  (For each code they were half of the kernel's
-// instructions, whose issue bounds it: 2^27 values 490 us and 715, root and divisions for each.)
+// instructions, whose issue bounds it: 2^27 values 490 us and 715, root and divisions for each, before
+// blocks were fetched ahead.)
 template <bool kVector, bool kRoot>
 __device__ __forceinline__ void store_f8(uint8_t* p, float* scale_at, const float (&x)[kPer],
                                          const float (&root)[kPer], int lane, int n) {
@@ -202,6 +203,12 @@ __device__ __forceinline__ void store_f8(uint8_t* p, float* scale_at, const floa
       p[at] = (uint8_t)encode2(q[i], 0.f);
     }
   }
+}
+
+// A lane's 8 of the values from `at` on, into L2.
+__device__ __forceinline__ void prefetch(const void* p, long long at, int bytes, int lane) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const unsigned char*>(p) +
+                                                (at + kPer * lane) * bytes));
 }
 
 // The block of n values (256 of kVector) that starts at value `at` of a tensor; block: its number.
@@ -257,6 +264,20 @@ __device__ __forceinline__ void update(const Table<N>& t, int k, long long at, l
   }
 }
 
+// Weights, gradients and codes of a whole block with 8-bit states, into L2, while a block is worked on, which
+// registers have no room for.  (2^27 bf16 weights 445 us and 490 without.  With fp32 states, which wait for
+// bandwidth and not for latency: 2^26 values 320 us and 295
+// without; with the scales 470.)
+template <int N>
+__device__ __forceinline__ void fetch(const Table<N>& t, int k, long long at) {
+  const int lane = threadIdx.x & 31;
+  if (t.master[k]) prefetch(t.master[k], at, 4, lane);
+  else prefetch(t.param[k], at, t.kind[k] & 1 ? 2 : 4, lane);
+  prefetch(t.grad[k], at, t.kind[k] & 2 ? 2 : 4, lane);
+  prefetch(t.m[k], at, 1, lane);
+  prefetch(t.v[k], at, 1, lane);
+}
+
 template <bool k8, int N>
 __global__ void __launch_bounds__(kThreads, kCtas)
 adamw_kernel(const __grid_constant__ Table<N> t, const __grid_constant__ Step s) {
@@ -291,6 +312,8 @@ adamw_kernel(const __grid_constant__ Table<N> t, const __grid_constant__ Step s)
     const bool vector = t.kind[lo] & 4;
     for (int b = warp * kBlock; b < count; b += kThreads / 32 * kBlock) {
       const int n = min(kBlock, count - b);
+      if (k8 && b + kThreads / 32 * kBlock + kBlock <= count)
+        fetch(t, lo, start + b + kThreads / 32 * kBlock);
       if (vector && n == kBlock)
         update<k8, true>(t, lo, start + b, (start + b) / kBlock, n, s, clip, a, root, keep);
       else
