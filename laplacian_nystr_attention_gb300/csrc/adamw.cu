@@ -8,7 +8,7 @@
 // HBM-bound: every value's weight, gradient and states are read and written once (28 bytes with fp32
 // states, 16 with 8-bit ones, of fp32 weights).  Measured, of 6.8 TB/s: 2^20 fp32 values in 24 tensors 5.9 us
 // (5.0 TB/s); 2^27 bf16 weights with masters and 8-bit states 445 us (4.8 TB/s), with instructions issued in
-// two thirds of the cycles: roots, divisions and conversions of 8-bit states.
+// three quarters of the cycles: roots, divisions and conversions of 8-bit states.
 #include <algorithm>
 #include <cmath>
 #include <new>

@@ -15,8 +15,8 @@
 // a turn, is one integer multiplication and off by 2^-33 of a turn.
 //
 // Measured, of 6.8 TB/s: 4 x 16384 tokens of 24 heads of 64, bf16, forward 98 us (4.1 TB/s of 403 MB) with
-// instructions issued in 63% of the cycles, some 25 a value; backward 134 us (4.0 TB/s of 537 MB), waiting
-// for loads with the 16 warps of an SM that registers allow.  8 x 3136 tokens of 6 heads of 32 in fp32 15 us,
+// instructions issued in 63% of the cycles, some 25 a value; backward 134 us (4.0 TB/s of 537 MB), 55%,
+// with the 16 warps of an SM that registers allow.  8 x 3136 tokens of 6 heads of 32 in fp32 15 us,
 // a token 3.8 us.
 #include <algorithm>
 #include <cmath>

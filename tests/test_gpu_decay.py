@@ -107,6 +107,15 @@ def test_dimensions(a, b, dtype):
     run(1, 2, 200, a, b, dtype, seed=a + b)
 
 
+@pytest.mark.parametrize("a,b", [(16, 32), (16, 64), (32, 32), (32, 128), (48, 96), (64, 64), (80, 80),
+                                 (80, 32), (76, 48), (96, 32), (96, 96), (128, 32)])
+@pytest.mark.parametrize("N", [11, 13, 16, 33, 203])
+def test_fp32_rows_at_a_stages_end(a, b, N):
+    """Rows that are read as they were copied and rows that are padded, and last stages of one token,
+    all and almost all."""
+    run(1, 2, N, a, b, "f32", reverse=bool(N % 2), seed=a + N)
+
+
 @pytest.mark.parametrize("reverse", [False, True])
 @pytest.mark.parametrize("dtype,a,b", [("bf16", 64, 64), ("bf16", 32, 24), ("f32", 32, 40),
                                        ("bf16", 128, 128), ("bf16", 56, 88)])
