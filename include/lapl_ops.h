@@ -284,7 +284,9 @@ lapl_status lapl_rope_destroy(lapl_rope_handle h);
  *   S_i = exp(log_decay) S_{i-1} + k_i v_i^T,   out_i = scale q_i S_i
  * with S_{-1} = state (zeros if NULL), a matrix of key_dim x value_dim.  The processing order is the
  * tokens' order, or with reverse the opposite one, from token len-1 down to token 0.  States and sums
- * are fp32.  The decays are constants: no gradient is formed for them.  An infinity or NaN in a
+ * are fp32; for bf16 outputs and gradients of bf16 inputs, what is computed (scores times decays, states)
+ * enters products rounded to 16 bits where they run on the tensor cores, 2^-16 of each term at most beside
+ * the results' own 2^-8.  The decays are constants: no gradient is formed for them.  An infinity or NaN in a
  * sequence's tokens leaves that sequence's outputs undefined, in this head, from 127 tokens before
  * it on.
  */

@@ -61,12 +61,13 @@ int row_segments(int tokens, long long bh, int rows, int cols, int sms, double* 
 }
 
 // Segments of a sequence in chunks: a CTA of an SM walks its chunks, of 64 columns of the state.  Times in
-// us, as measured, for rows of up to 64 values and for longer ones: a chunk of the outputs and what a CTA
-// has besides, the same of the segments' sums; the launch between 4, and 0.4 for each segment.  (4 x 8
-// sequences of 128 chunks of 64 x 64: 110 us in 4 segments, 249 in 1, 121 in 9.)
-int chunk_segments(int tokens, long long bh, int rows, int cols, int sms, double* us) {
-  static const double kTimes[2][4] = {{2.05, 4.5, 1.25, 3.0}, {3.6, 6.0, 1.9, 4.0}};
-  const double* t = kTimes[rows > 64];
+// us, as measured, for rows of up to 64 values and for longer ones, and the same for fp32 outputs: a chunk of
+// the outputs and what a CTA has besides, the same of the segments' sums; the launch between 4, and 0.4 for each
+// segment.  (4 x 8 sequences of 128 chunks of 64 x 64: 110 us in 4 segments, 249 in 1, 121 in 9.)
+int chunk_segments(int tokens, long long bh, int rows, int cols, bool exact, int sms, double* us) {
+  static const double kTimes[2][2][4] = {{{2.05, 4.5, 1.25, 3.0}, {3.6, 6.0, 1.9, 4.0}},
+                                         {{3.4, 5.5, 1.25, 3.0}, {4.0, 6.0, 1.9, 4.0}}};
+  const double* t = kTimes[exact][rows > 64];
   const int chunks = (tokens + decay::kTcChunk - 1) / decay::kTcChunk;
   bh *= (cols + 63) / 64;
   int best = 1;
@@ -93,11 +94,11 @@ bool tc_sizes(const lapl_decay_config& c) {
 // Segments of sequences by both kernels, and whether the tensor cores are faster where they can run: for
 // short sequences, up to one chunk, a CTA's own time against that of the tokens one by one.  (64 x 64 bf16:
 // 8 sequences of 16 tokens 8.3 us and 11.0, 512 of them 26 and 12.7, of 48 30 and 30.)
-void choose(const lapl_decay_config& c, long long bh, int rows, int cols, int sms, bool tc_can, int* row,
-            int* segments, int* tc) {
+void choose(const lapl_decay_config& c, long long bh, int rows, int cols, bool exact, int sms, bool tc_can,
+            int* row, int* segments, int* tc) {
   double row_us = 0, tc_us = 0;
   *row = row_segments(c.tokens, bh, rows, cols, sms, &row_us);
-  const int chunked = chunk_segments(c.tokens, bh, rows, cols, sms, &tc_us);
+  const int chunked = chunk_segments(c.tokens, bh, rows, cols, exact, sms, &tc_us);
   *tc = tc_can && tc_us < row_us;
   *segments = *tc ? chunked : *row;
 }
@@ -158,11 +159,11 @@ lapl_status lapl_decay_create(const lapl_decay_config* cfg, lapl_decay_handle* o
   p->device = device;
   p->dev_err = dev_err;
   p->wait_ns = kWaitNs;
-  choose(*cfg, p->bh, cfg->key_dim, cfg->value_dim, sms, tc_sizes(*cfg), &p->row_segments,
-         &p->info.segments, &p->info.tensor_cores);
+  choose(*cfg, p->bh, cfg->key_dim, cfg->value_dim, cfg->out_dtype == LAPL_F32, sms, tc_sizes(*cfg),
+         &p->row_segments, &p->info.segments, &p->info.tensor_cores);
   // The backward's three passes go side by side.
   const int most = std::max(cfg->key_dim, cfg->value_dim);
-  choose(*cfg, 3LL * p->bh, most, most, sms, tc_sizes(*cfg) && cfg->grad_dtype == LAPL_BF16,
+  choose(*cfg, 3LL * p->bh, most, most, false, sms, tc_sizes(*cfg) && cfg->grad_dtype == LAPL_BF16,
          &p->backward_row_segments, &p->info.backward_segments, &p->info.backward_tensor_cores);
   *out = p;
   return LAPL_OK;

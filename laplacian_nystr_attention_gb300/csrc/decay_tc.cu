@@ -10,10 +10,14 @@
 //   inner   P Z            P from tensor memory
 //   outer   X S
 //   add     Y^T Z'         Z' = Z with each token's decay to the chunk's end
-// x, y and z enter as they are.  What is computed is split into bf16 parts, so that no product loses
-// what fp32 holds: P and S into two, which leave out 2^-16 of a value at most (2.5e-6 on average; the
-// output's own rounding is 2^-8), Z' into three (2^-24), as what the state loses is carried along (two
-// parts: a state 2.4e-6 off instead of 0.7e-6).
+// x, y and z enter as they are.  What is computed is split into bf16 parts: Z' into three, which leave out
+// 2^-24 of a value, as what the state loses is carried along (of 8 heads of 4096 tokens of 64 x 64 the final
+// state is 2.0e-7 off, root mean square).  P and S into three as well where outputs are fp32 (5.5e-7 off; the
+// formula in fp32 5.3e-7; of 128 x 128 8.4e-7 and 5.4e-7: what is cut off in tensor memory), and into two, which
+// leave out 2^-16, where they are bf16: two parts alone make outputs 2.5e-6 off, their rounding to bf16 1.7e-3, and
+// both together no more than three parts do (1.65849e-3 either way).  The third part costs a stage of shared
+// memory: 32 sequences of 16384 tokens of 64 x 64 with fp32 outputs 155 us, with two parts 129; 104 us with
+// bf16 ones, with three parts 154.
 //
 // One CTA of an SM works through a segment of a sequence; its warps:
 //   0-7    scores to P (warp w: rows 32 (w % 4) and up, every other block of 32 columns), and the
@@ -51,8 +55,10 @@ constexpr int kPieces = kChunk * kD / 8;      // of a tile, of 16 bytes
 constexpr int kAhead = 2;                     // chunks from a copy to the prefetch into L2 beside it
 // kBoxes: tiles that rows of X and Y take, padded: 1 (up to 64 values) or 2 (up to 128).  Z is one, the
 // pass's columns in steps of 64.
-// Stages of X, Y and Z, and of Z': of the longer rows shared memory holds one.
-constexpr int stages_of(int boxes) { return boxes == 1 ? 2 : 1; }
+// kExact: P and S in three parts, for fp32 outputs.
+// Stages of X, Y and Z, and of Z': of the longer rows, and with a third part of S, shared memory holds one.
+constexpr int stages_of(int boxes, bool exact) { return boxes == 1 && !exact ? 2 : 1; }
+constexpr int parts_of(bool exact) { return exact ? 3 : 2; }   // of P and S
 
 // Columns of tensor memory.
 constexpr unsigned kScores = 0, kInner = 256, kOuter = 320, kAdd = 384, kColumns = 512;
@@ -193,9 +199,9 @@ struct Decays {
   }
 };
 
-template <int kBoxes>
+template <int kBoxes, bool kExact>
 struct OutLayout {
-  static constexpr int kStages = stages_of(kBoxes);
+  static constexpr int kStages = stages_of(kBoxes, kExact);
   static constexpr unsigned kStage = (2 * kBoxes + 1) * kTile;   // X, Y and Z
   static constexpr unsigned kState = kBoxes * kD * kD * 2;       // a part of S
   unsigned stage, parts, state, staging, decays, bars, total;
@@ -203,7 +209,7 @@ struct OutLayout {
     stage = 0;
     parts = kStages * kStage;
     state = parts + kStages * kParts * kTile;
-    staging = state + 2 * kState;
+    staging = state + parts_of(kExact) * kState;
     decays = staging + 8 * 2048;
     bars = decays + sizeof(Decays);
     total = bars + 8 * 32;
@@ -216,11 +222,14 @@ enum Bar {
 };
 static_assert(kBars < 32, "room of the barriers");
 
-template <int kBoxes>
+template <int kBoxes, bool kExact>
 __global__ void __launch_bounds__(kOutThreads, 1)
 decay_chunks_kernel(const __grid_constant__ TcArgs t) {
-  using Layout = OutLayout<kBoxes>;
-  constexpr int kStages = Layout::kStages;
+  using Layout = OutLayout<kBoxes, kExact>;
+  constexpr int kStages = Layout::kStages, kOutParts = parts_of(kExact);
+  // P's third part lies over the other tile of scores, whose product waits for the next chunk's copies and
+  // they for the end of what reads that part.
+  static_assert(kOutParts == 2 || kStages == 1, "where P's third part is read, no scores are written");
   constexpr unsigned kStage = Layout::kStage, kState = Layout::kState;
   extern __shared__ unsigned char smem_raw[];
   const Args& a = t.a;
@@ -336,14 +345,17 @@ decay_chunks_kernel(const __grid_constant__ TcArgs t) {
       if (!warp_wait(bar(kScoresFull + (i & 1)), (i >> 1) & 1, wait_ns)) return false;
       fence_after();
       const unsigned base = tmem + kScores + 128u * (i & 1) + lanes;
+      const unsigned third = tmem + kScores + 128u * ((i + 1) & 1) + lanes;
       const int tokens = chunks.tokens(i);
 #pragma unroll 1
       for (int j = odd; j < 4; j += 2) {    // blocks of 32 columns
-        unsigned hi[16], lo[16];
+        unsigned part[kOutParts][16];
         const bool none = p.reverse ? j < quad : j > quad;
         if (none || 32 * j >= tokens) {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) hi[e] = lo[e] = 0u;
+          for (int k = 0; k < kOutParts; ++k)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) part[k][e] = 0u;
         } else {
           unsigned s[32];
           tmem_load32(base + 32 * j, s);
@@ -374,12 +386,14 @@ decay_chunks_kernel(const __grid_constant__ TcArgs t) {
           }
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            hi[e] = take(v[e]);
-            lo[e] = ops::pack_bf16(v[e].f[0], v[e].f[1]);
+#pragma unroll
+            for (int k = 0; k < kOutParts - 1; ++k) part[k][e] = take(v[e]);
+            part[kOutParts - 1][e] = ops::pack_bf16(v[e].f[0], v[e].f[1]);
           }
         }
-        tmem_store16(base + 32 * j, hi);
-        tmem_store16(base + 32 * j + 16, lo);
+        tmem_store16(base + 32 * j, part[0]);
+        tmem_store16(base + 32 * j + 16, part[1]);
+        if constexpr (kExact) tmem_store16(third + 16 * j, part[2]);
       }
       tmem_stored();
       fence_before();
@@ -492,16 +506,18 @@ decay_chunks_kernel(const __grid_constant__ TcArgs t) {
     auto publish = [&] {
 #pragma unroll
       for (int c = 0; c < kCols / 8; ++c) {
-        uint4 hi, lo;
+        uint4 part[kOutParts];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           Vec<2> v = S[4 * c + e];
-          (&hi.x)[e] = take(v);
-          (&lo.x)[e] = ops::pack_bf16(v.f[0], v.f[1]);
+#pragma unroll
+          for (int k = 0; k < kOutParts - 1; ++k) (&part[k].x)[e] = take(v);
+          (&part[kOutParts - 1].x)[e] = ops::pack_bf16(v.f[0], v.f[1]);
         }
         const unsigned piece = (unsigned)((place.col / 8 + c) ^ (place.row & 7)) << 4;
-        *reinterpret_cast<uint4*>(operand_at + piece) = hi;
-        *reinterpret_cast<uint4*>(operand_at + kState + piece) = lo;
+#pragma unroll
+        for (int k = 0; k < kOutParts; ++k)
+          *reinterpret_cast<uint4*>(operand_at + k * kState + piece) = part[k];
       }
       fence_async();
       __syncwarp();
@@ -580,7 +596,7 @@ decay_chunks_kernel(const __grid_constant__ TcArgs t) {
       fence_after();
       if (leader) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+        for (int k = 0; k < kOutParts; ++k)
 #pragma unroll
           for (int s = 0; s < kBoxes * kD / 16; ++s)
             mma(tmem + kOuter, x + step(s), state + (k * kState + s * 2048) / 16,
@@ -592,12 +608,14 @@ decay_chunks_kernel(const __grid_constant__ TcArgs t) {
       fence_after();
       if (leader) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
+        for (int k = 0; k < kOutParts; ++k)
 #pragma unroll
-          for (int s = 0; s < kChunk / 16; ++s)
-            mma_tmem(tmem + kInner,
-                     tmem + kScores + 128u * (i & 1) + 32 * (s / 2) + 16 * k + 8 * (s & 1),
-                     z + s * 2048 / 16, instruction(kD, false, true), k > 0 || s > 0);
+          for (int s = 0; s < kChunk / 16; ++s) {
+            const unsigned p_at = k < 2 ? 128u * (i & 1) + 32 * (s / 2) + 16 * k + 8 * (s & 1)
+                                        : 128u * ((i + 1) & 1) + 8 * s;
+            mma_tmem(tmem + kInner, tmem + kScores + p_at, z + s * 2048 / 16, instruction(kD, false, true),
+                     k > 0 || s > 0);
+          }
         commit(bar(kOFull));
       }
       // The next chunk's scores, whose tile of P the last chunk's product has read: kOFree told.
@@ -833,12 +851,13 @@ bool tc_fits(const Args& a, int passes) {
 
 namespace {
 
-template <int kBoxes>
+template <int kBoxes, bool kExact>
 cudaError_t launch_boxes(const TcArgs& t, int passes, int bh, int tiles, cudaStream_t st) {
   const Args& a = t.a;
-  const unsigned sums = SumLayout<kBoxes>().total + 1024, outs = OutLayout<kBoxes>().total + 1024;
-  static_assert(OutLayout<kBoxes>::kStages * (OutLayout<kBoxes>::kStage + kParts * kTile) +
-                        2 * OutLayout<kBoxes>::kState + 8 * 2048 + 896 + 256 + 1024 <= kSmemMost,
+  using Out = OutLayout<kBoxes, kExact>;
+  const unsigned sums = SumLayout<kBoxes>().total + 1024, outs = Out().total + 1024;
+  static_assert(Out::kStages * (Out::kStage + kParts * kTile) + parts_of(kExact) * Out::kState + 8 * 2048 +
+                        896 + 256 + 1024 <= kSmemMost,
                 "shared memory of the outputs' kernel");
   cudaError_t e = cudaSuccess;
   if (a.segments > 1) {
@@ -851,10 +870,10 @@ cudaError_t launch_boxes(const TcArgs& t, int passes, int bh, int tiles, cudaStr
   }
   if (e == cudaSuccess && a.pass[0].states) e = launch_carry(a, passes, bh, a.segments > 1, st);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(decay_chunks_kernel<kBoxes>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  e = cudaFuncSetAttribute(decay_chunks_kernel<kBoxes, kExact>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            kSmemMost);
   if (e != cudaSuccess) return e;
-  return launch(decay_chunks_kernel<kBoxes>,
+  return launch(decay_chunks_kernel<kBoxes, kExact>,
                 dim3((unsigned)(bh * a.segments), (unsigned)tiles, (unsigned)passes), kOutThreads, outs,
                 a.pass[0].states != nullptr, st, t);
 }
@@ -869,8 +888,10 @@ cudaError_t launch_tc(const Args& a, int passes, int bh, unsigned* err, unsigned
   t.wait_ns = wait_ns;
   t.skip_last = skip_last;
   int rows = 0, cols = 0;
+  bool exact = false;
   for (int i = 0; i < passes; ++i) {
     const Pass& p = a.pass[i];
+    exact = exact || !p.out_half;
     rows = std::max(rows, p.a);
     cols = std::max(cols, p.b);
     if (!encode(&t.x[i], p.x, p.a, a.tokens, bh) || !encode(&t.y[i], p.y, p.a, a.tokens, bh) ||
@@ -878,8 +899,11 @@ cudaError_t launch_tc(const Args& a, int passes, int bh, unsigned* err, unsigned
       return cudaErrorInvalidValue;
   }
   const int tiles = (cols + kD - 1) / kD;
-  return rows <= kD ? launch_boxes<1>(t, passes, bh, tiles, st)
-                    : launch_boxes<2>(t, passes, bh, tiles, st);
+  if (exact)
+    return rows <= kD ? launch_boxes<1, true>(t, passes, bh, tiles, st)
+                      : launch_boxes<2, true>(t, passes, bh, tiles, st);
+  return rows <= kD ? launch_boxes<1, false>(t, passes, bh, tiles, st)
+                    : launch_boxes<2, false>(t, passes, bh, tiles, st);
 }
 
 }  // namespace decay

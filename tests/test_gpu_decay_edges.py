@@ -1,0 +1,43 @@
+"""Edges of the linear attention with decays (lapl_decay_*): what each type keeps, decays that are no
+numbers, waits that give up in each launch, workspaces."""
+import numpy as np
+import pytest
+import torch
+
+import more_operators_reference as ref
+from operators_reference import U
+from test_gpu_decay import dev, make
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from conftest import build_library
+    build_library()
+
+
+@pytest.mark.parametrize("a,b", [(64, 64), (32, 128), (128, 64), (128, 128)])
+@pytest.mark.parametrize("reverse", [False, True])
+def test_fp32_outputs_of_bf16_rows_keep_fp32s_precision(a, b, reverse):
+    """On the tensor cores too: root mean square, over every sequence's outputs.  A sum of up to 24
+    products in tensor memory is cut off at each by up to 2 U of what it is by then, U on average: 24 U if
+    it were as large from the start on.  (What is computed in two bf16 parts leaves out up to 2^-16 = 256 U
+    of each term, some 40 U on average.)"""
+    import laplacian_nystr_attention_gb300 as lna
+    B, H, N = 2, 4, 700
+    m = make(B, H, N, a, b, "bf16", seed=a + b, logs=(-1e-3, -0.01, -0.05, -0.3))
+    plan = lna.DecayAttention(lna.make_decay_config(B, H, N, a, b, scale=0.125, reverse=int(reverse),
+                                                    in_dtype="bf16", out_dtype="f32"))
+    assert lna.lapl_decay_plan_info_get(plan.handle)["tensor_cores"]
+    q, k, v = (dev(m[n], "bf16") for n in "qkv")
+    final = torch.empty(plan.state_shape, device="cuda")
+    out = plan.forward(q, k, v, dev(m["log_decay"]), state=dev(m["state"]), final=final)
+    plan.check_device_errors()
+    want = ref.decay(m["q"], m["k"], m["v"], m["log_decay"], 0.125, m["state"], None, reverse)
+    for got, (value, _) in ((out, want["out"]), (final, want["final"])):
+        off = got.double().cpu().numpy() - value
+        rms = np.sqrt((off ** 2).sum((-1, -2)) / (value ** 2).sum((-1, -2)))
+        assert rms.max() <= 24 * U, rms / U
