@@ -323,7 +323,8 @@ lapl_status lapl_decay_workspace_size(lapl_decay_handle h, size_t* forward_bytes
 
 /*
  * q, k: device [B,H,N,key_dim]; v, out: device [B,H,N,value_dim]; log_decay: device [H] fp32, at most
- * 0 (values above count as 0, below -1e30 as that); state: device [B,H,key_dim,value_dim] fp32 or
+ * 0 (values above count as 0, below -1e30 as that; a NaN makes NaN of what it is part of, and may of the rest
+ * of its head's gradients); state: device [B,H,key_dim,value_dim] fp32 or
  * NULL; lengths: device [B] int32 or NULL (all N): tokens at lengths[b] and beyond are padding, no
  * part of the sequence, and out is zero there (values below 0 count as 0, above N as N); final_state:
  * like state, or NULL: the state after the last token (state for a length of zero); may be state itself.

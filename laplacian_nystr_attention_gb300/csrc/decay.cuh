@@ -76,9 +76,10 @@ struct Range {
 
 // g^n, with log2g = log2(g).
 __device__ __forceinline__ float power(float log2g, int n) { return exp2f(log2g * (float)n); }
-// The logarithm of a head's decay, at most 0.
+// The logarithm of a head's decay, at most 0, or NaN.
 __device__ __forceinline__ float log_decay(const Args& a, int bh) {
-  return fmaxf(fminf(a.log_decay[bh % a.heads], 0.f), kLeastLog);
+  const float l = a.log_decay[bh % a.heads];
+  return l > 0.f ? 0.f : l < kLeastLog ? kLeastLog : l;   // (fmaxf and fminf drop a NaN)
 }
 // A state's decay over n tokens, s -> s exp(l n).  With a decay near 1 that factor's own rounding, the
 // same at every step, would add up over as many steps as the state remembers: there it is s + s m with
@@ -87,7 +88,7 @@ struct Fade {
   float factor, less;   // less: m, or 0 where the factor is used
   Fade() = default;
   __device__ __forceinline__ Fade(float l, int n) {
-    const float x = l * (float)n;
+    const float x = n == 0 ? 0.f : l * (float)n;   // (no token: nothing fades, by a NaN either)
     factor = exp2f(x * kLog2e);
     less = x > -0.5f ? expm1f(x) : 0.f;
     if (x > -0.5f) factor = 1.f;

@@ -41,3 +41,38 @@ def test_fp32_outputs_of_bf16_rows_keep_fp32s_precision(a, b, reverse):
         off = got.double().cpu().numpy() - value
         rms = np.sqrt((off ** 2).sum((-1, -2)) / (value ** 2).sum((-1, -2)))
         assert rms.max() <= 24 * U, rms / U
+
+
+@pytest.mark.parametrize("dtype,d,N", [("f32", 32, 1), ("f32", 32, 40), ("f32", 32, 3000), ("bf16", 64, 1),
+                                       ("bf16", 64, 300), ("bf16", 64, 3000), ("bf16", 128, 300)])
+@pytest.mark.parametrize("reverse", [False, True])
+def test_a_decay_that_is_no_number(dtype, d, N, reverse):
+    """It shows in all that it is part of, and in no other head and no sequence without tokens."""
+    import laplacian_nystr_attention_gb300 as lna
+    lens = [N, 0, max(1, N // 2)]
+    m = make(3, 2, N, d, d, dtype, seed=N)
+    plan = lna.DecayAttention(lna.make_decay_config(3, 2, N, d, d, scale=0.125, reverse=int(reverse),
+                                                    in_dtype=dtype, out_dtype=dtype, grad_dtype=dtype))
+    q, k, v, dout = (dev(m[n], dtype) for n in ("q", "k", "v", "dout"))
+    s0, df = dev(m["state"]), dev(m["dfinal"])
+    lengths = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    got = []
+    for bad in (-0.05, float("nan")):
+        log_decay = torch.tensor([bad, -0.01], device="cuda")
+        final = torch.empty(plan.state_shape, device="cuda")
+        out = plan.forward(q, k, v, log_decay, state=s0, lengths=lengths, final=final)
+        got.append((out, final, *plan.backward(q, k, v, log_decay, dout, state=s0, dfinal=df,
+                                               lengths=lengths)))
+        plan.check_device_errors()
+    for x, y in zip(*got):
+        assert torch.equal(x[:, 1], y[:, 1]) and not torch.isnan(x).any()
+    out, final, dq, dk, dv, dstate = got[1]
+    assert torch.equal(final[1], s0[1]) and torch.equal(dstate[1], df[1])
+    for b, n in ((0, lens[0]), (2, lens[2])):
+        assert torch.isnan(out[b, 0, :n]).all() and torch.isnan(dq[b, 0, :n]).all()
+        assert torch.isnan(final[b, 0]).all() and torch.isnan(dstate[b, 0]).all()
+        # The last token that is processed meets the final state's gradient undecayed.
+        decayed = slice(1, n) if reverse else slice(0, n - 1)
+        assert torch.isnan(dk[b, 0, decayed]).all() and torch.isnan(dv[b, 0, decayed]).all()
+        for t in (out, dq, dk, dv):
+            assert not t[b, :, n:].any()
