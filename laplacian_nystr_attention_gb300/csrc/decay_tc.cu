@@ -781,6 +781,7 @@ decay_sums_kernel(const __grid_constant__ TcArgs t) {
     int issued = 0;
     for (int i = 0; i < n; ++i) {
       const int s = i % kSumStages;
+      if (t.skip_last && i == n - 1) break;   // (fault injection: never copied)
       if (i >= kSumStages) ok = warp_wait(bar(kSumEmpty + s), ((i / kSumStages) - 1) & 1, wait_ns);
       if (!ok) break;
       const unsigned dst = smem_u32(smem + at.stage + s * kStage);

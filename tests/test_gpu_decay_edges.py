@@ -76,3 +76,40 @@ def test_a_decay_that_is_no_number(dtype, d, N, reverse):
         assert torch.isnan(dk[b, 0, decayed]).all() and torch.isnan(dv[b, 0, decayed]).all()
         for t in (out, dq, dk, dv):
             assert not t[b, :, n:].any()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("backward", [False, True])
+def test_waits_that_give_up_in_a_call_of_three_launches(d, backward):
+    """Segments whose last chunk never arrives, in the launch of their sums and in that of the outputs:
+    each ends, the error is told once, and the next call is right."""
+    import laplacian_nystr_attention_gb300 as lna
+    H, N = 2, 3000
+    m = make(1, H, N, d, d, "bf16", logs=(-1e-3, -0.05))
+    plan = lna.DecayAttention(lna.make_decay_config(1, H, N, d, d, scale=0.125, in_dtype="bf16",
+                                                    out_dtype="bf16", grad_dtype="bf16"))
+    info = lna.lapl_decay_plan_info_get(plan.handle)
+    kind = "backward_" if backward else ""
+    assert info[kind + "tensor_cores"] and info[kind + "segments"] > 1, info
+    q, k, v, dout = (dev(m[n], "bf16") for n in ("q", "k", "v", "dout"))
+    log_decay = dev(m["log_decay"])
+    call = (lambda: plan.backward(q, k, v, log_decay, dout)) if backward else \
+        (lambda: (plan.forward(q, k, v, log_decay),))
+    want = call()
+    plan.check_device_errors()
+    lna.lapl_decay_set_fault_injection(plan.handle, 5_000_000, 1)
+    start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    start.record()
+    call()
+    end.record()
+    with pytest.raises(lna.LaplAttnError) as e:
+        plan.check_device_errors()
+    assert e.value.status == lna._lib.LAPL_ERR_DEVICE_TIMEOUT and "linear attention" in str(e.value)
+    # Both launches waited.
+    assert start.elapsed_time(end) >= 2 * 5.0
+    plan.check_device_errors()
+    lna.lapl_decay_set_fault_injection(plan.handle, 0, 0)
+    got = call()
+    plan.check_device_errors()
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
