@@ -42,7 +42,8 @@ struct Part {            // q, k or v
   const void* grad;      // backward: gradient [B,heads,N,d]
   void* din;             // backward: gradient of the rows
   const float* weight;
-  int heads;
+  int heads;             // of the launch
+  int all_heads;
   int stride;
 };
 struct Args {
@@ -250,7 +251,7 @@ struct Place {
 #pragma unroll
     for (int i = 0; i < 3; ++i) {
       in[i] = (long long)at * a.part[i].stride;
-      out[i] = ((long long)b * a.part[i].heads * a.tokens + n) * a.d;
+      out[i] = ((long long)b * a.part[i].all_heads * a.tokens + n) * a.d;
     }
   }
 };
@@ -397,7 +398,9 @@ __device__ __forceinline__ void prefetch_l2(const void* p, long long bytes) {
   asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const unsigned char*>(p) + bytes));
 }
 
-// dw: a thread's rows are summed in fp32, some kSummed of them, what follows in pairs of floats.
+// dw: a thread's rows are summed in fp32, fewer than 2 kSummed of them, what follows in pairs of floats.
+// (Whole tiles are summed: a launch has no more heads than give a thread kSummed rows of a tile.  Turns of so
+// many heads within the kernel took 139 us for what takes 135 of 4 x 16384 tokens of 24 heads of 64.)
 constexpr int kSummed = 64;
 template <int V, int NS, bool kInterleaved, bool kHalfIn, bool kHalfGrad>
 __global__ void __launch_bounds__(kThreads, kBackCtas)
@@ -723,11 +726,20 @@ cudaError_t launch(const lapl_rope_plan& p, rope::Args& a, bool backward, int* c
   int at_once = std::min(rope::kTokens, groups);   // a group has one token of the CTA's at most
   while (at_once < std::min(rope::kMaxTokens, groups) && groups / at_once > heads) at_once *= 2;
   while (at_once > 1 && a.rows < (long long)at_once * 2 * p.sms) at_once /= 2;
+  // Heads of a launch: with weights' gradients, no more than give a thread kSummed rows of a tile; fewer tokens
+  // to a CTA first.
+  int all = 0, some = 0;
+  for (const rope::Part& t : a.part) all = std::max(all, t.heads);
+  some = all;
+  if (backward && a.partial) {
+    while (at_once > 1 && groups / at_once * rope::kSummed < all) at_once /= 2;
+    some = groups / at_once * rope::kSummed;
+  }
   a.at_once = at_once;
   const long long tiles = (a.rows + at_once - 1) / at_once;
   const long long most = backward ? (long long)rope::kBackCtas * p.sms : 1LL << 30;
   const int grid = (int)std::min(tiles, most);
-  *ctas = grid;
+  *ctas = 0;
   const int ns_rounded = ns <= 1 ? 1 : ns == 2 ? 2 : 4;
   const bool hi = c.in_dtype == LAPL_BF16;
   const bool ho = (backward ? c.grad_dtype : c.out_dtype) == LAPL_BF16;
@@ -742,8 +754,26 @@ cudaError_t launch(const lapl_rope_plan& p, rope::Args& a, bool backward, int* c
   const size_t smem =
       sizeof(float2) *
                       (rope::padded(a.d) + rope::turns_of(a.pairs * at_once) + (backward ? 2 * a.d : 0));
-  k<<<grid, rope::kThreads, smem, st>>>(a);
-  return cudaGetLastError();
+  cudaError_t e = cudaSuccess;
+  for (int low = 0; low < all && e == cudaSuccess; low += some) {
+    rope::Args s = a;
+    for (rope::Part& t : s.part) {
+      const long long row = (long long)low * a.d, plane = row * a.tokens;
+      auto moved = [](const void* q, long long n, int dtype) -> const void* {
+        return q ? static_cast<const char*>(q) + n * ops::dtype_bytes(dtype) : nullptr;
+      };
+      t.heads = std::max(0, std::min(t.heads - low, some));
+      t.in = moved(t.in, row, c.in_dtype);
+      t.out = const_cast<void*>(moved(t.out, plane, c.out_dtype));
+      t.grad = moved(t.grad, plane, c.grad_dtype);
+      t.din = const_cast<void*>(moved(t.din, row, c.grad_dtype));
+    }
+    if (s.partial) s.partial += (long long)*ctas * 4 * a.d;
+    k<<<grid, rope::kThreads, smem, st>>>(s);
+    e = cudaGetLastError();
+    *ctas += grid;
+  }
+  return e;
 }
 
 lapl_status check_pointers(std::initializer_list<std::pair<const void*, int>> list) {
@@ -791,7 +821,7 @@ lapl_status lapl_rope_create(const lapl_rope_config* cfg, lapl_rope_handle* out)
   const int heads[3] = {cfg->q_heads, cfg->k_heads, cfg->v_heads};
   const int strides[3] = {cfg->q_stride, cfg->k_stride, cfg->v_stride};
   for (int i = 0; i < 3; ++i) {
-    a.part[i].heads = heads[i];
+    a.part[i].heads = a.part[i].all_heads = heads[i];
     a.part[i].stride = strides[i] ? strides[i] : heads[i] * cfg->head_dim;
   }
   *out = p;
@@ -800,7 +830,10 @@ lapl_status lapl_rope_create(const lapl_rope_config* cfg, lapl_rope_handle* out)
 
 lapl_status lapl_rope_workspace_size(lapl_rope_handle p, size_t* bytes) {
   if (!p || !bytes) return LAPL_ERR_INVALID_ARG;
-  *bytes = align_up((size_t)rope::kBackCtas * p->sms * 2 * p->cfg.head_dim * sizeof(float2), kAlign);
+  // Launches: a CTA of one token has 8 groups of lanes at least.
+  const int heads = std::max(p->cfg.q_heads, std::max(p->cfg.k_heads, p->cfg.v_heads));
+  const int least = rope::kThreads / 32 * rope::kSummed, launches = (heads + least - 1) / least;
+  *bytes = align_up((size_t)launches * rope::kBackCtas * p->sms * 2 * p->cfg.head_dim * sizeof(float2), kAlign);
   return LAPL_OK;
 }
 
