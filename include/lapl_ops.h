@@ -221,8 +221,9 @@ lapl_status lapl_clip_destroy(lapl_clip_handle h);
  * where R turns pair p of values by position * frequencies[p], position being the token's on the
  * pair's axis: the first pairs[0] pairs go by axis 0, the next pairs[1] by axis 1, and so on.  With
  * P pairs in all, pair p is the values p and P+p of the head, or with interleaved 2p and 2p+1; values
- * from 2P on are not turned.  Value heads are copied.  Arithmetic is fp32; the angle is exact to 2^-32
- * of a turn for every 32-bit position.  Outputs are [B,heads,N,d].
+ * from 2P on are not turned.  Value heads are copied.  Arithmetic is fp32; the angle, for every 32-bit
+ * position and every frequency, is off by 2^-33 of a turn before it is taken modulo a turn and rounded to fp32
+ * (by 2^-26 of a turn at most).  Outputs are [B,heads,N,d].
  */
 #define LAPL_ROPE_MAX_DIM 256
 
@@ -235,7 +236,7 @@ typedef struct {
   int head_dim;              /* 1 <= d <= LAPL_ROPE_MAX_DIM                                       */
   int axes;                  /* 1 to 3                                                            */
   const int* pairs;          /* [axes] pairs of each axis, >= 0, 2 P <= d (host, read by create)  */
-  const double* frequencies; /* [P] radians a position, finite (host, read by create)             */
+  const double* frequencies; /* [P] radians a position, below 2^128 (host, read by create)        */
   int interleaved;           /* 0 or 1                                                            */
   int norm;                  /* 0 or 1                                                            */
   float eps;                 /* >= 0                                                              */
