@@ -12,7 +12,7 @@ struct lapl_decay_plan {
   lapl_decay_plan_info info;
   int row_segments, backward_row_segments;   // where the tensor-core kernels cannot run
   int bh;
-  int sms, device;
+  int device;
   unsigned* dev_err;
   unsigned long long wait_ns;
   int skip_last;
@@ -38,69 +38,110 @@ lapl_status validate(const lapl_decay_config* c) {
   return LAPL_OK;
 }
 
-// Segments of a sequence token by token.  A segment's warps walk its tokens alone; by registers 16, 12 or
-// 8 warps of an SM are resident.  Times in us, about as measured: a token of the outputs 0.35, of the
-// segments' sums 0.2, a launch 3, its CTAs 2, and 0.05 for each segment.  (16 sequences of 3136 tokens of
-// 32 x 32 in fp32: 33 us in 98 segments, 45 in 64, 68 in 32, 120 in 16.)
-int row_segments(int tokens, long long bh, int rows, int cols, int sms, double* us) {
-  const int per_warp = rows <= 32 && cols > 32 ? 64 : 32;
-  const long long warps = bh * ((cols + per_warp - 1) / per_warp);
-  const long long room = (rows <= 64 ? 16LL : 48LL) * sms;
-  int best = 1;
-  double least = 0;
-  for (int g = 1; g <= decay::kMostSegments && (g == 1 || tokens / g >= 16); ++g) {
-    const double waves = (double)((warps * g + room - 1) / room);
-    const int per = (tokens + g - 1) / g;
-    const double token = std::max(rows, 16) / 32.0;
-    double time = waves * (2.0 + 0.35 * token * per);
-    if (g > 1) time += waves * (2.0 + 0.2 * token * per) + 6.0 + 0.05 * g;
-    if (g == 1 || time < least) least = time, best = g;
-  }
-  *us = least;
-  return best;
-}
+// Rows and columns of a pass's states.
+struct Size {
+  int rows, cols;
+};
 
-// Segments of a sequence in chunks: a CTA of an SM walks its chunks, of 64 columns of the state.  Times in
-// us, as measured, for rows of up to 64 values and for longer ones, and the same for fp32 outputs: a chunk of
-// the outputs and what a CTA has besides, the same of the segments' sums; the launch between 4, and 0.4 for each
-// segment.  (4 x 8 sequences of 128 chunks of 64 x 64: 110 us in 4 segments, 249 in 1, 121 in 9.)
-int chunk_segments(int tokens, long long bh, int rows, int cols, bool exact, int sms, double* us) {
-  static const double kTimes[2][2][4] = {{{2.05, 4.5, 1.25, 3.0}, {3.6, 6.0, 1.9, 4.0}},
-                                         {{3.4, 5.5, 1.25, 3.0}, {4.0, 6.0, 1.9, 4.0}}};
-  const double* t = kTimes[exact][rows > 64];
-  const int chunks = (tokens + decay::kTcChunk - 1) / decay::kTcChunk;
-  bh *= (cols + 63) / 64;
-  int best = 1;
-  double least = 0;
-  for (int g = 1; g <= 64 && g <= chunks; ++g) {
-    const int per = (chunks + g - 1) / g, n = (chunks + per - 1) / per;
-    double time = (double)((bh * n + sms - 1) / sms) * (t[1] + t[0] * per);
-    if (n > 1) time += (double)((bh * (n - 1) + sms - 1) / sms) * (t[3] + t[2] * per) + 4.0 + 0.4 * n;
-    if (g == 1 || time < least) least = time, best = n;
-  }
-  *us = least;
-  return best;
-}
-
-// Tokens of a segment: whole stages or chunks.
+// Tokens of a segment: whole stages or chunks (step), and the segments that are left.
 int per_segment(int tokens, int segments, int step) {
-  return ((tokens + segments - 1) / segments + step - 1) / step * step;   // (step: of a stage or chunk)
+  return ((tokens + segments - 1) / segments + step - 1) / step * step;
+}
+int segments_of(int tokens, int segments, int step) {
+  const int per = per_segment(tokens, segments, step);
+  return (tokens + per - 1) / per;
+}
+
+// Time in us of the passes token by token, in segments.  A token takes a warp as long as its chain of
+// instructions does, or an SM as long as it takes to issue those of all its warps, whichever is longer; the
+// segments' sums their chain; a launch 3.2; and the states of segments, written and read twice, their bytes.
+// Fitted to 876 times: rows of 16 to 128 values, one sequence to 4096 and 16 to 16384 tokens in 1 to 126 segments,
+// forward and backward, fp32 and bf16: 15% off (root mean square), one in twenty by a third and none by half.
+// (8 x 2 sequences of 3136 tokens of 32 x 32 in fp32: 34 us in 98 segments, 160 in 8, 816 in 1.)
+double rows_time(const Size* size, int passes, bool half, int tokens, long long bh, int segments, int sms) {
+  const int per = std::min(per_segment(tokens, segments, decay::kRowsStep), tokens);
+  double us = 0, bytes = 0;
+  for (int i = 0; i < passes;) {
+    const int n = decay::rows_together(i, passes, [&](int k) { return size[k].rows; });
+    int cols = 0;
+    for (int k = i; k < i + n; ++k) cols = std::max(cols, size[k].cols);
+    const decay::RowsShape s = decay::rows_shape(size[i].rows, cols);
+    // Rows that have to be widened to fp32 or padded, or some of them.
+    bool padded = false;
+    for (int k = i; k < i + n; ++k) {
+      padded = padded || size[k].rows != s.rows || size[k].cols != s.warps * s.cols;
+      bytes += 16.0 * size[k].rows * size[k].cols * (double)(bh * segments);
+    }
+    const double widened = half ? 1.0 : padded ? 0.6 : 0.0;
+    const double warps = (double)(bh * n * segments * s.warps) / sms;
+    const double chain = 0.22 + 0.0016 * s.rows + 0.2 * widened;
+    const double issue = (0.019 + 0.0005 * s.rows) * (s.cols == 64 ? 1.8 : 1.0) * (1.0 + 0.22 * widened);
+    us += 3.2 + per * std::max(chain, issue * warps);
+    if (segments > 1) us += per * (0.105 + 0.0025 * s.rows + 0.13 * widened);
+    i += n;
+  }
+  return segments > 1 ? us + 4.0 + bytes / 3.2e6 : us;
+}
+
+// Time in us of the passes in chunks, in segments: a CTA of an SM walks its chunks, of 64 columns of the state.
+// For rows of up to 64 values and for longer ones, and the same for fp32 outputs: a chunk of the outputs and what
+// a CTA has besides, the same of the segments' sums; the launch between 2, and 0.4 for each segment.  Fitted to 378
+// times, 10 to 14% off and none by over 1.7.  (4 x 8 sequences of 128 chunks of 64 x 64 in bf16: 104 us in 4
+// segments, 249 in 1, 121 in 9.)
+double chunks_time(const Size* size, int passes, bool exact, int tokens, long long bh, int segments, int sms) {
+  static const double kTimes[2][2][4] = {{{2.1, 4.1, 0.8, 4.0}, {3.75, 3.9, 1.2, 8.0}},
+                                         {{3.7, 3.3, 0.85, 2.6}, {4.3, 3.7, 1.3, 8.0}}};
+  int rows = 0;
+  long long ctas = 0;   // of each segment
+  for (int i = 0; i < passes; ++i) {
+    rows = std::max(rows, size[i].rows);
+    ctas += bh * ((size[i].cols + 63) / 64);
+  }
+  const double* t = kTimes[exact][rows > 64];
+  const int per = per_segment(tokens, segments, decay::kTcChunk) / decay::kTcChunk;
+  const double us = (double)((ctas * segments + sms - 1) / sms) * (t[1] + t[0] * per);
+  if (segments == 1) return us;
+  return us + (double)((ctas * (segments - 1) + sms - 1) / sms) * (t[3] + t[2] * per) + 2.0 + 0.4 * segments;
+}
+
+// The segments, up to `most`, that take the least time.
+template <class Time>
+int best_segments(int tokens, int most, int step, Time time, double* us) {
+  int best = 1, last = 0;
+  for (int i = 1; i <= most && i <= (tokens + step - 1) / step; ++i) {
+    const int g = segments_of(tokens, i, step);
+    if (g == last) continue;
+    last = g;
+    const double t = time(g);
+    if (g == 1 || t < *us) *us = t, best = g;
+  }
+  return best;
 }
 
 bool tc_sizes(const lapl_decay_config& c) {
   return c.in_dtype == LAPL_BF16 && c.key_dim % 8 == 0 && c.value_dim % 8 == 0;
 }
 
-// Segments of sequences by both kernels, and whether the tensor cores are faster where they can run: for
-// short sequences, up to one chunk, a CTA's own time against that of the tokens one by one.  (64 x 64 bf16:
-// 8 sequences of 16 tokens 8.3 us and 11.0, 512 of them 26 and 12.7, of 48 30 and 30.)
-void choose(const lapl_decay_config& c, long long bh, int rows, int cols, bool exact, int sms, bool tc_can,
-            int* row, int* segments, int* tc) {
+// Segments of sequences by both kernels, and whether the tensor cores are faster where they can run.  (bf16,
+// 8 x 16 tokens of 64 x 64: 7.0 us in chunks and 11.3 token by token; 512 x 16: 24 and 13; 512 x 128: 26 and 123;
+// 512 x 16 of 128 x 128: 47 and 30; 512 x 64: 48 and 345; the backward of 512 x 128 of 128 x 128: 159 and 517.)
+// rows_only: the rows' kernel is there for pointers off 16 bytes alone; its states take no more room than
+// the other's or than `room`, bytes of a tensor of the call.
+void choose(const Size* size, int passes, int tokens, long long bh, bool half, bool exact, int sms, bool tc_can,
+            size_t room, int* row, int* segments, int* tc) {
   double row_us = 0, tc_us = 0;
-  *row = row_segments(c.tokens, bh, rows, cols, sms, &row_us);
-  const int chunked = chunk_segments(c.tokens, bh, rows, cols, exact, sms, &tc_us);
+  *row = best_segments(tokens, decay::kMostSegments, decay::kRowsStep, [&](int g) {
+    return rows_time(size, passes, half, tokens, bh, g, sms);
+  }, &row_us);
+  const int chunked = best_segments(tokens, 64, decay::kTcChunk, [&](int g) {
+    return chunks_time(size, passes, exact, tokens, bh, g, sms);
+  }, &tc_us);
   *tc = tc_can && tc_us < row_us;
   *segments = *tc ? chunked : *row;
+  if (!*tc) return;
+  const size_t states = sizeof(float) * (size_t)bh * size[0].rows * size[0].cols * passes;
+  const size_t most = std::max((size_t)chunked, room / std::max<size_t>(states, 1));
+  if ((size_t)*row > most) *row = segments_of(tokens, (int)most, decay::kRowsStep);
 }
 
 size_t states_bytes(const lapl_decay_plan& p, int segments) {
@@ -131,8 +172,8 @@ decay::Args common(const lapl_decay_plan& p, const float* log_decay, const int* 
   return a;
 }
 void cut(decay::Args* a, int segments, int step, int chunks) {
-  a->segments = segments;
   a->per_segment = per_segment(a->tokens, segments, step);
+  a->segments = segments;   // (as segments_of gave them: none is empty)
   a->chunks = chunks;
 }
 
@@ -155,15 +196,18 @@ lapl_status lapl_decay_create(const lapl_decay_config* cfg, lapl_decay_handle* o
   if (!p) return LAPL_ERR_INVALID_ARG;
   p->cfg = *cfg;
   p->bh = cfg->batch * cfg->heads;
-  p->sms = sms;
   p->device = device;
   p->dev_err = dev_err;
   p->wait_ns = kWaitNs;
-  choose(*cfg, p->bh, cfg->key_dim, cfg->value_dim, cfg->out_dtype == LAPL_F32, sms, tc_sizes(*cfg),
+  const bool half = cfg->in_dtype == LAPL_BF16, grad_half = cfg->grad_dtype == LAPL_BF16;
+  const Size across = {cfg->value_dim, cfg->key_dim}, along = {cfg->key_dim, cfg->value_dim};
+  const size_t room = (size_t)p->bh * cfg->tokens * std::max(cfg->key_dim, cfg->value_dim) *
+                      ops::dtype_bytes(cfg->in_dtype);
+  choose(&along, 1, cfg->tokens, p->bh, half, cfg->out_dtype == LAPL_F32, sms, tc_sizes(*cfg), room,
          &p->row_segments, &p->info.segments, &p->info.tensor_cores);
   // The backward's three passes go side by side.
-  const int most = std::max(cfg->key_dim, cfg->value_dim);
-  choose(*cfg, 3LL * p->bh, most, most, false, sms, tc_sizes(*cfg) && cfg->grad_dtype == LAPL_BF16,
+  const Size back[3] = {across, across, along};
+  choose(back, 3, cfg->tokens, p->bh, half || grad_half, false, sms, tc_sizes(*cfg) && grad_half, room,
          &p->backward_row_segments, &p->info.backward_segments, &p->info.backward_tensor_cores);
   *out = p;
   return LAPL_OK;
@@ -203,7 +247,7 @@ lapl_status lapl_decay_forward(lapl_decay_handle p, const void* q, const void* k
   f.zs = 1.f, f.os = c.scale;
   const bool tc = p->info.tensor_cores && decay::tc_fits(a, 1);
   if (tc) cut(&a, p->info.segments, decay::kTcChunk, 1);
-  else cut(&a, p->row_segments, 16, 0);
+  else cut(&a, p->row_segments, decay::kRowsStep, 0);
   f.states = a.segments > 1 ? static_cast<float*>(workspace) : nullptr;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = tc ? decay::launch_tc(a, 1, p->bh, p->dev_err, p->wait_ns, p->skip_last, s)
@@ -241,7 +285,7 @@ lapl_status lapl_decay_backward(lapl_decay_handle p, const void* q, const void* 
                back, 0, 1, c.scale, 1.f};
   const bool tc = p->info.backward_tensor_cores && decay::tc_fits(a, 3);
   if (tc) cut(&a, p->info.backward_segments, decay::kTcChunk, 1);
-  else cut(&a, p->backward_row_segments, 16, 0);
+  else cut(&a, p->backward_row_segments, decay::kRowsStep, 0);
   // dstate may be dfinal: the passes that read dfinal go by a copy of it then.
   const size_t step = align_up(states_bytes(*p, a.segments), kAlign);
   if (a.segments > 1 || (dfinal && dstate == dfinal))

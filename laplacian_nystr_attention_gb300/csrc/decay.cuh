@@ -43,6 +43,7 @@ struct Pass {
 
 constexpr int kMaxPasses = 3;
 constexpr int kTcChunk = 128;   // tokens of a chunk on the tensor cores
+constexpr int kRowsStep = 16;   // token by token, segments are multiples of this
 constexpr int kMostSegments = 128;
 struct Args {
   Pass pass[kMaxPasses];
@@ -121,6 +122,24 @@ cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, bo
   cfg.attrs = at;
   cfg.numAttrs = early ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, a...);
+}
+
+// How the kernel that goes token by token takes a pass's rows: as it pads them, a warp's columns, and a CTA's
+// warps.  A lane has 8 columns where that is no more than half of them padding, and where it has registers.
+struct RowsShape {
+  int rows, cols, warps;
+};
+inline RowsShape rows_shape(int rows, int cols) {
+  const int padded = rows <= 64 ? (rows + 15) / 16 * 16 : rows <= 80 ? 80 : rows <= 96 ? 96 : 128;
+  const int wide = cols > 32 && padded <= 32 ? 64 : 32;
+  return {padded, wide, (cols + wide - 1) / wide};
+}
+// Passes from the i-th on that one launch takes: those of the same padded rows.
+template <class Rows>
+int rows_together(int i, int passes, Rows rows) {
+  int n = 1;
+  while (i + n < passes && rows_shape(rows(i + n), 1).rows == rows_shape(rows(i), 1).rows) ++n;
+  return n;
 }
 
 // All launches of the passes token by token, for any sizes and types (decay_rows.cu).

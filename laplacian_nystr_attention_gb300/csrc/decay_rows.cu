@@ -423,11 +423,6 @@ cudaError_t launch_pass(const Args& a, int pass0, int passes, int bh, bool out, 
                 a, pass0);
 }
 
-// Rows of a pass as the kernels pad them.
-int padded(int rows) {
-  return rows <= 64 ? (rows + 15) / 16 * 16 : rows <= 80 ? 80 : rows <= 96 ? 96 : 128;
-}
-
 }  // namespace
 
 cudaError_t launch_carry(const Args& a, int passes, int bh, bool early, cudaStream_t st) {
@@ -447,15 +442,15 @@ cudaError_t launch_rows(const Args& a, int passes, int bh, cudaStream_t st) {
     }
     // Passes of the same padded rows in one launch.
     for (int i = 0; i < passes;) {
-      const int kd = padded(a.pass[i].a), tok = tokens_of(kd);
-      int n = 1;
-      while (i + n < passes && padded(a.pass[i + n].a) == kd) ++n;
+      const int n = rows_together(i, passes, [&](int k) { return a.pass[k].a; });
       int cols = 0;
+      for (int j = i; j < i + n; ++j) cols = std::max(cols, a.pass[j].b);
+      const RowsShape shape = rows_shape(a.pass[i].a, cols);
+      const int kd = shape.rows, tok = tokens_of(kd), warps = shape.warps;
       size_t smem = 0;
       const bool out = stage == 2, early = out && i == 0 && a.pass[0].states;   // right after the carry
       for (int j = i; j < i + n; ++j) {
         const Pass& p = a.pass[j];
-        cols = std::max(cols, p.b);
         const size_t x = stage == 2 ? align_up((size_t)tok * p.a * (p.x_half ? 2 : 4), 16) : 0;
         const size_t y = align_up((size_t)tok * p.a * (p.y_half ? 2 : 4), 16);
         const size_t z = align_up((size_t)tok * p.b * (p.z_half ? 2 : 4), 16);
@@ -464,11 +459,8 @@ cudaError_t launch_rows(const Args& a, int passes, int bh, cudaStream_t st) {
         smem = std::max(smem, 2 * (x + y + z) + sizeof(float) * tok * (padded_x + padded_y));
       }
       cudaError_t e;
-      // A lane's 8 columns where that is no more than half of them padding, and where it has registers.
-      const bool wide = cols > 32 && kd <= 32;
-      const int warps = wide ? (cols + 63) / 64 : (cols + 31) / 32;
-      smem += sizeof(float) * tok * (warps * (wide ? 64 : 32) + 2);
-      switch (kd * 2 + wide) {
+      smem += sizeof(float) * tok * (warps * shape.cols + 2);
+      switch (kd * 2 + (shape.cols == 64)) {
         case 32: e = launch_pass<16, 4>(a, i, n, bh, out, warps, smem, early, st); break;
         case 33: e = launch_pass<16, 8>(a, i, n, bh, out, warps, smem, early, st); break;
         case 64: e = launch_pass<32, 4>(a, i, n, bh, out, warps, smem, early, st); break;

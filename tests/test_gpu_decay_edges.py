@@ -6,7 +6,7 @@ import torch
 
 import more_operators_reference as ref
 from operators_reference import U
-from test_gpu_decay import dev, make
+from test_gpu_decay import dev, make, run
 
 pytestmark = pytest.mark.gpu
 
@@ -113,3 +113,25 @@ def test_waits_that_give_up_in_a_call_of_three_launches(d, backward):
     plan.check_device_errors()
     for x, y in zip(got, want):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("f32", 32)])
+@pytest.mark.parametrize("reverse", [False, True])
+def test_long_sequences_off_sixteen_bytes(dtype, d, reverse):
+    """By the rows' kernel in as many segments as the plan's workspace has room for."""
+    run(1, 2, 3000, d, d, dtype, reverse=reverse, shift=True, logs=(-1e-3, -0.05))
+    run(3, 2, 700, d, d, dtype, reverse=reverse, shift=True, lens=[700, 0, 333], logs=(-1e-3, -0.05))
+
+
+def test_no_segment_is_empty():
+    import laplacian_nystr_attention_gb300 as lna
+    for B, N, d, dtype in ((16, 3136, 32, "f32"), (15, 2047, 48, "f32"), (8, 512, 128, "f32"), (3, 999, 64, "bf16"),
+                           (32, 16384, 64, "bf16"), (2, 8192, 128, "bf16"), (1, 129, 64, "bf16"),
+                           (1, 17, 8, "f32")):
+        plan = lna.DecayAttention(lna.make_decay_config(B, 1, N, d, d, in_dtype=dtype, out_dtype=dtype,
+                                                        grad_dtype=dtype))
+        info = lna.lapl_decay_plan_info_get(plan.handle)
+        for kind in ("", "backward_"):
+            step, n = 128 if info[kind + "tensor_cores"] else 16, info[kind + "segments"]
+            each = -(-(-(-N // n)) // step) * step
+            assert -(-N // each) == n, info
