@@ -219,7 +219,7 @@ lapl_status lapl_decay_workspace_size(lapl_decay_handle p, size_t* forward_bytes
   const int f = std::max(p->info.segments, p->row_segments);
   const int b = std::max(p->info.backward_segments, p->backward_row_segments);
   *forward_bytes = f > 1 ? align_up(states_bytes(*p, f), kAlign) : 0;
-  *backward_bytes = decay::kMaxPasses * align_up(states_bytes(*p, b), kAlign);
+  *backward_bytes = (b > 1 ? decay::kMaxPasses : 1) * align_up(states_bytes(*p, b), kAlign);
   return LAPL_OK;
 }
 
@@ -286,14 +286,20 @@ lapl_status lapl_decay_backward(lapl_decay_handle p, const void* q, const void* 
   const bool tc = p->info.backward_tensor_cores && decay::tc_fits(a, 3);
   if (tc) cut(&a, p->info.backward_segments, decay::kTcChunk, 1);
   else cut(&a, p->backward_row_segments, decay::kRowsStep, 0);
-  // dstate may be dfinal: the passes that read dfinal go by a copy of it then.
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
   const size_t step = align_up(states_bytes(*p, a.segments), kAlign);
-  if (a.segments > 1 || (dfinal && dstate == dfinal))
+  if (a.segments > 1) {
     for (int n = 0; n < 3; ++n)
       a.pass[n].states = reinterpret_cast<float*>(static_cast<char*>(workspace) + n * step);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = tc ? decay::launch_tc(a, 3, p->bh, p->dev_err, p->wait_ns, p->skip_last, s)
-                           : decay::launch_rows(a, 3, p->bh, s);
+  } else if (dfinal && dstate == dfinal) {
+    // The passes that read dfinal go by a copy of it, as one of them writes dstate.
+    e = cudaMemcpyAsync(workspace, dfinal, states_bytes(*p, 1), cudaMemcpyDeviceToDevice, s);
+    a.pass[1].first = a.pass[2].first = static_cast<const float*>(workspace);
+  }
+  if (e == cudaSuccess)
+    e = tc ? decay::launch_tc(a, 3, p->bh, p->dev_err, p->wait_ns, p->skip_last, s)
+           : decay::launch_rows(a, 3, p->bh, s);
   if (e != cudaSuccess) {
     ops::set_error(p->last_error, e, "decay_backward");
     return LAPL_ERR_CUDA;

@@ -144,8 +144,8 @@ int rows_together(int i, int passes, Rows rows) {
 
 // All launches of the passes token by token, for any sizes and types (decay_rows.cu).
 cudaError_t launch_rows(const Args& a, int passes, int bh, cudaStream_t st);
-// The launch that turns segments' own states into those before each; early: right after theirs.
-cudaError_t launch_carry(const Args& a, int passes, int bh, bool early, cudaStream_t st);
+// The launch, right after that of the segments' own states, that turns them into those before each.
+cudaError_t launch_carry(const Args& a, int passes, int bh, cudaStream_t st);
 // All launches of the passes in chunks on the tensor cores (decay_tc.cu), where types, sizes and
 // alignment allow that.
 bool tc_fits(const Args& a, int passes);

@@ -425,18 +425,18 @@ cudaError_t launch_pass(const Args& a, int pass0, int passes, int bh, bool out, 
 
 }  // namespace
 
-cudaError_t launch_carry(const Args& a, int passes, int bh, bool early, cudaStream_t st) {
+cudaError_t launch_carry(const Args& a, int passes, int bh, cudaStream_t st) {
   int most = 0;
   for (int i = 0; i < passes; ++i) most = std::max(most, a.pass[i].a * a.pass[i].b);
   const int tiles = (most + 255) / 256;
-  return launch(decay_carry_kernel, dim3((unsigned)(bh * tiles), 1, (unsigned)passes), 256, 0, early, st, a,
+  return launch(decay_carry_kernel, dim3((unsigned)(bh * tiles), 1, (unsigned)passes), 256, 0, true, st, a,
                 tiles);
 }
 
 cudaError_t launch_rows(const Args& a, int passes, int bh, cudaStream_t st) {
-  for (int stage = a.segments > 1 ? 0 : a.pass[0].states ? 1 : 2; stage < 3; ++stage) {
+  for (int stage = a.segments > 1 ? 0 : 2; stage < 3; ++stage) {
     if (stage == 1) {
-      const cudaError_t e = launch_carry(a, passes, bh, a.segments > 1, st);
+      const cudaError_t e = launch_carry(a, passes, bh, st);
       if (e != cudaSuccess) return e;
       continue;
     }
@@ -448,7 +448,7 @@ cudaError_t launch_rows(const Args& a, int passes, int bh, cudaStream_t st) {
       const RowsShape shape = rows_shape(a.pass[i].a, cols);
       const int kd = shape.rows, tok = tokens_of(kd), warps = shape.warps;
       size_t smem = 0;
-      const bool out = stage == 2, early = out && i == 0 && a.pass[0].states;   // right after the carry
+      const bool out = stage == 2, early = out && i == 0 && a.segments > 1;   // right after the carry
       for (int j = i; j < i + n; ++j) {
         const Pass& p = a.pass[j];
         const size_t x = stage == 2 ? align_up((size_t)tok * p.a * (p.x_half ? 2 : 4), 16) : 0;

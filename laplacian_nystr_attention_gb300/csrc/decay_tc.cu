@@ -868,15 +868,15 @@ cudaError_t launch_boxes(const TcArgs& t, int passes, int bh, int tiles, cudaStr
     e = launch(decay_sums_kernel<kBoxes>,
                dim3((unsigned)(bh * (a.segments - 1)), (unsigned)tiles, (unsigned)passes), kSumThreads, sums,
                false, st, t);
+    if (e == cudaSuccess) e = launch_carry(a, passes, bh, st);
+    if (e != cudaSuccess) return e;
   }
-  if (e == cudaSuccess && a.pass[0].states) e = launch_carry(a, passes, bh, a.segments > 1, st);
-  if (e != cudaSuccess) return e;
   e = cudaFuncSetAttribute(decay_chunks_kernel<kBoxes, kExact>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            kSmemMost);
   if (e != cudaSuccess) return e;
   return launch(decay_chunks_kernel<kBoxes, kExact>,
                 dim3((unsigned)(bh * a.segments), (unsigned)tiles, (unsigned)passes), kOutThreads, outs,
-                a.pass[0].states != nullptr, st, t);
+                a.segments > 1, st, t);
 }
 
 }  // namespace

@@ -135,3 +135,34 @@ def test_no_segment_is_empty():
             step, n = 128 if info[kind + "tensor_cores"] else 16, info[kind + "segments"]
             each = -(-(-(-N // n)) // step) * step
             assert -(-N // each) == n, info
+
+
+@pytest.mark.parametrize("B,H,N,d,forward,backward", [(8, 32, 4096, 128, 0, 100e6), (2, 8, 8192, 128, 34e6, 34e6),
+                                                      (512, 1, 128, 128, 0, 34e6)])
+def test_workspaces_are_no_larger_than_a_tensor_of_the_call(B, H, N, d, forward, backward):
+    """Nor than the states of all sequences, where those weigh more."""
+    import laplacian_nystr_attention_gb300 as lna
+    plan = lna.DecayAttention(lna.make_decay_config(B, H, N, d, d, in_dtype="bf16", out_dtype="bf16",
+                                                    grad_dtype="bf16"))
+    assert plan.workspace_bytes <= forward and plan.backward_workspace_bytes <= backward
+
+
+@pytest.mark.parametrize("dtype,d,N", [("f32", 48, 5), ("bf16", 64, 100), ("bf16", 64, 3000)])
+def test_states_in_place_while_captured(dtype, d, N):
+    """The first state's gradient over the final's, replayed: each time from what the place then holds."""
+    import laplacian_nystr_attention_gb300 as lna
+    m = make(2, 2, N, d, d, dtype)
+    plan = lna.DecayAttention(lna.make_decay_config(2, 2, N, d, d, in_dtype=dtype, out_dtype=dtype,
+                                                    grad_dtype=dtype))
+    q, k, v, dout = (dev(m[n], dtype) for n in ("q", "k", "v", "dout"))
+    log_decay, s0, df = (dev(m[n]) for n in ("log_decay", "state", "dfinal"))
+    want = plan.backward(q, k, v, log_decay, dout, state=s0, dfinal=df)
+    over = df.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = plan.backward(q, k, v, log_decay, dout, state=s0, dfinal=over, grads={"dstate": over})
+    for _ in range(2):
+        over.copy_(df)
+        graph.replay()
+        for x, y in zip(got, want):
+            assert torch.equal(x, y)
