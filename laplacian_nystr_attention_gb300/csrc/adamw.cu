@@ -49,7 +49,7 @@ struct Table {
 
 struct Step {
   float beta1, beta2, one_beta1, one_beta2;   // 1 - beta rounded from double
-  float eps;
+  float eps, down_by;   // the update's divisors are held times down_by, eps among them
   double log_beta1, log_beta2;
   float lr, late1, late2;        // late: 1 - beta^t
   const float* lr_device;
@@ -249,7 +249,9 @@ __device__ __forceinline__ void update(const Table<N>& t, int k, long long at, l
     x.m[i] = __fadd_rn(__fmul_rn(s.beta1, x.m[i]), __fmul_rn(s.one_beta1, g));
     x.v[i] = __fadd_rn(__fmul_rn(s.beta2, x.v[i]), __fmul_rn(__fmul_rn(s.one_beta2, g), g));
     r[i] = fast_sqrt(x.v[i]);
-    // lr m / late1 / (sqrt(v / late2) + eps), with a = lr / late1 and root = 1 / sqrt(late2).
+    // lr m / late1 / (sqrt(v / late2) + eps), with a = lr / late1 and root = 1 / sqrt(late2), both times
+    // down_by.  (Root and quotient, off by 2 units each, are the step's alone: no state is made of them.  The
+    // quotient by more than 2^126 would be zero.)
     x.w[i] = x.w[i] * keep - __fdividef(a * x.m[i], fmaf(r[i], root, s.eps));
   }
   if (master) store_f32<kVector>(master + at, x.w, lane, n);
@@ -297,7 +299,7 @@ adamw_kernel(const __grid_constant__ Table<N> t, const __grid_constant__ Step s)
     late1 = -expm1f((float)(step * s.log_beta1));
     late2 = -expm1f((float)(step * s.log_beta2));
   }
-  const float a = lr / late1, root = 1.f / sqrtf(late2);
+  const float a = lr / late1 * s.down_by, root = s.down_by / sqrtf(late2);
   const int pieces = t.first[t.tensors];
   const int warp = threadIdx.x >> 5;
   for (int i = blockIdx.x; i < pieces; i += gridDim.x) {
@@ -388,7 +390,9 @@ void create(const lapl_adamw_config* cfg, int sms, lapl_adamw_plan* p) {
   s.one_beta2 = (float)(1.0 - p->beta2);
   s.log_beta1 = std::log(p->beta1);
   s.log_beta2 = std::log(p->beta2);
-  s.eps = (float)cfg->eps;
+  // Roots are below 2^64, and with their correction below 2^91.
+  s.down_by = (float)cfg->eps > 0x1p62f ? 0x1p-64f : 1.f;
+  s.eps = (float)cfg->eps * s.down_by;
   long long pieces = 0;
   for (int i = 0; i < T; ++i) {
     if (p->counts[i] == 0) continue;
