@@ -407,7 +407,8 @@ lapl_status lapl_adamw_create(const lapl_adamw_config* cfg, lapl_adamw_handle* o
  * each tensor, with 8-bit states only.  Zeros are the states (codes and scales) to start from.
  * lr, step: used where lr_device (1 fp32) or step_device (1 int64) is NULL; those are for steps that
  * are captured into a graph.  step >= 1.  norm: device, 1 fp32, or NULL; max_norm: finite, >= 0.
- * No buffer may overlap another (LAPL_ERR_INVALID_ARG), but that gradients may share memory.
+ * No buffer may overlap another (LAPL_ERR_INVALID_ARG), but that what is only read (gradients, lr_device,
+ * step_device, norm) may share memory.
  */
 lapl_status lapl_adamw_step(lapl_adamw_handle h, void* const* params, const void* const* grads,
                             float* const* masters, void* const* m, void* const* v,

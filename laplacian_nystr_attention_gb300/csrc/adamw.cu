@@ -377,7 +377,7 @@ void create(const lapl_adamw_config* cfg, int sms, lapl_adamw_plan* p) {
   p->dtypes.assign(cfg->dtypes, cfg->dtypes + T);
   p->grad_dtypes.assign(cfg->grad_dtypes, cfg->grad_dtypes + T);
   p->weight_decay.assign(cfg->weight_decay, cfg->weight_decay + T);
-  p->spans.reserve(7 * (size_t)T);
+  p->spans.reserve(7 * (size_t)T + 3);
   p->f8 = cfg->state_bits == 8;
   // In double: 1 - beta of a float near 1 would have few bits (0.999f is 1 - 0.00100005).
   p->beta1 = cfg->beta1;
@@ -473,7 +473,8 @@ cudaError_t launch(const lapl_adamw_plan& p, const lapl_adamw_plan::Batch& b, co
   return cudaGetLastError();
 }
 
-lapl_status check_arrays(lapl_adamw_plan* p, const Arrays& a) {
+// scalars: lr_device, step_device and norm, which every CTA reads whenever it starts.
+lapl_status check_arrays(lapl_adamw_plan* p, const Arrays& a, const void* const (&scalars)[3]) {
   auto& spans = p->spans;
   spans.clear();
   // A written span's end is odd-tagged: spans are doubled to make room for the tag.
@@ -483,6 +484,11 @@ lapl_status check_arrays(lapl_adamw_plan* p, const Arrays& a) {
     spans.emplace_back((uintptr_t)at, ((uintptr_t)at + (uintptr_t)n * size) * 2 + written);
     return LAPL_OK;
   };
+  for (int i = 0; i < 3; ++i)
+    if (scalars[i]) {
+      const lapl_status st = add(scalars[i], 1, i == 1 ? 8 : 4, false);
+      if (st != LAPL_OK) return st;
+    }
   for (size_t i = 0; i < p->counts.size(); ++i) {
     const long long n = p->counts[i];
     if (n == 0) continue;
@@ -548,10 +554,8 @@ lapl_status lapl_adamw_step(lapl_adamw_handle p, void* const* params, const void
   if (!lr_device && !std::isfinite(lr)) return LAPL_ERR_INVALID_ARG;
   if (!step_device && step < 1) return LAPL_ERR_INVALID_ARG;
   if (norm && (!(max_norm >= 0.f) || !std::isfinite(max_norm))) return LAPL_ERR_INVALID_ARG;
-  if (!ops::aligned(lr_device, 4) || !ops::aligned(step_device, 8) || !ops::aligned(norm, 4))
-    return LAPL_ERR_ALIGNMENT;
   const Arrays a = {params, grads, masters, m, v, m_scales, v_scales};
-  lapl_status st = check_arrays(p, a);
+  lapl_status st = check_arrays(p, a, {lr_device, step_device, norm});
   if (st != LAPL_OK) return st;
   st = ops::check_device(p->device, p->last_error, "adamw_step/device");
   if (st != LAPL_OK) return st;

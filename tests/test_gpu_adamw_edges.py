@@ -36,3 +36,22 @@ def test_an_eps_of_any_size(bits, eps, lr, scale, monkeypatch):
 
     monkeypatch.setattr(ref, "adamw", adamw)
     run([700, 256], ["f32", "f32"], bits=bits, eps=eps, lr=lr, scale=scale)
+
+
+def test_scalars_in_what_the_step_writes_are_refused():
+    """Every CTA reads them when it starts, and by then another may have written there."""
+    import laplacian_nystr_attention_gb300 as lna
+    plan = lna.AdamW([8], ["f32"])
+    p, g = [torch.ones(8, device="cuda")], [torch.ones(8, device="cuda")]
+    s = plan.new_states(p)
+    number = torch.ones((), dtype=torch.int64, device="cuda")
+    one = torch.ones((), device="cuda")
+    call = dict(params=p, grads=g, step=number, lr=one, **s)
+    for bad in (dict(lr=p[0][3:4]), dict(norm=s["m"][0][7:], max_norm=1.0), dict(lr=s["v"][0][:1]),
+                dict(step=p[0][2:4].view(torch.int64))):
+        with pytest.raises(lna.LaplAttnError) as e:
+            plan.step(**{**call, **bad})
+        assert e.value.status == 1
+    # What is only read may be one place, and a gradient.
+    plan.step(**{**call, "lr": g[0][:1], "norm": g[0][:1], "max_norm": 1.0})
+    assert (p[0] < 1).all()
