@@ -11,9 +11,10 @@
 //   outer   X S
 //   add     Y^T Z'         Z' = Z with each token's decay to the chunk's end
 // x, y and z enter as they are.  What is computed is split into bf16 parts: Z' into three, which leave out
-// 2^-24 of a value, as what the state loses is carried along (of 8 heads of 4096 tokens of 64 x 64 the final
-// state is 2.0e-7 off, root mean square).  P and S into three as well where outputs are fp32 (5.5e-7 off; the
-// formula in fp32 5.3e-7; of 128 x 128 8.4e-7 and 5.4e-7: what is cut off in tensor memory), and into two, which
+// 2^-24 of a value, as what the state loses is carried along (of 2 x 16 sequences of 4096 tokens of 64 x 128 the
+// final state is 1.8e-7 off, root mean square).  P and S into three as well where outputs are fp32 (2.5e-7 off, of
+// 128 x 128 3.1e-7; the formula in fp32 4.5e-7 and 4.7e-7), their smallest parts' products first: what is added in
+// tensor memory is cut off by the sum so far (largest parts first 5.1e-7 and 8.1e-7).  Into two parts, which
 // leave out 2^-16, where they are bf16: two parts alone make outputs 2.5e-6 off, their rounding to bf16 1.7e-3, and
 // both together no more than three parts do (1.65849e-3 either way).  The third part costs a stage of shared
 // memory: 32 sequences of 16384 tokens of 64 x 64 with fp32 outputs 155 us, with two parts 129; 104 us with
@@ -596,11 +597,11 @@ decay_chunks_kernel(const __grid_constant__ TcArgs t) {
       fence_after();
       if (leader) {
 #pragma unroll
-        for (int k = 0; k < kOutParts; ++k)
+        for (int k = kOutParts - 1; k >= 0; --k)   // (small parts first: what is added to later is cut off)
 #pragma unroll
           for (int s = 0; s < kBoxes * kD / 16; ++s)
             mma(tmem + kOuter, x + step(s), state + (k * kState + s * 2048) / 16,
-                instruction(kD, false, true), k > 0 || s > 0);
+                instruction(kD, false, true), k < kOutParts - 1 || s > 0);
         commit(bar(kSFree));
       }
       ok = warp_wait(bar(kPReady + (i & 1)), (i >> 1) & 1, wait_ns);
@@ -608,13 +609,13 @@ decay_chunks_kernel(const __grid_constant__ TcArgs t) {
       fence_after();
       if (leader) {
 #pragma unroll
-        for (int k = 0; k < kOutParts; ++k)
+        for (int k = kOutParts - 1; k >= 0; --k)
 #pragma unroll
           for (int s = 0; s < kChunk / 16; ++s) {
             const unsigned p_at = k < 2 ? 128u * (i & 1) + 32 * (s / 2) + 16 * k + 8 * (s & 1)
                                         : 128u * ((i + 1) & 1) + 8 * s;
             mma_tmem(tmem + kInner, tmem + kScores + p_at, z + s * 2048 / 16, instruction(kD, false, true),
-                     k > 0 || s > 0);
+                     k < kOutParts - 1 || s > 0);
           }
         commit(bar(kOFull));
       }
