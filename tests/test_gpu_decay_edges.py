@@ -166,3 +166,30 @@ def test_states_in_place_while_captured(dtype, d, N):
         graph.replay()
         for x, y in zip(got, want):
             assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("a,b", [(64, 64), (128, 128), (40, 104)])
+@pytest.mark.parametrize("reverse", [False, True])
+def test_fp32_outputs_of_bf16_rows_in_segments_and_padding(a, b, reverse):
+    run(1, 2, 3000, a, b, "bf16", out="f32", reverse=reverse, backward=False, tc=True, logs=(-1e-3, -0.05))
+    run(7, 2, 400, a, b, "bf16", out="f32", reverse=reverse, backward=False, tc=True,
+        lens=[400, 0, 1, 127, 128, 129, 385], logs=(-0.2, -0.01))
+
+
+@pytest.mark.parametrize("N", [300, 3000])
+def test_waits_that_give_up_with_fp32_outputs(N):
+    import laplacian_nystr_attention_gb300 as lna
+    m = make(1, 2, N, 64, 64, "bf16", logs=(-1e-3, -0.05))
+    plan = lna.DecayAttention(lna.make_decay_config(1, 2, N, 64, 64, in_dtype="bf16", out_dtype="f32"))
+    assert lna.lapl_decay_plan_info_get(plan.handle)["tensor_cores"]
+    q, k, v = (dev(m[n], "bf16") for n in "qkv")
+    log_decay = dev(m["log_decay"])
+    want = plan.forward(q, k, v, log_decay)
+    lna.lapl_decay_set_fault_injection(plan.handle, 5_000_000, 1)
+    plan.forward(q, k, v, log_decay)
+    with pytest.raises(lna.LaplAttnError) as e:
+        plan.check_device_errors()
+    assert e.value.status == lna._lib.LAPL_ERR_DEVICE_TIMEOUT
+    lna.lapl_decay_set_fault_injection(plan.handle, 0, 0)
+    assert torch.equal(plan.forward(q, k, v, log_decay), want)
+    plan.check_device_errors()
