@@ -54,13 +54,15 @@ int segments_of(int tokens, int segments, int step) {
 
 // Time in us of the passes token by token, in segments.  A token takes a warp as long as its chain of
 // instructions does, or an SM as long as it takes to issue those of all its warps, whichever is longer; the
-// segments' sums their chain; a launch 3.2; and the states of segments, written and read twice, their bytes.
-// Fitted to 876 times: rows of 16 to 128 values, one sequence to 4096 and 16 to 16384 tokens in 1 to 126 segments,
-// forward and backward, fp32 and bf16: 15% off (root mean square), one in twenty by a third and none by half.
-// (8 x 2 sequences of 3136 tokens of 32 x 32 in fp32: 34 us in 98 segments, 160 in 8, 816 in 1.)
+// segments' sums their chain; a launch 3.2; the states of segments, written and read twice, their bytes; and a last
+// round of warps that does not fill the SMs a tenth of what it leaves empty.  Fitted to 2532 times: rows of 16 to
+// 128 values, one sequence to 4096 and 16 to 16384 tokens in 1 to 128 segments, forward and backward, fp32 and bf16:
+// 14% off (root mean square), 3 in 100 by a third and none by over half.  Of 130 calls that were measured in several
+// numbers of segments the one it takes is 1% slower than the best, 17% at most.  (8 x 2 sequences of 3136 tokens of
+// 32 x 32 in fp32: 32 us in 98 segments, 160 in 8, 816 in 1.)
 double rows_time(const Size* size, int passes, bool half, int tokens, long long bh, int segments, int sms) {
   const int per = std::min(per_segment(tokens, segments, decay::kRowsStep), tokens);
-  double us = 0, bytes = 0;
+  double us = 0, bytes = 0, empty = 0;
   for (int i = 0; i < passes;) {
     const int n = decay::rows_together(i, passes, [&](int k) { return size[k].rows; });
     int cols = 0;
@@ -76,11 +78,14 @@ double rows_time(const Size* size, int passes, bool half, int tokens, long long 
     const double warps = (double)(bh * n * segments * s.warps) / sms;
     const double chain = 0.22 + 0.0016 * s.rows + 0.2 * widened;
     const double issue = (0.019 + 0.0005 * s.rows) * (s.cols == 64 ? 1.8 : 1.0) * (1.0 + 0.22 * widened);
+    const double rounds = warps / s.room;
+    if (rounds > 1.0) empty = std::max(empty, std::ceil(rounds) / rounds - 1.0);
     us += 3.2 + per * std::max(chain, issue * warps);
     if (segments > 1) us += per * (0.105 + 0.0025 * s.rows + 0.13 * widened);
     i += n;
   }
-  return segments > 1 ? us + 4.0 + bytes / 3.2e6 : us;
+  if (segments > 1) us += 4.0 + bytes / 3.2e6;
+  return us * (1.0 + 0.1 * empty);
 }
 
 // Time in us of the passes in chunks, in segments: a CTA of an SM walks its chunks, of 64 columns of the state.
@@ -104,16 +109,23 @@ double chunks_time(const Size* size, int passes, bool exact, int tokens, long lo
   return us + (double)((ctas * (segments - 1) + sms - 1) / sms) * (t[3] + t[2] * per) + 2.0 + 0.4 * segments;
 }
 
-// The segments, up to `most`, that take the least time.
+// The segments, up to `most`, that take the least time, or the fewest that take no more than `slack` of it.
 template <class Time>
-int best_segments(int tokens, int most, int step, Time time, double* us) {
-  int best = 1, last = 0;
-  for (int i = 1; i <= most && i <= (tokens + step - 1) / step; ++i) {
-    const int g = segments_of(tokens, i, step);
-    if (g == last) continue;
-    last = g;
-    const double t = time(g);
-    if (g == 1 || t < *us) *us = t, best = g;
+int best_segments(int tokens, int most, int step, double slack, Time time, double* us) {
+  int best = 1;
+  double least = 0;
+  for (const bool choosing : {false, true}) {
+    for (int i = 1, last = 0; i <= most && i <= (tokens + step - 1) / step; ++i) {
+      const int g = segments_of(tokens, i, step);
+      if (g == last) continue;
+      last = g;
+      const double t = time(g);
+      if (choosing && t <= slack * least) {
+        *us = t;
+        return g;
+      }
+      if (!choosing && (g == 1 || t < least)) least = t, best = g;
+    }
   }
   return best;
 }
@@ -130,10 +142,11 @@ bool tc_sizes(const lapl_decay_config& c) {
 void choose(const Size* size, int passes, int tokens, long long bh, bool half, bool exact, int sms, bool tc_can,
             size_t room, int* row, int* segments, int* tc) {
   double row_us = 0, tc_us = 0;
-  *row = best_segments(tokens, decay::kMostSegments, decay::kRowsStep, [&](int g) {
+  *row = best_segments(tokens, decay::kMostSegments, decay::kRowsStep, 1.0, [&](int g) {
     return rows_time(size, passes, half, tokens, bh, g, sms);
   }, &row_us);
-  const int chunked = best_segments(tokens, 64, decay::kTcChunk, [&](int g) {
+  // (The chunks' model is no finer: the backward of 32 x 16384 tokens of 64 x 64 258 us in 1 segment, 270 in 3.)
+  const int chunked = best_segments(tokens, 64, decay::kTcChunk, 1.05, [&](int g) {
     return chunks_time(size, passes, exact, tokens, bh, g, sms);
   }, &tc_us);
   *tc = tc_can && tc_us < row_us;

@@ -124,15 +124,18 @@ cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, bo
   return cudaLaunchKernelEx(&cfg, kernel, a...);
 }
 
-// How the kernel that goes token by token takes a pass's rows: as it pads them, a warp's columns, and a CTA's
-// warps.  A lane has 8 columns where that is no more than half of them padding, and where it has registers.
+// CTAs of four warps of the kernel that goes token by token that an SM has registers for, with as many padded
+// rows and columns of a lane.
+constexpr int rows_ctas(int rows, int cols) { return rows * cols <= 256 ? 4 : rows * cols <= 384 ? 3 : 2; }
+// How that kernel takes a pass's rows: as it pads them, a warp's columns, a CTA's warps, and those that an SM has
+// room for.  A lane has 8 columns where that is no more than half of them padding, and where it has registers.
 struct RowsShape {
-  int rows, cols, warps;
+  int rows, cols, warps, room;
 };
 inline RowsShape rows_shape(int rows, int cols) {
   const int padded = rows <= 64 ? (rows + 15) / 16 * 16 : rows <= 80 ? 80 : rows <= 96 ? 96 : 128;
   const int wide = cols > 32 && padded <= 32 ? 64 : 32;
-  return {padded, wide, (cols + wide - 1) / wide};
+  return {padded, wide, (cols + wide - 1) / wide, 4 * rows_ctas(padded, wide / 8)};
 }
 // Passes from the i-th on that one launch takes: those of the same padded rows.
 template <class Rows>

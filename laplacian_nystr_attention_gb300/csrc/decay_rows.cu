@@ -112,7 +112,7 @@ __device__ __forceinline__ void across_quarters(float (&v)[kCols], int lane) {
 
 // Registers for as many warps as a lane's part of the state allows: a warp issues every 4 to 5 clocks.
 template <int KD, int kCols, bool kOut>
-__global__ void __launch_bounds__(128, KD * kCols <= 256 ? 4 : KD * kCols <= 384 ? 3 : 2)
+__global__ void __launch_bounds__(128, rows_ctas(KD, kCols))
 decay_rows_kernel(const __grid_constant__ Args a, int pass0) {
   extern __shared__ __align__(16) unsigned char smem[];
   constexpr int kTok = tokens_of(KD);
