@@ -6,9 +6,10 @@
 // run of memory, and a block's largest value is one reduction over the warp.  Blocks that end early
 // and tensors off 16 bytes (8-bit states: off 4) go value by value, lane by lane.
 // HBM-bound: every value's weight, gradient and states are read and written once (28 bytes with fp32
-// states, 16 with 8-bit ones, of fp32 weights).  Measured, of 6.8 TB/s: 2^20 fp32 values in 24 tensors 5.9 us
-// (5.0 TB/s); 2^27 bf16 weights with masters and 8-bit states 445 us (4.8 TB/s), with instructions issued in
-// three quarters of the cycles: roots, divisions and conversions of 8-bit states.
+// states, 16 with 8-bit ones, of fp32 weights).  Measured, of 6.8 TB/s, from HBM: 2^20 fp32 values in 24 tensors 9.4 us
+// (3.1 TB/s: one round of loads, that of the table among them); with fp32 states 2^26 fp32 weights 297 us and 2^26
+// bf16 ones with masters 299 (6.3 TB/s); 2^27 bf16 weights with masters and 8-bit states 450 us (4.8 TB/s), with
+// instructions issued in three quarters of the cycles: roots, divisions and conversions of 8-bit states.
 #include <algorithm>
 #include <cmath>
 #include <new>
@@ -267,7 +268,7 @@ __device__ __forceinline__ void update(const Table<N>& t, int k, long long at, l
 }
 
 // Weights, gradients and codes of a whole block with 8-bit states, into L2, while a block is worked on, which
-// registers have no room for.  (2^27 bf16 weights 445 us and 490 without.  With fp32 states, which wait for
+// registers have no room for.  (2^27 bf16 weights 450 us and 490 without.  With fp32 states, which wait for
 // bandwidth and not for latency: 2^26 values 320 us and 295
 // without; with the scales 470.)
 template <int N>

@@ -135,10 +135,11 @@ bool tc_sizes(const lapl_decay_config& c) {
 }
 
 // Segments of sequences by both kernels, and whether the tensor cores are faster where they can run.  (bf16,
-// 8 x 16 tokens of 64 x 64: 7.0 us in chunks and 11.3 token by token; 512 x 16: 24 and 13; 512 x 128: 26 and 123;
-// 512 x 16 of 128 x 128: 47 and 30; 512 x 64: 48 and 345; the backward of 512 x 128 of 128 x 128: 159 and 517.)
-// rows_only: the rows' kernel is there for pointers off 16 bytes alone; its states take no more room than
-// the other's or than `room`, bytes of a tensor of the call.
+// 8 x 16 tokens of 64 x 64: 6.9 us in chunks and 11.6 token by token; 512 x 16: 24 and 13; 512 x 128: 25 and 76;
+// 512 x 16 of 128 x 128: 48 and 30; 512 x 64: 48 and 100; the backward of 512 x 128 of 128 x 128: 159 and 517.  Of
+// 368 calls by both, the one taken was over a tenth slower in 3, by a fifth at most.)
+// Where they are taken, the rows' kernel is left for pointers off 16 bytes, and its states have no more room than
+// the other's or than `room`, the bytes of a tensor of the call.
 void choose(const Size* size, int passes, int tokens, long long bh, bool half, bool exact, int sms, bool tc_can,
             size_t room, int* row, int* segments, int* tc) {
   double row_us = 0, tc_us = 0;

@@ -10,12 +10,12 @@
 // times g^i), and put right at the stage's end.  Where g^-16 is large (over 2^4; a larger one could
 // overflow what the sums do not) the state is multiplied at every token.  The warps of a CTA take the
 // same sequence's next columns, so that x and y are read and widened to fp32 once (rows in fp32 that need no
-// padding stay as they are: 490 us instead of 416); tokens are copied a stage ahead.
+// padding stay as they are: 416 us instead of 490); tokens are copied a stage ahead.
 //
 // Bound by fp32 instructions for long sequences (2 a b multiply-adds a token, 3 with segments), by the
-// bytes of the states for single tokens.  4 x 8 sequences of 16384 tokens of 64 x 64 in fp32: 416 us, 31
-// tera-operations a second (of 537 MB, 1.3 TB/s); 8 x 2 of 3136 tokens of 32 x 32: 33 us; one token of 512
-// sequences of 64 x 64 in bf16: 5.5 us (3.1 TB/s of 17 MB).
+// bytes of the states for single tokens.  4 x 8 sequences of 16384 tokens of 64 x 64 in fp32: 425 us, 30
+// tera-operations a second (of 537 MB, 1.3 TB/s); 8 x 2 of 3136 tokens of 32 x 32: 32 us; one token of 512
+// sequences of 64 x 64 in bf16: 6.4 us (2.7 TB/s of 17 MB).
 #include <algorithm>
 
 #include "decay.cuh"
@@ -27,7 +27,7 @@ namespace {
 using ops::Vec;
 
 // Tokens of a stage: as many as leave room in shared memory for the warps that registers do (64 x 64 in fp32
-// with 16: 472 us for what takes 416).
+// with 16: 472 us for what took 416).
 constexpr int kMostTok = 16;
 constexpr int tokens_of(int kd) { return kd <= 48 ? 16 : 12; }
 constexpr float kMostUp = 4.f;    // log2 of the largest g^-kMostTok that the state is held times

@@ -14,17 +14,17 @@
 // 2^-24 of a value, as what the state loses is carried along (of 2 x 16 sequences of 4096 tokens of 64 x 128 the
 // final state is 1.8e-7 off, root mean square).  P and S into three as well where outputs are fp32 (2.5e-7 off, of
 // 128 x 128 3.1e-7; the formula in fp32 4.5e-7 and 4.7e-7), their smallest parts' products first: what is added in
-// tensor memory is cut off by the sum so far (largest parts first 5.1e-7 and 8.1e-7).  Into two parts, which
-// leave out 2^-16, where they are bf16: two parts alone make outputs 2.5e-6 off, their rounding to bf16 1.7e-3, and
-// both together no more than three parts do (1.65849e-3 either way).  The third part costs a stage of shared
-// memory: 32 sequences of 16384 tokens of 64 x 64 with fp32 outputs 155 us, with two parts 129; 104 us with
+// tensor memory is cut off by the sum so far (largest parts first 5.1e-7 and 8.1e-7).  Where outputs are bf16, P and
+// S go into two parts, which leave out 2^-16: that alone makes outputs 2.5e-6 off, their rounding to bf16 1.7e-3,
+// and both together as much as with three parts (1.65849e-3 either way).  The third part costs a stage of shared
+// memory: 32 sequences of 16384 tokens of 64 x 64 with fp32 outputs 154 us, with two parts 130; 104 us with
 // bf16 ones, with three parts 154.
 //
 // One CTA of an SM works through a segment of a sequence; its warps:
 //   0-7    scores to P (warp w: rows 32 (w % 4) and up, every other block of 32 columns), and the
 //          outputs: both accumulators, the decays, through shared memory to whole runs of rows.  Warp 0:
 //          the copies of X, Y and Z tiles by TMA, 128-byte swizzle, a chunk ahead
-//   8-11   the state, fp32 in registers: g^n S + add, and its two parts as an operand
+//   8-11   the state, fp32 in registers: g^n S + add, and its parts as an operand
 //   8-14   Z' from Z
 //   15     the products
 // (16 warps, so that each may have 128 registers: with 18 it was 96, and spills.)
@@ -34,8 +34,8 @@
 //
 // Bound by the chain of a chunk: scores, P, its product, the outputs, and beside them Z', its product, the
 // state: 4,000 clocks, of which the products take 2,060 and the bytes, at 6.8 TB/s for all SMs, 2,790.  4 x 8
-// sequences of 16384 tokens of 64 x 64 in bf16: 105 us (2.6 TB/s of 268 MB; 34 us the sums, 73 the
-// outputs); the backward, three passes side by side, 259.  Of 128 x 128, 2 x 8 x 8192 tokens: 103 and 231,
+// sequences of 16384 tokens of 64 x 64 in bf16: 104 us (2.6 TB/s of 268 MB; 34 us the sums, 73 the
+// outputs); the backward, three passes side by side, 260.  Of 128 x 128, 2 x 8 x 8192 tokens: 102 and 228,
 // with room for one stage.
 #include <algorithm>
 

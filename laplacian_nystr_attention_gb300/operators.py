@@ -97,7 +97,7 @@ class _Layout:
 
 
 class _Plan:
-    """A handle, its device, and what the three operators' calls have in common."""
+    """A handle, its device, and what the operators' calls have in common."""
 
     _destroy = None
     _index = -1
@@ -570,6 +570,10 @@ class HeadRotary(_Plan):
 class DecayAttention(_Plan):
     """S_i = exp(log_decay) S_{i-1} + k_i v_i^T, out_i = scale q_i S_i over the tokens of each
     sequence, for every head: causal linear attention with a decay for each head.
+
+    fp32 outputs and states have fp32's precision by every kernel, whatever the inputs' type; for bf16
+    outputs of bf16 rows the tensor-core kernels hold what they compute on the way in 16 bits where it is
+    multiplied again.
 
     The tensor-core kernels bound each wait to a second; results of a call whose wait gave up are
     undefined, and check_device_errors() is what tells."""
